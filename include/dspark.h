@@ -63,6 +63,10 @@ typedef enum {
 #define DSPARK_MAX_SCHED_ITEMS 4096   /* B * gamma for dspark_schedule */
 #define DSPARK_MAX_STS_GRID 65536     /* candidate temperatures for dspark_sts_fit */
 #define DSPARK_MAX_STS_BINS 64        /* calibration-error bins for dspark_sts_fit */
+#define DSPARK_MAX_CACHE_REQUESTS 4096  /* B of the cache calls */
+#define DSPARK_MAX_HEAD_DIM 256       /* head_dim of the cache calls (a multiple of 8) */
+#define DSPARK_MAX_PAGE_SIZE 4096     /* positions in a page of the cache */
+#define DSPARK_CACHE_TILE 64          /* positions one entry of tile_off counts */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int dspark_version(void);
@@ -96,7 +100,9 @@ dspark_status dspark_workspace_set_wait_limit(void* ws, size_t ws_bytes, uint64_
  * raw status bits are stored there: bit 0 a token out of [0, V), bit 1 a
  * block length out of [0, gamma], bit 2 a bounded wait expired, bit 3 a
  * non-finite score or a temperature that is not positive and finite
- * (dspark_sts_fit), and with bit 2 the bits 8-23 name the wait that gave up
+ * (dspark_sts_fit), bit 4 a row of logits with no token left
+ * (dspark_logits_process), bit 5 a page or slot out of range, a block table
+ * too narrow or no free page left (the cache calls), and with bit 2 the bits 8-23 name the wait that gave up
  * (for diagnosis only). */
 dspark_status dspark_sync_status(void* ws, void* stream, uint32_t* bits);
 
@@ -392,6 +398,138 @@ dspark_status dspark_sts_fit(const float* score, const int32_t* acc_len, int N, 
                              const float* grid, int G, int M,
                              float* T_out, int32_t* idx_out, double* ece_out,
                              void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The paged key-value cache of the model that scores a block.  It serves the
+ * step around the verification: the gamma + 1 tokens of a request's block
+ * (the token before the drafts, and the admitted drafts) get slots
+ * (dspark_cache_plan), their keys and values are written there
+ * (dspark_cache_append), each of them attends to everything before it
+ * (dspark_cache_attention), and after the verification seq_len grows by the
+ * accepted count + 1: rejected positions are simply written again.
+ *
+ * Layout: k_cache and v_cache are [pages][kv_heads][page_size][head_dim],
+ * page_stride elements from one page to the next (so keys and values may
+ * alternate in one allocation, or belong to one layer of many).  Position i
+ * of request b lies in page block_table[b][i / page_size], row i % page_size.
+ *
+ * dspark_cache_plan: pages, slots and offsets of a step, from lengths on the
+ * device.  For request b, with len = seq_len[b] positions in the cache and
+ * n_new[b] tokens to come:
+ *     goal    = ceil((len + n_new) / page_size) pages; pages it lacks are
+ *               taken from the ring of free pages, pages beyond goal go back
+ *               (a request that has ended: len = n_new = 0).
+ *     kv_len  = len + n_new;  q_off = exclusive sums of n_new;  tile_off =
+ *               exclusive sums of ceil(kv_len / DSPARK_CACHE_TILE).
+ *     slot_map[t], positions[t] of token t = q_off[b] + i: the slot
+ *               block_table[b][pos / page_size] * page_size + pos % page_size
+ *               of pos = len + i, and pos.  From q_off[B] on: -1.
+ * Inputs : seq_len, n_new, owned [B] (owned pages: the entries of the block
+ *          table in use), ring [pages] and ring_state [2] = (head, free): the
+ *          free pages are ring[(head + i) % pages], i < free.
+ * Outputs: block_table [B][width] and ring, in place; owned_out [B] and
+ *          ring_state_out [2], which must not be owned and ring_state (the
+ *          next step's inputs); kv_len [B], q_off and tile_off [B+1], slot_map
+ *          and positions [max_tokens].  The same inputs give the same outputs,
+ *          so a repeated call is harmless.
+ * Requests are served in order while the ring has pages for them.  One that
+ * is not served (no page left, a table row too short, a negative length)
+ * keeps its pages, gets kv_len 0 and slots -1, and sets status bit 5.  More
+ * than max_tokens tokens set bit 1.
+ * ws     : NULL (no status), or any workspace of this library (its status word).
+ * Limits : 1 <= B <= DSPARK_MAX_CACHE_REQUESTS, pages * page_size < 2^31,
+ *          width * page_size < 2^31, max_tokens < 2^30.
+ */
+dspark_status dspark_cache_plan(
+    const int32_t* seq_len, const int32_t* n_new, const int32_t* owned, int B,
+    int32_t* ring, const int32_t* ring_state, int pages,
+    int32_t* block_table, int width, int page_size,
+    int32_t* owned_out, int32_t* ring_state_out, int32_t* kv_len,
+    int32_t* q_off, int32_t* tile_off, int32_t* slot_map, int32_t* positions,
+    int max_tokens, void* ws, void* stream);
+
+/*
+ * Write the keys and values of T tokens to their slots.
+ * Inputs : k, v [T][kv_heads][head_dim] (kv_t), k_stride and v_stride elements
+ *          between tokens (slices of a fused projection's output), slot_map
+ *          [T] (a negative slot: the token is skipped; one beyond the cache is
+ *          skipped and sets status bit 5).  No slot may appear twice.
+ * Outputs: k_cache, v_cache (layout above).
+ * Limits : head_dim % 8 == 0, <= DSPARK_MAX_HEAD_DIM; addresses and strides
+ *          multiples of 16 bytes.  ws as in dspark_cache_plan.
+ */
+dspark_status dspark_cache_append(
+    const void* k, const void* v, dspark_dtype kv_t, long long k_stride, long long v_stride,
+    const int32_t* slot_map, int T,
+    void* k_cache, void* v_cache, long long page_stride, int pages, int page_size,
+    int kv_heads, int head_dim, void* ws, void* stream);
+
+/*
+ * Attention of the new tokens over the cache.  Token i of request b (row
+ * q_off[b] + i of q) sits at position kv_len[b] - n + i, n = q_off[b+1] -
+ * q_off[b], and sees the positions up to its own; query head h uses key-value
+ * head h / (q_heads / kv_heads):
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j e^(scale * q . k_j).
+ * A row that sees no position (kv_len 0) gets out = 0 and lse = -inf.  What
+ * a page holds beyond kv_len is never used, whatever its bits.
+ * Inputs : q [N][q_heads][head_dim] (kv_t), q_stride elements between tokens;
+ *          caches, block_table, kv_len, q_off, tile_off as dspark_cache_plan
+ *          leaves them; max_new >= every n.
+ * Outputs: out [N][q_heads][head_dim] (kv_t); lse [N][q_heads] fp32 or NULL.
+ *          Rows outside q_off[0] .. q_off[B] are not written.
+ * Checks : a page out of range is left out and sets status bit 5; n above
+ *          max_new, offsets or lengths out of range set bit 1 (the rows
+ *          concerned are unspecified).
+ * ws     : dspark_cache_workspace_bytes(...) bytes, 256-byte aligned, cleared
+ *          once.  Results do not depend on what it holds.
+ * Limits : B as above, q_heads % kv_heads == 0, 1 <= max_new <=
+ *          DSPARK_MAX_GAMMA + 1, scale positive and finite, head_dim % 8 == 0,
+ *          <= DSPARK_MAX_HEAD_DIM, N * q_heads < 2^31.
+ */
+size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new);
+dspark_status dspark_cache_attention(
+    const void* q, long long q_stride, const void* k_cache, const void* v_cache, dspark_dtype kv_t,
+    long long page_stride, int pages, int page_size,
+    const int32_t* block_table, int width, const int32_t* kv_len, const int32_t* q_off, const int32_t* tile_off,
+    int B, int N, int q_heads, int kv_heads, int head_dim, int max_new, float scale,
+    void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on the logits that a
+ * verification (R = gamma + 1 target rows) or a draft (R = gamma rows of U)
+ * draws from.  Row i of request b follows the request's history and the first
+ * i drafted tokens, and its counts include them:
+ *     c(v)  = #{i >= prompt_len[b] : hist[b][i] = v} + #{j < i : draft_tok[b][j] = v}
+ *     x'    = x / rep if x > 0, x * rep otherwise, where v is in the history
+ *             (prompt included) or among those drafts; x elsewhere
+ *     y     = x' - freq * c(v) - pres * [c(v) > 0] + bias(v)
+ *     out   = y where bit v % 32 of mask[b][i][v / 32] is set, else -inf.
+ * Inputs : logits [B][R][V] (t), row_stride elements between rows (B * R rows
+ *          at one stride); hist [B][hist_stride] with hist_len [B] tokens, the
+ *          first prompt_len[b] (NULL: none) the prompt; draft_tok
+ *          [B][draft_stride >= R - 1]; rep, freq, pres [B] fp32; bias entries
+ *          bias_off[b] .. bias_off[b+1] of bias_tok (strictly ascending ids in
+ *          each request) and bias_val, bias_n in all; mask
+ *          [B][R][ceil(V/32)].  hist, draft_tok, rep (1), freq (0), pres (0),
+ *          bias_off and mask (everything allowed) may be NULL.
+ * Outputs: out [B][R][V] (t; may be logits itself where row_stride = V);
+ *          live [B][R] (or NULL): the entries of the row above -inf.  A row
+ *          with none sets status bit 4: no token can be drawn from it.
+ * Checks : a token id out of [0, V) is skipped and sets bit 0 (as do bias ids
+ *          out of order), a length or offset out of range bit 1, rep not
+ *          positive and finite bit 3.
+ * ws     : dspark_logits_workspace_bytes(B, R) bytes, 256-byte aligned,
+ *          cleared once.
+ * Limits : V % 8 == 0, 1 <= R <= DSPARK_MAX_GAMMA + 1, B <= 65535.
+ */
+size_t dspark_logits_workspace_bytes(int B, int R);
+dspark_status dspark_logits_process(
+    const void* logits, dspark_dtype t, long long row_stride, void* out, int B, int R, int V,
+    const int32_t* hist, int hist_stride, const int32_t* hist_len, const int32_t* prompt_len,
+    const int32_t* draft_tok, int draft_stride,
+    const float* rep, const float* freq, const float* pres,
+    const int32_t* bias_tok, const float* bias_val, const int32_t* bias_off, int bias_n,
+    const uint32_t* mask, int32_t* live, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Diagnostics: the random stream as the kernels draw it.  For columns

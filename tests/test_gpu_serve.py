@@ -1,0 +1,522 @@
+"""GPU tests of the serving operators (paged cache plan, append and attention,
+logit controls) against the 64-bit references of tests/_serve_ref.py."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _serve_ref as ref
+
+pytestmark = pytest.mark.gpu
+BAD_TOKEN, BAD_LENGTH, BAD_INPUT, DEAD_ROW, BAD_PAGE = 1, 2, 8, 16, 32
+
+
+@pytest.fixture(scope="module")
+def vm():
+    import verify_markov_head_gb300 as vm
+    return vm
+
+
+def _cu(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x), dtype=dtype).cuda()
+
+
+def _status(vm, ws):
+    return vm.dspark_sync_status(ws.buf)[1]
+
+
+# -------------------------------------------------------------------- plan
+def _plan_inputs(rng, B, P, hi, new_hi, width, spare, ended=0.1):
+    seq = rng.integers(0, hi + 1, B)
+    new = rng.integers(0, new_hi + 1, B)
+    owned = -(-seq // P)
+    owned = np.minimum(owned + (rng.random(B) < 0.3), width)
+    gone = rng.random(B) < ended
+    seq[gone] = 0
+    new[gone] = 0
+    pages = int(owned.sum()) + spare
+    perm = rng.permutation(pages)
+    table = np.full((B, width), -1)
+    o = 0
+    for b in range(B):
+        table[b, :owned[b]] = perm[o:o + owned[b]]
+        o += owned[b]
+    head = int(rng.integers(0, pages))
+    ring = np.roll(np.concatenate([perm[o:], np.full(o, -7)]), head)
+    return [a.astype(np.int32) for a in (seq, new, owned, ring)] + [np.array([head, spare], np.int32), table.astype(np.int32)]
+
+
+def _run_plan(vm, seq, new, owned, ring, state, table, P, T, ws=None, stream=None):
+    B = len(seq)
+    e = lambda n: torch.full((n,), -99, dtype=torch.int32, device="cuda")  # noqa: E731
+    o = dict(owned_out=e(B), ring_state_out=e(2), kv_len=e(B), q_off=e(B + 1), tile_off=e(B + 1), slot_map=e(T),
+             positions=e(T))
+    tab, rng_ = _cu(table), _cu(ring)
+    args = (_cu(seq), _cu(new), _cu(owned), rng_, _cu(state), tab, P)
+    for _ in range(2):                       # the same inputs give the same outputs
+        vm.dspark_cache_plan(*args, **o, ws=ws, stream=stream)
+    torch.cuda.synchronize()
+    return {k: v.cpu().numpy() for k, v in dict(o, block_table=tab, ring=rng_).items()}
+
+
+@pytest.mark.parametrize("B,P,hi,new_hi,spare", [
+    (1, 16, 40, 8, 9), (3, 1, 30, 8, 40), (64, 64, 5000, 8, 128), (513, 16, 300, 8, 700), (33, 24, 100, 90, 400),
+    (4096, 8, 50, 3, 4096), (40, 16, 200, 60, 37),     # the last: the ring runs out
+])
+def test_plan_matches_a_host_allocator(vm, B, P, hi, new_hi, spare):
+    rng = np.random.default_rng(B * 1000 + P)
+    width = -(-(hi + new_hi) // P) + 1
+    seq, new, owned, ring, state, table = _plan_inputs(rng, B, P, hi, new_hi, width, spare)
+    T = int(new.sum()) + 5
+    want = ref.plan(seq, new, owned, ring, state, table, P, T)
+    ws = vm.LogitsWorkspace(1, 1)
+    got = _run_plan(vm, seq, new, owned, ring, state, table, P, T, ws)
+    bad = want.pop("bad")
+    for k, v in want.items():
+        np.testing.assert_array_equal(got[k], v, err_msg=k)
+    assert _status(vm, ws) == (BAD_PAGE if bad else 0)
+
+
+def test_plan_reports_short_tables_negative_lengths_and_too_many_tokens(vm):
+    rng = np.random.default_rng(5)
+    seq, new, owned, ring, state, table = _plan_inputs(rng, 6, 16, 60, 8, 4, 20, ended=0.0)
+    seq[1], new[1] = 60, 8                   # 68 positions, a row holds 64
+    seq[3] = -5
+    new[4] = -1
+    ws = vm.LogitsWorkspace(1, 1)
+    T = 3
+    want = ref.plan(seq, new, owned, ring, state, table, 16, T)
+    got = _run_plan(vm, seq, new, owned, ring, state, table, 16, T, ws)
+    assert want.pop("bad")
+    for k in want:
+        if k != "positions":                 # the positions of a negative length are not defined
+            np.testing.assert_array_equal(got[k], want[k], err_msg=k)
+    assert _status(vm, ws) == BAD_PAGE | BAD_LENGTH
+
+
+def test_plan_chained_over_steps_never_shares_a_page(vm):
+    """Steps with random admitted and accepted counts: at every step the owned
+    pages and the free ones are a partition of all pages."""
+    rng = np.random.default_rng(8)
+    B, P, width, pages = 17, 8, 40, 420
+    table, ring = np.full((B, width), -1, np.int32), np.arange(pages, dtype=np.int32)
+    seq, owned, state = np.zeros(B, np.int32), np.zeros(B, np.int32), np.array([0, pages], np.int32)
+    for step in range(30):
+        new = rng.integers(1, 9, B).astype(np.int32)
+        ended = rng.random(B) < 0.05
+        ended |= seq + 8 > width * P
+        seq[ended], new[ended] = 0, 0
+        got = _run_plan(vm, seq, new, owned, ring, state, table, P, 8 * B)
+        table, ring, owned, state = got["block_table"], got["ring"], got["owned_out"], got["ring_state_out"]
+        held = np.concatenate([table[b, :owned[b]] for b in range(B)] + [ring[(state[0] + np.arange(state[1])) % pages]])
+        np.testing.assert_array_equal(np.sort(held), np.arange(pages))
+        slots = got["slot_map"][got["slot_map"] >= 0]
+        assert len(set(slots.tolist())) == int(new.sum())
+        seq = seq + np.minimum(new, rng.integers(1, 9, B)).astype(np.int32)     # accepted + 1
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,D,P", [(1, 1, 8, 1), (5, 3, 64, 24), (700, 8, 128, 16), (333, 2, 80, 64), (0, 2, 64, 8)])
+def test_append_writes_exactly_the_slots(vm, T, H, D, P, dtype):
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    pages = T // P + 4
+    qkv = torch.randn((T, 3 * H, D), generator=g, device="cuda").to(dtype)        # tokens at a stride
+    kv = torch.randn((pages, 2, H, P, D), generator=g, device="cuda").to(dtype)   # keys and values by turns
+    k, v = qkv[:, H:2 * H], qkv[:, 2 * H:]
+    slots = torch.randperm(pages * P, generator=g, device="cuda")[:T].to(torch.int32)
+    if T > 3:
+        slots[1], slots[3] = -1, pages * P + 7        # skipped; skipped and reported
+    want = kv.clone()
+    for t in range(T):
+        s = int(slots[t])
+        if 0 <= s < pages * P:
+            want[s // P, 0, :, s % P] = k[t]
+            want[s // P, 1, :, s % P] = v[t]
+    ws = vm.LogitsWorkspace(1, 1)
+    vm.dspark_cache_append(k, v, slots, kv[:, 0], kv[:, 1], ws=ws)
+    assert _status(vm, ws) == (BAD_PAGE if T > 3 else 0)
+    assert torch.equal(kv.view(torch.int16), want.view(torch.int16))
+
+
+# --------------------------------------------------------------- attention
+def _attention_inputs(rng, lens, news, Hq, Hkv, D, P, dtype, junk=True, q_pad=0, extra_pages=3):
+    """Caches whose unused places (other pages, rows beyond the length) hold
+    NaN, block tables with -1 beyond the owned pages."""
+    B, lens, news = len(lens), np.asarray(lens), np.asarray(news)
+    per = -(-lens // P)
+    width, pages = int(per.max()) + 1, int(per.sum()) + extra_pages
+    perm = rng.permutation(pages)
+    table = np.full((B, width), -1)
+    k, v = (np.full((pages, Hkv, P, D), np.nan if junk else 0.0, np.float32) for _ in range(2))
+    o = 0
+    for b in range(B):
+        table[b, :per[b]] = perm[o:o + per[b]]
+        o += per[b]
+        pos = np.arange(lens[b])
+        k[table[b, pos // P], :, pos % P] = rng.standard_normal((lens[b], Hkv, D))
+        v[table[b, pos // P], :, pos % P] = rng.standard_normal((lens[b], Hkv, D))
+    q_off = np.concatenate([[0], np.cumsum(news)])
+    N = int(q_off[-1])
+    q = torch.as_tensor(rng.standard_normal((N, Hq + q_pad, D)) * 2, dtype=torch.float32).to(dtype).cuda()[:, :Hq]
+    tile_off = np.concatenate([[0], np.cumsum(-(-lens // 64))])
+    return dict(q=q, k=torch.as_tensor(k).to(dtype).cuda(), v=torch.as_tensor(v).to(dtype).cuda(), table=_cu(table),
+                kv_len=_cu(lens), q_off=_cu(q_off), tile_off=_cu(tile_off))
+
+
+def _attend(vm, a, max_new, scale=None, ws=None, stream=None):
+    q = a["q"]
+    ws = ws or vm.CacheWorkspace(a["table"].shape[0], q.shape[1], a["k"].shape[1], q.shape[2], max_new)
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    vm.dspark_cache_attention(q, a["k"], a["v"], a["table"], a["kv_len"], a["q_off"], a["tile_off"], out, ws,
+                              max_new=max_new, scale=scale, lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    return out, lse, ws
+
+
+def _check_attention(a, out, lse, scale):
+    d = lambda t: t.cpu().double().numpy()  # noqa: E731
+    i = lambda t: t.cpu().numpy()  # noqa: E731
+    bf = a["q"].dtype == torch.bfloat16
+    want, wlse, tol, ltol = ref.attention(d(a["q"]), d(a["k"]), d(a["v"]), i(a["table"]), i(a["kv_len"]), i(a["q_off"]),
+                                          scale, ref.EPS16 if bf else 0.0, ref.EPS16 if bf else 4 * ref.EPS32)
+    got, glse = d(out), d(lse)
+    assert np.isfinite(got).all()
+    over = np.abs(got - want) / np.maximum(tol, 1e-30)
+    assert (np.abs(got - want) <= tol).all(), over.max()
+    empty = np.isinf(wlse)
+    np.testing.assert_array_equal(glse[empty], wlse[empty])
+    assert (np.abs(glse[~empty] - wlse[~empty]) <= ltol[~empty]).all()
+
+
+ATTENTION = [
+    # lens, news, Hq, Hkv, D, page size
+    ([1], [1], 4, 1, 64, 16),
+    ([64, 65, 63, 1, 128], [1, 1, 1, 1, 1], 8, 2, 128, 16),
+    ([0, 5, 0, 200], [2, 1, 0, 8], 4, 4, 64, 8),               # rows that see nothing, requests without a token
+    ([8, 130, 67, 9], [8, 3, 5, 8], 32, 8, 128, 64),           # blocks that fill the cache, ragged
+    ([300, 77], [8, 7], 14, 2, 64, 24),                        # 7 heads to a key head, an odd page size
+    ([500, 2, 129], [4, 2, 8], 16, 1, 128, 32),                # one key head: several tiles of rows
+    ([70], [17], 16, 2, 128, 1),                               # the longest block, pages of one position
+    ([1000, 1], [1, 1], 8, 8, 128, 128),                       # no shared heads
+    ([90, 33], [8, 2], 6, 2, 80, 16),                          # other head sizes: CUDA cores
+    ([90, 130], [3, 8], 4, 2, 256, 64),
+    ([45, 100], [8, 1], 8, 1, 8, 16),
+    ([4100], [8], 8, 2, 64, 64),                               # split over many CTAs
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("case", range(len(ATTENTION)))
+def test_attention_matches_the_definition(vm, case, dtype):
+    lens, news, Hq, Hkv, D, P = ATTENTION[case]
+    rng = np.random.default_rng(case)
+    a = _attention_inputs(rng, lens, news, Hq, Hkv, D, P, dtype, q_pad=case % 3)
+    out, lse, ws = _attend(vm, a, max(max(news), 1))
+    _check_attention(a, out, lse, D ** -0.5)
+    assert _status(vm, ws) == 0
+    again, lse2, _ = _attend(vm, a, max(max(news), 1), ws=ws)      # the same bits on a used workspace
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_attention_of_a_large_ragged_batch(vm):
+    rng = np.random.default_rng(77)
+    lens = rng.integers(1, 400, 150)
+    news = np.minimum(lens, rng.integers(1, 9, 150))
+    a = _attention_inputs(rng, lens, news, 8, 2, 64, 16, torch.bfloat16)
+    out, lse, ws = _attend(vm, a, 8)
+    _check_attention(a, out, lse, 64 ** -0.5)
+
+
+def test_attention_scale_and_large_scores(vm):
+    """A large scale makes the softmax a maximum: no overflow, the running
+    maximum carries over the tiles."""
+    rng = np.random.default_rng(3)
+    a = _attention_inputs(rng, [700, 40], [8, 8], 8, 2, 128, 16, torch.bfloat16)
+    out, lse, _ = _attend(vm, a, 8, scale=3.0)
+    _check_attention(a, out, lse, 3.0)
+
+
+def _vary_block_values(a, b, P, bad):
+    """The value of the last position of request b set to `bad` in every head."""
+    pos = int(a["kv_len"][b]) - 1
+    a["v"][int(a["table"][b, pos // P]), :, pos % P, ::3] = bad
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, dtype):
+    """A draft whose value is not finite: the rows before it, which do not see
+    it, are as they were; its own row is not finite where the value is not."""
+    rng = np.random.default_rng(4)
+    P = 16
+    a = _attention_inputs(rng, [70, 64, 8], [8, 5, 8], 8, 2, 128, P, dtype)
+    clean, _, _ = _attend(vm, a, 8)
+    for b in range(3):
+        _vary_block_values(a, b, P, bad)
+    got, _, _ = _attend(vm, a, 8)
+    last = (a["q_off"][1:] - 1).tolist()
+    for t in range(got.shape[0]):
+        if t in last:
+            assert not torch.isfinite(got[t, :, ::3].float()).any()
+            assert torch.isfinite(got[t, :, 1::3].float()).all()
+        else:
+            assert torch.equal(got[t], clean[t])
+
+
+def test_attention_reads_pages_beyond_32_bit_offsets(vm):
+    """Pages whose element offset passes 2^31, in caches of 2 x 4.4 GB."""
+    H, P, D = 8, 64, 128
+    pages = (1 << 31) // (H * P * D) + 600
+    k = torch.zeros((pages, H, P, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    rng = np.random.default_rng(9)
+    a = _attention_inputs(rng, [200, 64], [8, 1], 16, H, D, P, torch.bfloat16, extra_pages=0)
+    n = a["k"].shape[0]
+    k[pages - n:], v[pages - n:] = a["k"], a["v"]
+    big = dict(a, k=k, v=v, table=torch.where(a["table"] >= 0, a["table"] + pages - n, -1))
+    out, lse, _ = _attend(vm, a, 8)
+    out2, lse2, ws = _attend(vm, big, 8)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and _status(vm, ws) == 0
+    new_k = torch.randn((1, H, D), device="cuda").to(torch.bfloat16)
+    vm.dspark_cache_append(new_k, new_k, _cu([pages * P - 1]), k, v)
+    assert torch.equal(k[pages - 1, :, P - 1], new_k[0])
+
+
+def test_attention_on_another_stream_and_interleaved_caches(vm):
+    rng = np.random.default_rng(12)
+    a = _attention_inputs(rng, [300, 20], [8, 2], 8, 2, 128, 16, torch.bfloat16)
+    out, lse, _ = _attend(vm, a, 8)
+    kv = torch.stack([a["k"], a["v"]], 1)                   # [pages, 2, heads, page, dim]
+    b = dict(a, k=kv[:, 0], v=kv[:, 1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out2, lse2, _ = _attend(vm, b, 8, stream=s)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_attention_reports_bad_pages_and_lengths(vm):
+    rng = np.random.default_rng(13)
+    a = _attention_inputs(rng, [100, 50], [2, 2], 4, 2, 64, 16, torch.bfloat16)
+    out, _, ws = _attend(vm, a, 2)
+    hurt = dict(a, table=a["table"].clone())
+    hurt["table"][1, 1] = a["k"].shape[0]                   # a page that does not exist
+    got, _, _ = _attend(vm, hurt, 2, ws=ws)
+    assert _status(vm, ws) == BAD_PAGE
+    assert torch.equal(got[:2], out[:2]) and torch.isfinite(got.float()).all()
+    got, _, _ = _attend(vm, a, 1, ws=vm.CacheWorkspace(2, 4, 2, 64, 2))
+    ws2 = vm.CacheWorkspace(2, 4, 2, 64, 2)
+    _attend(vm, a, 1, ws=ws2)                               # two tokens a request, one announced
+    assert _status(vm, ws2) == BAD_LENGTH
+    far = dict(a, kv_len=a["kv_len"] + 100000)
+    _attend(vm, far, 2, ws=ws2)
+    assert _status(vm, ws2) & BAD_LENGTH
+
+
+def test_attention_in_a_cuda_graph(vm):
+    rng = np.random.default_rng(14)
+    a = _attention_inputs(rng, [300, 20], [8, 2], 8, 2, 128, 16, torch.bfloat16)
+    out, lse, ws = _attend(vm, a, 8)
+    got = torch.empty_like(out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        vm.dspark_cache_attention(a["q"], a["k"], a["v"], a["table"], a["kv_len"], a["q_off"], a["tile_off"], got, ws,
+                                  max_new=8)
+    for _ in range(3):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+
+
+# ------------------------------------------------------------------ logits
+def _logit_inputs(rng, B, R, V, dtype, L, masked=0.5, allowed=0.3):
+    x = torch.as_tensor(rng.standard_normal((B, R, V)) * 3, dtype=torch.float32).to(dtype)
+    hist = (V * rng.random((B, L)) ** 4).astype(np.int32)
+    hist_len = rng.integers(0, L + 1, B).astype(np.int32)
+    hist[np.arange(L)[None] >= hist_len[:, None]] = -12345      # beyond the length: never read
+    draft = (V * rng.random((B, R)) ** 4).astype(np.int32)      # one more than is used
+    mask = rng.random((B, R, V)) < allowed
+    mask[rng.random(B) >= masked] = True
+    mask[:, :, 3] = True
+    bias = []
+    for _ in range(B):
+        ids = np.sort(rng.choice(V, size=rng.integers(0, min(V, 40)), replace=False))
+        bias.append({int(i): float(np.float32(rng.standard_normal() * 4)) for i in ids})
+    f = lambda lo, hi: rng.uniform(lo, hi, B).astype(np.float32)  # noqa: E731
+    return dict(x=x, hist=hist, hist_len=hist_len, prompt_len=(hist_len // 2).astype(np.int32), draft=draft, mask=mask,
+                bias=bias, rep=f(0.7, 1.5), freq=f(-0.5, 0.7), pres=f(-0.3, 0.8))
+
+
+def _words(mask):
+    B, R, V = mask.shape
+    W = -(-V // 32)
+    bits = np.zeros((B, R, W * 32), np.uint64)
+    bits[:, :, :V] = mask
+    w = (bits.reshape(B, R, W, 32) << np.arange(32, dtype=np.uint64)).sum(-1)
+    return torch.as_tensor(w.astype(np.uint32).view(np.int32)).cuda()
+
+
+def _process(vm, a, ws=None, x=None, out=None, **drop):
+    x = a["x"].cuda() if x is None else x
+    B, R, V = x.shape
+    ws = ws or vm.LogitsWorkspace(B, R)
+    out = torch.empty((B, R, V), dtype=x.dtype, device="cuda") if out is None else out
+    live = torch.full((B, R), -9, dtype=torch.int32, device="cuda")
+    tok = [i for b in a["bias"] for i in b]
+    val = [w for b in a["bias"] for w in b.values()]
+    off = np.concatenate([[0], np.cumsum([len(b) for b in a["bias"]])])
+    kw = dict(hist=_cu(a["hist"]), hist_len=_cu(a["hist_len"]), prompt_len=_cu(a["prompt_len"]), draft_tok=_cu(a["draft"]),
+              rep=_cu(a["rep"], torch.float32), freq=_cu(a["freq"], torch.float32), pres=_cu(a["pres"], torch.float32),
+              bias_tok=_cu(tok), bias_val=_cu(val, torch.float32), bias_off=_cu(off), mask=_words(a["mask"]), live=live)
+    kw.update(drop)
+    vm.dspark_logits_process(x, out, ws, **kw)
+    torch.cuda.synchronize()
+    return out, live, ws
+
+
+def _check_logits(a, out, live, x=None, **drop):
+    x = (a["x"] if x is None else x).double().numpy()
+    B, R, V = x.shape
+    z, none = np.zeros(B), [dict() for _ in range(B)]
+    bf = out.dtype == torch.bfloat16
+    want, tol = ref.logits(x, a["hist"], z.astype(int) if "hist" in drop else a["hist_len"], a["prompt_len"], a["draft"],
+                           z + 1 if "rep" in drop else a["rep"].astype(float), z if "freq" in drop else a["freq"].astype(float),
+                           z if "pres" in drop else a["pres"].astype(float), none if "bias_off" in drop else a["bias"],
+                           None if "mask" in drop else a["mask"], ref.EPS16 if bf else 0.0)
+    got = out.cpu().double().numpy()
+    fin = np.isfinite(want)
+    np.testing.assert_array_equal(np.isfinite(got), fin)
+    np.testing.assert_array_equal(np.isneginf(got), np.isneginf(want))
+    err = np.abs(got[fin] - want[fin])
+    assert (err <= tol[fin]).all(), err.max()
+    np.testing.assert_array_equal(live.cpu().numpy(), (want > -np.inf).sum(2))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,R,V,L", [(1, 1, 8, 1), (3, 8, 1024, 50), (2, 17, 4104, 300), (5, 7, 32008, 3000), (40, 2, 264, 17)])
+def test_logits_match_the_definition(vm, B, R, V, L, dtype):
+    rng = np.random.default_rng(B * R + V)
+    a = _logit_inputs(rng, B, R, V, dtype, L)
+    out, live, ws = _process(vm, a)
+    _check_logits(a, out, live)
+    assert _status(vm, ws) == 0
+    again, live2, _ = _process(vm, a, ws=ws)                     # the counters are clear again
+    assert torch.equal(out, again) and torch.equal(live, live2)
+
+
+@pytest.mark.parametrize("drop", [("mask",), ("bias_off",), ("rep", "freq", "pres"), ("hist", "hist_len", "prompt_len"),
+                                  ("freq", "pres", "mask", "bias_off")])
+def test_logits_without_some_controls(vm, drop):
+    rng = np.random.default_rng(len(drop))
+    a = _logit_inputs(rng, 3, 8, 4104, torch.float32, 200)
+    out, live, _ = _process(vm, a, **{k: None for k in drop})
+    _check_logits(a, out, live, **{k: None for k in drop})
+
+
+def test_logits_in_place_and_strided_rows(vm):
+    rng = np.random.default_rng(21)
+    a = _logit_inputs(rng, 4, 5, 1032, torch.bfloat16, 60)
+    want, live, _ = _process(vm, a)
+    x = a["x"].cuda()
+    got, live2, _ = _process(vm, a, x=x, out=x)
+    assert torch.equal(got, want) and torch.equal(live, live2)
+    wide = torch.full((4, 5, 1032 + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, :, :1032] = a["x"].cuda()
+    got, live2, _ = _process(vm, a, x=wide[:, :, :1032])
+    assert torch.equal(got, want) and torch.equal(live, live2)
+
+
+def test_logits_with_infinities_nan_and_the_lowest_value(vm):
+    """NaN or infinity under the mask disappear; -inf and the type's lowest
+    value in allowed places stay what the formula makes of them."""
+    rng = np.random.default_rng(22)
+    for dtype in (torch.float32, torch.bfloat16):
+        a = _logit_inputs(rng, 2, 4, 520, dtype, 40, masked=1.0)
+        hidden = torch.as_tensor(~a["mask"])
+        x = a["x"].clone()
+        low = torch.finfo(dtype).min
+        x[:, :, 10:60] = -float("inf")
+        x[:, :, 60:110] = low
+        x[hidden] = float("nan")
+        x[:, 1][hidden[:, 1]] = float("inf")
+        out, live, _ = _process(vm, a, x=x.cuda())
+        y = out.float().cpu()
+        assert torch.isneginf(y[hidden]).all()
+        assert not torch.isnan(y).any() and not (y == float("inf")).any()
+        seen = ~hidden
+        assert torch.isneginf(y[:, :, 10:60]).all()
+        np.testing.assert_array_equal(live.cpu().numpy(), (y > -float("inf")).sum(2).numpy())
+        assert (y[:, :, 60:110][seen[:, :, 60:110]] < -1e38).all()
+
+
+def test_logits_report_rows_with_nothing_left_and_bad_inputs(vm):
+    rng = np.random.default_rng(23)
+    a = _logit_inputs(rng, 3, 4, 1024, torch.float32, 50)
+    a["mask"][1, 2] = False
+    out, live, ws = _process(vm, a)
+    _check_logits(a, out, live)
+    assert int(live[1, 2]) == 0 and _status(vm, ws) == DEAD_ROW
+    a["mask"][1, 2] = True
+    ok, _, _ = _process(vm, a, ws=ws)
+    assert _status(vm, ws) == 0
+    hist = a["hist"].copy()
+    hist_len = a["hist_len"].copy()
+    hist_len[0] = 50
+    hist[0, 7] = 1024
+    _process(vm, dict(a, hist=np.where(hist < 0, 0, hist), hist_len=hist_len), ws=ws)
+    assert _status(vm, ws) == BAD_TOKEN
+    long = a["hist_len"].copy()
+    long[2] = 51
+    _process(vm, dict(a, hist=np.where(a["hist"] < 0, 0, a["hist"]), hist_len=long), ws=ws)
+    assert _status(vm, ws) == BAD_LENGTH
+    rep = a["rep"].copy()
+    rep[0] = 0.0
+    _process(vm, dict(a, rep=rep), ws=ws)
+    assert _status(vm, ws) == BAD_INPUT
+    tok = _cu([5, 5])
+    _process(vm, a, ws=ws, bias_tok=tok, bias_val=tok.float(), bias_off=_cu([0, 2, 2, 2]))
+    assert _status(vm, ws) == BAD_TOKEN
+    _process(vm, a, ws=ws, bias_tok=tok, bias_val=tok.float(), bias_off=_cu([0, 9, 9, 9]))
+    assert _status(vm, ws) == BAD_LENGTH
+
+
+# ---------------------------------------------------------------- refusals
+def test_the_binding_refuses_wrong_shapes_types_and_strides(vm):
+    rng = np.random.default_rng(31)
+    a = _attention_inputs(rng, [20], [2], 4, 2, 64, 16, torch.bfloat16)
+    ws = vm.CacheWorkspace(1, 4, 2, 64, 2)
+    out = torch.empty_like(a["q"])
+    call = lambda **kw: vm.dspark_cache_attention(*[{**a, "out": out, **kw}[n] for n in (  # noqa: E731
+        "q", "k", "v", "table", "kv_len", "q_off", "tile_off", "out")], kw.get("ws", ws), max_new=kw.get("max_new", 2),
+        scale=kw.get("scale"))
+    call()
+    for kw, err in ((dict(q=a["q"].float()), ValueError), (dict(v=a["v"][:, :, ::2]), ValueError),
+                    (dict(kv_len=a["kv_len"].long()), TypeError), (dict(tile_off=a["tile_off"][:1]), ValueError),
+                    (dict(k=a["k"].transpose(1, 2), v=a["v"].transpose(1, 2)), ValueError),
+                    (dict(max_new=18), vm.DsparkError), (dict(max_new=0), vm.DsparkError),
+                    (dict(scale=0.0), vm.DsparkError), (dict(scale=float("nan")), vm.DsparkError),
+                    (dict(k=a["k"][:, :, :, :60].contiguous(), v=a["v"][:, :, :, :60].contiguous()), ValueError)):
+        with pytest.raises(err):
+            call(**kw)
+    with pytest.raises(vm.DsparkError):                       # a workspace for fewer rows
+        big = _attention_inputs(rng, [20], [2], 64, 2, 64, 16, torch.bfloat16)
+        vm.dspark_cache_attention(big["q"], big["k"], big["v"], big["table"], big["kv_len"], big["q_off"],
+                                  big["tile_off"], torch.empty_like(big["q"]), ws, max_new=2)
+    with pytest.raises(ValueError):
+        vm.CacheWorkspace(1, 5, 2, 64, 2)
+    x = torch.zeros((2, 3, 64), device="cuda")
+    lw = vm.LogitsWorkspace(2, 3)
+    for kw, err in ((dict(hist=_cu(np.zeros((2, 4)))), ValueError), (dict(draft_tok=_cu(np.zeros((2, 1)))), ValueError),
+                    (dict(rep=torch.ones(2, dtype=torch.float64, device="cuda")), TypeError),
+                    (dict(mask=_cu(np.zeros((2, 3, 3)))), ValueError)):
+        with pytest.raises(err):
+            vm.dspark_logits_process(x, torch.empty_like(x), lw, **kw)
+    odd = torch.zeros((2, 3, 60), device="cuda")
+    with pytest.raises(vm.DsparkError):
+        vm.dspark_logits_process(odd, torch.empty_like(odd), lw)
+    with pytest.raises(vm.DsparkError):
+        many = torch.zeros((70, 3, 64), device="cuda")         # a workspace for fewer requests
+        vm.dspark_logits_process(many, torch.empty_like(many), lw)

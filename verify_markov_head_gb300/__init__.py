@@ -21,19 +21,21 @@ __all__ = [
     "DsparkError", "lib_path", "dspark_version", "dspark_status_string", "dspark_workspace_bytes",
     "dspark_workspace_init", "dspark_workspace_set_wait_limit", "dspark_sync_status", "dspark_draft_markov", "dspark_confidence_sts",
     "dspark_schedule", "dspark_verify", "dspark_draft_markov_target", "target_stream_supported", "dspark_draft_rnn", "dspark_verify_rnn", "dspark_verify_logits", "dspark_rnn_input_table", "rnn_prepare", "dspark_sts_workspace_bytes", "dspark_sts_fit", "dspark_gumbel_stream", "dspark_draft_markov_noalloc", "dspark_noalloc_sync_status", "Workspace", "StepBuffers", "run_step", "run_step_host", "run_step_dp", "GlobalSchedule", "HostPipeline",
+    "dspark_cache_plan", "dspark_cache_append", "dspark_cache_workspace_bytes", "dspark_cache_attention", "dspark_logits_workspace_bytes", "dspark_logits_process", "CacheWorkspace", "LogitsWorkspace", "CACHE_TILE",
     "SCHED_OFF", "SCHED_SYNC", "SCHED_ASYNC",
 ]
 
 SCHED_OFF, SCHED_SYNC, SCHED_ASYNC = 0, 1, 2
 STORE_LOGITS_BYTES = 64 << 20   # StepBuffers keeps the draft logits up to this size
 _F32, _BF16 = 0, 1
+CACHE_TILE = 64                  # cache positions one entry of tile_off counts
 
 lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libdspark.so")
 if not os.path.exists(lib_path):
     raise ImportError(f"libdspark.so is not built ({lib_path}); run verify_markov_head_gb300/build.py")
 _lib = C.CDLL(lib_path)
 
-_vp, _i, _f, _u64, _sz = C.c_void_p, C.c_int, C.c_float, C.c_uint64, C.c_size_t
+_vp, _i, _f, _u64, _sz, _ll = C.c_void_p, C.c_int, C.c_float, C.c_uint64, C.c_size_t, C.c_longlong
 _lib.dspark_version.restype = _i
 _lib.dspark_status_string.argtypes = [_i]
 _lib.dspark_status_string.restype = C.c_char_p
@@ -84,6 +86,21 @@ _lib.dspark_sts_fit.argtypes = [_vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _v
 _lib.dspark_sts_fit.restype = _i
 _lib.dspark_gumbel_stream.argtypes = [_u64, _u64, C.c_uint32, C.c_uint32, _i, _vp, _vp, _vp]
 _lib.dspark_gumbel_stream.restype = _i
+_lib.dspark_cache_plan.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i,
+                                   _vp, _vp]
+_lib.dspark_cache_plan.restype = _i
+_lib.dspark_cache_append.argtypes = [_vp, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp, _ll, _i, _i, _i, _i, _vp, _vp]
+_lib.dspark_cache_append.restype = _i
+_lib.dspark_cache_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
+_lib.dspark_cache_workspace_bytes.restype = _sz
+_lib.dspark_cache_attention.argtypes = [_vp, _ll, _vp, _vp, _i, _ll, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                        _i, _f, _vp, _vp, _vp, _sz, _vp]
+_lib.dspark_cache_attention.restype = _i
+_lib.dspark_logits_workspace_bytes.argtypes = [_i, _i]
+_lib.dspark_logits_workspace_bytes.restype = _sz
+_lib.dspark_logits_process.argtypes = [_vp, _i, _ll, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp,
+                                       _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]
+_lib.dspark_logits_process.restype = _i
 
 
 class DsparkError(RuntimeError):
@@ -407,6 +424,164 @@ def dspark_noalloc_sync_status(stream=None):
 def dspark_gumbel_stream(seed, step, domain, row, n, gumbel_out=None, uniform_out=None, stream=None):
     _check("dspark_gumbel_stream", _lib.dspark_gumbel_stream(
         int(seed), int(step), int(domain), int(row), int(n), _p(gumbel_out), _p(uniform_out), _stream(stream)))
+
+
+class _Scratch(Workspace):
+    """Device scratch of a given size, cleared once; its status word is read
+    with dspark_sync_status(ws.buf)."""
+
+    def __init__(self, nbytes, device="cuda", stream=None):
+        if nbytes == 0:
+            raise ValueError("sizes out of range")
+        self.tensor = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        off = (-self.tensor.data_ptr()) % 256
+        self.buf = self.tensor[off:off + nbytes]
+        dspark_workspace_init(self.buf, stream)
+        torch.cuda.synchronize(self.buf.device)
+
+
+class CacheWorkspace(_Scratch):
+    """Workspace of the cache calls for B requests of at most max_new new
+    tokens, q_heads query heads over kv_heads key-value heads of head_dim."""
+
+    def __init__(self, B, q_heads, kv_heads, head_dim, max_new, device="cuda", stream=None):
+        super().__init__(dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new), device, stream)
+
+
+class LogitsWorkspace(_Scratch):
+    """Workspace of dspark_logits_process for B requests of R rows."""
+
+    def __init__(self, B, R, device="cuda", stream=None):
+        super().__init__(dspark_logits_workspace_bytes(B, R), device, stream)
+
+
+def dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new) -> int:
+    return int(_lib.dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new))
+
+
+def dspark_logits_workspace_bytes(B, R) -> int:
+    return int(_lib.dspark_logits_workspace_bytes(B, R))
+
+
+def _typed(t, dtype, shape, name):
+    """Address of a contiguous tensor of the given type and shape (None: any size)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return _p(t)
+
+
+def _cache_pair(k_cache, v_cache):
+    """(dtype code, page stride) of two caches [pages, kv_heads, page_size,
+    head_dim] whose pages are contiguous."""
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must share shape, dtype and strides")
+    _, H, P, D = k_cache.shape
+    if k_cache.stride()[1:] != (P * D, D, 1):
+        raise ValueError("a page of the cache must be contiguous [kv_heads, page_size, head_dim]")
+    return _dt(k_cache), k_cache.stride(0)
+
+
+def _token_stride(t, name):
+    """Elements between tokens of t [T, heads, head_dim], whose tokens are contiguous."""
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def dspark_cache_plan(seq_len, n_new, owned, ring, ring_state, block_table, page_size, *, owned_out, ring_state_out,
+                      kv_len, q_off, tile_off, slot_map, positions, ws: Workspace = None, stream=None):
+    """Pages, slots and offsets of a step from lengths on the device: seq_len,
+    n_new, owned [B] and ring [pages], ring_state [2] = (head, free) int32;
+    block_table [B, width] and ring are updated in place, owned_out and
+    ring_state_out are the next step's owned and ring_state."""
+    B, width = block_table.shape
+    T = slot_map.shape[0]
+    i32, b = torch.int32, (B,)
+    _check("dspark_cache_plan", _lib.dspark_cache_plan(
+        _typed(seq_len, i32, b, "seq_len"), _typed(n_new, i32, b, "n_new"), _typed(owned, i32, b, "owned"), B,
+        _typed(ring, i32, None, "ring"), _typed(ring_state, i32, (2,), "ring_state"), ring.numel(),
+        _typed(block_table, i32, None, "block_table"), width, page_size, _typed(owned_out, i32, b, "owned_out"),
+        _typed(ring_state_out, i32, (2,), "ring_state_out"), _typed(kv_len, i32, b, "kv_len"),
+        _typed(q_off, i32, (B + 1,), "q_off"), _typed(tile_off, i32, (B + 1,), "tile_off"),
+        _typed(slot_map, i32, (T,), "slot_map"), _typed(positions, i32, (T,), "positions"), T,
+        None if ws is None else ws.ptr(), _stream(stream)))
+
+
+def dspark_cache_append(k, v, slot_map, k_cache, v_cache, *, ws: Workspace = None, stream=None):
+    """Write keys and values k, v [T, kv_heads, head_dim] (any token stride)
+    to the slots slot_map [T] int32 of the caches; negative slots are skipped."""
+    T, H, D = k.shape
+    t, page_stride = _cache_pair(k_cache, v_cache)
+    pages, Hc, P, Dc = k_cache.shape
+    if v.shape != k.shape or (Hc, Dc) != (H, D) or k.dtype != k_cache.dtype or v.dtype != k.dtype:
+        raise ValueError("k and v must be [T, kv_heads, head_dim] of the cache's heads and dtype")
+    _check("dspark_cache_append", _lib.dspark_cache_append(
+        k.data_ptr(), v.data_ptr(), t, _token_stride(k, "k"), _token_stride(v, "v"),
+        _typed(slot_map, torch.int32, (T,), "slot_map"), T, k_cache.data_ptr(), v_cache.data_ptr(), page_stride, pages, P,
+        H, D, None if ws is None else ws.ptr(), _stream(stream)))
+
+
+def dspark_cache_attention(q, k_cache, v_cache, block_table, kv_len, q_off, tile_off, out, ws: Workspace, *, max_new,
+                           scale=None, lse=None, stream=None):
+    """Attention of the new tokens q [N, q_heads, head_dim] (any token stride)
+    over the paged cache: out [N, q_heads, head_dim], lse [N, q_heads] fp32 or
+    None.  scale defaults to head_dim ** -0.5; max_new bounds the new tokens
+    of a request."""
+    N, Hq, D = q.shape
+    t, page_stride = _cache_pair(k_cache, v_cache)
+    pages, Hkv, P, Dc = k_cache.shape
+    B, width = block_table.shape
+    if Dc != D or q.dtype != k_cache.dtype or out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("q and out must be [N, q_heads, head_dim] of the cache's head_dim and dtype")
+    i32 = torch.int32
+    _check("dspark_cache_attention", _lib.dspark_cache_attention(
+        q.data_ptr(), _token_stride(q, "q"), k_cache.data_ptr(), v_cache.data_ptr(), t, page_stride, pages, P,
+        _typed(block_table, i32, None, "block_table"), width, _typed(kv_len, i32, (B,), "kv_len"),
+        _typed(q_off, i32, (B + 1,), "q_off"), _typed(tile_off, i32, (B + 1,), "tile_off"), B, N, Hq, Hkv, D, max_new,
+        D ** -0.5 if scale is None else scale, _p(out),
+        None if lse is None else _typed(lse, torch.float32, (N, Hq), "lse"), ws.ptr(), ws.nbytes(), _stream(stream)))
+
+
+def dspark_logits_process(logits, out, ws: Workspace, *, hist=None, hist_len=None, prompt_len=None, draft_tok=None,
+                          rep=None, freq=None, pres=None, bias_tok=None, bias_val=None, bias_off=None, mask=None,
+                          live=None, stream=None):
+    """Penalties, biases and grammar masks on logits [B, R, V] (rows at one
+    stride), written to out [B, R, V] (may be logits itself).  hist [B, L]
+    int32 with hist_len (and prompt_len) [B]; draft_tok [B, >= R-1]: the
+    drafts before each row; rep, freq, pres [B] fp32; bias_tok, bias_val,
+    bias_off [B+1]: ascending ids per request; mask [B, R, ceil(V/32)] int32
+    words; live [B, R] int32 receives the entries left in each row."""
+    B, R, V = logits.shape
+    f32, i32, b = torch.float32, torch.int32, (B,)
+    if out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the logits' shape and dtype")
+    rs = logits.stride(1) if R > 1 else logits.stride(0)
+    if logits.stride(2) != 1 or (B > 1 and logits.stride(0) != R * rs):
+        raise ValueError("the rows of logits must lie at one stride")
+    if B * R == 1:
+        rs = V
+    if draft_tok is not None and (draft_tok.shape[0] != B or draft_tok.shape[1] < R - 1):
+        raise ValueError("draft_tok must be [B, R-1] or wider")
+    if (hist is None) != (hist_len is None):
+        raise ValueError("hist and hist_len go together")
+    n_bias = 0
+    if bias_off is not None:
+        n_bias = bias_tok.numel()
+        if bias_val.numel() != n_bias:
+            raise ValueError("bias_tok and bias_val must have one entry each")
+    opt = lambda t, dt, shape, name: None if t is None else _typed(t, dt, shape, name)  # noqa: E731
+    _check("dspark_logits_process", _lib.dspark_logits_process(
+        logits.data_ptr(), _dt(logits), rs, _p(out), B, R, V,
+        opt(hist, i32, None if hist is None else (B, hist.shape[1]), "hist"), 0 if hist is None else hist.shape[1],
+        opt(hist_len, i32, b, "hist_len"), opt(prompt_len, i32, b, "prompt_len"),
+        opt(draft_tok, i32, None, "draft_tok"), 0 if draft_tok is None else draft_tok.shape[1],
+        opt(rep, f32, b, "rep"), opt(freq, f32, b, "freq"), opt(pres, f32, b, "pres"),
+        None if bias_off is None else _typed(bias_tok, i32, None, "bias_tok"),
+        None if bias_off is None else _typed(bias_val, f32, None, "bias_val"), opt(bias_off, i32, (B + 1,), "bias_off"),
+        n_bias, opt(mask, i32, (B, R, -(-V // 32)), "mask"), opt(live, i32, (B, R), "live"), ws.ptr(), ws.nbytes(),
+        _stream(stream)))
 
 
 class StepBuffers:

@@ -1,0 +1,250 @@
+// cache.cu -- the paged key-value cache beside the verification: the plan of
+// a step (which pages each request owns, where its new tokens go) and the
+// append of new keys and values.
+#include "serve.cuh"
+
+namespace dspark {
+namespace {
+
+// ------------------------------------------------------------------- plan
+// For request b with len_b positions in the cache and new_b tokens to come:
+//     goal_b = ceil((len_b + new_b) / P)    pages it needs,
+//     need_b = max(0, goal_b - owned_b)     taken from the front of the ring,
+//     give_b = max(0, owned_b - goal_b)     put back at its end,
+// and every place follows from exclusive sums over b of new_b, need_b, give_b
+// and the attention tiles.  The pages taken are ring[head + i], the pages
+// returned go to ring[head + free + i]: the two ranges never meet, since the
+// ring has room for every page, so one launch does both and the same inputs
+// always give the same outputs.
+//
+// A few kilobytes are read and written, so latency bounds it.  Each CTA forms
+// the sums over all requests itself (B <= 4096 lengths, a few loads a thread)
+// instead of waiting for another launch, and then fills its share of the slot
+// map, the table entries and the ring entries.
+constexpr int kPlanThreads = 1024;
+
+struct Sum4 { int tok, need, give, tiles; };
+
+// sums stop at 2^30 (the totals of valid inputs stay below it), so lengths out
+// of range cannot wrap an index
+__device__ __forceinline__ int add_sat(int a, int b) { return min(a + b, 1 << 30); }
+__device__ __forceinline__ Sum4 operator+(const Sum4& a, const Sum4& b) {
+    return Sum4{add_sat(a.tok, b.tok), add_sat(a.need, b.need), add_sat(a.give, b.give), add_sat(a.tiles, b.tiles)};
+}
+__device__ __forceinline__ Sum4 shfl_up(const Sum4& a, int d) {
+    return Sum4{__shfl_up_sync(~0u, a.tok, d), __shfl_up_sync(~0u, a.need, d), __shfl_up_sync(~0u, a.give, d),
+                __shfl_up_sync(~0u, a.tiles, d)};
+}
+
+struct PlanItem {
+    int fresh;     // new tokens
+    int need;      // pages it asks for (0 where it cannot be served)
+    int goal;
+    int owned;
+    int seq;
+    bool ok;       // lengths in range and table wide enough
+};
+
+__device__ __forceinline__ PlanItem plan_item(const PlanParams& p, int b) {
+    PlanItem it;
+    it.seq = p.seq_len[b];
+    it.fresh = p.n_new[b];
+    it.owned = p.owned[b];
+    it.ok = it.seq >= 0 && it.fresh >= 0 && it.owned >= 0 && it.owned <= p.width;
+    it.fresh = min(max(0, it.fresh), 1 << 30);
+    const long long goal = ((long long)it.seq + it.fresh + p.page_size - 1) / p.page_size;
+    it.ok = it.ok && goal <= p.width;
+    it.goal = it.ok ? (int)goal : it.owned;
+    it.need = it.ok ? max(0, it.goal - it.owned) : 0;
+    return it;
+}
+
+// first b in [0, B) with off[b + 1] > x
+__device__ __forceinline__ int owner_of(const int* off, int B, int x) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanParams p) {
+    extern __shared__ int sm[];
+    int* s_q = sm;                      // [B + 1] exclusive sums of the new tokens
+    int* s_need = s_q + p.B + 1;        // [B + 1] of the pages asked for
+    int* s_give = s_need + p.B + 1;     // [B + 1] of the pages returned
+    __shared__ Sum4 s_warp[32];
+    __shared__ int s_popped;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int B = p.B;
+    int head = p.ring_state[0], avail = p.ring_state[1];
+    bool bad = false;
+    bool state_ok = head >= 0 && head < p.pages && avail >= 0 && avail <= p.pages;
+    if (!state_ok) { head = 0; avail = 0; }
+    if (tid == 0) s_popped = 0;
+
+    // pass 1: the pages asked for decide who can be served
+    const int per = (B + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    auto block_scan = [&](Sum4 v) {     // exclusive over the threads
+        Sum4 x = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const Sum4 y = shfl_up(x, d);
+            if (lane >= d) x = x + y;
+        }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        if (warp == 0) {
+            Sum4 w = s_warp[lane];
+            Sum4 z = w;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const Sum4 y = shfl_up(z, d);
+                if (lane >= d) z = z + y;
+            }
+            s_warp[lane] = Sum4{z.tok - w.tok, z.need - w.need, z.give - w.give, z.tiles - w.tiles};
+        }
+        __syncthreads();
+        const Sum4 o = s_warp[warp];
+        __syncthreads();
+        return Sum4{x.tok - v.tok + o.tok, x.need - v.need + o.need, x.give - v.give + o.give,
+                    x.tiles - v.tiles + o.tiles};
+    };
+    Sum4 mine{0, 0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const PlanItem it = plan_item(p, b);
+        mine = mine + Sum4{it.fresh, it.need, 0, 0};
+    }
+    Sum4 at = block_scan(mine);
+    // pass 2: requests are served in order while the ring has pages for them
+    Sum4 second{0, 0, 0, 0};
+    {
+        int need = at.need;
+        for (int b = b0; b < b1; ++b) {
+            const PlanItem it = plan_item(p, b);
+            const bool served = it.ok && (it.need == 0 || need + it.need <= avail);
+            need = add_sat(need, it.need);
+            if (served) {
+                second = second + Sum4{0, 0, max(0, it.owned - it.goal), (it.seq + it.fresh + kTile - 1) / kTile};
+                if (it.need) atomicAdd(&s_popped, it.need);     // an integer sum: any order gives the same
+            }
+        }
+    }
+    const Sum4 at2 = block_scan(second);
+    {
+        int tok = at.tok, need = at.need, give = at2.give, tiles = at2.tiles;
+        for (int b = b0; b < b1; ++b) {
+            const PlanItem it = plan_item(p, b);
+            const bool served = it.ok && (it.need == 0 || need + it.need <= avail);
+            bad |= !served;
+            s_q[b] = tok; s_need[b] = need; s_give[b] = give;
+            if (blockIdx.x == 0) {
+                p.owned_out[b] = served ? it.goal : it.owned;
+                p.kv_len[b] = served ? it.seq + it.fresh : 0;
+                p.q_off[b] = tok;
+                p.tile_off[b] = tiles;
+            }
+            tok = add_sat(tok, it.fresh);
+            need = add_sat(need, it.need);
+            if (served) {
+                give = add_sat(give, max(0, it.owned - it.goal));
+                tiles = add_sat(tiles, (it.seq + it.fresh + kTile - 1) / kTile);
+            }
+            if (b == B - 1) {
+                s_q[B] = tok; s_need[B] = need; s_give[B] = give;
+                if (blockIdx.x == 0) { p.q_off[B] = tok; p.tile_off[B] = tiles; }
+            }
+        }
+    }
+    __syncthreads();
+    const int popped = s_popped, given = s_give[B], tokens = s_q[B];
+    if (blockIdx.x == 0) {
+        if (bad) raise_status(p.status, kBadPage);
+        if (tid == 0) {
+            p.ring_state_out[0] = (int)(((long long)head + popped) % p.pages);
+            p.ring_state_out[1] = avail - popped + given;
+            if (!state_ok) raise_status(p.status, kBadPage);
+            if (tokens > p.T) raise_status(p.status, kBadLength);
+        }
+    }
+    auto ring_at = [&](long long i) { return (int)(((long long)head + i) % p.pages); };
+    const int g0 = blockIdx.x * kPlanThreads + tid, gs = gridDim.x * kPlanThreads;
+    // the pages that change hands
+    for (int g = g0; g < popped; g += gs) {
+        const int b = owner_of(s_need, B, g);
+        const int j = p.owned[b] + (g - s_need[b]);
+        if (j >= 0 && j < p.width) p.table[(size_t)b * p.width + j] = p.ring[ring_at(g)];
+    }
+    for (int g = g0; g < given; g += gs) {
+        const int b = owner_of(s_give, B, g);
+        const PlanItem it = plan_item(p, b);
+        const int j = it.goal + (g - s_give[b]);
+        if (j >= 0 && j < it.owned) p.ring[ring_at((long long)avail + g)] = p.table[(size_t)b * p.width + j];
+    }
+    // the slot of every new token; a page taken in this call is read from the
+    // ring, since another CTA may not have written the table yet
+    for (int t = g0; t < p.T; t += gs) {
+        int slot = -1, pos = -1;
+        if (t < tokens) {
+            const int b = owner_of(s_q, B, t);
+            const PlanItem it = plan_item(p, b);
+            pos = it.seq + (t - s_q[b]);
+            if (it.ok && t - s_q[b] < it.fresh && (it.need == 0 || s_need[b] + it.need <= avail)) {
+                const int j = pos / p.page_size;
+                const int page = j < it.owned ? p.table[(size_t)b * p.width + j]
+                                              : p.ring[ring_at((long long)s_need[b] + j - it.owned)];
+                if (page >= 0 && page < p.pages) slot = page * p.page_size + (pos - j * p.page_size);
+                else raise_status(p.status, kBadPage);
+            }
+        }
+        p.slot_map[t] = slot;
+        p.positions[t] = pos;
+    }
+}
+
+// ----------------------------------------------------------------- append
+// cache[slot] = row: a copy, bound by HBM for prompts and by latency for a
+// block.  One thread moves 16 bytes of a key and of the value beside it.
+__global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams p) {
+    const int vecs = p.row_bytes / 16, per = p.heads * vecs;
+    const long long total = (long long)p.T * per;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
+        const int t = (int)(i / per), e = (int)(i - (long long)t * per);
+        const int slot = p.slot_map[t];
+        if (slot < 0) continue;
+        const int page = slot / p.page_size, row = slot - page * p.page_size;
+        if (page >= p.pages) { raise_status(p.status, kBadPage); continue; }
+        const int h = e / vecs, c = e - h * vecs;
+        const uint4 k = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_stride) + e);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_stride) + e);
+        const long long o = page * p.page_bytes + ((long long)h * p.page_size + row) * p.row_bytes + 16 * c;
+        *reinterpret_cast<uint4*>(p.k_cache + o) = k;
+        *reinterpret_cast<uint4*>(p.v_cache + o) = v;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
+    const size_t smem = sizeof(int) * 3 * ((size_t)p.B + 1);
+    cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int items = p.T > p.B ? p.T : p.B;
+    int grid = (items + kPlanThreads - 1) / kPlanThreads;
+    if (grid > num_sms()) grid = num_sms();
+    cache_plan_kernel<<<grid, kPlanThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t s) {
+    if (p.T == 0) return cudaSuccess;
+    const long long total = (long long)p.T * p.heads * (p.row_bytes / 16);
+    long long grid = (total + 255) / 256;
+    if (grid > 8LL * num_sms()) grid = 8LL * num_sms();
+    cache_append_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace dspark

@@ -1,0 +1,129 @@
+// serve.cuh -- parameter blocks, work partition and launchers of the serving
+// operators around the draft + verify step: the paged key-value cache (plan,
+// append, attention) and the controls on logits.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dspark {
+
+// Status bits of the serving operators (beside those of common.cuh).
+enum ServeStatusBits : uint32_t {
+    kDeadRow = 1u << 4,      // a processed row of logits has no token left
+    kBadPage = 1u << 5,      // a page or slot out of range, a block table too narrow, or no free page left
+};
+
+constexpr int kTile = DSPARK_CACHE_TILE;   // cache positions per attention tile
+constexpr int kMaxAttnCtas = 320;          // CTAs of an attention launch (bounds its partial results)
+constexpr int kMaxRowTile = 64;            // query rows of one key-value head an attention CTA takes at once
+
+// ---------------------------------------------------------------- cache plan
+struct PlanParams {
+    const int32_t* seq_len; const int32_t* n_new; const int32_t* owned;
+    int32_t* ring; const int32_t* ring_state; int pages;
+    int32_t* table; int width; int page_size;
+    int B, T;
+    int32_t* owned_out; int32_t* ring_state_out; int32_t* kv_len; int32_t* q_off; int32_t* tile_off;
+    int32_t* slot_map; int32_t* positions;
+    uint32_t* status;   // may be null
+};
+cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s);
+
+// -------------------------------------------------------------- cache append
+struct AppendParams {
+    const char* k; const char* v; long long k_stride, v_stride;   // bytes between tokens
+    const int32_t* slot_map; int T;
+    char* k_cache; char* v_cache; long long page_bytes;           // bytes between pages
+    int pages, page_size, heads, row_bytes;                       // row_bytes: one head's vector
+    uint32_t* status;   // may be null
+};
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t s);
+
+// ----------------------------------------------------------- cache attention
+struct AttnParams {
+    const void* q; long long q_stride;                 // elements between tokens
+    const void* k; const void* v; long long page_stride;   // elements between pages
+    int bf16;
+    const int32_t* table; int width;
+    const int32_t* kv_len; const int32_t* q_off; const int32_t* tile_off;
+    int B, N, Hq, Hkv, G, D, pages, page_size, max_new;
+    float scale;
+    void* out; float* lse;
+    int row_tile, row_tiles;    // query rows of a key-value head per tile of rows, and such tiles
+    int ctas;                   // CTAs the work is split over
+    float* part;                // [2 ctas][row_tile][D] sums, then [2 ctas][row_tile][2] (max, sum)
+    uint32_t* status;
+};
+cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s);
+int attn_row_tile(int rows);    // rows of a row tile where a key-value head has `rows` query rows
+
+// The split of an attention launch.  The work is the list of all tiles of
+// kTile cache positions, ordered by request, key-value head, row tile and
+// position; CTA c takes the tiles [first(c), first(c + 1)).  A segment is the
+// run of tiles of one (request, head, row tile).  A segment that crosses CTA
+// boundaries leaves one partial result per CTA (slot 2c + 1 where the segment
+// starts in c, else 2c), which the join kernel adds up in CTA order.
+struct AttnSplit {
+    long long total;   // tiles
+    int n;             // CTAs that have tiles
+    int heads;         // key-value heads * row tiles
+    __device__ __forceinline__ AttnSplit(const AttnParams& p) {
+        heads = p.Hkv * p.row_tiles;
+        const long long most = (long long)p.B * (((long long)p.width * p.page_size + kTile - 1) / kTile);
+        const long long t = p.tile_off[p.B];
+        const bool ok = t >= 0 && t <= most && p.tile_off[0] == 0;
+        if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) raise_status(p.status, kBadLength);
+        total = ok ? t * heads : 0;
+        n = total < p.ctas ? (int)total : p.ctas;
+    }
+    __device__ __forceinline__ long long first(int c) const { return total * c / n; }
+    __device__ __forceinline__ int cta_of(long long t) const { return (int)(((t + 1) * n - 1) / total); }
+};
+
+struct AttnSegment {
+    int b, h, rt;        // request, key-value head, row tile
+    long long t0;        // its first tile in the list
+    int tiles;
+};
+
+// The segment of tile t: the request by binary search over its tile offsets.
+__device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnSplit& sp, long long t) {
+    const int tt = (int)(t / sp.heads);
+    int lo = 0, hi = p.B;                       // tile_off[lo] <= tt < tile_off[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.tile_off[mid] <= tt) lo = mid; else hi = mid;
+    }
+    AttnSegment g;
+    g.b = lo;
+    const int off = p.tile_off[lo];
+    g.tiles = max(1, p.tile_off[lo + 1] - off);
+    const long long local = t - (long long)off * sp.heads;
+    int hr = (int)(local / g.tiles);
+    hr = hr < 0 ? 0 : (hr >= sp.heads ? sp.heads - 1 : hr);
+    g.t0 = (long long)off * sp.heads + (long long)hr * g.tiles;
+    g.h = hr / p.row_tiles;
+    g.rt = hr - g.h * p.row_tiles;
+    return g;
+}
+
+// ------------------------------------------------------------------- logits
+struct LogitsParams {
+    const void* logits; long long row_stride; int bf16;   // elements between rows
+    void* out;
+    int B, R, V;
+    const int32_t* hist; int hist_stride; const int32_t* hist_len; const int32_t* prompt_len;
+    const int32_t* draft_tok; int draft_stride;
+    const float* rep; const float* freq; const float* pres;
+    const int32_t* bias_tok; const float* bias_val; const int32_t* bias_off; int bias_n;
+    const uint32_t* mask;
+    int32_t* live;
+    uint32_t* status; uint32_t* tickets; uint32_t* counts;   // [B], [B][R]: zero between launches
+};
+cudaError_t launch_logits(const LogitsParams& p, cudaStream_t s);
+
+}  // namespace dspark
