@@ -310,19 +310,24 @@ cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     attn_simt_kernel<T, MR><<<p.ctas, kSimtThreads, smem, s>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
+    if (p.ctas < 2) return cudaSuccess;
     return launch_dependent(attn_join_kernel<T>, dim3(p.ctas - 1, (p.row_tile + 7) / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
 
-int attn_row_tile(int rows) { return rows <= 8 ? 8 : 32; }
-
 cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s) {
-    if (p.N == 0) return cudaSuccess;
-    if (p.row_tile == 8) return p.bf16 ? launch_simt<uint16_t, 8>(p, s) : launch_simt<float, 8>(p, s);
-    return p.bf16 ? launch_simt<uint16_t, 32>(p, s) : launch_simt<float, 32>(p, s);
+    cudaError_t e;
+    if (attn_mma_supported(p)) e = launch_attn_mma(p, s);
+    else if (p.row_tile == 8) e = p.bf16 ? launch_simt<uint16_t, 8>(p, s) : launch_simt<float, 8>(p, s);
+    else e = p.bf16 ? launch_simt<uint16_t, 32>(p, s) : launch_simt<float, 32>(p, s);
+    if (e != cudaSuccess) return e;
+    return p.bf16 ? launch_join<uint16_t>(p, s) : launch_join<float>(p, s);
 }
 
 }  // namespace dspark

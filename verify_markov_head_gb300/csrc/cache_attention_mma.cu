@@ -1,0 +1,644 @@
+// cache_attention_mma.cu -- attention over the paged cache on the tensor
+// cores: bf16, head size 64 or 128, pages of a multiple of 8 positions (the
+// rest runs on CUDA cores, cache_attention.cu, where the formulas stand).
+//
+// Both products are taken transposed, so that 128 cache positions fill the
+// 128 lanes of the accumulator and the few query rows of a key-value head are
+// its columns (N = 16, 32 or 64 of them):
+//     S^T [128 positions x N] = K [128 x D] . Q^T       (K, Q: K-major)
+//     O^T [D x N]            += V^T [D x 128] . P^T      (V, P: MN-major)
+// K and V tiles go from the pages to shared memory by TMA exactly as they lie
+// there, each is read once by the tensor core whatever N is, and no lane is
+// spent on padding rows.  What is left per position and row is one 2^x.
+//
+// Roles (11 warps, one CTA per SM, a ring of 5 tiles of 32 KB):
+//   warps 0-3, 4-7   softmax of the first and the second half of the columns:
+//                    thread = position; column maxima by a warp reduction and
+//                    an exchange over the 4 warps; weights to shared memory
+//   warp 8           TMA producer (lane = box of a page)
+//   warp 9           MMA issuer
+//   warp 10          walks the CTA's segments: descriptors and Q tiles
+// The running maximum moves only when a column's maximum grows by more than
+// 2^8 (the weights then stay below 2^8, their relative precision is the
+// same), so O^T in tensor memory is rescaled rarely.
+//
+// Weights are rounded to bf16 for the second product (relative 2^-8 of each
+// weight, independent in sign); their sum l is taken in fp32 before rounding.
+#include <cudaTypedefs.h>
+
+#include "pdl.cuh"
+#include "serve.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSteps = 128;              // positions per step (one tile of K and one of V)
+constexpr int kSoftWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kSegWarp = 10, kWarps = 11;
+constexpr int kSegs = 4;                 // segment descriptors in flight
+constexpr int kBadRing = 8;              // steps the producer may be ahead of the softmax, and more
+constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
+constexpr long long kDrainCycles = 200000000LL;
+
+struct Seg {
+    int b, h, q0, n, len;     // request, key-value head, first token in q, tokens, cache length
+    int r0, rows;             // query rows of this tile
+    int pos0, pos1;           // cache positions [pos0, pos1)
+    int steps;                // -1: no more segments
+    int slot;                 // -1: the whole segment, else the partial result's slot
+    int pad;
+};
+
+template <int N, int D>
+struct Smem {
+    static constexpr int kTileBytes = kSteps * D * 2;
+    static constexpr int kStages = 5 * 128 / D;
+    static constexpr int kQBytes = N * D * 2;
+    static constexpr int kRing = 0;
+    static constexpr int kQ = kRing + kStages * kTileBytes;
+    static constexpr int kP = kQ + 2 * kQBytes;                   // [128][64] bf16, 128-byte rows
+    static constexpr int kMax = kP + kSteps * 128;                // [2][N][4]
+    static constexpr int kSum = kMax + 2 * N * 16;                // [N][4]
+    static constexpr int kSeg = kSum + N * 16;
+    static constexpr int kBar = kSeg + kSegs * (int)sizeof(Seg);
+    static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 + 2 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, non-finite flag, bad boxes
+    static constexpr int kTotal = kFlags + 16 + 4 * kBadRing;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ float warp_max(float x) {     // over the warp, NaN left out
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// N columns of 32 lanes, waited for.
+template <int C> __device__ __forceinline__ void tmem_get(uint32_t a, float (&v)[C]);
+template <> __device__ __forceinline__ void tmem_get<8>(uint32_t a, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(a) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_get<16>(uint32_t a, float (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 "\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+                   "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(a) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_get<32>(uint32_t a, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(a) : "memory");
+}
+template <int C> __device__ __forceinline__ void tmem_put(uint32_t a, const float (&v)[C]);
+template <> __device__ __forceinline__ void tmem_put<8>(uint32_t a, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;"
+                 ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_put<16>(uint32_t a, const float (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 "\n\ttcgen05.wait::st.sync.aligned;"
+                 ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+                   "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_put<32>(uint32_t a, const float (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\ttcgen05.wait::st.sync.aligned;"
+                 ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+                   "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+                   "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
+                   "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two 16-bit halves of w with the non-finite bf16 ones cleared.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    return w;
+}
+
+template <int N, int D>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const int bx) {
+    using L = Smem<N, D>;
+    constexpr int HC = N / 2;                   // columns of a softmax half
+    constexpr int kStages = L::kStages;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile uint32_t* s_flags = reinterpret_cast<volatile uint32_t*>(gbase + L::kFlags);   // [0] TMEM, [1] abort, [2] fix
+    volatile uint32_t* s_bad = s_flags + 4;     // [kBadRing] boxes of a step whose page is out of range
+    volatile Seg* s_seg = reinterpret_cast<volatile Seg*>(gbase + L::kSeg);
+    volatile uint32_t* abort_flag = s_flags + 1;
+    uint32_t bar = base + L::kBar;
+    auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
+    const uint32_t b_full = take(kStages), b_empty = take(kStages);
+    const uint32_t b_seg_full = take(kSegs), b_seg_empty = take(kSegs);
+    const uint32_t b_q_full = take(2), b_q_empty = take(2), b_s_full = take(2), b_s_empty = take(2);
+    const uint32_t b_o_empty = take(2), b_p_full = take(1), b_pv = take(1), b_end = take(1);
+
+    if (tid == 0) {
+        grid_launch_dependents();       // the join is scheduled now and waits for this grid
+        for (int i = 0; i < kStages; ++i) { ptx::mbar_init(b_full + 8 * i, 1); ptx::mbar_init(b_empty + 8 * i, 1); }
+        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 2 + kSoftWarps); }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(b_q_full + 8 * i, 1); ptx::mbar_init(b_q_empty + 8 * i, 1);
+            ptx::mbar_init(b_s_full + 8 * i, 1); ptx::mbar_init(b_s_empty + 8 * i, kSoftWarps);
+            ptx::mbar_init(b_o_empty + 8 * i, kSoftWarps);
+        }
+        ptx::mbar_init(b_p_full, kSoftWarps); ptx::mbar_init(b_pv, 1); ptx::mbar_init(b_end, 1);
+        s_flags[1] = 0u;
+        s_flags[2] = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(base + L::kFlags, 4 * N);
+        ptx::tmem_relinquish();
+    }
+    if (warp == kTmaWarp && lane == 0) { ptx::prefetch_tmap(&kmap); ptx::prefetch_tmap(&vmap); }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s_flags[0];
+    const long long wl = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
+    auto wait = [&](uint32_t b, uint32_t parity) { return ptx::mbar_wait_strict(b, parity & 1u, abort_flag, wl); };
+    auto give_up = [&](int site) {
+        raise_timeout(p.status, site);
+        *abort_flag = 1u;
+    };
+
+    if (warp == kSegWarp) {
+        // ------------------------------------------------ segments and Q tiles
+        const AttnSplit sp(p);
+        const int cta = blockIdx.x;
+        bool ok = true;
+        int si = 0;
+        long long t = 0, end = 0;
+        AttnSegment g{};
+        if (cta < sp.n) {
+            t = sp.first(cta);
+            end = sp.first(cta + 1);
+            g = attn_segment(p, sp, t);
+        }
+        while (ok) {
+            const int slot = si % kSegs;
+            if (si >= kSegs) ok = wait(b_seg_empty + 8 * slot, (si / kSegs) - 1);
+            ok = __all_sync(~0u, ok);
+            if (!ok) { if (lane == 0) give_up(0); break; }
+            const bool more = t < end;
+            Seg d{};
+            d.steps = -1;
+            if (more) {
+                d.b = g.b; d.h = g.h;
+                d.q0 = p.q_off[g.b];
+                d.n = p.q_off[g.b + 1] - d.q0;
+                d.len = p.kv_len[g.b];
+                const long long cap = (long long)p.width * p.page_size;
+                if (d.n > p.max_new || d.n < 0 || d.q0 < 0 || d.q0 > p.N - d.n || d.len < 0 || d.len > cap) {
+                    if (lane == 0) raise_status(p.status, kBadLength);
+                    d.n = d.q0 < 0 ? 0 : max(0, min(d.n, min(p.max_new, p.N - d.q0)));
+                    d.len = max(0, (int)min((long long)d.len, cap));
+                }
+                d.r0 = g.rt * p.row_tile;
+                d.rows = max(0, min(p.row_tile, d.n * p.G - d.r0));
+                const int j0 = (int)(t - g.t0), j1 = (int)min((long long)g.tiles, end - g.t0);
+                d.pos0 = min(j0 * kTile, d.len);
+                d.pos1 = min(j1 * kTile, d.len);
+                d.steps = max(1, (d.pos1 - d.pos0 + kSteps - 1) / kSteps);
+                d.slot = j0 == 0 && j1 == g.tiles ? -1 : 2 * cta + (j0 == 0 ? 1 : 0);
+                t = g.t0 + j1;
+                if (t < end) {      // the next segment: the next head or row tile, or the next request that has tiles
+                    if (++g.rt == p.row_tiles) { g.rt = 0; ++g.h; }
+                    if (g.h == p.Hkv) g = attn_segment(p, sp, t);
+                    else g.t0 = t;
+                }
+            }
+            if (lane == 0) {
+                const_cast<Seg&>(s_seg[slot]) = d;
+                ptx::mbar_arrive(b_seg_full + 8 * slot);
+            }
+            if (!more) break;
+            // the Q tile, rows beyond the request's as zeros
+            const int qb = si & 1;
+            if (si >= 2) ok = wait(b_q_empty + 8 * qb, (si / 2) - 1);
+            ok = __all_sync(~0u, ok);
+            if (!ok) { if (lane == 0) give_up(1); break; }
+            constexpr int kChunks = D / 8;
+            const uint16_t* q = static_cast<const uint16_t*>(p.q);
+            const uint32_t qs = base + L::kQ + qb * L::kQBytes;
+#pragma unroll 8
+            for (int i = lane; i < N * kChunks; i += 32) {
+                const int r = i / kChunks, c = i - r * kChunks;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (r < d.rows) {
+                    const int rr = d.r0 + r, tok = rr / p.G;
+                    x = __ldg(reinterpret_cast<const uint4*>(q + (d.q0 + tok) * p.q_stride + (size_t)(d.h * p.G + rr - tok * p.G) * D) + c);
+                }
+                const uint32_t at = qs + (c / 8) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
+            ++si;
+        }
+    } else if (warp == kTmaWarp) {
+        // ------------------------------------------------------------ producer
+        const uint64_t pol = p.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
+        const int nbox = kSteps / bx;
+        uint32_t fill = 0;                       // tiles issued
+        static_assert(kStages / 2 + 1 < kBadRing, "the producer stays within the ring of bad boxes");
+        bool ok = true;
+        for (int si = 0; ok; ++si) {
+            const int slot = si % kSegs;
+            ok = __all_sync(~0u, wait(b_seg_full + 8 * slot, si / kSegs));
+            if (!ok) { if (lane == 0) give_up(2); break; }
+            const Seg d = const_cast<Seg&>(s_seg[slot]);
+            __syncwarp();
+            if (d.steps < 0) break;
+            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
+            const int32_t* row = p.table + (size_t)d.b * p.width;
+            auto page_of = [&](int step) {       // this lane's box of a step: its page, -1 beyond the end
+                const int pos = d.pos0 + step * kSteps + lane * bx;
+                return lane < nbox && pos < d.pos1 ? __ldg(row + pos / p.page_size) : -1;
+            };
+            int page = page_of(0);
+            for (int s = 0; s < d.steps && ok; ++s) {
+                const int pos = d.pos0 + s * kSteps + lane * bx;
+                const bool want = lane < nbox && pos < d.pos1;
+                const bool have = want && page >= 0 && page < p.pages;
+                const uint32_t bad = __ballot_sync(~0u, want && !have);
+                const int boxes = __popc(__ballot_sync(~0u, have));
+                if (bad && lane == 0) raise_status(p.status, kBadPage);
+                const int y = pos % p.page_size, pg = page;
+                if (s + 1 < d.steps) page = page_of(s + 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++fill) {
+                    const int stage = fill % kStages;
+                    if (fill >= (uint32_t)kStages) ok = __all_sync(~0u, wait(b_empty + 8 * stage, fill / kStages - 1));
+                    if (!ok) { if (lane == 0) give_up(3); break; }
+                    const uint32_t full = b_full + 8 * stage;
+                    if (lane == 0) {
+                        if (!kv) s_bad[(fill / 2) % kBadRing] = bad;
+                        if (boxes) ptx::mbar_arrive_expect_tx(full, boxes * bx * D * 2);
+                        else ptx::mbar_arrive(full);
+                    }
+                    __syncwarp();
+                    if (have) {
+                        const uint32_t dst = base + L::kRing + stage * L::kTileBytes + lane * bx * 128;
+#pragma unroll
+                        for (int x = 0; x < D; x += 64)
+                            tma_load_4d(dst + (x / 64) * (kSteps * 128), kv ? &vmap : &kmap, x, y, d.h, pg, full, pol);
+                    }
+                }
+            }
+        }
+        // every copy issued lands before the CTA leaves
+        if (lane == 0)
+            for (uint32_t i = 0; i < (uint32_t)kStages; ++i)
+                if (fill > i) {
+                    const uint32_t last = (fill - 1) - ((fill - 1 - i) % kStages);
+                    ptx::mbar_wait_drain(b_full + 8 * i, (last / kStages) & 1u, kDrainCycles);
+                }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, N, false, false);
+            constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, N, true, true);
+            uint32_t step = 0;                   // steps whose S product was issued
+            bool ok = true;
+            // a step whose S product was issued and whose O product was not
+            bool pend = false, pend_first = false;
+            uint32_t pend_step = 0, pend_seg = 0;
+            auto second = [&]() {                // O^T (+)= V^T P^T of the pending step
+                const uint32_t vi = 2 * pend_step + 1, st = vi % kStages, ob = pend_seg & 1u;
+                ok = wait(b_full + 8 * st, vi / kStages) && wait(b_p_full, pend_step);
+                if (ok && pend_first && pend_seg >= 2) ok = wait(b_o_empty + 8 * ob, pend_seg / 2 - 1);
+                if (!ok) return;
+                ptx::tc_fence_after();
+                const uint32_t va = base + L::kRing + st * L::kTileBytes, pa = base + L::kP;
+                // V^T: entries of a position lie along M, the 64-entry halves a
+                // half tile apart (head size 64: the second half of the lanes
+                // repeats the first and is not used); 16 positions = 2 KB
+#pragma unroll
+                for (int k = 0; k < kSteps / 16; ++k)
+                    ptx::mma_f16(tmem + 2 * N + ob * N, ptx::smem_desc_sw128(va + k * 2048, D == 128 ? kSteps * 128 : 0, 1024),
+                                 ptx::smem_desc_sw128(pa + k * 2048, 16, 1024), id_o, pend_first && k == 0 ? 0u : 1u);
+                ptx::mma_commit(b_empty + 8 * st);
+                ptx::mma_commit(b_pv);
+                pend = false;
+            };
+            for (uint32_t si = 0; ok; ++si) {
+                const int slot = si % kSegs;
+                ok = wait(b_seg_full + 8 * slot, si / kSegs);
+                if (!ok) break;
+                const int steps = s_seg[slot].steps;
+                if (steps < 0) break;
+                ptx::mbar_arrive(b_seg_empty + 8 * slot);
+                const uint32_t qb = si & 1u;
+                ok = wait(b_q_full + 8 * qb, si / 2);
+                for (int s = 0; s < steps && ok; ++s, ++step) {
+                    const uint32_t ki = 2 * step, st = ki % kStages, sb = step & 1u;
+                    ok = wait(b_full + 8 * st, ki / kStages);
+                    if (ok && step >= 2) ok = wait(b_s_empty + 8 * sb, step / 2 - 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t ka = base + L::kRing + st * L::kTileBytes, qa = base + L::kQ + qb * L::kQBytes;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        ptx::mma_f16(tmem + sb * N, ptx::smem_desc_sw128(ka + (k / 4) * (kSteps * 128) + (k % 4) * 32, 16, 1024),
+                                     ptx::smem_desc_sw128(qa + (k / 4) * (N * 128) + (k % 4) * 32, 16, 1024), id_s, k ? 1u : 0u);
+                    ptx::mma_commit(b_empty + 8 * st);
+                    ptx::mma_commit(b_s_full + 8 * sb);
+                    if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
+                    if (pend) second();
+                    if (!ok) break;
+                    pend = true; pend_first = s == 0; pend_step = step; pend_seg = si;
+                }
+            }
+            if (ok && pend) second();
+            if (!ok) give_up(4);
+            // nothing is in flight in the tensor core when the CTA leaves
+            ptx::mma_commit(b_end);
+            ptx::mbar_wait_drain(b_end, 0, kDrainCycles);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------- softmax
+        const int half = warp >> 2, quarter = warp & 3, row = tid & 127;
+        const uint32_t lanes = (uint32_t)quarter << 21;             // TMEM lane offset of this warp
+        const float scale2 = p.scale * kLog2e;
+        const int my_box = row / bx;
+        float4* s_max = reinterpret_cast<float4*>(gbase + L::kMax);
+        float4* s_sum = reinterpret_cast<float4*>(gbase + L::kSum);
+        uint32_t step = 0;
+        bool ok = true;
+        for (uint32_t si = 0;; ++si) {
+            const int slot = si % kSegs;
+            ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
+            if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
+            const Seg d = const_cast<Seg&>(s_seg[slot]);
+            __syncwarp();
+            if (d.steps < 0) break;
+            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
+            const uint32_t o_at = tmem + lanes + 2 * N + (si & 1u) * N + half * HC;
+            const int first_new = d.len - d.n;                     // position of the block's first token
+            float m[HC], l[HC];                                    // log2 of the reference, sum of the weights (this thread's positions)
+#pragma unroll
+            for (int c = 0; c < HC; ++c) { m[c] = -INFINITY; l[c] = 0.f; }
+            bool stop = false;
+            for (int s = 0; s < d.steps; ++s, ++step) {
+                const int pos0 = d.pos0 + s * kSteps, pos = pos0 + row, there = d.pos1 - pos0;
+                ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
+                ok = __all_sync(~0u, ok);
+                float x[HC];
+                uint32_t bad = 0u;
+                if (ok) {
+                    ptx::tc_fence_after();
+                    tmem_get<HC>(tmem + lanes + (step & 1u) * N + half * HC, x);
+                    ptx::tc_fence_before();
+                    bad = s_bad[step % kBadRing];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) x[c] = 0.f;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_s_empty + 8 * (step & 1u));
+                // positions beyond the end or in a bad page, and the block's later tokens
+                const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
+                const bool gone = row >= there || (bad >> my_box & 1u);
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        const int last = first_new + (d.r0 + half * HC + c) / p.G;
+                        if (gone || pos > last) x[c] = -INFINITY;
+                    }
+                }
+                float mine = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < HC; ++c) {
+                    const float w = warp_max(x[c]);
+                    if (lane == c) mine = w;
+                }
+                float* mx = reinterpret_cast<float*>(s_max + (step & 1u) * N + half * HC);
+                if (lane < HC) mx[lane * 4 + quarter] = mine;
+                if (ptx::bar_red_or(1 + half, 128, !ok)) { stop = true; break; }
+                float top[HC];
+                bool grow = false;
+#pragma unroll
+                for (int c = 0; c < HC; ++c) {
+                    const float4 w = reinterpret_cast<const float4*>(mx)[c];
+                    top[c] = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * scale2;
+                    grow |= top[c] > m[c] + kSlack;
+                }
+                // the product before this one is done: P may be overwritten, O rescaled
+                if (step > 0) ok = wait(b_pv, step - 1) && ok;
+                if (grow) {                     // the same in every thread of the half
+                    ptx::tc_fence_after();
+                    float a[HC];
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        const float to = fmaxf(top[c], m[c]);
+                        a[c] = to > m[c] ? fast_exp2(m[c] - to) : 1.f;
+                        l[c] *= a[c];
+                        m[c] = to;
+                    }
+                    if (s > 0) {
+                        float o[HC];
+                        __syncwarp();
+                        tmem_get<HC>(o_at, o);
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) o[c] *= a[c];
+                        tmem_put<HC>(o_at, o);
+                    }
+                }
+                // weights: row `row` of P, columns half * HC ..
+                const uint32_t prow = base + L::kP + row * 128;
+#pragma unroll
+                for (int c0 = 0; c0 < HC; c0 += 8) {
+                    float w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float ref = m[c0 + e] == -INFINITY ? 0.f : m[c0 + e];
+                        w[e] = fast_exp2(fmaf(x[c0 + e], scale2, -ref));
+                        l[c0 + e] += w[e];
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                 ::"r"(prow + ((((half * HC + c0) / 8) ^ (row & 7)) << 4)), "r"(pack_bf16(w[0], w[1])),
+                                   "r"(pack_bf16(w[2], w[3])), "r"(pack_bf16(w[4], w[5])), "r"(pack_bf16(w[6], w[7])) : "memory");
+                }
+                if (edge) {
+                    // a value that no row may use is zero in shared memory: the
+                    // product would turn 0 * NaN into NaN.  Of the block's later
+                    // tokens, whose values some rows use, the non-finite entries
+                    // are cleared and added again below to the rows that see them.
+                    const uint32_t vi = 2 * step + 1;
+                    ok = wait(b_full + 8 * (vi % kStages), vi / kStages) && ok;
+                    const bool later = !gone && pos > first_new;
+                    if (gone || later) {
+                        uint4* v = reinterpret_cast<uint4*>(gbase + L::kRing + (vi % kStages) * L::kTileBytes) + row * 8;
+                        constexpr int kHalves = D / 64;
+                        // the two halves of the softmax warps share a row's chunks
+#pragma unroll
+                        for (int c = half; c < 8 * kHalves; c += 2) {
+                            uint4* at = v + (c / 8) * (kSteps * 8) + (c % 8);
+                            if (gone) *at = make_uint4(0u, 0u, 0u, 0u);
+                            else {
+                                const uint4 y = *at;
+                                const uint4 z = make_uint4(finite_only(y.x), finite_only(y.y), finite_only(y.z), finite_only(y.w));
+                                if (z.x != y.x || z.y != y.y || z.z != y.z || z.w != y.w) { *at = z; s_flags[2] = 1u; }
+                            }
+                        }
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_p_full);
+            }
+            if (stop) { ok = false; break; }
+            // ----------------------------------------------------- segment's end
+            ok = wait(b_pv, step - 1) && ok;
+            ok = __all_sync(~0u, ok);
+            float o[HC];
+            if (ok) {
+                ptx::tc_fence_after();
+                tmem_get<HC>(o_at, o);
+                ptx::tc_fence_before();
+            } else {
+#pragma unroll
+                for (int c = 0; c < HC; ++c) o[c] = 0.f;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (si & 1u));
+            float mine = 0.f;
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+                float t = l[c];
+#pragma unroll
+                for (int q = 16; q; q >>= 1) t += __shfl_xor_sync(~0u, t, q);
+                if (lane == c) mine = t;
+            }
+            float* sm = reinterpret_cast<float*>(s_sum + half * HC);
+            if (lane < HC) sm[lane * 4 + quarter] = mine;
+            if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
+            const int dim = row;
+            if (s_flags[2]) {
+                // non-finite values of the block's later tokens (this CTA's positions)
+                for (int pos = max(first_new + 1, d.pos0); pos < d.pos1 && dim < D; ++pos) {
+                    const int pg = pos / p.page_size, page = p.table[(size_t)d.b * p.width + pg];
+                    if (page < 0 || page >= p.pages) continue;
+                    const float v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
+                                          ((long long)d.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
+                    if (fabsf(v) < INFINITY) continue;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c)
+                        if (pos <= first_new + (d.r0 + half * HC + c) / p.G) o[c] += v;
+                }
+            }
+            const float* stats0 = p.part + (size_t)2 * p.ctas * p.row_tile * D;
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+                const int r = half * HC + c;
+                if (r >= d.rows) break;
+                const float4 s4 = reinterpret_cast<const float4*>(sm)[c];
+                const float sum = (s4.x + s4.y) + (s4.z + s4.w);
+                const int rr = d.r0 + r, tok = rr / p.G, head = d.h * p.G + rr - tok * p.G;
+                const size_t at = (size_t)(d.q0 + tok) * p.Hq + head;
+                if (d.slot < 0) {
+                    if (dim < D) {
+                        const float y = o[c] * (sum != 0.f ? 1.f / sum : 0.f);
+                        static_cast<uint16_t*>(p.out)[at * D + dim] = (uint16_t)pack_bf16(y, 0.f);
+                    }
+                    if (row == 0 && p.lse) p.lse[at] = sum != 0.f ? m[c] * kLn2 + logf(sum) : -INFINITY;
+                } else {
+                    const size_t pr = (size_t)d.slot * p.row_tile + r;
+                    if (dim < D) p.part[pr * D + dim] = o[c];
+                    if (row == 0) *reinterpret_cast<float2*>(const_cast<float*>(stats0) + pr * 2) = make_float2(m[c], sum);
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up(5);
+    }
+    // requests that own no cache position have no tile: their rows are zero
+    if (warp < kSoftWarps) {
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            if (p.tile_off[b + 1] > p.tile_off[b]) continue;
+            int q0 = p.q_off[b], n = p.q_off[b + 1] - q0;
+            n = q0 < 0 ? 0 : max(0, min(n, min(p.max_new, p.N - q0)));
+            for (int i = tid; i < n * p.Hq * D; i += kSoftWarps * 32) static_cast<uint16_t*>(p.out)[(size_t)q0 * p.Hq * D + i] = 0;
+            if (p.lse)
+                for (int i = tid; i < n * p.Hq; i += kSoftWarps * 32) p.lse[(size_t)q0 * p.Hq + i] = -INFINITY;
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 4 * N);
+}
+
+template <int N, int D>
+cudaError_t launch(const AttnParams& p, cudaStream_t s) {
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encoder());
+    if (!enc) return cudaErrorNotSupported;
+    int bx = 64;                                 // positions of a box: a power of two that divides a page
+    while (p.page_size % bx) bx >>= 1;
+    CUtensorMap maps[2];
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv, (cuuint64_t)p.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.page_size * D * 2, (cuuint64_t)p.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)bx, 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i ? p.v : p.k), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    const size_t smem = Smem<N, D>::kTotal + 1024;
+    static_assert(Smem<N, D>::kTotal + 1024 <= 232448, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    attn_mma_kernel<N, D><<<p.ctas, kWarps * 32, smem, s>>>(p, maps[0], maps[1], bx);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_mma_supported(const AttnParams& p) {
+    // a page stride that a tensor map can hold
+    return p.bf16 && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.page_stride < (1LL << 38) &&
+           tma_encoder() != nullptr;
+}
+
+cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s) {
+    if (p.D == 64) return p.row_tile == 16 ? launch<16, 64>(p, s) : p.row_tile == 32 ? launch<32, 64>(p, s) : launch<64, 64>(p, s);
+    return p.row_tile == 16 ? launch<16, 128>(p, s) : p.row_tile == 32 ? launch<32, 128>(p, s) : launch<64, 128>(p, s);
+}
+
+}  // namespace dspark

@@ -59,7 +59,12 @@ struct AttnParams {
     uint32_t* status;
 };
 cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s);
-int attn_row_tile(int rows);    // rows of a row tile where a key-value head has `rows` query rows
+bool attn_mma_supported(const AttnParams& p);
+cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
+// Rows of a row tile where a key-value head has `rows` query rows.
+inline int attn_row_tile(int rows, bool mma) {
+    return mma ? (rows <= 16 ? 16 : rows <= 32 ? 32 : 64) : (rows <= 8 ? 8 : 32);
+}
 
 // The split of an attention launch.  The work is the list of all tiles of
 // kTile cache positions, ordered by request, key-value head, row tile and

@@ -94,7 +94,7 @@ static bool attn_sizes_ok(int B, int q_heads, int kv_heads, int head_dim, int ma
 
 size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new) {
     if (!attn_sizes_ok(B, q_heads, kv_heads, head_dim, max_new)) return 0;
-    const size_t rows = attn_row_tile(q_heads / kv_heads * max_new);
+    const size_t rows = attn_row_tile(q_heads / kv_heads * max_new, true);   // the larger of the two kernels' tiles
     return kHead + ws_align256((size_t)2 * kMaxAttnCtas * rows * (head_dim + 2) * sizeof(float));
 }
 
@@ -128,9 +128,11 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     p.pages = pages; p.page_size = page_size; p.max_new = max_new;
     p.scale = scale; p.out = out; p.lse = lse;
     const int rows = p.G * max_new;
-    p.row_tile = attn_row_tile(rows);
+    const bool mma = attn_mma_supported(p);
+    p.row_tile = attn_row_tile(rows, mma);
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
-    p.ctas = 2 * num_sms() < kMaxAttnCtas ? 2 * num_sms() : kMaxAttnCtas;
+    const int ctas = (mma ? 1 : 2) * num_sms();      // resident CTAs: one or two per SM
+    p.ctas = ctas < kMaxAttnCtas ? ctas : kMaxAttnCtas;
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead);
     p.status = static_cast<uint32_t*>(ws);
     return launch_status(launch_cache_attention(p, static_cast<cudaStream_t>(stream)));
