@@ -263,31 +263,48 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rr = g.rt * p.row_tile + row;
     if (row >= p.row_tile || rr >= rm.n * p.G) return;
-    const float* stats = part_stats(p);
-    auto slot_of = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
+    const float2* stats = reinterpret_cast<const float2*>(part_stats(p));
+    auto place = [&](int i) { return (size_t)(i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * p.row_tile + row; };
     const int parts = last - c + 2;
     float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, stats[((size_t)slot_of(i) * p.row_tile + row) * 2]);
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, stats[place(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int i = 0; i < parts; ++i) {
-        const size_t at = (size_t)slot_of(i) * p.row_tile + row;
-        const float2 st = *reinterpret_cast<const float2*>(stats + at * 2);
-        const float w = fast_exp2(st.x - ref);
-        l = fmaf(w, st.y, l);
+    const bool d0 = 4 * lane < p.D, d1 = 4 * lane + 128 < p.D;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        // lane i weighs part i0 + i; the parts' rows are then read 8 at a time
+        float w = 0.f, s = 0.f;
+        if (i0 + lane < parts) {
+            const float2 st = stats[place(i0 + lane)];
+            w = fast_exp2(st.x - ref);
+            s = w * st.y;
+        }
+        const int n = min(32, parts - i0);
+        for (int j0 = 0; j0 < n; j0 += 8) {
+            float4 x[8], y[8];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int d = 4 * lane + 128 * hf;
-            if (d < p.D) {
-                const float4 x = *reinterpret_cast<const float4*>(p.part + at * p.D + d);
-                acc[4 * hf] = fmaf(w, x.x, acc[4 * hf]);
-                acc[4 * hf + 1] = fmaf(w, x.y, acc[4 * hf + 1]);
-                acc[4 * hf + 2] = fmaf(w, x.z, acc[4 * hf + 2]);
-                acc[4 * hf + 3] = fmaf(w, x.w, acc[4 * hf + 3]);
+            for (int j = 0; j < 8; ++j) {
+                x[j] = y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j0 + j < n) {
+                    const float4* at = reinterpret_cast<const float4*>(p.part + place(i0 + j0 + j) * p.D) + lane;
+                    if (d0) x[j] = at[0];
+                    if (d1) y[j] = at[32];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float wj = __shfl_sync(~0u, w, j0 + j);
+                l += __shfl_sync(~0u, s, j0 + j);
+                if (wj != 0.f) {
+                    acc[0] = fmaf(wj, x[j].x, acc[0]); acc[1] = fmaf(wj, x[j].y, acc[1]);
+                    acc[2] = fmaf(wj, x[j].z, acc[2]); acc[3] = fmaf(wj, x[j].w, acc[3]);
+                    acc[4] = fmaf(wj, y[j].x, acc[4]); acc[5] = fmaf(wj, y[j].y, acc[5]);
+                    acc[6] = fmaf(wj, y[j].z, acc[6]); acc[7] = fmaf(wj, y[j].w, acc[7]);
+                }
             }
         }
     }

@@ -13,14 +13,16 @@
 //
 // Roles (11 warps, one CTA per SM, a ring of 5 tiles of 32 KB):
 //   warps 0-3, 4-7   softmax of the first and the second half of the columns:
-//                    thread = position; column maxima by a warp reduction and
-//                    an exchange over the 4 warps; weights to shared memory
+//                    thread = position; weights to shared memory
 //   warp 8           TMA producer (lane = box of a page)
 //   warp 9           MMA issuer
 //   warp 10          walks the CTA's segments: descriptors and Q tiles
-// The running maximum moves only when a column's maximum grows by more than
-// 2^8 (the weights then stay below 2^8, their relative precision is the
-// same), so O^T in tensor memory is rescaled rarely.
+// The reference of a column's weights, 2^(s - ref), moves only when a score
+// exceeds it by more than 8 (weights stay below 2^8, their relative precision
+// is the same).  So an ordinary step needs no maximum: each thread forms the
+// exponents it needs anyway, a barrier ORs "one of mine is above 8" over the
+// half, and only then are the column maxima found (a warp reduction and an
+// exchange over the 4 warps), and the sums and O^T in tensor memory rescaled.
 //
 // Weights are rounded to bf16 for the second product (relative 2^-8 of each
 // weight, independent in sign); their sum l is taken in fp32 before rounding.
@@ -48,7 +50,7 @@ struct Seg {
     int pos0, pos1;           // cache positions [pos0, pos1)
     int steps;                // -1: no more segments
     int slot;                 // -1: the whole segment, else the partial result's slot
-    int pad;
+    int page[16];             // the pages of the first step's boxes
 };
 
 template <int N, int D>
@@ -59,8 +61,8 @@ struct Smem {
     static constexpr int kRing = 0;
     static constexpr int kQ = kRing + kStages * kTileBytes;
     static constexpr int kP = kQ + 2 * kQBytes;                   // [128][64] bf16, 128-byte rows
-    static constexpr int kMax = kP + kSteps * 128;                // [2][N][4]
-    static constexpr int kSum = kMax + 2 * N * 16;                // [N][4]
+    static constexpr int kMax = kP + kSteps * 128;                // [N][4]
+    static constexpr int kSum = kMax + N * 16;                    // [N][4]
     static constexpr int kSeg = kSum + N * 16;
     static constexpr int kBar = kSeg + kSegs * (int)sizeof(Seg);
     static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 + 2 + 2 + 2 + 2 + 2 + 1;
@@ -196,7 +198,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     if (warp == kSegWarp) {
         // ------------------------------------------------ segments and Q tiles
         const AttnSplit sp(p);
-        const int cta = blockIdx.x;
+        const int cta = blockIdx.x, nbox = kSteps / bx;
         bool ok = true;
         int si = 0;
         long long t = 0, end = 0;
@@ -241,8 +243,14 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             }
             if (lane == 0) {
                 const_cast<Seg&>(s_seg[slot]) = d;
-                ptx::mbar_arrive(b_seg_full + 8 * slot);
             }
+            __syncwarp();
+            if (more && lane < nbox) {
+                const int pos = d.pos0 + lane * bx;
+                s_seg[slot].page[lane] = pos < d.pos1 ? __ldg(p.table + (size_t)d.b * p.width + p.by_page(pos)) : -1;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(b_seg_full + 8 * slot);
             if (!more) break;
             // the Q tile, rows beyond the request's as zeros
             const int qb = si & 1;
@@ -252,17 +260,15 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             constexpr int kChunks = D / 8;
             const uint16_t* q = static_cast<const uint16_t*>(p.q);
             const uint32_t qs = base + L::kQ + qb * L::kQBytes;
-#pragma unroll 8
+#pragma unroll 4
             for (int i = lane; i < N * kChunks; i += 32) {
                 const int r = i / kChunks, c = i - r * kChunks;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (r < d.rows) {
-                    const int rr = d.r0 + r, tok = rr / p.G;
-                    x = __ldg(reinterpret_cast<const uint4*>(q + (d.q0 + tok) * p.q_stride + (size_t)(d.h * p.G + rr - tok * p.G) * D) + c);
-                }
-                const uint32_t at = qs + (c / 8) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+                const int rr = d.r0 + r, tok = p.by_group(rr);
+                const bool have = r < d.rows;
+                const uint16_t* src = q + (have ? (d.q0 + tok) * p.q_stride + (size_t)(d.h * p.G + rr - tok * p.G) * D + 8 * c : 0);
+                ptx::cp_async_16(qs + (c / 8) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, have ? 16u : 0u);
             }
+            ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
@@ -279,16 +285,17 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             const int slot = si % kSegs;
             ok = __all_sync(~0u, wait(b_seg_full + 8 * slot, si / kSegs));
             if (!ok) { if (lane == 0) give_up(2); break; }
-            const Seg d = const_cast<Seg&>(s_seg[slot]);
+            const Seg& sg = const_cast<Seg&>(s_seg[slot]);
+            struct { int b, h, pos0, pos1, steps; } d = {sg.b, sg.h, sg.pos0, sg.pos1, sg.steps};
+            int page = sg.page[lane & 15];
             __syncwarp();
             if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
             const int32_t* row = p.table + (size_t)d.b * p.width;
             auto page_of = [&](int step) {       // this lane's box of a step: its page, -1 beyond the end
                 const int pos = d.pos0 + step * kSteps + lane * bx;
-                return lane < nbox && pos < d.pos1 ? __ldg(row + pos / p.page_size) : -1;
+                return lane < nbox && pos < d.pos1 ? __ldg(row + p.by_page(pos)) : -1;
             };
-            int page = page_of(0);
             for (int s = 0; s < d.steps && ok; ++s) {
                 const int pos = d.pos0 + s * kSteps + lane * bx;
                 const bool want = lane < nbox && pos < d.pos1;
@@ -296,7 +303,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 const uint32_t bad = __ballot_sync(~0u, want && !have);
                 const int boxes = __popc(__ballot_sync(~0u, have));
                 if (bad && lane == 0) raise_status(p.status, kBadPage);
-                const int y = pos % p.page_size, pg = page;
+                const int y = pos - p.by_page(pos) * p.page_size, pg = page;
                 if (s + 1 < d.steps) page = page_of(s + 1);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++fill) {
@@ -382,8 +389,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     if (!ok) break;
                     pend = true; pend_first = s == 0; pend_step = step; pend_seg = si;
                 }
+                if (ok && pend) second();        // the segment's end does not wait for the next one's keys
             }
-            if (ok && pend) second();
             if (!ok) give_up(4);
             // nothing is in flight in the tensor core when the CTA leaves
             ptx::mma_commit(b_end);
@@ -404,15 +411,21 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             const int slot = si % kSegs;
             ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
             if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
-            const Seg d = const_cast<Seg&>(s_seg[slot]);
+            const Seg& sg = const_cast<Seg&>(s_seg[slot]);
+            struct { int b, h, q0, n, len, r0, rows, pos0, pos1, steps, slot; } d = {
+                sg.b, sg.h, sg.q0, sg.n, sg.len, sg.r0, sg.rows, sg.pos0, sg.pos1, sg.steps, sg.slot};
             __syncwarp();
             if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
             const uint32_t o_at = tmem + lanes + 2 * N + (si & 1u) * N + half * HC;
             const int first_new = d.len - d.n;                     // position of the block's first token
-            float m[HC], l[HC];                                    // log2 of the reference, sum of the weights (this thread's positions)
+            // lane c: query row, token and position of column c of this half
+            const int my_row = half * HC + (lane & (HC - 1)), my_tok = p.by_group(d.r0 + my_row), my_last = first_new + my_tok;
+            float neg[HC], l[HC];                                  // minus the reference, this thread's sum of the weights
 #pragma unroll
-            for (int c = 0; c < HC; ++c) { m[c] = -INFINITY; l[c] = 0.f; }
+            for (int c = 0; c < HC; ++c) { neg[c] = 0.f; l[c] = 0.f; }
+            float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
+            bool unset = true;                                     // a column of the half has no reference yet
             bool stop = false;
             for (int s = 0; s < d.steps; ++s, ++step) {
                 const int pos0 = d.pos0 + s * kSteps, pos = pos0 + row, there = d.pos1 - pos0;
@@ -437,42 +450,44 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 if (edge) {
 #pragma unroll
                     for (int c = 0; c < HC; ++c) {
-                        const int last = first_new + (d.r0 + half * HC + c) / p.G;
+                        const int last = __shfl_sync(~0u, my_last, c);
                         if (gone || pos > last) x[c] = -INFINITY;
                     }
                 }
-                float mine = -INFINITY;
+                float high = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < HC; ++c) {
-                    const float w = warp_max(x[c]);
-                    if (lane == c) mine = w;
-                }
-                float* mx = reinterpret_cast<float*>(s_max + (step & 1u) * N + half * HC);
-                if (lane < HC) mx[lane * 4 + quarter] = mine;
-                if (ptx::bar_red_or(1 + half, 128, !ok)) { stop = true; break; }
-                float top[HC];
-                bool grow = false;
-#pragma unroll
-                for (int c = 0; c < HC; ++c) {
-                    const float4 w = reinterpret_cast<const float4*>(mx)[c];
-                    top[c] = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * scale2;
-                    grow |= top[c] > m[c] + kSlack;
-                }
+                for (int c = 0; c < HC; ++c) high = fmaxf(high, fmaf(x[c], scale2, neg[c]));
+                const bool move = ptx::bar_red_or(1 + half, 128, unset || high > kSlack || !ok);
                 // the product before this one is done: P may be overwritten, O rescaled
                 if (step > 0) ok = wait(b_pv, step - 1) && ok;
-                if (grow) {                     // the same in every thread of the half
-                    ptx::tc_fence_after();
+                if (move) {                     // the same in every thread of the half
+                    float mine = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        const float w = warp_max(x[c]);
+                        if (lane == c) mine = w;
+                    }
+                    float* mx = reinterpret_cast<float*>(s_max + half * HC);
+                    if (lane < HC) mx[lane * 4 + quarter] = mine;
+                    if (ptx::bar_red_or(1 + half, 128, !ok)) { stop = true; break; }
+                    const float4 w4 = reinterpret_cast<const float4*>(mx)[lane & (HC - 1)];
+                    const float top = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) * scale2;
+                    const float to = fmaxf(my_ref, top);
+                    const float my_a = to > my_ref ? fast_exp2(my_ref - to) : 1.f;
+                    my_ref = to;
+                    unset = __any_sync(~0u, to == -INFINITY);
+                    // (the next write to s_max comes after another barrier)
                     float a[HC];
 #pragma unroll
                     for (int c = 0; c < HC; ++c) {
-                        const float to = fmaxf(top[c], m[c]);
-                        a[c] = to > m[c] ? fast_exp2(m[c] - to) : 1.f;
+                        a[c] = __shfl_sync(~0u, my_a, c);
+                        const float r = __shfl_sync(~0u, to, c);
+                        neg[c] = r == -INFINITY ? 0.f : -r;
                         l[c] *= a[c];
-                        m[c] = to;
                     }
                     if (s > 0) {
+                        ptx::tc_fence_after();
                         float o[HC];
-                        __syncwarp();
                         tmem_get<HC>(o_at, o);
 #pragma unroll
                         for (int c = 0; c < HC; ++c) o[c] *= a[c];
@@ -486,8 +501,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     float w[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float ref = m[c0 + e] == -INFINITY ? 0.f : m[c0 + e];
-                        w[e] = fast_exp2(fmaf(x[c0 + e], scale2, -ref));
+                        w[e] = fast_exp2(fmaf(x[c0 + e], scale2, neg[c0 + e]));
                         l[c0 + e] += w[e];
                     }
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
@@ -538,51 +552,66 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (si & 1u));
-            float mine = 0.f;
-#pragma unroll
-            for (int c = 0; c < HC; ++c) {
-                float t = l[c];
-#pragma unroll
-                for (int q = 16; q; q >>= 1) t += __shfl_xor_sync(~0u, t, q);
-                if (lane == c) mine = t;
-            }
+            // column sums: after the exchanges of 16, 8, .. lanes lane c holds
+            // column c % HC of this warp's positions, then the 4 warps' are added
             float* sm = reinterpret_cast<float*>(s_sum + half * HC);
-            if (lane < HC) sm[lane * 4 + quarter] = mine;
+            {
+#pragma unroll
+                for (int w = HC / 2; w; w >>= 1) {
+                    const bool up = lane & w;
+#pragma unroll
+                    for (int c = 0; c < HC / 2; ++c)
+                        if (c < w) {
+                            const float give = up ? l[c] : l[c + w], keep = up ? l[c + w] : l[c];
+                            l[c] = keep + __shfl_xor_sync(~0u, give, w);
+                        }
+                }
+#pragma unroll
+                for (int w = HC; w < 32; w <<= 1) l[0] += __shfl_xor_sync(~0u, l[0], w);
+            }
+            if (lane < HC) sm[lane * 4 + quarter] = l[0];
             if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
+            // lane c: sum, scale and place of column c's row
+            const float4 s4 = reinterpret_cast<const float4*>(sm)[lane & (HC - 1)];
+            const float my_sum = (s4.x + s4.y) + (s4.z + s4.w);
+            const float my_inv = my_sum != 0.f ? 1.f / my_sum : 0.f;
+            const int my_at = (d.q0 + my_tok) * p.Hq + d.h * p.G + (d.r0 + my_row - my_tok * p.G);   // below N * Hq < 2^31
             const int dim = row;
             if (s_flags[2]) {
                 // non-finite values of the block's later tokens (this CTA's positions)
-                for (int pos = max(first_new + 1, d.pos0); pos < d.pos1 && dim < D; ++pos) {
-                    const int pg = pos / p.page_size, page = p.table[(size_t)d.b * p.width + pg];
+                for (int pos = max(first_new + 1, d.pos0); pos < d.pos1; ++pos) {
+                    const int pg = p.by_page(pos), page = p.table[(size_t)d.b * p.width + pg];
                     if (page < 0 || page >= p.pages) continue;
-                    const float v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
-                                          ((long long)d.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
-                    if (fabsf(v) < INFINITY) continue;
+                    float v = 0.f;
+                    if (dim < D)
+                        v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
+                                   ((long long)d.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
+                    const bool odd = !(fabsf(v) < INFINITY);
 #pragma unroll
-                    for (int c = 0; c < HC; ++c)
-                        if (pos <= first_new + (d.r0 + half * HC + c) / p.G) o[c] += v;
+                    for (int c = 0; c < HC; ++c) {
+                        const int last = __shfl_sync(~0u, my_last, c);
+                        if (odd && pos <= last) o[c] += v;
+                    }
                 }
             }
-            const float* stats0 = p.part + (size_t)2 * p.ctas * p.row_tile * D;
+            const int cols = min(HC, d.rows - half * HC);
+            if (d.slot < 0) {
+                uint16_t* out = static_cast<uint16_t*>(p.out) + dim;
 #pragma unroll
-            for (int c = 0; c < HC; ++c) {
-                const int r = half * HC + c;
-                if (r >= d.rows) break;
-                const float4 s4 = reinterpret_cast<const float4*>(sm)[c];
-                const float sum = (s4.x + s4.y) + (s4.z + s4.w);
-                const int rr = d.r0 + r, tok = rr / p.G, head = d.h * p.G + rr - tok * p.G;
-                const size_t at = (size_t)(d.q0 + tok) * p.Hq + head;
-                if (d.slot < 0) {
-                    if (dim < D) {
-                        const float y = o[c] * (sum != 0.f ? 1.f / sum : 0.f);
-                        static_cast<uint16_t*>(p.out)[at * D + dim] = (uint16_t)pack_bf16(y, 0.f);
-                    }
-                    if (row == 0 && p.lse) p.lse[at] = sum != 0.f ? m[c] * kLn2 + logf(sum) : -INFINITY;
-                } else {
-                    const size_t pr = (size_t)d.slot * p.row_tile + r;
-                    if (dim < D) p.part[pr * D + dim] = o[c];
-                    if (row == 0) *reinterpret_cast<float2*>(const_cast<float*>(stats0) + pr * 2) = make_float2(m[c], sum);
+                for (int c = 0; c < HC; ++c) {
+                    const float inv = __shfl_sync(~0u, my_inv, c);
+                    const int at = __shfl_sync(~0u, my_at, c);
+                    if (c < cols && dim < D) out[(size_t)at * D] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
                 }
+                if (quarter == 0 && lane < cols && p.lse)
+                    p.lse[my_at] = my_sum != 0.f ? my_ref * kLn2 + logf(my_sum) : -INFINITY;
+            } else {
+                float* part = p.part + ((size_t)d.slot * p.row_tile + half * HC) * D + dim;
+#pragma unroll
+                for (int c = 0; c < HC; ++c)
+                    if (c < cols && dim < D) part[c * D] = o[c];
+                float2* stats = reinterpret_cast<float2*>(p.part + (size_t)2 * p.ctas * p.row_tile * D);
+                if (quarter == 0 && lane < cols) stats[(size_t)d.slot * p.row_tile + my_row] = make_float2(my_ref, my_sum);
             }
         }
         if (!ok && lane == 0) give_up(5);

@@ -44,6 +44,19 @@ struct AppendParams {
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t s);
 
 // ----------------------------------------------------------- cache attention
+// Division of 0 <= x < 2^31 by a number fixed on the host (Granlund and
+// Montgomery, "Division by invariant integers using multiplication").
+struct FastDiv {
+    uint32_t d = 1, mul = 1, shift = 0;
+    void set(uint32_t div) {
+        d = div;
+        shift = 0;
+        while ((1ull << shift) < div) ++shift;
+        mul = (uint32_t)((((1ull << shift) - div) << 32) / div + 1);
+    }
+    __device__ __forceinline__ int operator()(int x) const { return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift); }
+};
+
 struct AttnParams {
     const void* q; long long q_stride;                 // elements between tokens
     const void* k; const void* v; long long page_stride;   // elements between pages
@@ -53,6 +66,7 @@ struct AttnParams {
     int B, N, Hq, Hkv, G, D, pages, page_size, max_new;
     float scale;
     void* out; float* lse;
+    FastDiv by_page, by_group;  // by page_size, by G
     int row_tile, row_tiles;    // query rows of a key-value head per tile of rows, and such tiles
     int ctas;                   // CTAs the work is split over
     float* part;                // [2 ctas][row_tile][D] sums, then [2 ctas][row_tile][2] (max, sum)

@@ -127,6 +127,8 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     p.B = B; p.N = N; p.Hq = q_heads; p.Hkv = kv_heads; p.G = q_heads / kv_heads; p.D = head_dim;
     p.pages = pages; p.page_size = page_size; p.max_new = max_new;
     p.scale = scale; p.out = out; p.lse = lse;
+    p.by_page.set((uint32_t)page_size);
+    p.by_group.set((uint32_t)p.G);
     const int rows = p.G * max_new;
     const bool mma = attn_mma_supported(p);
     p.row_tile = attn_row_tile(rows, mma);
