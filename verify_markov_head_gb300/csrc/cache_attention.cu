@@ -85,19 +85,19 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnParam
     if (tid == 0) grid_launch_dependents();   // the join is scheduled now and waits for this grid
     const int cta = blockIdx.x;
     empty_rows<T>(p, cta, gridDim.x);
-    const AttnSplit sp(p);
+    const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
     if (cta >= sp.n) return;
     const T* kc = static_cast<const T*>(p.k);
     const T* vc = static_cast<const T*>(p.v);
     const float scale2 = p.scale * kLog2e;
     constexpr int RW = MR / 4;              // rows of a warp
-    const long long end = sp.first(cta + 1);
-    for (long long t = sp.first(cta); t < end;) {
-        const AttnSegment g = attn_segment(p, sp, t);
+    const int end = sp.first(cta + 1);
+    for (int t = sp.first(cta); t < end;) {
+        const AttnSegment g = attn_segment(p, sp, t, attn_first_round(p));
         const RowMap rm(p, g.b);
         const int r0 = g.rt * p.row_tile;
         const int rows = max(0, min(p.row_tile, rm.n * p.G - r0));
-        const int j0 = (int)(t - g.t0), j1 = (int)min((long long)g.tiles, end - g.t0);
+        const int j0 = t - g.t0, j1 = min(g.tiles, end - g.t0);
         __syncthreads();
         for (int i = tid; i < MR * D; i += kSimtThreads) {
             const int r = i / D, d = i - r * D;
@@ -252,11 +252,12 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnParam
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     grid_dependency_wait();
-    const AttnSplit sp(p);
+    const int mine = attn_first_round(p);
+    const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
     const int c = blockIdx.x + 1;
     if (c >= sp.n) return;
-    const long long t = sp.first(c);
-    const AttnSegment g = attn_segment(p, sp, t);
+    const int t = sp.first(c);
+    const AttnSegment g = attn_segment(p, sp, t, mine);
     if (g.t0 == t || sp.cta_of(g.t0) != c - 1) return;
     const int last = sp.cta_of(g.t0 + g.tiles - 1);
     const RowMap rm(p, g.b);

@@ -11,10 +11,12 @@
 // there, each is read once by the tensor core whatever N is, and no lane is
 // spent on padding rows.  What is left per position and row is one 2^x.
 //
-// Roles (11 warps, one CTA per SM, a ring of 5 tiles of 32 KB):
+// Roles (12 warps, one CTA per SM, a ring of 5 tiles of 32 KB):
 //   warps 0-3, 4-7   softmax of the first and the second half of the columns:
 //                    thread = position; weights to shared memory
-//   warp 8           TMA producer (lane = box of a page)
+//   warps 8, 11      TMA producers of the keys and of the values (lane = box of a
+//                    page: 8 positions x 64 entries x both halves of the head x
+//                    up to 8 such groups)
 //   warp 9           MMA issuer
 //   warp 10          walks the CTA's segments: descriptors and Q tiles
 // The reference of a column's weights, 2^(s - ref), moves only when a score
@@ -38,8 +40,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSteps = 128;              // positions per step (one tile of K and one of V)
 constexpr int kSoftWarps = 8;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kSegWarp = 10, kWarps = 11;
-constexpr int kSegs = 4;                 // segment descriptors in flight
+constexpr int kKeyWarp = 8, kMmaWarp = 9, kSegWarp = 10, kValWarp = 11, kWarps = 12;
+constexpr int kSegs = 8;                 // segment descriptors in flight
 constexpr int kBadRing = 8;              // steps the producer may be ahead of the softmax, and more
 constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
 constexpr long long kDrainCycles = 200000000LL;
@@ -56,6 +58,7 @@ struct Seg {
 template <int N, int D>
 struct Smem {
     static constexpr int kTileBytes = kSteps * D * 2;
+    static constexpr int kGroup = 8 * D * 2;                      // 8 positions: [half of the head][position][64 entries]
     static constexpr int kStages = 5 * 128 / D;
     static constexpr int kQBytes = N * D * 2;
     static constexpr int kRing = 0;
@@ -66,16 +69,16 @@ struct Smem {
     static constexpr int kSeg = kSum + N * 16;
     static constexpr int kBar = kSeg + kSegs * (int)sizeof(Seg);
     static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 + 2 + 2 + 2 + 2 + 2 + 1;
-    static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, non-finite flag, bad boxes
-    static constexpr int kTotal = kFlags + 16 + 4 * kBadRing;
+    static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, non-finite flag, -, the producers' counts, bad boxes
+    static constexpr int kTotal = kFlags + 24 + 4 * kBadRing;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar,
-                                            uint64_t policy) {
+// The box at group `g` of (page, head) `z` (its other coordinates are 0).
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* m, int g, int z, uint32_t bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(g), "r"(z), "r"(bar), "l"(policy)
         : "memory");
 }
 
@@ -145,7 +148,7 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
 template <int N, int D>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                const int bx) {
+                const int bx, const int page_heads) {
     using L = Smem<N, D>;
     constexpr int HC = N / 2;                   // columns of a softmax half
     constexpr int kStages = L::kStages;
@@ -155,7 +158,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     uint8_t* gbase = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile uint32_t* s_flags = reinterpret_cast<volatile uint32_t*>(gbase + L::kFlags);   // [0] TMEM, [1] abort, [2] fix
-    volatile uint32_t* s_bad = s_flags + 4;     // [kBadRing] boxes of a step whose page is out of range
+    volatile uint32_t* s_bad = s_flags + 6;     // [kBadRing] boxes of a step whose page is out of range
     volatile Seg* s_seg = reinterpret_cast<volatile Seg*>(gbase + L::kSeg);
     volatile uint32_t* abort_flag = s_flags + 1;
     uint32_t bar = base + L::kBar;
@@ -168,7 +171,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     if (tid == 0) {
         grid_launch_dependents();       // the join is scheduled now and waits for this grid
         for (int i = 0; i < kStages; ++i) { ptx::mbar_init(b_full + 8 * i, 1); ptx::mbar_init(b_empty + 8 * i, 1); }
-        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 2 + kSoftWarps); }
+        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 3 + kSoftWarps); }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(b_q_full + 8 * i, 1); ptx::mbar_init(b_q_empty + 8 * i, 1);
             ptx::mbar_init(b_s_full + 8 * i, 1); ptx::mbar_init(b_s_empty + 8 * i, kSoftWarps);
@@ -183,7 +186,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         ptx::tmem_alloc(base + L::kFlags, 4 * N);
         ptx::tmem_relinquish();
     }
-    if (warp == kTmaWarp && lane == 0) { ptx::prefetch_tmap(&kmap); ptx::prefetch_tmap(&vmap); }
+    if (warp == kKeyWarp && lane == 0) ptx::prefetch_tmap(&kmap);
+    if (warp == kValWarp && lane == 0) ptx::prefetch_tmap(&vmap);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -197,88 +201,102 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
 
     if (warp == kSegWarp) {
         // ------------------------------------------------ segments and Q tiles
-        const AttnSplit sp(p);
+        const int first_round = attn_first_round(p);
+        const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
         const int cta = blockIdx.x, nbox = kSteps / bx;
         bool ok = true;
-        int si = 0;
-        long long t = 0, end = 0;
+        int t = 0, end = 0;
         AttnSegment g{};
         if (cta < sp.n) {
             t = sp.first(cta);
             end = sp.first(cta + 1);
-            g = attn_segment(p, sp, t);
+            g = attn_segment(p, sp, t, first_round);
         }
-        while (ok) {
+        // descriptor si, then the Q tile of segment si - 1: the producers learn of
+        // a segment while the Q buffers are still taken by the two before it
+        int q0 = 0, qh = 0, qr0 = 0, qrows = 0;
+        for (int si = 0; ok; ++si) {
             const int slot = si % kSegs;
-            if (si >= kSegs) ok = wait(b_seg_empty + 8 * slot, (si / kSegs) - 1);
-            ok = __all_sync(~0u, ok);
+            if (si >= kSegs) ok = __all_sync(~0u, wait(b_seg_empty + 8 * slot, (si / kSegs) - 1));
             if (!ok) { if (lane == 0) give_up(0); break; }
             const bool more = t < end;
-            Seg d{};
-            d.steps = -1;
+            volatile Seg& d = s_seg[slot];
+            int n0 = 0, nrows = 0, nr0 = 0;
             if (more) {
-                d.b = g.b; d.h = g.h;
-                d.q0 = p.q_off[g.b];
-                d.n = p.q_off[g.b + 1] - d.q0;
-                d.len = p.kv_len[g.b];
-                const long long cap = (long long)p.width * p.page_size;
-                if (d.n > p.max_new || d.n < 0 || d.q0 < 0 || d.q0 > p.N - d.n || d.len < 0 || d.len > cap) {
+                const int len_in = p.kv_len[g.b], qa = p.q_off[g.b], qe = p.q_off[g.b + 1];
+                const int cap = p.width * p.page_size;
+                int n = qe - qa, len = len_in;
+                n0 = qa;
+                if (n > p.max_new || n < 0 || qa < 0 || qa > p.N - n || len < 0 || len > cap) {
                     if (lane == 0) raise_status(p.status, kBadLength);
-                    d.n = d.q0 < 0 ? 0 : max(0, min(d.n, min(p.max_new, p.N - d.q0)));
-                    d.len = max(0, (int)min((long long)d.len, cap));
+                    n = qa < 0 ? 0 : max(0, min(n, min(p.max_new, p.N - qa)));
+                    len = max(0, min(len, cap));
                 }
-                d.r0 = g.rt * p.row_tile;
-                d.rows = max(0, min(p.row_tile, d.n * p.G - d.r0));
-                const int j0 = (int)(t - g.t0), j1 = (int)min((long long)g.tiles, end - g.t0);
-                d.pos0 = min(j0 * kTile, d.len);
-                d.pos1 = min(j1 * kTile, d.len);
-                d.steps = max(1, (d.pos1 - d.pos0 + kSteps - 1) / kSteps);
-                d.slot = j0 == 0 && j1 == g.tiles ? -1 : 2 * cta + (j0 == 0 ? 1 : 0);
-                t = g.t0 + j1;
-                if (t < end) {      // the next segment: the next head or row tile, or the next request that has tiles
-                    if (++g.rt == p.row_tiles) { g.rt = 0; ++g.h; }
-                    if (g.h == p.Hkv) g = attn_segment(p, sp, t);
-                    else g.t0 = t;
+                nr0 = g.rt * p.row_tile;
+                nrows = max(0, min(p.row_tile, n * p.G - nr0));
+                const int j0 = t - g.t0, j1 = min(g.tiles, end - g.t0);
+                const int pos0 = min(j0 * kTile, len), pos1 = min(j1 * kTile, len);
+                if (lane < nbox) {
+                    const int pos = pos0 + lane * bx;
+                    d.page[lane] = pos < pos1 ? __ldg(p.table + (size_t)g.b * p.width + p.by_page(pos)) : -1;
                 }
-            }
-            if (lane == 0) {
-                const_cast<Seg&>(s_seg[slot]) = d;
-            }
-            __syncwarp();
-            if (more && lane < nbox) {
-                const int pos = d.pos0 + lane * bx;
-                s_seg[slot].page[lane] = pos < d.pos1 ? __ldg(p.table + (size_t)d.b * p.width + p.by_page(pos)) : -1;
-            }
+                if (lane == 0) {
+                    d.b = g.b; d.h = g.h; d.q0 = qa; d.n = n; d.len = len; d.r0 = nr0; d.rows = nrows;
+                    d.pos0 = pos0; d.pos1 = pos1;
+                    d.steps = max(1, (pos1 - pos0 + kSteps - 1) / kSteps);
+                    d.slot = j0 == 0 && j1 == g.tiles ? -1 : 2 * cta + (j0 == 0 ? 1 : 0);
+                }
+            } else if (lane == 0) d.steps = -1;
+            const int nh = g.h;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(b_seg_full + 8 * slot);
-            if (!more) break;
-            // the Q tile, rows beyond the request's as zeros
-            const int qb = si & 1;
-            if (si >= 2) ok = wait(b_q_empty + 8 * qb, (si / 2) - 1);
-            ok = __all_sync(~0u, ok);
-            if (!ok) { if (lane == 0) give_up(1); break; }
-            constexpr int kChunks = D / 8;
-            const uint16_t* q = static_cast<const uint16_t*>(p.q);
-            const uint32_t qs = base + L::kQ + qb * L::kQBytes;
+            if (si > 0) {
+                // the Q tile, rows beyond the request's as zeros
+                const int qi = si - 1, qb = qi & 1;
+                if (qi >= 2) ok = __all_sync(~0u, wait(b_q_empty + 8 * qb, (qi / 2) - 1));
+                if (!ok) { if (lane == 0) give_up(1); break; }
+                // lane: a 16-byte chunk c of rows r, r + kRows, ...
+                constexpr int kChunks = D / 8, kRows = 32 / kChunks;
+                const int c = lane % kChunks;
+                int r = lane / kChunks, tok = p.by_group(qr0 + r), head = qr0 + r - tok * p.G;
+                const uint16_t* q = static_cast<const uint16_t*>(p.q);
+                const uint16_t* src = q + (q0 + tok) * p.q_stride + (size_t)(qh * p.G + head) * D + 8 * c;
+                const uint32_t qs = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
 #pragma unroll 4
-            for (int i = lane; i < N * kChunks; i += 32) {
-                const int r = i / kChunks, c = i - r * kChunks;
-                const int rr = d.r0 + r, tok = p.by_group(rr);
-                const bool have = r < d.rows;
-                const uint16_t* src = q + (have ? (d.q0 + tok) * p.q_stride + (size_t)(d.h * p.G + rr - tok * p.G) * D + 8 * c : 0);
-                ptx::cp_async_16(qs + (c / 8) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, have ? 16u : 0u);
+                for (int i = 0; i < N / kRows; ++i) {
+                    const bool have = r < qrows;
+                    ptx::cp_async_16(qs + r * 128 + (((c & 7) ^ (r & 7)) << 4), have ? src : q, have ? 16u : 0u);
+                    r += kRows;
+                    head += kRows;
+                    src += kRows * D;
+                    while (head >= p.G) { head -= p.G; src += p.q_stride - (long long)p.G * D; }
+                }
+                ptx::cp_async_wait_all();
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
             }
-            ptx::cp_async_wait_all();
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
-            ++si;
+            if (!more) break;
+            q0 = n0; qh = nh; qr0 = nr0; qrows = nrows;
+            // the next segment: the next head or row tile, or the next request that has tiles
+            t = g.t0 + min(g.tiles, end - g.t0);
+            if (t < end) {
+                if (++g.rt == p.row_tiles) { g.rt = 0; ++g.h; }
+                g.t0 = t;
+                if (g.h == p.Hkv) {
+                    // usually the next request; else (requests without tiles) looked up
+                    const int off = p.tile_off[g.b + 1], next = p.tile_off[min(p.B, g.b + 2)];
+                    g = next > off ? attn_segment_of(p, sp, t, g.b + 1, off, next) : attn_segment(p, sp, t, attn_first_round(p));
+                }
+            }
         }
-    } else if (warp == kTmaWarp) {
-        // ------------------------------------------------------------ producer
+    } else if (warp == kKeyWarp || warp == kValWarp) {
+        // ------------------------------------------------------------ producers
+        const int kv = warp == kValWarp;
+        const CUtensorMap* map = kv ? &vmap : &kmap;
         const uint64_t pol = p.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
         const int nbox = kSteps / bx;
-        uint32_t fill = 0;                       // tiles issued
+        uint32_t fill = kv;                      // this warp's next tile: keys 0, 2, .., values 1, 3, ..
         static_assert(kStages / 2 + 1 < kBadRing, "the producer stays within the ring of bad boxes");
         bool ok = true;
         for (int si = 0; ok; ++si) {
@@ -292,47 +310,45 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
             const int32_t* row = p.table + (size_t)d.b * p.width;
-            auto page_of = [&](int step) {       // this lane's box of a step: its page, -1 beyond the end
-                const int pos = d.pos0 + step * kSteps + lane * bx;
-                return lane < nbox && pos < d.pos1 ? __ldg(row + p.by_page(pos)) : -1;
-            };
-            for (int s = 0; s < d.steps && ok; ++s) {
+            for (int s = 0; s < d.steps; ++s, fill += 2) {
                 const int pos = d.pos0 + s * kSteps + lane * bx;
                 const bool want = lane < nbox && pos < d.pos1;
                 const bool have = want && page >= 0 && page < p.pages;
                 const uint32_t bad = __ballot_sync(~0u, want && !have);
                 const int boxes = __popc(__ballot_sync(~0u, have));
                 if (bad && lane == 0) raise_status(p.status, kBadPage);
-                const int y = pos - p.by_page(pos) * p.page_size, pg = page;
-                if (s + 1 < d.steps) page = page_of(s + 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++fill) {
-                    const int stage = fill % kStages;
-                    if (fill >= (uint32_t)kStages) ok = __all_sync(~0u, wait(b_empty + 8 * stage, fill / kStages - 1));
-                    if (!ok) { if (lane == 0) give_up(3); break; }
-                    const uint32_t full = b_full + 8 * stage;
-                    if (lane == 0) {
-                        if (!kv) s_bad[(fill / 2) % kBadRing] = bad;
-                        if (boxes) ptx::mbar_arrive_expect_tx(full, boxes * bx * D * 2);
-                        else ptx::mbar_arrive(full);
-                    }
-                    __syncwarp();
-                    if (have) {
-                        const uint32_t dst = base + L::kRing + stage * L::kTileBytes + lane * bx * 128;
-#pragma unroll
-                        for (int x = 0; x < D; x += 64)
-                            tma_load_4d(dst + (x / 64) * (kSteps * 128), kv ? &vmap : &kmap, x, y, d.h, pg, full, pol);
-                    }
+                const int group = (pos - p.by_page(pos) * p.page_size) >> 3, z = page * page_heads + d.h;
+                // the next step's page
+                page = lane < nbox && pos + kSteps < d.pos1 ? __ldg(row + p.by_page(pos + kSteps)) : -1;
+                const int stage = fill % kStages;
+                if (fill >= (uint32_t)kStages) ok = __all_sync(~0u, wait(b_empty + 8 * stage, fill / kStages - 1));
+                if (!ok) { if (lane == 0) give_up(3); break; }
+                const uint32_t full = b_full + 8 * stage;
+                if (lane == 0) {
+                    if (!kv) s_bad[(fill / 2) % kBadRing] = bad;
+                    if (boxes) ptx::mbar_arrive_expect_tx(full, boxes * bx * D * 2);
+                    else ptx::mbar_arrive(full);
                 }
+                __syncwarp();
+                if (have)
+                    tma_load_box(base + L::kRing + stage * L::kTileBytes + lane * bx * D * 2, map, group, z, full, pol);
             }
         }
-        // every copy issued lands before the CTA leaves
-        if (lane == 0)
-            for (uint32_t i = 0; i < (uint32_t)kStages; ++i)
-                if (fill > i) {
-                    const uint32_t last = (fill - 1) - ((fill - 1 - i) % kStages);
-                    ptx::mbar_wait_drain(b_full + 8 * i, (last / kStages) & 1u, kDrainCycles);
-                }
+        // every copy issued lands before the CTA leaves: the last fill of each stage
+        if (lane == 0) s_flags[4 + kv] = fill;
+        ptx::named_barrier(3, 64);
+        if (lane == 0 && !kv) {
+            const uint32_t keys = s_flags[4], vals = s_flags[5];      // tiles 0, 2, .. < keys and 1, 3, .. < vals
+            for (uint32_t i = 0; i < (uint32_t)kStages; ++i) {
+                // the last tile of stage i: at most kStages - 1 below the higher count
+                const uint32_t top = max(keys, vals);
+                for (uint32_t f = top; f-- > 0 && f + 4 * kStages >= top;)
+                    if (f % kStages == i && f < (f & 1u ? vals : keys)) {
+                        ptx::mbar_wait_drain(b_full + 8 * i, (f / kStages) & 1u, kDrainCycles);
+                        break;
+                    }
+            }
+        }
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
@@ -351,12 +367,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 if (!ok) return;
                 ptx::tc_fence_after();
                 const uint32_t va = base + L::kRing + st * L::kTileBytes, pa = base + L::kP;
-                // V^T: entries of a position lie along M, the 64-entry halves a
-                // half tile apart (head size 64: the second half of the lanes
-                // repeats the first and is not used); 16 positions = 2 KB
+                // V^T: entries of a position lie along M, the 64-entry halves 1 KB
+                // apart (head size 64: the second half of the lanes repeats the
+                // first and is not used); 16 positions = 2 groups
 #pragma unroll
                 for (int k = 0; k < kSteps / 16; ++k)
-                    ptx::mma_f16(tmem + 2 * N + ob * N, ptx::smem_desc_sw128(va + k * 2048, D == 128 ? kSteps * 128 : 0, 1024),
+                    ptx::mma_f16(tmem + 2 * N + ob * N, ptx::smem_desc_sw128(va + k * 2 * L::kGroup, D == 128 ? 1024 : 0, L::kGroup),
                                  ptx::smem_desc_sw128(pa + k * 2048, 16, 1024), id_o, pend_first && k == 0 ? 0u : 1u);
                 ptx::mma_commit(b_empty + 8 * st);
                 ptx::mma_commit(b_pv);
@@ -380,7 +396,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     const uint32_t ka = base + L::kRing + st * L::kTileBytes, qa = base + L::kQ + qb * L::kQBytes;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        ptx::mma_f16(tmem + sb * N, ptx::smem_desc_sw128(ka + (k / 4) * (kSteps * 128) + (k % 4) * 32, 16, 1024),
+                        ptx::mma_f16(tmem + sb * N, ptx::smem_desc_sw128(ka + (k / 4) * 1024 + (k % 4) * 32, 16, L::kGroup),
                                      ptx::smem_desc_sw128(qa + (k / 4) * (N * 128) + (k % 4) * 32, 16, 1024), id_s, k ? 1u : 0u);
                     ptx::mma_commit(b_empty + 8 * st);
                     ptx::mma_commit(b_s_full + 8 * sb);
@@ -407,27 +423,31 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         float4* s_sum = reinterpret_cast<float4*>(gbase + L::kSum);
         uint32_t step = 0;
         bool ok = true;
+        // A segment's rows are written after the first step of the next segment
+        // (its O^T is in the other half of tensor memory), so the tensor core
+        // and the producers go on meanwhile.  What is kept of it until then:
+        bool pend = false;
+        float pend_ref = 0.f, pend_sum = 0.f;                      // lane c: column c's reference and sum
         for (uint32_t si = 0;; ++si) {
             const int slot = si % kSegs;
             ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
             if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
             const Seg& sg = const_cast<Seg&>(s_seg[slot]);
-            struct { int b, h, q0, n, len, r0, rows, pos0, pos1, steps, slot; } d = {
-                sg.b, sg.h, sg.q0, sg.n, sg.len, sg.r0, sg.rows, sg.pos0, sg.pos1, sg.steps, sg.slot};
-            __syncwarp();
-            if (d.steps < 0) break;
-            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
+            struct { int n, len, r0, pos0, pos1, steps; } d = {sg.n, sg.len, sg.r0, sg.pos0, sg.pos1, sg.steps};
+            const bool none = d.steps < 0;                         // no more segments
+            if (none && !pend) break;
             const uint32_t o_at = tmem + lanes + 2 * N + (si & 1u) * N + half * HC;
             const int first_new = d.len - d.n;                     // position of the block's first token
-            // lane c: query row, token and position of column c of this half
-            const int my_row = half * HC + (lane & (HC - 1)), my_tok = p.by_group(d.r0 + my_row), my_last = first_new + my_tok;
+            // lane c: the last position that column c of this half sees
+            const int my_last = first_new + p.by_group(d.r0 + half * HC + (lane & (HC - 1)));
             float neg[HC], l[HC];                                  // minus the reference, this thread's sum of the weights
 #pragma unroll
             for (int c = 0; c < HC; ++c) { neg[c] = 0.f; l[c] = 0.f; }
             float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
             bool unset = true;                                     // a column of the half has no reference yet
             bool stop = false;
-            for (int s = 0; s < d.steps; ++s, ++step) {
+            for (int s = 0; s < d.steps || s == 0; ++s) {
+                if (!none) {
                 const int pos0 = d.pos0 + s * kSteps, pos = pos0 + row, there = d.pos1 - pos0;
                 ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
                 ok = __all_sync(~0u, ok);
@@ -517,12 +537,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     ok = wait(b_full + 8 * (vi % kStages), vi / kStages) && ok;
                     const bool later = !gone && pos > first_new;
                     if (gone || later) {
-                        uint4* v = reinterpret_cast<uint4*>(gbase + L::kRing + (vi % kStages) * L::kTileBytes) + row * 8;
+                        uint4* v = reinterpret_cast<uint4*>(gbase + L::kRing + (vi % kStages) * L::kTileBytes + (row >> 3) * L::kGroup) + (row & 7) * 8;
                         constexpr int kHalves = D / 64;
                         // the two halves of the softmax warps share a row's chunks
 #pragma unroll
                         for (int c = half; c < 8 * kHalves; c += 2) {
-                            uint4* at = v + (c / 8) * (kSteps * 8) + (c % 8);
+                            uint4* at = v + (c / 8) * 64 + (c % 8);
                             if (gone) *at = make_uint4(0u, 0u, 0u, 0u);
                             else {
                                 const uint4 y = *at;
@@ -536,22 +556,73 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(b_p_full);
+                ++step;
+                }
+                if (s > 0 || !pend) continue;
+                // ------------------------------- the rows of the segment before
+                // (its last product was waited for in the step above)
+                pend = false;
+                if (none) ok = wait(b_pv, step - 1) && ok;
+                ok = __all_sync(~0u, ok);
+                const uint32_t pi = si - 1;
+                float o[HC];
+                if (ok) {
+                    ptx::tc_fence_after();
+                    tmem_get<HC>(tmem + lanes + 2 * N + (pi & 1u) * N + half * HC, o);
+                    ptx::tc_fence_before();
+                } else {
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) o[c] = 0.f;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (pi & 1u));
+                const Seg& e = const_cast<Seg&>(s_seg[pi % kSegs]);
+                const int e_row = half * HC + (lane & (HC - 1)), e_tok = p.by_group(e.r0 + e_row), dim = row;
+                const int e_at = (e.q0 + e_tok) * p.Hq + e.h * p.G + (e.r0 + e_row - e_tok * p.G);   // below N * Hq < 2^31
+                const int cols = min(HC, e.rows - half * HC);
+                if (s_flags[2]) {
+                    // non-finite values of the block's later tokens (this CTA's positions)
+                    const int e_new = e.len - e.n;
+                    for (int pos = max(e_new + 1, e.pos0); pos < e.pos1; ++pos) {
+                        const int pg = p.by_page(pos), page = p.table[(size_t)e.b * p.width + pg];
+                        if (page < 0 || page >= p.pages) continue;
+                        float v = 0.f;
+                        if (dim < D)
+                            v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
+                                       ((long long)e.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
+                        const bool odd = !(fabsf(v) < INFINITY);
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) {
+                            const int last = e_new + __shfl_sync(~0u, e_tok, c);
+                            if (odd && pos <= last) o[c] += v;
+                        }
+                    }
+                }
+                const int part_slot = e.slot;
+                if (part_slot < 0) {
+                    const float e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
+                    uint16_t* out = static_cast<uint16_t*>(p.out) + dim;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        const float inv = __shfl_sync(~0u, e_inv, c);
+                        const int at = __shfl_sync(~0u, e_at, c);
+                        if (c < cols && dim < D) out[(size_t)at * D] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
+                    }
+                    if (quarter == 0 && lane < cols && p.lse)
+                        p.lse[e_at] = pend_sum != 0.f ? pend_ref * kLn2 + logf(pend_sum) : -INFINITY;
+                } else {
+                    float* part = p.part + ((size_t)part_slot * p.row_tile + half * HC) * D + dim;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c)
+                        if (c < cols && dim < D) part[c * D] = o[c];
+                    float2* stats = reinterpret_cast<float2*>(p.part + (size_t)2 * p.ctas * p.row_tile * D);
+                    if (quarter == 0 && lane < cols) stats[(size_t)part_slot * p.row_tile + e_row] = make_float2(pend_ref, pend_sum);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * (pi % kSegs));
             }
             if (stop) { ok = false; break; }
-            // ----------------------------------------------------- segment's end
-            ok = wait(b_pv, step - 1) && ok;
-            ok = __all_sync(~0u, ok);
-            float o[HC];
-            if (ok) {
-                ptx::tc_fence_after();
-                tmem_get<HC>(o_at, o);
-                ptx::tc_fence_before();
-            } else {
-#pragma unroll
-                for (int c = 0; c < HC; ++c) o[c] = 0.f;
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (si & 1u));
+            if (none) break;
             // column sums: after the exchanges of 16, 8, .. lanes lane c holds
             // column c % HC of this warp's positions, then the 4 warps' are added
             float* sm = reinterpret_cast<float*>(s_sum + half * HC);
@@ -571,48 +642,10 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             }
             if (lane < HC) sm[lane * 4 + quarter] = l[0];
             if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
-            // lane c: sum, scale and place of column c's row
             const float4 s4 = reinterpret_cast<const float4*>(sm)[lane & (HC - 1)];
-            const float my_sum = (s4.x + s4.y) + (s4.z + s4.w);
-            const float my_inv = my_sum != 0.f ? 1.f / my_sum : 0.f;
-            const int my_at = (d.q0 + my_tok) * p.Hq + d.h * p.G + (d.r0 + my_row - my_tok * p.G);   // below N * Hq < 2^31
-            const int dim = row;
-            if (s_flags[2]) {
-                // non-finite values of the block's later tokens (this CTA's positions)
-                for (int pos = max(first_new + 1, d.pos0); pos < d.pos1; ++pos) {
-                    const int pg = p.by_page(pos), page = p.table[(size_t)d.b * p.width + pg];
-                    if (page < 0 || page >= p.pages) continue;
-                    float v = 0.f;
-                    if (dim < D)
-                        v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
-                                   ((long long)d.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
-                    const bool odd = !(fabsf(v) < INFINITY);
-#pragma unroll
-                    for (int c = 0; c < HC; ++c) {
-                        const int last = __shfl_sync(~0u, my_last, c);
-                        if (odd && pos <= last) o[c] += v;
-                    }
-                }
-            }
-            const int cols = min(HC, d.rows - half * HC);
-            if (d.slot < 0) {
-                uint16_t* out = static_cast<uint16_t*>(p.out) + dim;
-#pragma unroll
-                for (int c = 0; c < HC; ++c) {
-                    const float inv = __shfl_sync(~0u, my_inv, c);
-                    const int at = __shfl_sync(~0u, my_at, c);
-                    if (c < cols && dim < D) out[(size_t)at * D] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
-                }
-                if (quarter == 0 && lane < cols && p.lse)
-                    p.lse[my_at] = my_sum != 0.f ? my_ref * kLn2 + logf(my_sum) : -INFINITY;
-            } else {
-                float* part = p.part + ((size_t)d.slot * p.row_tile + half * HC) * D + dim;
-#pragma unroll
-                for (int c = 0; c < HC; ++c)
-                    if (c < cols && dim < D) part[c * D] = o[c];
-                float2* stats = reinterpret_cast<float2*>(p.part + (size_t)2 * p.ctas * p.row_tile * D);
-                if (quarter == 0 && lane < cols) stats[(size_t)d.slot * p.row_tile + my_row] = make_float2(my_ref, my_sum);
-            }
+            pend = true;
+            pend_ref = my_ref;
+            pend_sum = (s4.x + s4.y) + (s4.z + s4.w);
         }
         if (!ok && lane == 0) give_up(5);
     }
@@ -639,13 +672,16 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     if (!enc) return cudaErrorNotSupported;
     int bx = 64;                                 // positions of a box: a power of two that divides a page
     while (p.page_size % bx) bx >>= 1;
+    // a cache as [page and head][group of 8 positions][half of the head][position][64 entries]
+    const long long per_head = (long long)p.page_size * D;
+    const int page_heads = (int)(p.page_stride / per_head);
     CUtensorMap maps[2];
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv, (cuuint64_t)p.pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.page_size * D * 2, (cuuint64_t)p.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)bx, 1, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
+    const cuuint64_t dims[5] = {64, 8, D / 64, (cuuint64_t)p.page_size / 8, (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv};
+    const cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16, (cuuint64_t)per_head * 2};
+    const cuuint32_t box[5] = {64, 8, D / 64, (cuuint32_t)bx / 8, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < 2; ++i)
-        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i ? p.v : p.k), dims, strides, box, es,
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(i ? p.v : p.k), dims, strides, box, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
@@ -653,15 +689,17 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     static_assert(Smem<N, D>::kTotal + 1024 <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attn_mma_kernel<N, D><<<p.ctas, kWarps * 32, smem, s>>>(p, maps[0], maps[1], bx);
+    attn_mma_kernel<N, D><<<p.ctas, kWarps * 32, smem, s>>>(p, maps[0], maps[1], bx, page_heads);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 bool attn_mma_supported(const AttnParams& p) {
-    // a page stride that a tensor map can hold
-    return p.bf16 && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.page_stride < (1LL << 38) &&
+    // pages a whole number of heads apart, all of them within a tensor map's last dimension
+    const long long per_head = (long long)p.page_size * p.D;
+    return p.bf16 && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 &&
+           p.page_stride / per_head < (1LL << 31) && p.pages * (p.page_stride / per_head) < (1LL << 31) &&
            tma_encoder() != nullptr;
 }
 

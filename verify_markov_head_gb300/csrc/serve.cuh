@@ -82,52 +82,76 @@ inline int attn_row_tile(int rows, bool mma) {
 
 // The split of an attention launch.  The work is the list of all tiles of
 // kTile cache positions, ordered by request, key-value head, row tile and
-// position; CTA c takes the tiles [first(c), first(c + 1)).  A segment is the
-// run of tiles of one (request, head, row tile).  A segment that crosses CTA
-// boundaries leaves one partial result per CTA (slot 2c + 1 where the segment
-// starts in c, else 2c), which the join kernel adds up in CTA order.
+// position; CTA c takes the tiles [first(c), first(c + 1)), a contiguous share
+// that differs by one tile at most.  A segment is the run of tiles of one
+// (request, head, row tile).  A segment that crosses CTA boundaries leaves one
+// partial result per CTA (slot 2c + 1 where the segment starts in c, else 2c),
+// which the join kernel adds up in CTA order.
 struct AttnSplit {
-    long long total;   // tiles
+    int total;         // tiles
     int n;             // CTAs that have tiles
     int heads;         // key-value heads * row tiles
-    __device__ __forceinline__ AttnSplit(const AttnParams& p) {
+    int each, more;    // tiles of a CTA; the first `more` CTAs take one more
+    // tiles_all = tile_off[B], first_off = tile_off[0]
+    __device__ __forceinline__ AttnSplit(const AttnParams& p, int tiles_all, int first_off) {
         heads = p.Hkv * p.row_tiles;
         const long long most = (long long)p.B * (((long long)p.width * p.page_size + kTile - 1) / kTile);
-        const long long t = p.tile_off[p.B];
-        const bool ok = t >= 0 && t <= most && p.tile_off[0] == 0;
-        if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) raise_status(p.status, kBadLength);
-        total = ok ? t * heads : 0;
-        n = total < p.ctas ? (int)total : p.ctas;
+        const bool ok = tiles_all >= 0 && tiles_all <= most && first_off == 0 && (long long)tiles_all * heads < (1LL << 31);
+        if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x % 32 == 0) raise_status(p.status, kBadLength);
+        total = ok ? tiles_all * heads : 0;
+        n = total < p.ctas ? total : p.ctas;
+        each = n ? total / n : 0;
+        more = n ? total - each * n : 0;
     }
-    __device__ __forceinline__ long long first(int c) const { return total * c / n; }
-    __device__ __forceinline__ int cta_of(long long t) const { return (int)(((t + 1) * n - 1) / total); }
+    __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int cta_of(int t) const {
+        const int longer = more * (each + 1);
+        return t < longer ? t / (each + 1) : more + (t - longer) / each;
+    }
 };
 
 struct AttnSegment {
     int b, h, rt;        // request, key-value head, row tile
-    long long t0;        // its first tile in the list
+    int t0;              // its first tile in the list
     int tiles;
 };
 
-// The segment of tile t: the request by binary search over its tile offsets.
-__device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnSplit& sp, long long t) {
-    const int tt = (int)(t / sp.heads);
-    int lo = 0, hi = p.B;                       // tile_off[lo] <= tt < tile_off[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.tile_off[mid] <= tt) lo = mid; else hi = mid;
-    }
+// The segment of tile t, off and next being the tile offsets of its request b.
+__device__ __forceinline__ AttnSegment attn_segment_of(const AttnParams& p, const AttnSplit& sp, int t, int b, int off, int next) {
     AttnSegment g;
-    g.b = lo;
-    const int off = p.tile_off[lo];
-    g.tiles = max(1, p.tile_off[lo + 1] - off);
-    const long long local = t - (long long)off * sp.heads;
-    int hr = (int)(local / g.tiles);
+    g.b = b;
+    g.tiles = max(1, next - off);
+    const int local = t - off * sp.heads;
+    int hr = local / g.tiles;
     hr = hr < 0 ? 0 : (hr >= sp.heads ? sp.heads - 1 : hr);
-    g.t0 = (long long)off * sp.heads + (long long)hr * g.tiles;
+    g.t0 = off * sp.heads + hr * g.tiles;
     g.h = hr / p.row_tiles;
     g.rt = hr - g.h * p.row_tiles;
     return g;
+}
+
+// The segment of tile t, looked up by a whole warp: the request whose tile
+// offsets enclose t, 32 offsets at a time (`mine`: this lane's offset of the
+// first round, tile_off[min(B, lane * ceil(B / 32))]).
+__device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnSplit& sp, int t, int mine) {
+    const int lane = threadIdx.x & 31, tt = t / sp.heads;
+    int lo = 0, stride = (p.B + 31) / 32;
+    for (;;) {
+        const unsigned le = __ballot_sync(~0u, mine <= tt && lo + lane * stride < p.B);
+        const int k = le ? 31 - __clz(le) : 0;
+        lo += k * stride;
+        if (stride == 1) {
+            const int off = __shfl_sync(~0u, mine, k);
+            int next = __shfl_sync(~0u, mine, (k + 1) & 31);
+            if (k == 31) next = p.tile_off[min(p.B, lo + 1)];
+            return attn_segment_of(p, sp, t, lo, off, next);
+        }
+        stride = (stride + 31) / 32;
+        mine = p.tile_off[min(p.B, lo + lane * stride)];
+    }
+}
+__device__ __forceinline__ int attn_first_round(const AttnParams& p) {
+    return p.tile_off[min(p.B, (int)(threadIdx.x & 31) * ((p.B + 31) / 32))];
 }
 
 // ------------------------------------------------------------------- logits
