@@ -88,6 +88,13 @@ __device__ __forceinline__ float warp_max(float x) {     // over the warp, NaN l
     return y;
 }
 
+// Nonzero in one lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
 // N columns of 32 lanes, waited for.
 template <int C> __device__ __forceinline__ void tmem_get(uint32_t a, float (&v)[C]);
 template <> __device__ __forceinline__ void tmem_get<8>(uint32_t a, float (&v)[8]) {
@@ -352,66 +359,81 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, N, false, false);
-            constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, N, true, true);
-            uint32_t step = 0;                   // steps whose S product was issued
-            bool ok = true;
-            // a step whose S product was issued and whose O product was not
-            bool pend = false, pend_first = false;
-            uint32_t pend_step = 0, pend_seg = 0;
-            auto second = [&]() {                // O^T (+)= V^T P^T of the pending step
-                const uint32_t vi = 2 * pend_step + 1, st = vi % kStages, ob = pend_seg & 1u;
-                ok = wait(b_full + 8 * st, vi / kStages) && wait(b_p_full, pend_step);
-                if (ok && pend_first && pend_seg >= 2) ok = wait(b_o_empty + 8 * ob, pend_seg / 2 - 1);
-                if (!ok) return;
-                ptx::tc_fence_after();
-                const uint32_t va = base + L::kRing + st * L::kTileBytes, pa = base + L::kP;
-                // V^T: entries of a position lie along M, the 64-entry halves 1 KB
-                // apart (head size 64: the second half of the lanes repeats the
-                // first and is not used); 16 positions = 2 groups
+        // the whole warp runs the loop, so that descriptors are uniform values;
+        // one elected lane issues
+        constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, N, false, false);
+        constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, N, true, true);
+        const uint32_t one = elect_one();
+        const uint64_t k_desc = ptx::smem_desc_sw128(base + L::kRing, 16, L::kGroup);
+        // V^T: entries of a position lie along M, the 64-entry halves 1 KB
+        // apart (head size 64: the second half of the lanes repeats the
+        // first and is not used); 16 positions = 2 groups
+        const uint64_t v_desc = ptx::smem_desc_sw128(base + L::kRing, D == 128 ? 1024 : 0, L::kGroup);
+        const uint64_t q_desc = ptx::smem_desc_sw128(base + L::kQ, 16, 1024);
+        const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, 16, 1024);
+        uint32_t step = 0;                   // steps whose S product was issued
+        bool ok = true;
+        // a step whose S product was issued and whose O product was not
+        bool pend = false, pend_first = false;
+        uint32_t pend_step = 0, pend_seg = 0;
+        auto all = [&](bool x) { return __all_sync(~0u, x); };
+        auto second = [&]() {                // O^T (+)= V^T P^T of the pending step
+            const uint32_t vi = 2 * pend_step + 1, st = vi % kStages, ob = pend_seg & 1u;
+            ok = all(wait(b_full + 8 * st, vi / kStages) && wait(b_p_full, pend_step));
+            if (ok && pend_first && pend_seg >= 2) ok = all(wait(b_o_empty + 8 * ob, pend_seg / 2 - 1));
+            if (!ok) return;
+            ptx::tc_fence_after();
+            const uint64_t va = v_desc + st * (L::kTileBytes / 16);
+            if (one) {
 #pragma unroll
                 for (int k = 0; k < kSteps / 16; ++k)
-                    ptx::mma_f16(tmem + 2 * N + ob * N, ptx::smem_desc_sw128(va + k * 2 * L::kGroup, D == 128 ? 1024 : 0, L::kGroup),
-                                 ptx::smem_desc_sw128(pa + k * 2048, 16, 1024), id_o, pend_first && k == 0 ? 0u : 1u);
+                    ptx::mma_f16(tmem + 2 * N + ob * N, va + k * (2 * L::kGroup / 16), p_desc + k * (2048 / 16), id_o,
+                                 pend_first && k == 0 ? 0u : 1u);
                 ptx::mma_commit(b_empty + 8 * st);
                 ptx::mma_commit(b_pv);
-                pend = false;
-            };
-            for (uint32_t si = 0; ok; ++si) {
-                const int slot = si % kSegs;
-                ok = wait(b_seg_full + 8 * slot, si / kSegs);
+            }
+            __syncwarp();
+            pend = false;
+        };
+        for (uint32_t si = 0; ok; ++si) {
+            const int slot = si % kSegs;
+            ok = all(wait(b_seg_full + 8 * slot, si / kSegs));
+            if (!ok) break;
+            const int steps = s_seg[slot].steps;
+            __syncwarp();
+            if (steps < 0) break;
+            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
+            const uint32_t qb = si & 1u;
+            const uint64_t qa = q_desc + qb * (L::kQBytes / 16);
+            ok = all(wait(b_q_full + 8 * qb, si / 2));
+            for (int s = 0; s < steps && ok; ++s, ++step) {
+                const uint32_t ki = 2 * step, st = ki % kStages, sb = step & 1u;
+                ok = all(wait(b_full + 8 * st, ki / kStages));
+                if (ok && step >= 2) ok = all(wait(b_s_empty + 8 * sb, step / 2 - 1));
                 if (!ok) break;
-                const int steps = s_seg[slot].steps;
-                if (steps < 0) break;
-                ptx::mbar_arrive(b_seg_empty + 8 * slot);
-                const uint32_t qb = si & 1u;
-                ok = wait(b_q_full + 8 * qb, si / 2);
-                for (int s = 0; s < steps && ok; ++s, ++step) {
-                    const uint32_t ki = 2 * step, st = ki % kStages, sb = step & 1u;
-                    ok = wait(b_full + 8 * st, ki / kStages);
-                    if (ok && step >= 2) ok = wait(b_s_empty + 8 * sb, step / 2 - 1);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t ka = base + L::kRing + st * L::kTileBytes, qa = base + L::kQ + qb * L::kQBytes;
+                ptx::tc_fence_after();
+                const uint64_t ka = k_desc + st * (L::kTileBytes / 16);
+                if (one) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        ptx::mma_f16(tmem + sb * N, ptx::smem_desc_sw128(ka + (k / 4) * 1024 + (k % 4) * 32, 16, L::kGroup),
-                                     ptx::smem_desc_sw128(qa + (k / 4) * (N * 128) + (k % 4) * 32, 16, 1024), id_s, k ? 1u : 0u);
-                    ptx::mma_commit(b_empty + 8 * st);
+                        ptx::mma_f16(tmem + sb * N, ka + (k / 4) * (1024 / 16) + (k % 4) * 2,
+                                     qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, k ? 1u : 0u);
                     ptx::mma_commit(b_s_full + 8 * sb);
+                    ptx::mma_commit(b_empty + 8 * st);
                     if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
-                    if (pend) second();
-                    if (!ok) break;
-                    pend = true; pend_first = s == 0; pend_step = step; pend_seg = si;
                 }
-                if (ok && pend) second();        // the segment's end does not wait for the next one's keys
+                __syncwarp();
+                if (pend) second();
+                if (!ok) break;
+                pend = true; pend_first = s == 0; pend_step = step; pend_seg = si;
             }
-            if (!ok) give_up(4);
-            // nothing is in flight in the tensor core when the CTA leaves
-            ptx::mma_commit(b_end);
-            ptx::mbar_wait_drain(b_end, 0, kDrainCycles);
+            if (ok && pend) second();        // the segment's end does not wait for the next one's keys
         }
+        if (!ok && lane == 0) give_up(4);
+        // nothing is in flight in the tensor core when the CTA leaves
+        if (one) ptx::mma_commit(b_end);
+        __syncwarp();
+        ptx::mbar_wait_drain(b_end, 0, kDrainCycles);
         __syncwarp();
     } else {
         // ------------------------------------------------------------- softmax
