@@ -97,7 +97,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnParam
         const RowMap rm(p, g.b);
         const int r0 = g.rt * p.row_tile;
         const int rows = max(0, min(p.row_tile, rm.n * p.G - r0));
-        const int j0 = t - g.t0, j1 = min(g.tiles, end - g.t0);
+        const int j0 = g.tile(sp, t), j1 = g.tile(sp, end);
+        t = g.t0 + sp.pad + g.tiles;             // the next segment
+        if (j0 == j1) continue;
         __syncthreads();
         for (int i = tid; i < MR * D; i += kSimtThreads) {
             const int r = i / D, d = i - r * D;
@@ -241,7 +243,6 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnParam
                 }
             }
         }
-        t = g.t0 + j1;
     }
 }
 
@@ -258,8 +259,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     if (c >= sp.n) return;
     const int t = sp.first(c);
     const AttnSegment g = attn_segment(p, sp, t, mine);
-    if (g.t0 == t || sp.cta_of(g.t0) != c - 1) return;
-    const int last = sp.cta_of(g.t0 + g.tiles - 1);
+    const int t1 = g.t0 + sp.pad;                // the place of its first tile
+    if (g.tiles == 0 || t1 >= t || sp.cta_of(t1) != c - 1) return;
+    const int last = sp.cta_of(t1 + g.tiles - 1);
     const RowMap rm(p, g.b);
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rr = g.rt * p.row_tile + row;

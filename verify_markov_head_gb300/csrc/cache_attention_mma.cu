@@ -219,6 +219,22 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             end = sp.first(cta + 1);
             g = attn_segment(p, sp, t, first_round);
         }
+        // to the next segment of this CTA that has tiles: the next head or row
+        // tile, or the next request
+        auto skip = [&]() {
+            while (t < end && g.tile(sp, t) == g.tile(sp, end)) {
+                t = g.tiles > 0 ? g.t0 + sp.pad + g.tiles : attn_request_at(p, g.b + 1) * sp.heads;
+                if (t >= end) break;
+                if (g.tiles > 0 && ++g.rt == p.row_tiles) { g.rt = 0; ++g.h; }
+                g.t0 = t;
+                if (g.tiles == 0 || g.h == p.Hkv) {
+                    // the next request, or (after one without tiles) looked up
+                    if (g.tiles > 0) g = attn_segment_of(p, sp, t, g.b + 1, attn_request_at(p, g.b + 1), attn_request_at(p, min(p.B, g.b + 2)));
+                    else g = attn_segment(p, sp, t, attn_first_round(p));
+                }
+            }
+        };
+        skip();
         // descriptor si, then the Q tile of segment si - 1: the producers learn of
         // a segment while the Q buffers are still taken by the two before it
         int q0 = 0, qh = 0, qr0 = 0, qrows = 0;
@@ -241,7 +257,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 }
                 nr0 = g.rt * p.row_tile;
                 nrows = max(0, min(p.row_tile, n * p.G - nr0));
-                const int j0 = t - g.t0, j1 = min(g.tiles, end - g.t0);
+                const int j0 = g.tile(sp, t), j1 = g.tile(sp, end);
                 const int pos0 = min(j0 * kTile, len), pos1 = min(j1 * kTile, len);
                 if (lane < nbox) {
                     const int pos = pos0 + lane * bx;
@@ -285,17 +301,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             }
             if (!more) break;
             q0 = n0; qh = nh; qr0 = nr0; qrows = nrows;
-            // the next segment: the next head or row tile, or the next request that has tiles
-            t = g.t0 + min(g.tiles, end - g.t0);
-            if (t < end) {
-                if (++g.rt == p.row_tiles) { g.rt = 0; ++g.h; }
-                g.t0 = t;
-                if (g.h == p.Hkv) {
-                    // usually the next request; else (requests without tiles) looked up
-                    const int off = p.tile_off[g.b + 1], next = p.tile_off[min(p.B, g.b + 2)];
-                    g = next > off ? attn_segment_of(p, sp, t, g.b + 1, off, next) : attn_segment(p, sp, t, attn_first_round(p));
-                }
-            }
+            t = g.t0 + sp.pad + g.tile(sp, end);     // the place behind the tiles just taken
+            skip();
         }
     } else if (warp == kKeyWarp || warp == kValWarp) {
         // ------------------------------------------------------------ producers

@@ -69,6 +69,7 @@ struct AttnParams {
     FastDiv by_page, by_group;  // by page_size, by G
     int row_tile, row_tiles;    // query rows of a key-value head per tile of rows, and such tiles
     int ctas;                   // CTAs the work is split over
+    int pad;                    // what a segment costs beside its tiles, in tiles (at least 1)
     float* part;                // [2 ctas][row_tile][D] sums, then [2 ctas][row_tile][2] (max, sum)
     uint32_t* status;
 };
@@ -80,25 +81,30 @@ inline int attn_row_tile(int rows, bool mma) {
     return mma ? (rows <= 16 ? 16 : rows <= 32 ? 32 : 64) : (rows <= 8 ? 8 : 32);
 }
 
-// The split of an attention launch.  The work is the list of all tiles of
-// kTile cache positions, ordered by request, key-value head, row tile and
-// position; CTA c takes the tiles [first(c), first(c + 1)), a contiguous share
-// that differs by one tile at most.  A segment is the run of tiles of one
-// (request, head, row tile).  A segment that crosses CTA boundaries leaves one
-// partial result per CTA (slot 2c + 1 where the segment starts in c, else 2c),
-// which the join kernel adds up in CTA order.
+// The split of an attention launch.  A segment is the run of tiles of kTile
+// cache positions of one (request, key-value head, row tile); the work is the
+// list of all segments, ordered by request, head and row tile.  Beginning and
+// ending a segment costs a CTA about as much as `pad` tiles, so each segment
+// enters the list with `pad` places before its tiles, and CTA c takes the
+// places [first(c), first(c + 1)), a contiguous share that differs by one at
+// most.  A segment whose tiles lie in several CTAs leaves one partial result
+// in each (slot 2c + 1 where its first tile is in c, else 2c), which the join
+// kernel adds up in CTA order.
 struct AttnSplit {
-    int total;         // tiles
-    int n;             // CTAs that have tiles
+    int total;         // places
+    int n;             // CTAs that have places
     int heads;         // key-value heads * row tiles
-    int each, more;    // tiles of a CTA; the first `more` CTAs take one more
+    int pad;
+    int each, more;    // places of a CTA; the first `more` CTAs take one more
     // tiles_all = tile_off[B], first_off = tile_off[0]
     __device__ __forceinline__ AttnSplit(const AttnParams& p, int tiles_all, int first_off) {
         heads = p.Hkv * p.row_tiles;
+        pad = p.pad;
         const long long most = (long long)p.B * (((long long)p.width * p.page_size + kTile - 1) / kTile);
-        const bool ok = tiles_all >= 0 && tiles_all <= most && first_off == 0 && (long long)tiles_all * heads < (1LL << 31);
+        const long long all = ((long long)tiles_all + (long long)p.pad * p.B) * heads;
+        const bool ok = tiles_all >= 0 && tiles_all <= most && first_off == 0 && all < (1LL << 31);
         if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x % 32 == 0) raise_status(p.status, kBadLength);
-        total = ok ? tiles_all * heads : 0;
+        total = ok ? (int)all : 0;
         n = total < p.ctas ? total : p.ctas;
         each = n ? total / n : 0;
         more = n ? total - each * n : 0;
@@ -112,27 +118,33 @@ struct AttnSplit {
 
 struct AttnSegment {
     int b, h, rt;        // request, key-value head, row tile
-    int t0;              // its first tile in the list
-    int tiles;
+    int t0;              // its first place in the list
+    int tiles;           // its tiles (may be none), in the places t0 + pad ..
+    // the tile at place t, or the first one after it
+    __device__ __forceinline__ int tile(const AttnSplit& sp, int t) const { return min(max(0, t - t0 - sp.pad), tiles); }
 };
 
-// The segment of tile t, off and next being the tile offsets of its request b.
+// Place of request b's first segment, in units of `heads` places.
+__device__ __forceinline__ int attn_request_at(const AttnParams& p, int b) { return p.tile_off[b] + p.pad * b; }
+
+// The segment at place t of request b, whose places begin at off * heads and
+// end at next * heads.
 __device__ __forceinline__ AttnSegment attn_segment_of(const AttnParams& p, const AttnSplit& sp, int t, int b, int off, int next) {
     AttnSegment g;
     g.b = b;
-    g.tiles = max(1, next - off);
-    const int local = t - off * sp.heads;
-    int hr = local / g.tiles;
+    const int len = max(sp.pad, next - off), local = t - off * sp.heads;
+    int hr = local / len;
     hr = hr < 0 ? 0 : (hr >= sp.heads ? sp.heads - 1 : hr);
-    g.t0 = off * sp.heads + hr * g.tiles;
+    g.tiles = len - sp.pad;
+    g.t0 = off * sp.heads + hr * len;
     g.h = hr / p.row_tiles;
     g.rt = hr - g.h * p.row_tiles;
     return g;
 }
 
-// The segment of tile t, looked up by a whole warp: the request whose tile
-// offsets enclose t, 32 offsets at a time (`mine`: this lane's offset of the
-// first round, tile_off[min(B, lane * ceil(B / 32))]).
+// The segment at place t, looked up by a whole warp: the request whose places
+// enclose t, 32 requests at a time (`mine`: this lane's value of the first
+// round, attn_first_round).
 __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnSplit& sp, int t, int mine) {
     const int lane = threadIdx.x & 31, tt = t / sp.heads;
     int lo = 0, stride = (p.B + 31) / 32;
@@ -143,15 +155,15 @@ __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const A
         if (stride == 1) {
             const int off = __shfl_sync(~0u, mine, k);
             int next = __shfl_sync(~0u, mine, (k + 1) & 31);
-            if (k == 31) next = p.tile_off[min(p.B, lo + 1)];
+            if (k == 31) next = attn_request_at(p, min(p.B, lo + 1));
             return attn_segment_of(p, sp, t, lo, off, next);
         }
         stride = (stride + 31) / 32;
-        mine = p.tile_off[min(p.B, lo + lane * stride)];
+        mine = attn_request_at(p, min(p.B, lo + lane * stride));
     }
 }
 __device__ __forceinline__ int attn_first_round(const AttnParams& p) {
-    return p.tile_off[min(p.B, (int)(threadIdx.x & 31) * ((p.B + 31) / 32))];
+    return attn_request_at(p, min(p.B, (int)(threadIdx.x & 31) * ((p.B + 31) / 32)));
 }
 
 // ------------------------------------------------------------------- logits

@@ -135,6 +135,7 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
     const int ctas = (mma ? 1 : 2) * num_sms();      // resident CTAs: one or two per SM
     p.ctas = ctas < kMaxAttnCtas ? ctas : kMaxAttnCtas;
+    p.pad = mma ? (head_dim == 64 ? 6 : 3) : 1;
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead);
     p.status = static_cast<uint32_t*>(ws);
     return launch_status(launch_cache_attention(p, static_cast<cudaStream_t>(stream)));
