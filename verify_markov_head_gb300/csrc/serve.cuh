@@ -177,7 +177,8 @@ struct LogitsParams {
     const int32_t* bias_tok; const float* bias_val; const int32_t* bias_off; int bias_n;
     const uint32_t* mask;
     int32_t* live;
-    uint32_t* status; uint32_t* tickets; uint32_t* counts;   // [B], [B][R]: zero between launches
+    uint32_t* status;
+    unsigned long long* counts;   // [B][R] arrivals and entries left, zero between launches
 };
 cudaError_t launch_logits(const LogitsParams& p, cudaStream_t s);
 

@@ -143,7 +143,7 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
 
 size_t dspark_logits_workspace_bytes(int B, int R) {
     if (B < 1 || B > 65535 || R < 1 || R > DSPARK_MAX_GAMMA + 1) return 0;
-    return kHead + ws_align256(sizeof(uint32_t) * (size_t)B * (R + 1));
+    return kHead + ws_align256(sizeof(unsigned long long) * (size_t)B * R);
 }
 
 dspark_status dspark_logits_process(const void* logits, dspark_dtype t, long long row_stride, void* out, int B, int R,
@@ -177,8 +177,7 @@ dspark_status dspark_logits_process(const void* logits, dspark_dtype t, long lon
     p.mask = mask; p.live = live;
     char* base = static_cast<char*>(ws);
     p.status = reinterpret_cast<uint32_t*>(base);
-    p.tickets = reinterpret_cast<uint32_t*>(base + kHead);
-    p.counts = p.tickets + B;
+    p.counts = reinterpret_cast<unsigned long long*>(base + kHead);
     return launch_status(launch_logits(p, static_cast<cudaStream_t>(stream)));
 }
 
