@@ -132,7 +132,8 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building the object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -467,27 +468,31 @@ def _typed(t, dtype, shape, name):
     """Address of a contiguous tensor of the given type and shape (None: any size)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return _p(t)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _cache_pair(k_cache, v_cache):
     """(dtype code, page stride) of two caches [pages, kv_heads, page_size,
     head_dim] whose pages are contiguous."""
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.stride() != v_cache.stride():
+    shape, stride = k_cache.shape, k_cache.stride()
+    if shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or stride != v_cache.stride():
         raise ValueError("k_cache and v_cache must share shape, dtype and strides")
-    _, H, P, D = k_cache.shape
-    if k_cache.stride()[1:] != (P * D, D, 1):
-        raise ValueError("a page of the cache must be contiguous [kv_heads, page_size, head_dim]")
-    return _dt(k_cache), k_cache.stride(0)
+    if stride[3] != 1 or stride[2] != shape[3] or stride[1] != shape[2] * shape[3]:
+        if not k_cache[:1].is_contiguous():     # (the stride of a single row says nothing)
+            raise ValueError("a page of the cache must be contiguous [kv_heads, page_size, head_dim]")
+    return _dt(k_cache), stride[0] if shape[0] > 1 else shape[1] * shape[2] * shape[3]
 
 
-def _token_stride(t, name):
+def _token_stride(t, shape, name):
     """Elements between tokens of t [T, heads, head_dim], whose tokens are contiguous."""
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def dspark_cache_plan(seq_len, n_new, owned, ring, ring_state, block_table, page_size, *, owned_out, ring_state_out,
@@ -512,13 +517,13 @@ def dspark_cache_plan(seq_len, n_new, owned, ring, ring_state, block_table, page
 def dspark_cache_append(k, v, slot_map, k_cache, v_cache, *, ws: Workspace = None, stream=None):
     """Write keys and values k, v [T, kv_heads, head_dim] (any token stride)
     to the slots slot_map [T] int32 of the caches; negative slots are skipped."""
-    T, H, D = k.shape
+    shape = T, H, D = k.shape
     t, page_stride = _cache_pair(k_cache, v_cache)
     pages, Hc, P, Dc = k_cache.shape
-    if v.shape != k.shape or (Hc, Dc) != (H, D) or k.dtype != k_cache.dtype or v.dtype != k.dtype:
+    if v.shape != shape or Hc != H or Dc != D or k.dtype is not k_cache.dtype or v.dtype is not k.dtype:
         raise ValueError("k and v must be [T, kv_heads, head_dim] of the cache's heads and dtype")
     _check("dspark_cache_append", _lib.dspark_cache_append(
-        k.data_ptr(), v.data_ptr(), t, _token_stride(k, "k"), _token_stride(v, "v"),
+        k.data_ptr(), v.data_ptr(), t, _token_stride(k, shape, "k"), _token_stride(v, shape, "v"),
         _typed(slot_map, torch.int32, (T,), "slot_map"), T, k_cache.data_ptr(), v_cache.data_ptr(), page_stride, pages, P,
         H, D, None if ws is None else ws.ptr(), _stream(stream)))
 
@@ -529,15 +534,15 @@ def dspark_cache_attention(q, k_cache, v_cache, block_table, kv_len, q_off, tile
     over the paged cache: out [N, q_heads, head_dim], lse [N, q_heads] fp32 or
     None.  scale defaults to head_dim ** -0.5; max_new bounds the new tokens
     of a request."""
-    N, Hq, D = q.shape
+    shape = N, Hq, D = q.shape
     t, page_stride = _cache_pair(k_cache, v_cache)
     pages, Hkv, P, Dc = k_cache.shape
     B, width = block_table.shape
-    if Dc != D or q.dtype != k_cache.dtype or out.dtype != q.dtype or out.shape != q.shape:
+    if Dc != D or q.dtype is not k_cache.dtype or out.dtype is not q.dtype or out.shape != shape:
         raise ValueError("q and out must be [N, q_heads, head_dim] of the cache's head_dim and dtype")
     i32 = torch.int32
     _check("dspark_cache_attention", _lib.dspark_cache_attention(
-        q.data_ptr(), _token_stride(q, "q"), k_cache.data_ptr(), v_cache.data_ptr(), t, page_stride, pages, P,
+        q.data_ptr(), _token_stride(q, shape, "q"), k_cache.data_ptr(), v_cache.data_ptr(), t, page_stride, pages, P,
         _typed(block_table, i32, None, "block_table"), width, _typed(kv_len, i32, (B,), "kv_len"),
         _typed(q_off, i32, (B + 1,), "q_off"), _typed(tile_off, i32, (B + 1,), "tile_off"), B, N, Hq, Hkv, D, max_new,
         D ** -0.5 if scale is None else scale, _p(out),

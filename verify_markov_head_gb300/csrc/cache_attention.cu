@@ -13,6 +13,7 @@
 //     m = max_c m_c,   l = sum_c l_c e^(m_c - m),   o = sum_c o_c e^(m_c - m) / l.
 #include "pdl.cuh"
 #include "serve.cuh"
+#include "sm100_ptx.cuh"
 
 namespace dspark {
 namespace {
@@ -64,23 +65,67 @@ __device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int cta
 }
 
 // --------------------------------------------------- on CUDA cores, any type
-// fp32 caches, and bf16 ones with a head size the tensor-core kernel does not
-// take.  128 threads; a tile of 64 keys and values in shared memory as fp32.
-// Scores: thread t takes position t % 64 and half of the rows.  Outputs: warp
-// w takes MR / 4 rows, lane the dimensions 4 lane .. 4 lane + 3 (and + 128).
-constexpr int kSimtThreads = 128;
+// fp32 caches, and bf16 ones with a head size or a page size that the
+// tensor-core kernel does not take.  fp32 arithmetic throughout, so the FMA
+// rate and the shared-memory reads that feed it bound a block's many rows, HBM
+// a single row.  256 threads, MR = 8 or 32 rows, TT positions at a time: two
+// stages of keys and values by cp.async, 16-byte chunks swizzled so that eight
+// positions' chunks lie in different banks.
+//   scores   8 rows x TPT positions a thread over a quarter of the head
+//            (lane = position group + 8 * quarter), the quarters summed by
+//            shuffles, which leave each thread NR rows of one position;
+//   weights  maxima by shuffles and an exchange over the warps, weights to
+//            shared memory [position][row];
+//   output   8 rows x ND dimensions a thread over 1 / TS of the
+//            positions; the TS parts are added at the segment's end.
+constexpr int kSimtThreads = 256;
 
-template <typename T, int MR>
-__global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnParams p) {
-    extern __shared__ __align__(16) float smem[];
-    const int D = p.D, ldk = D + 4;
-    float* sk = smem;                       // [64][D + 4]
-    float* sv = sk + kTile * ldk;           // [64][D]
-    float* sq = sv + kTile * D;             // [MR][D]
-    float* ss = sq + MR * D;                // [MR][64 + 4] scores, then weights
-    constexpr int lds = kTile + 4;
-    __shared__ float s_m[MR], s_l[MR], s_a[MR];
-    __shared__ long long s_base[kTile];
+template <typename T, int MR, int TT>
+struct Simt {
+    static constexpr int TPT = MR == 32 ? 4 : 1;            // positions of a thread
+    static constexpr int NR = MR == 32 ? 8 : 2;             // rows of a thread after the sum over the quarters
+    static constexpr int kRowGroups = MR / 8;
+    static constexpr int kTokWarps = TT / (8 * TPT);        // warps that share the positions of a row group
+    static constexpr int kScoreWarps = kRowGroups * kTokWarps;
+    static constexpr int TS = 8 / kRowGroups;
+    static constexpr int ND = TT == 64 ? 4 : 8;             // dimensions of a thread: 4 lane .., and 128 + 4 lane ..
+    static size_t bytes(int D) {
+        return (size_t)4 * TT * D * sizeof(T) + sizeof(float) * ((size_t)MR * D + TT * MR + (size_t)(TS - 1) * MR * D);
+    }
+};
+
+template <typename T> struct Chunk;      // 16 bytes of a head as fp32
+template <> struct Chunk<float> {
+    static constexpr int E = 4;
+    __device__ __forceinline__ static void get(const uint4& r, float (&x)[4]) {
+        x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+    }
+};
+template <> struct Chunk<uint16_t> {
+    static constexpr int E = 8;
+    __device__ __forceinline__ static void get(const uint4& r, float (&x)[8]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+template <typename T, int MR, int TT>
+__global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnParams p) {
+    using S = Simt<T, MR, TT>;
+    using C = Chunk<T>;
+    constexpr int E = C::E, TPT = S::TPT, NR = S::NR, ND = S::ND;
+    extern __shared__ __align__(16) uint8_t raw[];
+    const int D = p.D, chunks = D / E, tile_elems = TT * D;
+    T* ring = reinterpret_cast<T*>(raw);                     // [2 stages][keys, values][TT][D]
+    float* sq = reinterpret_cast<float*>(ring + 4 * tile_elems);   // [MR][D]
+    float* sp_ = sq + MR * D;                                // weights [TT][MR]
+    float* merge = sp_ + TT * MR;                            // [TS - 1][MR][D]
+    __shared__ float s_max[S::kTokWarps][MR], s_sum[S::kTokWarps][MR], s_alpha[MR], s_ref[MR];
+    __shared__ long long s_base[2][TT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) grid_launch_dependents();   // the join is scheduled now and waits for this grid
     const int cta = blockIdx.x;
@@ -90,7 +135,14 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnParam
     const T* kc = static_cast<const T*>(p.k);
     const T* vc = static_cast<const T*>(p.v);
     const float scale2 = p.scale * kLog2e;
-    constexpr int RW = MR / 4;              // rows of a warp
+    // scores: position group and quarter of the head
+    const int tg = lane & 7, quarter = lane >> 3, rg = warp / S::kTokWarps, tw = warp % S::kTokWarps;
+    const bool scores = warp < S::kScoreWarps;
+    const int tok0 = tw * 8 * TPT + tg * TPT;                // the thread's first position
+    const int my_tok = MR == 32 ? tok0 + quarter : tok0;     // the position it keeps
+    const int my_row = MR == 32 ? rg * 8 : 2 * quarter;      // and its first row
+    // output: row group, part of the positions, dimensions
+    const int org = warp / S::TS, part = warp % S::TS;
     const int end = sp.first(cta + 1);
     for (int t = sp.first(cta); t < end;) {
         const AttnSegment g = attn_segment(p, sp, t, attn_first_round(p));
@@ -100,146 +152,225 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const AttnParam
         const int j0 = g.tile(sp, t), j1 = g.tile(sp, end);
         t = g.t0 + sp.pad + g.tiles;             // the next segment
         if (j0 == j1) continue;
+        const int steps = (j1 - j0) * (kTile / TT), first_new = rm.len - rm.n;
+        // where position `tid` of a step lies, -1 beyond the end or in a bad page
+        auto base_of = [&](int s) {
+            const int pos = j0 * kTile + s * TT + tid;
+            if (pos >= rm.len) return -1LL;
+            const int pg = p.by_page(pos), page = p.table[(size_t)g.b * p.width + pg];
+            if (page < 0 || page >= p.pages) { raise_status(p.status, kBadPage); return -1LL; }
+            return page * p.page_stride + ((long long)g.h * p.page_size + (pos - pg * p.page_size)) * D;
+        };
+        // chunk c of position r (whole groups of 8 chunks are swizzled)
+        auto place = [&](int r, int c) { return r * chunks + ((c | 7) < chunks ? c ^ ((r / TPT) & 7) : c); };
+        auto issue = [&](int s) {
+            const int st = s & 1;
+            const uint32_t k0 = ptx::smem_addr(ring + 2 * st * tile_elems), v0 = k0 + tile_elems * (uint32_t)sizeof(T);
+            for (int i = tid; i < TT * chunks; i += kSimtThreads) {
+                const int r = i / chunks, c = i - r * chunks;
+                const long long base = s_base[st][r];
+                const long long o = base < 0 ? 0 : base + c * E;
+                const uint32_t at = (uint32_t)place(r, c) * 16u;
+                ptx::cp_async_16(k0 + at, kc + o, base < 0 ? 0u : 16u);
+                ptx::cp_async_16(v0 + at, vc + o, base < 0 ? 0u : 16u);
+            }
+            ptx::cp_async_commit();
+        };
         __syncthreads();
+        if (tid < TT) s_base[0][tid] = base_of(0);
         for (int i = tid; i < MR * D; i += kSimtThreads) {
             const int r = i / D, d = i - r * D;
             float x = 0.f;
             if (r < rows) {
-                const int rr = r0 + r, tok = rr / p.G;
+                const int rr = r0 + r, tok = p.by_group(rr);
                 x = to_f32(static_cast<const T*>(p.q)[(rm.q0 + tok) * p.q_stride + (size_t)(g.h * p.G + rr - tok * p.G) * D + d]);
             }
             sq[i] = x;
         }
-        if (tid < MR) { s_m[tid] = -INFINITY; s_l[tid] = 0.f; }
-        float acc[RW][8];
+        __syncthreads();
+        issue(0);
+        if (tid < TT && steps > 1) s_base[1][tid] = base_of(1);
+        float m[NR], l[NR], acc[8][ND];
 #pragma unroll
-        for (int r = 0; r < RW; ++r)
+        for (int r = 0; r < NR; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[r][e] = 0.f;
-        for (int j = j0; j < j1; ++j) {
-            const int pos0 = j * kTile;
-            __syncthreads();
-            if (tid < kTile) {
-                const int pos = pos0 + tid;
-                long long base = -1;
-                if (pos < rm.len) {
-                    const int pg = pos / p.page_size;
-                    const int page = p.table[(size_t)g.b * p.width + pg];
-                    if (page >= 0 && page < p.pages)
-                        base = page * p.page_stride + ((long long)g.h * p.page_size + (pos - pg * p.page_size)) * D;
-                    else raise_status(p.status, kBadPage);
-                }
-                s_base[tid] = base;
-            }
-            __syncthreads();
-            const int quads = D / 4;
-            for (int i = tid; i < kTile * quads; i += kSimtThreads) {
-                const int r = i / quads, c = i - r * quads;
-                const long long base = s_base[r];
-                float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
-                if (base >= 0) { k4 = Vec4<T>::load(kc + base + 4 * c); v4 = Vec4<T>::load(vc + base + 4 * c); }
-                *reinterpret_cast<float4*>(sk + r * ldk + 4 * c) = k4;
-                *reinterpret_cast<float4*>(sv + r * D + 4 * c) = v4;
-            }
-            __syncthreads();
-            {   // scores
-                const int tk = tid & (kTile - 1), half = tid / kTile;
-                constexpr int RH = MR / 2;
-                float s[RH];
+        for (int r = 0; r < 8; ++r)
 #pragma unroll
-                for (int r = 0; r < RH; ++r) s[r] = 0.f;
-                for (int c = 0; c < D; c += 4) {
-                    const float4 k4 = *reinterpret_cast<const float4*>(sk + tk * ldk + c);
+            for (int e = 0; e < ND; ++e) acc[r][e] = 0.f;
+        for (int s = 0; s < steps; ++s) {
+            const int st = s & 1, pos0 = j0 * kTile + s * TT;
+            ptx::cp_async_wait_group<0>();
+            __syncthreads();                     // the step's tiles are there, the other stage is free
+            if (s + 1 < steps) issue(s + 1);
+            const long long later = tid < TT && s + 2 < steps ? base_of(s + 2) : -1LL;
+            const uint4* kt = reinterpret_cast<const uint4*>(ring + 2 * st * tile_elems);
+            float z[NR];
+            if (scores) {
+                float a[8][TPT];
 #pragma unroll
-                    for (int r = 0; r < RH; ++r) {
-                        const float4 q4 = *reinterpret_cast<const float4*>(sq + (half * RH + r) * D + c);
-                        s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int i = 0; i < TPT; ++i) a[r][i] = 0.f;
+                for (int c = quarter; c < chunks; c += 4) {
+                    float k[TPT][E];
+#pragma unroll
+                    for (int i = 0; i < TPT; ++i) C::get(kt[place(tok0 + i, c)], k[i]);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float4* q4 = reinterpret_cast<const float4*>(sq + (rg * 8 + r) * D + c * E);
+#pragma unroll
+                        for (int h = 0; h < E / 4; ++h) {
+                            const float4 q = q4[h];
+#pragma unroll
+                            for (int i = 0; i < TPT; ++i)
+                                a[r][i] = fmaf(q.x, k[i][4 * h], fmaf(q.y, k[i][4 * h + 1],
+                                          fmaf(q.z, k[i][4 * h + 2], fmaf(q.w, k[i][4 * h + 3], a[r][i]))));
+                        }
                     }
                 }
-                const bool there = s_base[tk] >= 0;
+                // the sum over the quarters, split on the way
+                const bool up2 = quarter & 2, up1 = quarter & 1;
+                if constexpr (MR == 32) {
+                    float b2[8][2];
 #pragma unroll
-                for (int r = 0; r < RH; ++r) {
-                    const int rr = r0 + half * RH + r;
-                    const int last = rm.len - rm.n + rr / p.G;     // the row's own position
-                    ss[(half * RH + r) * lds + tk] = (there && pos0 + tk <= last) ? s[r] * scale2 : -INFINITY;
+                    for (int r = 0; r < 8; ++r)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            b2[r][i] = (up2 ? a[r][i + 2] : a[r][i]) + __shfl_xor_sync(~0u, up2 ? a[r][i] : a[r][i + 2], 16);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        z[r] = (up1 ? b2[r][1] : b2[r][0]) + __shfl_xor_sync(~0u, up1 ? b2[r][0] : b2[r][1], 8);
+                } else {
+                    float b4[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        b4[r] = (up2 ? a[r + 4][0] : a[r][0]) + __shfl_xor_sync(~0u, up2 ? a[r][0] : a[r + 4][0], 16);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        z[r] = (up1 ? b4[r + 2] : b4[r]) + __shfl_xor_sync(~0u, up1 ? b4[r] : b4[r + 2], 8);
+                }
+                const bool there = s_base[st][my_tok] >= 0;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int last = first_new + p.by_group(r0 + my_row + r);     // the row's own position
+                    z[r] = there && pos0 + my_tok <= last ? z[r] * scale2 : -INFINITY;
+                }
+                // maxima over the warp's positions
+                float w[NR];
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    w[r] = z[r];
+#pragma unroll
+                    for (int o = 1; o < (MR == 32 ? 32 : 8); o <<= 1) w[r] = fmaxf(w[r], __shfl_xor_sync(~0u, w[r], o));
+                    if ((MR == 32 ? lane : tg) == 0) s_max[tw][my_row + r] = w[r];
                 }
             }
             __syncthreads();
-            for (int r = warp; r < MR; r += 4) {   // running maximum and sum, base 2
-                const float a = ss[r * lds + lane], b = ss[r * lds + 32 + lane];
-                float m = fmaxf(a, b);
+            if (tid < TT && s + 2 < steps) s_base[st][tid] = later;
+            if (scores) {
 #pragma unroll
-                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-                const float old = s_m[r];
-                m = fmaxf(m, old);
-                const float ref = m == -INFINITY ? 0.f : m;
-                const float pa = fast_exp2(a - ref), pb = fast_exp2(b - ref);
-                ss[r * lds + lane] = pa;
-                ss[r * lds + 32 + lane] = pb;
-                float sum = pa + pb;
+                for (int r = 0; r < NR; ++r) {
+                    float to = m[r];
 #pragma unroll
-                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-                if (lane == 0) {
-                    const float al = fast_exp2(old - ref);
-                    s_a[r] = al;
-                    s_l[r] = s_l[r] * al + sum;
-                    s_m[r] = m;
+                    for (int w = 0; w < S::kTokWarps; ++w) to = fmaxf(to, s_max[w][my_row + r]);
+                    const float ref = to == -INFINITY ? 0.f : to, al = fast_exp2(m[r] - ref), x = fast_exp2(z[r] - ref);
+                    m[r] = to;
+                    l[r] = fmaf(l[r], al, x);
+                    sp_[my_tok * MR + my_row + r] = x;
+                    if (tw == 0 && (MR == 32 ? lane : tg) == 0) s_alpha[my_row + r] = al;
                 }
             }
             __syncthreads();
-            float al[RW];
+            const T* vt = ring + (2 * st + 1) * tile_elems;
+            // a hidden position adds nothing, whatever its value holds
+            const bool guard = pos0 + TT > first_new + 1;
 #pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                al[r] = s_a[warp * RW + r];
+            for (int r = 0; r < 8; ++r) {
+                const float al = s_alpha[org * 8 + r];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[r][e] *= al[r];
+                for (int e = 0; e < ND; ++e) acc[r][e] *= al;
             }
-            const bool d0 = 4 * lane < D, d1 = 4 * lane + 128 < D;
-            for (int tk = 0; tk < kTile; ++tk) {
-                float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-                if (d0) v0 = *reinterpret_cast<const float4*>(sv + tk * D + 4 * lane);
-                if (d1) v1 = *reinterpret_cast<const float4*>(sv + tk * D + 4 * lane + 128);
+            constexpr int kPart = TT / S::TS;
+#pragma unroll 4
+            for (int i = 0; i < kPart; ++i) {
+                const int tk = part * kPart + i;
+                float w[8], v[ND];
+                *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(sp_ + tk * MR + org * 8);
+                *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(sp_ + tk * MR + org * 8 + 4);
 #pragma unroll
-                for (int r = 0; r < RW; ++r) {
-                    const float w = ss[(warp * RW + r) * lds + tk];
-                    if (w != 0.f) {     // a hidden position adds nothing, whatever its value holds
-                        acc[r][0] = fmaf(w, v0.x, acc[r][0]); acc[r][1] = fmaf(w, v0.y, acc[r][1]);
-                        acc[r][2] = fmaf(w, v0.z, acc[r][2]); acc[r][3] = fmaf(w, v0.w, acc[r][3]);
-                        acc[r][4] = fmaf(w, v1.x, acc[r][4]); acc[r][5] = fmaf(w, v1.y, acc[r][5]);
-                        acc[r][6] = fmaf(w, v1.z, acc[r][6]); acc[r][7] = fmaf(w, v1.w, acc[r][7]);
-                    }
+                for (int hf = 0; hf < ND / 4; ++hf) {
+                    const int d = 4 * lane + 128 * hf;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (d < D) y = Vec4<T>::load(vt + place(tk, d / E) * E + d % E);
+                    v[4 * hf] = y.x; v[4 * hf + 1] = y.y; v[4 * hf + 2] = y.z; v[4 * hf + 3] = y.w;
+                }
+                if (guard) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (w[r] != 0.f)
+#pragma unroll
+                            for (int e = 0; e < ND; ++e) acc[r][e] = fmaf(w[r], v[e], acc[r][e]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+#pragma unroll
+                        for (int e = 0; e < ND; ++e) acc[r][e] = fmaf(w[r], v[e], acc[r][e]);
                 }
             }
         }
+        // the segment's end: sums over the threads, parts of the output together
+        if (scores) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float x = l[r];
+#pragma unroll
+                for (int o = 1; o < (MR == 32 ? 32 : 8); o <<= 1) x += __shfl_xor_sync(~0u, x, o);
+                if ((MR == 32 ? lane : tg) == 0) {
+                    s_sum[tw][my_row + r] = x;
+                    if (tw == 0) s_ref[my_row + r] = m[r];
+                }
+            }
+        }
+        if (part > 0) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int e = 0; e < ND; ++e) {
+                    const int d = 4 * lane + 128 * (e / 4) + e % 4;
+                    if (d < D) merge[((part - 1) * MR + org * 8 + r) * D + d] = acc[r][e];
+                }
+        }
         __syncthreads();
+        if (part > 0) continue;
         const bool whole = j0 == 0 && j1 == g.tiles;
         const int slot = 2 * cta + (j0 == 0 ? 1 : 0);
 #pragma unroll
-        for (int r = 0; r < RW; ++r) {
-            const int row = warp * RW + r;
+        for (int r = 0; r < 8; ++r) {
+            const int row = org * 8 + r;
             if (row >= rows) continue;
-            const float l = s_l[row], inv = l != 0.f ? 1.f / l : 0.f;
-            const int rr = r0 + row, tok = rr / p.G, head = g.h * p.G + rr - tok * p.G;
+            float sum = 0.f;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int d = 4 * lane + 128 * hf;
+            for (int w = 0; w < S::kTokWarps; ++w) sum += s_sum[w][row];
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;
+            const int rr = r0 + row, tok = p.by_group(rr), head = g.h * p.G + rr - tok * p.G;
+            const size_t at = (size_t)(rm.q0 + tok) * p.Hq + head;
+#pragma unroll
+            for (int e = 0; e < ND; ++e) {
+                const int d = 4 * lane + 128 * (e / 4) + e % 4;
                 if (d >= D) continue;
-                if (whole) {
-                    T* o = static_cast<T*>(p.out) + ((size_t)(rm.q0 + tok) * p.Hq + head) * D + d;
+                float x = acc[r][e];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) store_out(o + e, acc[r][4 * hf + e] * inv);
-                } else {
-                    float* o = p.part + ((size_t)slot * p.row_tile + row) * D + d;
-                    *reinterpret_cast<float4*>(o) = make_float4(acc[r][4 * hf], acc[r][4 * hf + 1], acc[r][4 * hf + 2], acc[r][4 * hf + 3]);
-                }
+                for (int w = 0; w < S::TS - 1; ++w) x += merge[(w * MR + row) * D + d];
+                if (whole) store_out(static_cast<T*>(p.out) + at * D + d, x * inv);
+                else p.part[((size_t)slot * p.row_tile + row) * D + d] = x;
             }
             if (lane == 0) {
                 if (whole) {
-                    if (p.lse) p.lse[(size_t)(rm.q0 + tok) * p.Hq + head] = l != 0.f ? s_m[row] * kLn2 + logf(l) : -INFINITY;
+                    if (p.lse) p.lse[at] = sum != 0.f ? s_ref[row] * kLn2 + logf(sum) : -INFINITY;
                 } else {
-                    float* st = part_stats(p) + ((size_t)slot * p.row_tile + row) * 2;
-                    st[0] = s_m[row];
-                    st[1] = l;
+                    float* stats = part_stats(p) + ((size_t)slot * p.row_tile + row) * 2;
+                    stats[0] = s_ref[row];
+                    stats[1] = sum;
                 }
             }
         }
@@ -324,13 +455,18 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     if (lane == 0 && p.lse) p.lse[o0] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
+template <typename T, int MR, int TT>
+cudaError_t launch_simt_tile(const AttnParams& p, cudaStream_t s) {
+    const size_t smem = Simt<T, MR, TT>::bytes(p.D);
+    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, MR, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    attn_simt_kernel<T, MR, TT><<<p.ctas, kSimtThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
 template <typename T, int MR>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
-    const size_t smem = sizeof(float) * ((size_t)kTile * (2 * p.D + 4) + (size_t)MR * p.D + (size_t)MR * (kTile + 4));
-    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    attn_simt_kernel<T, MR><<<p.ctas, kSimtThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    // 64 positions at a time as far as shared memory holds two stages of them
+    return p.D <= 128 ? launch_simt_tile<T, MR, 64>(p, s) : launch_simt_tile<T, MR, 32>(p, s);
 }
 
 template <typename T>

@@ -18,7 +18,7 @@ enum ServeStatusBits : uint32_t {
 };
 
 constexpr int kTile = DSPARK_CACHE_TILE;   // cache positions per attention tile
-constexpr int kMaxAttnCtas = 320;          // CTAs of an attention launch (bounds its partial results)
+constexpr int kMaxAttnCtas = 160;          // CTAs of an attention launch (bounds its partial results)
 constexpr int kMaxRowTile = 64;            // query rows of one key-value head an attention CTA takes at once
 
 // ---------------------------------------------------------------- cache plan

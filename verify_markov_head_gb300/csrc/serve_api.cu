@@ -132,9 +132,11 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     const int rows = p.G * max_new;
     const bool mma = attn_mma_supported(p);
     p.row_tile = attn_row_tile(rows, mma);
+    // on CUDA cores, fewer rows at a time where SMs would be idle otherwise
+    const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
+    if (!mma && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
-    const int ctas = (mma ? 1 : 2) * num_sms();      // resident CTAs: one or two per SM
-    p.ctas = ctas < kMaxAttnCtas ? ctas : kMaxAttnCtas;
+    p.ctas = num_sms() < kMaxAttnCtas ? num_sms() : kMaxAttnCtas;      // one resident CTA per SM
     p.pad = mma ? (head_dim == 64 ? 6 : 3) : 1;
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead);
     p.status = static_cast<uint32_t*>(ws);
