@@ -206,22 +206,43 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
 
 // ----------------------------------------------------------------- append
 // cache[slot] = row: a copy, bound by HBM for prompts and by latency for a
-// block.  One thread moves 16 bytes of a key and of the value beside it.
-__global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams p) {
+// block.  A thread keeps one 16-byte place of a token's row (its head and
+// place follow once) and moves it for kAppend tokens at a time, keys and
+// values: the loads do not wait for the slots.
+constexpr int kAppendThreads = 256, kAppend = 2;
+
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p, int group) {
+    // `group` threads to a token, several tokens to a block
     const int vecs = p.row_bytes / 16, per = p.heads * vecs;
-    const long long total = (long long)p.T * per;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
-        const int t = (int)(i / per), e = (int)(i - (long long)t * per);
-        const int slot = p.slot_map[t];
-        if (slot < 0) continue;
-        const int page = slot / p.page_size, row = slot - page * p.page_size;
-        if (page >= p.pages) { raise_status(p.status, kBadPage); continue; }
-        const int h = e / vecs, c = e - h * vecs;
-        const uint4 k = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_stride) + e);
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_stride) + e);
-        const long long o = page * p.page_bytes + ((long long)h * p.page_size + row) * p.row_bytes + 16 * c;
-        *reinterpret_cast<uint4*>(p.k_cache + o) = k;
-        *reinterpret_cast<uint4*>(p.v_cache + o) = v;
+    const int side = kAppendThreads / group, lt = threadIdx.x / group, e0 = threadIdx.x - lt * group;
+    if (lt >= side) return;
+    for (int e = e0; e < per; e += group) {
+        const int h = e / vecs;
+        const long long in_page = (long long)h * p.page_size * p.row_bytes + 16 * (e - h * vecs);
+        const long long step = (long long)gridDim.x * side;
+        for (long long t0 = (long long)blockIdx.x * side + lt; t0 < p.T; t0 += step * kAppend) {
+            int slot[kAppend];
+            uint4 k[kAppend], v[kAppend];
+#pragma unroll
+            for (int u = 0; u < kAppend; ++u) {
+                const long long t = t0 + u * step;
+                slot[u] = -1;
+                if (t < p.T) {
+                    slot[u] = __ldg(p.slot_map + t);
+                    k[u] = __ldcs(reinterpret_cast<const uint4*>(p.k + t * p.k_stride) + e);
+                    v[u] = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.v_stride) + e);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAppend; ++u) {
+                if (slot[u] < 0) continue;
+                const int page = slot[u] / p.page_size, row = slot[u] - page * p.page_size;
+                if (page >= p.pages) { raise_status(p.status, kBadPage); continue; }
+                const long long o = page * p.page_bytes + in_page + (long long)row * p.row_bytes;
+                *reinterpret_cast<uint4*>(p.k_cache + o) = k[u];
+                *reinterpret_cast<uint4*>(p.v_cache + o) = v[u];
+            }
+        }
     }
 }
 
@@ -240,10 +261,15 @@ cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
 
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t s) {
     if (p.T == 0) return cudaSuccess;
-    const long long total = (long long)p.T * p.heads * (p.row_bytes / 16);
-    long long grid = (total + 255) / 256;
-    if (grid > 8LL * num_sms()) grid = 8LL * num_sms();
-    cache_append_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
+    const int per = p.heads * (p.row_bytes / 16), group = per < kAppendThreads ? per : kAppendThreads;
+    const int side = kAppendThreads / group;
+    // one pass of the tokens, kAppend to a thread, over as many blocks as there are
+    // (up to 64 per SM: 42.0 us for 32768 tokens of 4 KB, 43.9 with 8)
+    const long long blocks = ((long long)p.T + side - 1) / side;
+    long long grid = (blocks + kAppend - 1) / kAppend;
+    if (grid < num_sms()) grid = blocks < num_sms() ? blocks : num_sms();
+    if (grid > 64LL * num_sms()) grid = 64LL * num_sms();
+    cache_append_kernel<<<(unsigned)grid, kAppendThreads, 0, s>>>(p, group);
     return cudaGetLastError();
 }
 
