@@ -82,9 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
     bool bad = false;
     bool state_ok = head >= 0 && head < p.pages && avail >= 0 && avail <= p.pages;
     if (!state_ok) { head = 0; avail = 0; }
-    if (tid == 0) s_popped = 0;
 
-    // pass 1: the pages asked for decide who can be served
     const int per = (B + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     auto block_scan = [&](Sum4 v) {     // exclusive over the threads
@@ -112,31 +110,44 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
         return Sum4{x.tok - v.tok + o.tok, x.need - v.need + o.need, x.give - v.give + o.give,
                     x.tiles - v.tiles + o.tiles};
     };
+    // a thread's requests; up to 1024 of them stay in registers
+    PlanItem one{};
+    if (b0 < b1) one = plan_item(p, b0);
+    auto item = [&](int b) { return b == b0 ? one : plan_item(p, b); };
+    auto give_of = [](const PlanItem& it) { return max(0, it.owned - it.goal); };
+    auto tiles_of = [](const PlanItem& it) { return (it.seq + it.fresh + kTile - 1) / kTile; };
+    // sums as if every request could be served (usually so)
     Sum4 mine{0, 0, 0, 0};
     for (int b = b0; b < b1; ++b) {
-        const PlanItem it = plan_item(p, b);
-        mine = mine + Sum4{it.fresh, it.need, 0, 0};
+        const PlanItem it = item(b);
+        mine = mine + Sum4{it.fresh, it.need, it.ok ? give_of(it) : 0, it.ok ? tiles_of(it) : 0};
     }
     Sum4 at = block_scan(mine);
-    // pass 2: requests are served in order while the ring has pages for them
-    Sum4 second{0, 0, 0, 0};
-    {
+    if (tid == kPlanThreads - 1) s_popped = add_sat(at.need, mine.need);
+    __syncthreads();
+    Sum4 at2 = at;
+    if (s_popped > avail) {
+        // requests are served in order while the ring has pages for them
+        __syncthreads();
+        if (tid == 0) s_popped = 0;
+        __syncthreads();
+        Sum4 second{0, 0, 0, 0};
         int need = at.need;
         for (int b = b0; b < b1; ++b) {
-            const PlanItem it = plan_item(p, b);
+            const PlanItem it = item(b);
             const bool served = it.ok && (it.need == 0 || need + it.need <= avail);
             need = add_sat(need, it.need);
             if (served) {
-                second = second + Sum4{0, 0, max(0, it.owned - it.goal), (it.seq + it.fresh + kTile - 1) / kTile};
+                second = second + Sum4{0, 0, give_of(it), tiles_of(it)};
                 if (it.need) atomicAdd(&s_popped, it.need);     // an integer sum: any order gives the same
             }
         }
+        at2 = block_scan(second);
     }
-    const Sum4 at2 = block_scan(second);
     {
         int tok = at.tok, need = at.need, give = at2.give, tiles = at2.tiles;
         for (int b = b0; b < b1; ++b) {
-            const PlanItem it = plan_item(p, b);
+            const PlanItem it = item(b);
             const bool served = it.ok && (it.need == 0 || need + it.need <= avail);
             bad |= !served;
             s_q[b] = tok; s_need[b] = need; s_give[b] = give;
@@ -149,8 +160,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
             tok = add_sat(tok, it.fresh);
             need = add_sat(need, it.need);
             if (served) {
-                give = add_sat(give, max(0, it.owned - it.goal));
-                tiles = add_sat(tiles, (it.seq + it.fresh + kTile - 1) / kTile);
+                give = add_sat(give, give_of(it));
+                tiles = add_sat(tiles, tiles_of(it));
             }
             if (b == B - 1) {
                 s_q[B] = tok; s_need[B] = need; s_give[B] = give;
