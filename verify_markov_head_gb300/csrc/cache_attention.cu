@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
     const int cta = blockIdx.x;
     empty_rows<T>(p, cta, gridDim.x);
     const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
+    if (tid == 0) p.split[cta].parts = 0;
     if (cta >= sp.n) return;
     const T* kc = static_cast<const T*>(p.k);
     const T* vc = static_cast<const T*>(p.v);
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
         if (part > 0) continue;
         const bool whole = j0 == 0 && j1 == g.tiles;
         const int slot = 2 * cta + (j0 == 0 ? 1 : 0);
+        if (tid == 0 && j0 == 0 && !whole) p.split[cta] = attn_split_row(sp, g, cta, rm.q0, r0, rows);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const int row = org * 8 + r;
@@ -378,28 +380,21 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
 }
 
 // ------------------------------------------------------------------- join
-// Block (c, y): the segment that CTA c continues from CTA c - 1, if it began
-// there; one warp per row of rows 8 y .. 8 y + 7.  The partial results are
-// added in CTA order, so the result does not depend on which CTA ended first.
+// Block (c, y): the segment that begins in CTA c and ends in another; one warp
+// per row of rows 8 y .. 8 y + 7.  The partial results are added in CTA order,
+// so the result does not depend on which CTA ended first.  Latency bounds it:
+// three dependent loads (what CTA c left, the parts' maxima and sums, the parts
+// eight at a time).
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     grid_dependency_wait();
-    const int mine = attn_first_round(p);
-    const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
-    const int c = blockIdx.x + 1;
-    if (c >= sp.n) return;
-    const int t = sp.first(c);
-    const AttnSegment g = attn_segment(p, sp, t, mine);
-    const int t1 = g.t0 + sp.pad;                // the place of its first tile
-    if (g.tiles == 0 || t1 >= t || sp.cta_of(t1) != c - 1) return;
-    const int last = sp.cta_of(t1 + g.tiles - 1);
-    const RowMap rm(p, g.b);
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int rr = g.rt * p.row_tile + row;
-    if (row >= p.row_tile || rr >= rm.n * p.G) return;
+    const int c = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int4 w0 = __ldcg(reinterpret_cast<const int4*>(p.split + c));
+    const int parts = w0.x, rows = __ldcg(&p.split[c].rows);
+    if (row >= rows || parts < 2) return;
+    const int rr = w0.w + row;
     const float2* stats = reinterpret_cast<const float2*>(part_stats(p));
-    auto place = [&](int i) { return (size_t)(i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * p.row_tile + row; };
-    const int parts = last - c + 2;
+    auto place = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.row_tile + row; };
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, stats[place(i)].x);
 #pragma unroll
@@ -443,8 +438,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
         }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int tok = rr / p.G, head = g.h * p.G + rr - tok * p.G;
-    const size_t o0 = (size_t)(rm.q0 + tok) * p.Hq + head;
+    const int tok = p.by_group(rr), head = w0.z * p.G + rr - tok * p.G;
+    const size_t o0 = (size_t)(w0.y + tok) * p.Hq + head;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         const int d = 4 * lane + 128 * hf;
@@ -471,8 +466,7 @@ cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
-    if (p.ctas < 2) return cudaSuccess;
-    return launch_dependent(attn_join_kernel<T>, dim3(p.ctas - 1, (p.row_tile + 7) / 8), dim3(256), 0, s, p);
+    return launch_dependent(attn_join_kernel<T>, dim3(p.ctas, (p.row_tile + 7) / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace

@@ -214,6 +214,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         bool ok = true;
         int t = 0, end = 0;
         AttnSegment g{};
+        AttnSplitRow split{};                    // the segment that begins here and goes on in the next CTA
         if (cta < sp.n) {
             t = sp.first(cta);
             end = sp.first(cta + 1);
@@ -246,8 +247,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             volatile Seg& d = s_seg[slot];
             int n0 = 0, nrows = 0, nr0 = 0;
             if (more) {
-                const int len_in = p.kv_len[g.b], qa = p.q_off[g.b], qe = p.q_off[g.b + 1];
+                // four loads on their way together: the page of this lane's box as if
+                // the request were as long as its tiles say
+                const int j0 = g.tile(sp, t), j1 = g.tile(sp, end), pos_in = j0 * kTile + lane * bx;
                 const int cap = p.width * p.page_size;
+                const int len_in = p.kv_len[g.b], qa = p.q_off[g.b], qe = p.q_off[g.b + 1];
+                const int page_in = lane < nbox && pos_in < cap ? __ldg(p.table + (size_t)g.b * p.width + p.by_page(pos_in)) : -1;
                 int n = qe - qa, len = len_in;
                 n0 = qa;
                 if (n > p.max_new || n < 0 || qa < 0 || qa > p.N - n || len < 0 || len > cap) {
@@ -257,12 +262,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 }
                 nr0 = g.rt * p.row_tile;
                 nrows = max(0, min(p.row_tile, n * p.G - nr0));
-                const int j0 = g.tile(sp, t), j1 = g.tile(sp, end);
                 const int pos0 = min(j0 * kTile, len), pos1 = min(j1 * kTile, len);
-                if (lane < nbox) {
-                    const int pos = pos0 + lane * bx;
-                    d.page[lane] = pos < pos1 ? __ldg(p.table + (size_t)g.b * p.width + p.by_page(pos)) : -1;
-                }
+                if (lane < nbox) d.page[lane] = pos_in < pos1 ? page_in : -1;
+                if (j0 == 0 && j1 < g.tiles) split = attn_split_row(sp, g, cta, qa, nr0, nrows);
                 if (lane == 0) {
                     d.b = g.b; d.h = g.h; d.q0 = qa; d.n = n; d.len = len; d.r0 = nr0; d.rows = nrows;
                     d.pos0 = pos0; d.pos1 = pos1;
@@ -304,6 +306,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             t = g.t0 + sp.pad + g.tile(sp, end);     // the place behind the tiles just taken
             skip();
         }
+        if (lane == 0) p.split[cta] = split;
     } else if (warp == kKeyWarp || warp == kValWarp) {
         // ------------------------------------------------------------ producers
         const int kv = warp == kValWarp;

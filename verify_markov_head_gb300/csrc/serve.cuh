@@ -57,6 +57,13 @@ struct FastDiv {
     __device__ __forceinline__ int operator()(int x) const { return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift); }
 };
 
+// What a CTA leaves for the join of a segment that begins in it.
+struct __align__(16) AttnSplitRow {
+    int parts;           // CTAs that hold a part of it, 0: no such segment
+    int q0, h, r0;       // first token in q, key-value head, first query row
+    int rows, pad[3];
+};
+
 struct AttnParams {
     const void* q; long long q_stride;                 // elements between tokens
     const void* k; const void* v; long long page_stride;   // elements between pages
@@ -70,6 +77,7 @@ struct AttnParams {
     int row_tile, row_tiles;    // query rows of a key-value head per tile of rows, and such tiles
     int ctas;                   // CTAs the work is split over
     int pad;                    // what a segment costs beside its tiles, in tiles (at least 1)
+    AttnSplitRow* split;        // [ctas] the segment that begins in each CTA and ends in another
     float* part;                // [2 ctas][row_tile][D] sums, then [2 ctas][row_tile][2] (max, sum)
     uint32_t* status;
 };
@@ -123,6 +131,11 @@ struct AttnSegment {
     // the tile at place t, or the first one after it
     __device__ __forceinline__ int tile(const AttnSplit& sp, int t) const { return min(max(0, t - t0 - sp.pad), tiles); }
 };
+
+// What CTA c leaves of a segment that begins in it and goes on in the next.
+__device__ __forceinline__ AttnSplitRow attn_split_row(const AttnSplit& sp, const AttnSegment& g, int c, int q0, int r0, int rows) {
+    return AttnSplitRow{sp.cta_of(g.t0 + sp.pad + g.tiles - 1) - c + 1, q0, g.h, r0, rows, {0, 0, 0}};
+}
 
 // Place of request b's first segment, in units of `heads` places.
 __device__ __forceinline__ int attn_request_at(const AttnParams& p, int b) { return p.tile_off[b] + p.pad * b; }

@@ -95,7 +95,7 @@ static bool attn_sizes_ok(int B, int q_heads, int kv_heads, int head_dim, int ma
 size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new) {
     if (!attn_sizes_ok(B, q_heads, kv_heads, head_dim, max_new)) return 0;
     const size_t rows = attn_row_tile(q_heads / kv_heads * max_new, true);   // the larger of the two kernels' tiles
-    return kHead + ws_align256((size_t)2 * kMaxAttnCtas * rows * (head_dim + 2) * sizeof(float));
+    return kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas) + ws_align256((size_t)2 * kMaxAttnCtas * rows * (head_dim + 2) * sizeof(float));
 }
 
 dspark_status dspark_cache_attention(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -138,7 +138,8 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
     p.ctas = num_sms() < kMaxAttnCtas ? num_sms() : kMaxAttnCtas;      // one resident CTA per SM
     p.pad = mma ? (head_dim == 64 ? 6 : 3) : 1;
-    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead);
+    p.split = reinterpret_cast<AttnSplitRow*>(static_cast<char*>(ws) + kHead);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas));
     p.status = static_cast<uint32_t*>(ws);
     return launch_status(launch_cache_attention(p, static_cast<cudaStream_t>(stream)));
 }
