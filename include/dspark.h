@@ -503,7 +503,7 @@ dspark_status dspark_cache_attention(
  *     x'    = x / rep if x > 0, x * rep otherwise, where v is in the history
  *             (prompt included) or among those drafts; x elsewhere
  *     y     = x' - freq * c(v) - pres * [c(v) > 0] + bias(v)
- *     out   = y where bit v % 32 of mask[b][i][v / 32] is set, else -inf.
+ *     out   = y where bit v % 32 of mask[b][i][v / 32] is set, else fill.
  * Inputs : logits [B][R][V] (t), row_stride elements between rows (B * R rows
  *          at one stride); hist [B][hist_stride] with hist_len [B] tokens, the
  *          first prompt_len[b] (NULL: none) the prompt; draft_tok
@@ -511,10 +511,15 @@ dspark_status dspark_cache_attention(
  *          bias_off[b] .. bias_off[b+1] of bias_tok (strictly ascending ids in
  *          each request) and bias_val, bias_n in all; mask
  *          [B][R][ceil(V/32)].  hist, draft_tok, rep (1), freq (0), pres (0),
- *          bias_off and mask (everything allowed) may be NULL.
+ *          bias_off and mask (everything allowed) may be NULL.  fill is -inf
+ *          for target rows; for U give a finite one such as -1e4: the draft's
+ *          running sums take finite scores (the draw itself never picks one
+ *          that low, and a drafted token that the target rows mask is rejected
+ *          in any case).
  * Outputs: out [B][R][V] (t; may be logits itself where row_stride = V);
- *          live [B][R] (or NULL): the entries of the row above -inf.  A row
- *          with none sets status bit 4: no token can be drawn from it.
+ *          live [B][R] (or NULL): the row's entries that the mask leaves and
+ *          that are above -inf.  A row with none sets status bit 4: no token
+ *          can be drawn from it.
  * Checks : a token id out of [0, V) is skipped and sets bit 0 (as do bias ids
  *          out of order), a length or offset out of range bit 1, rep not
  *          positive and finite bit 3.
@@ -529,7 +534,7 @@ dspark_status dspark_logits_process(
     const int32_t* draft_tok, int draft_stride,
     const float* rep, const float* freq, const float* pres,
     const int32_t* bias_tok, const float* bias_val, const int32_t* bias_off, int bias_n,
-    const uint32_t* mask, int32_t* live, void* ws, size_t ws_bytes, void* stream);
+    const uint32_t* mask, float fill, int32_t* live, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Diagnostics: the random stream as the kernels draw it.  For columns

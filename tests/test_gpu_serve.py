@@ -483,6 +483,81 @@ def test_logits_report_rows_with_nothing_left_and_bad_inputs(vm):
     assert _status(vm, ws) == BAD_LENGTH
 
 
+def test_logits_with_a_finite_fill(vm):
+    """The rows of a draft take a finite value under the mask; the entries left
+    and the rows with nothing left are counted as with -inf."""
+    rng = np.random.default_rng(24)
+    for dtype in (torch.float32, torch.bfloat16):
+        a = _logit_inputs(rng, 3, 4, 1024, dtype, 50)
+        a["mask"][2, 1] = False
+        low, live, ws = _process(vm, a)
+        assert _status(vm, ws) == DEAD_ROW
+        got, live2, _ = _process(vm, a, ws=ws, fill=-1e4)
+        assert _status(vm, ws) == DEAD_ROW
+        assert torch.equal(live, live2)
+        fill = torch.tensor(-1e4, dtype=dtype, device="cuda")
+        assert torch.equal(got, torch.where(torch.as_tensor(a["mask"]).cuda(), low, fill))
+
+
+# ------------------------------------------- the operators around the step
+@pytest.mark.parametrize("B,V,r,wdt,mode", [(4, 1024, 32, torch.float32, 0), (5, 4104, 64, torch.bfloat16, 0),
+                                            (1, 4104, 64, torch.bfloat16, 0), (70, 8200, 128, torch.bfloat16, 1)])
+def test_a_constrained_step_matches_the_oracle(vm, B, V, r, wdt, mode):
+    """A grammar that leaves 0.2 % of the vocabulary, on the draft's rows and the
+    target's: the whole step draws what the oracle draws from the same rows, and
+    every emitted token is allowed where it stands."""
+    import oracle
+    import workload
+
+    w = workload.custom("tiny", B=B, V=V, r=r, w_dtype=wdt, seed=3, mode=mode)
+    inp = workload.inputs(w, device="cuda")
+    G = w.gamma
+    rng = np.random.default_rng(7)
+    allowed = rng.random((B, 1, V)) < 0.002          # the same law in every row of a request
+    allowed[:, :, 7] = True
+    words = _words(np.repeat(allowed, G + 1, 1))
+    ws = vm.LogitsWorkspace(B, G + 1)
+    vm.dspark_logits_process(inp["target"], inp["target"], ws, mask=words)
+    vm.dspark_logits_process(inp["U"], inp["U"], vm.LogitsWorkspace(B, G), mask=words[:, :G].contiguous(), fill=-1e4)
+    buf = vm.StepBuffers(B, G, V, r)
+    vm.run_step(inp, buf, mode=mode, seed=5)
+    assert vm.dspark_sync_status(buf.ws.buf) == (0, 0) and _status(vm, ws) == 0
+    want = oracle.step({k: (v.cpu() if torch.is_tensor(v) else v) for k, v in inp.items()}, mode=mode, seed=5)
+    np.testing.assert_array_equal(buf.draft_tok.cpu().numpy(), want["draft"]["tok"])
+    n = int(buf.out_off[-1])
+    tok, req = buf.out_tok[:n].cpu().numpy(), buf.out_req[:n].cpu().numpy()
+    np.testing.assert_array_equal(tok, want["out"]["out_tok"])
+    assert allowed[req, 0, tok].all()
+
+
+# ------------------------------------------------------------ expired waits
+def test_expired_waits_are_reported_and_the_workspace_recovers(vm):
+    """With a wait bound of 300 cycles the attention and the logit controls give
+    up, report a timeout and return; after dspark_workspace_init the same calls
+    give the results of a fresh workspace.  Every wait on the path is bounded."""
+    rng = np.random.default_rng(15)
+    a = _attention_inputs(rng, [3000, 700], [8, 8], 32, 8, 128, 16, torch.bfloat16)
+    out, lse, ws = _attend(vm, a, 8)
+    vm.dspark_workspace_set_wait_limit(ws.buf, 300)
+    _attend(vm, a, 8, ws=ws)
+    st, bits = vm.dspark_sync_status(ws.buf)
+    assert st == -3 and bits & 4
+    vm.dspark_workspace_init(ws.buf)
+    again, lse2, _ = _attend(vm, a, 8, ws=ws)
+    assert _status(vm, ws) == 0 and torch.equal(again, out) and torch.equal(lse, lse2)
+    # 17 rows: more than the ring holds, so the producer waits for the warps that
+    # are still reading the history
+    b = _logit_inputs(rng, 4, 17, 32008, torch.float32, 5000)
+    want, live, lw = _process(vm, b)
+    vm.dspark_workspace_set_wait_limit(lw.buf, 300)
+    _process(vm, b, ws=lw)
+    st, bits = vm.dspark_sync_status(lw.buf)
+    assert st == -3 and bits & 4
+    vm.dspark_workspace_init(lw.buf)
+    got, live2, _ = _process(vm, b, ws=lw)
+    assert _status(vm, lw) == 0 and torch.equal(got, want) and torch.equal(live, live2)
+
+
 # ---------------------------------------------------------------- refusals
 def test_the_binding_refuses_wrong_shapes_types_and_strides(vm):
     rng = np.random.default_rng(31)

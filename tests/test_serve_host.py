@@ -63,11 +63,13 @@ def test_attention_refuses_bad_arguments(host):
 
 
 def test_logits_refuse_bad_arguments(host):
-    def call(p, t=0, rs=64, B=2, R=3, V=64, hist=None, hist_len=None, draft=None, ds=0, nb=1 << 20):
+    def call(p, t=0, rs=64, B=2, R=3, V=64, hist=None, hist_len=None, draft=None, ds=0, nb=1 << 20,
+             fill=float("-inf")):
         return vm._lib.dspark_logits_process(p, t, rs, p, B, R, V, hist, 4, hist_len, None, draft, ds, None, None, None,
-                                             None, None, None, 0, None, None, p, nb, None)
+                                             None, None, None, 0, None, fill, None, p, nb, None)
 
     assert call(None) == -1 and call(host) == -1
     assert call(host, t=3) == -4
-    for kw in (dict(V=60), dict(V=0), dict(rs=63), dict(R=18), dict(R=0), dict(B=0), dict(B=70000), dict(nb=0)):
+    for kw in (dict(V=60), dict(V=0), dict(rs=63), dict(R=18), dict(R=0), dict(B=0), dict(B=70000), dict(nb=0),
+               dict(fill=float("nan"))):
         assert call(host, **kw) == -1, kw

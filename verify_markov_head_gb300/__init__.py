@@ -99,7 +99,7 @@ _lib.dspark_cache_attention.restype = _i
 _lib.dspark_logits_workspace_bytes.argtypes = [_i, _i]
 _lib.dspark_logits_workspace_bytes.restype = _sz
 _lib.dspark_logits_process.argtypes = [_vp, _i, _ll, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp,
-                                       _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]
+                                       _vp, _vp, _i, _vp, _f, _vp, _vp, _sz, _vp]
 _lib.dspark_logits_process.restype = _i
 
 
@@ -551,13 +551,14 @@ def dspark_cache_attention(q, k_cache, v_cache, block_table, kv_len, q_off, tile
 
 def dspark_logits_process(logits, out, ws: Workspace, *, hist=None, hist_len=None, prompt_len=None, draft_tok=None,
                           rep=None, freq=None, pres=None, bias_tok=None, bias_val=None, bias_off=None, mask=None,
-                          live=None, stream=None):
+                          fill=float("-inf"), live=None, stream=None):
     """Penalties, biases and grammar masks on logits [B, R, V] (rows at one
     stride), written to out [B, R, V] (may be logits itself).  hist [B, L]
     int32 with hist_len (and prompt_len) [B]; draft_tok [B, >= R-1]: the
     drafts before each row; rep, freq, pres [B] fp32; bias_tok, bias_val,
     bias_off [B+1]: ascending ids per request; mask [B, R, ceil(V/32)] int32
-    words; live [B, R] int32 receives the entries left in each row."""
+    words, whose clear bits become fill (for the rows of U a finite value such
+    as -1e4); live [B, R] int32 receives the entries left in each row."""
     B, R, V = logits.shape
     f32, i32, b = torch.float32, torch.int32, (B,)
     if out.shape != logits.shape or out.dtype != logits.dtype:
@@ -585,7 +586,7 @@ def dspark_logits_process(logits, out, ws: Workspace, *, hist=None, hist_len=Non
         opt(rep, f32, b, "rep"), opt(freq, f32, b, "freq"), opt(pres, f32, b, "pres"),
         None if bias_off is None else _typed(bias_tok, i32, None, "bias_tok"),
         None if bias_off is None else _typed(bias_val, f32, None, "bias_val"), opt(bias_off, i32, (B + 1,), "bias_off"),
-        n_bias, opt(mask, i32, (B, R, -(-V // 32)), "mask"), opt(live, i32, (B, R), "live"), ws.ptr(), ws.nbytes(),
+        n_bias, opt(mask, i32, (B, R, -(-V // 32)), "mask"), fill, opt(live, i32, (B, R), "live"), ws.ptr(), ws.nbytes(),
         _stream(stream)))
 
 

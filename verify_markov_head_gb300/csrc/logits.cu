@@ -7,7 +7,7 @@
 //     seen_i(v) = v in the prompt, or c_i(v) > 0,
 //     x' = seen ? (x > 0 ? x / rep : x * rep) : x,
 //     y  = x' - freq * c_i(v) - pres * [c_i(v) > 0] + bias(v),
-//     out = allowed_i(v) ? y : -inf.
+//     out = allowed_i(v) ? y : fill              (fill = -inf unless the caller names another).
 // With these rows as the target, the verification stays lossless for the
 // constrained distribution: row i is the law after exactly those i drafts.
 #include "serve.cuh"
@@ -24,11 +24,10 @@ constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30, kDraft = 1u << 29, kCou
 template <typename T> struct Row;
 template <> struct Row<float> {
     static constexpr int kVec = 4;
-    static constexpr uint32_t kLow = 0xff800000u;     // -inf
     __device__ __forceinline__ static float round(float x) { return x; }
-    // r with -inf where a bit is clear
-    __device__ __forceinline__ static uint4 masked(const uint4& r, uint32_t bits) {
-        return make_uint4(bits & 1u ? r.x : kLow, bits & 2u ? r.y : kLow, bits & 4u ? r.z : kLow, bits & 8u ? r.w : kLow);
+    // r with `low` where a bit is clear
+    __device__ __forceinline__ static uint4 masked(const uint4& r, uint32_t bits, uint32_t low) {
+        return make_uint4(bits & 1u ? r.x : low, bits & 2u ? r.y : low, bits & 4u ? r.z : low, bits & 8u ? r.w : low);
     }
     // entries above -inf among those whose bit is set: all of them where the
     // least entry is (NaN carries through the minimum)
@@ -45,10 +44,9 @@ template <> struct Row<float> {
 };
 template <> struct Row<uint16_t> {
     static constexpr int kVec = 8;
-    static constexpr uint32_t kLow = 0xff80ff80u;     // -inf, twice
-    // r with -inf where a bit is clear.  (4 bits) * 0x10204080 has them in the
+    // r with `low` (twice in the word) where a bit is clear.  (4 bits) * 0x10204080 has them in the
     // tops of the four bytes; the byte permutation spreads a top over a half word.
-    __device__ __forceinline__ static uint4 masked(const uint4& r, uint32_t bits) {
+    __device__ __forceinline__ static uint4 masked(const uint4& r, uint32_t bits, uint32_t low) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
         uint32_t o[4];
 #pragma unroll
@@ -57,7 +55,7 @@ template <> struct Row<uint16_t> {
             const uint32_t tops = (i < 2 ? bits & 15u : bits >> 4) * 0x10204080u;
             if (i & 1) asm("prmt.b32 %0, %1, 0, 0xbbaa;" : "=r"(keep) : "r"(tops));
             else asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(keep) : "r"(tops));
-            o[i] = (w[i] & keep) | (kLow & ~keep);
+            o[i] = (w[i] & keep) | (low & ~keep);
         }
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -322,7 +320,7 @@ __global__ void __launch_bounds__(kThreads + 32, Ring<T>::kCtas) logits_kernel(c
             for (int j = 0; j < kPer; ++j) {
                 bits[j] = (uint32_t)kAll;
                 if (kMask) bits[j] &= s_mask[s * L::kMaskWords + (tid * kVec) / 32 + j * (kThreads * kVec / 32)] >> shift;
-                raw[j] = make_uint4(Row<T>::kLow, Row<T>::kLow, Row<T>::kLow, Row<T>::kLow);
+                raw[j] = make_uint4(p.low, p.low, p.low, p.low);
                 if (read && tid + j * kThreads < vecs) raw[j] = reinterpret_cast<const uint4*>(slice)[tid + j * kThreads];
             }
             __syncwarp();
@@ -331,7 +329,7 @@ __global__ void __launch_bounds__(kThreads + 32, Ring<T>::kCtas) logits_kernel(c
             for (int j = 0; j < kPer; ++j) {
                 if (tid + j * kThreads >= vecs) continue;
                 live += Row<T>::live(raw[j], bits[j]);
-                if (kMask && bits[j] != (uint32_t)kAll) raw[j] = Row<T>::masked(raw[j], bits[j]);
+                if (kMask && bits[j] != (uint32_t)kAll) raw[j] = Row<T>::masked(raw[j], bits[j], p.low);
                 out[j * kThreads] = raw[j];
             }
             live = __reduce_add_sync(~0u, live);

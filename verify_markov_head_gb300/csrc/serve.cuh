@@ -189,6 +189,7 @@ struct LogitsParams {
     const float* rep; const float* freq; const float* pres;
     const int32_t* bias_tok; const float* bias_val; const int32_t* bias_off; int bias_n;
     const uint32_t* mask;
+    uint32_t low;                 // what a masked entry becomes: an fp32 word, or a bf16 one twice
     int32_t* live;
     uint32_t* status;
     unsigned long long* counts;   // [B][R] arrivals and entries left, zero between launches

@@ -2,6 +2,7 @@
 // host-side argument checks, workspace layout and launches.
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
+#include <string.h>
 
 #include "serve.cuh"
 
@@ -154,7 +155,7 @@ dspark_status dspark_logits_process(const void* logits, dspark_dtype t, long lon
                                     const int32_t* prompt_len, const int32_t* draft_tok, int draft_stride,
                                     const float* rep, const float* freq, const float* pres, const int32_t* bias_tok,
                                     const float* bias_val, const int32_t* bias_off, int bias_n, const uint32_t* mask,
-                                    int32_t* live, void* ws, size_t ws_bytes, void* stream) {
+                                    float fill, int32_t* live, void* ws, size_t ws_bytes, void* stream) {
     const CallRange range_(__func__);
     if (!dtype_ok(t)) return DSPARK_ERR_UNSUPPORTED;
     const size_t need = dspark_logits_workspace_bytes(B, R);
@@ -167,6 +168,7 @@ dspark_status dspark_logits_process(const void* logits, dspark_dtype t, long lon
     if (draft_tok && (!dev(draft_tok) || draft_stride < R - 1)) return DSPARK_ERR_INVALID;
     if (!dev_or_null(rep) || !dev_or_null(freq) || !dev_or_null(pres) || !dev_or_null(mask) || !dev_or_null(live))
         return DSPARK_ERR_INVALID;
+    if (fill != fill) return DSPARK_ERR_INVALID;
     if (bias_off && (bias_n < 0 || !dev(bias_off))) return DSPARK_ERR_INVALID;
     if (bias_off && bias_n > 0 && (!dev(bias_tok) || !dev(bias_val))) return DSPARK_ERR_INVALID;
     LogitsParams p;
@@ -178,6 +180,13 @@ dspark_status dspark_logits_process(const void* logits, dspark_dtype t, long lon
     p.bias_tok = bias_off && bias_n > 0 ? bias_tok : nullptr;
     p.bias_val = bias_val; p.bias_off = bias_off; p.bias_n = bias_n;
     p.mask = mask; p.live = live;
+    uint32_t word;
+    memcpy(&word, &fill, sizeof(word));
+    if (p.bf16) {                                  // nearest even
+        word = (word + 0x7fffu + (word >> 16 & 1u)) >> 16;
+        word |= word << 16;
+    }
+    p.low = word;
     char* base = static_cast<char*>(ws);
     p.status = reinterpret_cast<uint32_t*>(base);
     p.counts = reinterpret_cast<unsigned long long*>(base + kHead);
