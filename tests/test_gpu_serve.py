@@ -203,6 +203,8 @@ ATTENTION = [
     ([90, 130], [3, 8], 4, 2, 256, 64),
     ([45, 100], [8, 1], 8, 1, 8, 16),
     ([4100], [8], 8, 2, 64, 64),                               # split over many CTAs
+    ([130, 20], [8, 3], 96, 1, 64, 16),                        # 96 heads to a key head
+    ([2000, 70, 900], [0, 1, 0], 8, 4, 128, 32),               # requests that wait
 ]
 
 

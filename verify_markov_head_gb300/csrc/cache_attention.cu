@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
         const int rows = max(0, min(p.row_tile, rm.n * p.G - r0));
         const int j0 = g.tile(sp, t), j1 = g.tile(sp, end);
         t = g.t0 + sp.pad + g.tiles;             // the next segment
-        if (j0 == j1) continue;
+        if (j0 == j1 || rows == 0) continue;
         const int steps = (j1 - j0) * (kTile / TT), first_new = rm.len - rm.n;
         // where position `tid` of a step lies, -1 beyond the end or in a bad page
         auto base_of = [&](int s) {

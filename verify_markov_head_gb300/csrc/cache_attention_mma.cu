@@ -263,6 +263,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 nr0 = g.rt * p.row_tile;
                 nrows = max(0, min(p.row_tile, n * p.G - nr0));
                 const int pos0 = min(j0 * kTile, len), pos1 = min(j1 * kTile, len);
+                if (nrows == 0) {                    // no row of the request here: nothing to publish
+                    t = g.t0 + sp.pad + j1;
+                    skip();
+                    --si;
+                    continue;
+                }
                 if (lane < nbox) d.page[lane] = pos_in < pos1 ? page_in : -1;
                 if (j0 == 0 && j1 < g.tiles) split = attn_split_row(sp, g, cta, qa, nr0, nrows);
                 if (lane == 0) {

@@ -90,7 +90,8 @@ template <> struct Row<uint16_t> {
 //
 // Every logit is read once and written once, so HBM bounds the large calls.  A
 // producer thread copies the rows' slices into a ring in shared memory (bulk
-// copies, kStages ahead; a slice that the mask empties is not read), so the
+// copies, kStages ahead; a slice that the mask empties is not read, and of one
+// that keeps little only the 16-byte vectors with an allowed entry), so the
 // reads go on while the other warps prepare: what a row needs of the history
 // is found once per CTA for all its rows, a word in shared memory per
 // vocabulary entry with the output count and flags (prompt, bias, in the
@@ -104,6 +105,11 @@ template <typename T> struct Ring;
 template <> struct Ring<float> { static constexpr int kStages = 3, kCtas = 3; };       // 16 KB slices
 template <> struct Ring<uint16_t> { static constexpr int kStages = 2, kCtas = 5; };    // 8 KB slices
 constexpr long long kDrainCycles = 200000000LL;
+
+// Arrive on an mbarrier once this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 template <typename T, int kPer>
 struct Smem {
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(kThreads + 32, Ring<T>::kCtas) logits_kernel(c
     volatile uint32_t* abort_flag = &s_abort;
     const long long wl = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { ptx::mbar_init(full(i), 1); ptx::mbar_init(empty(i), kThreads / 32); }
+        for (int i = 0; i < kStages; ++i) { ptx::mbar_init(full(i), 33); ptx::mbar_init(empty(i), kThreads / 32); }
         s_abort = 0u;
         s_listed = 0;
         ptx::fence_mbar_init();
@@ -155,7 +161,13 @@ __global__ void __launch_bounds__(kThreads + 32, Ring<T>::kCtas) logits_kernel(c
         const uint32_t* mask = kMask ? p.mask + ((size_t)b * p.R + row0) * words + lo / 32 : nullptr;
         // mask words of a slice, kLane a lane, two rows ahead
         constexpr int kLane = L::kMaskWords / 32, kAhead = 2;
-        const int mine = (n + 31) / 32;
+        const int mine = (n + 31) / 32, vecs = n / kVec;
+        auto groups_of = [](uint32_t w) {            // vectors of a mask word with an allowed entry
+            uint32_t x = w | w >> 1;
+            x |= x >> 2;
+            if (kVec == 8) x |= x >> 4;
+            return __popc(x & (kVec == 8 ? 0x01010101u : 0x11111111u));
+        };
         uint32_t ahead[kAhead][kLane];
         auto fetch = [&](int i, uint32_t (&w)[kLane]) {
 #pragma unroll
@@ -174,23 +186,41 @@ __global__ void __launch_bounds__(kThreads + 32, Ring<T>::kCtas) logits_kernel(c
                 if (i >= rows || !ok) break;
                 if (i >= kStages) ok = __all_sync(~0u, ptx::mbar_wait_strict(empty(s), (i / kStages - 1) & 1, abort_flag, wl));
                 if (!ok) break;
-                bool read = true;
+                // how the slice is read: 0 not at all, 1 the vectors that keep an entry, 2 whole
+                int how = 2;
+                const T* row = in + i * p.row_stride;
                 if (kMask) {
-                    uint32_t any = 0u;
+                    int groups = 0;              // vectors with an allowed entry
 #pragma unroll
                     for (int k = 0; k < kLane; ++k) {
-                        any |= ahead[r][k];
+                        groups += groups_of(ahead[r][k]);
                         s_mask[s * L::kMaskWords + lane + 32 * k] = ahead[r][k];
                     }
-                    read = __any_sync(~0u, any != 0u);
+                    groups = __reduce_add_sync(~0u, groups);
+                    how = groups == 0 ? 0 : groups <= vecs / 4 ? 1 : 2;
+                    if (how == 1)
+#pragma unroll
+                        for (int k = 0; k < kLane; ++k)
+#pragma unroll
+                            for (int g = 0; g < 32 / kVec; ++g)
+                                if (ahead[r][k] >> (g * kVec) & (uint32_t)kAll) {
+                                    const int c = (lane + 32 * k) * (32 / kVec) + g;
+                                    if (c < vecs) ptx::cp_async_16(ring + s * L::kSlice + 16 * c, row + c * kVec, 16u);
+                                }
                     fetch(i + kAhead, ahead[r]);
                     __syncwarp();
                 }
+                // each lane arrives once, or its copies do, and lane 0 once more
+                // behind the words that the warp wrote
+                if (how == 1) cp_async_arrive(full(s));
+                else ptx::mbar_arrive(full(s));
                 if (lane == 0) {
-                    s_skip[s] = !read;
-                    if (read) {
+                    s_skip[s] = how == 0;
+                    if (how == 2) {
+                        // (the stage may have been written by copies of the other kind)
+                        if (kMask) ptx::fence_proxy_async_smem();
                         ptx::mbar_arrive_expect_tx(full(s), bytes);
-                        ptx::bulk_load(ring + s * L::kSlice, in + i * p.row_stride, bytes, full(s), pol);
+                        ptx::bulk_load(ring + s * L::kSlice, row, bytes, full(s), pol);
                     } else ptx::mbar_arrive(full(s));
                 }
                 filled = i + 1;
