@@ -16,8 +16,6 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;
-
 // The word a vocabulary entry has in shared memory; 0 = nothing to do but the mask.
 constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30, kDraft = 1u << 29, kCount = kDraft - 1;
 
@@ -111,7 +109,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <typename T, int kPer>
+template <typename T, int kPer, int kThreads>
 struct Smem {
     static constexpr int kRange = kPer * kThreads * Row<T>::kVec;
     static constexpr int kStages = kPer == 1 ? 4 : Ring<T>::kStages;
@@ -124,9 +122,9 @@ struct Smem {
     static constexpr int kTotal = kBar + 16 * kStages;
 };
 
-template <typename T, bool kMask, int kPer>
-__global__ void __launch_bounds__(kThreads + 32, Ring<T>::kCtas) logits_kernel(const LogitsParams p, const int part) {
-    using L = Smem<T, kPer>;
+template <typename T, bool kMask, int kPer, int kThreads>
+__global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? Ring<T>::kCtas : 2) logits_kernel(const LogitsParams p, const int part) {
+    using L = Smem<T, kPer, kThreads>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_listed;
     __shared__ int s_live[DSPARK_MAX_GAMMA + 1];
@@ -382,29 +380,35 @@ __global__ void __launch_bounds__(kThreads + 32, Ring<T>::kCtas) logits_kernel(c
     }
 }
 
-template <typename T, bool kMask, int kPer>
+template <typename T, bool kMask, int kPer, int kThreads>
 cudaError_t launch(const LogitsParams& p, cudaStream_t s) {
-    using L = Smem<T, kPer>;
-    const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kMask, kPer>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+    using L = Smem<T, kPer, kThreads>;
+    const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kMask, kPer, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
     if (e != cudaSuccess) return e;
     // few CTAs: the rows of a request split over several, which saves the rows' turn
     const int ranges = (p.V + L::kRange - 1) / L::kRange;
     int parts = 1;
     while (2 * parts <= p.R && 2LL * parts * ranges * p.B <= 3LL * num_sms()) parts *= 2;
     const int part = (p.R + parts - 1) / parts;
-    logits_kernel<T, kMask, kPer><<<dim3(ranges, p.B, (p.R + part - 1) / part), kThreads + 32, L::kTotal, s>>>(p, part);
+    logits_kernel<T, kMask, kPer, kThreads><<<dim3(ranges, p.B, (p.R + part - 1) / part), kThreads + 32, L::kTotal, s>>>(p, part);
     return cudaGetLastError();
 }
 
-// Entries of a CTA: 4096, or down to 1024 (bf16 2048) where that leaves SMs idle.
+// Entries of a CTA: 4096 (8192: b64 146 us, not 100; 512 threads: 108), or 2048
+// where that leaves SMs idle, and then, where it still does, 512 threads, which
+// read a history in half the turns (one request: 8.2 us, 10.4 with 256 threads).
 template <typename T, bool kMask>
 cudaError_t launch_range(const LogitsParams& p, cudaStream_t s) {
-    constexpr int kUnit = kThreads * Row<T>::kVec;
-    int per = 4096 / kUnit;
-    while (per > 1 && (long long)p.B * ((p.V + per * kUnit - 1) / (per * kUnit)) < 2LL * num_sms()) per >>= 1;
-    if constexpr (4 * kUnit <= 4096)
-        if (per == 4) return launch<T, kMask, 4>(p, s);
-    return per == 2 ? launch<T, kMask, 2>(p, s) : launch<T, kMask, 1>(p, s);
+    constexpr int kUnit = 256 * Row<T>::kVec;
+    auto fills = [&](int range) { return (long long)p.B * ((p.V + range - 1) / range) >= 2LL * num_sms(); };
+    if constexpr (kUnit == 1024) {
+        if (fills(4096)) return launch<T, kMask, 4, 256>(p, s);
+        if (fills(2048)) return launch<T, kMask, 2, 256>(p, s);
+    } else {
+        if (fills(4096)) return launch<T, kMask, 2, 256>(p, s);
+        if (fills(2048)) return launch<T, kMask, 1, 256>(p, s);
+    }
+    return launch<T, kMask, 1, 512>(p, s);
 }
 
 }  // namespace
