@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
 // eight at a time).
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
+    if (threadIdx.x == 0) grid_launch_dependents();
     grid_dependency_wait();
     const int c = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int4 w0 = __ldcg(reinterpret_cast<const int4*>(p.split + c));

@@ -199,6 +199,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_flags[0];
+    grid_dependency_wait();             // the set-up above overlaps the launch before this one
     const long long wl = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
     auto wait = [&](uint32_t b, uint32_t parity) { return ptx::mbar_wait_strict(b, parity & 1u, abort_flag, wl); };
     auto give_up = [&](int site) {
@@ -727,8 +728,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     static_assert(Smem<N, D>::kTotal + 1024 <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attn_mma_kernel<N, D><<<p.ctas, kWarps * 32, smem, s>>>(p, maps[0], maps[1], bx, page_heads);
-    return cudaGetLastError();
+    return launch_dependent(attn_mma_kernel<N, D>, dim3(p.ctas), dim3(kWarps * 32), smem, s, p, maps[0], maps[1], bx, page_heads);
 }
 
 }  // namespace
