@@ -1,6 +1,7 @@
 // cache.cu -- the paged key-value cache beside the verification: the plan of
 // a step (which pages each request owns, where its new tokens go) and the
 // append of new keys and values.
+#include "pdl.cuh"
 #include "serve.cuh"
 
 namespace dspark {
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
     __shared__ int s_popped;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = p.B;
+    grid_dependency_wait();
     int head = p.ring_state[0], avail = p.ring_state[1];
     bool bad = false;
     bool state_ok = head >= 0 && head < p.pages && avail >= 0 && avail <= p.pages;
@@ -224,6 +226,7 @@ constexpr int kAppendThreads = 256, kAppend = 2;
 
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p, int group) {
     // `group` threads to a token, several tokens to a block
+    grid_dependency_wait();
     const int vecs = p.row_bytes / 16, per = p.heads * vecs;
     const int side = kAppendThreads / group, lt = threadIdx.x / group, e0 = threadIdx.x - lt * group;
     if (lt >= side) return;
@@ -266,8 +269,7 @@ cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
     const int items = p.T > p.B ? p.T : p.B;
     int grid = (items + kPlanThreads - 1) / kPlanThreads;
     if (grid > num_sms()) grid = num_sms();
-    cache_plan_kernel<<<grid, kPlanThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(cache_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, s, p);
 }
 
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t s) {
@@ -280,8 +282,7 @@ cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t s) {
     long long grid = (blocks + kAppend - 1) / kAppend;
     if (grid < num_sms()) grid = blocks < num_sms() ? blocks : num_sms();
     if (grid > 64LL * num_sms()) grid = 64LL * num_sms();
-    cache_append_kernel<<<(unsigned)grid, kAppendThreads, 0, s>>>(p, group);
-    return cudaGetLastError();
+    return launch_dependent(cache_append_kernel, dim3((unsigned)grid), dim3(kAppendThreads), 0, s, p, group);
 }
 
 }  // namespace dspark

@@ -10,6 +10,7 @@
 //     out = allowed_i(v) ? y : fill              (fill = -inf unless the caller names another).
 // With these rows as the target, the verification stays lossless for the
 // constrained distribution: row i is the law after exactly those i drafts.
+#include "pdl.cuh"
 #include "serve.cuh"
 #include "sm100_ptx.cuh"
 
@@ -142,7 +143,6 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? Ring<T>::kCta
     auto full = [&](int s) { return bar + 8u * s; };
     auto empty = [&](int s) { return bar + 8u * (kStages + s); };
     volatile uint32_t* abort_flag = &s_abort;
-    const long long wl = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) { ptx::mbar_init(full(i), 33); ptx::mbar_init(empty(i), kThreads / 32); }
         s_abort = 0u;
@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? Ring<T>::kCta
         ptx::fence_mbar_init();
     }
     __syncthreads();
+    grid_dependency_wait();
+    const long long wl = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
 
     if (tid >= kThreads) {
         // ------------------------------------------------------------ producer
@@ -390,8 +392,8 @@ cudaError_t launch(const LogitsParams& p, cudaStream_t s) {
     int parts = 1;
     while (2 * parts <= p.R && 2LL * parts * ranges * p.B <= 3LL * num_sms()) parts *= 2;
     const int part = (p.R + parts - 1) / parts;
-    logits_kernel<T, kMask, kPer, kThreads><<<dim3(ranges, p.B, (p.R + part - 1) / part), kThreads + 32, L::kTotal, s>>>(p, part);
-    return cudaGetLastError();
+    return launch_dependent(logits_kernel<T, kMask, kPer, kThreads>, dim3(ranges, p.B, (p.R + part - 1) / part), dim3(kThreads + 32),
+                            (size_t)L::kTotal, s, p, part);
 }
 
 // Entries of a CTA: 4096 (8192: b64 146 us, not 100; 512 threads: 108), or 2048
