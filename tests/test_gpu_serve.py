@@ -418,6 +418,16 @@ def test_logits_without_some_controls(vm, drop):
     _check_logits(a, out, live, **{k: None for k in drop})
 
 
+def test_logits_with_an_empty_history(vm):
+    rng = np.random.default_rng(20)
+    a = _logit_inputs(rng, 2, 3, 1024, torch.float32, 10)
+    want, live, _ = _process(vm, a, hist=None, hist_len=None, prompt_len=None)
+    z = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for hist in (torch.empty((2, 0), dtype=torch.int32, device="cuda"), _cu(a["hist"])):
+        got, live2, _ = _process(vm, a, hist=hist, hist_len=z, prompt_len=z)
+        assert torch.equal(got, want) and torch.equal(live, live2)
+
+
 def test_logits_in_place_and_strided_rows(vm):
     rng = np.random.default_rng(21)
     a = _logit_inputs(rng, 4, 5, 1032, torch.bfloat16, 60)

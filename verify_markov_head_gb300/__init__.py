@@ -572,6 +572,8 @@ def dspark_logits_process(logits, out, ws: Workspace, *, hist=None, hist_len=Non
         raise ValueError("draft_tok must be [B, R-1] or wider")
     if (hist is None) != (hist_len is None):
         raise ValueError("hist and hist_len go together")
+    if hist is not None and hist.shape[1] == 0:      # no history yet
+        hist = hist_len = prompt_len = None
     n_bias = 0
     if bias_off is not None:
         n_bias = bias_tok.numel()

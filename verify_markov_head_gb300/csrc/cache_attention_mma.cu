@@ -26,6 +26,21 @@
 // half, and only then are the column maxima found (a warp reduction and an
 // exchange over the 4 warps), and the sums and O^T in tensor memory rescaled.
 //
+// What bounds it: HBM.  A key-value head's position is 512 bytes (head size
+// 128) and 4 N multiply-adds per byte pair; at 6.8 TB/s an SM has 2800 cycles
+// for a step of 128 positions, of which the tensor core is busy 1024 (it reads
+// the 128 x 16 operand at 64 bytes a cycle, whatever N is) and a softmax warp
+// 600-1600 (N = 16-64).  So the work is to keep copies in flight: two producer
+// warps (one issued a tile in 1200 cycles with pages of 16 positions, too slow),
+// segment ends off the way (the rows are written behind the next segment's
+// first step), the split over CTAs weighted by segments (AttnSplit).
+// Measured on one GB300: 64 requests of 1024-8192 positions, 32 rows, 1.22 GB:
+// 184 us (6.6 TB/s); 256 requests of 128-4096, 8 rows, 2.22 GB: 321 us (6.9
+// TB/s); one of 131072, 64 rows, 0.54 GB: 92 us (5.8 TB/s, 6 us of it before
+// the ring is full and the join).  Taking the column maxima in every step cost
+// 263 us for the first, one producer warp and serial segment ends 203, MMAs
+// issued from a diverged lane 203, an unweighted split 197.
+//
 // Weights are rounded to bf16 for the second product (relative 2^-8 of each
 // weight, independent in sign); their sum l is taken in fp32 before rounding.
 #include <cudaTypedefs.h>

@@ -97,9 +97,14 @@ template <> struct Row<uint16_t> {
 // drafted block), from a scan of the request's history.  The entries with a
 // word, few beside the vocabulary, are listed; in each row they are corrected
 // in the ring, before the row leaves with the mask applied.
-// (Measured on the way, 64 requests, 556 MB: rows through registers with the
-// formula inlined in the stream 283 us, with the listed entries corrected in
-// the output afterwards 119-125 us.)
+// Measured on one GB300: 64 requests of 8 fp32 rows of 151936, a quarter of
+// them under a tight mask, 556 MB: 100 us (5.5 TB/s); 256 requests of 8 bf16
+// rows of 129280, half of them under a loose mask, 1067 MB: 187 us (5.7 TB/s; a
+// plain copy of these rows takes 156); one request 8.0 us.  On the way, the
+// first of them: rows through registers with the formula inlined in the stream
+// 283 us, with the listed entries corrected in the output afterwards 119, with
+// mask words read by every thread (the first-level cache is small beside this
+// much shared memory) 116, whole slices read under tight masks 106.
 template <typename T> struct Ring;
 template <> struct Ring<float> { static constexpr int kStages = 3, kCtas = 3; };       // 16 KB slices
 template <> struct Ring<uint16_t> { static constexpr int kStages = 2, kCtas = 5; };    // 8 KB slices
