@@ -76,14 +76,15 @@ struct Smem {
     static constexpr int kGroup = 8 * D * 2;                      // 8 positions: [half of the head][position][64 entries]
     static constexpr int kStages = 5 * 128 / D;
     static constexpr int kQBytes = N * D * 2;
+    static constexpr int kQBufs = N * D <= 32 * 128 ? 4 : 2;      // Q tiles: segments may be a step long
     static constexpr int kRing = 0;
     static constexpr int kQ = kRing + kStages * kTileBytes;
-    static constexpr int kP = kQ + 2 * kQBytes;                   // [128][64] bf16, 128-byte rows
+    static constexpr int kP = kQ + kQBufs * kQBytes;                   // [128][64] bf16, 128-byte rows
     static constexpr int kMax = kP + kSteps * 128;                // [N][4]
     static constexpr int kSum = kMax + N * 16;                    // [N][4]
     static constexpr int kSeg = kSum + N * 16;
     static constexpr int kBar = kSeg + kSegs * (int)sizeof(Seg);
-    static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 + 2 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 3;
     static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, non-finite flag, -, the producers' counts, bad boxes
     static constexpr int kTotal = kFlags + 24 + 4 * kBadRing;
 };
@@ -101,6 +102,11 @@ __device__ __forceinline__ float warp_max(float x) {     // over the warp, NaN l
     float y;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Arrive on an mbarrier once this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Nonzero in one lane of the (converged) warp.
@@ -187,7 +193,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
     const uint32_t b_full = take(kStages), b_empty = take(kStages);
     const uint32_t b_seg_full = take(kSegs), b_seg_empty = take(kSegs);
-    const uint32_t b_q_full = take(2), b_q_empty = take(2), b_s_full = take(2), b_s_empty = take(2);
+    const uint32_t b_q_full = take(L::kQBufs), b_q_empty = take(L::kQBufs), b_s_full = take(2), b_s_empty = take(2);
     const uint32_t b_o_empty = take(2), b_p_full = take(1), b_pv = take(1), b_end = take(1);
 
     if (tid == 0) {
@@ -195,10 +201,10 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         for (int i = 0; i < kStages; ++i) { ptx::mbar_init(b_full + 8 * i, 1); ptx::mbar_init(b_empty + 8 * i, 1); }
         for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 3 + kSoftWarps); }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(b_q_full + 8 * i, 1); ptx::mbar_init(b_q_empty + 8 * i, 1);
             ptx::mbar_init(b_s_full + 8 * i, 1); ptx::mbar_init(b_s_empty + 8 * i, kSoftWarps);
             ptx::mbar_init(b_o_empty + 8 * i, kSoftWarps);
         }
+        for (int i = 0; i < L::kQBufs; ++i) { ptx::mbar_init(b_q_full + 8 * i, 32); ptx::mbar_init(b_q_empty + 8 * i, 1); }
         ptx::mbar_init(b_p_full, kSoftWarps); ptx::mbar_init(b_pv, 1); ptx::mbar_init(b_end, 1);
         s_flags[1] = 0u;
         s_flags[2] = 0u;
@@ -299,8 +305,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (lane == 0) ptx::mbar_arrive(b_seg_full + 8 * slot);
             if (si > 0) {
                 // the Q tile, rows beyond the request's as zeros
-                const int qi = si - 1, qb = qi & 1;
-                if (qi >= 2) ok = __all_sync(~0u, wait(b_q_empty + 8 * qb, (qi / 2) - 1));
+                const int qi = si - 1, qb = qi % L::kQBufs;
+                if (qi >= L::kQBufs) ok = __all_sync(~0u, wait(b_q_empty + 8 * qb, (qi / L::kQBufs) - 1));
                 if (!ok) { if (lane == 0) give_up(1); break; }
                 // lane: a 16-byte chunk c of rows r, r + kRows, ...
                 constexpr int kChunks = D / 8, kRows = 32 / kChunks;
@@ -318,10 +324,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     src += kRows * D;
                     while (head >= p.G) { head -= p.G; src += p.q_stride - (long long)p.G * D; }
                 }
-                ptx::cp_async_wait_all();
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
+                cp_async_arrive(b_q_full + 8 * qb);  // when this lane's copies have landed
             }
             if (!more) break;
             q0 = n0; qh = nh; qr0 = nr0; qrows = nrows;
@@ -403,63 +406,84 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         const uint64_t v_desc = ptx::smem_desc_sw128(base + L::kRing, D == 128 ? 1024 : 0, L::kGroup);
         const uint64_t q_desc = ptx::smem_desc_sw128(base + L::kQ, 16, 1024);
         const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, 16, 1024);
-        uint32_t step = 0;                   // steps whose S product was issued
-        bool ok = true;
-        // a step whose S product was issued and whose O product was not
-        bool pend = false, pend_first = false;
-        uint32_t pend_step = 0, pend_seg = 0;
-        auto all = [&](bool x) { return __all_sync(~0u, x); };
-        auto second = [&]() {                // O^T (+)= V^T P^T of the pending step
-            const uint32_t vi = 2 * pend_step + 1, st = vi % kStages, ob = pend_seg & 1u;
-            ok = all(wait(b_full + 8 * st, vi / kStages) && wait(b_p_full, pend_step));
-            if (ok && pend_first && pend_seg >= 2) ok = all(wait(b_o_empty + 8 * ob, pend_seg / 2 - 1));
-            if (!ok) return;
-            ptx::tc_fence_after();
-            const uint64_t va = v_desc + st * (L::kTileBytes / 16);
-            if (one) {
+        // Whatever is ready goes first: the O product of the oldest step whose S
+        // product was issued, or the next S product (of the next segment, too), at
+        // most one step ahead.  Short segments keep both going.
+        struct Step { uint32_t step, seg; bool first; } old{}, young{};   // S issued, O not: the oldest, and one behind it
+        bool has_old = false, has_young = false, in_seg = false, q_ready = false, done = false, ok = true;
+        uint32_t step = 0, si = 0;
+        int s = 0, steps = 0, idle = 0;
+        long long since = clock64();
+        auto ready = [&](uint32_t b, uint32_t phase) { return __all_sync(~0u, ptx::mbar_test_wait(b, phase & 1u)); };
+        while (!(done && !has_old)) {
+            bool moved = false;
+            if (has_old) {                       // O^T (+)= V^T P^T
+                const uint32_t vi = 2 * old.step + 1, st = vi % kStages, ob = old.seg & 1u;
+                if (ready(b_p_full, old.step) && ready(b_full + 8 * st, vi / kStages) &&
+                    (!old.first || old.seg < 2 || ready(b_o_empty + 8 * ob, old.seg / 2 - 1))) {
+                    ptx::tc_fence_after();
+                    const uint64_t va = v_desc + st * (L::kTileBytes / 16);
+                    if (one) {
 #pragma unroll
-                for (int k = 0; k < kSteps / 16; ++k)
-                    ptx::mma_f16(tmem + 2 * N + ob * N, va + k * (2 * L::kGroup / 16), p_desc + k * (2048 / 16), id_o,
-                                 pend_first && k == 0 ? 0u : 1u);
-                ptx::mma_commit(b_empty + 8 * st);
-                ptx::mma_commit(b_pv);
-            }
-            __syncwarp();
-            pend = false;
-        };
-        for (uint32_t si = 0; ok; ++si) {
-            const int slot = si % kSegs;
-            ok = all(wait(b_seg_full + 8 * slot, si / kSegs));
-            if (!ok) break;
-            const int steps = s_seg[slot].steps;
-            __syncwarp();
-            if (steps < 0) break;
-            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
-            const uint32_t qb = si & 1u;
-            const uint64_t qa = q_desc + qb * (L::kQBytes / 16);
-            ok = all(wait(b_q_full + 8 * qb, si / 2));
-            for (int s = 0; s < steps && ok; ++s, ++step) {
-                const uint32_t ki = 2 * step, st = ki % kStages, sb = step & 1u;
-                ok = all(wait(b_full + 8 * st, ki / kStages));
-                if (ok && step >= 2) ok = all(wait(b_s_empty + 8 * sb, step / 2 - 1));
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint64_t ka = k_desc + st * (L::kTileBytes / 16);
-                if (one) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        ptx::mma_f16(tmem + sb * N, ka + (k / 4) * (1024 / 16) + (k % 4) * 2,
-                                     qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, k ? 1u : 0u);
-                    ptx::mma_commit(b_s_full + 8 * sb);
-                    ptx::mma_commit(b_empty + 8 * st);
-                    if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
+                        for (int k = 0; k < kSteps / 16; ++k)
+                            ptx::mma_f16(tmem + 2 * N + ob * N, va + k * (2 * L::kGroup / 16), p_desc + k * (2048 / 16), id_o,
+                                         old.first && k == 0 ? 0u : 1u);
+                        ptx::mma_commit(b_empty + 8 * st);
+                        ptx::mma_commit(b_pv);
+                    }
+                    __syncwarp();
+                    old = young;
+                    has_old = has_young;
+                    has_young = false;
+                    moved = true;
                 }
-                __syncwarp();
-                if (pend) second();
-                if (!ok) break;
-                pend = true; pend_first = s == 0; pend_step = step; pend_seg = si;
             }
-            if (ok && pend) second();        // the segment's end does not wait for the next one's keys
+            if (!done && !in_seg && ready(b_seg_full + 8 * (si % kSegs), si / kSegs)) {
+                steps = s_seg[si % kSegs].steps;
+                __syncwarp();
+                if (steps < 0) done = true;
+                else {
+                    if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * (si % kSegs));
+                    in_seg = true;
+                    q_ready = false;
+                    s = 0;
+                }
+                moved = true;
+            }
+            if (in_seg && !has_young) {          // S^T = K Q^T
+                const uint32_t qb = si % L::kQBufs, ki = 2 * step, st = ki % kStages, sb = step & 1u;
+                if (!q_ready && ready(b_q_full + 8 * qb, si / L::kQBufs)) {
+                    ptx::fence_proxy_async_smem();       // the Q tile came by the generic proxy
+                    q_ready = true;
+                }
+                if (q_ready && ready(b_full + 8 * st, ki / kStages) && (step < 2 || ready(b_s_empty + 8 * sb, step / 2 - 1))) {
+                    ptx::tc_fence_after();
+                    const uint64_t ka = k_desc + st * (L::kTileBytes / 16), qa = q_desc + qb * (L::kQBytes / 16);
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            ptx::mma_f16(tmem + sb * N, ka + (k / 4) * (1024 / 16) + (k % 4) * 2,
+                                         qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, k ? 1u : 0u);
+                        ptx::mma_commit(b_s_full + 8 * sb);
+                        ptx::mma_commit(b_empty + 8 * st);
+                        if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
+                    }
+                    __syncwarp();
+                    const Step now{step, si, s == 0};
+                    if (has_old) { young = now; has_young = true; }
+                    else { old = now; has_old = true; }
+                    ++step;
+                    if (++s == steps) { in_seg = false; ++si; }
+                    moved = true;
+                }
+            }
+            if (moved) idle = 0;
+            else {
+                if (idle == 0) since = clock64();
+                __nanosleep(20);
+                if ((++idle & 15) == 0 || wl < (1LL << 20))
+                    if (__any_sync(~0u, *abort_flag != 0u || clock64() - since > wl)) { ok = false; break; }
+            }
         }
         if (!ok && lane == 0) give_up(4);
         // nothing is in flight in the tensor core when the CTA leaves
@@ -593,10 +617,11 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     if (gone || later) {
                         uint4* v = reinterpret_cast<uint4*>(gbase + L::kRing + (vi % kStages) * L::kTileBytes + (row >> 3) * L::kGroup) + (row & 7) * 8;
                         constexpr int kHalves = D / 64;
-                        // the two halves of the softmax warps share a row's chunks
+                        // the two halves of the softmax warps share a row's chunks,
+                        // each row begins at another one (other banks)
 #pragma unroll
                         for (int c = half; c < 8 * kHalves; c += 2) {
-                            uint4* at = v + (c / 8) * 64 + (c % 8);
+                            uint4* at = v + (c / 8) * 64 + ((c + row) & 7);
                             if (gone) *at = make_uint4(0u, 0u, 0u, 0u);
                             else {
                                 const uint4 y = *at;
