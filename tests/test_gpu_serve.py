@@ -139,12 +139,12 @@ def test_append_writes_exactly_the_slots(vm, T, H, D, P, dtype):
 
 
 # --------------------------------------------------------------- attention
-def _attention_inputs(rng, lens, news, Hq, Hkv, D, P, dtype, junk=True, q_pad=0, extra_pages=3):
+def _attention_inputs(rng, lens, news, Hq, Hkv, D, P, dtype, junk=True, q_pad=0, extra_pages=3, wide=0):
     """Caches whose unused places (other pages, rows beyond the length) hold
     NaN, block tables with -1 beyond the owned pages."""
     B, lens, news = len(lens), np.asarray(lens), np.asarray(news)
     per = -(-lens // P)
-    width, pages = int(per.max()) + 1, int(per.sum()) + extra_pages
+    width, pages = int(per.max()) + 1 + wide, int(per.sum()) + extra_pages
     perm = rng.permutation(pages)
     table = np.full((B, width), -1)
     k, v = (np.full((pages, Hkv, P, D), np.nan if junk else 0.0, np.float32) for _ in range(2))
@@ -221,6 +221,22 @@ def test_attention_matches_the_definition(vm, case, dtype):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("lens,news,Hq,Hkv,D,P", [
+    ([500, 2, 129], [4, 2, 8], 16, 1, 128, 32), ([70, 1], [17, 1], 16, 2, 128, 8), ([130, 20], [8, 3], 96, 1, 64, 16),
+    ([3000], [8], 16, 1, 128, 64),
+])
+def test_attention_with_128_rows_at_once(vm, lens, news, Hq, Hkv, D, P):
+    """Block tables for long contexts (most of them empty here): more than 64 rows
+    of a key head are taken together."""
+    rng = np.random.default_rng(len(lens) + Hq)
+    a = _attention_inputs(rng, lens, news, Hq, Hkv, D, P, torch.bfloat16, wide=400000 // P)
+    out, lse, ws = _attend(vm, a, max(news))
+    _check_attention(a, out, lse, D ** -0.5)
+    assert _status(vm, ws) == 0
+    again, lse2, _ = _attend(vm, a, max(news), ws=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_attention_of_a_large_ragged_batch(vm):
     rng = np.random.default_rng(77)
     lens = rng.integers(1, 400, 150)
@@ -245,14 +261,14 @@ def _vary_block_values(a, b, P, bad):
     a["v"][int(a["table"][b, pos // P]), :, pos % P, ::3] = bad
 
 
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dtype,Hq,wide", [(torch.bfloat16, 8, 0), (torch.float32, 8, 0), (torch.bfloat16, 32, 30000)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, dtype):
+def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, dtype, Hq, wide):
     """A draft whose value is not finite: the rows before it, which do not see
     it, are as they were; its own row is not finite where the value is not."""
     rng = np.random.default_rng(4)
     P = 16
-    a = _attention_inputs(rng, [70, 64, 8], [8, 5, 8], 8, 2, 128, P, dtype)
+    a = _attention_inputs(rng, [70, 64, 8], [8, 5, 8], Hq, 2, 128, P, dtype, wide=wide)
     clean, _, _ = _attend(vm, a, 8)
     for b in range(3):
         _vary_block_values(a, b, P, bad)

@@ -12,7 +12,8 @@
 // spent on padding rows.  What is left per position and row is one 2^x.
 //
 // Roles (12 warps, one CTA per SM, a ring of 5 tiles of 32 KB):
-//   warps 0-3, 4-7   softmax of the first and the second half of the columns:
+//   warps 0-3, 4-7   softmax of the first and the second part of the columns (of 2; or 4
+//                    parts, and the numbers below move up):
 //                    thread = position; weights to shared memory
 //   warps 8, 11      TMA producers of the keys and of the values (lane = box of a
 //                    page: 8 positions x 64 entries x both halves of the head x
@@ -54,8 +55,17 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSteps = 128;              // positions per step (one tile of K and one of V)
-constexpr int kSoftWarps = 8;
-constexpr int kKeyWarp = 8, kMmaWarp = 9, kSegWarp = 10, kValWarp = 11, kWarps = 12;
+// The columns are shared by kParts groups of 4 softmax warps: 8, 16 or (of 128
+// columns) 32 a thread.  64 columns over two groups, 32 a thread in registers,
+// took 209 us for 64 requests of 64 rows, over four 195; 32 columns over four 70
+// us for 256 requests of 16-300 positions, over two 82, and the same for long
+// ones (head size 64: two, 111 us against 114).
+template <int N, int D>
+struct Roles {
+    static constexpr int kParts = N >= 64 || (N == 32 && D == 128) ? 4 : 2, kSoftWarps = 4 * kParts;
+    static constexpr int kKeyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kSegWarp = kSoftWarps + 2, kValWarp = kSoftWarps + 3;
+    static constexpr int kWarps = kSoftWarps + 4;
+};
 constexpr int kSegs = 8;                 // segment descriptors in flight
 constexpr int kBadRing = 8;              // steps the producer may be ahead of the softmax, and more
 constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
@@ -74,15 +84,17 @@ template <int N, int D>
 struct Smem {
     static constexpr int kTileBytes = kSteps * D * 2;
     static constexpr int kGroup = 8 * D * 2;                      // 8 positions: [half of the head][position][64 entries]
-    static constexpr int kStages = 5 * 128 / D;
+    static constexpr int kStages = (N == 128 ? 4 : 5) * 128 / D;
     static constexpr int kQBytes = N * D * 2;
-    static constexpr int kQBufs = N * D <= 32 * 128 ? 4 : 2;      // Q tiles: segments may be a step long
+    static constexpr int kQBufs = N * D <= 32 * 128 ? 4 : N == 128 ? 1 : 2;      // Q tiles: segments may be a step long
     static constexpr int kRing = 0;
     static constexpr int kQ = kRing + kStages * kTileBytes;
-    static constexpr int kP = kQ + kQBufs * kQBytes;                   // [128][64] bf16, 128-byte rows
-    static constexpr int kMax = kP + kSteps * 128;                // [N][4]
+    static constexpr int kP = kQ + kQBufs * kQBytes;                   // [128][64] bf16, 128-byte rows (128 columns: twice)
+    static constexpr int kPBytes = kSteps * 128 * (N == 128 ? 2 : 1);
+    static constexpr int kMax = kP + kPBytes;                     // [N][4]
     static constexpr int kSum = kMax + N * 16;                    // [N][4]
-    static constexpr int kSeg = kSum + N * 16;
+    static constexpr int kNeg = kSum + N * 16;                    // [N], where 32 columns a thread leave no registers for it
+    static constexpr int kSeg = kNeg + (N == 128 ? N * 4 : 0);
     static constexpr int kBar = kSeg + kSegs * (int)sizeof(Seg);
     static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 3;
     static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, non-finite flag, -, the producers' counts, bad boxes
@@ -130,16 +142,6 @@ template <> __device__ __forceinline__ void tmem_get<16>(uint32_t a, float (&v)[
                    "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
                  : "r"(a) : "memory");
 }
-template <> __device__ __forceinline__ void tmem_get<32>(uint32_t a, float (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(a) : "memory");
-}
 template <int C> __device__ __forceinline__ void tmem_put(uint32_t a, const float (&v)[C]);
 template <> __device__ __forceinline__ void tmem_put<8>(uint32_t a, const float (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;"
@@ -150,14 +152,6 @@ template <> __device__ __forceinline__ void tmem_put<16>(uint32_t a, const float
                  "\n\ttcgen05.wait::st.sync.aligned;"
                  ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
                    "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_put<32>(uint32_t a, const float (&v)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\ttcgen05.wait::st.sync.aligned;"
-                 ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-                   "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
-                   "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
-                   "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -174,11 +168,13 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
 }
 
 template <int N, int D>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(Roles<N, D>::kWarps * 32, 1)
 attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const int bx, const int page_heads) {
     using L = Smem<N, D>;
-    constexpr int HC = N / 2;                   // columns of a softmax half
+    using R = Roles<N, D>;
+    constexpr int kParts = R::kParts, kSoftWarps = R::kSoftWarps, kKeyWarp = R::kKeyWarp, kMmaWarp = R::kMmaWarp, kSegWarp = R::kSegWarp, kValWarp = R::kValWarp;
+    constexpr int HC = N / kParts;           // columns of a softmax group
     constexpr int kStages = L::kStages;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -378,7 +374,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         }
         // every copy issued lands before the CTA leaves: the last fill of each stage
         if (lane == 0) s_flags[4 + kv] = fill;
-        ptx::named_barrier(3, 64);
+        ptx::named_barrier(1 + kParts, 64);
         if (lane == 0 && !kv) {
             const uint32_t keys = s_flags[4], vals = s_flags[5];      // tiles 0, 2, .. < keys and 1, 3, .. < vals
             for (uint32_t i = 0; i < (uint32_t)kStages; ++i) {
@@ -405,7 +401,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         // first and is not used); 16 positions = 2 groups
         const uint64_t v_desc = ptx::smem_desc_sw128(base + L::kRing, D == 128 ? 1024 : 0, L::kGroup);
         const uint64_t q_desc = ptx::smem_desc_sw128(base + L::kQ, 16, 1024);
-        const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, 16, 1024);
+        const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, N == 128 ? kSteps * 128 : 16, 1024);
         // Whatever is ready goes first: the O product of the oldest step whose S
         // product was issued, or the next S product (of the next segment, too), at
         // most one step ahead.  Short segments keep both going.
@@ -499,6 +495,10 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         const int my_box = row / bx;
         float4* s_max = reinterpret_cast<float4*>(gbase + L::kMax);
         float4* s_sum = reinterpret_cast<float4*>(gbase + L::kSum);
+        // columns in chunks of CH; with more than one, scores are read from tensor
+        // memory twice and the references from shared memory
+        constexpr int CH = HC > 16 ? 16 : HC, NCH = HC / CH;
+        float* s_neg = reinterpret_cast<float*>(gbase + L::kNeg) + half * HC;
         uint32_t step = 0;
         bool ok = true;
         // A segment's rows are written after the first step of the next segment
@@ -518,9 +518,11 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             const int first_new = d.len - d.n;                     // position of the block's first token
             // lane c: the last position that column c of this half sees
             const int my_last = first_new + p.by_group(d.r0 + half * HC + (lane & (HC - 1)));
-            float neg[HC], l[HC];                                  // minus the reference, this thread's sum of the weights
+            float neg[CH], l[HC];                                  // minus the reference, this thread's sum of the weights
 #pragma unroll
-            for (int c = 0; c < HC; ++c) { neg[c] = 0.f; l[c] = 0.f; }
+            for (int c = 0; c < CH; ++c) neg[c] = 0.f;
+#pragma unroll
+            for (int c = 0; c < HC; ++c) l[c] = 0.f;
             float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
             bool unset = true;                                     // a column of the half has no reference yet
             bool stop = false;
@@ -529,41 +531,64 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 const int pos0 = d.pos0 + s * kSteps, pos = pos0 + row, there = d.pos1 - pos0;
                 ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
                 ok = __all_sync(~0u, ok);
-                float x[HC];
-                uint32_t bad = 0u;
-                if (ok) {
-                    ptx::tc_fence_after();
-                    tmem_get<HC>(tmem + lanes + (step & 1u) * N + half * HC, x);
-                    ptx::tc_fence_before();
-                    bad = s_bad[step % kBadRing];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < HC; ++c) x[c] = 0.f;
-                }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(b_s_empty + 8 * (step & 1u));
+                const uint32_t s_at = tmem + lanes + (step & 1u) * N + half * HC;
+                const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
                 // positions beyond the end or in a bad page, and the block's later tokens
                 const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
                 const bool gone = row >= there || (bad >> my_box & 1u);
-                if (edge) {
+                float x[CH];
+                // the scores of chunk k, -inf where the column does not see the position
+                auto scores = [&](int k) {
+                    if (ok) tmem_get<CH>(s_at + k * CH, x);
+                    else {
 #pragma unroll
-                    for (int c = 0; c < HC; ++c) {
-                        const int last = __shfl_sync(~0u, my_last, c);
-                        if (gone || pos > last) x[c] = -INFINITY;
+                        for (int c = 0; c < CH; ++c) x[c] = 0.f;
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const int last = __shfl_sync(~0u, my_last, k * CH + c);
+                            if (gone || pos > last) x[c] = -INFINITY;
+                        }
+                    }
+                };
+                auto refs = [&](int k) {
+                    if constexpr (NCH > 1) {
+#pragma unroll
+                        for (int c = 0; c < CH; c += 4)
+                            *reinterpret_cast<float4*>(neg + c) = *reinterpret_cast<const float4*>(s_neg + k * CH + c);
+                    }
+                };
+                auto read_done = [&]() {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(b_s_empty + 8 * (step & 1u));
+                };
+                ptx::tc_fence_after();
+                float high = -INFINITY;
+                if (NCH == 1 || !unset) {
+#pragma unroll
+                    for (int k = 0; k < NCH; ++k) {
+                        scores(k);
+                        refs(k);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) high = fmaxf(high, fmaf(x[c], scale2, neg[c]));
                     }
                 }
-                float high = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < HC; ++c) high = fmaxf(high, fmaf(x[c], scale2, neg[c]));
+                if (NCH == 1) read_done();
                 const bool move = ptx::bar_red_or(1 + half, 128, unset || high > kSlack || !ok);
                 // the product before this one is done: P may be overwritten, O rescaled
                 if (step > 0) ok = wait(b_pv, step - 1) && ok;
-                if (move) {                     // the same in every thread of the half
+                if (move) {                     // the same in every thread of the group
                     float mine = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < HC; ++c) {
-                        const float w = warp_max(x[c]);
-                        if (lane == c) mine = w;
+                    for (int k = 0; k < NCH; ++k) {
+                        if (NCH > 1) scores(k);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const float w = warp_max(x[c]);
+                            if (lane == k * CH + c) mine = w;
+                        }
                     }
                     float* mx = reinterpret_cast<float*>(s_max + half * HC);
                     if (lane < HC) mx[lane * 4 + quarter] = mine;
@@ -575,37 +600,52 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     my_ref = to;
                     unset = __any_sync(~0u, to == -INFINITY);
                     // (the next write to s_max comes after another barrier)
-                    float a[HC];
-#pragma unroll
-                    for (int c = 0; c < HC; ++c) {
-                        a[c] = __shfl_sync(~0u, my_a, c);
-                        const float r = __shfl_sync(~0u, to, c);
-                        neg[c] = r == -INFINITY ? 0.f : -r;
-                        l[c] *= a[c];
+                    if (NCH > 1) {
+                        if (quarter == 0) s_neg[lane] = to == -INFINITY ? 0.f : -to;
+                        ptx::named_barrier(1 + half, 128);
                     }
-                    if (s > 0) {
-                        ptx::tc_fence_after();
-                        float o[HC];
-                        tmem_get<HC>(o_at, o);
+                    if (s > 0) ptx::tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < HC; ++c) o[c] *= a[c];
-                        tmem_put<HC>(o_at, o);
+                    for (int k = 0; k < NCH; ++k) {
+                        float a[CH];
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            a[c] = __shfl_sync(~0u, my_a, k * CH + c);
+                            if (NCH == 1) {
+                                const float r = __shfl_sync(~0u, to, c);
+                                neg[c] = r == -INFINITY ? 0.f : -r;
+                            }
+                            l[k * CH + c] *= a[c];
+                        }
+                        if (s > 0) {
+                            float o[CH];
+                            tmem_get<CH>(o_at + k * CH, o);
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) o[c] *= a[c];
+                            tmem_put<CH>(o_at + k * CH, o);
+                        }
                     }
                 }
                 // weights: row `row` of P, columns half * HC ..
-                const uint32_t prow = base + L::kP + row * 128;
 #pragma unroll
-                for (int c0 = 0; c0 < HC; c0 += 8) {
-                    float w[8];
+                for (int k = 0; k < NCH; ++k) {
+                    if (NCH > 1) { scores(k); refs(k); }
+                    const int col0 = half * HC + k * CH;
+                    const uint32_t prow = base + L::kP + (col0 / 64) * (kSteps * 128) + row * 128;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        w[e] = fast_exp2(fmaf(x[c0 + e], scale2, neg[c0 + e]));
-                        l[c0 + e] += w[e];
+                    for (int c0 = 0; c0 < CH; c0 += 8) {
+                        float w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            w[e] = fast_exp2(fmaf(x[c0 + e], scale2, neg[c0 + e]));
+                            l[k * CH + c0 + e] += w[e];
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                     ::"r"(prow + ((((col0 + c0) / 8 & 7) ^ (row & 7)) << 4)), "r"(pack_bf16(w[0], w[1])),
+                                       "r"(pack_bf16(w[2], w[3])), "r"(pack_bf16(w[4], w[5])), "r"(pack_bf16(w[6], w[7])) : "memory");
                     }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                 ::"r"(prow + ((((half * HC + c0) / 8) ^ (row & 7)) << 4)), "r"(pack_bf16(w[0], w[1])),
-                                   "r"(pack_bf16(w[2], w[3])), "r"(pack_bf16(w[4], w[5])), "r"(pack_bf16(w[6], w[7])) : "memory");
                 }
+                if (NCH > 1) read_done();
                 if (edge) {
                     // a value that no row may use is zero in shared memory: the
                     // product would turn 0 * NaN into NaN.  Of the block's later
@@ -620,7 +660,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                         // the two halves of the softmax warps share a row's chunks,
                         // each row begins at another one (other banks)
 #pragma unroll
-                        for (int c = half; c < 8 * kHalves; c += 2) {
+                        for (int c = half; c < 8 * kHalves; c += kParts) {
                             uint4* at = v + (c / 8) * 64 + ((c + row) & 7);
                             if (gone) *at = make_uint4(0u, 0u, 0u, 0u);
                             else {
@@ -644,58 +684,61 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 if (none) ok = wait(b_pv, step - 1) && ok;
                 ok = __all_sync(~0u, ok);
                 const uint32_t pi = si - 1;
-                float o[HC];
-                if (ok) {
-                    ptx::tc_fence_after();
-                    tmem_get<HC>(tmem + lanes + 2 * N + (pi & 1u) * N + half * HC, o);
-                    ptx::tc_fence_before();
-                } else {
-#pragma unroll
-                    for (int c = 0; c < HC; ++c) o[c] = 0.f;
-                }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (pi & 1u));
                 const Seg& e = const_cast<Seg&>(s_seg[pi % kSegs]);
                 const int e_row = half * HC + (lane & (HC - 1)), e_tok = p.by_group(e.r0 + e_row), dim = row;
                 const int e_at = (e.q0 + e_tok) * p.Hq + e.h * p.G + (e.r0 + e_row - e_tok * p.G);   // below N * Hq < 2^31
                 const int cols = min(HC, e.rows - half * HC);
-                if (s_flags[2]) {
-                    // non-finite values of the block's later tokens (this CTA's positions)
-                    const int e_new = e.len - e.n;
-                    for (int pos = max(e_new + 1, e.pos0); pos < e.pos1; ++pos) {
-                        const int pg = p.by_page(pos), page = p.table[(size_t)e.b * p.width + pg];
-                        if (page < 0 || page >= p.pages) continue;
-                        float v = 0.f;
-                        if (dim < D)
-                            v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
-                                       ((long long)e.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
-                        const bool odd = !(fabsf(v) < INFINITY);
+                const int part_slot = e.slot, e_new = e.len - e.n;
+                const float e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
+                ptx::tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < HC; ++c) {
-                            const int last = e_new + __shfl_sync(~0u, e_tok, c);
-                            if (odd && pos <= last) o[c] += v;
+                for (int k = 0; k < NCH; ++k) {
+                    float o[CH];
+                    if (ok) tmem_get<CH>(tmem + lanes + 2 * N + (pi & 1u) * N + half * HC + k * CH, o);
+                    else {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) o[c] = 0.f;
+                    }
+                    if (s_flags[2]) {
+                        // non-finite values of the block's later tokens (this CTA's positions)
+                        for (int pos = max(e_new + 1, e.pos0); pos < e.pos1; ++pos) {
+                            const int pg = p.by_page(pos), page = p.table[(size_t)e.b * p.width + pg];
+                            if (page < 0 || page >= p.pages) continue;
+                            float v = 0.f;
+                            if (dim < D)
+                                v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
+                                           ((long long)e.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
+                            const bool odd = !(fabsf(v) < INFINITY);
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) {
+                                const int last = e_new + __shfl_sync(~0u, e_tok, k * CH + c);
+                                if (odd && pos <= last) o[c] += v;
+                            }
                         }
                     }
-                }
-                const int part_slot = e.slot;
-                if (part_slot < 0) {
-                    const float e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
-                    uint16_t* out = static_cast<uint16_t*>(p.out) + dim;
+                    if (part_slot < 0) {
+                        uint16_t* out = static_cast<uint16_t*>(p.out) + dim;
 #pragma unroll
-                    for (int c = 0; c < HC; ++c) {
-                        const float inv = __shfl_sync(~0u, e_inv, c);
-                        const int at = __shfl_sync(~0u, e_at, c);
-                        if (c < cols && dim < D) out[(size_t)at * D] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
+                        for (int c = 0; c < CH; ++c) {
+                            const float inv = __shfl_sync(~0u, e_inv, k * CH + c);
+                            const int at = __shfl_sync(~0u, e_at, k * CH + c);
+                            if (k * CH + c < cols && dim < D) out[(size_t)at * D] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
+                        }
+                    } else {
+                        float* part = p.part + ((size_t)part_slot * p.row_tile + half * HC + k * CH) * D + dim;
+#pragma unroll
+                        for (int c = 0; c < CH; ++c)
+                            if (k * CH + c < cols && dim < D) part[c * D] = o[c];
                     }
-                    if (quarter == 0 && lane < cols && p.lse)
-                        p.lse[e_at] = pend_sum != 0.f ? pend_ref * kLn2 + logf(pend_sum) : -INFINITY;
-                } else {
-                    float* part = p.part + ((size_t)part_slot * p.row_tile + half * HC) * D + dim;
-#pragma unroll
-                    for (int c = 0; c < HC; ++c)
-                        if (c < cols && dim < D) part[c * D] = o[c];
-                    float2* stats = reinterpret_cast<float2*>(p.part + (size_t)2 * p.ctas * p.row_tile * D);
-                    if (quarter == 0 && lane < cols) stats[(size_t)part_slot * p.row_tile + e_row] = make_float2(pend_ref, pend_sum);
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (pi & 1u));
+                if (quarter == 0 && lane < cols) {
+                    if (part_slot >= 0) {
+                        float2* stats = reinterpret_cast<float2*>(p.part + (size_t)2 * p.ctas * p.row_tile * D);
+                        stats[(size_t)part_slot * p.row_tile + e_row] = make_float2(pend_ref, pend_sum);
+                    } else if (p.lse) p.lse[e_at] = pend_sum != 0.f ? pend_ref * kLn2 + logf(pend_sum) : -INFINITY;
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * (pi % kSegs));
@@ -768,7 +811,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     static_assert(Smem<N, D>::kTotal + 1024 <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_mma_kernel<N, D>, dim3(p.ctas), dim3(kWarps * 32), smem, s, p, maps[0], maps[1], bx, page_heads);
+    return launch_dependent(attn_mma_kernel<N, D>, dim3(p.ctas), dim3(Roles<N, D>::kWarps * 32), smem, s, p, maps[0], maps[1], bx, page_heads);
 }
 
 }  // namespace
@@ -781,9 +824,18 @@ bool attn_mma_supported(const AttnParams& p) {
            tma_encoder() != nullptr;
 }
 
+template <int D>
+static cudaError_t launch_head(const AttnParams& p, cudaStream_t s) {
+    switch (p.row_tile) {
+        case 16: return launch<16, D>(p, s);
+        case 32: return launch<32, D>(p, s);
+        case 64: return launch<64, D>(p, s);
+        default: return launch<128, D>(p, s);
+    }
+}
+
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s) {
-    if (p.D == 64) return p.row_tile == 16 ? launch<16, 64>(p, s) : p.row_tile == 32 ? launch<32, 64>(p, s) : launch<64, 64>(p, s);
-    return p.row_tile == 16 ? launch<16, 128>(p, s) : p.row_tile == 32 ? launch<32, 128>(p, s) : launch<64, 128>(p, s);
+    return p.D == 64 ? launch_head<64>(p, s) : launch_head<128>(p, s);
 }
 
 }  // namespace dspark

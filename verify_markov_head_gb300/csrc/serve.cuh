@@ -19,7 +19,6 @@ enum ServeStatusBits : uint32_t {
 
 constexpr int kTile = DSPARK_CACHE_TILE;   // cache positions per attention tile
 constexpr int kMaxAttnCtas = 160;          // CTAs of an attention launch (bounds its partial results)
-constexpr int kMaxRowTile = 64;            // query rows of one key-value head an attention CTA takes at once
 
 // ---------------------------------------------------------------- cache plan
 struct PlanParams {
@@ -86,7 +85,7 @@ bool attn_mma_supported(const AttnParams& p);
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
 // Rows of a row tile where a key-value head has `rows` query rows.
 inline int attn_row_tile(int rows, bool mma) {
-    return mma ? (rows <= 16 ? 16 : rows <= 32 ? 32 : 64) : (rows <= 8 ? 8 : 32);
+    return mma ? (rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128) : (rows <= 8 ? 8 : 32);
 }
 
 // The split of an attention launch.  A segment is the run of tiles of kTile
