@@ -199,7 +199,7 @@ ATTENTION = [
     ([500, 2, 129], [4, 2, 8], 16, 1, 128, 32),                # one key head: several tiles of rows
     ([70], [17], 16, 2, 128, 1),                               # the longest block, pages of one position
     ([1000, 1], [1, 1], 8, 8, 128, 128),                       # no shared heads
-    ([90, 33], [8, 2], 6, 2, 80, 16),                          # other head sizes: CUDA cores
+    ([90, 33], [8, 2], 6, 2, 80, 16),                          # other head sizes
     ([90, 130], [3, 8], 4, 2, 256, 64),
     ([45, 100], [8, 1], 8, 1, 8, 16),
     ([4100], [8], 8, 2, 64, 64),                               # split over many CTAs
@@ -237,6 +237,25 @@ def test_attention_with_128_rows_at_once(vm, lens, news, Hq, Hkv, D, P):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("P,group,new,wide", [(8, 1, 8, 0), (16, 4, 4, 0), (64, 4, 8, 0), (128, 8, 1, 0), (32, 12, 8, 400000), (5, 3, 8, 0)])
+@pytest.mark.parametrize("D", [16, 40, 80, 96, 112, 120, 192, 256, 136])
+def test_attention_of_other_head_sizes(vm, D, P, group, new, wide):
+    """Heads that do not fill a tile's row, or fill two; 8 to 96 rows of a key
+    head (wide: 96 at once); lengths about the tiles' ends; q and cache with
+    gaps between tokens and pages; positions beyond the lengths hold NaN."""
+    rng = np.random.default_rng(D + P)
+    lens = [300, 1, 0, 128, 129, 64, 700]
+    news = np.minimum([new, 1, 2, new, max(new - 1, 1), new, new], new)
+    a = _attention_inputs(rng, lens, news, 2 * group, 2, D, P, torch.bfloat16, q_pad=1, wide=wide // P)
+    kv = torch.stack([a["k"], a["v"]], 1)
+    a = dict(a, k=kv[:, 0], v=kv[:, 1])
+    out, lse, ws = _attend(vm, a, new)
+    _check_attention(a, out, lse, D ** -0.5)
+    assert _status(vm, ws) == 0
+    again, lse2, _ = _attend(vm, a, new, ws=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_attention_of_a_large_ragged_batch(vm):
     rng = np.random.default_rng(77)
     lens = rng.integers(1, 400, 150)
@@ -262,13 +281,14 @@ def _vary_block_values(a, b, P, bad):
 
 
 @pytest.mark.parametrize("dtype,Hq,wide", [(torch.bfloat16, 8, 0), (torch.float32, 8, 0), (torch.bfloat16, 32, 30000)])
+@pytest.mark.parametrize("D", [128, 96, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, dtype, Hq, wide):
+def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, D, dtype, Hq, wide):
     """A draft whose value is not finite: the rows before it, which do not see
     it, are as they were; its own row is not finite where the value is not."""
     rng = np.random.default_rng(4)
     P = 16
-    a = _attention_inputs(rng, [70, 64, 8], [8, 5, 8], Hq, 2, 128, P, dtype, wide=wide)
+    a = _attention_inputs(rng, [70, 64, 8], [8, 5, 8], Hq, 2, D, P, dtype, wide=wide)
     clean, _, _ = _attend(vm, a, 8)
     for b in range(3):
         _vary_block_values(a, b, P, bad)

@@ -1,46 +1,56 @@
 // cache_attention_mma.cu -- attention over the paged cache on the tensor
-// cores: bf16, head size 64 or 128, pages of a multiple of 8 positions (the
-// rest runs on CUDA cores, cache_attention.cu, where the formulas stand).
+// cores: bf16, head sizes up to 128, 192 and 256, pages of a multiple of 8
+// positions (the rest runs on CUDA cores, cache_attention.cu, where the
+// formulas stand).
 //
 // Both products are taken transposed, so that 128 cache positions fill the
 // 128 lanes of the accumulator and the few query rows of a key-value head are
-// its columns (N = 16, 32 or 64 of them):
+// its columns (N = 16, 32, 64 or 128 of them):
 //     S^T [128 positions x N] = K [128 x D] . Q^T       (K, Q: K-major)
 //     O^T [D x N]            += V^T [D x 128] . P^T      (V, P: MN-major)
 // K and V tiles go from the pages to shared memory by TMA exactly as they lie
 // there, each is read once by the tensor core whatever N is, and no lane is
 // spent on padding rows.  What is left per position and row is one 2^x.
 //
-// Roles (12 warps, one CTA per SM, a ring of 5 tiles of 32 KB):
-//   warps 0-3, 4-7   softmax of the first and the second part of the columns (of 2; or 4
-//                    parts, and the numbers below move up):
-//                    thread = position; weights to shared memory
-//   warps 8, 11      TMA producers of the keys and of the values (lane = box of a
-//                    page: 8 positions x 64 entries x both halves of the head x
-//                    up to 8 such groups)
-//   warp 9           MMA issuer
-//   warp 10          walks the CTA's segments: descriptors and Q tiles
+// Head sizes: a row of a tile has D = 64, 128 or 256 entries.  Sizes below 128
+// other than 64 come in two boxes of 64 entries, what lies beyond the head
+// read as zeros; sizes of 192 and 256 in two stages of 128 entries, whose
+// products go to the same S^T and to two O^T.  Against the CUDA cores, 64
+// requests of 32 rows: head size 96 150 us (1900), 192 286 (3230), 256 348
+// (3460).
+//
+// Roles (12 or 20 warps, one CTA per SM, a ring of 5 stages of 32 KB, 4 with 128 columns):
+//   first 8 or 16    softmax, 2 or 4 groups of 4 warps, each with its share of the
+//                    columns: thread = position; weights to shared memory
+//   then two         TMA producers of the keys and of the values (lane = box of a
+//                    page: a multiple of 8 positions, up to 64)
+//   one              MMA issuer: whichever of the two products is ready
+//   one              walks the CTA's segments: descriptors and Q tiles
 // The reference of a column's weights, 2^(s - ref), moves only when a score
 // exceeds it by more than 8 (weights stay below 2^8, their relative precision
 // is the same).  So an ordinary step needs no maximum: each thread forms the
 // exponents it needs anyway, a barrier ORs "one of mine is above 8" over the
-// half, and only then are the column maxima found (a warp reduction and an
+// group, and only then are the column maxima found (a warp reduction and an
 // exchange over the 4 warps), and the sums and O^T in tensor memory rescaled.
 //
 // What bounds it: HBM.  A key-value head's position is 512 bytes (head size
 // 128) and 4 N multiply-adds per byte pair; at 6.8 TB/s an SM has 2800 cycles
 // for a step of 128 positions, of which the tensor core is busy 1024 (it reads
-// the 128 x 16 operand at 64 bytes a cycle, whatever N is) and a softmax warp
-// 600-1600 (N = 16-64).  So the work is to keep copies in flight: two producer
+// the 128 x 16 operand at 64 bytes a cycle, whatever N is up to 64) and a
+// softmax warp 600-1600.  So the work is to keep copies in flight: two producer
 // warps (one issued a tile in 1200 cycles with pages of 16 positions, too slow),
 // segment ends off the way (the rows are written behind the next segment's
 // first step), the split over CTAs weighted by segments (AttnSplit).
-// Measured on one GB300: 64 requests of 1024-8192 positions, 32 rows, 1.22 GB:
-// 184 us (6.6 TB/s); 256 requests of 128-4096, 8 rows, 2.22 GB: 321 us (6.9
-// TB/s); one of 131072, 64 rows, 0.54 GB: 92 us (5.8 TB/s, 6 us of it before
-// the ring is full and the join).  Taking the column maxima in every step cost
+// Measured on one GB300: 64 requests of 1024-8192 positions, 1.22 GB: 32 rows
+// 183 us (6.6 TB/s), 64 rows 196, 128 rows 249 (three chunks of work a step on
+// 32 columns a thread: the softmax bounds it); 256 requests of 128-4096, 8
+// rows, 2.22 GB: 322 us (6.9 TB/s); one of 131072, 64 rows, 0.54 GB: 89 us (6.0
+// TB/s, 6 us of it before the ring is full and the join); 256 of 16-300
+// positions, 32 rows: 68 us (43 % of the rate, a segment's beginning and end
+// cost as much as 4 tiles).  Taking the column maxima in every step cost
 // 263 us for the first, one producer warp and serial segment ends 203, MMAs
-// issued from a diverged lane 203, an unweighted split 197.
+// issued from a diverged lane 203, an unweighted split 197, products in fixed
+// order 188.  A second buffer for P gained nothing (64 rows 202, short ones 74).
 //
 // Weights are rounded to bf16 for the second product (relative 2^-8 of each
 // weight, independent in sign); their sum l is taken in fp32 before rounding.
@@ -80,13 +90,23 @@ struct Seg {
     int page[16];             // the pages of the first step's boxes
 };
 
-template <int N, int D>
+// D: entries of a tile's row, the head size p.D rounded up to 64, 128 or 256.
+// kApart: rows that the head does not fill (p.D is no multiple of 64, D is 128),
+// copied 64 entries at a time.
+template <int N, int D, bool kApart>
 struct Smem {
-    static constexpr int kTileBytes = kSteps * D * 2;
-    static constexpr int kGroup = 8 * D * 2;                      // 8 positions: [half of the head][position][64 entries]
-    static constexpr int kStages = (N == 128 ? 4 : 5) * 128 / D;
+    static constexpr int kUnits = D == 256 ? 2 : 1;               // a tile in parts of 128 entries, each a stage
+    static constexpr int kUnit = D / kUnits;                      // entries of a part
+    static constexpr int kTileBytes = kSteps * kUnit * 2;         // a stage
+    // a stage is [8 positions][64-entry half][position][64] as one box brings it,
+    // or [half][position][64] where the halves come apart
+    static constexpr int kGroup = kApart ? 1024 : 8 * kUnit * 2;  // from 8 positions to the next 8
+    static constexpr int kHalf = kApart ? kSteps * 128 : kUnit == 128 ? 1024 : 0;
+    static constexpr int kStages = (N == 128 ? 4 : 5) * 128 / kUnit;
     static constexpr int kQBytes = N * D * 2;
-    static constexpr int kQBufs = N * D <= 32 * 128 ? 4 : N == 128 ? 1 : 2;      // Q tiles: segments may be a step long
+    static constexpr int kQBufs = N * D <= 32 * 128 ? 4 : N == 128 || N * D == 64 * 256 ? 1 : 2;      // Q tiles: segments may be a step long
+    static constexpr int kCols = (2 + 2 * kUnits) * N;            // tensor memory: two S, two O of kUnits parts
+    static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kRing = 0;
     static constexpr int kQ = kRing + kStages * kTileBytes;
     static constexpr int kP = kQ + kQBufs * kQBytes;                   // [128][64] bf16, 128-byte rows (128 columns: twice)
@@ -101,12 +121,21 @@ struct Smem {
     static constexpr int kTotal = kFlags + 24 + 4 * kBadRing;
 };
 
-// The box at group `g` of (page, head) `z` (its other coordinates are 0).
-__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* m, int g, int z, uint32_t bar, uint64_t policy) {
+// The box at half `h` and group `g` of 8 positions of (page, head) `z`.
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* m, int h, int g, int z, uint32_t bar, uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(g), "r"(z), "r"(bar), "l"(policy)
+        " [%0], [%1, {%2, %2, %3, %4, %5}], [%6], %7;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(h), "r"(g), "r"(z), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// The box from entry `x` of position `pos` of (page, head) `z`; entries beyond the head are zeros.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m, int x, int pos, int z, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(pos), "r"(z), "r"(bar), "l"(policy)
         : "memory");
 }
 
@@ -167,15 +196,16 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
     return w;
 }
 
-template <int N, int D>
+template <int N, int D, bool kApart>
 __global__ void __launch_bounds__(Roles<N, D>::kWarps * 32, 1)
 attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const int bx, const int page_heads) {
-    using L = Smem<N, D>;
+    using L = Smem<N, D, kApart>;
     using R = Roles<N, D>;
     constexpr int kParts = R::kParts, kSoftWarps = R::kSoftWarps, kKeyWarp = R::kKeyWarp, kMmaWarp = R::kMmaWarp, kSegWarp = R::kSegWarp, kValWarp = R::kValWarp;
     constexpr int HC = N / kParts;           // columns of a softmax group
-    constexpr int kStages = L::kStages;
+    constexpr int kStages = L::kStages, kUnits = L::kUnits;
+    const int hd = kApart || kUnits > 1 ? p.D : D;           // the head size
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -207,7 +237,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         ptx::fence_mbar_init();
     }
     if (warp == kMmaWarp) {
-        ptx::tmem_alloc(base + L::kFlags, 4 * N);
+        ptx::tmem_alloc(base + L::kFlags, L::kTmem);
         ptx::tmem_relinquish();
     }
     if (warp == kKeyWarp && lane == 0) ptx::prefetch_tmap(&kmap);
@@ -309,16 +339,17 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 const int c = lane % kChunks;
                 int r = lane / kChunks, tok = p.by_group(qr0 + r), head = qr0 + r - tok * p.G;
                 const uint16_t* q = static_cast<const uint16_t*>(p.q);
-                const uint16_t* src = q + (q0 + tok) * p.q_stride + (size_t)(qh * p.G + head) * D + 8 * c;
+                const uint16_t* src = q + (q0 + tok) * p.q_stride + (size_t)(qh * p.G + head) * hd + 8 * c;
+                const bool in_head = !kApart && D < 256 ? true : 8 * c < hd;
                 const uint32_t qs = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
 #pragma unroll 4
                 for (int i = 0; i < N / kRows; ++i) {
-                    const bool have = r < qrows;
+                    const bool have = r < qrows && in_head;
                     ptx::cp_async_16(qs + r * 128 + (((c & 7) ^ (r & 7)) << 4), have ? src : q, have ? 16u : 0u);
                     r += kRows;
                     head += kRows;
-                    src += kRows * D;
-                    while (head >= p.G) { head -= p.G; src += p.q_stride - (long long)p.G * D; }
+                    src += kRows * hd;
+                    while (head >= p.G) { head -= p.G; src += p.q_stride - (long long)p.G * hd; }
                 }
                 cp_async_arrive(b_q_full + 8 * qb);  // when this lane's copies have landed
             }
@@ -334,7 +365,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         const CUtensorMap* map = kv ? &vmap : &kmap;
         const uint64_t pol = p.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
         const int nbox = kSteps / bx;
-        uint32_t fill = kv;                      // this warp's next tile: keys 0, 2, .., values 1, 3, ..
+        uint32_t fill = kv * kUnits;             // this warp's next stage: keys tiles 0, 2, .., values tiles 1, 3, ..
         static_assert(kStages / 2 + 1 < kBadRing, "the producer stays within the ring of bad boxes");
         bool ok = true;
         for (int si = 0; ok; ++si) {
@@ -348,7 +379,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
             const int32_t* row = p.table + (size_t)d.b * p.width;
-            for (int s = 0; s < d.steps; ++s, fill += 2) {
+            for (int s = 0; s < d.steps; ++s, fill += kUnits) {
                 const int pos = d.pos0 + s * kSteps + lane * bx;
                 const bool want = lane < nbox && pos < d.pos1;
                 const bool have = want && page >= 0 && page < p.pages;
@@ -358,30 +389,39 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 const int group = (pos - p.by_page(pos) * p.page_size) >> 3, z = page * page_heads + d.h;
                 // the next step's page
                 page = lane < nbox && pos + kSteps < d.pos1 ? __ldg(row + p.by_page(pos + kSteps)) : -1;
-                const int stage = fill % kStages;
-                if (fill >= (uint32_t)kStages) ok = __all_sync(~0u, wait(b_empty + 8 * stage, fill / kStages - 1));
-                if (!ok) { if (lane == 0) give_up(3); break; }
-                const uint32_t full = b_full + 8 * stage;
-                if (lane == 0) {
-                    if (!kv) s_bad[(fill / 2) % kBadRing] = bad;
-                    if (boxes) ptx::mbar_arrive_expect_tx(full, boxes * bx * D * 2);
-                    else ptx::mbar_arrive(full);
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u, ++fill) {
+                    const int stage = fill % kStages;
+                    if (fill >= (uint32_t)kStages) ok = __all_sync(~0u, wait(b_empty + 8 * stage, fill / kStages - 1));
+                    if (!ok) { if (lane == 0) give_up(3); break; }
+                    const uint32_t full = b_full + 8 * stage;
+                    if (lane == 0) {
+                        if (!kv) s_bad[(fill / (2 * kUnits)) % kBadRing] = bad;
+                        if (boxes) ptx::mbar_arrive_expect_tx(full, boxes * bx * L::kUnit * 2);
+                        else ptx::mbar_arrive(full);
+                    }
+                    __syncwarp();
+                    const uint32_t to = base + L::kRing + stage * L::kTileBytes + lane * (bx / 8) * L::kGroup;
+                    if (have) {
+                        if constexpr (kApart) {
+                            tma_load_rows(to, map, 0, 8 * group, z, full, pol);
+                            tma_load_rows(to + L::kHalf, map, 64, 8 * group, z, full, pol);
+                        } else tma_load_box(to, map, 2 * u, group, z, full, pol);
+                    }
                 }
-                __syncwarp();
-                if (have)
-                    tma_load_box(base + L::kRing + stage * L::kTileBytes + lane * bx * D * 2, map, group, z, full, pol);
+                if (!ok) break;
             }
         }
         // every copy issued lands before the CTA leaves: the last fill of each stage
         if (lane == 0) s_flags[4 + kv] = fill;
         ptx::named_barrier(1 + kParts, 64);
         if (lane == 0 && !kv) {
-            const uint32_t keys = s_flags[4], vals = s_flags[5];      // tiles 0, 2, .. < keys and 1, 3, .. < vals
+            const uint32_t keys = s_flags[4], vals = s_flags[5];      // stages of tiles 0, 2, .. < keys and of 1, 3, .. < vals
             for (uint32_t i = 0; i < (uint32_t)kStages; ++i) {
-                // the last tile of stage i: at most kStages - 1 below the higher count
+                // the last fill of stage i
                 const uint32_t top = max(keys, vals);
                 for (uint32_t f = top; f-- > 0 && f + 4 * kStages >= top;)
-                    if (f % kStages == i && f < (f & 1u ? vals : keys)) {
+                    if (f % kStages == i && f < (f / kUnits & 1u ? vals : keys)) {
                         ptx::mbar_wait_drain(b_full + 8 * i, (f / kStages) & 1u, kDrainCycles);
                         break;
                     }
@@ -396,10 +436,10 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, N, true, true);
         const uint32_t one = elect_one();
         const uint64_t k_desc = ptx::smem_desc_sw128(base + L::kRing, 16, L::kGroup);
-        // V^T: entries of a position lie along M, the 64-entry halves 1 KB
+        // V^T: entries of a position lie along M, the 64-entry halves kHalf
         // apart (head size 64: the second half of the lanes repeats the
         // first and is not used); 16 positions = 2 groups
-        const uint64_t v_desc = ptx::smem_desc_sw128(base + L::kRing, D == 128 ? 1024 : 0, L::kGroup);
+        const uint64_t v_desc = ptx::smem_desc_sw128(base + L::kRing, L::kHalf, L::kGroup);
         const uint64_t q_desc = ptx::smem_desc_sw128(base + L::kQ, 16, 1024);
         const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, N == 128 ? kSteps * 128 : 16, 1024);
         // Whatever is ready goes first: the O product of the oldest step whose S
@@ -411,20 +451,28 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         int s = 0, steps = 0, idle = 0;
         long long since = clock64();
         auto ready = [&](uint32_t b, uint32_t phase) { return __all_sync(~0u, ptx::mbar_test_wait(b, phase & 1u)); };
+        auto landed = [&](uint32_t fill) {       // the tile that begins at this fill
+            return ready(b_full + 8 * (fill % kStages), fill / kStages) &&
+                   (kUnits == 1 || ready(b_full + 8 * ((fill + 1) % kStages), (fill + 1) / kStages));
+        };
         while (!(done && !has_old)) {
             bool moved = false;
             if (has_old) {                       // O^T (+)= V^T P^T
-                const uint32_t vi = 2 * old.step + 1, st = vi % kStages, ob = old.seg & 1u;
-                if (ready(b_p_full, old.step) && ready(b_full + 8 * st, vi / kStages) &&
+                const uint32_t vi = (2 * old.step + 1) * kUnits, ob = old.seg & 1u;
+                if (ready(b_p_full, old.step) && landed(vi) &&
                     (!old.first || old.seg < 2 || ready(b_o_empty + 8 * ob, old.seg / 2 - 1))) {
                     ptx::tc_fence_after();
-                    const uint64_t va = v_desc + st * (L::kTileBytes / 16);
                     if (one) {
 #pragma unroll
-                        for (int k = 0; k < kSteps / 16; ++k)
-                            ptx::mma_f16(tmem + 2 * N + ob * N, va + k * (2 * L::kGroup / 16), p_desc + k * (2048 / 16), id_o,
-                                         old.first && k == 0 ? 0u : 1u);
-                        ptx::mma_commit(b_empty + 8 * st);
+                        for (int u = 0; u < kUnits; ++u) {
+                            const uint32_t st = (vi + u) % kStages;
+                            const uint64_t va = v_desc + st * (L::kTileBytes / 16);
+#pragma unroll
+                            for (int k = 0; k < kSteps / 16; ++k)
+                                ptx::mma_f16(tmem + 2 * N + (ob * kUnits + u) * N, va + k * (2 * L::kGroup / 16),
+                                             p_desc + k * (2048 / 16), id_o, old.first && k == 0 ? 0u : 1u);
+                            ptx::mma_commit(b_empty + 8 * st);
+                        }
                         ptx::mma_commit(b_pv);
                     }
                     __syncwarp();
@@ -447,21 +495,26 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 moved = true;
             }
             if (in_seg && !has_young) {          // S^T = K Q^T
-                const uint32_t qb = si % L::kQBufs, ki = 2 * step, st = ki % kStages, sb = step & 1u;
+                const uint32_t qb = si % L::kQBufs, ki = 2 * step * kUnits, sb = step & 1u;
                 if (!q_ready && ready(b_q_full + 8 * qb, si / L::kQBufs)) {
                     ptx::fence_proxy_async_smem();       // the Q tile came by the generic proxy
                     q_ready = true;
                 }
-                if (q_ready && ready(b_full + 8 * st, ki / kStages) && (step < 2 || ready(b_s_empty + 8 * sb, step / 2 - 1))) {
+                if (q_ready && landed(ki) && (step < 2 || ready(b_s_empty + 8 * sb, step / 2 - 1))) {
                     ptx::tc_fence_after();
-                    const uint64_t ka = k_desc + st * (L::kTileBytes / 16), qa = q_desc + qb * (L::kQBytes / 16);
                     if (one) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            ptx::mma_f16(tmem + sb * N, ka + (k / 4) * (1024 / 16) + (k % 4) * 2,
-                                         qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, k ? 1u : 0u);
+                        for (int u = 0; u < kUnits; ++u) {
+                            const uint32_t st = (ki + u) % kStages;
+                            const uint64_t ka = k_desc + st * (L::kTileBytes / 16);
+                            const uint64_t qa = q_desc + qb * (L::kQBytes / 16) + u * (2 * N * 128 / 16);
+#pragma unroll
+                            for (int k = 0; k < L::kUnit / 16; ++k)
+                                ptx::mma_f16(tmem + sb * N, ka + (k / 4) * (L::kHalf / 16) + (k % 4) * 2,
+                                             qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, u || k ? 1u : 0u);
+                            ptx::mma_commit(b_empty + 8 * st);
+                        }
                         ptx::mma_commit(b_s_full + 8 * sb);
-                        ptx::mma_commit(b_empty + 8 * st);
                         if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
                     }
                     __syncwarp();
@@ -489,7 +542,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         __syncwarp();
     } else {
         // ------------------------------------------------------------- softmax
-        const int half = warp >> 2, quarter = warp & 3, row = tid & 127;
+        const int group = warp >> 2, quarter = warp & 3, row = tid & 127;
         const uint32_t lanes = (uint32_t)quarter << 21;             // TMEM lane offset of this warp
         const float scale2 = p.scale * kLog2e;
         const int my_box = row / bx;
@@ -498,7 +551,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         // columns in chunks of CH; with more than one, scores are read from tensor
         // memory twice and the references from shared memory
         constexpr int CH = HC > 16 ? 16 : HC, NCH = HC / CH;
-        float* s_neg = reinterpret_cast<float*>(gbase + L::kNeg) + half * HC;
+        float* s_neg = reinterpret_cast<float*>(gbase + L::kNeg) + group * HC;
         uint32_t step = 0;
         bool ok = true;
         // A segment's rows are written after the first step of the next segment
@@ -509,29 +562,29 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         for (uint32_t si = 0;; ++si) {
             const int slot = si % kSegs;
             ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
-            if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
+            if (ptx::bar_red_or(1 + group, 128, !ok)) { ok = false; break; }
             const Seg& sg = const_cast<Seg&>(s_seg[slot]);
             struct { int n, len, r0, pos0, pos1, steps; } d = {sg.n, sg.len, sg.r0, sg.pos0, sg.pos1, sg.steps};
             const bool none = d.steps < 0;                         // no more segments
             if (none && !pend) break;
-            const uint32_t o_at = tmem + lanes + 2 * N + (si & 1u) * N + half * HC;
+            const uint32_t o_at = tmem + lanes + 2 * N + (si & 1u) * (kUnits * N) + group * HC;
             const int first_new = d.len - d.n;                     // position of the block's first token
-            // lane c: the last position that column c of this half sees
-            const int my_last = first_new + p.by_group(d.r0 + half * HC + (lane & (HC - 1)));
+            // lane c: the last position that column c of this group sees
+            const int my_last = first_new + p.by_group(d.r0 + group * HC + (lane & (HC - 1)));
             float neg[CH], l[HC];                                  // minus the reference, this thread's sum of the weights
 #pragma unroll
             for (int c = 0; c < CH; ++c) neg[c] = 0.f;
 #pragma unroll
             for (int c = 0; c < HC; ++c) l[c] = 0.f;
             float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
-            bool unset = true;                                     // a column of the half has no reference yet
+            bool unset = true;                                     // a column of the group has no reference yet
             bool stop = false;
             for (int s = 0; s < d.steps || s == 0; ++s) {
                 if (!none) {
                 const int pos0 = d.pos0 + s * kSteps, pos = pos0 + row, there = d.pos1 - pos0;
                 ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
                 ok = __all_sync(~0u, ok);
-                const uint32_t s_at = tmem + lanes + (step & 1u) * N + half * HC;
+                const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
                 const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
                 // positions beyond the end or in a bad page, and the block's later tokens
                 const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
@@ -576,7 +629,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     }
                 }
                 if (NCH == 1) read_done();
-                const bool move = ptx::bar_red_or(1 + half, 128, unset || high > kSlack || !ok);
+                const bool move = ptx::bar_red_or(1 + group, 128, unset || high > kSlack || !ok);
                 // the product before this one is done: P may be overwritten, O rescaled
                 if (step > 0) ok = wait(b_pv, step - 1) && ok;
                 if (move) {                     // the same in every thread of the group
@@ -590,9 +643,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             if (lane == k * CH + c) mine = w;
                         }
                     }
-                    float* mx = reinterpret_cast<float*>(s_max + half * HC);
+                    float* mx = reinterpret_cast<float*>(s_max + group * HC);
                     if (lane < HC) mx[lane * 4 + quarter] = mine;
-                    if (ptx::bar_red_or(1 + half, 128, !ok)) { stop = true; break; }
+                    if (ptx::bar_red_or(1 + group, 128, !ok)) { stop = true; break; }
                     const float4 w4 = reinterpret_cast<const float4*>(mx)[lane & (HC - 1)];
                     const float top = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) * scale2;
                     const float to = fmaxf(my_ref, top);
@@ -602,7 +655,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     // (the next write to s_max comes after another barrier)
                     if (NCH > 1) {
                         if (quarter == 0) s_neg[lane] = to == -INFINITY ? 0.f : -to;
-                        ptx::named_barrier(1 + half, 128);
+                        ptx::named_barrier(1 + group, 128);
                     }
                     if (s > 0) ptx::tc_fence_after();
 #pragma unroll
@@ -617,20 +670,22 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             }
                             l[k * CH + c] *= a[c];
                         }
-                        if (s > 0) {
-                            float o[CH];
-                            tmem_get<CH>(o_at + k * CH, o);
+                        if (s > 0)
 #pragma unroll
-                            for (int c = 0; c < CH; ++c) o[c] *= a[c];
-                            tmem_put<CH>(o_at + k * CH, o);
-                        }
+                            for (int u = 0; u < kUnits; ++u) {
+                                float o[CH];
+                                tmem_get<CH>(o_at + u * N + k * CH, o);
+#pragma unroll
+                                for (int c = 0; c < CH; ++c) o[c] *= a[c];
+                                tmem_put<CH>(o_at + u * N + k * CH, o);
+                            }
                     }
                 }
-                // weights: row `row` of P, columns half * HC ..
+                // weights: row `row` of P, columns group * HC ..
 #pragma unroll
                 for (int k = 0; k < NCH; ++k) {
                     if (NCH > 1) { scores(k); refs(k); }
-                    const int col0 = half * HC + k * CH;
+                    const int col0 = group * HC + k * CH;
                     const uint32_t prow = base + L::kP + (col0 / 64) * (kSteps * 128) + row * 128;
 #pragma unroll
                     for (int c0 = 0; c0 < CH; c0 += 8) {
@@ -651,17 +706,17 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     // product would turn 0 * NaN into NaN.  Of the block's later
                     // tokens, whose values some rows use, the non-finite entries
                     // are cleared and added again below to the rows that see them.
-                    const uint32_t vi = 2 * step + 1;
-                    ok = wait(b_full + 8 * (vi % kStages), vi / kStages) && ok;
+                    const uint32_t vi = (2 * step + 1) * kUnits;
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) ok = wait(b_full + 8 * ((vi + u) % kStages), (vi + u) / kStages) && ok;
                     const bool later = !gone && pos > first_new;
                     if (gone || later) {
-                        uint4* v = reinterpret_cast<uint4*>(gbase + L::kRing + (vi % kStages) * L::kTileBytes + (row >> 3) * L::kGroup) + (row & 7) * 8;
-                        constexpr int kHalves = D / 64;
                         // the two halves of the softmax warps share a row's chunks,
                         // each row begins at another one (other banks)
 #pragma unroll
-                        for (int c = half; c < 8 * kHalves; c += kParts) {
-                            uint4* at = v + (c / 8) * 64 + ((c + row) & 7);
+                        for (int c = group; c < D / 8; c += kParts) {
+                            uint4* at = reinterpret_cast<uint4*>(gbase + L::kRing + ((vi + c / 16) % kStages) * L::kTileBytes +
+                                                                 (row >> 3) * L::kGroup + (c / 8 % 2) * L::kHalf) + (row & 7) * 8 + ((c + row) & 7);
                             if (gone) *at = make_uint4(0u, 0u, 0u, 0u);
                             else {
                                 const uint4 y = *at;
@@ -685,16 +740,17 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 ok = __all_sync(~0u, ok);
                 const uint32_t pi = si - 1;
                 const Seg& e = const_cast<Seg&>(s_seg[pi % kSegs]);
-                const int e_row = half * HC + (lane & (HC - 1)), e_tok = p.by_group(e.r0 + e_row), dim = row;
+                const int e_row = group * HC + (lane & (HC - 1)), e_tok = p.by_group(e.r0 + e_row);
                 const int e_at = (e.q0 + e_tok) * p.Hq + e.h * p.G + (e.r0 + e_row - e_tok * p.G);   // below N * Hq < 2^31
-                const int cols = min(HC, e.rows - half * HC);
+                const int cols = min(HC, e.rows - group * HC);
                 const int part_slot = e.slot, e_new = e.len - e.n;
                 const float e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
                 ptx::tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < NCH; ++k) {
+                for (int i = 0; i < NCH * kUnits; ++i) {
+                    const int k = i % NCH, u = i / NCH, dim = u * 128 + row;
                     float o[CH];
-                    if (ok) tmem_get<CH>(tmem + lanes + 2 * N + (pi & 1u) * N + half * HC + k * CH, o);
+                    if (ok) tmem_get<CH>(tmem + lanes + 2 * N + ((pi & 1u) * kUnits + u) * N + group * HC + k * CH, o);
                     else {
 #pragma unroll
                         for (int c = 0; c < CH; ++c) o[c] = 0.f;
@@ -705,9 +761,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             const int pg = p.by_page(pos), page = p.table[(size_t)e.b * p.width + pg];
                             if (page < 0 || page >= p.pages) continue;
                             float v = 0.f;
-                            if (dim < D)
+                            if (dim < hd)
                                 v = to_f32(static_cast<const uint16_t*>(p.v)[page * p.page_stride +
-                                           ((long long)e.h * p.page_size + (pos - pg * p.page_size)) * D + dim]);
+                                           ((long long)e.h * p.page_size + (pos - pg * p.page_size)) * hd + dim]);
                             const bool odd = !(fabsf(v) < INFINITY);
 #pragma unroll
                             for (int c = 0; c < CH; ++c) {
@@ -722,13 +778,13 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                         for (int c = 0; c < CH; ++c) {
                             const float inv = __shfl_sync(~0u, e_inv, k * CH + c);
                             const int at = __shfl_sync(~0u, e_at, k * CH + c);
-                            if (k * CH + c < cols && dim < D) out[(size_t)at * D] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
+                            if (k * CH + c < cols && dim < hd) out[(size_t)at * hd] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
                         }
                     } else {
-                        float* part = p.part + ((size_t)part_slot * p.row_tile + half * HC + k * CH) * D + dim;
+                        float* part = p.part + ((size_t)part_slot * p.row_tile + group * HC + k * CH) * hd + dim;
 #pragma unroll
                         for (int c = 0; c < CH; ++c)
-                            if (k * CH + c < cols && dim < D) part[c * D] = o[c];
+                            if (k * CH + c < cols && dim < hd) part[c * hd] = o[c];
                     }
                 }
                 ptx::tc_fence_before();
@@ -736,7 +792,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (pi & 1u));
                 if (quarter == 0 && lane < cols) {
                     if (part_slot >= 0) {
-                        float2* stats = reinterpret_cast<float2*>(p.part + (size_t)2 * p.ctas * p.row_tile * D);
+                        float2* stats = reinterpret_cast<float2*>(p.part + (size_t)2 * p.ctas * p.row_tile * hd);
                         stats[(size_t)part_slot * p.row_tile + e_row] = make_float2(pend_ref, pend_sum);
                     } else if (p.lse) p.lse[e_at] = pend_sum != 0.f ? pend_ref * kLn2 + logf(pend_sum) : -INFINITY;
                 }
@@ -747,7 +803,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (none) break;
             // column sums: after the exchanges of 16, 8, .. lanes lane c holds
             // column c % HC of this warp's positions, then the 4 warps' are added
-            float* sm = reinterpret_cast<float*>(s_sum + half * HC);
+            float* sm = reinterpret_cast<float*>(s_sum + group * HC);
             {
 #pragma unroll
                 for (int w = HC / 2; w; w >>= 1) {
@@ -763,7 +819,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 for (int w = HC; w < 32; w <<= 1) l[0] += __shfl_xor_sync(~0u, l[0], w);
             }
             if (lane < HC) sm[lane * 4 + quarter] = l[0];
-            if (ptx::bar_red_or(1 + half, 128, !ok)) { ok = false; break; }
+            if (ptx::bar_red_or(1 + group, 128, !ok)) { ok = false; break; }
             const float4 s4 = reinterpret_cast<const float4*>(sm)[lane & (HC - 1)];
             pend = true;
             pend_ref = my_ref;
@@ -777,7 +833,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (p.tile_off[b + 1] > p.tile_off[b]) continue;
             int q0 = p.q_off[b], n = p.q_off[b + 1] - q0;
             n = q0 < 0 ? 0 : max(0, min(n, min(p.max_new, p.N - q0)));
-            for (int i = tid; i < n * p.Hq * D; i += kSoftWarps * 32) static_cast<uint16_t*>(p.out)[(size_t)q0 * p.Hq * D + i] = 0;
+            for (int i = tid; i < n * p.Hq * hd; i += kSoftWarps * 32) static_cast<uint16_t*>(p.out)[(size_t)q0 * p.Hq * hd + i] = 0;
             if (p.lse)
                 for (int i = tid; i < n * p.Hq; i += kSoftWarps * 32) p.lse[(size_t)q0 * p.Hq + i] = -INFINITY;
         }
@@ -785,33 +841,48 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 4 * N);
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, L::kTmem);
 }
 
-template <int N, int D>
+template <int N, int D, bool kApart>
 cudaError_t launch(const AttnParams& p, cudaStream_t s) {
+    using L = Smem<N, D, kApart>;
     auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encoder());
     if (!enc) return cudaErrorNotSupported;
     int bx = 64;                                 // positions of a box: a power of two that divides a page
     while (p.page_size % bx) bx >>= 1;
-    // a cache as [page and head][group of 8 positions][half of the head][position][64 entries]
-    const long long per_head = (long long)p.page_size * D;
+    const long long per_head = (long long)p.page_size * p.D;
     const int page_heads = (int)(p.page_stride / per_head);
+    const cuuint64_t heads = (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv, row = (cuuint64_t)p.D * 2, page = (cuuint64_t)per_head * 2;
     CUtensorMap maps[2];
-    const cuuint64_t dims[5] = {64, 8, D / 64, (cuuint64_t)p.page_size / 8, (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv};
-    const cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16, (cuuint64_t)per_head * 2};
-    const cuuint32_t box[5] = {64, 8, D / 64, (cuuint32_t)bx / 8, 1};
+    // a cache as [page and head][group of 8 positions][64-entry half][position][64 entries], or
+    // [page and head][position][entry], what lies beyond the last entry read as zeros
+    const cuuint64_t dims5[5] = {64, 8, (cuuint64_t)p.D / 64, (cuuint64_t)p.page_size / 8, heads}, strides5[4] = {row, 128, 8 * row, page};
+    const cuuint32_t box5[5] = {64, 8, L::kUnit / 64, (cuuint32_t)bx / 8, 1};
+    const cuuint64_t dims3[3] = {(cuuint64_t)p.D, (cuuint64_t)p.page_size, heads}, strides3[2] = {row, page};
+    const cuuint32_t box3[3] = {64, (cuuint32_t)bx, 1};
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < 2; ++i)
-        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(i ? p.v : p.k), dims, strides, box, es,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kApart ? 3 : 5, const_cast<void*>(i ? p.v : p.k), kApart ? dims3 : dims5,
+                kApart ? strides3 : strides5, kApart ? box3 : box5, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
-    const size_t smem = Smem<N, D>::kTotal + 1024;
-    static_assert(Smem<N, D>::kTotal + 1024 <= 232448, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = L::kTotal + 1024;
+    static_assert(L::kTotal + 1024 <= 232448 && L::kCols <= 512, "shared and tensor memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D, kApart>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_mma_kernel<N, D>, dim3(p.ctas), dim3(Roles<N, D>::kWarps * 32), smem, s, p, maps[0], maps[1], bx, page_heads);
+    return launch_dependent(attn_mma_kernel<N, D, kApart>, dim3(p.ctas), dim3(Roles<N, D>::kWarps * 32), smem, s, p, maps[0], maps[1], bx, page_heads);
+}
+
+template <int D, bool kApart>
+cudaError_t launch_head(const AttnParams& p, cudaStream_t s) {
+    switch (p.row_tile) {
+        case 16: return launch<16, D, kApart>(p, s);
+        case 32: return launch<32, D, kApart>(p, s);
+        case 64: return launch<64, D, kApart>(p, s);
+    }
+    if constexpr (D <= 128) return launch<128, D, kApart>(p, s);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -819,23 +890,15 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
 bool attn_mma_supported(const AttnParams& p) {
     // pages a whole number of heads apart, all of them within a tensor map's last dimension
     const long long per_head = (long long)p.page_size * p.D;
-    return p.bf16 && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 &&
+    return p.bf16 && (p.D <= 128 || p.D % 64 == 0) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 &&
            p.page_stride / per_head < (1LL << 31) && p.pages * (p.page_stride / per_head) < (1LL << 31) &&
            tma_encoder() != nullptr;
 }
 
-template <int D>
-static cudaError_t launch_head(const AttnParams& p, cudaStream_t s) {
-    switch (p.row_tile) {
-        case 16: return launch<16, D>(p, s);
-        case 32: return launch<32, D>(p, s);
-        case 64: return launch<64, D>(p, s);
-        default: return launch<128, D>(p, s);
-    }
-}
-
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s) {
-    return p.D == 64 ? launch_head<64>(p, s) : launch_head<128>(p, s);
+    if (p.D > 128) return launch_head<256, false>(p, s);
+    if (p.D == 128) return launch_head<128, false>(p, s);
+    return p.D == 64 ? launch_head<64, false>(p, s) : launch_head<128, true>(p, s);
 }
 
 }  // namespace dspark

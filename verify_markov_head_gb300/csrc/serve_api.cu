@@ -136,13 +136,16 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     // tiles the block tables can hold: few of them, fewer rows at a time.  On
     // CUDA cores where SMs would be idle otherwise; 128 rows in two tiles of 64 below
     // 32 tiles an SM (8 requests of 8192 positions, 2 heads: 34 us, at once 37;
-    // 64 requests, 8 heads: 402 us, at once 253, the cache read once)
+    // 64 requests, 8 heads: 402 us, at once 249, the cache read once) and for
+    // heads above 128, whose O^T of 128 columns tensor memory does not hold
     const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
-    if (mma && p.row_tile == 128 && tiles < 32LL * num_sms()) p.row_tile = 64;
+    if (mma && p.row_tile == 128 && (head_dim > 128 || tiles < 32LL * num_sms())) p.row_tile = 64;
     if (!mma && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
     p.ctas = num_sms() < kMaxAttnCtas ? num_sms() : kMaxAttnCtas;      // one resident CTA per SM
-    p.pad = mma ? (head_dim == 64 ? 6 : 3) : 1;
+    // (tensor cores: 64 requests of 64 rows, head size 128: 3 places 203 us, 4 196; 256 of 16-300
+    // positions 72, 68; head size 96, the same: 4 places 73.4, 6 72.2, 32 rows 152.7 with 3, 150.5 with 6)
+    p.pad = mma ? (head_dim < 128 ? 6 : 4) : 1;
     p.split = reinterpret_cast<AttnSplitRow*>(static_cast<char*>(ws) + kHead);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas));
     p.status = static_cast<uint32_t*>(ws);
