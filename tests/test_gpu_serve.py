@@ -237,11 +237,11 @@ def test_attention_with_128_rows_at_once(vm, lens, news, Hq, Hkv, D, P):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("P,group,new,wide", [(8, 1, 8, 0), (16, 4, 4, 0), (64, 4, 8, 0), (128, 8, 1, 0), (32, 12, 8, 400000), (5, 3, 8, 0)])
+@pytest.mark.parametrize("P,group,new,wide", [(8, 1, 8, 0), (16, 4, 4, 0), (64, 4, 8, 0), (128, 8, 1, 0), (32, 12, 8, 400000), (5, 3, 8, 0), (1, 2, 4, 0), (12, 8, 8, 0)])
 @pytest.mark.parametrize("D", [16, 40, 80, 96, 112, 120, 192, 256, 136])
 def test_attention_of_other_head_sizes(vm, D, P, group, new, wide):
-    """Heads that do not fill a tile's row, or fill two; 8 to 96 rows of a key
-    head (wide: 96 at once); lengths about the tiles' ends; q and cache with
+    """Heads that do not fill a tile's row, or fill two; pages that are no
+    multiple of 8 positions; 8 to 96 rows of a key head (wide: 96 at once); lengths about the tiles' ends; q and cache with
     gaps between tokens and pages; positions beyond the lengths hold NaN."""
     rng = np.random.default_rng(D + P)
     lens = [300, 1, 0, 128, 129, 64, 700]
@@ -281,13 +281,12 @@ def _vary_block_values(a, b, P, bad):
 
 
 @pytest.mark.parametrize("dtype,Hq,wide", [(torch.bfloat16, 8, 0), (torch.float32, 8, 0), (torch.bfloat16, 32, 30000)])
-@pytest.mark.parametrize("D", [128, 96, 256])
+@pytest.mark.parametrize("D,P", [(128, 16), (96, 16), (256, 16), (128, 1), (256, 12)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, D, dtype, Hq, wide):
+def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, D, P, dtype, Hq, wide):
     """A draft whose value is not finite: the rows before it, which do not see
     it, are as they were; its own row is not finite where the value is not."""
     rng = np.random.default_rng(4)
-    P = 16
     a = _attention_inputs(rng, [70, 64, 8], [8, 5, 8], Hq, 2, D, P, dtype, wide=wide)
     clean, _, _ = _attend(vm, a, 8)
     for b in range(3):
@@ -333,9 +332,10 @@ def test_attention_on_another_stream_and_interleaved_caches(vm):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
-def test_attention_reports_bad_pages_and_lengths(vm):
+@pytest.mark.parametrize("P", [16, 4])
+def test_attention_reports_bad_pages_and_lengths(vm, P):
     rng = np.random.default_rng(13)
-    a = _attention_inputs(rng, [100, 50], [2, 2], 4, 2, 64, 16, torch.bfloat16)
+    a = _attention_inputs(rng, [100, 50], [2, 2], 4, 2, 64, P, torch.bfloat16)
     out, _, ws = _attend(vm, a, 2)
     hurt = dict(a, table=a["table"].clone())
     hurt["table"][1, 1] = a["k"].shape[0]                   # a page that does not exist

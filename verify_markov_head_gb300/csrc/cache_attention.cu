@@ -52,23 +52,20 @@ __device__ __forceinline__ void store_out<uint16_t>(uint16_t* out, float x) {
 }
 
 // Requests that own no cache position have no tile: their rows are zero.
-template <typename T>
 __device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int ctas) {
     for (int b = cta; b < p.B; b += ctas) {
         if (p.tile_off[b + 1] > p.tile_off[b]) continue;
         const RowMap r(p, b);
         const size_t o0 = (size_t)r.q0 * p.Hq * p.D, n = (size_t)r.n * p.Hq * p.D;
-        for (size_t i = threadIdx.x; i < n; i += blockDim.x) store_out(static_cast<T*>(p.out) + o0 + i, 0.f);
+        for (size_t i = threadIdx.x; i < n; i += blockDim.x) static_cast<float*>(p.out)[o0 + i] = 0.f;
         if (p.lse)
             for (int i = threadIdx.x; i < r.n * p.Hq; i += blockDim.x) p.lse[(size_t)r.q0 * p.Hq + i] = -INFINITY;
     }
 }
 
-// --------------------------------------------------- on CUDA cores, any type
-// fp32 caches, and bf16 ones with a head size or a page size that the
-// tensor-core kernel does not take.  fp32 arithmetic throughout, so the FMA
-// rate and the shared-memory reads that feed it bound a block's many rows, HBM
-// a single row.  256 threads, MR = 8 or 32 rows, TT positions at a time: two
+// --------------------------------------------------- on CUDA cores: fp32
+// fp32 arithmetic throughout, so the FMA rate and the shared-memory reads that
+// feed it bound a block's many rows, HBM a single row.  256 threads, MR = 8 or 32 rows, TT positions at a time: two
 // stages of keys and values by cp.async, 16-byte chunks swizzled so that eight
 // positions' chunks lie in different banks.
 // Measured on one GB300: 16 requests of up to 8192 positions, 8 fp32 heads of
@@ -83,7 +80,7 @@ __device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int cta
 //            positions; the TS parts are added at the segment's end.
 constexpr int kSimtThreads = 256;
 
-template <typename T, int MR, int TT>
+template <int MR, int TT>
 struct Simt {
     static constexpr int TPT = MR == 32 ? 4 : 1;            // positions of a thread
     static constexpr int NR = MR == 32 ? 8 : 2;             // rows of a thread after the sum over the quarters
@@ -93,37 +90,17 @@ struct Simt {
     static constexpr int TS = 8 / kRowGroups;
     static constexpr int ND = TT == 64 ? 4 : 8;             // dimensions of a thread: 4 lane .., and 128 + 4 lane ..
     static size_t bytes(int D) {
-        return (size_t)4 * TT * D * sizeof(T) + sizeof(float) * ((size_t)MR * D + TT * MR + (size_t)(TS - 1) * MR * D);
+        return (size_t)4 * TT * D * sizeof(float) + sizeof(float) * ((size_t)MR * D + TT * MR + (size_t)(TS - 1) * MR * D);
     }
 };
 
-template <typename T> struct Chunk;      // 16 bytes of a head as fp32
-template <> struct Chunk<float> {
-    static constexpr int E = 4;
-    __device__ __forceinline__ static void get(const uint4& r, float (&x)[4]) {
-        x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
-    }
-};
-template <> struct Chunk<uint16_t> {
-    static constexpr int E = 8;
-    __device__ __forceinline__ static void get(const uint4& r, float (&x)[8]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-};
-
-template <typename T, int MR, int TT>
+template <int MR, int TT>
 __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnParams p) {
-    using S = Simt<T, MR, TT>;
-    using C = Chunk<T>;
-    constexpr int E = C::E, TPT = S::TPT, NR = S::NR, ND = S::ND;
+    using S = Simt<MR, TT>;
+    constexpr int E = 4, TPT = S::TPT, NR = S::NR, ND = S::ND;
     extern __shared__ __align__(16) uint8_t raw[];
     const int D = p.D, chunks = D / E, tile_elems = TT * D;
-    T* ring = reinterpret_cast<T*>(raw);                     // [2 stages][keys, values][TT][D]
+    float* ring = reinterpret_cast<float*>(raw);                     // [2 stages][keys, values][TT][D]
     float* sq = reinterpret_cast<float*>(ring + 4 * tile_elems);   // [MR][D]
     float* sp_ = sq + MR * D;                                // weights [TT][MR]
     float* merge = sp_ + TT * MR;                            // [TS - 1][MR][D]
@@ -132,12 +109,12 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) grid_launch_dependents();   // the join is scheduled now and waits for this grid
     const int cta = blockIdx.x;
-    empty_rows<T>(p, cta, gridDim.x);
+    empty_rows(p, cta, gridDim.x);
     const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
     if (tid == 0) p.split[cta].parts = 0;
     if (cta >= sp.n) return;
-    const T* kc = static_cast<const T*>(p.k);
-    const T* vc = static_cast<const T*>(p.v);
+    const float* kc = static_cast<const float*>(p.k);
+    const float* vc = static_cast<const float*>(p.v);
     const float scale2 = p.scale * kLog2e;
     // scores: position group and quarter of the head
     const int tg = lane & 7, quarter = lane >> 3, rg = warp / S::kTokWarps, tw = warp % S::kTokWarps;
@@ -169,7 +146,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
         auto place = [&](int r, int c) { return r * chunks + ((c | 7) < chunks ? c ^ ((r / TPT) & 7) : c); };
         auto issue = [&](int s) {
             const int st = s & 1;
-            const uint32_t k0 = ptx::smem_addr(ring + 2 * st * tile_elems), v0 = k0 + tile_elems * (uint32_t)sizeof(T);
+            const uint32_t k0 = ptx::smem_addr(ring + 2 * st * tile_elems), v0 = k0 + tile_elems * (uint32_t)sizeof(float);
             for (int i = tid; i < TT * chunks; i += kSimtThreads) {
                 const int r = i / chunks, c = i - r * chunks;
                 const long long base = s_base[st][r];
@@ -187,7 +164,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
             float x = 0.f;
             if (r < rows) {
                 const int rr = r0 + r, tok = p.by_group(rr);
-                x = to_f32(static_cast<const T*>(p.q)[(rm.q0 + tok) * p.q_stride + (size_t)(g.h * p.G + rr - tok * p.G) * D + d]);
+                x = static_cast<const float*>(p.q)[(rm.q0 + tok) * p.q_stride + (size_t)(g.h * p.G + rr - tok * p.G) * D + d];
             }
             sq[i] = x;
         }
@@ -207,7 +184,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
             __syncthreads();                     // the step's tiles are there, the other stage is free
             if (s + 1 < steps) issue(s + 1);
             const long long later = tid < TT && s + 2 < steps ? base_of(s + 2) : -1LL;
-            const uint4* kt = reinterpret_cast<const uint4*>(ring + 2 * st * tile_elems);
+            const float4* kt = reinterpret_cast<const float4*>(ring + 2 * st * tile_elems);
             float z[NR];
             if (scores) {
                 float a[8][TPT];
@@ -216,20 +193,15 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
 #pragma unroll
                     for (int i = 0; i < TPT; ++i) a[r][i] = 0.f;
                 for (int c = quarter; c < chunks; c += 4) {
-                    float k[TPT][E];
+                    float4 k[TPT];
 #pragma unroll
-                    for (int i = 0; i < TPT; ++i) C::get(kt[place(tok0 + i, c)], k[i]);
+                    for (int i = 0; i < TPT; ++i) k[i] = kt[place(tok0 + i, c)];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float4* q4 = reinterpret_cast<const float4*>(sq + (rg * 8 + r) * D + c * E);
+                        const float4 q = *reinterpret_cast<const float4*>(sq + (rg * 8 + r) * D + c * E);
 #pragma unroll
-                        for (int h = 0; h < E / 4; ++h) {
-                            const float4 q = q4[h];
-#pragma unroll
-                            for (int i = 0; i < TPT; ++i)
-                                a[r][i] = fmaf(q.x, k[i][4 * h], fmaf(q.y, k[i][4 * h + 1],
-                                          fmaf(q.z, k[i][4 * h + 2], fmaf(q.w, k[i][4 * h + 3], a[r][i]))));
-                        }
+                        for (int i = 0; i < TPT; ++i)
+                            a[r][i] = fmaf(q.x, k[i].x, fmaf(q.y, k[i].y, fmaf(q.z, k[i].z, fmaf(q.w, k[i].w, a[r][i]))));
                     }
                 }
                 // the sum over the quarters, split on the way
@@ -285,7 +257,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
                 }
             }
             __syncthreads();
-            const T* vt = ring + (2 * st + 1) * tile_elems;
+            const float* vt = ring + (2 * st + 1) * tile_elems;
             // a hidden position adds nothing, whatever its value holds
             const bool guard = pos0 + TT > first_new + 1;
 #pragma unroll
@@ -305,7 +277,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
                 for (int hf = 0; hf < ND / 4; ++hf) {
                     const int d = 4 * lane + 128 * hf;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (d < D) y = Vec4<T>::load(vt + place(tk, d / E) * E + d % E);
+                    if (d < D) y = *reinterpret_cast<const float4*>(vt + place(tk, d / E) * E);
                     v[4 * hf] = y.x; v[4 * hf + 1] = y.y; v[4 * hf + 2] = y.z; v[4 * hf + 3] = y.w;
                 }
                 if (guard) {
@@ -366,7 +338,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
                 float x = acc[r][e];
 #pragma unroll
                 for (int w = 0; w < S::TS - 1; ++w) x += merge[(w * MR + row) * D + d];
-                if (whole) store_out(static_cast<T*>(p.out) + at * D + d, x * inv);
+                if (whole) static_cast<float*>(p.out)[at * D + d] = x * inv;
                 else p.part[((size_t)slot * p.row_tile + row) * D + d] = x;
             }
             if (lane == 0) {
@@ -454,18 +426,18 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     if (lane == 0 && p.lse) p.lse[o0] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
-template <typename T, int MR, int TT>
+template <int MR, int TT>
 cudaError_t launch_simt_tile(const AttnParams& p, cudaStream_t s) {
-    const size_t smem = Simt<T, MR, TT>::bytes(p.D);
-    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, MR, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = Simt<MR, TT>::bytes(p.D);
+    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<MR, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attn_simt_kernel<T, MR, TT><<<p.ctas, kSimtThreads, smem, s>>>(p);
+    attn_simt_kernel<MR, TT><<<p.ctas, kSimtThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
-template <typename T, int MR>
+template <int MR>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
     // 64 positions at a time as far as shared memory holds two stages of them
-    return p.D <= 128 ? launch_simt_tile<T, MR, 64>(p, s) : launch_simt_tile<T, MR, 32>(p, s);
+    return p.D <= 128 ? launch_simt_tile<MR, 64>(p, s) : launch_simt_tile<MR, 32>(p, s);
 }
 
 template <typename T>
@@ -477,9 +449,8 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
 
 cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s) {
     cudaError_t e;
-    if (attn_mma_supported(p)) e = launch_attn_mma(p, s);
-    else if (p.row_tile == 8) e = p.bf16 ? launch_simt<uint16_t, 8>(p, s) : launch_simt<float, 8>(p, s);
-    else e = p.bf16 ? launch_simt<uint16_t, 32>(p, s) : launch_simt<float, 32>(p, s);
+    if (p.bf16) e = launch_attn_mma(p, s);
+    else e = p.row_tile == 8 ? launch_simt<8>(p, s) : launch_simt<32>(p, s);
     if (e != cudaSuccess) return e;
     return p.bf16 ? launch_join<uint16_t>(p, s) : launch_join<float>(p, s);
 }

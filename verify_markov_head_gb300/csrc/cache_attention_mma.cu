@@ -1,7 +1,6 @@
 // cache_attention_mma.cu -- attention over the paged cache on the tensor
-// cores: bf16, head sizes up to 128, 192 and 256, pages of a multiple of 8
-// positions (the rest runs on CUDA cores, cache_attention.cu, where the
-// formulas stand).
+// cores: bf16 (fp32 runs on CUDA cores, cache_attention.cu, where the formulas
+// stand).
 //
 // Both products are taken transposed, so that 128 cache positions fill the
 // 128 lanes of the accumulator and the few query rows of a key-value head are
@@ -14,16 +13,18 @@
 //
 // Head sizes: a row of a tile has D = 64, 128 or 256 entries.  Sizes below 128
 // other than 64 come in two boxes of 64 entries, what lies beyond the head
-// read as zeros; sizes of 192 and 256 in two stages of 128 entries, whose
-// products go to the same S^T and to two O^T.  Against the CUDA cores, 64
-// requests of 32 rows: head size 96 150 us (1900), 192 286 (3230), 256 348
-// (3460).
+// read as zeros; sizes above 128 in two stages of 128 entries, whose products
+// go to the same S^T and to two O^T.  Pages that are no boxes (not a multiple
+// of 8 positions, not a whole number of heads apart, or heads above 128 that
+// are no multiple of 64) are copied row by row, by cp.async of four warps.
+// 64 requests of 32 rows, and on CUDA cores before: head size 96 151 us (1900),
+// 192 283 (3230), 256 349 (3460); 128 in pages of 1 position 207 (1869).
 //
-// Roles (12 or 20 warps, one CTA per SM, a ring of 5 stages of 32 KB, 4 with 128 columns):
+// Roles (12 or 20 warps, 2 more row by row, one CTA per SM, a ring of 5 stages of 32 KB, 4 with 128 columns):
 //   first 8 or 16    softmax, 2 or 4 groups of 4 warps, each with its share of the
 //                    columns: thread = position; weights to shared memory
-//   then two         TMA producers of the keys and of the values (lane = box of a
-//                    page: a multiple of 8 positions, up to 64)
+//   then two         producers of the keys and of the values (lane = box of a page:
+//                    a multiple of 8 positions, up to 64); four, row by row
 //   one              MMA issuer: whichever of the two products is ready
 //   one              walks the CTA's segments: descriptors and Q tiles
 // The reference of a column's weights, 2^(s - ref), moves only when a score
@@ -65,16 +66,23 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSteps = 128;              // positions per step (one tile of K and one of V)
+// How a tile comes to shared memory: a box of a page with whole rows; two boxes
+// of 64 entries, where the head does not fill the row; row by row, where pages
+// are no boxes.
+enum class Copy { kBoxes, kHalves, kRows };
+
 // The columns are shared by kParts groups of 4 softmax warps: 8, 16 or (of 128
 // columns) 32 a thread.  64 columns over two groups, 32 a thread in registers,
 // took 209 us for 64 requests of 64 rows, over four 195; 32 columns over four 70
 // us for 256 requests of 16-300 positions, over two 82, and the same for long
 // ones (head size 64: two, 111 us against 114).
-template <int N, int D>
+template <int N, int D, Copy kCopy>
 struct Roles {
     static constexpr int kParts = N >= 64 || (N == 32 && D == 128) ? 4 : 2, kSoftWarps = 4 * kParts;
     static constexpr int kKeyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kSegWarp = kSoftWarps + 2, kValWarp = kSoftWarps + 3;
-    static constexpr int kWarps = kSoftWarps + 4;
+    // row by row two warps copy keys and two values, half of a tile's positions each
+    // (one of each: 64 requests of 32 rows in pages of 1 position 239 us, 8 rows 207)
+    static constexpr int kWarps = kSoftWarps + (kCopy == Copy::kRows ? 6 : 4), kProducers = kWarps - kSoftWarps - 2;
 };
 constexpr int kSegs = 8;                 // segment descriptors in flight
 constexpr int kBadRing = 8;              // steps the producer may be ahead of the softmax, and more
@@ -91,17 +99,15 @@ struct Seg {
 };
 
 // D: entries of a tile's row, the head size p.D rounded up to 64, 128 or 256.
-// kApart: rows that the head does not fill (p.D is no multiple of 64, D is 128),
-// copied 64 entries at a time.
-template <int N, int D, bool kApart>
+template <int N, int D, Copy kCopy>
 struct Smem {
     static constexpr int kUnits = D == 256 ? 2 : 1;               // a tile in parts of 128 entries, each a stage
     static constexpr int kUnit = D / kUnits;                      // entries of a part
     static constexpr int kTileBytes = kSteps * kUnit * 2;         // a stage
     // a stage is [8 positions][64-entry half][position][64] as one box brings it,
     // or [half][position][64] where the halves come apart
-    static constexpr int kGroup = kApart ? 1024 : 8 * kUnit * 2;  // from 8 positions to the next 8
-    static constexpr int kHalf = kApart ? kSteps * 128 : kUnit == 128 ? 1024 : 0;
+    static constexpr int kGroup = kCopy == Copy::kHalves ? 1024 : 8 * kUnit * 2;  // from 8 positions to the next 8
+    static constexpr int kHalf = kCopy == Copy::kHalves ? kSteps * 128 : kUnit == 128 ? 1024 : 0;
     static constexpr int kStages = (N == 128 ? 4 : 5) * 128 / kUnit;
     static constexpr int kQBytes = N * D * 2;
     static constexpr int kQBufs = N * D <= 32 * 128 ? 4 : N == 128 || N * D == 64 * 256 ? 1 : 2;      // Q tiles: segments may be a step long
@@ -118,7 +124,7 @@ struct Smem {
     static constexpr int kBar = kSeg + kSegs * (int)sizeof(Seg);
     static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 3;
     static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, non-finite flag, -, the producers' counts, bad boxes
-    static constexpr int kTotal = kFlags + 24 + 4 * kBadRing;
+    static constexpr int kTotal = kFlags + 24 + 16 * kBadRing;
 };
 
 // The box at half `h` and group `g` of 8 positions of (page, head) `z`.
@@ -196,23 +202,24 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
     return w;
 }
 
-template <int N, int D, bool kApart>
-__global__ void __launch_bounds__(Roles<N, D>::kWarps * 32, 1)
+template <int N, int D, Copy kCopy>
+__global__ void __launch_bounds__(Roles<N, D, kCopy>::kWarps * 32, 1)
 attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const int bx, const int page_heads) {
-    using L = Smem<N, D, kApart>;
-    using R = Roles<N, D>;
+    using L = Smem<N, D, kCopy>;
+    using R = Roles<N, D, kCopy>;
     constexpr int kParts = R::kParts, kSoftWarps = R::kSoftWarps, kKeyWarp = R::kKeyWarp, kMmaWarp = R::kMmaWarp, kSegWarp = R::kSegWarp, kValWarp = R::kValWarp;
     constexpr int HC = N / kParts;           // columns of a softmax group
     constexpr int kStages = L::kStages, kUnits = L::kUnits;
-    const int hd = kApart || kUnits > 1 ? p.D : D;           // the head size
+    constexpr bool kExact = kCopy == Copy::kBoxes && kUnits == 1;     // the head fills the row
+    const int hd = kExact ? D : p.D;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile uint32_t* s_flags = reinterpret_cast<volatile uint32_t*>(gbase + L::kFlags);   // [0] TMEM, [1] abort, [2] fix
-    volatile uint32_t* s_bad = s_flags + 6;     // [kBadRing] boxes of a step whose page is out of range
+    volatile uint32_t* s_bad = s_flags + 6;     // [kBadRing][4] boxes (one word), or positions, of a step whose page is out of range
     volatile Seg* s_seg = reinterpret_cast<volatile Seg*>(gbase + L::kSeg);
     volatile uint32_t* abort_flag = s_flags + 1;
     uint32_t bar = base + L::kBar;
@@ -224,8 +231,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
 
     if (tid == 0) {
         grid_launch_dependents();       // the join is scheduled now and waits for this grid
-        for (int i = 0; i < kStages; ++i) { ptx::mbar_init(b_full + 8 * i, 1); ptx::mbar_init(b_empty + 8 * i, 1); }
-        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 3 + kSoftWarps); }
+        for (int i = 0; i < kStages; ++i) { ptx::mbar_init(b_full + 8 * i, kCopy == Copy::kRows ? 2 * 33 : 1); ptx::mbar_init(b_empty + 8 * i, 1); }
+        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 1 + R::kProducers + kSoftWarps); }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(b_s_full + 8 * i, 1); ptx::mbar_init(b_s_empty + 8 * i, kSoftWarps);
             ptx::mbar_init(b_o_empty + 8 * i, kSoftWarps);
@@ -240,8 +247,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         ptx::tmem_alloc(base + L::kFlags, L::kTmem);
         ptx::tmem_relinquish();
     }
-    if (warp == kKeyWarp && lane == 0) ptx::prefetch_tmap(&kmap);
-    if (warp == kValWarp && lane == 0) ptx::prefetch_tmap(&vmap);
+    if (kCopy != Copy::kRows && warp == kKeyWarp && lane == 0) ptx::prefetch_tmap(&kmap);
+    if (kCopy != Copy::kRows && warp == kValWarp && lane == 0) ptx::prefetch_tmap(&vmap);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -258,7 +265,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         // ------------------------------------------------ segments and Q tiles
         const int first_round = attn_first_round(p);
         const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
-        const int cta = blockIdx.x, nbox = kSteps / bx;
+        const int cta = blockIdx.x, nbox = kCopy == Copy::kRows ? 0 : kSteps / bx;
         bool ok = true;
         int t = 0, end = 0;
         AttnSegment g{};
@@ -340,7 +347,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 int r = lane / kChunks, tok = p.by_group(qr0 + r), head = qr0 + r - tok * p.G;
                 const uint16_t* q = static_cast<const uint16_t*>(p.q);
                 const uint16_t* src = q + (q0 + tok) * p.q_stride + (size_t)(qh * p.G + head) * hd + 8 * c;
-                const bool in_head = !kApart && D < 256 ? true : 8 * c < hd;
+                const bool in_head = kExact || 8 * c < hd;
                 const uint32_t qs = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
 #pragma unroll 4
                 for (int i = 0; i < N / kRows; ++i) {
@@ -359,9 +366,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             skip();
         }
         if (lane == 0) p.split[cta] = split;
-    } else if (warp == kKeyWarp || warp == kValWarp) {
+    } else if (warp == kKeyWarp || warp >= kValWarp) {
         // ------------------------------------------------------------ producers
-        const int kv = warp == kValWarp;
+        const int kv = (warp - kKeyWarp) & 1, part = warp > kValWarp;     // (part: row by row, the second half)
         const CUtensorMap* map = kv ? &vmap : &kmap;
         const uint64_t pol = p.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
         const int nbox = kSteps / bx;
@@ -379,6 +386,61 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
             const int32_t* row = p.table + (size_t)d.b * p.width;
+            if constexpr (kCopy == Copy::kRows) {
+                const uint16_t* from = static_cast<const uint16_t*>(kv ? p.v : p.k) + (long long)d.h * p.page_size * hd;
+                constexpr int kChunks = L::kUnit / 8, kAt = 32 / kChunks;      // 16-byte chunks of a row, rows of an instruction
+                const int c = lane % kChunks, sub = lane / kChunks;
+                int pages[2];                    // of this lane's positions 64 part + lane, + 32
+                auto look_up = [&](int pos0) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int pos = pos0 + 64 * part + 32 * i + lane;
+                        pages[i] = pos < d.pos1 ? __ldg(row + p.by_page(pos)) : -1;
+                    }
+                };
+                look_up(d.pos0);
+                for (int s = 0; s < d.steps && ok; ++s, fill += kUnits) {
+                    long long at[2];             // where they lie, -1: nowhere, their rows are zeros
+                    uint32_t bad[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int pos = d.pos0 + s * kSteps + 64 * part + 32 * i + lane;
+                        const bool have = pos < d.pos1 && pages[i] >= 0 && pages[i] < p.pages;
+                        at[i] = have ? pages[i] * p.page_stride + (long long)(pos - p.by_page(pos) * p.page_size) * hd : -1;
+                        bad[i] = __ballot_sync(~0u, pos < d.pos1 && !have);
+                    }
+                    if ((bad[0] | bad[1]) && lane == 0) raise_status(p.status, kBadPage);
+                    look_up(d.pos0 + (s + 1) * kSteps);
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u, ++fill) {
+                        const int stage = fill % kStages;
+                        if (fill >= (uint32_t)kStages) ok = __all_sync(~0u, wait(b_empty + 8 * stage, fill / kStages - 1));
+                        if (!ok) { if (lane == 0) give_up(3); break; }
+                        if (lane == 0) {
+                            if (!kv) {
+                                s_bad[(fill / (2 * kUnits)) % kBadRing * 4 + 2 * part] = bad[0];
+                                s_bad[(fill / (2 * kUnits)) % kBadRing * 4 + 2 * part + 1] = bad[1];
+                            }
+                            ptx::mbar_arrive(b_full + 8 * stage);
+                        }
+                        const uint32_t to = base + L::kRing + stage * L::kTileBytes + 8 * part * L::kGroup + (c / 8) * L::kHalf;
+                        const uint16_t* mine = from + u * 128 + 8 * c;
+                        const bool in_head = u * 128 + 8 * c < hd;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < 32; j += kAt) {
+                                const int r = j + sub;                         // row 64 part + 32 i + r of the tile
+                                const long long o = __shfl_sync(~0u, at[i], r);
+                                const bool have = in_head && o >= 0;
+                                ptx::cp_async_16(to + (4 * i + j / 8) * L::kGroup + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                                                 have ? mine + o : from, have ? 16u : 0u);
+                            }
+                        cp_async_arrive(b_full + 8 * stage);       // when this lane's copies have landed
+                    }
+                }
+                continue;
+            }
             for (int s = 0; s < d.steps; ++s, fill += kUnits) {
                 const int pos = d.pos0 + s * kSteps + lane * bx;
                 const bool want = lane < nbox && pos < d.pos1;
@@ -396,14 +458,14 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     if (!ok) { if (lane == 0) give_up(3); break; }
                     const uint32_t full = b_full + 8 * stage;
                     if (lane == 0) {
-                        if (!kv) s_bad[(fill / (2 * kUnits)) % kBadRing] = bad;
+                        if (!kv) s_bad[(fill / (2 * kUnits)) % kBadRing * 4] = bad;
                         if (boxes) ptx::mbar_arrive_expect_tx(full, boxes * bx * L::kUnit * 2);
                         else ptx::mbar_arrive(full);
                     }
                     __syncwarp();
                     const uint32_t to = base + L::kRing + stage * L::kTileBytes + lane * (bx / 8) * L::kGroup;
                     if (have) {
-                        if constexpr (kApart) {
+                        if constexpr (kCopy == Copy::kHalves) {
                             tma_load_rows(to, map, 0, 8 * group, z, full, pol);
                             tma_load_rows(to + L::kHalf, map, 64, 8 * group, z, full, pol);
                         } else tma_load_box(to, map, 2 * u, group, z, full, pol);
@@ -413,9 +475,12 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             }
         }
         // every copy issued lands before the CTA leaves: the last fill of each stage
-        if (lane == 0) s_flags[4 + kv] = fill;
-        ptx::named_barrier(1 + kParts, 64);
-        if (lane == 0 && !kv) {
+        if constexpr (kCopy == Copy::kRows) ptx::cp_async_wait_all();
+        else {
+            if (lane == 0) s_flags[4 + kv] = fill;
+            ptx::named_barrier(1 + kParts, 64);
+        }
+        if (kCopy != Copy::kRows && lane == 0 && !kv) {
             const uint32_t keys = s_flags[4], vals = s_flags[5];      // stages of tiles 0, 2, .. < keys and of 1, 3, .. < vals
             for (uint32_t i = 0; i < (uint32_t)kStages; ++i) {
                 // the last fill of stage i
@@ -462,6 +527,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 if (ready(b_p_full, old.step) && landed(vi) &&
                     (!old.first || old.seg < 2 || ready(b_o_empty + 8 * ob, old.seg / 2 - 1))) {
                     ptx::tc_fence_after();
+                    if (kCopy == Copy::kRows) ptx::fence_proxy_async_smem();
                     if (one) {
 #pragma unroll
                         for (int u = 0; u < kUnits; ++u) {
@@ -502,6 +568,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 }
                 if (q_ready && landed(ki) && (step < 2 || ready(b_s_empty + 8 * sb, step / 2 - 1))) {
                     ptx::tc_fence_after();
+                    if (kCopy == Copy::kRows) ptx::fence_proxy_async_smem();   // the rows came by the generic proxy
                     if (one) {
 #pragma unroll
                         for (int u = 0; u < kUnits; ++u) {
@@ -545,7 +612,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         const int group = warp >> 2, quarter = warp & 3, row = tid & 127;
         const uint32_t lanes = (uint32_t)quarter << 21;             // TMEM lane offset of this warp
         const float scale2 = p.scale * kLog2e;
-        const int my_box = row / bx;
+        const int my_box = kCopy == Copy::kRows ? lane : row / bx, bad_word = kCopy == Copy::kRows ? quarter : 0;
         float4* s_max = reinterpret_cast<float4*>(gbase + L::kMax);
         float4* s_sum = reinterpret_cast<float4*>(gbase + L::kSum);
         // columns in chunks of CH; with more than one, scores are read from tensor
@@ -585,7 +652,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
                 ok = __all_sync(~0u, ok);
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
-                const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
+                const uint32_t bad = ok ? s_bad[step % kBadRing * 4 + bad_word] : 0u;
                 // positions beyond the end or in a bad page, and the block's later tokens
                 const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
                 const bool gone = row >= there || (bad >> my_box & 1u);
@@ -844,61 +911,67 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, L::kTmem);
 }
 
-template <int N, int D, bool kApart>
+template <int N, int D, Copy kCopy>
 cudaError_t launch(const AttnParams& p, cudaStream_t s) {
-    using L = Smem<N, D, kApart>;
-    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encoder());
-    if (!enc) return cudaErrorNotSupported;
+    using L = Smem<N, D, kCopy>;
+    constexpr bool kHalves = kCopy == Copy::kHalves;
     int bx = 64;                                 // positions of a box: a power of two that divides a page
     while (p.page_size % bx) bx >>= 1;
     const long long per_head = (long long)p.page_size * p.D;
     const int page_heads = (int)(p.page_stride / per_head);
-    const cuuint64_t heads = (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv, row = (cuuint64_t)p.D * 2, page = (cuuint64_t)per_head * 2;
-    CUtensorMap maps[2];
-    // a cache as [page and head][group of 8 positions][64-entry half][position][64 entries], or
-    // [page and head][position][entry], what lies beyond the last entry read as zeros
-    const cuuint64_t dims5[5] = {64, 8, (cuuint64_t)p.D / 64, (cuuint64_t)p.page_size / 8, heads}, strides5[4] = {row, 128, 8 * row, page};
-    const cuuint32_t box5[5] = {64, 8, L::kUnit / 64, (cuuint32_t)bx / 8, 1};
-    const cuuint64_t dims3[3] = {(cuuint64_t)p.D, (cuuint64_t)p.page_size, heads}, strides3[2] = {row, page};
-    const cuuint32_t box3[3] = {64, (cuuint32_t)bx, 1};
-    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    for (int i = 0; i < 2; ++i)
-        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kApart ? 3 : 5, const_cast<void*>(i ? p.v : p.k), kApart ? dims3 : dims5,
-                kApart ? strides3 : strides5, kApart ? box3 : box5, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
+    CUtensorMap maps[2] = {};
+    if constexpr (kCopy != Copy::kRows) {
+        auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encoder());
+        const cuuint64_t heads = (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv, row = (cuuint64_t)p.D * 2, page = (cuuint64_t)per_head * 2;
+        // a cache as [page and head][group of 8 positions][64-entry half][position][64 entries], or
+        // [page and head][position][entry], what lies beyond the last entry read as zeros
+        const cuuint64_t dims5[5] = {64, 8, (cuuint64_t)p.D / 64, (cuuint64_t)p.page_size / 8, heads}, strides5[4] = {row, 128, 8 * row, page};
+        const cuuint32_t box5[5] = {64, 8, L::kUnit / 64, (cuuint32_t)bx / 8, 1};
+        const cuuint64_t dims3[3] = {(cuuint64_t)p.D, (cuuint64_t)p.page_size, heads}, strides3[2] = {row, page};
+        const cuuint32_t box3[3] = {64, (cuuint32_t)bx, 1};
+        const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+        for (int i = 0; i < 2; ++i)
+            if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kHalves ? 3 : 5, const_cast<void*>(i ? p.v : p.k), kHalves ? dims3 : dims5,
+                    kHalves ? strides3 : strides5, kHalves ? box3 : box5, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
+    }
     const size_t smem = L::kTotal + 1024;
     static_assert(L::kTotal + 1024 <= 232448 && L::kCols <= 512, "shared and tensor memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D, kApart>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<N, D, kCopy>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_mma_kernel<N, D, kApart>, dim3(p.ctas), dim3(Roles<N, D>::kWarps * 32), smem, s, p, maps[0], maps[1], bx, page_heads);
+    return launch_dependent(attn_mma_kernel<N, D, kCopy>, dim3(p.ctas), dim3(Roles<N, D, kCopy>::kWarps * 32), smem, s, p, maps[0], maps[1], bx, page_heads);
 }
 
-template <int D, bool kApart>
+template <int D, Copy kCopy>
 cudaError_t launch_head(const AttnParams& p, cudaStream_t s) {
     switch (p.row_tile) {
-        case 16: return launch<16, D, kApart>(p, s);
-        case 32: return launch<32, D, kApart>(p, s);
-        case 64: return launch<64, D, kApart>(p, s);
+        case 16: return launch<16, D, kCopy>(p, s);
+        case 32: return launch<32, D, kCopy>(p, s);
+        case 64: return launch<64, D, kCopy>(p, s);
     }
-    if constexpr (D <= 128) return launch<128, D, kApart>(p, s);
+    if constexpr (D <= 128 && kCopy != Copy::kRows) return launch<128, D, kCopy>(p, s);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-bool attn_mma_supported(const AttnParams& p) {
+bool attn_pages_are_boxes(const AttnParams& p) {
     // pages a whole number of heads apart, all of them within a tensor map's last dimension
     const long long per_head = (long long)p.page_size * p.D;
-    return p.bf16 && (p.D <= 128 || p.D % 64 == 0) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 &&
+    return (p.D <= 128 || p.D % 64 == 0) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 &&
            p.page_stride / per_head < (1LL << 31) && p.pages * (p.page_stride / per_head) < (1LL << 31) &&
            tma_encoder() != nullptr;
 }
 
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s) {
-    if (p.D > 128) return launch_head<256, false>(p, s);
-    if (p.D == 128) return launch_head<128, false>(p, s);
-    return p.D == 64 ? launch_head<64, false>(p, s) : launch_head<128, true>(p, s);
+    if (!attn_pages_are_boxes(p)) {
+        if (p.D > 128) return launch_head<256, Copy::kRows>(p, s);
+        return p.D > 64 ? launch_head<128, Copy::kRows>(p, s) : launch_head<64, Copy::kRows>(p, s);
+    }
+    if (p.D > 128) return launch_head<256, Copy::kBoxes>(p, s);
+    if (p.D == 128) return launch_head<128, Copy::kBoxes>(p, s);
+    return p.D == 64 ? launch_head<64, Copy::kBoxes>(p, s) : launch_head<128, Copy::kHalves>(p, s);
 }
 
 }  // namespace dspark

@@ -81,7 +81,7 @@ struct AttnParams {
     uint32_t* status;
 };
 cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s);
-bool attn_mma_supported(const AttnParams& p);
+bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can copy
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
 // Rows of a row tile where a key-value head has `rows` query rows.
 inline int attn_row_tile(int rows, bool mma) {

@@ -131,15 +131,16 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     p.by_page.set((uint32_t)page_size);
     p.by_group.set((uint32_t)p.G);
     const int rows = p.G * max_new;
-    const bool mma = attn_mma_supported(p);
+    const bool mma = p.bf16;                       // tensor cores
     p.row_tile = attn_row_tile(rows, mma);
     // tiles the block tables can hold: few of them, fewer rows at a time.  On
     // CUDA cores where SMs would be idle otherwise; 128 rows in two tiles of 64 below
     // 32 tiles an SM (8 requests of 8192 positions, 2 heads: 34 us, at once 37;
     // 64 requests, 8 heads: 402 us, at once 249, the cache read once) and for
-    // heads above 128, whose O^T of 128 columns tensor memory does not hold
+    // heads above 128, whose O^T of 128 columns tensor memory does not hold, and
+    // row by row, where the copies bound it (64 rows: 267 us)
     const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
-    if (mma && p.row_tile == 128 && (head_dim > 128 || tiles < 32LL * num_sms())) p.row_tile = 64;
+    if (mma && p.row_tile == 128 && (head_dim > 128 || tiles < 32LL * num_sms() || !attn_pages_are_boxes(p))) p.row_tile = 64;
     if (!mma && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
     p.ctas = num_sms() < kMaxAttnCtas ? num_sms() : kMaxAttnCtas;      // one resident CTA per SM
