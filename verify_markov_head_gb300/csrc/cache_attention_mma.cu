@@ -18,7 +18,7 @@
 // of 8 positions, not a whole number of heads apart, or heads above 128 that
 // are no multiple of 64) are copied row by row, by cp.async of four warps.
 // 64 requests of 32 rows, and on CUDA cores before: head size 96 151 us (1900),
-// 192 283 (3230), 256 349 (3460); 128 in pages of 1 position 207 (1869).
+// 192 283 (3230), 256 349 (3460); 128 in pages of 1 position 204 (1869).
 //
 // Roles (12 or 20 warps, 2 more row by row, one CTA per SM, a ring of 5 stages of 32 KB, 4 with 128 columns):
 //   first 8 or 16    softmax, 2 or 4 groups of 4 warps, each with its share of the
@@ -43,15 +43,16 @@
 // segment ends off the way (the rows are written behind the next segment's
 // first step), the split over CTAs weighted by segments (AttnSplit).
 // Measured on one GB300: 64 requests of 1024-8192 positions, 1.22 GB: 32 rows
-// 183 us (6.6 TB/s), 64 rows 196, 128 rows 249 (three chunks of work a step on
-// 32 columns a thread: the softmax bounds it); 256 requests of 128-4096, 8
-// rows, 2.22 GB: 322 us (6.9 TB/s); one of 131072, 64 rows, 0.54 GB: 89 us (6.0
-// TB/s, 6 us of it before the ring is full and the join); 256 of 16-300
-// positions, 32 rows: 68 us (43 % of the rate, a segment's beginning and end
-// cost as much as 4 tiles).  Taking the column maxima in every step cost
-// 263 us for the first, one producer warp and serial segment ends 203, MMAs
-// issued from a diverged lane 203, an unweighted split 197, products in fixed
-// order 188.  A second buffer for P gained nothing (64 rows 202, short ones 74).
+// 182 us (6.7 TB/s), 64 rows 190, 128 rows 236 (32 columns a thread: the
+// softmax bounds it); 256 requests of 128-4096, 8 rows, 2.22 GB: 318 us (7.0
+// TB/s); one of 131072, 64 rows, 0.54 GB: 88 us (6.1 TB/s, 6 us of it before
+// the ring is full and the join); 256 of 16-300 positions, 32 rows: 67 us (44 %
+// of the rate: a segment takes the softmax 9000 cycles, of which its beginning
+// and end are half).  Taking the column maxima in every step cost 263 us for
+// the first, one producer warp and serial segment ends 203, MMAs issued from a
+// diverged lane 203, an unweighted split 197, products in fixed order 188, a
+// barrier more in a segment's first step and at its end 184 (64 rows 197).  A
+// second buffer for P gained nothing (64 rows 202, short ones 74).
 //
 // Weights are rounded to bf16 for the second product (relative 2^-8 of each
 // weight, independent in sign); their sum l is taken in fp32 before rounding.
@@ -117,9 +118,9 @@ struct Smem {
     static constexpr int kQ = kRing + kStages * kTileBytes;
     static constexpr int kP = kQ + kQBufs * kQBytes;                   // [128][64] bf16, 128-byte rows (128 columns: twice)
     static constexpr int kPBytes = kSteps * 128 * (N == 128 ? 2 : 1);
-    static constexpr int kMax = kP + kPBytes;                     // [N][4]
-    static constexpr int kSum = kMax + N * 16;                    // [N][4]
-    static constexpr int kNeg = kSum + N * 16;                    // [N], where 32 columns a thread leave no registers for it
+    static constexpr int kMax = kP + kPBytes;                     // [2][N][4], by the step's parity
+    static constexpr int kSum = kMax + 2 * N * 16;                    // [2][N][4], by the segment's parity
+    static constexpr int kNeg = kSum + 2 * N * 16;                    // [N], where 32 columns a thread leave no registers for it
     static constexpr int kSeg = kNeg + (N == 128 ? N * 4 : 0);
     static constexpr int kBar = kSeg + kSegs * (int)sizeof(Seg);
     static constexpr int kBars = 2 * kStages + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 3;
@@ -439,9 +440,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                         cp_async_arrive(b_full + 8 * stage);       // when this lane's copies have landed
                     }
                 }
-                continue;
-            }
-            for (int s = 0; s < d.steps; ++s, fill += kUnits) {
+            } else for (int s = 0; s < d.steps; ++s, fill += kUnits) {
                 const int pos = d.pos0 + s * kSteps + lane * bx;
                 const bool want = lane < nbox && pos < d.pos1;
                 const bool have = want && page >= 0 && page < p.pages;
@@ -625,7 +624,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         // (its O^T is in the other half of tensor memory), so the tensor core
         // and the producers go on meanwhile.  What is kept of it until then:
         bool pend = false;
-        float pend_ref = 0.f, pend_sum = 0.f;                      // lane c: column c's reference and sum
+        float pend_ref = 0.f;                                      // lane c: column c's reference
         for (uint32_t si = 0;; ++si) {
             const int slot = si % kSegs;
             ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
@@ -696,7 +695,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     }
                 }
                 if (NCH == 1) read_done();
-                const bool move = ptx::bar_red_or(1 + group, 128, unset || high > kSlack || !ok);
+                // (unset is the same in the whole group)
+                const bool move = unset || ptx::bar_red_or(1 + group, 128, high > kSlack || !ok);
                 // the product before this one is done: P may be overwritten, O rescaled
                 if (step > 0) ok = wait(b_pv, step - 1) && ok;
                 if (move) {                     // the same in every thread of the group
@@ -710,7 +710,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             if (lane == k * CH + c) mine = w;
                         }
                     }
-                    float* mx = reinterpret_cast<float*>(s_max + group * HC);
+                    float* mx = reinterpret_cast<float*>(s_max + (step & 1u) * N + group * HC);
                     if (lane < HC) mx[lane * 4 + quarter] = mine;
                     if (ptx::bar_red_or(1 + group, 128, !ok)) { stop = true; break; }
                     const float4 w4 = reinterpret_cast<const float4*>(mx)[lane & (HC - 1)];
@@ -719,7 +719,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     const float my_a = to > my_ref ? fast_exp2(my_ref - to) : 1.f;
                     my_ref = to;
                     unset = __any_sync(~0u, to == -INFINITY);
-                    // (the next write to s_max comes after another barrier)
+                    // (the next write here, two steps on, comes after another barrier)
                     if (NCH > 1) {
                         if (quarter == 0) s_neg[lane] = to == -INFINITY ? 0.f : -to;
                         ptx::named_barrier(1 + group, 128);
@@ -811,7 +811,9 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 const int e_at = (e.q0 + e_tok) * p.Hq + e.h * p.G + (e.r0 + e_row - e_tok * p.G);   // below N * Hq < 2^31
                 const int cols = min(HC, e.rows - group * HC);
                 const int part_slot = e.slot, e_new = e.len - e.n;
-                const float e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
+                // (written before the barrier that began this segment)
+                const float4 s4 = s_sum[(pi & 1u) * N + e_row];
+                const float pend_sum = (s4.x + s4.y) + (s4.z + s4.w), e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < NCH * kUnits; ++i) {
@@ -870,7 +872,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (none) break;
             // column sums: after the exchanges of 16, 8, .. lanes lane c holds
             // column c % HC of this warp's positions, then the 4 warps' are added
-            float* sm = reinterpret_cast<float*>(s_sum + group * HC);
+            float* sm = reinterpret_cast<float*>(s_sum + (si & 1u) * N + group * HC);
             {
 #pragma unroll
                 for (int w = HC / 2; w; w >>= 1) {
@@ -886,11 +888,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 for (int w = HC; w < 32; w <<= 1) l[0] += __shfl_xor_sync(~0u, l[0], w);
             }
             if (lane < HC) sm[lane * 4 + quarter] = l[0];
-            if (ptx::bar_red_or(1 + group, 128, !ok)) { ok = false; break; }
-            const float4 s4 = reinterpret_cast<const float4*>(sm)[lane & (HC - 1)];
             pend = true;
             pend_ref = my_ref;
-            pend_sum = (s4.x + s4.y) + (s4.z + s4.w);
         }
         if (!ok && lane == 0) give_up(5);
     }

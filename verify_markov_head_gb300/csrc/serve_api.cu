@@ -136,7 +136,7 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     // tiles the block tables can hold: few of them, fewer rows at a time.  On
     // CUDA cores where SMs would be idle otherwise; 128 rows in two tiles of 64 below
     // 32 tiles an SM (8 requests of 8192 positions, 2 heads: 34 us, at once 37;
-    // 64 requests, 8 heads: 402 us, at once 249, the cache read once) and for
+    // 64 requests, 8 heads: 402 us, at once 236, the cache read once) and for
     // heads above 128, whose O^T of 128 columns tensor memory does not hold, and
     // row by row, where the copies bound it (64 rows: 267 us)
     const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
