@@ -71,7 +71,9 @@ template <> struct Row<uint16_t> {
         asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(r.x), "r"(r.y));
         asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(r.z), "r"(r.w));
         asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(n));
-        if (!(__uint_as_float(m << 16) > -INFINITY && __uint_as_float(m & 0xffff0000u) > -INFINITY)) {
+        uint32_t both;
+        asm("set.gt.u32.bf16x2 %0, %1, %2;" : "=r"(both) : "r"(m), "r"(0xff80ff80u));
+        if (both != 0xffffffffu) {
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
             uint32_t above = 0u;
 #pragma unroll
@@ -99,7 +101,7 @@ template <> struct Row<uint16_t> {
 // in the ring, before the row leaves with the mask applied.
 // Measured on one GB300: 64 requests of 8 fp32 rows of 151936, a quarter of
 // them under a tight mask, 556 MB: 100 us (5.5 TB/s); 256 requests of 8 bf16
-// rows of 129280, half of them under a loose mask, 1067 MB: 187 us (5.7 TB/s; a
+// rows of 129280, half of them under a loose mask, 1067 MB: 184 us (5.8 TB/s; a
 // plain copy of these rows takes 156); one request 8.0 us.  On the way, the
 // first of them: rows through registers with the formula inlined in the stream
 // 283 us, with the listed entries corrected in the output afterwards 119, with
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? Ring<T>::kCta
 
         uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + ((size_t)b * p.R + row0) * p.V + lo) + tid;
         const size_t out_step = p.V / kVec;
-        const int shift = (tid * kVec) & 31;
+        const int shift = (tid * kVec) & 7;
         bool ok = true;
         for (int i = 0; i < rows; ++i, out += out_step) {
             const int s = i % kStages;
@@ -354,7 +356,8 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? Ring<T>::kCta
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 bits[j] = (uint32_t)kAll;
-                if (kMask) bits[j] &= s_mask[s * L::kMaskWords + (tid * kVec) / 32 + j * (kThreads * kVec / 32)] >> shift;
+                // a byte of the mask: the bits of one vector of 8, or of two of 4
+                if (kMask) bits[j] &= reinterpret_cast<const uint8_t*>(s_mask)[s * L::kMaskWords * 4 + tid * kVec / 8 + j * (kThreads * kVec / 8)] >> shift;
                 raw[j] = make_uint4(p.low, p.low, p.low, p.low);
                 if (read && tid + j * kThreads < vecs) raw[j] = reinterpret_cast<const uint4*>(slice)[tid + j * kThreads];
             }
