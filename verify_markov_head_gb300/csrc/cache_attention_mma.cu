@@ -508,7 +508,8 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, N == 128 ? kSteps * 128 : 16, 1024);
         // Whatever is ready goes first: the O product of the oldest step whose S
         // product was issued, or the next S product (of the next segment, too), at
-        // most one step ahead.  Short segments keep both going.
+        // most one step ahead: further, a producer could be two phases ahead of a
+        // stage's barrier, whose parity tells only one.  Short segments keep both going.
         struct Step { uint32_t step, seg; bool first; } old{}, young{};   // S issued, O not: the oldest, and one behind it
         bool has_old = false, has_young = false, in_seg = false, q_ready = false, done = false, ok = true;
         uint32_t step = 0, si = 0;
