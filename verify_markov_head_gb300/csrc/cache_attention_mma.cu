@@ -190,6 +190,16 @@ template <> __device__ __forceinline__ void tmem_put<16>(uint32_t a, const float
                    "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
 }
 
+// x * s + n, and l + w, of two columns in one instruction each.
+__device__ __forceinline__ void fma_pair(float& x0, float& x1, float s, float n0, float n1) {
+    asm("{\n\t.reg .b64 x, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 n, {%3, %4};\n\t"
+        "fma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(x0), "+f"(x1) : "f"(s), "f"(n0), "f"(n1));
+}
+__device__ __forceinline__ void add_pair(float& l0, float& l1, float w0, float w1) {
+    asm("{\n\t.reg .b64 l, w;\n\tmov.b64 l, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 l, l, w;\n\tmov.b64 {%0, %1}, l;\n\t}"
+        : "+f"(l0), "+f"(l1) : "f"(w0), "f"(w1));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -658,6 +668,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 const bool gone = row >= there || (bad >> my_box & 1u);
                 float x[CH];
                 // the scores of chunk k, -inf where the column does not see the position
+                // (read again where a reference moves)
                 auto scores = [&](int k) {
                     if (ok) tmem_get<CH>(s_at + k * CH, x);
                     else {
@@ -679,6 +690,11 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             *reinterpret_cast<float4*>(neg + c) = *reinterpret_cast<const float4*>(s_neg + k * CH + c);
                     }
                 };
+                // .. as exponents
+                auto exponents = [&]() {
+#pragma unroll
+                    for (int c = 0; c < CH; c += 2) fma_pair(x[c], x[c + 1], scale2, neg[c], neg[c + 1]);
+                };
                 auto read_done = [&]() {
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -691,11 +707,11 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     for (int k = 0; k < NCH; ++k) {
                         scores(k);
                         refs(k);
+                        exponents();
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) high = fmaxf(high, fmaf(x[c], scale2, neg[c]));
+                        for (int c = 0; c < CH; ++c) high = fmaxf(high, x[c]);
                     }
                 }
-                if (NCH == 1) read_done();
                 // (unset is the same in the whole group)
                 const bool move = unset || ptx::bar_red_or(1 + group, 128, high > kSlack || !ok);
                 // the product before this one is done: P may be overwritten, O rescaled
@@ -704,7 +720,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     float mine = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < NCH; ++k) {
-                        if (NCH > 1) scores(k);
+                        scores(k);
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
                             const float w = warp_max(x[c]);
@@ -749,19 +765,24 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             }
                     }
                 }
+                if (NCH == 1) {
+                    if (move) exponents();
+                    read_done();
+                }
                 // weights: row `row` of P, columns group * HC ..
 #pragma unroll
                 for (int k = 0; k < NCH; ++k) {
-                    if (NCH > 1) { scores(k); refs(k); }
+                    if (NCH > 1) { scores(k); refs(k); exponents(); }
                     const int col0 = group * HC + k * CH;
                     const uint32_t prow = base + L::kP + (col0 / 64) * (kSteps * 128) + row * 128;
 #pragma unroll
                     for (int c0 = 0; c0 < CH; c0 += 8) {
                         float w[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            w[e] = fast_exp2(fmaf(x[c0 + e], scale2, neg[c0 + e]));
-                            l[k * CH + c0 + e] += w[e];
+                        for (int e = 0; e < 8; e += 2) {
+                            w[e] = fast_exp2(x[c0 + e]);
+                            w[e + 1] = fast_exp2(x[c0 + e + 1]);
+                            add_pair(l[k * CH + c0 + e], l[k * CH + c0 + e + 1], w[e], w[e + 1]);
                         }
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                                      ::"r"(prow + ((((col0 + c0) / 8 & 7) ^ (row & 7)) << 4)), "r"(pack_bf16(w[0], w[1])),
