@@ -17,8 +17,8 @@
 // go to the same S^T and to two O^T.  Pages that are no boxes (not a multiple
 // of 8 positions, not a whole number of heads apart, or heads above 128 that
 // are no multiple of 64) are copied row by row, by cp.async of four warps.
-// 64 requests of 32 rows, and on CUDA cores before: head size 96 151 us (1900),
-// 192 283 (3230), 256 349 (3460); 128 in pages of 1 position 204 (1869).
+// 64 requests of 32 rows, and on CUDA cores before: head size 96 149 us (1900),
+// 192 283 (3230), 256 349 (3460); 128 in pages of 1 position 203 (1869).
 //
 // Roles (12 or 20 warps, 2 more row by row, one CTA per SM, a ring of 5 stages of 32 KB, 4 with 128 columns):
 //   first 8 or 16    softmax, 2 or 4 groups of 4 warps, each with its share of the
@@ -51,8 +51,10 @@
 // and end are half).  Taking the column maxima in every step cost 263 us for
 // the first, one producer warp and serial segment ends 203, MMAs issued from a
 // diverged lane 203, an unweighted split 197, products in fixed order 188, a
-// barrier more in a segment's first step and at its end 184 (64 rows 197).  A
-// second buffer for P gained nothing (64 rows 202, short ones 74).
+// barrier more in a segment's first step and at its end 184 (64 rows 197).
+// Exponents formed twice and column by column: head size 256 with 64 rows 418
+// us, 384 in pairs and kept.  A second buffer for P gained nothing (64 rows
+// 202, short ones 74).
 //
 // Weights are rounded to bf16 for the second product (relative 2^-8 of each
 // weight, independent in sign); their sum l is taken in fp32 before rounding.

@@ -138,7 +138,7 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     // 32 tiles an SM (8 requests of 8192 positions, 2 heads: 34 us, at once 37;
     // 64 requests, 8 heads: 402 us, at once 236, the cache read once) and for
     // heads above 128, whose O^T of 128 columns tensor memory does not hold, and
-    // row by row, where the copies bound it (64 rows: 267 us)
+    // row by row, where the copies bound it (64 rows: 250 us)
     const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
     if (mma && p.row_tile == 128 && (head_dim > 128 || tiles < 32LL * num_sms() || !attn_pages_are_boxes(p))) p.row_tile = 64;
     if (!mma && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
