@@ -3,6 +3,7 @@ arguments are refused before the device is touched, workspaces are sized."""
 import ctypes as C
 
 import pytest
+import torch
 
 import verify_markov_head_gb300 as vm
 
@@ -73,3 +74,85 @@ def test_logits_refuse_bad_arguments(host):
     for kw in (dict(V=60), dict(V=0), dict(rs=63), dict(R=18), dict(R=0), dict(B=0), dict(B=70000), dict(nb=0),
                dict(fill=float("nan"))):
         assert call(host, **kw) == -1, kw
+
+
+def _plan_args(B=3, T=5):
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    return dict(seq_len=i(B), n_new=i(B), owned=i(B), ring=i(20), ring_state=i(2), block_table=i(B, 4), page_size=16,
+                owned_out=i(B), ring_state_out=i(2), kv_len=i(B), q_off=i(B + 1), tile_off=i(B + 1), slot_map=i(T),
+                positions=i(T))
+
+
+def test_the_binding_names_what_is_wrong_with_a_tensor():
+    a = _plan_args()
+    with pytest.raises(vm.DsparkError):                          # all in order, but not on the device
+        vm.dspark_cache_plan(**a, stream=0)
+    for name in a:
+        if name == "page_size":
+            continue
+        other = ("ring", "block_table")                          # any number of entries
+        cases = [(a[name].float(), TypeError), (a[name].long(), TypeError), (None, TypeError), ([1, 2], TypeError)]
+        if name not in other:
+            cases += [(a[name][:-1], ValueError), (a[name][None], ValueError)]
+        if name != "block_table":
+            cases.append((torch.zeros(2 * a[name].numel(), dtype=torch.int32)[::2], ValueError))
+        for bad, err in cases:
+            # (slot_map's length is the number of slots, so positions is the one that differs)
+            with pytest.raises(err, match="positions" if name == "slot_map" and err is ValueError and bad is not None and
+                               bad.dim() == 1 and bad.is_contiguous() else name):
+                vm.dspark_cache_plan(**{**a, name: bad}, stream=0)
+    with pytest.raises(ValueError):
+        vm.dspark_cache_plan(**{**a, "page_size": 1 << 40}, stream=0)
+    with pytest.raises(TypeError):
+        vm.dspark_cache_plan(**{**a, "page_size": "16"}, stream=0)
+    with pytest.raises(AttributeError):
+        vm.dspark_cache_plan(**a, stream="x")
+
+
+@pytest.mark.parametrize("call", ["append", "attention"])
+def test_the_binding_refuses_caches_that_do_not_fit(call):
+    k = torch.zeros((6, 2, 16, 64), dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    x = torch.zeros((3, 2 if call == "append" else 4, 64), dtype=torch.bfloat16)
+    ws = type("W", (), {"buf": torch.zeros(1 << 20, dtype=torch.uint8)})
+
+    def run(k=k, v=k, x=x, y=None):
+        y = torch.empty(x.shape, dtype=x.dtype) if y is None else y
+        if call == "append":
+            vm.dspark_cache_append(x, y, i(x.shape[0]), k, v, stream=0)
+        else:
+            vm.dspark_cache_attention(x, k, v, i(1, 4), i(1), i(2), i(2), y, ws, max_new=3, stream=0)
+
+    with pytest.raises(vm.DsparkError):                          # all in order, but not on the device
+        run()
+    kv = torch.zeros((6, 2, 2, 16, 64), dtype=torch.bfloat16)    # keys and values of a page side by side: fits
+    with pytest.raises(vm.DsparkError):
+        run(k=kv[:, 0], v=kv[:, 1])
+    for kw in (dict(v=k.float()), dict(v=k[:5]), dict(v=kv[:, 0]), dict(k=k.transpose(1, 2), v=k.transpose(1, 2)),
+               dict(k=k[..., :32], v=k[..., :32]), dict(x=x[..., :32]), dict(x=x.float()), dict(x=x[:, :, None]),
+               dict(x=torch.zeros((3, 64, x.shape[1]), dtype=torch.bfloat16).transpose(1, 2)), dict(y=x[:2])):
+        with pytest.raises(ValueError):
+            run(**kw)
+    with pytest.raises(TypeError):
+        run(k=k.double(), v=k.double())
+
+
+def test_the_binding_refuses_logits_that_do_not_fit():
+    x = torch.zeros((2, 3, 64))
+    ws = type("W", (), {"buf": torch.zeros(1 << 16, dtype=torch.uint8)})
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    run = lambda x=x, out=None, **kw: vm.dspark_logits_process(  # noqa: E731
+        x, torch.empty(x.shape, dtype=x.dtype) if out is None else out, ws, stream=0, **kw)
+    good = dict(hist=i(2, 7), hist_len=i(2), prompt_len=i(2), draft_tok=i(2, 2), rep=torch.ones(2), freq=torch.ones(2),
+                pres=torch.ones(2), bias_tok=i(4), bias_val=torch.zeros(4), bias_off=i(3), mask=i(2, 3, 2), live=i(2, 3))
+    with pytest.raises(vm.DsparkError):                          # all in order, but not on the device
+        run(**good)
+    for kw in (dict(out=x[:1]), dict(out=x.double()), dict(x=torch.zeros((2, 64, 3)).transpose(1, 2)),
+               dict(x=torch.zeros((2, 5, 64))[:, :3]), dict(hist=None), dict(hist_len=None), dict(hist=i(3, 7)),
+               dict(draft_tok=i(2, 1)), dict(draft_tok=i(1, 2)), dict(bias_val=torch.zeros(3)), dict(bias_off=i(2)),
+               dict(mask=i(2, 3, 3)), dict(live=i(3, 2)), dict(rep=torch.ones(3))):
+        with pytest.raises(ValueError):
+            run(**{**good, **kw})
+    for kw in (dict(rep=torch.ones(2).double()), dict(mask=i(2, 3, 2).long()), dict(x=x.half()), dict(fill="low")):
+        with pytest.raises(TypeError):
+            run(**{**good, **kw})

@@ -12,6 +12,7 @@ ImportError: there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 
 import torch
@@ -34,6 +35,21 @@ lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 if not os.path.exists(lib_path):
     raise ImportError(f"libdspark.so is not built ({lib_path}); run verify_markov_head_gb300/build.py")
 _lib = C.CDLL(lib_path)
+
+
+def _load_serve():
+    """The module of the serving operators (csrc/serve_py.cpp): it checks their
+    tensors and calls the library in a third of the time that Python takes."""
+    path = os.path.join(os.path.dirname(lib_path), f"_serve-{torch.__version__}.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built for this PyTorch; run verify_markov_head_gb300/build.py")
+    spec = importlib.util.spec_from_file_location("_serve", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_serve = _load_serve()
 
 _vp, _i, _f, _u64, _sz, _ll = C.c_void_p, C.c_int, C.c_float, C.c_uint64, C.c_size_t, C.c_longlong
 _lib.dspark_version.restype = _i
@@ -464,68 +480,21 @@ def dspark_logits_workspace_bytes(B, R) -> int:
     return int(_lib.dspark_logits_workspace_bytes(B, R))
 
 
-def _typed(t, dtype, shape, name):
-    """Address of a contiguous tensor of the given type and shape (None: any size)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _cache_pair(k_cache, v_cache):
-    """(dtype code, page stride) of two caches [pages, kv_heads, page_size,
-    head_dim] whose pages are contiguous."""
-    shape, stride = k_cache.shape, k_cache.stride()
-    if shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or stride != v_cache.stride():
-        raise ValueError("k_cache and v_cache must share shape, dtype and strides")
-    if stride[3] != 1 or stride[2] != shape[3] or stride[1] != shape[2] * shape[3]:
-        if not k_cache[:1].is_contiguous():     # (the stride of a single row says nothing)
-            raise ValueError("a page of the cache must be contiguous [kv_heads, page_size, head_dim]")
-    return _dt(k_cache), stride[0] if shape[0] > 1 else shape[1] * shape[2] * shape[3]
-
-
-def _token_stride(t, shape, name):
-    """Elements between tokens of t [T, heads, head_dim], whose tokens are contiguous."""
-    stride = t.stride()
-    if stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
-
-
 def dspark_cache_plan(seq_len, n_new, owned, ring, ring_state, block_table, page_size, *, owned_out, ring_state_out,
                       kv_len, q_off, tile_off, slot_map, positions, ws: Workspace = None, stream=None):
     """Pages, slots and offsets of a step from lengths on the device: seq_len,
     n_new, owned [B] and ring [pages], ring_state [2] = (head, free) int32;
     block_table [B, width] and ring are updated in place, owned_out and
     ring_state_out are the next step's owned and ring_state."""
-    B, width = block_table.shape
-    T = slot_map.shape[0]
-    i32, b = torch.int32, (B,)
-    _check("dspark_cache_plan", _lib.dspark_cache_plan(
-        _typed(seq_len, i32, b, "seq_len"), _typed(n_new, i32, b, "n_new"), _typed(owned, i32, b, "owned"), B,
-        _typed(ring, i32, None, "ring"), _typed(ring_state, i32, (2,), "ring_state"), ring.numel(),
-        _typed(block_table, i32, None, "block_table"), width, page_size, _typed(owned_out, i32, b, "owned_out"),
-        _typed(ring_state_out, i32, (2,), "ring_state_out"), _typed(kv_len, i32, b, "kv_len"),
-        _typed(q_off, i32, (B + 1,), "q_off"), _typed(tile_off, i32, (B + 1,), "tile_off"),
-        _typed(slot_map, i32, (T,), "slot_map"), _typed(positions, i32, (T,), "positions"), T,
-        None if ws is None else ws.ptr(), _stream(stream)))
+    _check("dspark_cache_plan", _serve.cache_plan(
+        seq_len, n_new, owned, ring, ring_state, block_table, page_size, owned_out, ring_state_out, kv_len, q_off, tile_off,
+        slot_map, positions, None if ws is None else ws.buf, stream))
 
 
 def dspark_cache_append(k, v, slot_map, k_cache, v_cache, *, ws: Workspace = None, stream=None):
     """Write keys and values k, v [T, kv_heads, head_dim] (any token stride)
     to the slots slot_map [T] int32 of the caches; negative slots are skipped."""
-    shape = T, H, D = k.shape
-    t, page_stride = _cache_pair(k_cache, v_cache)
-    pages, Hc, P, Dc = k_cache.shape
-    if v.shape != shape or Hc != H or Dc != D or k.dtype is not k_cache.dtype or v.dtype is not k.dtype:
-        raise ValueError("k and v must be [T, kv_heads, head_dim] of the cache's heads and dtype")
-    _check("dspark_cache_append", _lib.dspark_cache_append(
-        k.data_ptr(), v.data_ptr(), t, _token_stride(k, shape, "k"), _token_stride(v, shape, "v"),
-        _typed(slot_map, torch.int32, (T,), "slot_map"), T, k_cache.data_ptr(), v_cache.data_ptr(), page_stride, pages, P,
-        H, D, None if ws is None else ws.ptr(), _stream(stream)))
+    _check("dspark_cache_append", _serve.cache_append(k, v, slot_map, k_cache, v_cache, None if ws is None else ws.buf, stream))
 
 
 def dspark_cache_attention(q, k_cache, v_cache, block_table, kv_len, q_off, tile_off, out, ws: Workspace, *, max_new,
@@ -534,19 +503,8 @@ def dspark_cache_attention(q, k_cache, v_cache, block_table, kv_len, q_off, tile
     over the paged cache: out [N, q_heads, head_dim], lse [N, q_heads] fp32 or
     None.  scale defaults to head_dim ** -0.5; max_new bounds the new tokens
     of a request."""
-    shape = N, Hq, D = q.shape
-    t, page_stride = _cache_pair(k_cache, v_cache)
-    pages, Hkv, P, Dc = k_cache.shape
-    B, width = block_table.shape
-    if Dc != D or q.dtype is not k_cache.dtype or out.dtype is not q.dtype or out.shape != shape:
-        raise ValueError("q and out must be [N, q_heads, head_dim] of the cache's head_dim and dtype")
-    i32 = torch.int32
-    _check("dspark_cache_attention", _lib.dspark_cache_attention(
-        q.data_ptr(), _token_stride(q, shape, "q"), k_cache.data_ptr(), v_cache.data_ptr(), t, page_stride, pages, P,
-        _typed(block_table, i32, None, "block_table"), width, _typed(kv_len, i32, (B,), "kv_len"),
-        _typed(q_off, i32, (B + 1,), "q_off"), _typed(tile_off, i32, (B + 1,), "tile_off"), B, N, Hq, Hkv, D, max_new,
-        D ** -0.5 if scale is None else scale, _p(out),
-        None if lse is None else _typed(lse, torch.float32, (N, Hq), "lse"), ws.ptr(), ws.nbytes(), _stream(stream)))
+    _check("dspark_cache_attention", _serve.cache_attention(
+        q, k_cache, v_cache, block_table, kv_len, q_off, tile_off, out, ws.buf, max_new, scale, lse, stream))
 
 
 def dspark_logits_process(logits, out, ws: Workspace, *, hist=None, hist_len=None, prompt_len=None, draft_tok=None,
@@ -559,37 +517,9 @@ def dspark_logits_process(logits, out, ws: Workspace, *, hist=None, hist_len=Non
     bias_off [B+1]: ascending ids per request; mask [B, R, ceil(V/32)] int32
     words, whose clear bits become fill (for the rows of U a finite value such
     as -1e4); live [B, R] int32 receives the entries left in each row."""
-    B, R, V = logits.shape
-    f32, i32, b = torch.float32, torch.int32, (B,)
-    if out.shape != logits.shape or out.dtype != logits.dtype:
-        raise ValueError("out must have the logits' shape and dtype")
-    rs = logits.stride(1) if R > 1 else logits.stride(0)
-    if logits.stride(2) != 1 or (B > 1 and logits.stride(0) != R * rs):
-        raise ValueError("the rows of logits must lie at one stride")
-    if B * R == 1:
-        rs = V
-    if draft_tok is not None and (draft_tok.shape[0] != B or draft_tok.shape[1] < R - 1):
-        raise ValueError("draft_tok must be [B, R-1] or wider")
-    if (hist is None) != (hist_len is None):
-        raise ValueError("hist and hist_len go together")
-    if hist is not None and hist.shape[1] == 0:      # no history yet
-        hist = hist_len = prompt_len = None
-    n_bias = 0
-    if bias_off is not None:
-        n_bias = bias_tok.numel()
-        if bias_val.numel() != n_bias:
-            raise ValueError("bias_tok and bias_val must have one entry each")
-    opt = lambda t, dt, shape, name: None if t is None else _typed(t, dt, shape, name)  # noqa: E731
-    _check("dspark_logits_process", _lib.dspark_logits_process(
-        logits.data_ptr(), _dt(logits), rs, _p(out), B, R, V,
-        opt(hist, i32, None if hist is None else (B, hist.shape[1]), "hist"), 0 if hist is None else hist.shape[1],
-        opt(hist_len, i32, b, "hist_len"), opt(prompt_len, i32, b, "prompt_len"),
-        opt(draft_tok, i32, None, "draft_tok"), 0 if draft_tok is None else draft_tok.shape[1],
-        opt(rep, f32, b, "rep"), opt(freq, f32, b, "freq"), opt(pres, f32, b, "pres"),
-        None if bias_off is None else _typed(bias_tok, i32, None, "bias_tok"),
-        None if bias_off is None else _typed(bias_val, f32, None, "bias_val"), opt(bias_off, i32, (B + 1,), "bias_off"),
-        n_bias, opt(mask, i32, (B, R, -(-V // 32)), "mask"), fill, opt(live, i32, (B, R), "live"), ws.ptr(), ws.nbytes(),
-        _stream(stream)))
+    _check("dspark_logits_process", _serve.logits_process(
+        logits, out, ws.buf, hist, hist_len, prompt_len, draft_tok, rep, freq, pres, bias_tok, bias_val, bias_off, mask, fill,
+        live, stream))
 
 
 class StepBuffers:

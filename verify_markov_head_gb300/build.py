@@ -3,14 +3,18 @@
 Each translation unit under csrc/ is compiled separately (in parallel) and
 linked into verify_markov_head_gb300/_lib/libdspark.so with the CUDA runtime
 linked statically, so the library needs nothing from the Python environment.
+Beside it the Python module of the serving operators (csrc/serve_py.cpp) is
+built with the headers of the installed PyTorch, whose version is in its name.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(HERE, "csrc")
@@ -41,8 +45,35 @@ def _stale(lib):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def serve_module() -> str:
+    version: dict = {}
+    with open(os.path.join(torch_dir(), "version.py")) as f:      # (without importing torch)
+        for line in f:
+            if line.startswith("__version__"):
+                exec(line, version)
+    return os.path.join(OUT, f"_serve-{version['__version__']}.so")
+
+
+def _compile_serve(cc):
+    """Object file of the Python module, and what its link needs."""
+    torch = torch_dir()
+    obj = os.path.join(OUT, "serve_py.o")
+    dirs = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+            os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *(f"-I{d}" for d in dirs), "-c", os.path.join(SRC, "serve_py.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on serve_py.cpp:\n{r.stderr}")
+    return obj, os.path.join(torch, "lib")
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not _stale(LIB):
+    if not force and not _stale(LIB) and not _stale(serve_module()):
         return LIB
     os.makedirs(OUT, exist_ok=True)
     cc = nvcc()
@@ -59,13 +90,22 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        serve = ex.submit(_compile_serve, cc)
         objs = list(ex.map(compile_one, sources()))
+        serve_obj, torch_lib = serve.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    module = serve_module()
+    tmp = module + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, serve_obj, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+                        "-lc10", "-L", OUT, "-l:libdspark.so", "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, module)
     return LIB
 
 
