@@ -267,8 +267,10 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 
 cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
     const size_t smem = sizeof(int) * 3 * ((size_t)p.B + 1);
-    cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     const int items = p.T > p.B ? p.T : p.B;
     int grid = (items + kPlanThreads - 1) / kPlanThreads;
     if (grid > num_sms()) grid = num_sms();

@@ -69,8 +69,9 @@ __device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int cta
 // stages of keys and values by cp.async, 16-byte chunks swizzled so that eight
 // positions' chunks lie in different banks.
 // Measured on one GB300: 16 requests of up to 8192 positions, 8 fp32 heads of
-// 128, 32 rows: 633 us (18 TFLOP/s; 1075 us without the register tiles), one
-// row a head 4: 248 us (2.9 TB/s); a call of 4 short requests 12.4 us.
+// 128, 32 rows: 623 us (18 TFLOP/s; 1075 us without the register tiles), one
+// row a head 4: 246 us (2.9 TB/s); a call of 4 short requests 12.1 us (14.3 us a
+// call without its programmatic launch, now 12.8).
 //   scores   8 rows x TPT positions a thread over a quarter of the head
 //            (lane = position group + 8 * quarter), the quarters summed by
 //            shuffles, which leave each thread NR rows of one position;
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
     __shared__ long long s_base[2][TT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) grid_launch_dependents();   // the join is scheduled now and waits for this grid
+    grid_dependency_wait();
     const int cta = blockIdx.x;
     empty_rows(p, cta, gridDim.x);
     const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
@@ -431,8 +433,7 @@ cudaError_t launch_simt_tile(const AttnParams& p, cudaStream_t s) {
     const size_t smem = Simt<MR, TT>::bytes(p.D);
     cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<MR, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attn_simt_kernel<MR, TT><<<p.ctas, kSimtThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(attn_simt_kernel<MR, TT>, dim3(p.ctas), dim3(kSimtThreads), smem, s, p);
 }
 template <int MR>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {

@@ -1,8 +1,9 @@
 // serve_py.cpp -- the serving operators as functions of a Python module: the
 // tensors' types, shapes and layout are checked and the C function is called
 // (include/dspark.h), whose status is returned.  A small call is over on the
-// GPU before Python has looked at its tensors one attribute at a time: through
-// ctypes the plan of 64 requests took 10.8 us a call, 4.7 of them on the GPU.
+// GPU before Python has looked at its tensors one attribute at a time.  Host
+// time of a call on an Arm core, through ctypes before: plan of 64 requests
+// 4.0 us (10.8), append 3.0 (7.3), attention 5.7 (13.9), logits 4.3 (13).
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/cuda/CUDAStream.h>
