@@ -256,6 +256,23 @@ def test_attention_of_other_head_sizes(vm, D, P, group, new, wide):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("group,new", [(1, 1), (8, 1), (3, 3), (2, 8), (4, 8), (8, 8), (16, 8)])
+def test_attention_stays_within_its_workspace(vm, group, new, dtype):
+    """Segments split over all SMs, both kinds of tables; what lies behind the workspace is untouched."""
+    D, P = 64, 16
+    for wide in (0, 300000 // P):
+        a = _attention_inputs(np.random.default_rng(group + new), [5000, 3000], [new, 1], 2 * group, 2, D, P, dtype, wide=wide)
+        n = vm.dspark_cache_workspace_bytes(2, 2 * group, 2, D, new)
+        ws = vm.CacheWorkspace(2, 2 * group, 2, D, new)
+        big = torch.full((16 << 20,), 0x5a, dtype=torch.uint8, device="cuda")       # 256-byte aligned, far larger
+        ws.buf = big[:n]
+        vm.dspark_workspace_init(ws.buf)
+        out, lse, _ = _attend(vm, a, new, ws=ws)
+        _check_attention(a, out, lse, D ** -0.5)
+        assert bool((big[n:] == 0x5a).all())
+
+
 def test_attention_of_a_large_ragged_batch(vm):
     rng = np.random.default_rng(77)
     lens = rng.integers(1, 400, 150)

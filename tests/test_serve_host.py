@@ -76,6 +76,15 @@ def test_logits_refuse_bad_arguments(host):
         assert call(host, **kw) == -1, kw
 
 
+@pytest.mark.parametrize("heads,new", [(1, 1), (8, 1), (3, 3), (2, 8), (16, 1), (4, 8), (8, 8), (16, 8)])
+def test_the_workspace_holds_two_tiles_of_rows_a_cta(heads, new):
+    """Sums, maximum and weight of each row, for the tiles of either kernel, on 152 SMs."""
+    rows = heads * new
+    tile = max(8 if rows <= 8 else 32, min(128, 16 if rows <= 16 else 32 if rows <= 32 else 64 if rows <= 64 else 128))
+    for D in (8, 64, 256):
+        assert vm.dspark_cache_workspace_bytes(3, 2 * heads, 2, D, new) >= 256 + 152 * 32 + 2 * 152 * tile * (D + 2) * 4
+
+
 def _plan_args(B=3, T=5):
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     return dict(seq_len=i(B), n_new=i(B), owned=i(B), ring=i(20), ring_state=i(2), block_table=i(B, 4), page_size=16,

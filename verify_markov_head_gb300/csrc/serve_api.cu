@@ -95,7 +95,9 @@ static bool attn_sizes_ok(int B, int q_heads, int kv_heads, int head_dim, int ma
 
 size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new) {
     if (!attn_sizes_ok(B, q_heads, kv_heads, head_dim, max_new)) return 0;
-    const size_t rows = attn_row_tile(q_heads / kv_heads * max_new, true);   // the larger of the two kernels' tiles
+    // the larger of the two kernels' tiles (of 9 to 16 rows 32 on CUDA cores, 16 on tensor cores)
+    const int all = q_heads / kv_heads * max_new, mma = attn_row_tile(all, true), simt = attn_row_tile(all, false);
+    const size_t rows = mma > simt ? mma : simt;
     return kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas) + ws_align256((size_t)2 * kMaxAttnCtas * rows * (head_dim + 2) * sizeof(float));
 }
 
