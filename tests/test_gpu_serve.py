@@ -318,9 +318,10 @@ def test_a_later_drafts_value_never_reaches_an_earlier_row(vm, bad, D, P, dtype,
             assert torch.equal(got[t], clean[t])
 
 
-def test_attention_reads_pages_beyond_32_bit_offsets(vm):
+@pytest.mark.parametrize("P", [64, 20])
+def test_attention_reads_pages_beyond_32_bit_offsets(vm, P):
     """Pages whose element offset passes 2^31, in caches of 2 x 4.4 GB."""
-    H, P, D = 8, 64, 128
+    H, D = 8, 128
     pages = (1 << 31) // (H * P * D) + 600
     k = torch.zeros((pages, H, P, D), dtype=torch.bfloat16, device="cuda")
     v = torch.zeros_like(k)
