@@ -802,7 +802,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                     for (int u = 0; u < kUnits; ++u) ok = wait(b_full + 8 * ((vi + u) % kStages), (vi + u) / kStages) && ok;
                     const bool later = !gone && pos > first_new;
                     if (gone || later) {
-                        // the two halves of the softmax warps share a row's chunks,
+                        // the groups share a row's chunks,
                         // each row begins at another one (other banks)
 #pragma unroll
                         for (int c = group; c < D / 8; c += kParts) {

@@ -76,6 +76,7 @@ struct AttnParams {
     int row_tile, row_tiles;    // query rows of a key-value head per tile of rows, and such tiles
     int ctas;                   // CTAs the work is split over
     int pad;                    // what a segment costs beside its tiles, in tiles (at least 1)
+    int spare;                  // few tiles: fewer CTAs, rather than a place for each
     AttnSplitRow* split;        // [ctas] the segment that begins in each CTA and ends in another
     float* part;                // [2 ctas][row_tile][D] sums, then [2 ctas][row_tile][2] (max, sum)
     uint32_t* status;
@@ -113,6 +114,15 @@ struct AttnSplit {
         if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x % 32 == 0) raise_status(p.status, kBadLength);
         total = ok ? (int)all : 0;
         n = total < p.ctas ? total : p.ctas;
+        if (p.spare && n) {
+            // few places: a place more is half a step, a part more a read of the join
+            // behind the others', so shares grow as the root of a segment's length
+            // (1000 positions, 8 heads: one place a CTA 11.0 us, two 9.5, five 10.2;
+            // 8000, one head: one 30.2, two 21.4, five 17.6)
+            int least = 2;                           // half the root of the mean length
+            for (const float segments = 4.f * (float)(p.B * heads); segments * (float)((least + 1) * (least + 1)) <= (float)total;) ++least;
+            n = min(n, (total + least - 1) / least);
+        }
         each = n ? total / n : 0;
         more = n ? total - each * n : 0;
     }

@@ -149,6 +149,7 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     // (tensor cores: 64 requests of 64 rows, head size 128: 3 places 203 us, 4 196; 256 of 16-300
     // positions 72, 68; head size 96, the same: 4 places 73.4, 6 72.2, 32 rows 152.7 with 3, 150.5 with 6)
     p.pad = mma ? (head_dim < 128 ? 6 : 4) : 1;
+    p.spare = mma;              // (on CUDA cores a tile costs more than its part: 4 short requests 13.4 us, two places a CTA 14.0)
     p.split = reinterpret_cast<AttnSplitRow*>(static_cast<char*>(ws) + kHead);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas));
     p.status = static_cast<uint32_t*>(ws);
