@@ -205,6 +205,7 @@ ATTENTION = [
     ([4100], [8], 8, 2, 64, 64),                               # split over many CTAs
     ([130, 20], [8, 3], 96, 1, 64, 16),                        # 96 heads to a key head
     ([2000, 70, 900], [0, 1, 0], 8, 4, 128, 32),               # requests that wait
+    ([9000], [8], 8, 1, 128, 16),                              # one key head, few CTAs with long shares
 ]
 
 

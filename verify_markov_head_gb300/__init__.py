@@ -2,8 +2,9 @@
 
 Argument marshalling only: every function below checks tensor shapes, passes
 ``data_ptr()`` values and sizes to the C function of the same name, and
-raises ``DsparkError`` on a non-OK status.  All arithmetic runs in the CUDA
-kernels of the library.  PyTorch provides device memory and streams.
+raises ``DsparkError`` on a non-OK status (the serving operators do so in a
+native module, csrc/serve_py.cpp).  All arithmetic runs in the CUDA kernels of
+the library.  PyTorch provides device memory and streams.
 
 The library must be built first (``python verify_markov_head_gb300/build.py``
 or ``__graft_entry__.build()``); importing this package without it raises
