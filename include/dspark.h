@@ -433,9 +433,11 @@ dspark_status dspark_sts_fit(const float* score, const int32_t* acc_len, int N, 
  *          and positions [max_tokens].  The same inputs give the same outputs,
  *          so a repeated call is harmless.
  * Requests are served in order while the ring has pages for them.  One that
- * is not served (no page left, a table row too short, a negative length)
- * keeps its pages, gets kv_len 0 and slots -1, and sets status bit 5.  More
- * than max_tokens tokens set bit 1.
+ * is not served (no page left, a table row too short, a length out of range)
+ * keeps its pages, gets kv_len 0 and slots -1, and sets status bit 5.  Its
+ * tokens keep their places in q_off, unless their number itself is out of
+ * [0, width * page_size]: then it counts none.  More than max_tokens tokens
+ * set bit 1; offsets stop at 2^31 - 1.
  * ws     : NULL (no status), or any workspace of this library (its status word).
  * Limits : 1 <= B <= DSPARK_MAX_CACHE_REQUESTS, pages * page_size < 2^31,
  *          width * page_size < 2^31, max_tokens < 2^30.

@@ -114,6 +114,56 @@ def test_plan_chained_over_steps_never_shares_a_page(vm):
         seq = seq + np.minimum(new, rng.integers(1, 9, B)).astype(np.int32)     # accepted + 1
 
 
+M = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("news", [[8, 8, M, 8], [8, 2 ** 30, 8, 2 ** 30, 8], [M, M, 0, 0, 8, 0, M, M], [8, M, M], [-2 ** 31, 8, M],
+                                  [8] * 31 + [M, 8, M] + [8] * 40])
+def test_plan_keeps_numbers_of_tokens_out_of_range_from_the_other_requests(vm, news):
+    """A number of new tokens beyond the table's rows counts none, as a negative
+    one does; the other requests are planned as if it were not there."""
+    rng = np.random.default_rng(len(news))
+    B = len(news)
+    seq, new, owned, ring, state, table = _plan_inputs(rng, B, 16, 300, 8, 24, 10 + 2 * B, ended=0.0)
+    new[:] = news
+    wild = (new < 0) | (new > 24 * 16)
+    T = 8 * B + 3
+    want = ref.plan(seq, np.where(wild, -1, new), owned, ring, state, table, 16, T)
+    ws = vm.LogitsWorkspace(1, 1)
+    got = _run_plan(vm, seq, new, owned, ring, state, table, 16, T, ws)
+    assert want.pop("bad")
+    for k in want:
+        np.testing.assert_array_equal(got[k], want[k], err_msg=k)
+    assert _status(vm, ws) == BAD_PAGE
+
+
+def test_plan_stops_its_sums_and_reports_too_many_tokens(vm):
+    """Numbers of tokens that a row of the table holds, but no ring: their sum
+    passes 2^31.  Lengths near 2^31 have no pages."""
+    P, n, width = 4096, 1 << 30, (1 << 18) + 1
+    seq = np.array([5, 7, 0, 2 ** 31 - 1, 9, 0, 2 ** 31 - 64], np.int32)
+    new = np.array([8, n, 8, 8, n, n, 0], np.int32)
+    B, T = len(new), 40
+    owned = np.array([1, 1, 0, 0, 1, 0, 0], np.int32)
+    table = np.full((B, width), -1, np.int32)
+    table[0, 0], table[1, 0], table[4, 0] = 3, 1, 4
+    ring = np.array([0, 2, 5, -7, -7, -7], np.int32)
+    ws = vm.LogitsWorkspace(1, 1)
+    got = _run_plan(vm, seq, new, owned, ring, np.array([0, 3], np.int32), table, P, T, ws)
+    assert _status(vm, ws) == BAD_PAGE | BAD_LENGTH
+    off = np.minimum(np.concatenate([[0], np.cumsum(new.astype(np.int64))]), M)
+    np.testing.assert_array_equal(got["q_off"], off)
+    # requests are served in order while the ring has pages: the second asks for more than there are
+    np.testing.assert_array_equal(got["kv_len"], [13, 0, 0, 0, 0, 0, 0])
+    np.testing.assert_array_equal(got["tile_off"], [0, 1, 1, 1, 1, 1, 1, 1])
+    np.testing.assert_array_equal(got["owned_out"], owned)
+    np.testing.assert_array_equal(got["ring_state_out"], [0, 3])
+    np.testing.assert_array_equal(got["slot_map"], list(range(3 * P + 5, 3 * P + 13)) + [-1] * (T - 8))
+    np.testing.assert_array_equal(got["positions"][:8], range(5, 13))
+    np.testing.assert_array_equal(got["block_table"], table)
+    np.testing.assert_array_equal(got["ring"], ring)
+
+
 # ------------------------------------------------------------------ append
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,H,D,P", [(1, 1, 8, 1), (5, 3, 64, 24), (700, 8, 128, 16), (333, 2, 80, 64), (0, 2, 64, 8)])

@@ -26,11 +26,12 @@ namespace {
 // rare case that the ring runs out in every call).
 constexpr int kPlanThreads = 1024;
 
-struct Sum4 { int tok, need, give, tiles; };
+struct Sum4 { unsigned tok, need, give, tiles; };
 
-// sums stop at 2^30 (the totals of valid inputs stay below it), so lengths out
-// of range cannot wrap an index
-__device__ __forceinline__ int add_sat(int a, int b) { return min(a + b, 1 << 30); }
+// Terms and sums stop at 2^31 - 1 (two of them do not wrap 32 bits).  A sum that
+// stops is still the same in any order of its terms, but its terms cannot be
+// taken off again: exclusive sums are formed without subtracting.
+__device__ __forceinline__ unsigned add_sat(unsigned a, unsigned b) { return min(a + b, 0x7fffffffu); }
 __device__ __forceinline__ Sum4 operator+(const Sum4& a, const Sum4& b) {
     return Sum4{add_sat(a.tok, b.tok), add_sat(a.need, b.need), add_sat(a.give, b.give), add_sat(a.tiles, b.tiles)};
 }
@@ -40,7 +41,7 @@ __device__ __forceinline__ Sum4 shfl_up(const Sum4& a, int d) {
 }
 
 struct PlanItem {
-    int fresh;     // new tokens
+    int fresh;     // new tokens, none where their number is out of [0, width * page_size]
     int need;      // pages it asks for (0 where it cannot be served)
     int goal;
     int owned;
@@ -53,8 +54,9 @@ __device__ __forceinline__ PlanItem plan_item(const PlanParams& p, int b) {
     it.seq = p.seq_len[b];
     it.fresh = p.n_new[b];
     it.owned = p.owned[b];
-    it.ok = it.seq >= 0 && it.fresh >= 0 && it.owned >= 0 && it.owned <= p.width;
-    it.fresh = min(max(0, it.fresh), 1 << 30);
+    const bool fresh_ok = it.fresh >= 0 && it.fresh <= p.width * p.page_size;     // (below 2^31)
+    if (!fresh_ok) it.fresh = 0;
+    it.ok = fresh_ok && it.seq >= 0 && it.owned >= 0 && it.owned <= p.width;
     const long long goal = ((long long)it.seq + it.fresh + p.page_size - 1) / p.page_size;
     it.ok = it.ok && goal <= p.width;
     it.goal = it.ok ? (int)goal : it.owned;
@@ -62,8 +64,8 @@ __device__ __forceinline__ PlanItem plan_item(const PlanParams& p, int b) {
     return it;
 }
 
-// first b in [0, B) with off[b + 1] > x
-__device__ __forceinline__ int owner_of(const int* off, int B, int x) {
+// the b in [0, B) with off[b] <= x < off[b + 1], where off[0] = 0 and x < off[B]
+__device__ __forceinline__ int owner_of(const unsigned* off, int B, unsigned x) {
     int lo = 0, hi = B;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -73,12 +75,12 @@ __device__ __forceinline__ int owner_of(const int* off, int B, int x) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanParams p) {
-    extern __shared__ int sm[];
-    int* s_q = sm;                      // [B + 1] exclusive sums of the new tokens
-    int* s_need = s_q + p.B + 1;        // [B + 1] of the pages asked for
-    int* s_give = s_need + p.B + 1;     // [B + 1] of the pages returned
+    extern __shared__ unsigned sm[];
+    unsigned* s_q = sm;                      // [B + 1] exclusive sums of the new tokens
+    unsigned* s_need = s_q + p.B + 1;        // [B + 1] of the pages asked for
+    unsigned* s_give = s_need + p.B + 1;     // [B + 1] of the pages returned
     __shared__ Sum4 s_warp[32];
-    __shared__ int s_popped;
+    __shared__ unsigned s_popped;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = p.B;
     grid_dependency_wait();
@@ -97,69 +99,73 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
             if (lane >= d) x = x + y;
         }
         if (lane == 31) s_warp[warp] = x;
+        Sum4 before = shfl_up(x, 1);
+        if (lane == 0) before = Sum4{0u, 0u, 0u, 0u};
         __syncthreads();
         if (warp == 0) {
-            Sum4 w = s_warp[lane];
-            Sum4 z = w;
+            Sum4 z = s_warp[lane];
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const Sum4 y = shfl_up(z, d);
                 if (lane >= d) z = z + y;
             }
-            s_warp[lane] = Sum4{z.tok - w.tok, z.need - w.need, z.give - w.give, z.tiles - w.tiles};
+            z = shfl_up(z, 1);
+            s_warp[lane] = lane == 0 ? Sum4{0u, 0u, 0u, 0u} : z;
         }
         __syncthreads();
-        const Sum4 o = s_warp[warp];
+        before = s_warp[warp] + before;
         __syncthreads();
-        return Sum4{x.tok - v.tok + o.tok, x.need - v.need + o.need, x.give - v.give + o.give,
-                    x.tiles - v.tiles + o.tiles};
+        return before;
     };
     // a thread's requests; up to 1024 of them stay in registers
     PlanItem one{};
     if (b0 < b1) one = plan_item(p, b0);
     auto item = [&](int b) { return b == b0 ? one : plan_item(p, b); };
-    auto give_of = [](const PlanItem& it) { return max(0, it.owned - it.goal); };
-    auto tiles_of = [](const PlanItem& it) { return (it.seq + it.fresh + kTile - 1) / kTile; };
+    auto give_of = [](const PlanItem& it) { return (unsigned)max(0, it.owned - it.goal); };
+    auto tiles_of = [](const PlanItem& it) { return ((unsigned)it.seq + it.fresh + kTile - 1) / kTile; };
+    auto served_at = [&](const PlanItem& it, unsigned need) {     // `need` pages asked for before it
+        return it.ok && (it.need == 0 || need + it.need <= (unsigned)avail);
+    };
     // sums as if every request could be served (usually so)
-    Sum4 mine{0, 0, 0, 0};
+    Sum4 mine{0u, 0u, 0u, 0u};
     for (int b = b0; b < b1; ++b) {
         const PlanItem it = item(b);
-        mine = mine + Sum4{it.fresh, it.need, it.ok ? give_of(it) : 0, it.ok ? tiles_of(it) : 0};
+        mine = mine + Sum4{(unsigned)it.fresh, (unsigned)it.need, it.ok ? give_of(it) : 0u, it.ok ? tiles_of(it) : 0u};
     }
     Sum4 at = block_scan(mine);
     if (tid == kPlanThreads - 1) s_popped = add_sat(at.need, mine.need);
     __syncthreads();
     Sum4 at2 = at;
-    if (s_popped > avail) {
+    if (s_popped > (unsigned)avail) {
         // requests are served in order while the ring has pages for them
         __syncthreads();
         if (tid == 0) s_popped = 0;
         __syncthreads();
-        Sum4 second{0, 0, 0, 0};
-        int need = at.need;
+        Sum4 second{0u, 0u, 0u, 0u};
+        unsigned need = at.need;
         for (int b = b0; b < b1; ++b) {
             const PlanItem it = item(b);
-            const bool served = it.ok && (it.need == 0 || need + it.need <= avail);
+            const bool served = served_at(it, need);
             need = add_sat(need, it.need);
             if (served) {
-                second = second + Sum4{0, 0, give_of(it), tiles_of(it)};
-                if (it.need) atomicAdd(&s_popped, it.need);     // an integer sum: any order gives the same
+                second = second + Sum4{0u, 0u, give_of(it), tiles_of(it)};
+                if (it.need) atomicAdd(&s_popped, (unsigned)it.need);     // an integer sum: any order gives the same
             }
         }
         at2 = block_scan(second);
     }
     {
-        int tok = at.tok, need = at.need, give = at2.give, tiles = at2.tiles;
+        unsigned tok = at.tok, need = at.need, give = at2.give, tiles = at2.tiles;
         for (int b = b0; b < b1; ++b) {
             const PlanItem it = item(b);
-            const bool served = it.ok && (it.need == 0 || need + it.need <= avail);
+            const bool served = served_at(it, need);
             bad |= !served;
             s_q[b] = tok; s_need[b] = need; s_give[b] = give;
             if (blockIdx.x == 0) {
                 p.owned_out[b] = served ? it.goal : it.owned;
                 p.kv_len[b] = served ? it.seq + it.fresh : 0;
-                p.q_off[b] = tok;
-                p.tile_off[b] = tiles;
+                p.q_off[b] = (int)tok;
+                p.tile_off[b] = (int)tiles;
             }
             tok = add_sat(tok, it.fresh);
             need = add_sat(need, it.need);
@@ -169,44 +175,45 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
             }
             if (b == B - 1) {
                 s_q[B] = tok; s_need[B] = need; s_give[B] = give;
-                if (blockIdx.x == 0) { p.q_off[B] = tok; p.tile_off[B] = tiles; }
+                if (blockIdx.x == 0) { p.q_off[B] = (int)tok; p.tile_off[B] = (int)tiles; }
             }
         }
     }
     __syncthreads();
-    const int popped = s_popped, given = s_give[B], tokens = s_q[B];
+    const unsigned popped = s_popped, given = s_give[B], tokens = s_q[B];
     if (blockIdx.x == 0) {
         if (bad) raise_status(p.status, kBadPage);
         if (tid == 0) {
             p.ring_state_out[0] = (int)(((long long)head + popped) % p.pages);
-            p.ring_state_out[1] = avail - popped + given;
+            p.ring_state_out[1] = (int)add_sat((unsigned)avail - popped, given);
             if (!state_ok) raise_status(p.status, kBadPage);
-            if (tokens > p.T) raise_status(p.status, kBadLength);
+            if (tokens > (unsigned)p.T) raise_status(p.status, kBadLength);
         }
     }
     auto ring_at = [&](long long i) { return (int)(((long long)head + i) % p.pages); };
-    const int g0 = blockIdx.x * kPlanThreads + tid, gs = gridDim.x * kPlanThreads;
+    const unsigned g0 = blockIdx.x * kPlanThreads + tid, gs = gridDim.x * kPlanThreads;
     // the pages that change hands
-    for (int g = g0; g < popped; g += gs) {
+    for (unsigned g = g0; g < popped; g += gs) {
         const int b = owner_of(s_need, B, g);
-        const int j = p.owned[b] + (g - s_need[b]);
+        const int j = (int)(p.owned[b] + (g - s_need[b]));
         if (j >= 0 && j < p.width) p.table[(size_t)b * p.width + j] = p.ring[ring_at(g)];
     }
-    for (int g = g0; g < given; g += gs) {
+    for (unsigned g = g0; g < given; g += gs) {
         const int b = owner_of(s_give, B, g);
         const PlanItem it = plan_item(p, b);
-        const int j = it.goal + (g - s_give[b]);
+        const int j = (int)(it.goal + (g - s_give[b]));
         if (j >= 0 && j < it.owned) p.ring[ring_at((long long)avail + g)] = p.table[(size_t)b * p.width + j];
     }
     // the slot of every new token; a page taken in this call is read from the
     // ring, since another CTA may not have written the table yet
-    for (int t = g0; t < p.T; t += gs) {
+    for (unsigned t = g0; t < (unsigned)p.T; t += gs) {
         int slot = -1, pos = -1;
         if (t < tokens) {
             const int b = owner_of(s_q, B, t);
             const PlanItem it = plan_item(p, b);
-            pos = it.seq + (t - s_q[b]);
-            if (it.ok && t - s_q[b] < it.fresh && (it.need == 0 || s_need[b] + it.need <= avail)) {
+            const unsigned i = t - s_q[b];           // below it.fresh
+            pos = (int)(it.seq + i);                 // (of a served request below 2^31)
+            if (i < (unsigned)it.fresh && served_at(it, s_need[b])) {
                 const int j = pos / p.page_size;
                 const int page = j < it.owned ? p.table[(size_t)b * p.width + j]
                                               : p.ring[ring_at((long long)s_need[b] + j - it.owned)];
