@@ -513,7 +513,9 @@ dspark_status dspark_cache_attention(
  *          bias_off[b] .. bias_off[b+1] of bias_tok (strictly ascending ids in
  *          each request) and bias_val, bias_n in all; mask
  *          [B][R][ceil(V/32)].  hist, draft_tok, rep (1), freq (0), pres (0),
- *          bias_off and mask (everything allowed) may be NULL.  fill is -inf
+ *          bias_off and mask (everything allowed) may be NULL (hist_len and
+ *          prompt_len are NULL with hist; hist_stride and draft_stride say
+ *          nothing without their array).  fill is -inf
  *          for target rows; for U give a finite one such as -1e4: the draft's
  *          running sums take finite scores (the draw itself never picks one
  *          that low, and a drafted token that the target rows mask is rejected

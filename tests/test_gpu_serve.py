@@ -533,6 +533,24 @@ def test_logits_with_an_empty_history(vm):
         assert torch.equal(got, want) and torch.equal(live, live2)
 
 
+@pytest.mark.parametrize("B,V", [(1, 1024), (3, 8200)])
+def test_logits_without_a_history_but_with_its_stride(vm, B, V):
+    """The C call with hist = NULL beside the row widths a caller always passes: nothing is read there."""
+    rng = np.random.default_rng(B)
+    a = _logit_inputs(rng, B, 4, V, torch.float32, 10)
+    want, live, _ = _process(vm, a, hist=None, hist_len=None, prompt_len=None, draft_tok=None, bias_off=None)
+    x, words = a["x"].cuda(), _words(a["mask"])
+    f = [_cu(a[k], torch.float32) for k in ("rep", "freq", "pres")]
+    ws = vm.LogitsWorkspace(B, 4)
+    out, got = torch.empty_like(x), torch.zeros_like(live)
+    st = vm._lib.dspark_logits_process(x.data_ptr(), 0, V, out.data_ptr(), B, 4, V, None, 8192, None, None, None, 17,
+                                       *[t.data_ptr() for t in f], None, None, None, 0, words.data_ptr(), float("-inf"),
+                                       got.data_ptr(), ws.buf.data_ptr(), ws.buf.numel(), None)
+    torch.cuda.synchronize()
+    assert st == 0 and _status(vm, ws) == 0
+    assert torch.equal(out, want) and torch.equal(got, live)
+
+
 def test_logits_in_place_and_strided_rows(vm):
     rng = np.random.default_rng(21)
     a = _logit_inputs(rng, 4, 5, 1032, torch.bfloat16, 60)

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? Ring<T>::kCta
         const int draft = p.draft_tok && tid < p.R - 1 ? p.draft_tok[(size_t)b * p.draft_stride + tid] : -1;
         const int32_t* h = p.hist + (size_t)b * p.hist_stride;
         int past[kPast];
-        auto load_past = [&](int i0) {               // within the row of hist; judged by the length later
+        auto load_past = [&](int i0) {               // within the row of hist (of no tokens without one); judged by the length later
 #pragma unroll
             for (int u = 0; u < kPast; ++u) past[u] = i0 + u * kThreads < p.hist_stride ? __ldg(h + i0 + u * kThreads) : -1;
         };

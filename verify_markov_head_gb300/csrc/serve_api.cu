@@ -185,7 +185,8 @@ dspark_status dspark_logits_process(const void* logits, dspark_dtype t, long lon
     LogitsParams p;
     p.logits = logits; p.row_stride = row_stride; p.bf16 = t == DSPARK_BF16;
     p.out = out; p.B = B; p.R = R; p.V = V;
-    p.hist = hist; p.hist_stride = hist_stride; p.hist_len = hist_len; p.prompt_len = prompt_len;
+    p.hist = hist; p.hist_stride = hist ? hist_stride : 0;     // (tokens a row of hist holds)
+    p.hist_len = hist_len; p.prompt_len = prompt_len;
     p.draft_tok = draft_tok; p.draft_stride = draft_stride;
     p.rep = rep; p.freq = freq; p.pres = pres;
     p.bias_tok = bias_off && bias_n > 0 ? bias_tok : nullptr;
