@@ -480,8 +480,9 @@ dspark_status dspark_cache_append(
  * Outputs: out [N][q_heads][head_dim] (kv_t); lse [N][q_heads] fp32 or NULL.
  *          Rows outside q_off[0] .. q_off[B] are not written.
  * Checks : a page out of range is left out and sets status bit 5; n above
- *          max_new, offsets or lengths out of range set bit 1 (the rows
- *          concerned are unspecified).
+ *          max_new, offsets or lengths out of range, and tile_off that are not
+ *          the sums of ceil(kv_len / DSPARK_CACHE_TILE) (of an earlier step, say)
+ *          set bit 1 (the rows concerned are unspecified).
  * ws     : dspark_cache_workspace_bytes(...) bytes, 256-byte aligned, cleared
  *          once.  Results do not depend on what it holds.
  * Limits : B as above, q_heads % kv_heads == 0, 1 <= max_new <=

@@ -420,6 +420,68 @@ def test_attention_reports_bad_pages_and_lengths(vm, P):
     assert _status(vm, ws2) & BAD_LENGTH
 
 
+def _rows_as_defined(a, out, lse, requests):
+    """The rows of these requests against the definition."""
+    q_off, n = a["q_off"].cpu(), a["kv_len"].shape[0]
+    take = torch.cat([torch.arange(int(q_off[b]), int(q_off[b + 1])) for b in range(n) if b in requests]).cuda()
+    news = [int(q_off[b + 1] - q_off[b]) for b in range(n) if b in requests]
+    keep = torch.tensor([b for b in range(n) if b in requests], device="cuda")
+    part = dict(a, q=a["q"][take], table=a["table"][keep], kv_len=a["kv_len"][keep], q_off=_cu(np.concatenate([[0], np.cumsum(news)])))
+    _check_attention(part, out[take], lse[take], a["q"].shape[2] ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,P", [(3, 16), (3, 4), (70, 64)])
+def test_attention_reports_tile_offsets_of_an_earlier_step(vm, B, P, dtype):
+    """The lengths grew and tile_off did not: status bit 1 where a request has a
+    tile more; the requests with as many tiles as before are as they should be."""
+    rng = np.random.default_rng(B + P)
+    lens = rng.integers(9, 700, B)
+    lens[0], lens[1] = 128, 127                    # one position more: a new tile; none
+    news = rng.integers(1, 9, B)
+    a = _attention_inputs(rng, lens + 1, news, 8, 2, 64, P, dtype)
+    old = np.concatenate([[0], np.cumsum(-(-lens // 64))])
+    grown = -(-(lens + 1) // 64) > -(-lens // 64)
+    assert grown[0] and not grown[1]
+    out, lse, ws = _attend(vm, dict(a, tile_off=_cu(old)), 8)
+    assert _status(vm, ws) == BAD_LENGTH
+    _rows_as_defined(a, out, lse, np.flatnonzero(~grown).tolist())
+    out, lse, ws = _attend(vm, a, 8, ws=ws)
+    _rows_as_defined(a, out, lse, list(range(B)))
+    assert _status(vm, ws) == 0
+
+
+@pytest.mark.parametrize("dtype,D,wide", [(torch.bfloat16, 64, 0), (torch.float32, 64, 0), (torch.bfloat16, 256, 0), (torch.bfloat16, 64, 40000)])
+@pytest.mark.parametrize("B", [2, 5, 70])
+def test_attention_reports_tile_offsets_out_of_range(vm, B, D, dtype, wide):
+    """Entries that do not ascend, negative and large ones between good ones: the
+    status bit, nothing written beside the rows, and the workspace as good as before."""
+    rng = np.random.default_rng(B + D)
+    lens, P = rng.integers(1, 700, B), 16
+    a = _attention_inputs(rng, lens, np.minimum(lens, 8), 8, 2, D, P, dtype, wide=wide)
+    want, wlse, ws = _attend(vm, a, 8)
+    off = a["tile_off"].cpu().numpy()
+    total, width = int(off[-1]), a["table"].shape[1]
+    room = B * -(-width * P // 64)                 # tiles that the tables could hold
+    N = want.shape[0]
+    big = torch.full((N + 8, *want.shape[1:]), 7.0, dtype=dtype, device="cuda")
+    cases = []
+    for i in range(1, B, max(1, B // 3)):
+        for x in (-2 ** 31, -(1 << 25), -1, 1 << 25, 2 ** 31 - 1, total + 3, int(off[i + 1]) + 1, int(off[i - 1]) - 1):
+            cases.append(np.concatenate([off[:i], [x], off[i + 1:]]))
+    cases += [np.concatenate([[0], np.sort(off[1:B])[::-1], [total]]), np.concatenate([off[:B], [total - 1]]),
+              np.concatenate([off[:B], [min(room, total + 100)]]), np.concatenate([off[:B], [room + 1]]), np.full(B + 1, -1),
+              off + 1, np.where(np.arange(B + 1) < B, 0, total)]
+    for o in cases:
+        if (o == off).all():
+            continue
+        vm.dspark_cache_attention(a["q"], a["k"], a["v"], a["table"], a["kv_len"], a["q_off"], _cu(o), big[4:N + 4], ws, max_new=8)
+        assert _status(vm, ws) == BAD_LENGTH, o
+        assert bool((big[:4] == 7).all()) and bool((big[N + 4:] == 7).all())
+    out, lse, _ = _attend(vm, a, 8, ws=ws)
+    assert torch.equal(out, want) and torch.equal(lse, wlse) and _status(vm, ws) == 0
+
+
 def test_attention_in_a_cuda_graph(vm):
     rng = np.random.default_rng(14)
     a = _attention_inputs(rng, [300, 20], [8, 2], 8, 2, 128, 16, torch.bfloat16)

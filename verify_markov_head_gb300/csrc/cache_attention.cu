@@ -51,10 +51,13 @@ __device__ __forceinline__ void store_out<uint16_t>(uint16_t* out, float x) {
     asm("{\n\t.reg .b16 h;\n\tcvt.rn.bf16.f32 h, %1;\n\tmov.b16 %0, h;\n\t}" : "=h"(*out) : "f"(x));
 }
 
-// Requests that own no cache position have no tile: their rows are zero.
+// Requests that own no cache position have no tile: their rows are zero.  The
+// offsets of every request are compared with its length here.
 __device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int ctas) {
     for (int b = cta; b < p.B; b += ctas) {
-        if (p.tile_off[b + 1] > p.tile_off[b]) continue;
+        const int off = p.tile_off[b], next = p.tile_off[b + 1];
+        if (threadIdx.x == 0 && !attn_offsets_fit(p, b, off, next)) raise_status(p.status, kBadLength);
+        if (next > off) continue;
         const RowMap r(p, b);
         const size_t o0 = (size_t)r.q0 * p.Hq * p.D, n = (size_t)r.n * p.Hq * p.D;
         for (size_t i = threadIdx.x; i < n; i += blockDim.x) static_cast<float*>(p.out)[o0 + i] = 0.f;
@@ -132,9 +135,10 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
         const RowMap rm(p, g.b);
         const int r0 = g.rt * p.row_tile;
         const int rows = max(0, min(p.row_tile, rm.n * p.G - r0));
-        const int j0 = g.tile(sp, t), j1 = g.tile(sp, end);
-        t = g.t0 + sp.pad + g.tiles;             // the next segment
-        if (j0 == j1 || rows == 0) continue;
+        const int j0 = g.tile(sp, t), j1 = g.tile(sp, end), next = g.t0 + sp.pad + g.tiles;
+        if (next <= t) break;                    // (offsets that do not ascend)
+        t = next;                                // the next segment
+        if (j0 == j1 || rows == 0 || g.tiles != attn_tiles(rm.len)) continue;
         const int steps = (j1 - j0) * (kTile / TT), first_new = rm.len - rm.n;
         // where position `tid` of a step lies, -1 beyond the end or in a bad page
         auto base_of = [&](int s) {

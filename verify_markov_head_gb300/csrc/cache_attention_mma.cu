@@ -292,13 +292,16 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         // tile, or the next request
         auto skip = [&]() {
             while (t < end && g.tile(sp, t) == g.tile(sp, end)) {
-                t = g.tiles > 0 ? g.t0 + sp.pad + g.tiles : attn_request_at(p, g.b + 1) * sp.heads;
+                const int to = g.tiles > 0 ? g.t0 + sp.pad + g.tiles : attn_request_at(p, sp, g.b + 1) * sp.heads;
+                // offsets that do not ascend: nothing more (the places, or the requests at
+                // one place, ascend from here on, so the walk ends)
+                t = to > t || (to == t && g.tiles > 0) ? to : end;
                 if (t >= end) break;
                 if (g.tiles > 0 && ++g.rt == p.row_tiles) { g.rt = 0; ++g.h; }
                 g.t0 = t;
                 if (g.tiles == 0 || g.h == p.Hkv) {
                     // the next request, or (after one without tiles) looked up
-                    if (g.tiles > 0) g = attn_segment_of(p, sp, t, g.b + 1, attn_request_at(p, g.b + 1), attn_request_at(p, min(p.B, g.b + 2)));
+                    if (g.tiles > 0) g = attn_segment_of(p, sp, t, g.b + 1, attn_request_at(p, sp, g.b + 1), attn_request_at(p, sp, min(p.B, g.b + 2)));
                     else g = attn_segment(p, sp, t, attn_first_round(p));
                 }
             }
@@ -317,10 +320,11 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (more) {
                 // four loads on their way together: the page of this lane's box as if
                 // the request were as long as its tiles say
-                const int j0 = g.tile(sp, t), j1 = g.tile(sp, end), pos_in = j0 * kTile + lane * bx;
+                const int j0 = g.tile(sp, t), j1 = g.tile(sp, end);
+                const unsigned pos_in = (unsigned)j0 * kTile + lane * bx;
                 const int cap = p.width * p.page_size;
                 const int len_in = p.kv_len[g.b], qa = p.q_off[g.b], qe = p.q_off[g.b + 1];
-                const int page_in = lane < nbox && pos_in < cap ? __ldg(p.table + (size_t)g.b * p.width + p.by_page(pos_in)) : -1;
+                const int page_in = lane < nbox && pos_in < (unsigned)cap ? __ldg(p.table + (size_t)g.b * p.width + p.by_page((int)pos_in)) : -1;
                 int n = qe - qa, len = len_in;
                 n0 = qa;
                 if (n > p.max_new || n < 0 || qa < 0 || qa > p.N - n || len < 0 || len > cap) {
@@ -330,14 +334,15 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 }
                 nr0 = g.rt * p.row_tile;
                 nrows = max(0, min(p.row_tile, n * p.G - nr0));
-                const int pos0 = min(j0 * kTile, len), pos1 = min(j1 * kTile, len);
-                if (nrows == 0) {                    // no row of the request here: nothing to publish
+                // no row of the request here, or offsets that do not fit its length: nothing to publish
+                if (nrows == 0 || g.tiles != attn_tiles(len)) {
                     t = g.t0 + sp.pad + j1;
                     skip();
                     --si;
                     continue;
                 }
-                if (lane < nbox) d.page[lane] = pos_in < pos1 ? page_in : -1;
+                const int pos0 = min(j0 * kTile, len), pos1 = min(j1 * kTile, len);
+                if (lane < nbox) d.page[lane] = (int)pos_in < pos1 ? page_in : -1;
                 if (j0 == 0 && j1 < g.tiles) split = attn_split_row(sp, g, cta, qa, nr0, nrows);
                 if (lane == 0) {
                     d.b = g.b; d.h = g.h; d.q0 = qa; d.n = n; d.len = len; d.r0 = nr0; d.rows = nrows;
@@ -917,10 +922,13 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         }
         if (!ok && lane == 0) give_up(5);
     }
-    // requests that own no cache position have no tile: their rows are zero
+    // requests that own no cache position have no tile: their rows are zero; the
+    // offsets of every request are compared with its length
     if (warp < kSoftWarps) {
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            if (p.tile_off[b + 1] > p.tile_off[b]) continue;
+            const int off = p.tile_off[b], next = p.tile_off[b + 1];
+            if (tid == 0 && !attn_offsets_fit(p, b, off, next)) raise_status(p.status, kBadLength);
+            if (next > off) continue;
             int q0 = p.q_off[b], n = p.q_off[b + 1] - q0;
             n = q0 < 0 ? 0 : max(0, min(n, min(p.max_new, p.N - q0)));
             for (int i = tid; i < n * p.Hq * hd; i += kSoftWarps * 32) static_cast<uint16_t*>(p.out)[(size_t)q0 * p.Hq * hd + i] = 0;

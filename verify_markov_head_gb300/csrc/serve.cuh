@@ -99,10 +99,11 @@ inline int attn_row_tile(int rows, bool mma) {
 // in each (slot 2c + 1 where its first tile is in c, else 2c), which the join
 // kernel adds up in CTA order.
 struct AttnSplit {
-    int total;         // places
+    int total;         // places, below 2^30
     int n;             // CTAs that have places
     int heads;         // key-value heads * row tiles
     int pad;
+    int tiles;         // of one head and row tile
     int each, more;    // places of a CTA; the first `more` CTAs take one more
     // tiles_all = tile_off[B], first_off = tile_off[0]
     __device__ __forceinline__ AttnSplit(const AttnParams& p, int tiles_all, int first_off) {
@@ -110,9 +111,10 @@ struct AttnSplit {
         pad = p.pad;
         const long long most = (long long)p.B * (((long long)p.width * p.page_size + kTile - 1) / kTile);
         const long long all = ((long long)tiles_all + (long long)p.pad * p.B) * heads;
-        const bool ok = tiles_all >= 0 && tiles_all <= most && first_off == 0 && all < (1LL << 31);
+        const bool ok = tiles_all >= 0 && tiles_all <= most && first_off == 0 && all < (1LL << 30);
         if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x % 32 == 0) raise_status(p.status, kBadLength);
         total = ok ? (int)all : 0;
+        tiles = ok ? tiles_all : 0;
         n = total < p.ctas ? total : p.ctas;
         if (p.spare && n) {
             // few places: a place more is half a step, a part more a read of the join
@@ -126,6 +128,10 @@ struct AttnSplit {
         each = n ? total / n : 0;
         more = n ? total - each * n : 0;
     }
+    // Place of request b's first segment, in units of `heads` places, from the
+    // entry tile_off[b].  An entry out of range is taken as the nearest one
+    // within, so no place leaves the list whatever tile_off holds.
+    __device__ __forceinline__ int at(int entry, int b) const { return min(max(entry, 0), tiles) + pad * b; }
     __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
     __device__ __forceinline__ int cta_of(int t) const {
         const int longer = more * (each + 1);
@@ -141,13 +147,22 @@ struct AttnSegment {
     __device__ __forceinline__ int tile(const AttnSplit& sp, int t) const { return min(max(0, t - t0 - sp.pad), tiles); }
 };
 
+// Tiles of a request of `len` positions.  What tile_off says of a request is
+// compared with it: attn_offsets_fit for the status, and before a segment is
+// worked on, since positions and table entries follow from its tiles.
+__device__ __forceinline__ int attn_tiles(int len) { return len > 0 ? (len - 1) / kTile + 1 : 0; }
+__device__ __forceinline__ bool attn_offsets_fit(const AttnParams& p, int b, int off, int next) {
+    const int len = p.kv_len[b];
+    return len >= 0 && len <= p.width * p.page_size && (unsigned)next - (unsigned)off == (unsigned)attn_tiles(len);
+}
+
 // What CTA c leaves of a segment that begins in it and goes on in the next.
 __device__ __forceinline__ AttnSplitRow attn_split_row(const AttnSplit& sp, const AttnSegment& g, int c, int q0, int r0, int rows) {
     return AttnSplitRow{sp.cta_of(g.t0 + sp.pad + g.tiles - 1) - c + 1, q0, g.h, r0, rows, {0, 0, 0}};
 }
 
 // Place of request b's first segment, in units of `heads` places.
-__device__ __forceinline__ int attn_request_at(const AttnParams& p, int b) { return p.tile_off[b] + p.pad * b; }
+__device__ __forceinline__ int attn_request_at(const AttnParams& p, const AttnSplit& sp, int b) { return sp.at(p.tile_off[b], b); }
 
 // The segment at place t of request b, whose places begin at off * heads and
 // end at next * heads.
@@ -165,11 +180,11 @@ __device__ __forceinline__ AttnSegment attn_segment_of(const AttnParams& p, cons
 }
 
 // The segment at place t, looked up by a whole warp: the request whose places
-// enclose t, 32 requests at a time (`mine`: this lane's value of the first
+// enclose t, 32 requests at a time (`entry`: this lane's entry of the first
 // round, attn_first_round).
-__device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnSplit& sp, int t, int mine) {
+__device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const AttnSplit& sp, int t, int entry) {
     const int lane = threadIdx.x & 31, tt = t / sp.heads;
-    int lo = 0, stride = (p.B + 31) / 32;
+    int lo = 0, stride = (p.B + 31) / 32, mine = sp.at(entry, min(p.B, lane * stride));
     for (;;) {
         const unsigned le = __ballot_sync(~0u, mine <= tt && lo + lane * stride < p.B);
         const int k = le ? 31 - __clz(le) : 0;
@@ -177,15 +192,15 @@ __device__ __forceinline__ AttnSegment attn_segment(const AttnParams& p, const A
         if (stride == 1) {
             const int off = __shfl_sync(~0u, mine, k);
             int next = __shfl_sync(~0u, mine, (k + 1) & 31);
-            if (k == 31) next = attn_request_at(p, min(p.B, lo + 1));
+            if (k == 31) next = attn_request_at(p, sp, min(p.B, lo + 1));
             return attn_segment_of(p, sp, t, lo, off, next);
         }
         stride = (stride + 31) / 32;
-        mine = attn_request_at(p, min(p.B, lo + lane * stride));
+        mine = attn_request_at(p, sp, min(p.B, lo + lane * stride));
     }
 }
 __device__ __forceinline__ int attn_first_round(const AttnParams& p) {
-    return attn_request_at(p, min(p.B, (int)(threadIdx.x & 31) * ((p.B + 31) / 32)));
+    return p.tile_off[min(p.B, (int)(threadIdx.x & 31) * ((p.B + 31) / 32))];
 }
 
 // ------------------------------------------------------------------- logits
