@@ -487,7 +487,8 @@ dspark_status dspark_cache_append(
  *          once.  Results do not depend on what it holds.
  * Limits : B as above, q_heads % kv_heads == 0, 1 <= max_new <=
  *          DSPARK_MAX_GAMMA + 1, scale positive and finite, head_dim % 8 == 0,
- *          <= DSPARK_MAX_HEAD_DIM, N * q_heads < 2^31.
+ *          <= DSPARK_MAX_HEAD_DIM, N * q_heads < 2^31, width * page_size <=
+ *          2^31 - 256.
  */
 size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new);
 dspark_status dspark_cache_attention(

@@ -63,6 +63,15 @@ def test_attention_refuses_bad_arguments(host):
     assert call(None, N=0) == 0
 
 
+@pytest.mark.parametrize("page,width,status", [(16, (1 << 27) - 16, 0), (16, (1 << 27) - 15, -1), (16, (1 << 27) - 1, -1),
+                                               (1, (1 << 31) - 256, 0), (1, (1 << 31) - 255, -1), (1, (1 << 31) - 1, -1)])
+def test_attention_refuses_tables_whose_positions_reach_the_end_of_32_bits(page, width, status):
+    """The positions of the two steps behind a length stay below 2^31."""
+    call = vm._lib.dspark_cache_attention
+    assert call(None, 1024, None, None, 1, 16384, 10, page, None, width, None, None, None, 2, 0, 8, 2, 128, 2, 1.0, None, None,
+                None, 0, None) == status
+
+
 def test_logits_refuse_bad_arguments(host):
     def call(p, t=0, rs=64, B=2, R=3, V=64, hist=None, hist_len=None, draft=None, ds=0, nb=1 << 20,
              fill=float("-inf")):

@@ -109,8 +109,9 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
                                      void* ws, size_t ws_bytes, void* stream) {
     const CallRange range_(__func__);
     if (!dtype_ok(kv_t)) return DSPARK_ERR_UNSUPPORTED;
+    // (the kernels look up to two steps of 128 positions beyond a length)
     if (!attn_sizes_ok(B, q_heads, kv_heads, head_dim, max_new) || N < 0 || width < 1 || !pages_ok(pages, page_size) ||
-        (long long)width * page_size >= (1LL << 31) || (long long)N * q_heads >= (1LL << 31))
+        (long long)width * page_size > (1LL << 31) - 256 || (long long)N * q_heads >= (1LL << 31))
         return DSPARK_ERR_INVALID;
     if (!(scale > 0.f && scale < 3e38f)) return DSPARK_ERR_INVALID;
     const int es = bytes_of(kv_t);
