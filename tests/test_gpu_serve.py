@@ -482,6 +482,31 @@ def test_attention_reports_tile_offsets_out_of_range(vm, B, D, dtype, wide):
     assert torch.equal(out, want) and torch.equal(lse, wlse) and _status(vm, ws) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attention_reports_query_offsets_out_of_range(vm, dtype):
+    """q_off beyond N, descending, negative, and so large that the tokens behind
+    them pass 2^31: status bit 1, the other requests' rows as they should be."""
+    rng = np.random.default_rng(40)
+    lens, news, B, N = [70, 5, 130, 40], [2, 3, 1, 2], 4, 8
+    a = _attention_inputs(rng, lens, news, 4, 2, 64, 16, dtype)
+    off = a["q_off"].tolist()
+    M = 2 ** 31 - 1
+    for bad, good in (([0, 2, 5, 9, 11], [0, 1]), ([0, 2, M, -2 ** 31, -2 ** 31 + 1], [0]), ([0, 2, 5, M, -2 ** 31], [0, 1]),
+                      ([-3, 2, 5, 6, 8], [1, 2, 3]), ([0, 2, 5, 4, 4], [0, 1]), ([M - 2, M, M, M, M], []), ([0, 2, 5, 6, M], [0, 1, 2]),
+                      ([-2 ** 31, M, -2 ** 31, M, -2 ** 31], [])):
+        big = torch.full((N + 40, 4, 64), 7.0, dtype=dtype, device="cuda")
+        ws = vm.CacheWorkspace(B, 4, 2, 64, 3)
+        lse = torch.full((N, 4), 7.0, device="cuda")
+        vm.dspark_cache_attention(a["q"], a["k"], a["v"], a["table"], a["kv_len"], _cu(bad), a["tile_off"], big[20:20 + N], ws,
+                                  max_new=3, lse=lse)
+        assert _status(vm, ws) == BAD_LENGTH, bad
+        assert bool((big[:20] == 7).all()) and bool((big[20 + N:] == 7).all())
+        for b in good:
+            assert bad[b:b + 2] == off[b:b + 2]
+        if good:
+            _rows_as_defined(a, big[20:20 + N], lse, good)
+
+
 def test_attention_in_a_cuda_graph(vm):
     rng = np.random.default_rng(14)
     a = _attention_inputs(rng, [300, 20], [8, 2], 8, 2, 128, 16, torch.bfloat16)

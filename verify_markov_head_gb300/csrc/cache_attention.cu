@@ -32,10 +32,10 @@ struct RowMap {
         q0 = p.q_off[b];
         n = p.q_off[b + 1] - q0;
         len = p.kv_len[b];
-        if (n > p.max_new || n < 0 || q0 < 0 || q0 + n > p.N || (long long)len > (long long)p.width * p.page_size || len < 0) {
+        // (n is right modulo 2^32; with q0 in range and n in [0, max_new], q0 + n is compared without a sum)
+        if (n > p.max_new || n < 0 || q0 < 0 || q0 > p.N - n || (long long)len > (long long)p.width * p.page_size || len < 0) {
             if (threadIdx.x == 0) raise_status(p.status, kBadLength);
-            n = max(0, min(n, min(p.max_new, p.N - q0)));
-            if (q0 < 0) n = 0;
+            n = q0 < 0 ? 0 : max(0, min(n, min(p.max_new, p.N - q0)));
             len = max(0, min(len, p.width * p.page_size));
         }
     }
