@@ -507,6 +507,26 @@ def test_attention_reports_query_offsets_out_of_range(vm, dtype):
             _rows_as_defined(a, big[20:20 + N], lse, good)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attention_reports_query_offsets_of_requests_without_positions(vm, dtype):
+    """More tokens than max_new, or rows beyond N, of a request with an empty cache."""
+    rng = np.random.default_rng(41)
+    a = _attention_inputs(rng, [70, 0, 20], [2, 2, 2], 4, 2, 64, 16, dtype)
+    out, lse, ws = _attend(vm, a, 2)
+    assert _status(vm, ws) == 0
+    _rows_as_defined(a, out, lse, [0, 1, 2])
+    for lens, bad, good in (([70, 0, 20], [0, 2, 6, 6], [0]), ([70, 20, 0], [0, 2, 4, 2 ** 31 - 1], [0, 1]), ([0, 20, 70], [-1, 2, 4, 6], [1, 2]),
+                            ([70, 20, 0], [0, 2, 4, 3], [0, 1])):
+        a = _attention_inputs(rng, lens, [2, 2, 2], 4, 2, 64, 16, dtype)
+        big = torch.full((46, 4, 64), 7.0, dtype=dtype, device="cuda")
+        lse = torch.full((6, 4), 7.0, device="cuda")
+        vm.dspark_cache_attention(a["q"], a["k"], a["v"], a["table"], a["kv_len"], _cu(bad), a["tile_off"], big[20:26], ws,
+                                  max_new=2, lse=lse)
+        assert _status(vm, ws) == BAD_LENGTH, bad
+        assert bool((big[:20] == 7).all()) and bool((big[26:] == 7).all())
+        _rows_as_defined(a, big[20:26], lse, good)
+
+
 def test_attention_in_a_cuda_graph(vm):
     rng = np.random.default_rng(14)
     a = _attention_inputs(rng, [300, 20], [8, 2], 8, 2, 128, 16, torch.bfloat16)

@@ -930,6 +930,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             if (tid == 0 && !attn_offsets_fit(p, b, off, next)) raise_status(p.status, kBadLength);
             if (next > off) continue;
             int q0 = p.q_off[b], n = p.q_off[b + 1] - q0;
+            if (tid == 0 && (n > p.max_new || n < 0 || q0 < 0 || q0 > p.N - n)) raise_status(p.status, kBadLength);
             n = q0 < 0 ? 0 : max(0, min(n, min(p.max_new, p.N - q0)));
             for (int i = tid; i < n * p.Hq * hd; i += kSoftWarps * 32) static_cast<uint16_t*>(p.out)[(size_t)q0 * p.Hq * hd + i] = 0;
             if (p.lse)
