@@ -428,10 +428,11 @@ dspark_status dspark_sts_fit(const float* score, const int32_t* acc_len, int N, 
  *          table in use), ring [pages] and ring_state [2] = (head, free): the
  *          free pages are ring[(head + i) % pages], i < free.
  * Outputs: block_table [B][width] and ring, in place; owned_out [B] and
- *          ring_state_out [2], which must not be owned and ring_state (the
- *          next step's inputs); kv_len [B], q_off and tile_off [B+1], slot_map
- *          and positions [max_tokens].  The same inputs give the same outputs,
- *          so a repeated call is harmless.
+ *          ring_state_out [2] (the next step's inputs); kv_len [B], q_off and
+ *          tile_off [B+1], slot_map and positions [max_tokens].  None of them
+ *          may overlap an input or another output (kv_len is not seq_len,
+ *          owned_out not owned): such a call is refused.  The same inputs give
+ *          the same outputs, so a repeated call is harmless.
  * Requests are served in order while the ring has pages for them.  One that
  * is not served (no page left, a table row too short, a length out of range)
  * keeps its pages, gets kv_len 0 and slots -1, and sets status bit 5.  Its

@@ -164,6 +164,31 @@ def test_plan_stops_its_sums_and_reports_too_many_tokens(vm):
     np.testing.assert_array_equal(got["ring"], ring)
 
 
+def test_plan_refuses_outputs_that_overlap_its_inputs_or_each_other(vm):
+    """kv_len in place of seq_len and the like: CTAs read the lengths again while the first one writes."""
+    rng = np.random.default_rng(6)
+    B, P, T = 40, 16, 300
+    seq, new, owned, ring, state, table = _plan_inputs(rng, B, P, 200, 8, 16, 90, ended=0.0)
+    i = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    ins = dict(seq_len=_cu(seq), n_new=_cu(new), owned=_cu(owned), ring=_cu(ring), ring_state=_cu(state), block_table=_cu(table))
+    outs = dict(owned_out=i(B), ring_state_out=i(2), kv_len=i(B), q_off=i(B + 1), tile_off=i(B + 1), slot_map=i(T), positions=i(T))
+    vm.dspark_cache_plan(**ins, page_size=P, **outs)
+    torch.cuda.synchronize()
+    pair = i(2 * B)
+    pair[:B] = ins["seq_len"]
+    for kw in (dict(kv_len=ins["seq_len"]), dict(kv_len=ins["n_new"]), dict(owned_out=ins["owned"]), dict(ring_state_out=ins["ring_state"]),
+               dict(seq_len=pair[:B], kv_len=pair[B - 1:2 * B - 1]), dict(positions=outs["slot_map"]), dict(tile_off=outs["q_off"]),
+               dict(ring_state_out=ins["seq_len"][3:5]), dict(kv_len=ins["block_table"].view(-1)[:B]), dict(slot_map=i(T)[:T], positions=ins["ring"][:T])):
+        if kw.get("positions") is not None and kw["positions"].numel() != T:
+            kw["slot_map"] = kw["slot_map"][:kw["positions"].numel()].contiguous()
+        with pytest.raises(vm.DsparkError):
+            vm.dspark_cache_plan(**{**ins, **outs, **kw}, page_size=P)
+    vm.dspark_cache_plan(**{**ins, **outs, "seq_len": pair[:B], "kv_len": pair[B:]}, page_size=P)     # side by side
+    same = dict(ins, n_new=ins["seq_len"])                                                            # inputs may be one
+    vm.dspark_cache_plan(**same, page_size=P, **outs)
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ append
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,H,D,P", [(1, 1, 8, 1), (5, 3, 64, 24), (700, 8, 128, 16), (333, 2, 80, 64), (0, 2, 64, 8)])

@@ -26,6 +26,16 @@ bool pages_ok(int pages, int page_size) {
     return pages >= 1 && page_size >= 1 && page_size <= DSPARK_MAX_PAGE_SIZE && (long long)pages * page_size < (1LL << 31);
 }
 
+// A run of n 32-bit words.
+struct Words {
+    const int32_t* p;
+    long long n;
+    bool meets(const Words& o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return n > 0 && o.n > 0 && a < b + 4 * o.n && b < a + 4 * n;
+    }
+};
+
 // Workspaces: the status word in the first 256 bytes, then the regions.
 constexpr size_t kHead = 256;
 
@@ -49,7 +59,16 @@ dspark_status dspark_cache_plan(const int32_t* seq_len, const int32_t* n_new, co
         !dev(owned_out) || !dev(ring_state_out) || !dev(kv_len) || !dev(q_off) || !dev(tile_off) ||
         (max_tokens > 0 && (!dev(slot_map) || !dev(positions))) || !dev_or_null(ws, 256))
         return DSPARK_ERR_INVALID;
-    if (owned_out == owned || ring_state_out == ring_state) return DSPARK_ERR_INVALID;
+    // the inputs are read again while the outputs are written
+    const Words in[] = {{seq_len, B}, {n_new, B}, {owned, B}, {ring_state, 2}};
+    const Words out[] = {{owned_out, B}, {ring_state_out, 2}, {kv_len, B}, {q_off, B + 1}, {tile_off, B + 1}, {slot_map, max_tokens},
+                         {positions, max_tokens}, {block_table, (long long)B * width}, {ring, pages}};
+    for (const Words& o : out) {
+        for (const Words& i : in)
+            if (o.meets(i)) return DSPARK_ERR_INVALID;
+        for (const Words* q = out; q != &o; ++q)
+            if (o.meets(*q)) return DSPARK_ERR_INVALID;
+    }
     PlanParams p;
     p.seq_len = seq_len; p.n_new = n_new; p.owned = owned;
     p.ring = ring; p.ring_state = ring_state; p.pages = pages;
