@@ -527,12 +527,14 @@ dspark_status dspark_cache_attention(
  *          live [B][R] (or NULL): the row's entries that the mask leaves and
  *          that are above -inf.  A row with none sets status bit 4: no token
  *          can be drawn from it.
- * Checks : a token id out of [0, V) is skipped and sets bit 0 (as do bias ids
- *          out of order), a length or offset out of range bit 1, rep not
+ * Checks : a token id out of [0, V) is skipped and sets bit 0, and so is a
+ *          bias entry whose id is not above every valid one before it in the
+ *          request; a length or offset out of range bit 1, rep not
  *          positive and finite bit 3.
  * ws     : dspark_logits_workspace_bytes(B, R) bytes, 256-byte aligned,
  *          cleared once.
- * Limits : V % 8 == 0, 1 <= R <= DSPARK_MAX_GAMMA + 1, B <= 65535.
+ * Limits : V % 8 == 0, 1 <= R <= DSPARK_MAX_GAMMA + 1, B <= 65535,
+ *          hist_stride < 2^28 (counts are held in 28 bits).
  */
 size_t dspark_logits_workspace_bytes(int B, int R);
 dspark_status dspark_logits_process(

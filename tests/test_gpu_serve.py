@@ -750,6 +750,32 @@ def test_logits_report_rows_with_nothing_left_and_bad_inputs(vm):
     assert _status(vm, ws) == BAD_LENGTH
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_logits_skip_invalid_biases_and_keep_the_valid_ones(vm, dtype):
+    """Ids out of range, out of order or twice: an entry counts where its id is
+    above every valid one before it, whatever stands beside it."""
+    rng = np.random.default_rng(26)
+    V = 4104
+    rows = [[10, -1], [100, 3, 200], [5, 5], [2 ** 31 - 1, 7, 4103], [4104, 4103], [9, 9, 9, 11, -2 ** 31, 12, 11, 13],
+            [100, 3, 50, 100, 4000], [0, 1, 2], [-1], [], [4103, 0, 4102], rng.integers(-50, V + 50, 300).tolist()]
+    a = _logit_inputs(rng, len(rows), 3, V, dtype, 40)
+    vals = [rng.standard_normal(len(r)).astype(np.float32) * 8 for r in rows]
+    kept = []
+    for r, w in zip(rows, vals):
+        top, d = -1, {}
+        for v, y in zip(r, w):
+            if top < v < V:
+                top, d[v] = v, float(y)
+        kept.append(d)
+    assert sum(map(len, kept)) < sum(map(len, rows))
+    off = np.concatenate([[0], np.cumsum([len(r) for r in rows])])
+    out, live, ws = _process(vm, dict(a, bias=kept), bias_tok=_cu(sum(rows, [])), bias_val=_cu(np.concatenate(vals), torch.float32), bias_off=_cu(off))
+    assert _status(vm, ws) == BAD_TOKEN
+    _check_logits(dict(a, bias=kept), out, live)
+    want, live2, _ = _process(vm, dict(a, bias=kept), ws=ws)
+    assert _status(vm, ws) == 0 and torch.equal(out, want) and torch.equal(live, live2)
+
+
 def test_logits_with_a_finite_fill(vm):
     """The rows of a draft take a finite value under the mask; the entries left
     and the rows with nothing left are counted as with -inf."""

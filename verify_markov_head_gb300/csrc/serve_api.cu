@@ -194,7 +194,7 @@ dspark_status dspark_logits_process(const void* logits, dspark_dtype t, long lon
         return DSPARK_ERR_INVALID;
     if (!dev(logits, 16) || !dev(out, 16) || !dev(ws, 256) || ws_bytes < need) return DSPARK_ERR_INVALID;
     if (out == logits && row_stride != V) return DSPARK_ERR_INVALID;      // in place: the same rows
-    if (hist && (!dev(hist) || !dev(hist_len) || !dev_or_null(prompt_len) || hist_stride < 0)) return DSPARK_ERR_INVALID;
+    if (hist && (!dev(hist) || !dev(hist_len) || !dev_or_null(prompt_len) || hist_stride < 0 || hist_stride >= (1 << 28))) return DSPARK_ERR_INVALID;
     if (!hist && (hist_len || prompt_len)) return DSPARK_ERR_INVALID;
     if (draft_tok && (!dev(draft_tok) || draft_stride < R - 1)) return DSPARK_ERR_INVALID;
     if (!dev_or_null(rep) || !dev_or_null(freq) || !dev_or_null(pres) || !dev_or_null(mask) || !dev_or_null(live))
