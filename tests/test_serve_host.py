@@ -1,6 +1,9 @@
 """Host-side checks of the serving operators' C ABI that need no GPU: bad
 arguments are refused before the device is touched, workspaces are sized."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -92,6 +95,71 @@ def test_the_workspace_holds_two_tiles_of_rows_a_cta(heads, new):
     tile = max(8 if rows <= 8 else 32, min(128, 16 if rows <= 16 else 32 if rows <= 32 else 64 if rows <= 64 else 128))
     for D in (8, 64, 256):
         assert vm.dspark_cache_workspace_bytes(3, 2 * heads, 2, D, new) >= 256 + 152 * 32 + 2 * 152 * tile * (D + 2) * 4
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_the_draft_and_verification_import_without_the_serving_module():
+    """Under another PyTorch than the module was built for: the package imports
+    and the library answers; a serving operator says what is missing."""
+    code = """
+import torch
+torch.__version__ = "0.0+other"
+import verify_markov_head_gb300 as vm
+assert vm.dspark_version() > 0 and vm.dspark_workspace_bytes(4, 7, 1024, 64) > 0
+assert vm.dspark_cache_workspace_bytes(64, 32, 8, 128, 8) > 0
+for _ in range(2):
+    try:
+        vm.dspark_cache_append(None, None, None, None, None)
+    except ImportError as e:
+        assert "0.0+other" in str(e) and "build.py" in str(e), e
+    else:
+        raise AssertionError("no error")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.fixture
+def builder(tmp_path, monkeypatch):
+    """build.py with an output folder of its own and compilers that only write their output files."""
+    from verify_markov_head_gb300 import build
+
+    tool = tmp_path / "bin" / "nvcc"
+    tool.parent.mkdir()
+    tool.write_text(f"#!{sys.executable}\nimport sys\nopen(sys.argv[sys.argv.index('-o') + 1], 'w').write('made')\n")
+    tool.chmod(0o755)
+    (tool.parent / "g++").write_text(tool.read_text())
+    (tool.parent / "g++").chmod(0o755)
+    monkeypatch.setenv("NVCC", str(tool))
+    monkeypatch.setenv("PATH", f"{tool.parent}{os.pathsep}{os.environ['PATH']}")
+    monkeypatch.setattr(build, "OUT", str(tmp_path / "out"))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "out" / "libdspark.so"))
+    return build
+
+
+def test_the_library_builds_without_pytorch(builder, monkeypatch):
+    made = lambda: sorted(f for f in os.listdir(builder.OUT) if f.endswith(".so"))  # noqa: E731
+    find = builder.importlib.util.find_spec
+    monkeypatch.setattr(builder.importlib.util, "find_spec", lambda name: None if name == "torch" else find(name))
+    assert builder.build() == builder.LIB
+    assert made() == ["libdspark.so"]
+    at = os.path.getmtime(builder.LIB)
+    assert builder.build() == builder.LIB and os.path.getmtime(builder.LIB) == at     # nothing to do
+    monkeypatch.setattr(builder.importlib.util, "find_spec", find)
+    builder.build()                                              # PyTorch is there now: the module too
+    assert made() == [f"_serve-{torch.__version__}.so", "libdspark.so"]
+
+
+def test_the_library_stands_where_the_python_module_does_not_compile(builder, monkeypatch):
+    def broken(cc):
+        raise RuntimeError("g++ failed on serve_py.cpp")
+
+    monkeypatch.setattr(builder, "_compile_serve", broken)
+    with pytest.raises(RuntimeError, match="serve_py.cpp"):
+        builder.build()
+    assert os.listdir(builder.OUT).count("libdspark.so") == 1
 
 
 def _plan_args(B=3, T=5):

@@ -43,14 +43,25 @@ def _load_serve():
     tensors and calls the library in a third of the time that Python takes."""
     path = os.path.join(os.path.dirname(lib_path), f"_serve-{torch.__version__}.so")
     if not os.path.exists(path):
-        raise ImportError(f"{path} is not built for this PyTorch; run verify_markov_head_gb300/build.py")
+        raise ImportError(f"the serving operators' module is not built for this PyTorch ({path}); "
+                          "run verify_markov_head_gb300/build.py -v")
     spec = importlib.util.spec_from_file_location("_serve", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     return module
 
 
-_serve = _load_serve()
+class _Serving:
+    """Stands for the module until a serving operator is called: the draft and
+    the verification need the library only."""
+
+    def __getattr__(self, name):
+        global _serve
+        _serve = _load_serve()
+        return getattr(_serve, name)
+
+
+_serve = _Serving()
 
 _vp, _i, _f, _u64, _sz, _ll = C.c_void_p, C.c_int, C.c_float, C.c_uint64, C.c_size_t, C.c_longlong
 _lib.dspark_version.restype = _i

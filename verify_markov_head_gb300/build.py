@@ -3,8 +3,9 @@
 Each translation unit under csrc/ is compiled separately (in parallel) and
 linked into verify_markov_head_gb300/_lib/libdspark.so with the CUDA runtime
 linked statically, so the library needs nothing from the Python environment.
-Beside it the Python module of the serving operators (csrc/serve_py.cpp) is
-built with the headers of the installed PyTorch, whose version is in its name.
+Beside it, where PyTorch is installed, the Python module of the serving
+operators (csrc/serve_py.cpp) is built with its headers; its version is in the
+module's name.
 """
 from __future__ import annotations
 
@@ -45,11 +46,26 @@ def _stale(lib):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def torch_dir() -> str:
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+def torch_dir():
+    """PyTorch's folder, None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def serve_lacks():
+    """What the Python module's build needs and does not find, None where all is there."""
+    torch = torch_dir()
+    if torch is None:
+        return "PyTorch"
+    if not os.path.exists(os.path.join(torch, "include", "c10", "cuda", "CUDAStream.h")):
+        return "PyTorch's CUDA headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None if shutil.which("g++") else "g++"
 
 
 def serve_module() -> str:
+    """Where the Python module of this PyTorch is built."""
     version: dict = {}
     with open(os.path.join(torch_dir(), "version.py")) as f:      # (without importing torch)
         for line in f:
@@ -73,7 +89,8 @@ def _compile_serve(cc):
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not _stale(LIB) and not _stale(serve_module()):
+    lacks = serve_lacks()
+    if not force and not _stale(LIB) and (lacks or not _stale(serve_module())):
         return LIB
     os.makedirs(OUT, exist_ok=True)
     cc = nvcc()
@@ -90,15 +107,19 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        serve = ex.submit(_compile_serve, cc)
+        serve = None if lacks else ex.submit(_compile_serve, cc)
         objs = list(ex.map(compile_one, sources()))
-        serve_obj, torch_lib = serve.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    if serve is None:
+        if verbose:
+            print(f"the serving operators' Python module is not built: no {lacks}", file=sys.stderr)
+        return LIB
+    serve_obj, torch_lib = serve.result()            # (the library stands whatever came of the module)
     module = serve_module()
     tmp = module + f".tmp{os.getpid()}"
     r = subprocess.run(["g++", "-shared", "-o", tmp, serve_obj, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
