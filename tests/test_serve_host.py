@@ -121,6 +121,12 @@ for _ in range(2):
     assert r.returncode == 0, r.stderr
 
 
+def test_the_default_stream_of_a_call_is_the_current_one_by_pytorchs_public_function(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("S", (), {"cuda_stream": 1234}))
+    assert vm._stream(None) == 1234
+    assert vm._stream(77) == 77 and vm._stream(type("S", (), {"cuda_stream": 5})) == 5
+
+
 @pytest.fixture
 def builder(tmp_path, monkeypatch):
     """build.py with an output folder of its own and compilers that only write their output files."""

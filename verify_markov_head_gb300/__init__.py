@@ -160,8 +160,7 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        # the handle of torch.cuda.current_stream(), without building the object (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 
