@@ -475,6 +475,9 @@ dspark_status dspark_cache_append(
  *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j e^(scale * q . k_j).
  * A row that sees no position (kv_len 0) gets out = 0 and lse = -inf.  What
  * a page holds beyond kv_len is never used, whatever its bits.
+ * Products and sums are held in fp32.  In bf16 calls the softmax's weights
+ * take part in the second product to 2^-15 of each; where max_new * q_heads /
+ * kv_heads is above 64 they may be rounded to bf16 (2^-8 of each).
  * Inputs : q [N][q_heads][head_dim] (kv_t), q_stride elements between tokens;
  *          caches, block_table, kv_len, q_off, tile_off as dspark_cache_plan
  *          leaves them; max_new >= every n.

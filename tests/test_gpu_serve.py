@@ -507,6 +507,44 @@ def test_attention_reports_tile_offsets_out_of_range(vm, B, D, dtype, wide):
     assert torch.equal(out, want) and torch.equal(lse, wlse) and _status(vm, ws) == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,new,D,P", [(4, 4, 1, 128, 16), (8, 2, 3, 64, 16), (16, 2, 4, 128, 64), (8, 2, 8, 96, 16), (8, 2, 8, 64, 4),
+                                            (16, 2, 8, 128, 16), (16, 2, 8, 64, 8), (16, 2, 8, 256, 16), (8, 2, 8, 256, 12), (16, 2, 8, 80, 1)])
+def test_attention_of_up_to_64_rows_holds_its_weights_to_2_to_the_minus_15(vm, Hq, Hkv, new, D, P):
+    """4 to 64 rows a key head: a weight w enters the second product as its leading 8
+    bits, cut off, and the rest of (1 + 2^-20) w rounded to 8 bits: off by at most
+    2^-8 (2^-7 + 2^-20) w + 2^-20 w.  The product's 2 len / 16 additions in binary32
+    may each cut off 2^-23 of the sum of magnitudes."""
+    rng = np.random.default_rng(Hq + D + P)
+    lens = [700, 64, 129]
+    a = _attention_inputs(rng, lens, [new] * 3, Hq, Hkv, D, P, torch.bfloat16)
+    out, _, ws = _attend(vm, a, new)
+    d = lambda t: t.cpu().double().numpy()  # noqa: E731
+    i = lambda t: t.cpu().numpy()  # noqa: E731
+    weight = 2.0 ** -8 * (2.0 ** -7 + 2.0 ** -20) + 2.0 ** -20 + max(lens) / 8 * 2.0 ** -23
+    want, _, tol, _ = ref.attention(d(a["q"]), d(a["k"]), d(a["v"]), i(a["table"]), i(a["kv_len"]), i(a["q_off"]), D ** -0.5, weight, ref.EPS16)
+    assert _status(vm, ws) == 0
+    assert (np.abs(d(out) - want) <= tol).all(), (np.abs(d(out) - want) / tol).max()
+
+
+@pytest.mark.parametrize("dtype,Hq,wide", [(torch.bfloat16, 2, 0), (torch.bfloat16, 8, 0), (torch.bfloat16, 16, 0), (torch.bfloat16, 32, 30000),
+                                           (torch.float32, 8, 0)])
+def test_an_infinite_value_in_the_history_gives_the_infinity_of_the_definition(vm, dtype, Hq, wide):
+    """Values that every row sees, with weights that are powers of two and others."""
+    rng = np.random.default_rng(44)
+    a = _attention_inputs(rng, [300, 20], [8, 8], Hq, 2, 64, 16, dtype, wide=wide)
+    clean, _, _ = _attend(vm, a, 8)
+    for b, pos, dim, bad in ((0, 0, 0, float("inf")), (0, 130, 1, -float("inf")), (0, 250, 2, float("nan")), (0, 5, 3, float("inf")),
+                             (0, 200, 3, float("inf")), (0, 7, 4, float("inf")), (0, 8, 4, -float("inf")), (1, 3, 5, -float("inf"))):
+        a["v"][int(a["table"][b, pos // 16]), :, pos % 16, dim] = bad
+    a["q"][9] = 0                                   # all weights of this row are 1
+    got, _, _ = _attend(vm, a, 8)
+    inf = float("inf")
+    for b, dim, value in ((0, 0, inf), (0, 1, -inf), (0, 3, inf), (1, 5, -inf)):
+        assert bool((got[8 * b:8 * b + 8, :, dim] == value).all()), (b, dim)
+    assert bool(torch.isnan(got[:8, :, [2, 4]]).all())
+    assert torch.equal(got[:8, :, 5:], clean[:8, :, 5:]) and torch.equal(got[10:, :, 6:], clean[10:, :, 6:])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_attention_reports_query_offsets_out_of_range(vm, dtype):
     """q_off beyond N, descending, negative, and so large that the tokens behind

@@ -56,8 +56,19 @@
 // us, 384 in pairs and kept.  A second buffer for P gained nothing (64 rows
 // 202, short ones 74).
 //
-// Weights are rounded to bf16 for the second product (relative 2^-8 of each
-// weight, independent in sign); their sum l is taken in fp32 before rounding.
+// Weights go into the second product as two bf16 parts, the leading 8 bits and
+// the rest (what is left is 2^-15 of a weight): with one part, rounded, the
+// outputs' error against 64 bits is 2.3e-3 of their norm, with two 1.7e-3, the
+// rounding of the outputs themselves.  Up to 32 columns the parts are columns of
+// one product, whose time does not grow with them, and the halves of O^T are
+// added at a segment's end; of 64 columns the second part is a product of its
+// own.  One part / two, us: 64 requests of 32 rows 182.1 / 183.1 (the second part
+// as its own product 184.6), of 64 rows 190 / 196, 131072 positions of 64 rows
+// 88.6 / 90.4, 256 requests of 8 rows 322.4 / 323.2, head size 64 with 32 rows 107
+// / 114, with 64 148 / 185.  128 columns keep one part, rounded to nearest, since
+// shared memory does not hold another (taken as two tiles of 64 columns they
+// read the cache twice: 390 us for 237): more than 64 rows of a key head have the
+// larger error.  The sum l is taken in fp32 of the whole weights.
 #include <cudaTypedefs.h>
 
 #include "pdl.cuh"
@@ -101,6 +112,9 @@ struct Seg {
     int page[16];             // the pages of the first step's boxes
 };
 
+// The weights' parts in P: one, two side by side, or two blocks (and products).
+enum class Weights { kOne, kBeside, kBlocks };
+
 // D: entries of a tile's row, the head size p.D rounded up to 64, 128 or 256.
 template <int N, int D, Copy kCopy>
 struct Smem {
@@ -111,15 +125,18 @@ struct Smem {
     // or [half][position][64] where the halves come apart
     static constexpr int kGroup = kCopy == Copy::kHalves ? 1024 : 8 * kUnit * 2;  // from 8 positions to the next 8
     static constexpr int kHalf = kCopy == Copy::kHalves ? kSteps * 128 : kUnit == 128 ? 1024 : 0;
-    static constexpr int kStages = (N == 128 ? 4 : 5) * 128 / kUnit;
+    static constexpr Weights kWeights = N <= 32 ? Weights::kBeside : N == 64 ? Weights::kBlocks : Weights::kOne;
+    static constexpr int kStages = (N == 128 || (N == 64 && D >= 128) ? 4 : 5) * 128 / kUnit;
     static constexpr int kQBytes = N * D * 2;
-    static constexpr int kQBufs = N * D <= 32 * 128 ? 4 : N == 128 || N * D == 64 * 256 ? 1 : 2;      // Q tiles: segments may be a step long
-    static constexpr int kCols = (2 + 2 * kUnits) * N;            // tensor memory: two S, two O of kUnits parts
+    // Q tiles: segments may be a step long
+    static constexpr int kQBufs = N <= 32 && N * D <= 32 * 128 ? 4 : N == 128 || N * D == 64 * 256 ? 1 : 2;
+    static constexpr int kO = kWeights == Weights::kBeside ? 2 * N : N;      // columns of an O^T
+    static constexpr int kCols = 2 * N + 2 * kUnits * kO;         // tensor memory: two S, two O of kUnits parts
     static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kRing = 0;
     static constexpr int kQ = kRing + kStages * kTileBytes;
-    static constexpr int kP = kQ + kQBufs * kQBytes;                   // [128][64] bf16, 128-byte rows (128 columns: twice)
-    static constexpr int kPBytes = kSteps * 128 * (N == 128 ? 2 : 1);
+    static constexpr int kP = kQ + kQBufs * kQBytes;                   // [128][64] bf16, 128-byte rows (columns 64 .., or the second part: another)
+    static constexpr int kPBytes = kSteps * 128 * (N >= 64 ? 2 : 1);
     static constexpr int kMax = kP + kPBytes;                     // [2][N][4], by the step's parity
     static constexpr int kSum = kMax + 2 * N * 16;                    // [2][N][4], by the segment's parity
     static constexpr int kNeg = kSum + 2 * N * 16;                    // [N], where 32 columns a thread leave no registers for it
@@ -206,6 +223,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Weights x, y >= 0 as a leading part, cut off, and the rest.  The rest is made of
+// (1 + 2^-20) times the weight, so that it is above zero wherever the weight is:
+// an infinite value then gives the same infinity with both parts.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& high, uint32_t& low) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    high = __byte_perm(a, b, 0x7632);
+    constexpr float kUp = 1.f + 0x1p-20f;
+    low = pack_bf16(fmaf(x, kUp, -__uint_as_float(a & 0xffff0000u)), fmaf(y, kUp, -__uint_as_float(b & 0xffff0000u)));
+}
+
+__device__ __forceinline__ void store_chunk(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // Two 16-bit halves of w with the non-finite bf16 ones cleared.
@@ -514,7 +545,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         // the whole warp runs the loop, so that descriptors are uniform values;
         // one elected lane issues
         constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, N, false, false);
-        constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, N, true, true);
+        constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, L::kO, true, true);
         const uint32_t one = elect_one();
         const uint64_t k_desc = ptx::smem_desc_sw128(base + L::kRing, 16, L::kGroup);
         // V^T: entries of a position lie along M, the 64-entry halves kHalf
@@ -551,9 +582,11 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             const uint32_t st = (vi + u) % kStages;
                             const uint64_t va = v_desc + st * (L::kTileBytes / 16);
 #pragma unroll
-                            for (int k = 0; k < kSteps / 16; ++k)
-                                ptx::mma_f16(tmem + 2 * N + (ob * kUnits + u) * N, va + k * (2 * L::kGroup / 16),
-                                             p_desc + k * (2048 / 16), id_o, old.first && k == 0 ? 0u : 1u);
+                            for (int w = 0; w < (L::kWeights == Weights::kBlocks ? 2 : 1); ++w)
+#pragma unroll
+                                for (int k = 0; k < kSteps / 16; ++k)
+                                    ptx::mma_f16(tmem + 2 * N + (ob * kUnits + u) * L::kO, va + k * (2 * L::kGroup / 16),
+                                                 p_desc + w * (kSteps * 128 / 16) + k * (2048 / 16), id_o, old.first && w + k == 0 ? 0u : 1u);
                             ptx::mma_commit(b_empty + 8 * st);
                         }
                         ptx::mma_commit(b_pv);
@@ -651,7 +684,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
             struct { int n, len, r0, pos0, pos1, steps; } d = {sg.n, sg.len, sg.r0, sg.pos0, sg.pos1, sg.steps};
             const bool none = d.steps < 0;                         // no more segments
             if (none && !pend) break;
-            const uint32_t o_at = tmem + lanes + 2 * N + (si & 1u) * (kUnits * N) + group * HC;
+            const uint32_t o_at = tmem + lanes + 2 * N + (si & 1u) * (kUnits * L::kO) + group * HC;
             const int first_new = d.len - d.n;                     // position of the block's first token
             // lane c: the last position that column c of this group sees
             const int my_last = first_new + p.by_group(d.r0 + group * HC + (lane & (HC - 1)));
@@ -763,7 +796,7 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                         }
                         if (s > 0)
 #pragma unroll
-                            for (int u = 0; u < kUnits; ++u) {
+                            for (int u = 0; u < kUnits * L::kO / N; ++u) {
                                 float o[CH];
                                 tmem_get<CH>(o_at + u * N + k * CH, o);
 #pragma unroll
@@ -791,9 +824,18 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                             w[e + 1] = fast_exp2(x[c0 + e + 1]);
                             add_pair(l[k * CH + c0 + e], l[k * CH + c0 + e + 1], w[e], w[e + 1]);
                         }
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                     ::"r"(prow + ((((col0 + c0) / 8 & 7) ^ (row & 7)) << 4)), "r"(pack_bf16(w[0], w[1])),
-                                       "r"(pack_bf16(w[2], w[3])), "r"(pack_bf16(w[4], w[5])), "r"(pack_bf16(w[6], w[7])) : "memory");
+                        const int chunk = (col0 + c0) / 8;
+                        if constexpr (L::kWeights == Weights::kOne) {
+                            store_chunk(prow + (((chunk & 7) ^ (row & 7)) << 4), pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]),
+                                        pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7]));
+                        } else {
+                            uint32_t high[4], low[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) split_bf16(w[2 * e], w[2 * e + 1], high[e], low[e]);
+                            constexpr int kBlock = L::kWeights == Weights::kBlocks ? kSteps * 128 : 0;
+                            store_chunk(prow + ((chunk ^ (row & 7)) << 4), high[0], high[1], high[2], high[3]);
+                            store_chunk(prow + kBlock + (((kBlock ? chunk : chunk + N / 8) ^ (row & 7)) << 4), low[0], low[1], low[2], low[3]);
+                        }
                     }
                 }
                 if (NCH > 1) read_done();
@@ -848,8 +890,16 @@ attn_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
                 for (int i = 0; i < NCH * kUnits; ++i) {
                     const int k = i % NCH, u = i / NCH, dim = u * 128 + row;
                     float o[CH];
-                    if (ok) tmem_get<CH>(tmem + lanes + 2 * N + ((pi & 1u) * kUnits + u) * N + group * HC + k * CH, o);
-                    else {
+                    if (ok) {
+                        const uint32_t at = tmem + lanes + 2 * N + ((pi & 1u) * kUnits + u) * L::kO + group * HC + k * CH;
+                        tmem_get<CH>(at, o);
+                        if constexpr (L::kWeights == Weights::kBeside) {
+                            float y[CH];
+                            tmem_get<CH>(at + N, y);
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) o[c] += y[c];
+                        }
+                    } else {
 #pragma unroll
                         for (int c = 0; c < CH; ++c) o[c] = 0.f;
                     }
