@@ -358,6 +358,16 @@ def test_attention_of_a_large_ragged_batch(vm):
     _check_attention(a, out, lse, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("dtype,Hq", [(torch.bfloat16, 2), (torch.bfloat16, 8), (torch.float32, 2)])
+def test_attention_of_a_long_context(vm, dtype, Hq):
+    """131071 positions of one key head beside a short request: split over all SMs."""
+    rng = np.random.default_rng(78)
+    a = _attention_inputs(rng, [131071, 9], [2, 8], Hq, 1, 64, 64, dtype)
+    out, lse, ws = _attend(vm, a, 8)
+    _check_attention(a, out, lse, 64 ** -0.5)
+    assert _status(vm, ws) == 0
+
+
 def test_attention_scale_and_large_scores(vm):
     """A large scale makes the softmax a maximum: no overflow, the running
     maximum carries over the tiles."""
