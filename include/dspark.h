@@ -492,7 +492,11 @@ dspark_status dspark_cache_append(
  * Limits : B as above, q_heads % kv_heads == 0, 1 <= max_new <=
  *          DSPARK_MAX_GAMMA + 1, scale positive and finite, head_dim % 8 == 0,
  *          <= DSPARK_MAX_HEAD_DIM, N * q_heads < 2^31, width * page_size <=
- *          2^31 - 256.
+ *          2^31 - 256, and below 2^30 pieces of work (tiles of all requests x
+ *          kv_heads x tiles of 8 to 128 query rows; more set status bit 1 and
+ *          nothing is computed).  A prompt's chunk, which plan and append take whole, has to
+ *          pass in pieces of at most DSPARK_MAX_GAMMA + 1 tokens, each of which
+ *          reads the cache again.
  */
 size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new);
 dspark_status dspark_cache_attention(

@@ -21,9 +21,10 @@ namespace {
 // A few kilobytes are read and written, so latency bounds it.  Each CTA forms
 // the sums over all requests itself (B <= 4096 lengths, a few loads a thread)
 // instead of waiting for another launch, and then fills its share of the slot
-// map, the table entries and the ring entries.  64 requests 4.7 us, 512
-// requests with 135168 slots 6.3 us (5.6 and 7.4 with a second scan for the
-// rare case that the ring runs out in every call).
+// map, the table entries and the ring entries.  64 requests 4.8 us, 512
+// requests with 135168 slots 6.2 us (0.9 and 1.1 more with a second scan, for the
+// rare case that the ring runs out, in every call; 0.5 more with sums that
+// notice a carry instead of stopping by a minimum).
 constexpr int kPlanThreads = 1024;
 
 struct Sum4 { unsigned tok, need, give, tiles; };
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
 // cache[slot] = row: a copy, bound by HBM for prompts and by latency for a
 // block.  A thread keeps one 16-byte place of a token's row (its head and
 // place follow once) and moves it for kAppend tokens at a time, keys and
-// values: the loads do not wait for the slots.  512 tokens of 4 KB 2.0 us, 32768
+// values: the loads do not wait for the slots.  512 tokens of 4 KB 1.8 us, 32768
 // 42.2 us (6.4 TB/s, read and written).
 constexpr int kAppendThreads = 256, kAppend = 2;
 

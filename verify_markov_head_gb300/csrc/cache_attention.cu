@@ -71,10 +71,12 @@ __device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int cta
 // feed it bound a block's many rows, HBM a single row.  256 threads, MR = 8 or 32 rows, TT positions at a time: two
 // stages of keys and values by cp.async, 16-byte chunks swizzled so that eight
 // positions' chunks lie in different banks.
-// Measured on one GB300: 16 requests of up to 8192 positions, 8 fp32 heads of
-// 128, 32 rows: 623 us (18 TFLOP/s; 1075 us without the register tiles), one
-// row a head 4: 246 us (2.9 TB/s); a call of 4 short requests 12.1 us (14.3 us a
-// call without its programmatic launch, now 12.8).
+// Measured on one GB300: 16 requests of 2730-8192 positions, 8 fp32 heads of
+// 128, 0.72 GB, 32 rows: 629 us (18 TFLOP/s; 1075 us without the register tiles),
+// 4 rows: 245 us (2.9 TB/s), of 8192 positions each 808 and 305; a call of 4
+// short requests 12.3 us (14.3 us a call without its programmatic launch, now
+// 12.8).  Issue slots are used to 53 %, a warp waits for shared memory and for
+// its own products.
 //   scores   8 rows x TPT positions a thread over a quarter of the head
 //            (lane = position group + 8 * quarter), the quarters summed by
 //            shuffles, which leave each thread NR rows of one position;

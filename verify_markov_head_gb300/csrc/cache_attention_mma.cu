@@ -17,10 +17,10 @@
 // go to the same S^T and to two O^T.  Pages that are no boxes (not a multiple
 // of 8 positions, not a whole number of heads apart, or heads above 128 that
 // are no multiple of 64) are copied row by row, by cp.async of four warps.
-// 64 requests of 32 rows, and on CUDA cores before: head size 96 149 us (1900),
-// 192 283 (3230), 256 349 (3460); 128 in pages of 1 position 203 (1869).
+// 64 requests of 32 rows, and on CUDA cores before: head size 96 154 us (1900),
+// 192 284 (3230), 256 350 (3460); 128 in pages of 1 position 206 (1869).
 //
-// Roles (12 or 20 warps, 2 more row by row, one CTA per SM, a ring of 5 stages of 32 KB, 4 with 128 columns):
+// Roles (12 or 20 warps, 2 more row by row, one CTA per SM, a ring of 5 stages of 32 KB, 4 with 64 or 128 columns):
 //   first 8 or 16    softmax, 2 or 4 groups of 4 warps, each with its share of the
 //                    columns: thread = position; weights to shared memory
 //   then two         producers of the keys and of the values (lane = box of a page:
@@ -37,24 +37,26 @@
 // What bounds it: HBM.  A key-value head's position is 512 bytes (head size
 // 128) and 4 N multiply-adds per byte pair; at 6.8 TB/s an SM has 2800 cycles
 // for a step of 128 positions, of which the tensor core is busy 1024 (it reads
-// the 128 x 16 operand at 64 bytes a cycle, whatever N is up to 64) and a
-// softmax warp 600-1600.  So the work is to keep copies in flight: two producer
-// warps (one issued a tile in 1200 cycles with pages of 16 positions, too slow),
+// the 128 x 16 operand at 64 bytes a cycle, whatever N is up to 64; with 64
+// columns 1536) and a softmax warp 600-1600 (with weights of one part).  So the
+// work is to keep copies in flight: two producer warps (one issued a tile in
+// 1200 cycles with pages of 16 positions, too slow),
 // segment ends off the way (the rows are written behind the next segment's
 // first step), the split over CTAs weighted by segments (AttnSplit).
-// Measured on one GB300: 64 requests of 1024-8192 positions, 1.22 GB: 32 rows
-// 182 us (6.7 TB/s), 64 rows 190, 128 rows 236 (32 columns a thread: the
-// softmax bounds it); 256 requests of 128-4096, 8 rows, 2.22 GB: 318 us (7.0
-// TB/s); one of 131072, 64 rows, 0.54 GB: 88 us (6.1 TB/s, 6 us of it before
-// the ring is full and the join); 256 of 16-300 positions, 32 rows: 67 us (44 %
-// of the rate: a segment takes the softmax 9000 cycles, of which its beginning
-// and end are half).  Taking the column maxima in every step cost 263 us for
-// the first, one producer warp and serial segment ends 203, MMAs issued from a
-// diverged lane 203, an unweighted split 197, products in fixed order 188, a
-// barrier more in a segment's first step and at its end 184 (64 rows 197).
-// Exponents formed twice and column by column: head size 256 with 64 rows 418
-// us, 384 in pairs and kept.  A second buffer for P gained nothing (64 rows
-// 202, short ones 74).
+// Measured on one GB300 (another card reads up to 5 % more): 64 requests of
+// 1024-8192 positions, 1.22 GB: 32 rows 182 us (6.7 TB/s), 64 rows 195, 128 rows
+// 237 (32 columns a thread: the softmax bounds it); 256 requests of 128-4096, 8
+// rows, 2.22 GB: 318 us (7.0 TB/s); one of 131072, 64 rows, 0.54 GB: 90 us (6.0
+// TB/s, 6 us of it before the ring is full and the join); 256 of 16-300
+// positions, 32 rows: 68 us (43 % of the rate: a segment takes the softmax 9000
+// cycles, of which its beginning and end are half).
+// Steps on the way, with weights of one part, the first of these cases: column
+// maxima in every step 263 us, one producer warp and serial segment ends 203,
+// MMAs issued from a diverged lane 203, an unweighted split 197, products in
+// fixed order 188, a barrier more in a segment's first step and at its end 184
+// (64 rows 197), then 182 (190).  Exponents formed twice and column by column:
+// head size 256 with 64 rows 418 us, 384 in pairs and kept.  A second buffer for
+// P gained nothing (64 rows 202, short ones 74).
 //
 // Weights go into the second product as two bf16 parts, the leading 8 bits and
 // the rest (what is left is 2^-15 of a weight): with one part, rounded, the

@@ -114,8 +114,8 @@ template <> struct Row<uint16_t> {
 // in the ring, before the row leaves with the mask applied.
 // Measured on one GB300: 64 requests of 8 fp32 rows of 151936, a quarter of
 // them under a tight mask, 556 MB: 100 us (5.5 TB/s); 256 requests of 8 bf16
-// rows of 129280, half of them under a loose mask, 1067 MB: 184 us (5.8 TB/s; a
-// plain copy of these rows takes 156); one request 8.0 us.  On the way, the
+// rows of 129280, half of them under a loose mask, 1067 MB: 182 us (5.9 TB/s; a
+// plain copy of these rows takes 156); one request 7.3 us.  On the way, the
 // first of them: rows through registers with the formula inlined in the stream
 // 283 us, with the listed entries corrected in the output afterwards 119, with
 // mask words read by every thread (the first-level cache is small beside this
@@ -430,7 +430,7 @@ cudaError_t launch(const LogitsParams& p, cudaStream_t s) {
 
 // Entries of a CTA: 4096 (8192: b64 146 us, not 100; 512 threads: 108), or 2048
 // where that leaves SMs idle, and then, where it still does, 512 threads, which
-// read a history in half the turns (one request: 8.2 us, 10.4 with 256 threads).
+// read a history in half the turns (one request: 7.3 us, 8.1 with 256 threads).
 template <typename T, bool kMask>
 cudaError_t launch_range(const LogitsParams& p, cudaStream_t s) {
     constexpr int kUnit = 256 * Row<T>::kVec;

@@ -155,12 +155,15 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     const int rows = p.G * max_new;
     const bool mma = p.bf16;                       // tensor cores
     p.row_tile = attn_row_tile(rows, mma);
-    // tiles the block tables can hold: few of them, fewer rows at a time.  On
-    // CUDA cores where SMs would be idle otherwise; 128 rows in two tiles of 64 below
-    // 32 tiles an SM (8 requests of 8192 positions, 2 heads: 34 us, at once 37;
-    // 64 requests, 8 heads: 402 us, at once 236, the cache read once) and for
-    // heads above 128, whose O^T of 128 columns tensor memory does not hold, and
-    // row by row, where the copies bound it (64 rows: 250 us)
+    // tiles the block tables can hold (the lengths are on the device): few of
+    // them, fewer rows at a time.  On CUDA cores where SMs would be idle
+    // otherwise; 128 rows in two tiles of 64 below 32 tiles an SM and for heads
+    // above 128, whose O^T of 128 columns tensor memory does not hold, and row
+    // by row, where the copies bound it.  In two tiles / at once: 64 requests of
+    // 1024-8192 positions, 8 heads 390 / 237 us (the cache read once); 8 of 8192,
+    // 2 heads 32.3 / 32.3.  Tables far wider than the contexts go by the tables:
+    // of 131072 positions, 64 requests of 1000 111 / 84, 8 of 1000 28.3 / 30.4, 8
+    // of 100-300 19.8 / 24.4
     const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
     if (mma && p.row_tile == 128 && (head_dim > 128 || tiles < 32LL * num_sms() || !attn_pages_are_boxes(p))) p.row_tile = 64;
     if (!mma && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
