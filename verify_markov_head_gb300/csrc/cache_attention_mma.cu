@@ -67,10 +67,11 @@
 // own.  One part / two, us: 64 requests of 32 rows 182.1 / 183.1 (the second part
 // as its own product 184.6), of 64 rows 190 / 196, 131072 positions of 64 rows
 // 88.6 / 90.4, 256 requests of 8 rows 322.4 / 323.2, head size 64 with 32 rows 107
-// / 114, with 64 148 / 185.  128 columns keep one part, rounded to nearest, since
-// shared memory does not hold another (taken as two tiles of 64 columns they
-// read the cache twice: 390 us for 237): more than 64 rows of a key head have the
-// larger error.  The sum l is taken in fp32 of the whole weights.
+// / 114, with 64 148 / 185.  128 columns keep one part, rounded to nearest: 237
+// us for 64 requests, where two take 318 with the second one in the stage of the
+// keys, the only place left (64 columns 201 so, head size 64 167), and 390 as
+// two tiles of 64 columns, which read the cache twice.  So more than 64 rows of a
+// key head have the larger error.  The sum l is taken in fp32 of the whole weights.
 #include <cudaTypedefs.h>
 
 #include "pdl.cuh"
