@@ -109,6 +109,9 @@ torch.__version__ = "0.0+other"
 import verify_markov_head_gb300 as vm
 assert vm.dspark_version() > 0 and vm.dspark_workspace_bytes(4, 7, 1024, 64) > 0
 assert vm.dspark_cache_workspace_bytes(64, 32, 8, 128, 8) > 0
+import inspect
+inspect.getmembers(vm, inspect.isfunction)               # looking about in the package loads nothing
+assert not hasattr(vm._serve, "__wrapped__")
 for _ in range(2):
     try:
         vm.dspark_cache_append(None, None, None, None, None)

@@ -56,6 +56,8 @@ class _Serving:
     the verification need the library only."""
 
     def __getattr__(self, name):
+        if name.startswith("__"):            # inspection asks for these
+            raise AttributeError(name)
         global _serve
         _serve = _load_serve()
         return getattr(_serve, name)
