@@ -507,6 +507,90 @@ dspark_status dspark_cache_attention(
     void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * The cache held in 4 bits: the plan, slots and block tables are those above,
+ * what a page holds is
+ *     codes  k_cache, v_cache  [pages][kv_heads][page_size][head_dim / 2] bytes, page_stride bytes
+ *            from one page to the next: entry 2 i in the low half of byte i, entry 2 i + 1 in the high
+ *            half; a sign bit and 3 bits for 0, 1/2, 1, 3/2, 2, 3, 4, 6 (2 bits of exponent, 1 of mantissa)
+ *     scales k_scale, v_scale  [pages][kv_heads][page_size][head_dim / DSPARK_CACHE4_GROUP] bytes,
+ *            scale_stride bytes from one page to the next: an 8-bit float (4 bits of exponent, 3 of
+ *            mantissa, the largest 448, no infinity) for each 16 neighbouring entries
+ * and an entry stands for code * scale * 2^exp, exp being k_exp for the keys
+ * and v_exp for the values (-DSPARK_CACHE4_MAX_EXP .. DSPARK_CACHE4_MAX_EXP):
+ * it brings a tensor's usual entries / 6 well inside 2^-6 .. 448.
+ *
+ * dspark_cache_append4: as dspark_cache_append, the rows quantised on the way.
+ *     scale = the 8-bit float nearest to max |x| * 2^-exp / 6 over the 16 entries, at most 448
+ *     code  = the level nearest to x * 2^-exp / scale (0 where the scale is 0)
+ * (nearest, ties to the even number; entries beyond 6 scales become 6 scales,
+ * infinite ones among them).  A group with a NaN gets a scale that is NaN: it
+ * reads as NaN.
+ * dspark_cache_read4: the entries of the slots slot_map, in k_t (exact in bf16
+ * and fp32 as far as their range goes); a negative slot leaves its row as it
+ * was, one beyond the cache too, and sets status bit 5.
+ * Limits : head_dim % DSPARK_CACHE4_GROUP == 0, <= DSPARK_MAX_HEAD_DIM; rows at
+ *          multiples of 16 bytes, k_cache, v_cache and page_stride of 8, the rest as dspark_cache_append.
+ */
+#define DSPARK_CACHE4_GROUP 16
+#define DSPARK_CACHE4_MAX_EXP 64
+dspark_status dspark_cache_append4(
+    const void* k, const void* v, dspark_dtype kv_t, long long k_stride, long long v_stride,
+    const int32_t* slot_map, int T,
+    void* k_cache, void* v_cache, void* k_scale, void* v_scale, long long page_stride, long long scale_stride,
+    int pages, int page_size, int kv_heads, int head_dim, int k_exp, int v_exp, void* ws, void* stream);
+dspark_status dspark_cache_read4(
+    const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+    long long page_stride, long long scale_stride, int pages, int page_size, int kv_heads, int head_dim,
+    int k_exp, int v_exp, const int32_t* slot_map, int T,
+    void* k, void* v, dspark_dtype kv_t, long long k_stride, long long v_stride, void* ws, void* stream);
+
+/*
+ * dspark_cache_attention over a cache held in 4 bits (layout above): the same
+ * rows, masks, checks, status bits and workspace.  q and out are fp32 or bf16
+ * (q_t).  Keys and values take part as the values they stand for.  In bf16
+ * calls a row of q is scaled by a power of two and held in fp16 (entries below
+ * 2^-14 of the row's largest to 2^-25 of it), the softmax's weights are rounded
+ * to fp16 (2^-11 of each, those below 2^-21 of the row's largest to 2^-31 of it);
+ * products are exact and sums in fp32.  fp32 calls hold everything in fp32.
+ * Limits : as dspark_cache_attention, head_dim % DSPARK_CACHE4_GROUP == 0;
+ *          codes at multiples of 16 bytes from page to page, scales of 4.
+ */
+dspark_status dspark_cache_attention4(
+    const void* q, long long q_stride, dspark_dtype q_t,
+    const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+    long long page_stride, long long scale_stride, int pages, int page_size, int k_exp, int v_exp,
+    const int32_t* block_table, int width, const int32_t* kv_len, const int32_t* q_off, const int32_t* tile_off,
+    int B, int N, int q_heads, int kv_heads, int head_dim, int max_new, float scale,
+    void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions: the first rotary_dim entries of every head of q and k are
+ * turned in pairs, by an angle that grows with the token's position.  With
+ * theta_i = 2 pi * frac(positions[t] * turns[i] / 2^64) for pair i,
+ *     x'_a = mult * (x_a cos theta_i - x_b sin theta_i)
+ *     x'_b = mult * (x_b cos theta_i + x_a sin theta_i)
+ * where (a, b) = (2 i, 2 i + 1) if interleaved, (i, i + rotary_dim / 2)
+ * otherwise.  The other entries are copied.
+ * Inputs : q [T][q_heads][head_dim], k [T][kv_heads][head_dim] (t; k may be
+ *          NULL with kv_heads 0), strides in elements between tokens;
+ *          positions [T] int32 as dspark_cache_plan leaves them (a token whose
+ *          position is negative is padding: its rows of the outputs are left
+ *          as they were); turns [rotary_dim / 2]: turns per position in units
+ *          of 2^-64, taken modulo a turn.  The product is formed in 64-bit
+ *          integers, so a position of 2^31 is as exact as the first.
+ * Outputs: q_out, k_out, with strides of their own; each may be its input
+ *          (same address and stride), and overlaps no other memory here.
+ * Limits : head_dim % 8 == 0, <= DSPARK_MAX_HEAD_DIM, rotary_dim even, 2 ..
+ *          head_dim; addresses and strides multiples of 16 bytes; q_heads +
+ *          kv_heads <= 8192; mult finite.
+ */
+dspark_status dspark_rope(
+    const void* q, long long q_stride, const void* k, long long k_stride, dspark_dtype t,
+    const int32_t* positions, const uint64_t* turns, int rotary_dim, int interleaved, float mult,
+    void* q_out, long long q_out_stride, void* k_out, long long k_out_stride,
+    int T, int q_heads, int kv_heads, int head_dim, void* stream);
+
+/*
  * Penalties for repeated tokens, biases and grammar masks on the logits that a
  * verification (R = gamma + 1 target rows) or a draft (R = gamma rows of U)
  * draws from.  Row i of request b follows the request's history and the first
@@ -551,6 +635,39 @@ dspark_status dspark_logits_process(
     const float* rep, const float* freq, const float* pres,
     const int32_t* bias_tok, const float* bias_val, const int32_t* bias_off, int bias_n,
     const uint32_t* mask, float fill, int32_t* live, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A token of each row of logits, from a given random number.  With the weights
+ * w_v = e^((x_v - max x) / temperature) of row n, in descending order of x (ties:
+ * the lower id first),
+ *     top_k   leaves the first top_k[n] entries          (<= 0: all),
+ *     top_p   of those the shortest run whose weight reaches top_p[n] of theirs,
+ *             at least one                               (>= 1: all),
+ *     min_p   of those the ones with w_v >= min_p[n]     (<= 0: all; above 1 as 1),
+ * and the token is the first id, in ascending order, at which the sum of the
+ * weights left exceeds u[n] times their total; logprob = ln of its weight's
+ * share.  temperature 0: the row's largest entry (the lowest id), logprob 0.
+ * Weights are formed to about 2^-32 of each and summed as integers of 2^-42 of
+ * the largest, so the result does not depend on the order of the sums.
+ * Inputs : logits [N][V] (t), row_stride elements between rows; u [N] fp32 in
+ *          [0, 1) (taken into that range; NaN as 0); temperature [N] (NULL: 1),
+ *          top_k [N] int32, top_p, min_p [N] fp32 (NULL: all).  A
+ *          temperature that is negative or not finite counts as 0, a NaN in top_p or min_p as
+ *          off, and both set status bit 3.
+ * Outputs: tok [N]; logprob [N] or NULL.
+ * Entries that are NaN or +inf are left out and set status bit 3.  A row of
+ * which nothing is left gets token -1 and logprob -inf, and sets bit 4.
+ * ws     : dspark_sample_workspace_bytes(N) bytes, 256-byte aligned, cleared once.
+ * Limits : 1 <= V <= DSPARK_MAX_SAMPLE_VOCAB; logits and row strides multiples of 16
+ *          bytes; 0 <= N <= DSPARK_MAX_SAMPLE_ROWS.
+ */
+#define DSPARK_MAX_SAMPLE_VOCAB (1 << 19)
+#define DSPARK_MAX_SAMPLE_ROWS (1 << 20)
+size_t dspark_sample_workspace_bytes(int N);
+dspark_status dspark_sample(
+    const void* logits, dspark_dtype t, long long row_stride, int N, int V, const float* u,
+    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+    int32_t* tok, float* logprob, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Diagnostics: the random stream as the kernels draw it.  For columns

@@ -14,7 +14,9 @@ from __future__ import annotations
 
 import ctypes as C
 import importlib.util
+import math
 import os
+from fractions import Fraction
 
 import torch
 
@@ -24,6 +26,7 @@ __all__ = [
     "dspark_workspace_init", "dspark_workspace_set_wait_limit", "dspark_sync_status", "dspark_draft_markov", "dspark_confidence_sts",
     "dspark_schedule", "dspark_verify", "dspark_draft_markov_target", "target_stream_supported", "dspark_draft_rnn", "dspark_verify_rnn", "dspark_verify_logits", "dspark_rnn_input_table", "rnn_prepare", "dspark_sts_workspace_bytes", "dspark_sts_fit", "dspark_gumbel_stream", "dspark_draft_markov_noalloc", "dspark_noalloc_sync_status", "Workspace", "StepBuffers", "run_step", "run_step_host", "run_step_dp", "GlobalSchedule", "HostPipeline",
     "dspark_cache_plan", "dspark_cache_append", "dspark_cache_workspace_bytes", "dspark_cache_attention", "dspark_logits_workspace_bytes", "dspark_logits_process", "CacheWorkspace", "LogitsWorkspace", "CACHE_TILE",
+    "dspark_cache_append4", "dspark_cache_read4", "dspark_cache_attention4", "Cache4", "CACHE4_GROUP", "dspark_rope", "RopeTable", "rope_frequencies", "dspark_sample_workspace_bytes", "dspark_sample", "SampleWorkspace",
     "SCHED_OFF", "SCHED_SYNC", "SCHED_ASYNC",
 ]
 
@@ -31,6 +34,7 @@ SCHED_OFF, SCHED_SYNC, SCHED_ASYNC = 0, 1, 2
 STORE_LOGITS_BYTES = 64 << 20   # StepBuffers keeps the draft logits up to this size
 _F32, _BF16 = 0, 1
 CACHE_TILE = 64                  # cache positions one entry of tile_off counts
+CACHE4_GROUP = 16                # entries of a cache in 4 bits that share a scale
 
 lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libdspark.so")
 if not os.path.exists(lib_path):
@@ -71,6 +75,8 @@ _lib.dspark_status_string.argtypes = [_i]
 _lib.dspark_status_string.restype = C.c_char_p
 _lib.dspark_workspace_bytes.argtypes = [_i, _i, _i, _i]
 _lib.dspark_workspace_bytes.restype = _sz
+_lib.dspark_sample_workspace_bytes.argtypes = [_i]
+_lib.dspark_sample_workspace_bytes.restype = _sz
 _lib.dspark_workspace_init.argtypes = [_vp, _sz, _vp]
 _lib.dspark_workspace_init.restype = _i
 _lib.dspark_workspace_set_wait_limit.argtypes = [_vp, _sz, _u64, _vp]
@@ -116,6 +122,17 @@ _lib.dspark_sts_fit.argtypes = [_vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _v
 _lib.dspark_sts_fit.restype = _i
 _lib.dspark_gumbel_stream.argtypes = [_u64, _u64, C.c_uint32, C.c_uint32, _i, _vp, _vp, _vp]
 _lib.dspark_gumbel_stream.restype = _i
+_lib.dspark_cache_append4.argtypes = [_vp, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp, _vp, _vp, _ll, _ll, _i, _i, _i, _i, _i, _i, _vp, _vp]
+_lib.dspark_cache_append4.restype = _i
+_lib.dspark_cache_read4.argtypes = [_vp, _vp, _vp, _vp, _ll, _ll, _i, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _i, _ll, _ll, _vp, _vp]
+_lib.dspark_cache_read4.restype = _i
+_lib.dspark_cache_attention4.argtypes = [_vp, _ll, _i, _vp, _vp, _vp, _vp, _ll, _ll, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp,
+                                         _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _sz, _vp]
+_lib.dspark_cache_attention4.restype = _i
+_lib.dspark_rope.argtypes = [_vp, _ll, _vp, _ll, _i, _vp, _vp, _i, _i, _f, _vp, _ll, _vp, _ll, _i, _i, _i, _i, _vp]
+_lib.dspark_rope.restype = _i
+_lib.dspark_sample.argtypes = [_vp, _i, _ll, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.dspark_sample.restype = _i
 _lib.dspark_cache_plan.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i,
                                    _vp, _vp]
 _lib.dspark_cache_plan.restype = _i
@@ -533,6 +550,156 @@ def dspark_logits_process(logits, out, ws: Workspace, *, hist=None, hist_len=Non
     _check("dspark_logits_process", _serve.logits_process(
         logits, out, ws.buf, hist, hist_len, prompt_len, draft_tok, rep, freq, pres, bias_tok, bias_val, bias_off, mask, fill,
         live, stream))
+
+
+class SampleWorkspace(_Scratch):
+    """Workspace of dspark_sample for N rows."""
+
+    def __init__(self, N, device="cuda", stream=None):
+        super().__init__(dspark_sample_workspace_bytes(N), device, stream)
+
+
+class Cache4:
+    """A paged cache held in 4 bits: codes k, v [pages, kv_heads, page_size,
+    head_dim / 2] and scales k_scale, v_scale [.., head_dim / 16] uint8 (all
+    zero: every entry 0), and the exponents k_exp, v_exp of its values."""
+
+    def __init__(self, pages, kv_heads, page_size, head_dim, *, k_exp=0, v_exp=0, device="cuda"):
+        if head_dim % CACHE4_GROUP:
+            raise ValueError(f"head_dim must be a multiple of {CACHE4_GROUP}")
+        u8 = dict(dtype=torch.uint8, device=device)
+        shape = (pages, kv_heads, page_size)
+        self.k, self.v = torch.zeros((*shape, head_dim // 2), **u8), torch.zeros((*shape, head_dim // 2), **u8)
+        self.k_scale = torch.zeros((*shape, head_dim // CACHE4_GROUP), **u8)
+        self.v_scale = torch.zeros_like(self.k_scale)
+        self.k_exp, self.v_exp = int(k_exp), int(v_exp)
+
+    @property
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+
+def dspark_cache_append4(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, k_exp=0, v_exp=0, ws: Workspace = None,
+                         stream=None):
+    """Quantise keys and values k, v [T, kv_heads, head_dim] (any token stride)
+    to 4 bits and write them to the slots slot_map [T] int32 of a Cache4's
+    tensors; negative slots are skipped."""
+    _check("dspark_cache_append4", _serve.cache_append4(
+        k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_exp, v_exp, None if ws is None else ws.buf, stream))
+
+
+def dspark_cache_read4(k_cache, v_cache, k_scale, v_scale, slot_map, k, v, *, k_exp=0, v_exp=0, ws: Workspace = None,
+                       stream=None):
+    """Read the slots slot_map [T] int32 of a Cache4's tensors into k, v
+    [T, kv_heads, head_dim] (any token stride); rows of negative slots are left
+    as they were."""
+    _check("dspark_cache_read4", _serve.cache_read4(
+        k_cache, v_cache, k_scale, v_scale, slot_map, k, v, k_exp, v_exp, None if ws is None else ws.buf, stream))
+
+
+def dspark_cache_attention4(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out,
+                            ws: Workspace, *, max_new, k_exp=0, v_exp=0, scale=None, lse=None, stream=None):
+    """dspark_cache_attention over a Cache4's tensors: q and out [N, q_heads,
+    head_dim] bf16 or fp32, the same plan and workspace (CacheWorkspace)."""
+    _check("dspark_cache_attention4", _serve.cache_attention4(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out, ws.buf, max_new, k_exp, v_exp, scale, lse,
+        stream))
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
+    """Radians per position of the rotary_dim / 2 pairs (a list of floats) and
+    the multiplier of the turned entries.  Pair i turns by base^(-2 i /
+    rotary_dim) a position.  scaling, for contexts longer than the trained
+    one: None or {"kind": .., "factor": f, ..} with the kinds
+      "linear"      all pairs f times slower;
+      "ntk"         base * f^(rotary_dim / (rotary_dim - 2)): the slowest pair f
+                    times slower, the fastest as it was;
+      "yarn"        ("trained": n, "fast": 32, "slow": 1) pairs that turn more than
+                    `fast` times in n positions as they were, less than `slow` times
+                    f times slower, a ramp over the pairs between; multiplier
+                    0.1 ln f + 1, or "mult";
+      "wavelength"  ("trained": n, "low": 1, "high": 4) wavelengths above n / low f
+                    times longer, below n / high as they were, between them mixed by
+                    n / wavelength."""
+    r = int(rotary_dim)
+    if r < 2 or r % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    if not base > 0 or not math.isfinite(base):
+        raise ValueError("base must be positive and finite")
+    s = dict(scaling or {})
+    kind, f = s.pop("kind", None), float(s.pop("factor", 1.0))
+    if not f > 0 or not math.isfinite(f):
+        raise ValueError("factor must be positive and finite")
+    known = {None: (), "linear": (), "ntk": (), "yarn": ("trained", "fast", "slow", "mult"), "wavelength": ("trained", "low", "high")}
+    if kind not in known:
+        raise ValueError(f"unknown scaling {kind!r}")
+    if set(s) - set(known[kind]):
+        raise ValueError(f"unknown entries of scaling {kind!r}: {sorted(set(s) - set(known[kind]))}")
+    if kind in ("yarn", "wavelength") and not s.get("trained", 0) > 0:
+        raise ValueError(f"scaling {kind!r} needs the trained length")
+    if kind == "ntk":
+        if r == 2:
+            raise ValueError("scaling 'ntk' needs a rotary_dim above 2")
+        base *= f ** (r / (r - 2))
+    freq = [base ** (-2.0 * i / r) for i in range(r // 2)]
+    if kind == "linear":
+        return [x / f for x in freq], 1.0
+    if kind == "yarn":
+        pair = [r * math.log(s["trained"] / (turns * 2 * math.pi)) / (2 * math.log(base)) for turns in (s.get("fast", 32), s.get("slow", 1))]
+        low, high = max(0, math.floor(pair[0])), min(r - 1, math.ceil(pair[1]))
+        ramp = [min(1.0, max(0.0, (i - low) / max(high - low, 1e-3))) for i in range(r // 2)]
+        return [x * (1 - a) + x / f * a for x, a in zip(freq, ramp)], float(s.get("mult", 0.1 * math.log(f) + 1.0))
+    if kind == "wavelength":
+        low, high = s.get("low", 1), s.get("high", 4)
+        if not high > low:
+            raise ValueError("scaling 'wavelength' needs high > low")
+        mix = [min(1.0, max(0.0, (s["trained"] * x / (2 * math.pi) - low) / (high - low))) for x in freq]
+        return [x * a + x / f * (1 - a) for x, a in zip(freq, mix)], 1.0
+    return freq, 1.0
+
+
+class RopeTable:
+    """The turns of dspark_rope for rotary_dim entries of a head: the
+    frequencies of rope_frequencies(rotary_dim, base, scaling), or those given
+    (radians per position), in units of 2^-64 turns on the device."""
+
+    def __init__(self, rotary_dim, base=10000.0, scaling=None, *, frequencies=None, mult=None, device="cuda"):
+        freq, m = rope_frequencies(rotary_dim, base, scaling) if frequencies is None else (list(frequencies), 1.0)
+        if len(freq) != int(rotary_dim) // 2:
+            raise ValueError("one frequency for each pair")
+        self.rotary_dim, self.mult = int(rotary_dim), float(m if mult is None else mult)
+        turns = [int(Fraction(float(x)) / _TURN * 2 ** 64 + Fraction(1, 2)) % 2 ** 64 for x in freq]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+# 2 pi to 2^-100
+_TURN = Fraction(7964883625991394727376702227904, 2 ** 100)
+
+
+def dspark_rope(q, k, positions, table: RopeTable, q_out=None, k_out=None, *, interleaved=False, stream=None):
+    """Turn the first table.rotary_dim entries of every head of q [T, q_heads,
+    head_dim] and k [T, kv_heads, head_dim] (or None) by the tokens' positions
+    [T] int32, into q_out and k_out (None: in place; any token stride).  Pairs
+    are (2 i, 2 i + 1) if interleaved, (i, i + rotary_dim / 2) otherwise; rows
+    of negative positions are left as they were."""
+    if q_out is None:
+        q_out = q
+    if k_out is None:
+        k_out = k
+    _check("dspark_rope", _serve.rope(q, k, positions, table.turns, table.rotary_dim, table.mult, q_out, k_out, interleaved, stream))
+
+
+def dspark_sample_workspace_bytes(N) -> int:
+    return int(_lib.dspark_sample_workspace_bytes(N))
+
+
+def dspark_sample(logits, u, tok, ws: Workspace, *, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
+                  stream=None):
+    """Draw a token of each row of logits [N, V] (any row stride) from the
+    random numbers u [N] fp32 in [0, 1): tok [N] int32, logprob [N] fp32 or None
+    (of the token among what is left).  temperature, top_p, min_p [N] fp32 and
+    top_k [N] int32, or None; temperature 0 takes the largest entry."""
+    _check("dspark_sample", _serve.sample(logits, u, tok, ws.buf, temperature, top_k, top_p, min_p, logprob, stream))
 
 
 class StepBuffers:

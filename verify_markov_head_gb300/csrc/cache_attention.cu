@@ -11,6 +11,8 @@
 // the cache keeps the running maximum and sum of every row; partial results
 // (m, l, unnormalised o) of disjoint ranges of positions join exactly:
 //     m = max_c m_c,   l = sum_c l_c e^(m_c - m),   o = sum_c o_c e^(m_c - m) / l.
+#include "attn_rows.cuh"
+#include "fp4.cuh"
 #include "pdl.cuh"
 #include "serve.cuh"
 #include "sm100_ptx.cuh"
@@ -19,52 +21,6 @@ namespace dspark {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-// Start of the partial maxima and sums behind the partial outputs.
-__device__ __forceinline__ float* part_stats(const AttnParams& p) {
-    return p.part + (size_t)2 * p.ctas * p.row_tile * p.D;
-}
-
-// Query row `rr` of request b: token rr / G, head h * G + rr % G.
-struct RowMap {
-    int q0, n, len;       // first token of the request in q, its tokens, its cache length
-    __device__ __forceinline__ RowMap(const AttnParams& p, int b) {
-        q0 = p.q_off[b];
-        n = p.q_off[b + 1] - q0;
-        len = p.kv_len[b];
-        // (n is right modulo 2^32; with q0 in range and n in [0, max_new], q0 + n is compared without a sum)
-        if (n > p.max_new || n < 0 || q0 < 0 || q0 > p.N - n || (long long)len > (long long)p.width * p.page_size || len < 0) {
-            if (threadIdx.x == 0) raise_status(p.status, kBadLength);
-            n = q0 < 0 ? 0 : max(0, min(n, min(p.max_new, p.N - q0)));
-            len = max(0, min(len, p.width * p.page_size));
-        }
-    }
-};
-
-template <typename T>
-__device__ __forceinline__ void store_out(T* out, float x);
-template <>
-__device__ __forceinline__ void store_out<float>(float* out, float x) { *out = x; }
-template <>
-__device__ __forceinline__ void store_out<uint16_t>(uint16_t* out, float x) {
-    // the one rounding of the result (nearest even)
-    asm("{\n\t.reg .b16 h;\n\tcvt.rn.bf16.f32 h, %1;\n\tmov.b16 %0, h;\n\t}" : "=h"(*out) : "f"(x));
-}
-
-// Requests that own no cache position have no tile: their rows are zero.  The
-// offsets of every request are compared with its length here.
-__device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int ctas) {
-    for (int b = cta; b < p.B; b += ctas) {
-        const int off = p.tile_off[b], next = p.tile_off[b + 1];
-        if (threadIdx.x == 0 && !attn_offsets_fit(p, b, off, next)) raise_status(p.status, kBadLength);
-        if (next > off) continue;
-        const RowMap r(p, b);
-        const size_t o0 = (size_t)r.q0 * p.Hq * p.D, n = (size_t)r.n * p.Hq * p.D;
-        for (size_t i = threadIdx.x; i < n; i += blockDim.x) static_cast<float*>(p.out)[o0 + i] = 0.f;
-        if (p.lse)
-            for (int i = threadIdx.x; i < r.n * p.Hq; i += blockDim.x) p.lse[(size_t)r.q0 * p.Hq + i] = -INFINITY;
-    }
-}
 
 // --------------------------------------------------- on CUDA cores: fp32
 // fp32 arithmetic throughout, so the FMA rate and the shared-memory reads that
@@ -100,7 +56,9 @@ struct Simt {
     }
 };
 
-template <int MR, int TT>
+// k4: a cache in 4 bits, made fp32 on its way to shared memory by the threads,
+// which wait for its codes before a step's arithmetic.
+template <int MR, int TT, bool k4>
 __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnParams p) {
     using S = Simt<MR, TT>;
     constexpr int E = 4, TPT = S::TPT, NR = S::NR, ND = S::ND;
@@ -111,12 +69,12 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
     float* sp_ = sq + MR * D;                                // weights [TT][MR]
     float* merge = sp_ + TT * MR;                            // [TS - 1][MR][D]
     __shared__ float s_max[S::kTokWarps][MR], s_sum[S::kTokWarps][MR], s_alpha[MR], s_ref[MR];
-    __shared__ long long s_base[2][TT];
+    __shared__ long long s_base[2][TT], s_scale[k4 ? 2 : 1][k4 ? TT : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) grid_launch_dependents();   // the join is scheduled now and waits for this grid
     grid_dependency_wait();
     const int cta = blockIdx.x;
-    empty_rows(p, cta, gridDim.x);
+    empty_rows<float>(p, cta, gridDim.x);
     const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
     if (tid == 0) p.split[cta].parts = 0;
     if (cta >= sp.n) return;
@@ -134,7 +92,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
     const int end = sp.first(cta + 1);
     for (int t = sp.first(cta); t < end;) {
         const AttnSegment g = attn_segment(p, sp, t, attn_first_round(p));
-        const RowMap rm(p, g.b);
+        const RowMap rm(p, g.b, tid == 0);
         const int r0 = g.rt * p.row_tile;
         const int rows = max(0, min(p.row_tile, rm.n * p.G - r0));
         const int j0 = g.tile(sp, t), j1 = g.tile(sp, end), next = g.t0 + sp.pad + g.tiles;
@@ -148,12 +106,37 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
             if (pos >= rm.len) return -1LL;
             const int pg = p.by_page(pos), page = p.table[(size_t)g.b * p.width + pg];
             if (page < 0 || page >= p.pages) { raise_status(p.status, kBadPage); return -1LL; }
-            return page * p.page_stride + ((long long)g.h * p.page_size + (pos - pg * p.page_size)) * D;
+            const long long row = (long long)g.h * p.page_size + (pos - pg * p.page_size);
+            if constexpr (k4) s_scale[s & 1][tid] = page * p.scale_stride + row * (D / fp4::kGroup);
+            return page * p.page_stride + row * (k4 ? D / 2 : D);
         };
         // chunk c of position r (whole groups of 8 chunks are swizzled)
         auto place = [&](int r, int c) { return r * chunks + ((c | 7) < chunks ? c ^ ((r / TPT) & 7) : c); };
         auto issue = [&](int s) {
             const int st = s & 1;
+            if constexpr (k4) {
+                for (int i = tid; i < TT * (D / 8); i += kSimtThreads) {
+                    const int r = i / (D / 8), c = i - r * (D / 8);
+                    const long long base = s_base[st][r], scale = s_scale[st][r] + c / 2;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        uint32_t w = 0u, h[4];
+                        float by = 0.f;
+                        if (base >= 0) {
+                            w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(kv ? p.v : p.k) + base + 4 * c);
+                            by = fp4::scale_value((kv ? p.vs : p.ks)[scale]);
+                        }
+                        fp4::unpack(w, h);
+                        float4* to = reinterpret_cast<float4*>(ring + (2 * st + kv) * tile_elems);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 a = fp4::floats(h[2 * e]), b = fp4::floats(h[2 * e + 1]);
+                            to[place(r, 2 * c + e)] = make_float4(a.x * by, a.y * by, b.x * by, b.y * by);
+                        }
+                    }
+                }
+                return;
+            }
             const uint32_t k0 = ptx::smem_addr(ring + 2 * st * tile_elems), v0 = k0 + tile_elems * (uint32_t)sizeof(float);
             for (int i = tid; i < TT * chunks; i += kSimtThreads) {
                 const int r = i / chunks, c = i - r * chunks;
@@ -346,6 +329,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
                 float x = acc[r][e];
 #pragma unroll
                 for (int w = 0; w < S::TS - 1; ++w) x += merge[(w * MR + row) * D + d];
+                if constexpr (k4) x *= p.out_by;
                 if (whole) static_cast<float*>(p.out)[at * D + d] = x * inv;
                 else p.part[((size_t)slot * p.row_tile + row) * D + d] = x;
             }
@@ -434,22 +418,21 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     if (lane == 0 && p.lse) p.lse[o0] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
-template <int MR, int TT>
+template <int MR, int TT, bool k4>
 cudaError_t launch_simt_tile(const AttnParams& p, cudaStream_t s) {
     const size_t smem = Simt<MR, TT>::bytes(p.D);
-    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<MR, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<MR, TT, k4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_simt_kernel<MR, TT>, dim3(p.ctas), dim3(kSimtThreads), smem, s, p);
+    return launch_dependent(attn_simt_kernel<MR, TT, k4>, dim3(p.ctas), dim3(kSimtThreads), smem, s, p);
 }
-template <int MR>
+template <int MR, bool k4>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
     // 64 positions at a time as far as shared memory holds two stages of them
-    return p.D <= 128 ? launch_simt_tile<MR, 64>(p, s) : launch_simt_tile<MR, 32>(p, s);
+    return p.D <= 128 ? launch_simt_tile<MR, 64, k4>(p, s) : launch_simt_tile<MR, 32, k4>(p, s);
 }
 
-template <typename T>
 cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
-    return launch_dependent(attn_join_kernel<T>, dim3(p.ctas, (p.row_tile + 7) / 8), dim3(256), 0, s, p);
+    return launch_dependent(p.bf16 ? attn_join_kernel<uint16_t> : attn_join_kernel<float>, dim3(p.ctas, (p.row_tile + 7) / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -457,9 +440,15 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
 cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s) {
     cudaError_t e;
     if (p.bf16) e = launch_attn_mma(p, s);
-    else e = p.row_tile == 8 ? launch_simt<8>(p, s) : launch_simt<32>(p, s);
-    if (e != cudaSuccess) return e;
-    return p.bf16 ? launch_join<uint16_t>(p, s) : launch_join<float>(p, s);
+    else e = p.row_tile == 8 ? launch_simt<8, false>(p, s) : launch_simt<32, false>(p, s);
+    return e == cudaSuccess ? launch_join(p, s) : e;
+}
+
+cudaError_t launch_cache_attention4(const AttnParams& p, cudaStream_t s) {
+    cudaError_t e;
+    if (p.bf16) e = launch_attn4_mma(p, s);
+    else e = p.row_tile == 8 ? launch_simt<8, true>(p, s) : launch_simt<32, true>(p, s);
+    return e == cudaSuccess ? launch_join(p, s) : e;
 }
 
 }  // namespace dspark

@@ -42,7 +42,7 @@ struct AppendParams {
 };
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t s);
 
-// ----------------------------------------------------------- cache attention
+// ------------------------------------------------------------------ division
 // Division of 0 <= x < 2^31 by a number fixed on the host (Granlund and
 // Montgomery, "Division by invariant integers using multiplication").
 struct FastDiv {
@@ -56,6 +56,47 @@ struct FastDiv {
     __device__ __forceinline__ int operator()(int x) const { return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift); }
 };
 
+// ---------------------------------------------------------- cache in 4 bits
+struct Cache4Params {
+    const void* k; const void* v; long long k_stride, v_stride;   // rows (written by the read), elements between tokens
+    int bf16;
+    const int32_t* slot_map; int T;
+    uint8_t* k_cache; uint8_t* v_cache; uint8_t* k_scale; uint8_t* v_scale;
+    long long page_bytes, scale_bytes;                            // bytes between pages of codes, of scales
+    int pages, page_size, heads, groups;                          // groups of a head's vector
+    float k_by, v_by;             // what entries are multiplied by: 2^-exp to be written, 2^exp to be read
+    FastDiv by_page, by_groups;   // by page_size, by groups
+    uint32_t* status;   // may be null
+};
+cudaError_t launch_cache_append4(const Cache4Params& p, cudaStream_t s);
+cudaError_t launch_cache_read4(const Cache4Params& p, cudaStream_t s);
+
+// ----------------------------------------------------------- rotary positions
+struct RopeParams {
+    const void* q; const void* k; void* q_out; void* k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;     // elements between tokens
+    int bf16;
+    const int32_t* positions; const unsigned long long* turns;
+    int T, Hq, Hkv, D, rotary, interleaved;
+    float mult;
+    // set by the launch: tokens of a block, a head's items and those of them that are turned
+    int side, items, turned;
+    FastDiv by_items, by_half, by_heads;
+};
+cudaError_t launch_rope(RopeParams p, cudaStream_t s);
+
+// ------------------------------------------------------------------- sampling
+struct SampleParams {
+    const void* logits; long long row_stride; int bf16;   // elements between rows
+    int N, V;
+    const float* u; const float* temperature; const int32_t* top_k; const float* top_p; const float* min_p;
+    int32_t* tok; float* logprob;
+    int ctas, slice;    // set by the launch: CTAs of a row, entries of each
+    uint32_t* status;
+};
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t s);
+
+// ----------------------------------------------------------- cache attention
 // What a CTA leaves for the join of a segment that begins in it.
 struct __align__(16) AttnSplitRow {
     int parts;           // CTAs that hold a part of it, 0: no such segment
@@ -65,7 +106,9 @@ struct __align__(16) AttnSplitRow {
 
 struct AttnParams {
     const void* q; long long q_stride;                 // elements between tokens
-    const void* k; const void* v; long long page_stride;   // elements between pages
+    const void* k; const void* v; long long page_stride;   // elements between pages (of a cache in 4 bits: bytes)
+    const uint8_t* ks; const uint8_t* vs; long long scale_stride;   // scales of a cache in 4 bits, bytes between pages
+    float out_by;                                      // what its sums of values are multiplied by
     int bf16;
     const int32_t* table; int width;
     const int32_t* kv_len; const int32_t* q_off; const int32_t* tile_off;
@@ -82,8 +125,11 @@ struct AttnParams {
     uint32_t* status;
 };
 cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_cache_attention4(const AttnParams& p, cudaStream_t s);
 bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can copy
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
+int attn4_row_tile(int rows, int D);              // query rows at a time over a cache in 4 bits
+cudaError_t launch_attn4_mma(const AttnParams& p, cudaStream_t s);   // bf16 queries, a cache in 4 bits
 // Rows of a row tile where a key-value head has `rows` query rows.
 inline int attn_row_tile(int rows, bool mma) {
     return mma ? (rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128) : (rows <= 8 ? 8 : 32);

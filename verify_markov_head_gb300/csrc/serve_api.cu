@@ -2,6 +2,7 @@
 // host-side argument checks, workspace layout and launches.
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
+#include <math.h>
 #include <string.h>
 
 #include "serve.cuh"
@@ -21,6 +22,11 @@ bool dev_or_null(const void* p, size_t a = 4) { return !p || dev(p, a); }
 bool dtype_ok(dspark_dtype t) { return t == DSPARK_F32 || t == DSPARK_BF16; }
 int bytes_of(dspark_dtype t) { return t == DSPARK_BF16 ? 2 : 4; }
 
+// Addresses and page strides as whole rows allow: the largest power of two that divides a row, 16 at most.
+int row_align(int row) { return (row | 16) & -(row | 16); }
+bool exp_ok(int e) { return e >= -DSPARK_CACHE4_MAX_EXP && e <= DSPARK_CACHE4_MAX_EXP; }
+float power(int e) { return ldexpf(1.f, e); }
+
 bool head_ok(int D) { return D >= 8 && D <= DSPARK_MAX_HEAD_DIM && D % 8 == 0; }
 bool pages_ok(int pages, int page_size) {
     return pages >= 1 && page_size >= 1 && page_size <= DSPARK_MAX_PAGE_SIZE && (long long)pages * page_size < (1LL << 31);
@@ -35,6 +41,24 @@ struct Words {
         return n > 0 && o.n > 0 && a < b + 4 * o.n && b < a + 4 * n;
     }
 };
+
+struct Bytes {
+    const char* p;
+    long long n;
+    bool meets(const Bytes& o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return n > 0 && o.n > 0 && a < b + o.n && b < a + n;
+    }
+};
+// Whether rows of `width` bytes, `stride` apart, share a byte with others.  Slices
+// of one projection's rows (the same stride) interleave without sharing any.
+bool rows_meet(const Bytes& a, long long a_stride, long long a_width, const Bytes& b, long long b_stride, long long b_width) {
+    if (!a.meets(b)) return false;
+    if (a_stride != b_stride) return true;
+    long long gap = (reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) % a_stride;
+    if (gap < 0) gap += a_stride;                // b's rows begin `gap` behind a's
+    return gap < a_width || gap + b_width > a_stride;
+}
 
 // Workspaces: the status word in the first 256 bytes, then the regions.
 constexpr size_t kHead = 256;
@@ -107,6 +131,139 @@ dspark_status dspark_cache_append(const void* k, const void* v, dspark_dtype kv_
     return launch_status(launch_cache_append(p, static_cast<cudaStream_t>(stream)));
 }
 
+// What the two calls over a cache in 4 bits share; false: an argument is refused.
+static bool cache4_params(Cache4Params& p, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                          long long page_stride, long long scale_stride, int pages, int page_size, int kv_heads, int head_dim,
+                          int k_exp, int v_exp, const int32_t* slot_map, int T, const void* k, const void* v, dspark_dtype kv_t,
+                          long long k_stride, long long v_stride, void* ws) {
+    if (T < 0 || kv_heads < 1 || kv_heads > 4096 || !head_ok(head_dim) || head_dim % DSPARK_CACHE4_GROUP || !pages_ok(pages, page_size) ||
+        !exp_ok(k_exp) || !exp_ok(v_exp))
+        return false;
+    const int es = bytes_of(kv_t), groups = head_dim / DSPARK_CACHE4_GROUP;
+    const long long row = (long long)kv_heads * head_dim, rows = (long long)kv_heads * page_size;
+    if (k_stride < row || v_stride < row || (k_stride * es) % 16 || (v_stride * es) % 16) return false;
+    if (page_stride < rows * (head_dim / 2) || page_stride % 8 || scale_stride < rows * groups) return false;
+    if (T > 0 && (!dev(k, 16) || !dev(v, 16) || !dev(slot_map) || !dev(k_cache, 8) || !dev(v_cache, 8) || !dev(k_scale, 1) ||
+                  !dev(v_scale, 1) || !dev_or_null(ws, 256)))
+        return false;
+    p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.bf16 = kv_t == DSPARK_BF16;
+    p.slot_map = slot_map; p.T = T;
+    p.k_cache = static_cast<uint8_t*>(const_cast<void*>(k_cache)); p.v_cache = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+    p.k_scale = static_cast<uint8_t*>(const_cast<void*>(k_scale)); p.v_scale = static_cast<uint8_t*>(const_cast<void*>(v_scale));
+    p.page_bytes = page_stride; p.scale_bytes = scale_stride;
+    p.pages = pages; p.page_size = page_size; p.heads = kv_heads; p.groups = groups;
+    p.by_page.set((uint32_t)page_size);
+    p.by_groups.set((uint32_t)groups);
+    p.status = static_cast<uint32_t*>(ws);
+    return true;
+}
+
+dspark_status dspark_cache_append4(const void* k, const void* v, dspark_dtype kv_t, long long k_stride, long long v_stride,
+                                   const int32_t* slot_map, int T, void* k_cache, void* v_cache, void* k_scale,
+                                   void* v_scale, long long page_stride, long long scale_stride, int pages, int page_size,
+                                   int kv_heads, int head_dim, int k_exp, int v_exp, void* ws, void* stream) {
+    const CallRange range_(__func__);
+    if (!dtype_ok(kv_t)) return DSPARK_ERR_UNSUPPORTED;
+    Cache4Params p;
+    if (!cache4_params(p, k_cache, v_cache, k_scale, v_scale, page_stride, scale_stride, pages, page_size, kv_heads, head_dim,
+                       k_exp, v_exp, slot_map, T, k, v, kv_t, k_stride, v_stride, ws))
+        return DSPARK_ERR_INVALID;
+    if (T == 0) return DSPARK_OK;
+    p.k_by = power(-k_exp);
+    p.v_by = power(-v_exp);
+    return launch_status(launch_cache_append4(p, static_cast<cudaStream_t>(stream)));
+}
+
+dspark_status dspark_cache_read4(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                                 long long page_stride, long long scale_stride, int pages, int page_size, int kv_heads,
+                                 int head_dim, int k_exp, int v_exp, const int32_t* slot_map, int T, void* k, void* v,
+                                 dspark_dtype kv_t, long long k_stride, long long v_stride, void* ws, void* stream) {
+    const CallRange range_(__func__);
+    if (!dtype_ok(kv_t)) return DSPARK_ERR_UNSUPPORTED;
+    Cache4Params p;
+    if (!cache4_params(p, k_cache, v_cache, k_scale, v_scale, page_stride, scale_stride, pages, page_size, kv_heads, head_dim,
+                       k_exp, v_exp, slot_map, T, k, v, kv_t, k_stride, v_stride, ws))
+        return DSPARK_ERR_INVALID;
+    if (T == 0) return DSPARK_OK;
+    p.k_by = power(k_exp);
+    p.v_by = power(v_exp);
+    return launch_status(launch_cache_read4(p, static_cast<cudaStream_t>(stream)));
+}
+
+dspark_status dspark_rope(const void* q, long long q_stride, const void* k, long long k_stride, dspark_dtype t,
+                          const int32_t* positions, const uint64_t* turns, int rotary_dim, int interleaved, float mult,
+                          void* q_out, long long q_out_stride, void* k_out, long long k_out_stride, int T, int q_heads,
+                          int kv_heads, int head_dim, void* stream) {
+    const CallRange range_(__func__);
+    if (!dtype_ok(t)) return DSPARK_ERR_UNSUPPORTED;
+    if (T < 0 || q_heads < 1 || kv_heads < 0 || q_heads > 8192 || kv_heads > 8192 || q_heads + kv_heads > 8192 || !head_ok(head_dim) ||
+        rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim || !(fabsf(mult) < INFINITY))
+        return DSPARK_ERR_INVALID;
+    const int es = bytes_of(t);
+    const long long strides[] = {q_stride, q_out_stride, k_stride, k_out_stride};
+    for (int i = 0; i < (kv_heads ? 4 : 2); ++i)
+        if (strides[i] < (long long)(i < 2 ? q_heads : kv_heads) * head_dim || (strides[i] * es) % 16) return DSPARK_ERR_INVALID;
+    if (T == 0) return DSPARK_OK;
+    if (!dev(q, 16) || !dev(q_out, 16) || !dev(positions) || !dev(turns, 8)) return DSPARK_ERR_INVALID;
+    if (kv_heads && (!dev(k, 16) || !dev(k_out, 16))) return DSPARK_ERR_INVALID;
+    // an output is its input (the same rows), or apart from all the others
+    auto rows = [&](const void* a, long long stride, int heads) {
+        return Bytes{static_cast<const char*>(a), ((T - 1) * stride + (long long)heads * head_dim) * es};
+    };
+    const int sides = kv_heads ? 2 : 1;
+    const void* in[] = {q, k};
+    void* out[] = {q_out, k_out};
+    const long long in_stride[] = {q_stride, k_stride}, out_stride[] = {q_out_stride, k_out_stride};
+    const int heads[] = {q_heads, kv_heads};
+    for (int o = 0; o < sides; ++o) {
+        const Bytes to = rows(out[o], out_stride[o], heads[o]);
+        for (int i = 0; i < sides; ++i) {
+            const bool same = i == o && in[i] == out[o] && in_stride[i] == out_stride[o];
+            if (!same && rows_meet(to, out_stride[o] * es, heads[o] * head_dim * es, rows(in[i], in_stride[i], heads[i]), in_stride[i] * es,
+                                   heads[i] * head_dim * es))
+                return DSPARK_ERR_INVALID;
+        }
+        const Bytes fixed[] = {{reinterpret_cast<const char*>(positions), 4LL * T}, {reinterpret_cast<const char*>(turns), 4LL * rotary_dim}};
+        for (const Bytes& f : fixed)
+            if (to.meets(f)) return DSPARK_ERR_INVALID;
+    }
+    if (sides == 2 && rows_meet(rows(q_out, q_out_stride, q_heads), q_out_stride * es, q_heads * head_dim * es,
+                                rows(k_out, k_out_stride, kv_heads), k_out_stride * es, kv_heads * head_dim * es))
+        return DSPARK_ERR_INVALID;
+    RopeParams p;
+    p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
+    p.q_stride = q_stride; p.k_stride = k_stride; p.q_out_stride = q_out_stride; p.k_out_stride = k_out_stride;
+    p.bf16 = t == DSPARK_BF16;
+    p.positions = positions; p.turns = reinterpret_cast<const unsigned long long*>(turns);
+    p.T = T; p.Hq = q_heads; p.Hkv = kv_heads; p.D = head_dim; p.rotary = rotary_dim; p.interleaved = interleaved != 0;
+    p.mult = mult;
+    return launch_status(launch_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dspark_sample_workspace_bytes(int N) { return N < 0 || N > DSPARK_MAX_SAMPLE_ROWS ? 0 : kHead; }
+
+dspark_status dspark_sample(const void* logits, dspark_dtype t, long long row_stride, int N, int V, const float* u,
+                            const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                            int32_t* tok, float* logprob, void* ws, size_t ws_bytes, void* stream) {
+    const CallRange range_(__func__);
+    if (!dtype_ok(t)) return DSPARK_ERR_UNSUPPORTED;
+    const size_t need = dspark_sample_workspace_bytes(N);
+    if (need == 0 || V < 1 || V > DSPARK_MAX_SAMPLE_VOCAB) return DSPARK_ERR_INVALID;
+    if (N > 1 && (row_stride < V || (row_stride * bytes_of(t)) % 16)) return DSPARK_ERR_INVALID;
+    if (N == 0) return DSPARK_OK;
+    if (!dev(logits, 16) || !dev(u) || !dev_or_null(temperature) || !dev_or_null(top_k) || !dev_or_null(top_p) ||
+        !dev_or_null(min_p) || !dev(tok) || !dev_or_null(logprob) || !dev(ws, 256) || ws_bytes < need)
+        return DSPARK_ERR_INVALID;
+    SampleParams p;
+    p.logits = logits; p.row_stride = row_stride; p.bf16 = t == DSPARK_BF16;
+    p.N = N; p.V = V;
+    p.u = u; p.temperature = temperature; p.top_k = top_k; p.top_p = top_p; p.min_p = min_p;
+    p.tok = tok; p.logprob = logprob;
+    p.status = static_cast<uint32_t*>(ws);
+    return launch_status(launch_sample(p, static_cast<cudaStream_t>(stream)));
+}
+
 static bool attn_sizes_ok(int B, int q_heads, int kv_heads, int head_dim, int max_new) {
     return B >= 1 && B <= DSPARK_MAX_CACHE_REQUESTS && kv_heads >= 1 && q_heads >= kv_heads && q_heads <= 4096 &&
            q_heads % kv_heads == 0 && head_ok(head_dim) && max_new >= 1 && max_new <= DSPARK_MAX_GAMMA + 1;
@@ -177,6 +334,56 @@ dspark_status dspark_cache_attention(const void* q, long long q_stride, const vo
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas));
     p.status = static_cast<uint32_t*>(ws);
     return launch_status(launch_cache_attention(p, static_cast<cudaStream_t>(stream)));
+}
+
+dspark_status dspark_cache_attention4(const void* q, long long q_stride, dspark_dtype q_t, const void* k_cache,
+                                      const void* v_cache, const void* k_scale, const void* v_scale, long long page_stride,
+                                      long long scale_stride, int pages, int page_size, int k_exp, int v_exp,
+                                      const int32_t* block_table, int width, const int32_t* kv_len, const int32_t* q_off,
+                                      const int32_t* tile_off, int B, int N, int q_heads, int kv_heads, int head_dim,
+                                      int max_new, float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    const CallRange range_(__func__);
+    if (!dtype_ok(q_t)) return DSPARK_ERR_UNSUPPORTED;
+    if (!attn_sizes_ok(B, q_heads, kv_heads, head_dim, max_new) || head_dim % DSPARK_CACHE4_GROUP || N < 0 || width < 1 ||
+        !pages_ok(pages, page_size) || (long long)width * page_size > (1LL << 31) - 256 || (long long)N * q_heads >= (1LL << 31) ||
+        !exp_ok(k_exp) || !exp_ok(v_exp))
+        return DSPARK_ERR_INVALID;
+    if (!(scale > 0.f && scale < 3e38f) || !(scale * power(k_exp) > 0.f && scale * power(k_exp) < 3e38f)) return DSPARK_ERR_INVALID;
+    const int code_row = head_dim / 2, scale_row = head_dim / DSPARK_CACHE4_GROUP;
+    const long long rows_a_page = (long long)kv_heads * page_size;
+    if (page_stride < rows_a_page * code_row || page_stride % row_align(code_row) || scale_stride < rows_a_page * scale_row ||
+        scale_stride % row_align(scale_row) || q_stride < (long long)q_heads * head_dim || (q_stride * bytes_of(q_t)) % 16)
+        return DSPARK_ERR_INVALID;
+    if (N == 0) return DSPARK_OK;
+    if (!dev(q, 16) || !dev(k_cache, row_align(code_row)) || !dev(v_cache, row_align(code_row)) || !dev(k_scale, row_align(scale_row)) ||
+        !dev(v_scale, row_align(scale_row)) || !dev(block_table) || !dev(kv_len) || !dev(q_off) || !dev(tile_off) || !dev(out, 16) ||
+        !dev_or_null(lse) || !dev(ws, 256))
+        return DSPARK_ERR_INVALID;
+    if (ws_bytes < dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new)) return DSPARK_ERR_INVALID;
+    AttnParams p;
+    p.q = q; p.q_stride = q_stride; p.k = k_cache; p.v = v_cache; p.page_stride = page_stride;
+    p.ks = static_cast<const uint8_t*>(k_scale); p.vs = static_cast<const uint8_t*>(v_scale); p.scale_stride = scale_stride;
+    p.out_by = power(v_exp);
+    p.bf16 = q_t == DSPARK_BF16;
+    p.table = block_table; p.width = width;
+    p.kv_len = kv_len; p.q_off = q_off; p.tile_off = tile_off;
+    p.B = B; p.N = N; p.Hq = q_heads; p.Hkv = kv_heads; p.G = q_heads / kv_heads; p.D = head_dim;
+    p.pages = pages; p.page_size = page_size; p.max_new = max_new;
+    p.scale = scale * power(k_exp); p.out = out; p.lse = lse;
+    p.by_page.set((uint32_t)page_size);
+    p.by_group.set((uint32_t)p.G);
+    const int rows = p.G * max_new;
+    p.row_tile = p.bf16 ? attn4_row_tile(rows, head_dim) : attn_row_tile(rows, false);
+    const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
+    if (!p.bf16 && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
+    p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
+    p.ctas = num_sms() < kMaxAttnCtas ? num_sms() : kMaxAttnCtas;      // one resident CTA per SM
+    p.pad = p.bf16 ? 4 : 1;
+    p.spare = p.bf16;
+    p.split = reinterpret_cast<AttnSplitRow*>(static_cast<char*>(ws) + kHead);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas));
+    p.status = static_cast<uint32_t*>(ws);
+    return launch_status(launch_cache_attention4(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t dspark_logits_workspace_bytes(int B, int R) {

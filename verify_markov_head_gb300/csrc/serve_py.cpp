@@ -219,6 +219,151 @@ PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+struct Cache4 {
+    void* p[4];                              // codes of keys and values, scales of keys and values
+    int pages, heads, page_size, dim;
+    long long page_stride, scale_stride;
+};
+
+// Codes [pages, kv_heads, page_size, head_dim / 2] and scales [.., head_dim / 16], bytes; a page's contiguous.
+Cache4 caches4(PyObject* const* o) {
+    const char* const names[4] = {"k_cache", "v_cache", "k_scale", "v_scale"};
+    Cache4 c;
+    for (int i = 0; i < 4; ++i) {
+        const Tensor& t = of_dim(o[i], names[i], 4);
+        if (t.scalar_type() != at::kByte) fail(PyExc_TypeError, std::string(names[i]) + " must be torch.uint8, got " + type_name(t.scalar_type()));
+        const int64_t pages = t.size(0), heads = t.size(1), rows = t.size(2), row = t.size(3);
+        if ((row > 1 && t.stride(3) != 1) || (rows > 1 && t.stride(2) != row) || (heads > 1 && t.stride(1) != rows * row))
+            fail(PyExc_ValueError, "a page of the cache must be contiguous [kv_heads, page_size, bytes of a row]");
+        const long long stride = pages > 1 ? t.stride(0) : heads * rows * row;
+        if (i == 0) {
+            c.pages = extent(pages); c.heads = extent(heads); c.page_size = extent(rows); c.dim = extent(2 * row);
+            c.page_stride = stride;
+        } else {
+            if (i == 2) c.scale_stride = stride;
+            if (pages != c.pages || heads != c.heads || rows != c.page_size || stride != (i < 2 ? c.page_stride : c.scale_stride) ||
+                (i < 2 ? row * 2 : row * DSPARK_CACHE4_GROUP) != c.dim)
+                fail(PyExc_ValueError, "k_cache and v_cache must be [pages, kv_heads, page_size, head_dim / 2], k_scale and v_scale [.., head_dim / 16], "
+                                       "and share their strides");
+        }
+        c.p[i] = t.data_ptr();
+    }
+    return c;
+}
+
+// append: k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_exp, v_exp, ws, stream
+// read: k_cache, v_cache, k_scale, v_scale, slot_map, k, v, k_exp, v_exp, ws, stream
+template <bool kRead>
+PyObject* cache_rows4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 11, [&]() {
+        PyObject *ko = a[kRead ? 5 : 0], *vo = a[kRead ? 6 : 1], *so = a[kRead ? 4 : 2];
+        const Tensor &k = of_dim(ko, "k", 3), &v = of_dim(vo, "v", 3);
+        const Cache4 c = caches4(a + (kRead ? 0 : 3));
+        if (v.sizes() != k.sizes() || c.heads != k.size(1) || c.dim != k.size(2) || v.scalar_type() != k.scalar_type())
+            fail(PyExc_ValueError, "k and v must be [T, kv_heads, head_dim] of the cache's heads, of one dtype");
+        const dspark_dtype type = dtype_of(k);
+        const long long ks = token_stride(k, "k"), vs = token_stride(v, "v");
+        const int T = extent(k.size(0)), k_exp = integer(a[7]), v_exp = integer(a[8]);
+        const auto* slots = static_cast<const int32_t*>(typed(so, "slot_map", at::kInt, k.size(0)));
+        void *kp = k.data_ptr(), *vp = v.data_ptr(), *ws = workspace(a[9], nullptr), *s = stream_of(a[10]);
+        if constexpr (kRead) {
+            DSPARK_UNLOCKED(st, dspark_cache_read4(c.p[0], c.p[1], c.p[2], c.p[3], c.page_stride, c.scale_stride, c.pages, c.page_size,
+                                                   c.heads, c.dim, k_exp, v_exp, slots, T, kp, vp, type, ks, vs, ws, s));
+            return st;
+        } else {
+            DSPARK_UNLOCKED(st, dspark_cache_append4(kp, vp, type, ks, vs, slots, T, c.p[0], c.p[1], c.p[2], c.p[3], c.page_stride,
+                                                     c.scale_stride, c.pages, c.page_size, c.heads, c.dim, k_exp, v_exp, ws, s));
+            return st;
+        }
+    });
+}
+
+// q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out, ws, max_new, k_exp, v_exp, scale, lse, stream
+PyObject* cache_attention4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 17, [&]() {
+        const Tensor &q = of_dim(a[0], "q", 3), &table = of_dim(a[5], "block_table", 2), &out = tensor(a[9], "out");
+        const Cache4 c = caches4(a + 1);
+        if (c.dim != q.size(2) || out.scalar_type() != q.scalar_type() || out.sizes() != q.sizes())
+            fail(PyExc_ValueError, "q and out must be [N, q_heads, head_dim] of the cache's head_dim, of one dtype");
+        if (!out.is_contiguous()) fail(PyExc_ValueError, "tensors must be contiguous");
+        const dspark_dtype type = dtype_of(q);
+        const int64_t B = table.size(0), N = q.size(0), Hq = q.size(1);
+        const long long qs = token_stride(q, "q");
+        const auto* tab = static_cast<const int32_t*>(typed(a[5], "block_table", at::kInt));
+        const auto* len = static_cast<const int32_t*>(typed(a[6], "kv_len", at::kInt, B));
+        const auto* q_off = static_cast<const int32_t*>(typed(a[7], "q_off", at::kInt, B + 1));
+        const auto* tile_off = static_cast<const int32_t*>(typed(a[8], "tile_off", at::kInt, B + 1));
+        auto* lse = static_cast<float*>(typed_or_null(a[15], "lse", at::kFloat, N, Hq));
+        const int b = extent(B), nn = extent(N), width = extent(table.size(1)), hq = extent(Hq), max_new = integer(a[11]),
+                  k_exp = integer(a[12]), v_exp = integer(a[13]);
+        const float scale = a[14] == Py_None ? (float)std::pow((double)c.dim, -0.5) : number(a[14]);
+        const void* qp = q.data_ptr();
+        void* op = out.data_ptr();
+        size_t bytes = 0;
+        void *ws = workspace(a[10], &bytes), *s = stream_of(a[16]);
+        DSPARK_UNLOCKED(st, dspark_cache_attention4(qp, qs, type, c.p[0], c.p[1], c.p[2], c.p[3], c.page_stride, c.scale_stride, c.pages,
+                                                    c.page_size, k_exp, v_exp, tab, width, len, q_off, tile_off, b, nn, hq, c.heads, c.dim,
+                                                    max_new, scale, op, lse, ws, bytes, s));
+        return st;
+    });
+}
+
+// q, k (None: no keys), positions, turns, rotary_dim, mult, q_out, k_out, interleaved, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 10, [&]() {
+        const Tensor &q = of_dim(a[0], "q", 3), &qo = of_dim(a[6], "q_out", 3);
+        if (qo.sizes() != q.sizes() || qo.scalar_type() != q.scalar_type()) fail(PyExc_ValueError, "q_out must have q's shape and dtype");
+        const int64_t T = q.size(0), D = q.size(2);
+        const dspark_dtype type = dtype_of(q);
+        const long long qs = token_stride(q, "q"), qos = token_stride(qo, "q_out");
+        long long ks = 0, kos = 0;
+        int heads = 0;
+        const void* kp = nullptr;
+        void* kop = nullptr;
+        if ((a[1] == Py_None) != (a[7] == Py_None)) fail(PyExc_ValueError, "k and k_out go together");
+        if (a[1] != Py_None) {
+            const Tensor &k = of_dim(a[1], "k", 3), &ko = of_dim(a[7], "k_out", 3);
+            if (k.size(0) != T || k.size(2) != D || k.scalar_type() != q.scalar_type())
+                fail(PyExc_ValueError, "k must have q's tokens, head_dim and dtype");
+            if (ko.sizes() != k.sizes() || ko.scalar_type() != k.scalar_type()) fail(PyExc_ValueError, "k_out must have k's shape and dtype");
+            ks = token_stride(k, "k"); kos = token_stride(ko, "k_out");
+            heads = extent(k.size(1)); kp = k.data_ptr(); kop = ko.data_ptr();
+        }
+        const int tokens = extent(T), hq = extent(q.size(1)), dim = extent(D), rotary = integer(a[4]), interleaved = PyObject_IsTrue(a[8]);
+        const float mult = number(a[5]);
+        const auto* positions = static_cast<const int32_t*>(typed(a[2], "positions", at::kInt, T));
+        const auto* turns = static_cast<const uint64_t*>(typed(a[3], "turns", at::kLong, rotary / 2));
+        const void* qp = q.data_ptr();
+        void *qop = qo.data_ptr(), *s = stream_of(a[9]);
+        DSPARK_UNLOCKED(st, dspark_rope(qp, qs, kp, ks, type, positions, turns, rotary, interleaved, mult, qop, qos, kop, kos, tokens, hq, heads, dim, s));
+        return st;
+    });
+}
+
+// logits, u, tok, ws, temperature, top_k, top_p, min_p, logprob, stream
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 10, [&]() {
+        const Tensor& x = of_dim(a[0], "logits", 2);
+        const int64_t N = x.size(0), V = x.size(1);
+        if (V > 1 && x.stride(1) != 1) fail(PyExc_ValueError, "the entries of a row of logits must be contiguous");
+        const long long rs = N > 1 ? x.stride(0) : V;
+        const dspark_dtype type = dtype_of(x);
+        const auto* u = static_cast<const float*>(typed(a[1], "u", at::kFloat, N));
+        auto* tok = static_cast<int32_t*>(typed(a[2], "tok", at::kInt, N));
+        const auto* temperature = static_cast<const float*>(typed_or_null(a[4], "temperature", at::kFloat, N));
+        const auto* top_k = static_cast<const int32_t*>(typed_or_null(a[5], "top_k", at::kInt, N));
+        const auto* top_p = static_cast<const float*>(typed_or_null(a[6], "top_p", at::kFloat, N));
+        const auto* min_p = static_cast<const float*>(typed_or_null(a[7], "min_p", at::kFloat, N));
+        auto* logprob = static_cast<float*>(typed_or_null(a[8], "logprob", at::kFloat, N));
+        const int rows = extent(N), v = extent(V);
+        const void* xp = x.data_ptr();
+        size_t bytes = 0;
+        void *ws = workspace(a[3], &bytes), *s = stream_of(a[9]);
+        DSPARK_UNLOCKED(st, dspark_sample(xp, type, rs, rows, v, u, temperature, top_k, top_p, min_p, tok, logprob, ws, bytes, s));
+        return st;
+    });
+}
+
 // logits, out, ws, hist, hist_len, prompt_len, draft_tok, rep, freq, pres, bias_tok, bias_val, bias_off, mask, fill, live, stream
 PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 17, [&]() {
@@ -276,6 +421,11 @@ PyMethodDef methods[] = {
     {"cache_plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_plan)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"cache_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_attention)), METH_FASTCALL, nullptr},
+    {"cache_append4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_rows4<false>)), METH_FASTCALL, nullptr},
+    {"cache_read4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_rows4<true>)), METH_FASTCALL, nullptr},
+    {"cache_attention4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_attention4)), METH_FASTCALL, nullptr},
+    {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
+    {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sample)), METH_FASTCALL, nullptr},
     {"logits_process", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(logits_process)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
