@@ -79,9 +79,9 @@ struct RopeParams {
     const int32_t* positions; const unsigned long long* turns;
     int T, Hq, Hkv, D, rotary, interleaved;
     float mult;
-    // set by the launch: tokens of a block, a head's items and those of them that are turned
-    int side, items, turned;
-    FastDiv by_items, by_half, by_heads;
+    // set by the launch: a head's items and those of them that are turned, heads that a
+    // warp takes at a time, warps of a token
+    int items, turned, side, shares;
 };
 cudaError_t launch_rope(RopeParams p, cudaStream_t s);
 
