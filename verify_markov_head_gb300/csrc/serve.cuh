@@ -128,7 +128,10 @@ cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_cache_attention4(const AttnParams& p, cudaStream_t s);
 bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can copy
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
-int attn4_row_tile(int rows, int D);              // query rows at a time over a cache in 4 bits
+// Over a cache in 4 bits every warp is a worker of its own (AttnParams::ctas of them): query
+// rows at a time, and warps of a CTA for groups of 8 rows, as registers allow.
+inline int attn4_row_tile(int rows, int D) { return rows <= 8 ? 8 : rows <= 16 || D > 128 ? 16 : 32; }
+constexpr int attn4_warps(int groups, int D) { return groups == 1 && D <= 128 ? 12 : 8; }
 cudaError_t launch_attn4_mma(const AttnParams& p, cudaStream_t s);   // bf16 queries, a cache in 4 bits
 // Rows of a row tile where a key-value head has `rows` query rows.
 inline int attn_row_tile(int rows, bool mma) {

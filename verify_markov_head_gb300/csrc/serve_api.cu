@@ -274,7 +274,13 @@ size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_d
     // the larger of the two kernels' tiles (of 9 to 16 rows 32 on CUDA cores, 16 on tensor cores)
     const int all = q_heads / kv_heads * max_new, mma = attn_row_tile(all, true), simt = attn_row_tile(all, false);
     const size_t rows = mma > simt ? mma : simt;
-    return kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas) + ws_align256((size_t)2 * kMaxAttnCtas * rows * (head_dim + 2) * sizeof(float));
+    size_t parts = kMaxAttnCtas * rows, splits = kMaxAttnCtas;
+    if (head_dim % DSPARK_CACHE4_GROUP == 0) {       // and the warps over a cache in 4 bits
+        const size_t tile = attn4_row_tile(all, head_dim), workers = (size_t)kMaxAttnCtas * attn4_warps((int)tile / 8, head_dim);
+        if (workers * tile > parts) parts = workers * tile;
+        splits = workers;
+    }
+    return kHead + ws_align256(sizeof(AttnSplitRow) * splits) + ws_align256(2 * parts * (head_dim + 2) * sizeof(float));
 }
 
 dspark_status dspark_cache_attention(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -378,10 +384,11 @@ dspark_status dspark_cache_attention4(const void* q, long long q_stride, dspark_
     if (!p.bf16 && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
     p.ctas = num_sms() < kMaxAttnCtas ? num_sms() : kMaxAttnCtas;      // one resident CTA per SM
-    p.pad = p.bf16 ? 4 : 1;
+    if (p.bf16) p.ctas *= attn4_warps(p.row_tile / 8, head_dim);
+    p.pad = p.bf16 ? 2 : 1;
     p.spare = p.bf16;
     p.split = reinterpret_cast<AttnSplitRow*>(static_cast<char*>(ws) + kHead);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas));
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * p.ctas));
     p.status = static_cast<uint32_t*>(ws);
     return launch_status(launch_cache_attention4(p, static_cast<cudaStream_t>(stream)));
 }
