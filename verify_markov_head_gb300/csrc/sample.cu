@@ -3,23 +3,25 @@
 //
 // A cluster of CTAs takes a row and keeps it in shared memory: it is read from
 // HBM once, whatever is asked of it.  With weights w_v = e^((x_v - max) / T):
-//   thresholds  the k-th largest entry, and the entry at which the descending sum of
-//               weights reaches top_p of the total, by digits of the entries' bits
-//               taken as ordered integers (11, 11 and 10 bits, 11 and 5 of bf16):
-//               a histogram of counts, or of weights, over the row, the digit in
-//               which the wanted count or sum is reached, then the next digit of
-//               the entries that share it.  No sort.
-//   the draw    sums of the weights left, by warp and CTA in the order of the ids, and a
-//               walk through the one warp's share that holds u times the total.
+//   few      top-k up to 512: of the threads' own maxima, the 1/32 power of 2 of the weight in
+//            which the k-th largest lies is a bound that k entries reach; the entries that
+//            reach it, hardly more than k, go to one CTA, which ranks, cuts and draws.
+//   many     top-k beyond, and top-p: a histogram of counts, or of weights, over such
+//            steps, the step in which the wanted count or sum is reached, and its entries (a
+//            hundredth of the row) to one CTA, which finds the last one kept bit by bit.
+//            No sort.
+//   the draw sums of the weights left, by warp and CTA in the order of the ids, and a
+//            walk through the one warp's share that holds u times the total.
 //
 // A token's boundaries are sums over up to 2^19 entries, and a sum that is off by
 // 2^-24 moves the draw across one in a row of some thousand (the boundaries of a
 // flat row are 10^-5 apart).  So weights are integers of 2^-42 of the largest:
 // sums are exact, and the same in any order, atomics among them.  A weight is
-//     2^(y - M),  y = x log2(e) / T = k / 64 + r,  |r| <= 2^-7,
-// the product y in two floats, 2^(k mod 64 / 64) from a table of integers, and
-// 2^r - 1 by its series to r^4: off by 2^-31 of the weight.  In double precision it
-// would be the FP64 units' two operations a cycle that bound the kernel.
+//     2^(y - ref),  y = x log2(e) / T = k / 256 + r,  |r| <= 2^-9,
+// y by fused multiply-adds with log2(e) / T in two floats, 2^(k mod 256 / 256) from a
+// table of integers, and 2^r - 1 by its series to r^3, as an integer: off by 2^-31 of
+// the weight, in 15 operations (floats two at a time).  In double precision it would be
+// the FP64 units' two operations a cycle that bound the kernel.
 #include <cooperative_groups.h>
 
 #include "pdl.cuh"
@@ -32,54 +34,81 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048;
 constexpr int kUnit = 42;                        // a weight of 1 is 2^kUnit
+constexpr int kFine = 8;                         // log2 of the table's entries
+constexpr int kCoarse = 3;                       // log2 of the table's steps to a bin
+constexpr float kDeep = 50.f;                    // entries that many powers of 2 below the largest weigh nothing
+constexpr int kFew = 512, kCandidates = 1024;    // top_k that is looked for among candidates, and their most
+constexpr int kListed = 4096;                    // entries of a step that one CTA takes
 constexpr uint32_t kLowest = 0x007fffffu;        // the key of -inf
 constexpr uint32_t kAll = 0xffffffffu;
 
 using u64 = unsigned long long;
 
-// 2^(j / 64) * 2^kUnit, from the 64th root of 2 (by Newton's method).
+// 2^(31 + j / 256), from the 256th root of 2 (square roots by Newton's method).
 struct Powers {
-    u64 v[64];
+    uint32_t v[1 << kFine];
     constexpr Powers() : v{} {
         double root = 2.0;
-        for (int i = 0; i < 6; ++i) {            // six square roots
+        for (int i = 0; i < kFine; ++i) {
             double x = 1.5;
             for (int n = 0; n < 30; ++n) x = 0.5 * (x + root / x);
             root = x;
         }
-        for (int j = 0; j < 64; ++j) {
+        for (int j = 0; j < 1 << kFine; ++j) {
             double x = 1.0, f = root;            // root^j by squares: few roundings
             for (int n = j; n; n >>= 1, f *= f)
                 if (n & 1) x *= f;
-            v[j] = (u64)(x * (double)(1ull << kUnit) + 0.5);
+            v[j] = (uint32_t)(x * 2147483648.0 + 0.5);
         }
     }
 };
 __constant__ Powers c_powers = Powers();
 
-// Integers in the order of the numbers they stand for (no NaN, no -0).
+// Integers in the order of the numbers they stand for (no NaN; -0 is 0).
 __device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.f);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
+// Two numbers at a time.
+__device__ __forceinline__ u64 two(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(u64 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 shift_right(u64 x, uint32_t n) {   // (0 from 64 on)
+    u64 r;
+    asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(x), "r"(n));
+    return r;
+}
 
-// log2(e) / temperature in two floats, and what entries are taken from.  In
-// double precision, by one thread of a CTA: the FP64 units do two operations a
-// cycle, 512 threads would take 4 us.
+// log2(e) / temperature in two floats, and what entries are taken from.
 struct Scale {
     float base, low, c_hi, c_lo;
-    __device__ __forceinline__ void set(float top, float T) {
-        // entries 50 powers of 2 below the largest weigh nothing.  Where y itself
-        // is so large that its fraction is lost, entries are taken from the
-        // largest one: exactly, since what still weighs something is that near to it
-        const double c = fmin(fmax(1.4426950408889634 / (double)T, 1e-37), 1e30);
-        c_hi = (float)c;
-        c_lo = (float)(c - (double)c_hi);
-        base = fabs(top * c) > 16384.0 ? top : 0.f;
-        low = fmaxf((float)((double)(top - base) - 50.0 / c), -3.4e38f);      // (behind the base)
+    __device__ __forceinline__ Scale(float top, float T) {
+        // (Temperatures are taken into 10^-30 .. 10^36: below only the largest entries weigh
+        // anything, above -inf would.)
+        T = fminf(fmaxf(T, 1e-30f), 1e36f);
+        constexpr float e_hi = 1.44269502f, e_lo = 1.92596303e-8f;
+        c_hi = e_hi / T;
+        c_lo = (fmaf(-c_hi, T, e_hi) + e_lo) / T;
+        // Where y itself is so large that its fraction is lost, entries are taken from
+        // the largest one: exactly, since what still weighs something is that near to it.
+        base = fabsf(top * c_hi) > 4096.f ? top : 0.f;
+        low = fmaxf((top - base) - kDeep / c_hi, -3.4e38f);      // (behind the base)
     }
 };
 
@@ -92,35 +121,75 @@ __device__ __forceinline__ u64 part_of(float x, u64 n, bool& rest) {
 
 // Weights of a row's entries.
 struct Weigher {
-    float base, low, c_hi, c_lo;
-    int ref;
-    const u64* powers;
-    // (k, r) of y = k / 64 + r
-    __device__ __forceinline__ int split(float x, float& r) const {
-        constexpr float kMagic = 196608.f;       // 1.5 * 2^17: a sum's last place is 1 / 64
-        const float z = fmaxf(x - base, low), y = z * c_hi;
-        const float rest = fmaf(z, c_lo, fmaf(z, c_hi, -y)), m = y + kMagic;
-        r = (y - (m - kMagic)) + rest;
-        return __float_as_int(m) - __float_as_int(kMagic);
+    u64 base, c_hi, c_lo;                        // (the negative base)
+    float low;
+    uint32_t ref;                                // the step of the largest entry, rounded down to a power of 2
+    const uint32_t* powers;
+    static constexpr float kMagic = 1.5f * (1 << (23 - kFine));      // a sum's last place is a step
+    static constexpr float kRound = 12582912.f;                      // 1.5 * 2^23: a sum's last place is 1
+    // z = x less the base, not below `low`, and k (as the bits of a float) of two entries
+    __device__ __forceinline__ u64 steps(float x0, float x1, uint32_t& k0, uint32_t& k1, u64& m) const {
+        float a, b, s, t;
+        apart(add2(two(x0, x1), base), a, b);
+        const u64 z = two(fmaxf(a, low), fmaxf(b, low));
+        m = fma2(z, c_hi, two(kMagic, kMagic));
+        apart(m, s, t);
+        k0 = __float_as_uint(s);
+        k1 = __float_as_uint(t);
+        return z;
     }
-    __device__ __forceinline__ void set(const Scale& c, float top, const u64* table) {
-        base = c.base; low = c.low; c_hi = c.c_hi; c_lo = c.c_lo;
+    __device__ __forceinline__ void set(const Scale& c, float top, const uint32_t* table) {
+        base = two(-c.base, -c.base); c_hi = two(c.c_hi, c.c_hi); c_lo = two(c.c_lo, c.c_lo);
+        low = c.low;
         powers = table;
-        ref = 0;
-        float r;
-        ref = split(top, r) >> 6;
+        uint32_t k, same;
+        u64 m;
+        steps(top, top, k, same, m);
+        ref = k >> kFine;
     }
-    __device__ __forceinline__ u64 operator()(float x) const {
-        float r;
-        const int k = split(x, r);
-        // 2^r - 1 = r ln 2 + (r ln 2)^2 / 2 + ..
-        const float p = r * fmaf(r, fmaf(r, fmaf(r, 0.00961812911f, 0.0555041087f), 0.240226507f), 0.693147181f);
-        const u64 t = powers[k & 63];
-        const int more = __float2int_rn(p * __uint2float_rn((uint32_t)(t >> (kUnit - 30))) * 128.f);      // of 2^-37
-        const int down = min(ref - (k >> 6), 63);
-        return x == -INFINITY ? 0ull : (t + (u64)((long long)more << (kUnit - 37))) >> down;
+    __device__ __forceinline__ void operator()(float x0, float x1, u64& w0, u64& w1, uint32_t& k0, uint32_t& k1) const {
+        u64 m;
+        const u64 z = steps(x0, x1, k0, k1, m);
+        u64 r = fma2(z, c_hi, fma2(m, two(-1.f, -1.f), two(kMagic, kMagic)));
+        r = fma2(z, c_lo, r);
+        // (2^r - 1) 2^31 = 2^31 (r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6 ..), to an integer
+        constexpr float a1 = 1488522236.f, a2 = 515882496.f, a3 = 119194166.f;
+        const u64 e = fma2(r, fma2(r, fma2(r, two(a3, a3), two(a2, a2)), two(a1, a1)), two(kRound, kRound));
+        float f0, f1;
+        apart(e, f0, f1);
+        constexpr uint32_t kOne = 0x80000000u - 0x4b400000u;       // 2^31, less the bits of kRound
+        w0 = shift_right((u64)powers[k0 & ((1 << kFine) - 1)] * (__float_as_uint(f0) + kOne), 62 - kUnit + (ref - (k0 >> kFine)));
+        w1 = shift_right((u64)powers[k1 & ((1 << kFine) - 1)] * (__float_as_uint(f1) + kOne), 62 - kUnit + (ref - (k1 >> kFine)));
+    }
+    __device__ __forceinline__ u64 of(float x) const {
+        u64 w, same;
+        uint32_t k0, k1;
+        (*this)(x, x, w, same, k0, k1);
+        return w;
+    }
+    // the bin of a step, from the largest entry's down
+    __device__ __forceinline__ uint32_t top_bin() const { return (ref << kFine | ((1 << kFine) - 1)) >> kCoarse; }
+    __device__ __forceinline__ uint32_t bin(uint32_t k) const { return top_bin() - (k >> kCoarse); }
+    // numbers that no entry of a bin is below, or above: its ends and a little more
+    // (the last bins also hold what lies below them)
+    __device__ __forceinline__ float least(uint32_t b, const Scale& c) const {
+        if (b >= (uint32_t)(kDeep - 1.f) << (kFine - kCoarse)) return -INFINITY;
+        const int at = (int)(top_bin() - (__float_as_uint(kMagic) >> kCoarse) - b) << kCoarse;
+        const float x = c.base + ((float)at * (1.f / (1 << kFine)) - 0.01f) / c.c_hi;
+        return x - 1e-5f * fabsf(x);
+    }
+    __device__ __forceinline__ float most(uint32_t b, const Scale& c) const {
+        const int at = (int)(top_bin() - (__float_as_uint(kMagic) >> kCoarse) - b + 1) << kCoarse;
+        const float x = c.base + ((float)at * (1.f / (1 << kFine)) + 0.01f) / c.c_hi;
+        return x + 1e-5f * fabsf(x);
     }
 };
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 template <typename T> struct Row;
 template <> struct Row<float> {
@@ -132,6 +201,9 @@ template <> struct Row<float> {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
     static __device__ __forceinline__ float one(const float* p) { return *p; }
+    static __device__ __forceinline__ float top(uint4 w) {
+        return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
 };
 template <> struct Row<uint16_t> {
     static constexpr int kVec = 8;
@@ -147,21 +219,33 @@ template <> struct Row<uint16_t> {
         return make_uint4(u[0], u[1], u[2], u[3]);
     }
     static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+    static __device__ __forceinline__ float top(uint4 w) {
+        uint32_t m;
+        asm("{\n\t.reg .b32 a, b;\n\tmax.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 b, %3, %4;\n\tmax.NaN.bf16x2 %0, a, b;\n\t}"
+            : "=r"(m) : "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
 };
 
 struct Shared {
-    u64 powers[64];
-    uint32_t lo[kBins], hi[kBins];               // counts, or weights in two words
-    u64 merged[kBins];                           // this CTA's share of the bins, over the cluster
-    u64 warp_sum[kWarps];
+    uint32_t powers[1 << kFine];
+    union {
+        struct { uint32_t lo[kBins], hi[kBins]; u64 merged[kBins]; } hist;       // counts, or weights in two words; this CTA's share of the bins, over the cluster
+        struct { float x[kCandidates]; uint32_t id[kCandidates]; u64 w[kCandidates]; } cand;
+        struct { float x[kListed]; uint32_t id[kListed]; } list;
+    };
+    float tops[kThreads];                        // the threads' maxima
+    u64 warp_sum[kWarps], block;
     u64 total, sums[2];                          // read by the other CTAs
-    u64 found_above, found_at;
-    uint32_t found_bin, best;
-    Scale scale;
-    float floor;                                 // the least entry that min_p keeps
+    u64 share_above, share_all;
+    u64 found_above;
+    uint32_t found_bin, found_share;
     float top;
-    uint32_t bad;
-    uint32_t warp_ties[kWarps], ties;
+    uint32_t bad, best;
+    uint32_t gathered;                           // candidates, or entries listed, of CTA 0
+    float last_x; uint32_t last_id;              // the last entry kept, of CTA 0
+    float bound;
+    uint32_t warp_word[kWarps];
 };
 
 __device__ __forceinline__ u64 warp_add(u64 x) {
@@ -179,7 +263,31 @@ __device__ __forceinline__ u64 warp_scan(u64 x) {            // inclusive
     return x;
 }
 
-struct Found { uint32_t key; u64 above, at, want; };   // a key, the sum above it and at it, the sum that was wanted
+
+// The sum over the CTA, in every thread.
+__device__ __forceinline__ u64 block_add(u64 x, Shared& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    x = warp_add(x);
+    if (lane == 0) s.warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        x = warp_add(lane < kWarps ? s.warp_sum[lane] : 0ull);
+        if (lane == 0) s.block = x;
+    }
+    __syncthreads();
+    return s.block;
+}
+
+// ln(w / total), a share near 1 by what it lacks.  The quotient q is off by r / total,
+// which its logarithm takes up: the numbers are in two floats.
+__device__ __forceinline__ float log_share(u64 w, u64 total) {
+    const bool near = total - w < w;
+    const u64 n = near ? total - w : w;
+    const float n_hi = __ull2float_rn(n), t_hi = __ull2float_rn(total);
+    const float n_lo = (float)(long long)(n - __float2ull_rn(n_hi)), t_lo = (float)(long long)(total - __float2ull_rn(t_hi));
+    const float q = n_hi / t_hi, r = (fmaf(-q, t_hi, n_hi) + fmaf(-q, t_lo, n_lo)) / t_hi;
+    return near ? log1pf(-q) - r / (1.f - q) : logf(q) + r / q;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
@@ -191,51 +299,79 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = p.ctas, rank = (int)(blockIdx.x % ctas), row = (int)(blockIdx.x / ctas);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < 64) s.powers[tid] = c_powers.v[tid];
-    if (tid == 0) s.bad = 0u;
+    if (tid < 1 << kFine) s.powers[tid] = c_powers.v[tid];
+    if (tid == 0) s.bad = s.gathered = 0u;
     __syncthreads();
     grid_dependency_wait();
 
     // the row's slice, into shared memory; entries that are no numbers become -inf
     const int first = min(p.V, rank * p.slice), count = min(p.V - first, p.slice), vecs = (count + kVec - 1) / kVec;
     const T* src = static_cast<const T*>(p.logits) + row * p.row_stride + first;
-    float top = -INFINITY;
-    bool bad = false;
-#pragma unroll 4
-    for (int i = tid; i < vecs; i += kThreads) {
-        float x[kVec];
-        if ((i + 1) * kVec <= count) R::get(__ldcs(reinterpret_cast<const uint4*>(src) + i), x);
-        else
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) x[j] = i * kVec + j < count ? R::one(src + i * kVec + j) : -INFINITY;
+    float top = -INFINITY;                       // NaN once an entry is, +inf once one is
+    auto clean = [&](int i) {
+        float x[kVec], most = -INFINITY;
+        R::get(slice[i], x);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            if (!(x[j] < INFINITY)) { x[j] = -INFINITY; bad = true; }
-            x[j] += 0.f;                         // -0 is 0
-            top = fmaxf(top, x[j]);
+            if (!(x[j] < INFINITY)) x[j] = -INFINITY;
+            most = fmaxf(most, x[j]);
         }
         slice[i] = R::put(x);
-    }
+        return most;
+    };
+    const int whole = count / kVec;
+    constexpr int kAhead = 8;
+    for (int i0 = tid; i0 < whole; i0 += kAhead * kThreads) {
+        uint4 w[kAhead];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (lane == 0) s.warp_sum[warp] = key_of(top);
-    if (bad) s.bad = 1u;
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u * kThreads < whole) w[u] = __ldcs(reinterpret_cast<const uint4*>(src) + i0 + u * kThreads);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u * kThreads < whole) {
+                top = max_nan(top, R::top(w[u]));
+                slice[i0 + u * kThreads] = w[u];
+            }
+    }
+    if (whole < vecs && tid == 0) {
+        float x[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[j] = whole * kVec + j < count ? R::one(src + whole * kVec + j) : -INFINITY;
+        slice[whole] = R::put(x);
+        top = max_nan(top, R::top(slice[whole]));
+    }
+    if (!(top < INFINITY)) {                     // some are no numbers: they become -inf
+        s.bad = 1u;
+        top = -INFINITY;
+        // (the vectors that this thread brought, the last one by the first thread)
+        for (int i = tid; i < vecs; i += kThreads) {
+            if (i == whole) break;
+            top = fmaxf(top, clean(i));
+        }
+        if (whole < vecs && tid == 0) top = fmaxf(top, clean(whole));
+    }
+    s.tops[tid] = top;
+    const uint32_t warp_top = __reduce_max_sync(~0u, key_of(top));
+    if (lane == 0) s.warp_word[warp] = warp_top;
     __syncthreads();
-    if (tid == 0) {
-        uint32_t k = 0u;
-        for (int w = 0; w < kWarps; ++w) k = max(k, (uint32_t)s.warp_sum[w]);
-        s.top = value_of(k);
-        if (s.bad) raise_status(p.status, kBadInput);
+    if (warp == 0) {
+        const uint32_t k = __reduce_max_sync(~0u, lane < kWarps ? s.warp_word[lane] : 0u);
+        if (lane == 0) {
+            s.top = value_of(k);
+            if (s.bad) raise_status(p.status, kBadInput);
+        }
     }
     cluster.sync();
-    for (int r = 0; r < ctas; ++r) top = fmaxf(top, *cluster.map_shared_rank(&s.top, r));
+    top = value_of(__reduce_max_sync(~0u, key_of(lane < ctas ? *cluster.map_shared_rank(&s.top, lane) : -INFINITY)));
 
     // a warp's share of the slice, in the order of the ids
     const int share = (vecs + kWarps - 1) / kWarps, v0 = min(vecs, warp * share), v1 = min(vecs, v0 + share);
     const float T_ = p.temperature ? p.temperature[row] : 1.f;
     const bool T_ok = T_ >= 0.f && T_ < INFINITY;
     float top_p = p.top_p ? p.top_p[row] : 1.f, min_p = p.min_p ? p.min_p[row] : 0.f;
-    const int top_k = p.top_k ? p.top_k[row] : 0;
+    int top_k = p.top_k ? p.top_k[row] : 0;
+    if (top_k <= 0 || top_k >= p.V) top_k = 0;   // all
+    const float u_ = p.u[row], u = u_ > 0.f ? fminf(u_, 0x1.fffffep-1f) : 0.f;
     if (rank == 0 && tid == 0 && (!T_ok || top_p != top_p || min_p != min_p)) raise_status(p.status, kBadInput);
     if (top_p != top_p) top_p = 1.f;
     if (min_p != min_p) min_p = 0.f;
@@ -246,7 +382,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             p.tok[row] = -1;
             if (p.logprob) p.logprob[row] = -INFINITY;
         }
-    } else if (!T_ok || T_ == 0.f) {             // the lowest id of the largest
+        cluster.sync();                          // (shared memory stays until all have read it)
+        return;
+    }
+    if (!T_ok || T_ == 0.f) {                    // the lowest id of the largest
         uint32_t best = kAll;
         for (int v = v0 + lane; v < v1; v += 32) {
             float x[kVec];
@@ -256,10 +395,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
                 if (x[j] == top) best = min(best, (uint32_t)(first + v * kVec + j));
         }
         best = __reduce_min_sync(~0u, best);
-        if (lane == 0) s.warp_ties[warp] = best;
+        if (lane == 0) s.warp_word[warp] = best;
         __syncthreads();
         if (tid == 0) {
-            for (int w = 0; w < kWarps; ++w) best = min(best, s.warp_ties[w]);
+            for (int w = 0; w < kWarps; ++w) best = min(best, s.warp_word[w]);
             s.best = best;
         }
         cluster.sync();
@@ -268,263 +407,432 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             p.tok[row] = (int)best;
             if (p.logprob) p.logprob[row] = 0.f;
         }
-    } else {
-        if (tid == 0) {
-            s.scale.set(top, T_);
-            // (rounded up: an entry is kept where it is not below the exact border)
-            s.floor = min_p > 0.f ? __double2float_ru((double)top + (double)T_ * log((double)fminf(min_p, 1.f))) : -INFINITY;
+        cluster.sync();
+        return;
+    }
+    const Scale scale(top, T_);
+    Weigher weight;
+    weight.set(scale, top, s.powers);
+    // min_p, of the largest entry's weight
+    u64 least_w = 0ull;
+    if (min_p > 0.f) {
+        least_w = weight.of(top);
+        if (min_p < 1.f) {
+            bool rest;
+            const u64 part = part_of(min_p, least_w, rest);
+            least_w = part + (rest ? 1ull : 0ull);
         }
-        __syncthreads();
-        Weigher weight;
-        weight.set(s.scale, top, s.powers);
-        const int chunk = kBins / ctas;
+    }
 
-        // The key above `floor` at which the sum from the largest key down reaches a
-        // wanted amount: `want` entries, or weights of `part` of all of them and
-        // `beside` together (then the key is `floor` where they do not reach it).
-        auto select = [&](bool mass, u64 want, float part, u64 beside, uint32_t floor) {
-            Found f{0u, 0ull, 0ull, want};
-            int shift = 32;
-#pragma unroll 1
-            for (int level = 0; level < (sizeof(T) == 2 ? 2 : 3); ++level) {
-                const int bits = level == 0 ? 11 : sizeof(T) == 2 ? 5 : level == 1 ? 11 : 10, above = shift;
-                shift -= bits;
-                for (int i = tid; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0u;
-                __syncthreads();
-                for (int v = tid; v < vecs; v += kThreads) {
-                    float x[kVec];
-                    R::get(slice[v], x);
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        const uint32_t k = key_of(x[j]);
-                        if (k <= floor || (level && k >> above != f.key >> above)) continue;
-                        const uint32_t bin = (k >> shift) & ((1u << bits) - 1u);
-                        if (mass) {
-                            const u64 w = weight(x[j]);
-                            const uint32_t lo = (uint32_t)w, old = atomicAdd(&s.lo[bin], lo);
-                            const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
-                            if (hi) atomicAdd(&s.hi[bin], hi);
-                        } else {
-                            atomicAdd(&s.lo[bin], 1u);
-                        }
-                    }
-                }
-                cluster.sync();
-                // the cluster's sums of this CTA's share of the bins
-                u64 mine = 0ull;
-                for (int i = tid; i < chunk; i += kThreads) {
-                    u64 sum = 0ull;
-                    for (int r = 0; r < ctas; ++r) {
-                        const Shared* o = cluster.map_shared_rank(&s, r);
-                        sum += ((u64)o->hi[rank * chunk + i] << 32) + o->lo[rank * chunk + i];
-                    }
-                    s.merged[i] = sum;
-                    mine += sum;
-                }
-                mine = warp_add(mine);
-                if (lane == 0) s.warp_sum[warp] = mine;
-                __syncthreads();
-                if (tid == 0) {
-                    u64 sum = 0ull;
-                    for (int w = 0; w < kWarps; ++w) sum += s.warp_sum[w];
-                    s.total = sum;
-                }
-                cluster.sync();
-                if (level == 0 && mass) {
-                    u64 all = 0ull;
-                    for (int r = 0; r < ctas; ++r) all += *cluster.map_shared_rank(&s.total, r);
-                    bool rest;
-                    const u64 goal = part_of(part, all + beside, rest);
-                    f.want = max(1ull, goal + (rest ? 1ull : 0ull));
-                    if (f.want > all) { f.key = floor; f.above = all; break; }
-                }
-                // the share of the bins that the wanted sum is reached in, from the top
-                u64 sum = f.above;
-                int r = ctas - 1;
-                for (; r > 0; --r) {
-                    const u64 t = *cluster.map_shared_rank(&s.total, r);
-                    if (sum + t >= f.want) break;
-                    sum += t;
-                }
-                // and the bin: the share's bins in descending order, `each` to a thread
-                const u64* bins = cluster.map_shared_rank(s.merged, r);
-                const int each = (chunk + kThreads - 1) / kThreads;
-                u64 own[4], all = 0ull;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = tid * each + e;
-                    own[e] = e < each && i < chunk ? bins[chunk - 1 - i] : 0ull;
-                    all += own[e];
-                }
-                const u64 scan = warp_scan(all);
-                if (lane == 31) s.warp_sum[warp] = scan;
-                __syncthreads();
-                u64 before = sum + scan - all;
-                for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (before < f.want && before + own[e] >= f.want) {
-                        s.found_bin = (uint32_t)(r * chunk + chunk - 1 - (tid * each + e));
-                        s.found_above = before;
-                        s.found_at = own[e];
-                    }
-                    before += own[e];
-                }
-                __syncthreads();
-                f.key |= s.found_bin << shift;
-                f.above = s.found_above;
-                f.at = s.found_at;
+    // ------------------------------------------------------------------- few
+    if (top_k && top_k <= kFew) {
+        if (rank == 0) {
+            // the bin of the threads' maxima in which the top_k-th lies
+            for (int i = tid; i < kBins; i += kThreads) s.hist.lo[i] = 0u;
+            __syncthreads();
+            for (int r = 0; r < ctas; r += 2) {
+                const float a = cluster.map_shared_rank(s.tops, r)[tid], b = r + 1 < ctas ? cluster.map_shared_rank(s.tops, r + 1)[tid] : -INFINITY;
+                uint32_t ka, kb;
+                u64 m;
+                weight.steps(a, b, ka, kb, m);
+                if (a > -INFINITY) atomicAdd(&s.hist.lo[weight.bin(ka)], 1u);
+                if (b > -INFINITY) atomicAdd(&s.hist.lo[weight.bin(kb)], 1u);
             }
+            if (tid == 0) s.bound = -INFINITY;
             __syncthreads();
-            if (sizeof(T) == 2 && f.key != floor && !(f.key & 0x80000000u)) f.key |= 0xffffu;     // (negative: the low bits are set)
-            return f;
-        };
-        // a sum over the cluster of what each thread counted (a place of its own: another
-        // CTA may still read the one before)
-        auto sum_all = [&](u64 mine, int which) {
-            mine = warp_add(mine);
+            const uint4 own = reinterpret_cast<const uint4*>(s.hist.lo)[tid];
+            const uint32_t all = own.x + own.y + own.z + own.w;
+            const u64 scan = warp_scan(all);
+            if (lane == 31) s.warp_word[warp] = (uint32_t)scan;
             __syncthreads();
-            if (lane == 0) s.warp_sum[warp] = mine;
-            __syncthreads();
-            if (tid == 0) {
-                u64 sum = 0ull;
-                for (int w = 0; w < kWarps; ++w) sum += s.warp_sum[w];
-                s.sums[which] = sum;
+            uint32_t before = (uint32_t)scan - all;
+            for (int w = 0; w < warp; ++w) before += s.warp_word[w];
+            if (before < (uint32_t)top_k && before + all >= (uint32_t)top_k) {
+                uint32_t b = 4 * tid;
+                if ((before += own.x) < (uint32_t)top_k) {
+                    ++b;
+                    if ((before += own.y) < (uint32_t)top_k) b += before + own.z < (uint32_t)top_k ? 2u : 1u;
+                }
+                s.bound = weight.least(b, scale);
             }
-            cluster.sync();
-            u64 all = 0ull;
-            for (int r = 0; r < ctas; ++r) all += *cluster.map_shared_rank(&s.sums[which], r);
-            return all;
-        };
-
-        // what is kept: the keys above `cut`, and the first `ties` entries at it
-        uint32_t cut = kLowest, ties = 0u;
-        if (top_k > 0 && top_k < p.V) {
-            u64 mine = 0ull;
+        }
+        cluster.sync();
+        Shared* const to = cluster.map_shared_rank(&s, 0);
+        const float least = to->bound;
+        if (least > -INFINITY) {                 // (else fewer than top_k maxima weigh something)
             for (int v = tid; v < vecs; v += kThreads) {
                 float x[kVec];
                 R::get(slice[v], x);
+                bool any = false;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) mine += x[j] > -INFINITY ? 1ull : 0ull;
-            }
-            if ((u64)top_k < sum_all(mine, 0)) {
-                const Found f = select(false, (u64)top_k, 0.f, 0ull, kLowest);
-                const u64 n = f.want - f.above;
-                cut = n < f.at ? f.key : f.key - 1u;
-                ties = n < f.at ? (uint32_t)n : 0u;
-            }
-        }
-        if (top_p < 1.f) {
-            const u64 at_cut = ties ? weight(value_of(cut)) : 0ull;
-            const Found f = select(true, 0ull, fmaxf(top_p, 0.f), at_cut * ties, cut);
-            const bool above = f.key != cut;             // reached above the cut
-            const u64 w = max(above ? weight(value_of(f.key)) : at_cut, 1ull), n = (f.want - f.above + w - 1ull) / w;
-            if (above) {
-                const bool all = n * w >= f.at;
-                cut = all ? f.key - 1u : f.key;
-                ties = all ? 0u : (uint32_t)n;
-            } else {
-                ties = (uint32_t)min((u64)ties, n);
-            }
-        }
-        if (min_p > 0.f) {
-            const uint32_t k = key_of(s.floor + 0.f);
-            if (k > cut) { cut = k - 1u; ties = 0u; }
-        }
-
-        // entries at the cut in the shares before this warp's
-        uint32_t ties_before = 0u;
-        if (ties) {
-            uint32_t n = 0u;
-            for (int v = v0 + lane; v < v1; v += 32) {
-                float x[kVec];
-                R::get(slice[v], x);
+                for (int j = 0; j < kVec; ++j) any |= x[j] >= least;
+                if (!any) continue;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) n += key_of(x[j]) == cut ? 1u : 0u;
-            }
-            n = __reduce_add_sync(~0u, n);
-            if (lane == 0) s.warp_ties[warp] = n;
-            __syncthreads();
-            if (tid == 0) {
-                uint32_t sum = 0u;
-                for (int w = 0; w < kWarps; ++w) sum += s.warp_ties[w];
-                s.ties = sum;
+                for (int j = 0; j < kVec; ++j)
+                    if (x[j] >= least) {
+                        const uint32_t at = atomicAdd(&to->gathered, 1u);
+                        if (at < kCandidates) {
+                            to->cand.x[at] = x[j];
+                            to->cand.id[at] = (uint32_t)(first + v * kVec + j);
+                        }
+                    }
             }
             cluster.sync();
-            for (int r = 0; r < rank; ++r) ties_before += *cluster.map_shared_rank(&s.ties, r);
-            for (int w = 0; w < warp; ++w) ties_before += s.warp_ties[w];
-        }
-        // the weights of a vector's entries (0: left out); warps walk their shares in the order of the ids
-        uint32_t ties_seen = ties_before;
-        auto weigh = [&](int v, u64 (&w)[kVec]) {
-            float x[kVec];
+            const int n = (int)to->gathered;
+            cluster.sync();
+            if (n <= kCandidates) {
+                if (rank) return;                // (CTA 0 reads its own memory alone from here on)
+                constexpr int kEach = kCandidates / kThreads;
+                float x[kEach];
+                uint32_t id[kEach], before[kEach];
+                u64 w[kEach], mass[kEach];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) x[j] = -INFINITY;
-            if (v < v1) R::get(slice[v], x);
-            uint32_t mine = 0u, order = 0u;
-            if (ties) {
+                for (int e = 0; e < kEach; ++e) {
+                    const int i = tid + e * kThreads;
+                    x[e] = i < n ? s.cand.x[i] : -INFINITY;
+                    id[e] = i < n ? s.cand.id[i] : kAll;
+                    w[e] = i < n ? weight.of(x[e]) : 0ull;
+                    if (i < n) s.cand.w[i] = w[e];
+                    before[e] = 0u;
+                    mass[e] = 0ull;
+                }
+                __syncthreads();
+                // the number and the weight of those that come before, in descending order
+                const bool works = (warp << 5) < n;
+                const int rounds = n > kThreads ? kEach : 1;
+                if (works)
+                    for (int j = 0; j < n; ++j) {
+                        const float xj = s.cand.x[j];
+                        const uint32_t ij = s.cand.id[j];
+                        const u64 wj = s.cand.w[j];
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) mine += key_of(x[j]) == cut ? 1u : 0u;
-                if (__any_sync(~0u, mine)) {
-                    uint32_t scan = mine;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const uint32_t y = __shfl_up_sync(~0u, scan, o);
-                        if (lane >= o) scan += y;
+                        for (int e = 0; e < kEach; ++e)
+                            if (e < rounds && (xj > x[e] || (xj == x[e] && ij < id[e]))) { ++before[e]; mass[e] += wj; }
                     }
-                    order = ties_seen + scan - mine;
-                    ties_seen += __shfl_sync(~0u, scan, 31);
+                u64 sum = 0ull;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    if (before[e] >= (uint32_t)top_k) w[e] = 0ull;
+                    sum += w[e];
+                }
+                if (top_p < 1.f) {
+                    bool rest;
+                    u64 want = part_of(fmaxf(top_p, 0.f), block_add(sum, s), rest);
+                    want = max(1ull, want + (rest ? 1ull : 0ull));
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (mass[e] >= want) w[e] = 0ull;
+                }
+                sum = 0ull;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    if (w[e] < least_w) w[e] = 0ull;
+                    sum += w[e];
+                }
+                const u64 total = block_add(sum, s);      // (all have read the weights)
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                    if (tid + e * kThreads < n) s.cand.w[tid + e * kThreads] = w[e];
+                __syncthreads();
+                bool rest;
+                const u64 target = part_of(u, total, rest);       // (below the total)
+                if (works) {
+                    u64 at[kEach];
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) at[e] = 0ull;
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t ij = s.cand.id[j];
+                        const u64 wj = s.cand.w[j];
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e)
+                            if (e < rounds && ij < id[e]) at[e] += wj;
+                    }
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (at[e] <= target && target < at[e] + w[e]) {
+                            p.tok[row] = (int)id[e];
+                            if (p.logprob) p.logprob[row] = log_share(w[e], total);
+                        }
+                }
+                return;
+            }
+        }
+    }
+
+    // ------------------------------------------------------------------ many
+    // what is kept: entries above `last`, and those at it up to id `last_id`
+    float last = -INFINITY;
+    uint32_t last_id = 0u;
+    auto kept = [&](float x, uint32_t id) { return x > last || (x == last && id <= last_id && x > -INFINITY); };
+    const int chunk = kBins / ctas;
+    int turn = 0;
+    // a sum over the cluster of what each thread counted (places in turn: another CTA
+    // may still read the one before), and what the CTAs before this one counted
+    auto sum_all = [&](u64 mine) {
+        mine = block_add(mine, s);
+        if (tid == 0) s.sums[turn] = mine;
+        cluster.sync();
+        if (warp == 0) {
+            const u64 x = lane < ctas ? *cluster.map_shared_rank(&s.sums[turn], lane) : 0ull, all = warp_add(x), less = warp_add(lane < rank ? x : 0ull);
+            if (lane == 0) { s.share_all = all; s.share_above = less; }
+        }
+        __syncthreads();
+        turn ^= 1;
+        return s.share_all;
+    };
+    // Keeps, of what is kept, the entries in descending order (ties: the lower id first)
+    // until they reach a wanted amount: `want` of them, or `part` of their weight.
+    auto keep = [&](const bool mass, u64 want, float part) {
+        for (int i = tid; i < kBins / 4; i += kThreads) {
+            reinterpret_cast<uint4*>(s.hist.lo)[i] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(s.hist.hi)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncthreads();
+        for (int v = tid; v < vecs; v += kThreads) {
+            float x[kVec];
+            R::get(slice[v], x);
+#pragma unroll
+            for (int j = 0; j < kVec; j += 2) {
+                u64 w[2] = {0ull, 0ull}, m;
+                uint32_t k[2];
+                if (mass) weight(x[j], x[j + 1], w[0], w[1], k[0], k[1]);
+                else weight.steps(x[j], x[j + 1], k[0], k[1], m);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!kept(x[j + e], (uint32_t)(first + v * kVec + j + e))) continue;
+                    const uint32_t bin = weight.bin(k[e]);
+                    if (!mass) { atomicAdd(&s.hist.lo[bin], 1u); continue; }
+                    const uint32_t lo = (uint32_t)w[e], old = atomicAdd(&s.hist.lo[bin], lo);
+                    const uint32_t hi = (uint32_t)(w[e] >> 32) + (old + lo < old ? 1u : 0u);
+                    if (hi) atomicAdd(&s.hist.hi[bin], hi);
                 }
             }
+        }
+        if (tid == 0) s.gathered = 0u;
+        cluster.sync();
+        // the cluster's sums of this CTA's share of the bins
+        u64 mine = 0ull;
+        for (int i = tid; i < chunk; i += kThreads) {
+            u64 sum = 0ull;
+#pragma unroll 4
+            for (int r = 0; r < ctas; ++r) {
+                const Shared* o = cluster.map_shared_rank(&s, r);
+                sum += ((u64)o->hist.hi[rank * chunk + i] << 32) + o->hist.lo[rank * chunk + i];
+            }
+            s.hist.merged[i] = sum;
+            mine += sum;
+        }
+        mine = block_add(mine, s);
+        if (tid == 0) s.total = mine;
+        cluster.sync();
+        // the share of the bins that the wanted sum is reached in
+        if (warp == 0) {
+            const u64 x = lane < ctas ? *cluster.map_shared_rank(&s.total, lane) : 0ull, scan = warp_scan(x), all = __shfl_sync(~0u, scan, 31);
+            if (mass) {
+                bool rest;
+                want = part_of(part, all, rest);
+                want = max(1ull, want + (rest ? 1ull : 0ull));
+            }
+            if (lane == 0) s.share_all = want <= all ? want : 0ull;
+            if (scan - x < want && scan >= want) { s.share_above = scan - x; s.found_share = (uint32_t)lane; }
+        }
+        __syncthreads();
+        want = s.share_all;
+        if (want == 0ull) { cluster.sync(); return; }        // all are kept (counts)
+        // and the bin, `each` of them to a thread
+        {
+            const u64* bins = cluster.map_shared_rank(s.hist.merged, s.found_share);
+            const int each = (chunk + kThreads - 1) / kThreads;
+            u64 own[4], all = 0ull;
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const uint32_t k = key_of(x[j]);
-                const bool tie = mine && k == cut;
-                w[j] = k > cut || (tie && order < ties) ? weight(x[j]) : 0ull;
-                order += tie ? 1u : 0u;
+            for (int e = 0; e < 4; ++e) {
+                const int i = tid * each + e;
+                own[e] = e < each && i < chunk ? bins[i] : 0ull;
+                all += own[e];
+            }
+            const u64 scan = warp_scan(all);
+            if (lane == 31) s.warp_sum[warp] = scan;
+            __syncthreads();
+            u64 before = s.share_above + scan - all;
+            for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (before < want && before + own[e] >= want) {
+                    s.found_bin = s.found_share * chunk + (uint32_t)(tid * each + e);
+                    s.found_above = before;
+                }
+                before += own[e];
+            }
+        }
+        cluster.sync();                          // (the bins' sums were read: their place takes the list)
+        const uint32_t found = s.found_bin;
+        const u64 above = s.found_above;
+        const float from = weight.least(found, scale), to = weight.most(found, scale);
+        Shared* const list = cluster.map_shared_rank(&s, 0);
+        // body(x, id) for the entries of the bin in this CTA's slice
+        auto each_entry = [&](auto&& body) {
+            for (int v = tid; v < vecs; v += kThreads) {
+                float x[kVec];
+                R::get(slice[v], x);
+                bool any = false;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) any |= x[j] >= from && x[j] <= to;
+                if (!any) continue;
+#pragma unroll
+                for (int j = 0; j < kVec; j += 2) {
+                    uint32_t k[2];
+                    u64 m;
+                    weight.steps(x[j], x[j + 1], k[0], k[1], m);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t id = (uint32_t)(first + v * kVec + j + e);
+                        if (weight.bin(k[e]) == found && kept(x[j + e], id)) body(x[j + e], id);
+                    }
+                }
             }
         };
-        u64 mine = 0ull;
-        for (int v = v0; v < v1; v += 32) {
-            u64 w[kVec];
-            weigh(v + lane, w);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) mine += w[j];
-        }
-        const u64 total = sum_all(mine, 1);
-        bool rest;
-        const float u = p.u[row];
-        const u64 target = part_of(u > 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f, total, rest);    // (below the total)
-        u64 before = 0ull;
-        for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&s.sums[1], r);
-        for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-        if (before <= target && target < before + s.warp_sum[warp]) {
-            ties_seen = ties_before;
-            for (int v = v0; v < v1; v += 32) {
-                u64 w[kVec], own = 0ull;
-                weigh(v + lane, w);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) own += w[j];
-                const u64 scan = warp_scan(own);
-                u64 at = before + scan - own;
-                const bool here = at <= target && target < at + own;
-                before += __shfl_sync(~0u, scan, 31);
-                if (here) {
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        if (at <= target && target < at + w[j]) {
-                            p.tok[row] = first + (v + lane) * kVec + j;
-                            if (p.logprob) {
-                                // (a share near 1 by what it lacks)
-                                const double lack = (double)(total - w[j]) / (double)total;
-                                p.logprob[row] = lack < 0.5 ? log1pf(-(float)lack) : logf((float)((double)w[j] / (double)total));
-                            }
-                        }
-                        at += w[j];
-                    }
-                }
-                if (__any_sync(~0u, here)) break;
+        each_entry([&](float x, uint32_t id) {
+            const uint32_t at = atomicAdd(&list->gathered, 1u);
+            if (at < kListed) { list->list.x[at] = x; list->list.id[at] = id; }
+        });
+        cluster.sync();
+        const uint32_t n = list->gathered;
+        // The last entry: the largest key at which the sum over the keys from it up
+        // reaches what is wanted, and among the entries at it the number of ids that are needed.
+        // sum(body): the sum of body(key, id, x) over the entries, in every thread that is here.
+        auto search = [&](uint32_t key, int bits, auto&& sum) {
+            for (int b = bits - 1; b >= 0; --b) {
+                const uint32_t tried = key | 1u << b;
+                if (above + sum([&](uint32_t k, uint32_t, float x) { return k < tried ? 0ull : mass ? weight.of(x) : 1ull; }) >= want) key = tried;
             }
+            const u64 over = above + sum([&](uint32_t k, uint32_t, float x) { return k <= key ? 0ull : mass ? weight.of(x) : 1ull; });
+            const u64 at = sum([&](uint32_t k, uint32_t, float) { return k == key ? 1ull : 0ull; });
+            const u64 w = mass ? max(weight.of(value_of(key)), 1ull) : 1ull, needed = (want - over + w - 1ull) / w;
+            uint32_t id = 0x7fffffffu;
+            if (needed < at) {
+                id = 0u;                         // the id that has needed - 1 others below it
+                for (int b = 18; b >= 0; --b) {
+                    const uint32_t tried = id | 1u << b;
+                    if (sum([&](uint32_t k, uint32_t i, float) { return k == key && i < tried ? 1ull : 0ull; }) < needed) id = tried;
+                }
+            }
+            if (tid == 0) { s.last_x = value_of(key); s.last_id = id; }
+        };
+        if (n <= kListed) {
+            if (rank == 0) {
+                constexpr int kEach = kListed / kThreads;
+                uint32_t k[kEach], most = 0u, least = kAll;
+                const int rounds = ((int)n + kThreads - 1) / kThreads;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const int i = tid + e * kThreads;
+                    k[e] = i < (int)n ? key_of(s.list.x[i]) : 0u;          // (no entry's key)
+                    most = max(most, k[e]);
+                    if (i < (int)n) least = min(least, k[e]);
+                }
+                most = __reduce_max_sync(~0u, most);
+                least = __reduce_min_sync(~0u, least);
+                if (tid == 0) { s.best = 0u; s.found_bin = kAll; }
+                __syncthreads();
+                if (lane == 0) { atomicMax(&s.best, most); atomicMin(&s.found_bin, least); }
+                __syncthreads();
+                most = s.best;
+                // the digits that all keys share are known
+                const int bits = 32 - __clz(most ^ s.found_bin);
+                const uint32_t known = bits == 32 ? 0u : most >> bits << bits;
+                search(known, bits, [&](auto&& body) {
+                    u64 sum = 0ull;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (e < rounds && k[e]) sum += body(k[e], s.list.id[tid + e * kThreads], s.list.x[tid + e * kThreads]);
+                    return block_add(sum, s);
+                });
+            }
+        } else {                                 // very many equal entries: over the slices
+            search(0u, 32, [&](auto&& body) {
+                u64 sum = 0ull;
+                each_entry([&](float x, uint32_t id) { sum += body(key_of(x), id, x); });
+                return sum_all(sum);
+            });
+        }
+        cluster.sync();
+        const float new_x = list->last_x;
+        const uint32_t new_id = list->last_id;
+        cluster.sync();                          // (before the next call writes them)
+        last = new_x;
+        last_id = new_id;
+    };
+    if (top_k) keep(false, (u64)top_k, 0.f);
+    if (top_p < 1.f) keep(true, 0ull, fmaxf(top_p, 0.f));
+
+    // ------------------------------------------------------------------ draw
+    // the weights of a vector's entries (0: left out); warps walk their shares in the order of the ids
+    auto weigh = [&](int v, u64 (&w)[kVec]) {
+        float x[kVec];
+        R::get(slice[v], x);
+        if (last > -INFINITY) {
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const bool in = x[j] >= last;
+                any |= in;
+                if (!in) x[j] = -INFINITY;
+            }
+            if (!any) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) w[j] = 0ull;
+                return;
+            }
+            if (last_id < 0x7fffffffu)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (x[j] == last && (uint32_t)(first + v * kVec + j) > last_id) x[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; j += 2) {
+            uint32_t k0, k1;
+            weight(x[j], x[j + 1], w[j], w[j + 1], k0, k1);
+        }
+        if (least_w)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (w[j] < least_w) w[j] = 0ull;
+    };
+    u64 mine = 0ull;
+    for (int v = v0 + lane; v < v1; v += 32) {
+        u64 w[kVec];
+        weigh(v, w);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) mine += w[j];
+    }
+    const u64 total = sum_all(mine);
+    bool rest;
+    const u64 target = part_of(u, total, rest);           // (below the total)
+    u64 before = s.share_above;
+    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+    if (before <= target && target < before + s.warp_sum[warp]) {
+        for (int v = v0; v < v1; v += 32) {
+            u64 w[kVec], own = 0ull;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) w[j] = 0ull;
+            if (v + lane < v1) weigh(v + lane, w);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) own += w[j];
+            const u64 scan = warp_scan(own);
+            u64 at = before + scan - own;
+            const bool here = at <= target && target < at + own;
+            before += __shfl_sync(~0u, scan, 31);
+            if (here) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    if (at <= target && target < at + w[j]) {
+                        p.tok[row] = first + (v + lane) * kVec + j;
+                        if (p.logprob) p.logprob[row] = log_share(w[j], total);
+                    }
+                    at += w[j];
+                }
+            }
+            if (__any_sync(~0u, here)) break;
         }
     }
     cluster.sync();                              // shared memory stays until all have read it
