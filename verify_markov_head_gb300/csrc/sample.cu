@@ -1,8 +1,8 @@
 // sample.cu -- a token of each row of logits, with temperature, top-k, top-p and
 // min-p, from a given random number (definition: include/dspark.h).
 //
-// A cluster of CTAs takes a row and keeps it in shared memory: it is read from
-// HBM once, whatever is asked of it.  With weights w_v = e^((x_v - max) / T):
+// A cluster of CTAs takes a row, in a few passes: the first from HBM, which finds the
+// largest entry, the others from L2 or L1.  With weights w_v = e^((x_v - max) / T):
 //   few      top-k up to 512: of the threads' own maxima, the 1/32 power of 2 of the weight in
 //            which the k-th largest lies is a bound that k entries reach; the entries that
 //            reach it, hardly more than k, go to one CTA, which ranks, cuts and draws.
@@ -231,8 +231,8 @@ struct Shared {
     uint32_t powers[1 << kFine];
     union {
         struct { uint32_t lo[kBins], hi[kBins]; u64 merged[kBins]; } hist;       // counts, or weights in two words; this CTA's share of the bins, over the cluster
-        struct { float x[kCandidates]; uint32_t id[kCandidates]; u64 w[kCandidates]; } cand;
-        struct { float x[kListed]; uint32_t id[kListed]; } list;
+        struct { uint2 entry[kCandidates]; u64 w[kCandidates]; } cand;      // an entry and its id
+        struct { float x[kListed]; uint32_t id[kListed]; u64 w[kListed]; } list;
     };
     float tops[kThreads];                        // the threads' maxima
     u64 warp_sum[kWarps], block;
@@ -241,7 +241,7 @@ struct Shared {
     u64 found_above;
     uint32_t found_bin, found_share;
     float top;
-    uint32_t bad, best;
+    uint32_t best;
     uint32_t gathered;                           // candidates, or entries listed, of CTA 0
     float last_x; uint32_t last_id;              // the last entry kept, of CTA 0
     float bound;
@@ -290,65 +290,68 @@ __device__ __forceinline__ float log_share(u64 w, u64 total) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
     using R = Row<T>;
     constexpr int kVec = R::kVec;
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& s = *reinterpret_cast<Shared*>(raw);
-    uint4* slice = reinterpret_cast<uint4*>(raw + ((sizeof(Shared) + 15) & ~(size_t)15));
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = p.ctas, rank = (int)(blockIdx.x % ctas), row = (int)(blockIdx.x / ctas);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < 1 << kFine) s.powers[tid] = c_powers.v[tid];
-    if (tid == 0) s.bad = s.gathered = 0u;
+    if (tid == 0) s.gathered = 0u;
     __syncthreads();
     grid_dependency_wait();
 
-    // the row's slice, into shared memory; entries that are no numbers become -inf
+    // this CTA's slice of the row.  Every pass reads it again, from L1 or L2
     const int first = min(p.V, rank * p.slice), count = min(p.V - first, p.slice), vecs = (count + kVec - 1) / kVec;
-    const T* src = static_cast<const T*>(p.logits) + row * p.row_stride + first;
-    float top = -INFINITY;                       // NaN once an entry is, +inf once one is
-    auto clean = [&](int i) {
-        float x[kVec], most = -INFINITY;
-        R::get(slice[i], x);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            if (!(x[j] < INFINITY)) x[j] = -INFINITY;
-            most = fmaxf(most, x[j]);
-        }
-        slice[i] = R::put(x);
-        return most;
-    };
-    const int whole = count / kVec;
-    constexpr int kAhead = 8;
-    for (int i0 = tid; i0 < whole; i0 += kAhead * kThreads) {
-        uint4 w[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (i0 + u * kThreads < whole) w[u] = __ldcs(reinterpret_cast<const uint4*>(src) + i0 + u * kThreads);
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (i0 + u * kThreads < whole) {
-                top = max_nan(top, R::top(w[u]));
-                slice[i0 + u * kThreads] = w[u];
-            }
-    }
-    if (whole < vecs && tid == 0) {
+    const T* const src = static_cast<const T*>(p.logits) + row * p.row_stride + first;
+    bool dirty = false;                          // some entries are no numbers: they are taken as -inf
+    // body(v, x) for the vectors begin, begin + step, .. below end, kAhead loads ahead
+    constexpr int kAhead = 4;
+    auto load = [&](int v) {
+        if ((v + 1) * kVec <= count) return __ldg(reinterpret_cast<const uint4*>(src) + v);
         float x[kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) x[j] = whole * kVec + j < count ? R::one(src + whole * kVec + j) : -INFINITY;
-        slice[whole] = R::put(x);
-        top = max_nan(top, R::top(slice[whole]));
-    }
-    if (!(top < INFINITY)) {                     // some are no numbers: they become -inf
-        s.bad = 1u;
-        top = -INFINITY;
-        // (the vectors that this thread brought, the last one by the first thread)
-        for (int i = tid; i < vecs; i += kThreads) {
-            if (i == whole) break;
-            top = fmaxf(top, clean(i));
+        for (int j = 0; j < kVec; ++j) x[j] = v * kVec + j < count ? R::one(src + v * kVec + j) : -INFINITY;
+        return R::put(x);
+    };
+    auto each_vec = [&](int begin, int end, int step, auto&& body) {
+        for (int v = begin; v < end; v += kAhead * step) {
+            uint4 w[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (v + i * step < end) w[i] = load(v + i * step);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (v + i * step < end) {
+                    float x[kVec];
+                    R::get(w[i], x);
+                    if (dirty)
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j)
+                            if (!(x[j] < INFINITY)) x[j] = -INFINITY;
+                    body(v + i * step, x);
+                }
         }
-        if (whole < vecs && tid == 0) top = fmaxf(top, clean(whole));
+    };
+    float top = -INFINITY;                       // NaN once an entry is, +inf once one is
+    for (int v = tid; v < vecs; v += 8 * kThreads) {
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (v + i * kThreads < vecs) w[i] = load(v + i * kThreads);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (v + i * kThreads < vecs) top = max_nan(top, R::top(w[i]));
+    }
+    dirty = __syncthreads_or(!(top < INFINITY));
+    if (dirty) {
+        top = -INFINITY;
+        each_vec(tid, vecs, kThreads, [&](int, float (&x)[kVec]) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) top = fmaxf(top, x[j]);
+        });
     }
     s.tops[tid] = top;
     const uint32_t warp_top = __reduce_max_sync(~0u, key_of(top));
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         const uint32_t k = __reduce_max_sync(~0u, lane < kWarps ? s.warp_word[lane] : 0u);
         if (lane == 0) {
             s.top = value_of(k);
-            if (s.bad) raise_status(p.status, kBadInput);
+            if (dirty) raise_status(p.status, kBadInput);
         }
     }
     cluster.sync();
@@ -387,13 +390,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     }
     if (!T_ok || T_ == 0.f) {                    // the lowest id of the largest
         uint32_t best = kAll;
-        for (int v = v0 + lane; v < v1; v += 32) {
-            float x[kVec];
-            R::get(slice[v], x);
+        each_vec(tid, vecs, kThreads, [&](int v, float (&x)[kVec]) {
 #pragma unroll
             for (int j = kVec - 1; j >= 0; --j)
                 if (x[j] == top) best = min(best, (uint32_t)(first + v * kVec + j));
-        }
+        });
         best = __reduce_min_sync(~0u, best);
         if (lane == 0) s.warp_word[warp] = best;
         __syncthreads();
@@ -440,119 +441,140 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             }
             if (tid == 0) s.bound = -INFINITY;
             __syncthreads();
-            const uint4 own = reinterpret_cast<const uint4*>(s.hist.lo)[tid];
-            const uint32_t all = own.x + own.y + own.z + own.w;
+            constexpr int kBinsEach = kBins / kThreads;
+            uint32_t own[kBinsEach], all = 0u;
+#pragma unroll
+            for (int e = 0; e < kBinsEach; ++e) all += own[e] = s.hist.lo[kBinsEach * tid + e];
             const u64 scan = warp_scan(all);
             if (lane == 31) s.warp_word[warp] = (uint32_t)scan;
             __syncthreads();
             uint32_t before = (uint32_t)scan - all;
             for (int w = 0; w < warp; ++w) before += s.warp_word[w];
-            if (before < (uint32_t)top_k && before + all >= (uint32_t)top_k) {
-                uint32_t b = 4 * tid;
-                if ((before += own.x) < (uint32_t)top_k) {
-                    ++b;
-                    if ((before += own.y) < (uint32_t)top_k) b += before + own.z < (uint32_t)top_k ? 2u : 1u;
-                }
-                s.bound = weight.least(b, scale);
+#pragma unroll
+            for (int e = 0; e < kBinsEach; ++e) {
+                if (before < (uint32_t)top_k && before + own[e] >= (uint32_t)top_k) s.bound = weight.least(kBinsEach * tid + e, scale);
+                before += own[e];
             }
         }
         cluster.sync();
         Shared* const to = cluster.map_shared_rank(&s, 0);
         const float least = to->bound;
         if (least > -INFINITY) {                 // (else fewer than top_k maxima weigh something)
-            for (int v = tid; v < vecs; v += kThreads) {
-                float x[kVec];
-                R::get(slice[v], x);
+            each_vec(tid, vecs, kThreads, [&](int v, float (&x)[kVec]) {
                 bool any = false;
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) any |= x[j] >= least;
-                if (!any) continue;
+                if (!any) return;
 #pragma unroll
                 for (int j = 0; j < kVec; ++j)
                     if (x[j] >= least) {
                         const uint32_t at = atomicAdd(&to->gathered, 1u);
-                        if (at < kCandidates) {
-                            to->cand.x[at] = x[j];
-                            to->cand.id[at] = (uint32_t)(first + v * kVec + j);
-                        }
+                        if (at < kCandidates) to->cand.entry[at] = make_uint2(__float_as_uint(x[j]), (uint32_t)(first + v * kVec + j));
                     }
-            }
+            });
             cluster.sync();
             const int n = (int)to->gathered;
             cluster.sync();
             if (n <= kCandidates) {
                 if (rank) return;                // (CTA 0 reads its own memory alone from here on)
                 constexpr int kEach = kCandidates / kThreads;
+                // `lanes` neighbouring threads to a candidate, or kEach candidates to a thread
+                int lanes = 1;
+                while (lanes < 32 && 2 * lanes * n <= kThreads) lanes *= 2;
+                const int part = tid % lanes, rounds = n > kThreads ? kEach : 1;
                 float x[kEach];
-                uint32_t id[kEach], before[kEach];
-                u64 w[kEach], mass[kEach];
+                uint32_t id[kEach], before[kEach], lower[kEach];
+                u64 w[kEach];
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) {
-                    const int i = tid + e * kThreads;
-                    x[e] = i < n ? s.cand.x[i] : -INFINITY;
-                    id[e] = i < n ? s.cand.id[i] : kAll;
+                    const int i = tid / lanes + e * kThreads;
+                    const uint2 c = i < n ? s.cand.entry[i] : make_uint2(0xff800000u, kAll);
+                    x[e] = __uint_as_float(c.x);
+                    id[e] = c.y;
                     w[e] = i < n ? weight.of(x[e]) : 0ull;
-                    if (i < n) s.cand.w[i] = w[e];
-                    before[e] = 0u;
-                    mass[e] = 0ull;
+                    before[e] = lower[e] = 0u;
                 }
-                __syncthreads();
-                // the number and the weight of those that come before, in descending order
-                const bool works = (warp << 5) < n;
-                const int rounds = n > kThreads ? kEach : 1;
-                if (works)
-                    for (int j = 0; j < n; ++j) {
-                        const float xj = s.cand.x[j];
-                        const uint32_t ij = s.cand.id[j];
-                        const u64 wj = s.cand.w[j];
+                // the numbers of those that come before: in descending order, and in the order of the ids
+#pragma unroll 2
+                for (int j = part; j < n; j += lanes) {
+                    const uint2 c = s.cand.entry[j];
+                    const float xj = __uint_as_float(c.x);
 #pragma unroll
-                        for (int e = 0; e < kEach; ++e)
-                            if (e < rounds && (xj > x[e] || (xj == x[e] && ij < id[e]))) { ++before[e]; mass[e] += wj; }
+                    for (int e = 0; e < kEach; ++e)
+                        if (e < rounds) {
+                            const bool less = c.y < id[e];
+                            lower[e] += less ? 1u : 0u;
+                            before[e] += xj > x[e] || (xj == x[e] && less) ? 1u : 0u;
+                        }
+                }
+                auto over_lanes = [&](uint32_t y) {
+                    for (int o = 1; o < lanes; o <<= 1) y += __shfl_xor_sync(~0u, y, o);
+                    return y;
+                };
+                // sums over the places before each (kEach neighbouring ones to a thread), and over all
+                auto scan_places = [&]() {
+                    u64 own[kEach], all = 0ull;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) all += own[e] = s.cand.w[kEach * tid + e];
+                    const u64 scan = warp_scan(all);
+                    if (lane == 31) s.warp_sum[warp] = scan;
+                    __syncthreads();
+                    u64 sum = scan - all, total = 0ull;
+#pragma unroll
+                    for (int i = 0; i < kWarps; ++i) {
+                        sum += i < warp ? s.warp_sum[i] : 0ull;
+                        total += s.warp_sum[i];
                     }
-                u64 sum = 0ull;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        s.cand.w[kEach * tid + e] = sum;
+                        sum += own[e];
+                    }
+                    __syncthreads();
+                    return total;
+                };
+                auto clear_places = [&]() {
+                    for (int i = tid; i < kCandidates; i += kThreads) s.cand.w[i] = 0ull;
+                    __syncthreads();
+                };
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) {
+                    before[e] = over_lanes(before[e]);
+                    lower[e] = over_lanes(lower[e]);
                     if (before[e] >= (uint32_t)top_k) w[e] = 0ull;
-                    sum += w[e];
                 }
                 if (top_p < 1.f) {
+                    clear_places();
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (part == 0 && w[e]) s.cand.w[before[e]] = w[e];
+                    __syncthreads();
                     bool rest;
-                    u64 want = part_of(fmaxf(top_p, 0.f), block_add(sum, s), rest);
+                    u64 want = part_of(fmaxf(top_p, 0.f), scan_places(), rest);
                     want = max(1ull, want + (rest ? 1ull : 0ull));
 #pragma unroll
                     for (int e = 0; e < kEach; ++e)
-                        if (mass[e] >= want) w[e] = 0ull;
+                        if (w[e] && s.cand.w[before[e]] >= want) w[e] = 0ull;
+                    __syncthreads();
                 }
-                sum = 0ull;
+                clear_places();
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) {
                     if (w[e] < least_w) w[e] = 0ull;
-                    sum += w[e];
+                    if (part == 0 && w[e]) s.cand.w[lower[e]] = w[e];
                 }
-                const u64 total = block_add(sum, s);      // (all have read the weights)
-#pragma unroll
-                for (int e = 0; e < kEach; ++e)
-                    if (tid + e * kThreads < n) s.cand.w[tid + e * kThreads] = w[e];
                 __syncthreads();
+                const u64 total = scan_places();
                 bool rest;
                 const u64 target = part_of(u, total, rest);       // (below the total)
-                if (works) {
-                    u64 at[kEach];
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e) at[e] = 0ull;
-                    for (int j = 0; j < n; ++j) {
-                        const uint32_t ij = s.cand.id[j];
-                        const u64 wj = s.cand.w[j];
-#pragma unroll
-                        for (int e = 0; e < kEach; ++e)
-                            if (e < rounds && ij < id[e]) at[e] += wj;
+                for (int e = 0; e < kEach; ++e) {
+                    if (part || w[e] == 0ull) continue;
+                    const u64 at = s.cand.w[lower[e]];
+                    if (at <= target && target < at + w[e]) {
+                        p.tok[row] = (int)id[e];
+                        if (p.logprob) p.logprob[row] = log_share(w[e], total);
                     }
-#pragma unroll
-                    for (int e = 0; e < kEach; ++e)
-                        if (at[e] <= target && target < at[e] + w[e]) {
-                            p.tok[row] = (int)id[e];
-                            if (p.logprob) p.logprob[row] = log_share(w[e], total);
-                        }
                 }
                 return;
             }
@@ -588,26 +610,32 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             reinterpret_cast<uint4*>(s.hist.hi)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         __syncthreads();
-        for (int v = tid; v < vecs; v += kThreads) {
-            float x[kVec];
-            R::get(slice[v], x);
+        each_vec(tid, vecs, kThreads, [&](int v, float (&x)[kVec]) {
+            if (last > -INFINITY)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (!kept(x[j], (uint32_t)(first + v * kVec + j))) x[j] = -INFINITY;
 #pragma unroll
             for (int j = 0; j < kVec; j += 2) {
-                u64 w[2] = {0ull, 0ull}, m;
+                u64 w[2], m;
                 uint32_t k[2];
-                if (mass) weight(x[j], x[j + 1], w[0], w[1], k[0], k[1]);
-                else weight.steps(x[j], x[j + 1], k[0], k[1], m);
+                if (mass) {
+                    weight(x[j], x[j + 1], w[0], w[1], k[0], k[1]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (!kept(x[j + e], (uint32_t)(first + v * kVec + j + e))) continue;
-                    const uint32_t bin = weight.bin(k[e]);
-                    if (!mass) { atomicAdd(&s.hist.lo[bin], 1u); continue; }
-                    const uint32_t lo = (uint32_t)w[e], old = atomicAdd(&s.hist.lo[bin], lo);
-                    const uint32_t hi = (uint32_t)(w[e] >> 32) + (old + lo < old ? 1u : 0u);
-                    if (hi) atomicAdd(&s.hist.hi[bin], hi);
+                    for (int e = 0; e < 2; ++e) {
+                        if (w[e] == 0ull) continue;
+                        const uint32_t bin = weight.bin(k[e]), lo = (uint32_t)w[e], old = atomicAdd(&s.hist.lo[bin], lo);
+                        const uint32_t hi = (uint32_t)(w[e] >> 32) + (old > ~lo ? 1u : 0u);
+                        if (hi) atomicAdd(&s.hist.hi[bin], hi);
+                    }
+                } else {
+                    weight.steps(x[j], x[j + 1], k[0], k[1], m);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (x[j + e] > -INFINITY) atomicAdd(&s.hist.lo[weight.bin(k[e])], 1u);
                 }
             }
-        }
+        });
         if (tid == 0) s.gathered = 0u;
         cluster.sync();
         // the cluster's sums of this CTA's share of the bins
@@ -643,9 +671,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         {
             const u64* bins = cluster.map_shared_rank(s.hist.merged, s.found_share);
             const int each = (chunk + kThreads - 1) / kThreads;
-            u64 own[4], all = 0ull;
+            u64 own[kBins / kThreads], all = 0ull;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kBins / kThreads; ++e) {
                 const int i = tid * each + e;
                 own[e] = e < each && i < chunk ? bins[i] : 0ull;
                 all += own[e];
@@ -656,7 +684,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             u64 before = s.share_above + scan - all;
             for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kBins / kThreads; ++e) {
                 if (before < want && before + own[e] >= want) {
                     s.found_bin = s.found_share * chunk + (uint32_t)(tid * each + e);
                     s.found_above = before;
@@ -671,13 +699,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         Shared* const list = cluster.map_shared_rank(&s, 0);
         // body(x, id) for the entries of the bin in this CTA's slice
         auto each_entry = [&](auto&& body) {
-            for (int v = tid; v < vecs; v += kThreads) {
-                float x[kVec];
-                R::get(slice[v], x);
+            each_vec(tid, vecs, kThreads, [&](int v, float (&x)[kVec]) {
                 bool any = false;
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) any |= x[j] >= from && x[j] <= to;
-                if (!any) continue;
+                if (!any) return;
 #pragma unroll
                 for (int j = 0; j < kVec; j += 2) {
                     uint32_t k[2];
@@ -689,7 +715,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
                         if (weight.bin(k[e]) == found && kept(x[j + e], id)) body(x[j + e], id);
                     }
                 }
-            }
+            });
         };
         each_entry([&](float x, uint32_t id) {
             const uint32_t at = atomicAdd(&list->gathered, 1u);
@@ -699,21 +725,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         const uint32_t n = list->gathered;
         // The last entry: the largest key at which the sum over the keys from it up
         // reaches what is wanted, and among the entries at it the number of ids that are needed.
-        // sum(body): the sum of body(key, id, x) over the entries, in every thread that is here.
+        // sum(body): the sum of body(key, id, weight or 1) over the entries, in every thread that is here.
         auto search = [&](uint32_t key, int bits, auto&& sum) {
             for (int b = bits - 1; b >= 0; --b) {
                 const uint32_t tried = key | 1u << b;
-                if (above + sum([&](uint32_t k, uint32_t, float x) { return k < tried ? 0ull : mass ? weight.of(x) : 1ull; }) >= want) key = tried;
+                if (above + sum([&](uint32_t k, uint32_t, u64 w) { return k < tried ? 0ull : w; }) >= want) key = tried;
             }
-            const u64 over = above + sum([&](uint32_t k, uint32_t, float x) { return k <= key ? 0ull : mass ? weight.of(x) : 1ull; });
-            const u64 at = sum([&](uint32_t k, uint32_t, float) { return k == key ? 1ull : 0ull; });
+            const u64 over = above + sum([&](uint32_t k, uint32_t, u64 w) { return k <= key ? 0ull : w; });
+            const u64 at = sum([&](uint32_t k, uint32_t, u64) { return k == key ? 1ull : 0ull; });
             const u64 w = mass ? max(weight.of(value_of(key)), 1ull) : 1ull, needed = (want - over + w - 1ull) / w;
             uint32_t id = 0x7fffffffu;
             if (needed < at) {
                 id = 0u;                         // the id that has needed - 1 others below it
                 for (int b = 18; b >= 0; --b) {
                     const uint32_t tried = id | 1u << b;
-                    if (sum([&](uint32_t k, uint32_t i, float) { return k == key && i < tried ? 1ull : 0ull; }) < needed) id = tried;
+                    if (sum([&](uint32_t k, uint32_t i, u64) { return k == key && i < tried ? 1ull : 0ull; }) < needed) id = tried;
                 }
             }
             if (tid == 0) { s.last_x = value_of(key); s.last_id = id; }
@@ -728,7 +754,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
                     const int i = tid + e * kThreads;
                     k[e] = i < (int)n ? key_of(s.list.x[i]) : 0u;          // (no entry's key)
                     most = max(most, k[e]);
-                    if (i < (int)n) least = min(least, k[e]);
+                    if (i < (int)n) {
+                        least = min(least, k[e]);
+                        s.list.w[i] = mass ? weight.of(s.list.x[i]) : 1ull;
+                    }
                 }
                 most = __reduce_max_sync(~0u, most);
                 least = __reduce_min_sync(~0u, least);
@@ -744,14 +773,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
                     u64 sum = 0ull;
 #pragma unroll
                     for (int e = 0; e < kEach; ++e)
-                        if (e < rounds && k[e]) sum += body(k[e], s.list.id[tid + e * kThreads], s.list.x[tid + e * kThreads]);
+                        if (e < rounds && k[e]) sum += body(k[e], s.list.id[tid + e * kThreads], s.list.w[tid + e * kThreads]);
                     return block_add(sum, s);
                 });
             }
         } else {                                 // very many equal entries: over the slices
             search(0u, 32, [&](auto&& body) {
                 u64 sum = 0ull;
-                each_entry([&](float x, uint32_t id) { sum += body(key_of(x), id, x); });
+                each_entry([&](float x, uint32_t id) { sum += body(key_of(x), id, mass ? weight.of(x) : 1ull); });
                 return sum_all(sum);
             });
         }
@@ -767,9 +796,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
 
     // ------------------------------------------------------------------ draw
     // the weights of a vector's entries (0: left out); warps walk their shares in the order of the ids
-    auto weigh = [&](int v, u64 (&w)[kVec]) {
-        float x[kVec];
-        R::get(slice[v], x);
+    auto weigh = [&](int v, float (&x)[kVec], u64 (&w)[kVec]) {
         if (last > -INFINITY) {
             bool any = false;
 #pragma unroll
@@ -799,12 +826,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
                 if (w[j] < least_w) w[j] = 0ull;
     };
     u64 mine = 0ull;
-    for (int v = v0 + lane; v < v1; v += 32) {
+    each_vec(v0 + lane, v1, 32, [&](int v, float (&x)[kVec]) {
         u64 w[kVec];
-        weigh(v, w);
+        weigh(v, x, w);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) mine += w[j];
-    }
+    });
     const u64 total = sum_all(mine);
     bool rest;
     const u64 target = part_of(u, total, rest);           // (below the total)
@@ -815,7 +842,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             u64 w[kVec], own = 0ull;
 #pragma unroll
             for (int j = 0; j < kVec; ++j) w[j] = 0ull;
-            if (v + lane < v1) weigh(v + lane, w);
+            each_vec(v + lane, min(v1, v + 32), 32, [&](int at, float (&x)[kVec]) { weigh(at, x, w); });
 #pragma unroll
             for (int j = 0; j < kVec; ++j) own += w[j];
             const u64 scan = warp_scan(own);
@@ -841,21 +868,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
 template <typename T>
 cudaError_t launch(SampleParams p, cudaStream_t s) {
     constexpr int kVec = Row<T>::kVec;
-    const size_t fixed = (sizeof(Shared) + 15) & ~(size_t)15;
-    auto bytes = [&](int ctas) { return fixed + (size_t)(((p.V + ctas - 1) / ctas + kVec - 1) / kVec) * 16; };
-    // as many CTAs to a row as leave two rows' slices on an SM, more where SMs would be idle
-    int ctas = 1;
-    while (ctas < 16 && (bytes(ctas) > 112 * 1024 || ((long long)p.N * ctas * 2 <= num_sms() && p.V > ctas * 2048))) ctas *= 2;
+    // two CTAs to a row, and on an SM: the phases of two rows overlap, and the rows at
+    // work fit the L2 for their later passes (512 rows of 151936: 271 us; one CTA of
+    // 1024 threads 276, of 512 322; four of 512 283, eight that keep the row in shared
+    // memory 323).  Up to 16 where SMs would be idle.
+    int ctas = p.V > 16384 ? 2 : 1;
+    while (ctas < 16 && (long long)p.N * ctas * 2 <= num_sms() && p.V > ctas * 4096) ctas *= 2;
     p.ctas = ctas;
     p.slice = ((p.V + ctas - 1) / ctas + kVec - 1) / kVec * kVec;
-    const size_t smem = bytes(ctas);
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
     if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.N * ctas));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
