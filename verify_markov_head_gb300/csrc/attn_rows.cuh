@@ -40,17 +40,18 @@ __device__ __forceinline__ void store_out<uint16_t>(uint16_t* out, float x) {
 
 // Requests that own no cache position have no tile: their rows are zero.  The
 // offsets of every request are compared with its length here.
+// (the first `threads` threads of the CTA)
 template <typename T>
-__device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int ctas) {
+__device__ __forceinline__ void empty_rows(const AttnParams& p, int cta, int ctas, int threads) {
     for (int b = cta; b < p.B; b += ctas) {
         const int off = p.tile_off[b], next = p.tile_off[b + 1];
         if (threadIdx.x == 0 && !attn_offsets_fit(p, b, off, next)) raise_status(p.status, kBadLength);
         if (next > off) continue;
         const RowMap r(p, b, threadIdx.x == 0);
         const size_t o0 = (size_t)r.q0 * p.Hq * p.D, n = (size_t)r.n * p.Hq * p.D;
-        for (size_t i = threadIdx.x; i < n; i += blockDim.x) static_cast<T*>(p.out)[o0 + i] = T(0);
+        for (size_t i = threadIdx.x; i < n; i += threads) static_cast<T*>(p.out)[o0 + i] = T(0);
         if (p.lse)
-            for (int i = threadIdx.x; i < r.n * p.Hq; i += blockDim.x) p.lse[(size_t)r.q0 * p.Hq + i] = -INFINITY;
+            for (int i = threadIdx.x; i < r.n * p.Hq; i += threads) p.lse[(size_t)r.q0 * p.Hq + i] = -INFINITY;
     }
 }
 

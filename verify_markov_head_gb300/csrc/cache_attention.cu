@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
     if (tid == 0) grid_launch_dependents();   // the join is scheduled now and waits for this grid
     grid_dependency_wait();
     const int cta = blockIdx.x;
-    empty_rows<float>(p, cta, gridDim.x);
+    empty_rows<float>(p, cta, gridDim.x, blockDim.x);
     const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
     if (tid == 0) p.split[cta].parts = 0;
     if (cta >= sp.n) return;
@@ -444,9 +444,10 @@ cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s) {
     return e == cudaSuccess ? launch_join(p, s) : e;
 }
 
-cudaError_t launch_cache_attention4(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_cache_attention4(const AttnParams& p, bool tensor, cudaStream_t s) {
     cudaError_t e;
-    if (p.bf16) e = launch_attn4_mma(p, s);
+    if (tensor) e = launch_attn4_tensor(p, s);
+    else if (p.bf16) e = launch_attn4_mma(p, s);
     else e = p.row_tile == 8 ? launch_simt<8, true>(p, s) : launch_simt<32, true>(p, s);
     return e == cudaSuccess ? launch_join(p, s) : e;
 }

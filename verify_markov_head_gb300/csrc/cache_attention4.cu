@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
     const int D = kExact ? DP : p.D;
     if (tid == 0) grid_launch_dependents();  // the join is scheduled now and waits for this grid
     grid_dependency_wait();
-    empty_rows<uint16_t>(p, blockIdx.x, gridDim.x);
+    empty_rows<uint16_t>(p, blockIdx.x, gridDim.x, blockDim.x);
     // workers with neighbouring shares on different SMs: a short list reaches them all
     const int worker = warp * gridDim.x + blockIdx.x;
     const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);

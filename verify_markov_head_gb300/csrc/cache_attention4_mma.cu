@@ -1,0 +1,796 @@
+// cache_attention4_mma.cu -- attention over a paged cache held in 4 bits on the
+// tensor cores: bf16 queries, head size 128, more than 16 query rows a key-value
+// head (formulas: cache_attention.cu; formats: fp4.cuh; fewer rows and other head
+// sizes: cache_attention4.cu).
+//
+// Both products are taken transposed, 128 cache positions at a time:
+//     S^T [128 positions x N] = K [128 x 128] . Q^T       (A: K, B: Q)
+//     O^T [128 entries x N]  += V^T [128 x 128] . P^T     (A: V^T, B: P)
+// with A in tensor memory.  The codes (18 KB for 128 positions) come to shared memory
+// by cp.async; eight warps turn them into fp16 in registers, exactly, and write
+// them straight into tensor memory, as the rows of A: 64 KB that do not cross shared
+// memory, where the products would read them at 64 bytes a cycle (cache_attention_mma.cu).
+//   keys     a lane of A is a position: a thread takes its 64 bytes of codes and 8
+//            scales; rows of 80 bytes in shared memory keep its reads apart
+//   values   a lane of A is an entry of the head: a thread takes 4 entries of four
+//            positions at a time, pairs the positions' nibbles (4 operations for 16
+//            entries) and writes fragments of 16 lanes.  Position r of 16 is the
+//            product's step 2r mod 8 + ..: P's rows are written in that order.
+// The softmax, the segments and the split over CTAs are cache_attention_mma.cu's; weights
+// are fp16, 2^(s - ref + 7), as in cache_attention4.cu, whose notes on precision hold
+// here too, except that the rows of a tile share the power of two that q is scaled by.
+//
+// Roles (20 warps, 28 with 64 columns, one CTA per SM):
+//   first 8 or 16    softmax: groups of 4 warps, 16 columns each; thread = position
+//   then eight       keys, values: codes to tensor memory (warp & 3 = its 32 lanes)
+//   then two         copies of the keys' and of the values' codes and scales
+//   one              MMA issuer, one more the segments and Q tiles
+#include "attn_rows.cuh"
+#include "fp4.cuh"
+#include "pdl.cuh"
+#include "serve.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSteps = 128;              // positions per step
+constexpr int kDim = 128;                // head size
+constexpr int kSegs = 8;                 // segment descriptors in flight
+constexpr int kBadRing = 16;             // steps the copies may be ahead of the softmax, and more
+constexpr float kLift = 7.f;             // log2 of a weight at the reference
+constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
+constexpr long long kDrainCycles = 200000000LL;
+constexpr int kRow = 80;                 // bytes from row to row of codes in shared memory
+constexpr int kCodes = kSteps * kRow;    // of a stage, then the scales
+constexpr int kStageBytes = kCodes + kSteps * (kDim / fp4::kGroup);
+constexpr int kStages = 5;               // of keys, and of values
+constexpr int kTiles = 4;                // A tiles in tensor memory: keys 0 and 2, values 1 and 3
+constexpr int kTileCols = kDim / 2;      // columns of one
+
+template <int N>
+struct Roles {
+    static constexpr int kParts = N / 16, kSoftWarps = 4 * kParts;
+    static constexpr int kKeyWarp = kSoftWarps, kValWarp = kSoftWarps + 4, kCopyWarp = kSoftWarps + 8;
+    static constexpr int kMmaWarp = kSoftWarps + 10, kSegWarp = kSoftWarps + 11, kWarps = kSoftWarps + 12;
+};
+
+struct Seg {
+    int b, h, q0, n, len;     // request, key-value head, first token in q, tokens, cache length
+    int r0, rows;             // query rows of this tile
+    int pos0, pos1;           // cache positions [pos0, pos1)
+    int steps;                // -1: no more segments
+    int slot;                 // -1: the whole segment, else the partial result's slot
+};
+
+template <int N>
+struct Smem {
+    static constexpr int kQBytes = N * kDim * 2, kQBufs = 2;
+    static constexpr int kCols = 4 * N + kTiles * kTileCols;      // tensor memory: two S, two O, the A tiles
+    static constexpr int kTmem = 512;
+    static constexpr int kQ = 0;
+    static constexpr int kP = kQ + kQBufs * kQBytes;              // [128][64] fp16, 128-byte rows
+    static constexpr int kRing = kP + kSteps * 128;               // [keys, values][stage]
+    static constexpr int kMax = kRing + 2 * kStages * kStageBytes;    // [2][N][4], by the step's parity
+    static constexpr int kSum = kMax + 2 * N * 16;                // [2][N][4], by the segment's parity
+    static constexpr int kSeg = kSum + 2 * N * 16;
+    static constexpr int kBar = (kSeg + kSegs * (int)sizeof(Seg) + 7) / 8 * 8;
+    static constexpr int kBars = 4 * kStages + 2 * kTiles + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 3;
+    static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, NaN flag, -
+    static constexpr int kExp = kFlags + 16;                      // [kSegs] exponents of the Q tiles
+    static constexpr int kLater = kExp + 4 * kSegs;               // [kStages] first of a step's positions that not every row sees
+    static constexpr int kBad = kLater + 4 * kStages;             // [kBadRing][4] positions whose page is out of range
+    static constexpr int kTotal = kBad + 16 * kBadRing;
+};
+
+__device__ __forceinline__ float warp_max(float x) {     // over the warp, NaN left out
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Arrive on an mbarrier once this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Nonzero in one lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// N columns of 32 lanes, waited for.
+template <int C> __device__ __forceinline__ void tmem_get(uint32_t a, float (&v)[C]);
+template <> __device__ __forceinline__ void tmem_get<16>(uint32_t a, float (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 "\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+                   "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(a) : "memory");
+}
+template <int C> __device__ __forceinline__ void tmem_put(uint32_t a, const float (&v)[C]);
+template <> __device__ __forceinline__ void tmem_put<16>(uint32_t a, const float (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 "\n\ttcgen05.wait::st.sync.aligned;"
+                 ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+                   "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
+}
+
+// x * s + n, and l + w, of two columns in one instruction each.
+__device__ __forceinline__ void fma_pair(float& x0, float& x1, float s, float n0, float n1) {
+    asm("{\n\t.reg .b64 x, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 n, {%3, %4};\n\t"
+        "fma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(x0), "+f"(x1) : "f"(s), "f"(n0), "f"(n1));
+}
+__device__ __forceinline__ void add_pair(float& l0, float& l1, float w0, float w1) {
+    asm("{\n\t.reg .b64 l, w;\n\tmov.b64 l, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 l, l, w;\n\tmov.b64 {%0, %1}, l;\n\t}"
+        : "+f"(l0), "+f"(l1) : "f"(w0), "f"(w1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void store_chunk(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void cp_async_8(uint32_t to, const void* from, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+// 16 lanes x 32 columns of tensor memory, as fragments: thread t holds of every 4 columns
+// column t % 4 of lanes t / 4 and t / 4 + 8.
+__device__ __forceinline__ void tmem_put_16x128b(uint32_t a, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                   "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+}
+// kind::f16 with both operands fp16 (format 0), A K-major.
+constexpr uint32_t idesc_half(int N, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int N>
+__global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(const AttnParams p) {
+    using L = Smem<N>;
+    using R = Roles<N>;
+    constexpr int kSoftWarps = R::kSoftWarps, HC = 16;             // columns of a softmax group
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile uint32_t* s_flags = reinterpret_cast<volatile uint32_t*>(gbase + L::kFlags);   // [0] TMEM, [1] abort, [2] NaN
+    volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(gbase + L::kBad);
+    volatile int* s_exp = reinterpret_cast<volatile int*>(gbase + L::kExp);
+    volatile int* s_later = reinterpret_cast<volatile int*>(gbase + L::kLater);
+    volatile Seg* s_seg = reinterpret_cast<volatile Seg*>(gbase + L::kSeg);
+    volatile uint32_t* abort_flag = s_flags + 1;
+    uint32_t bar = base + L::kBar;
+    auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
+    const uint32_t b_cfull = take(2 * kStages), b_cempty = take(2 * kStages);       // codes: keys' stages, then values'
+    const uint32_t b_full = take(kTiles), b_empty = take(kTiles);                   // A tiles
+    const uint32_t b_seg_full = take(kSegs), b_seg_empty = take(kSegs);
+    const uint32_t b_q_full = take(L::kQBufs), b_q_empty = take(L::kQBufs), b_s_full = take(2), b_s_empty = take(2);
+    const uint32_t b_o_empty = take(2), b_p_full = take(1), b_pv = take(1), b_end = take(1);
+
+    if (tid == 0) {
+        grid_launch_dependents();       // the join is scheduled now and waits for this grid
+        for (int i = 0; i < 2 * kStages; ++i) { ptx::mbar_init(b_cfull + 8 * i, 33); ptx::mbar_init(b_cempty + 8 * i, 4); }
+        for (int i = 0; i < kTiles; ++i) { ptx::mbar_init(b_full + 8 * i, 4); ptx::mbar_init(b_empty + 8 * i, 1); }
+        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 1 + 2 + 8 + kSoftWarps); }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(b_s_full + 8 * i, 1); ptx::mbar_init(b_s_empty + 8 * i, kSoftWarps);
+            ptx::mbar_init(b_o_empty + 8 * i, kSoftWarps);
+        }
+        for (int i = 0; i < L::kQBufs; ++i) { ptx::mbar_init(b_q_full + 8 * i, 1); ptx::mbar_init(b_q_empty + 8 * i, 1); }
+        ptx::mbar_init(b_p_full, kSoftWarps); ptx::mbar_init(b_pv, 1); ptx::mbar_init(b_end, 1);
+        s_flags[1] = 0u;
+        s_flags[2] = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == R::kMmaWarp) {
+        ptx::tmem_alloc(base + L::kFlags, L::kTmem);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s_flags[0], tiles = tmem + 4 * N;
+    grid_dependency_wait();             // the set-up above overlaps the launch before this one
+    const long long wl = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
+    auto wait = [&](uint32_t b, uint32_t parity) { return ptx::mbar_wait_strict(b, parity & 1u, abort_flag, wl); };
+    auto wait_all = [&](uint32_t b, uint32_t parity) { return (bool)__all_sync(~0u, wait(b, parity)); };
+    auto give_up = [&](int site) {
+        raise_timeout(p.status, site);
+        *abort_flag = 1u;
+    };
+
+    if (warp == R::kSegWarp) {
+        // ------------------------------------------------ segments and Q tiles
+        const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
+        const int cta = blockIdx.x;
+        int place = 0, end = 0;
+        if (cta < sp.n) { place = sp.first(cta); end = sp.first(cta + 1); }
+        AttnSplitRow split{};                    // the segment that begins here and goes on in the next CTA
+        bool ok = true;
+        for (int si = 0; ok; ++si) {
+            Seg d;
+            d.steps = -1;
+            while (place < end) {
+                const AttnSegment g = attn_segment(p, sp, place, attn_first_round(p));
+                const RowMap rm(p, g.b, lane == 0);
+                d.r0 = g.rt * p.row_tile;
+                d.rows = max(0, min(p.row_tile, rm.n * p.G - d.r0));
+                const int j0 = g.tile(sp, place), j1 = g.tile(sp, end), next = g.t0 + sp.pad + g.tiles;
+                if (next <= place) { place = end; break; }         // (offsets that do not ascend)
+                place = next;
+                if (j0 == j1 || d.rows == 0 || g.tiles != attn_tiles(rm.len)) continue;
+                d.b = g.b; d.h = g.h; d.q0 = rm.q0; d.n = rm.n; d.len = rm.len;
+                d.pos0 = j0 * kTile;
+                d.pos1 = min(j1 * kTile, rm.len);
+                d.steps = (d.pos1 - d.pos0 + kSteps - 1) / kSteps;
+                const bool whole = j0 == 0 && j1 == g.tiles;
+                d.slot = whole ? -1 : 2 * cta + (j0 == 0 ? 1 : 0);
+                if (j0 == 0 && !whole) split = attn_split_row(sp, g, cta, rm.q0, d.r0, d.rows);
+                break;
+            }
+            const int slot = si % kSegs;
+            if (si >= kSegs) ok = wait_all(b_seg_empty + 8 * slot, (si / kSegs) - 1);
+            if (!ok) { if (lane == 0) give_up(0); break; }
+            if (lane == 0) {
+                const_cast<Seg&>(s_seg[slot]) = d;
+                ptx::mbar_arrive(b_seg_full + 8 * slot);
+            }
+            __syncwarp();
+            if (d.steps < 0) break;
+            // the Q tile, scaled by a power of two to below 1, rows beyond the request's as zeros
+            const int qb = si % L::kQBufs;
+            if (si >= L::kQBufs) ok = wait_all(b_q_empty + 8 * qb, (si / L::kQBufs) - 1);
+            if (!ok) { if (lane == 0) give_up(1); break; }
+            const int c = lane & 15, sub = lane >> 4;              // a 16-byte chunk of rows sub, sub + 2, ..
+            auto chunk_of = [&](int r) {
+                const int rr = d.r0 + r, tok = p.by_group(rr);
+                const uint16_t* src = static_cast<const uint16_t*>(p.q) + (d.q0 + tok) * p.q_stride + (size_t)(d.h * p.G + rr - tok * p.G) * kDim;
+                return r < d.rows ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+            };
+            uint32_t top = 0u;
+#pragma unroll 8
+            for (int r = sub; r < N; r += 2) {
+                const uint4 x = chunk_of(r);
+                top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+            }
+            top = __reduce_max_sync(~0u, max(top << 16, top & 0xffff0000u));
+            const int e = min(max((int)(top >> 23) - 126, -100), 100);
+            const float down = __int_as_float((127 - e) << 23);
+            const uint32_t to = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
+#pragma unroll 8
+            for (int r = sub; r < N; r += 2) {
+                const uint4 x = chunk_of(r);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = pack_half(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xffff0000u) * down);
+                store_chunk(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+            }
+            if (lane == 0) s_exp[slot] = e;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
+        }
+        if (lane == 0) p.split[cta] = split;
+    } else if (warp == R::kCopyWarp || warp == R::kCopyWarp + 1) {
+        // --------------------------------------------------------------- copies
+        const int kv = warp - R::kCopyWarp;
+        const uint8_t* codes = static_cast<const uint8_t*>(kv ? p.v : p.k);
+        const uint8_t* scales = kv ? p.vs : p.ks;
+        uint32_t step = 0;
+        bool ok = true;
+        for (int si = 0; ok; ++si) {
+            const int slot = si % kSegs;
+            ok = wait_all(b_seg_full + 8 * slot, si / kSegs);
+            if (!ok) { if (lane == 0) give_up(2); break; }
+            const Seg& sg = const_cast<Seg&>(s_seg[slot]);
+            struct { int b, h, pos0, pos1, steps, seen; } d = {sg.b, sg.h, sg.pos0, sg.pos1, sg.steps, sg.len - sg.n + 1};
+            __syncwarp();
+            if (d.steps < 0) break;
+            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
+            const int32_t* row = p.table + (size_t)d.b * p.width;
+            int pages[4];                        // of this lane's positions lane, + 32, + 64, + 96
+            auto look_up = [&](int pos0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pos = pos0 + 32 * i + lane;
+                    pages[i] = pos < d.pos1 ? __ldg(row + p.by_page(pos)) : -1;
+                }
+            };
+            look_up(d.pos0);
+            for (int s = 0; s < d.steps; ++s, ++step) {
+                const int stage = step % kStages, pos0 = d.pos0 + s * kSteps;
+                const uint32_t full = b_cfull + 8 * (kv * kStages + stage);
+                // where this lane's rows lie, in rows of the head's pages
+                int at[4];
+                uint32_t bad[4], there[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pos = pos0 + 32 * i + lane;
+                    const bool in = pos < d.pos1, have = in && pages[i] >= 0 && pages[i] < p.pages;
+                    at[i] = have ? pos - p.by_page(pos) * p.page_size : 0;
+                    if (!have) pages[i] = 0;
+                    there[i] = __ballot_sync(~0u, have);
+                    bad[i] = __ballot_sync(~0u, in && !have);
+                }
+                if ((bad[0] | bad[1] | bad[2] | bad[3]) && lane == 0) raise_status(p.status, kBadPage);
+                if (step >= (uint32_t)kStages) ok = wait_all(b_cempty + 8 * (kv * kStages + stage), step / kStages - 1);
+                if (!ok) { if (lane == 0) give_up(3); break; }
+                if (lane == 0) {
+                    if (!kv) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s_bad[step % kBadRing * 4 + i] = bad[i];
+                    } else s_later[stage] = d.seen - pos0;
+                    ptx::mbar_arrive(full);
+                }
+                const uint32_t to = base + L::kRing + (kv * kStages + stage) * kStageBytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const long long mine = (long long)d.h * p.page_size + at[i];
+                    const long long code_at = pages[i] * p.page_stride + mine * (kDim / 2);
+                    const bool have = there[i] >> lane & 1u;
+                    cp_async_8(to + kCodes + (32 * i + lane) * 8, scales + pages[i] * p.scale_stride + mine * (kDim / fp4::kGroup), have ? 8u : 0u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 8 * j + (lane >> 2), c = lane & 3;
+                        const long long o = __shfl_sync(~0u, code_at, r);
+                        ptx::cp_async_16(to + (32 * i + r) * kRow + 16 * c, codes + o + 16 * c, there[i] >> r & 1u ? 16u : 0u);
+                    }
+                }
+                cp_async_arrive(full);           // when this lane's copies have landed
+                look_up(pos0 + kSteps);
+            }
+        }
+        ptx::cp_async_wait_all();                // every copy lands before the CTA leaves
+        __syncwarp();
+    } else if (warp >= R::kKeyWarp && warp < R::kCopyWarp) {
+        // ------------------------------------------------ codes to tensor memory
+        const int kv = warp >= R::kValWarp, quarter = warp & 3, g = lane >> 2, t = lane & 3;
+        uint32_t step = 0;
+        bool ok = true;
+        for (int si = 0; ok; ++si) {
+            const int slot = si % kSegs;
+            ok = wait_all(b_seg_full + 8 * slot, si / kSegs);
+            if (!ok) { if (lane == 0) give_up(6); break; }
+            const int steps = s_seg[slot].steps;
+            __syncwarp();
+            if (steps < 0) break;
+            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
+            for (int s = 0; s < steps; ++s, ++step) {
+                const int stage = step % kStages;
+                const uint32_t fill = 2 * step + kv, tile = fill % kTiles, at = tiles + tile * kTileCols + ((uint32_t)quarter << 21);
+                ok = wait_all(b_cfull + 8 * (kv * kStages + stage), step / kStages);
+                if (fill >= (uint32_t)kTiles) ok = wait_all(b_empty + 8 * tile, fill / kTiles - 1) && ok;
+                if (!ok) { if (lane == 0) give_up(7); break; }
+                ptx::tc_fence_after();
+                const uint8_t* st = gbase + L::kRing + (kv * kStages + stage) * kStageBytes;
+                if (!kv) {
+                    // position 32 * quarter + lane: its entries in order
+                    const uint8_t* mine = st + (32 * quarter + lane) * kRow;
+                    const uint2 sc = *reinterpret_cast<const uint2*>(st + kCodes + (32 * quarter + lane) * 8);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t v[32];
+                        const uint32_t s4 = hf ? sc.y : sc.x;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 w = reinterpret_cast<const uint4*>(mine)[2 * hf + i];
+                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                            const uint32_t both = fp4::scale_pair(i ? s4 >> 16 : s4);
+                            const uint32_t by[2] = {__byte_perm(both, both, 0x1010), __byte_perm(both, both, 0x3232)};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t h[4];
+                                fp4::unpack(words[j], h);
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) v[16 * i + 4 * j + x] = fp4::mul2(h[x], by[j / 2]);
+                            }
+                        }
+                        ptx::tmem_st32(at + 32 * hf, v);
+                    }
+                } else {
+                    // entries 32 * quarter + 4 g .. + 3 of positions t, t + 4, t + 8, t + 12 of each 16
+                    const uint8_t* mine = st + t * kRow + 16 * quarter + 2 * g;
+                    const uint8_t* sc = st + kCodes + t * 8 + 2 * quarter + (g >> 2);
+                    const int later = s_later[stage];
+                    const bool edge = later < kSteps;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t lo[16], hi[16];             // lanes 0-15 of the quarter, and 16-31
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int p0 = 16 * (4 * hf + k);
+                            uint32_t v[4], b[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                v[i] = *reinterpret_cast<const uint16_t*>(mine + (p0 + 4 * i) * kRow);
+                                b[i] = sc[(p0 + 4 * i) * 8];
+                            }
+                            if (edge) {
+                                // a NaN among the values of later tokens of the block must not reach the rows
+                                // that do not see it (0 * NaN): it is left out here and added at the segment's end
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (p0 + t + 4 * i >= later && (b[i] & 0x7fu) == 0x7fu) { b[i] = 0u; s_flags[2] = 1u; }
+                            }
+                            // positions t, t + 4 in the lower half of a word, t + 8, t + 12 in the upper
+                            const uint32_t a = v[0] | v[2] << 16, c = v[1] | v[3] << 16;
+                            const uint32_t s0 = fp4::scale_pair(b[0] | b[1] << 8), s1 = fp4::scale_pair(b[2] | b[3] << 8);
+                            uint32_t even[4], odd[4];        // [entry / 2 + 2 * half of the 16 positions]
+                            fp4::unpack((a & 0x0f0f0f0fu) | (c << 4 & 0xf0f0f0f0u), even);
+                            fp4::unpack((a >> 4 & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u), odd);
+                            lo[4 * k] = fp4::mul2(even[0], s0);
+                            lo[4 * k + 1] = fp4::mul2(odd[0], s0);
+                            lo[4 * k + 2] = fp4::mul2(even[2], s1);
+                            lo[4 * k + 3] = fp4::mul2(odd[2], s1);
+                            hi[4 * k] = fp4::mul2(even[1], s0);
+                            hi[4 * k + 1] = fp4::mul2(odd[1], s0);
+                            hi[4 * k + 2] = fp4::mul2(even[3], s1);
+                            hi[4 * k + 3] = fp4::mul2(odd[3], s1);
+                        }
+                        tmem_put_16x128b(at + 32 * hf, lo);
+                        tmem_put_16x128b(at + 32 * hf + (16u << 16), hi);
+                    }
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(b_cempty + 8 * (kv * kStages + stage));
+                    ptx::mbar_arrive(b_full + 8 * tile);
+                }
+            }
+        }
+    } else if (warp == R::kMmaWarp) {
+        // ---------------------------------------------------------- MMA issuer
+        // the whole warp runs the loop, so that descriptors are uniform values;
+        // one elected lane issues
+        constexpr uint32_t id_s = idesc_half(N, false), id_o = idesc_half(N, true);
+        const uint32_t one = elect_one();
+        const uint64_t q_desc = ptx::smem_desc_sw128(base + L::kQ, 16, 1024);
+        const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, 16, 1024);
+        // Whatever is ready goes first: the O product of the oldest step whose S
+        // product was issued, or the next S product (of the next segment, too), at
+        // most one step ahead, as two S and P fit.  Short segments keep both going.
+        struct Step { uint32_t step, seg; bool first; } old{}, young{};   // S issued, O not: the oldest, and one behind it
+        bool has_old = false, has_young = false, in_seg = false, q_ready = false, done = false, ok = true;
+        uint32_t step = 0, si = 0;
+        int s = 0, steps = 0, idle = 0;
+        long long since = clock64();
+        auto ready = [&](uint32_t b, uint32_t phase) { return __all_sync(~0u, ptx::mbar_test_wait(b, phase & 1u)); };
+        auto landed = [&](uint32_t fill) { return ready(b_full + 8 * (fill % kTiles), fill / kTiles); };
+        while (!(done && !has_old)) {
+            bool moved = false;
+            if (has_old) {                       // O^T (+)= V^T P^T
+                const uint32_t vi = 2 * old.step + 1, ob = old.seg & 1u;
+                if (ready(b_p_full, old.step) && landed(vi) &&
+                    (!old.first || old.seg < 2 || ready(b_o_empty + 8 * ob, old.seg / 2 - 1))) {
+                    ptx::tc_fence_after();
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < kSteps / 16; ++k)
+                            ptx::mma_f16_ts(tmem + (2 + ob) * N, tiles + vi % kTiles * kTileCols + 8 * k, p_desc + k * (2048 / 16), id_o,
+                                            old.first && k == 0 ? 0u : 1u);
+                        ptx::mma_commit(b_empty + 8 * (vi % kTiles));
+                        ptx::mma_commit(b_pv);
+                    }
+                    __syncwarp();
+                    old = young;
+                    has_old = has_young;
+                    has_young = false;
+                    moved = true;
+                }
+            }
+            if (!done && !in_seg && ready(b_seg_full + 8 * (si % kSegs), si / kSegs)) {
+                steps = s_seg[si % kSegs].steps;
+                __syncwarp();
+                if (steps < 0) done = true;
+                else {
+                    if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * (si % kSegs));
+                    in_seg = true;
+                    q_ready = false;
+                    s = 0;
+                }
+                moved = true;
+            }
+            if (in_seg && !has_young) {          // S^T = K Q^T
+                const uint32_t qb = si % L::kQBufs, ki = 2 * step, sb = step & 1u;
+                if (!q_ready && ready(b_q_full + 8 * qb, si / L::kQBufs)) {
+                    q_ready = true;
+                }
+                if (q_ready && landed(ki) && (step < 2 || ready(b_s_empty + 8 * sb, step / 2 - 1))) {
+                    ptx::tc_fence_after();
+                    if (one) {
+                        const uint64_t qa = q_desc + qb * (L::kQBytes / 16);
+#pragma unroll
+                        for (int k = 0; k < kDim / 16; ++k)
+                            ptx::mma_f16_ts(tmem + sb * N, tiles + ki % kTiles * kTileCols + 8 * k, qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s,
+                                            k ? 1u : 0u);
+                        ptx::mma_commit(b_empty + 8 * (ki % kTiles));
+                        ptx::mma_commit(b_s_full + 8 * sb);
+                        if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
+                    }
+                    __syncwarp();
+                    const Step now{step, si, s == 0};
+                    if (has_old) { young = now; has_young = true; }
+                    else { old = now; has_old = true; }
+                    ++step;
+                    if (++s == steps) { in_seg = false; ++si; }
+                    moved = true;
+                }
+            }
+            if (moved) idle = 0;
+            else {
+                if (idle == 0) since = clock64();
+                __nanosleep(20);
+                if ((++idle & 15) == 0 || wl < (1LL << 20))
+                    if (__any_sync(~0u, *abort_flag != 0u || clock64() - since > wl)) { ok = false; break; }
+            }
+        }
+        if (!ok && lane == 0) give_up(4);
+        // nothing is in flight in the tensor core when the CTA leaves
+        if (one) ptx::mma_commit(b_end);
+        __syncwarp();
+        ptx::mbar_wait_drain(b_end, 0, kDrainCycles);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------- softmax
+        const int group = warp >> 2, quarter = warp & 3, row = tid & 127;
+        const uint32_t lanes = (uint32_t)quarter << 21;             // TMEM lane offset of this warp
+        float4* s_max = reinterpret_cast<float4*>(gbase + L::kMax);
+        float4* s_sum = reinterpret_cast<float4*>(gbase + L::kSum);
+        // the product's step that this position is: of 16, r is (r & 8) + 2 (r & 3) + (r >> 2 & 1)
+        const int prow = (row & ~7) | (row & 3) << 1 | (row >> 2 & 1);
+        // the entry of the head that this lane of O^T holds
+        const int dim = (row & ~31) | (row & 7) << 2 | (row >> 4 & 1) << 1 | (row >> 3 & 1);
+        uint32_t step = 0;
+        bool ok = true;
+        // A segment's rows are written after the first step of the next segment
+        // (its O^T is in the other half of tensor memory), so the tensor core
+        // and the producers go on meanwhile.  What is kept of it until then:
+        bool pend = false;
+        float pend_ref = 0.f;                                      // lane c: column c's reference
+        for (uint32_t si = 0;; ++si) {
+            const int slot = si % kSegs;
+            ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
+            if (ptx::bar_red_or(1 + group, 128, !ok)) { ok = false; break; }
+            const Seg& sg = const_cast<Seg&>(s_seg[slot]);
+            struct { int n, len, r0, pos0, pos1, steps; } d = {sg.n, sg.len, sg.r0, sg.pos0, sg.pos1, sg.steps};
+            const bool none = d.steps < 0;                         // no more segments
+            if (none && !pend) break;
+            const uint32_t o_at = tmem + lanes + (2 + (si & 1u)) * N + group * HC;
+            const int first_new = d.len - d.n;                     // position of the block's first token
+            // lane c: the last position that column c of this group sees
+            const int my_last = first_new + p.by_group(d.r0 + group * HC + (lane & (HC - 1)));
+            float neg[HC], l[HC], scale2 = 0.f;                    // kLift less the reference, this thread's sum of the weights
+#pragma unroll
+            for (int c = 0; c < HC; ++c) neg[c] = l[c] = 0.f;
+            float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
+            bool unset = true;                                     // a column of the group has no reference yet
+            bool stop = false;
+            for (int s = 0; s < d.steps || s == 0; ++s) {
+                if (!none) {
+                const int pos0 = d.pos0 + s * kSteps, pos = pos0 + row, there = d.pos1 - pos0;
+                ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
+                ok = __all_sync(~0u, ok);
+                const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
+                const uint32_t bad = ok ? s_bad[step % kBadRing * 4 + quarter] : 0u;
+                // (a segment's first scores follow its Q tile)
+                if (s == 0) scale2 = p.scale * kLog2e * __int_as_float((127 + s_exp[slot]) << 23);
+                // positions beyond the end or in a bad page, and the block's later tokens
+                const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
+                const bool gone = row >= there || (bad >> lane & 1u);
+                float x[HC];
+                // the scores, -inf where the column does not see the position (read
+                // again where a reference moves)
+                auto scores = [&]() {
+                    if (ok) tmem_get<HC>(s_at, x);
+                    else {
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) x[c] = 0.f;
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) {
+                            const int last = __shfl_sync(~0u, my_last, c);
+                            if (gone || pos > last) x[c] = -INFINITY;
+                        }
+                    }
+                };
+                // .. as exponents
+                auto exponents = [&]() {
+#pragma unroll
+                    for (int c = 0; c < HC; c += 2) fma_pair(x[c], x[c + 1], scale2, neg[c], neg[c + 1]);
+                };
+                ptx::tc_fence_after();
+                float high = -INFINITY;
+                if (!unset) {
+                    scores();
+                    exponents();
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) high = fmaxf(high, x[c]);
+                }
+                // (unset is the same in the whole group)
+                const bool move = unset || ptx::bar_red_or(1 + group, 128, high > kLift + kSlack || !ok);
+                // the product before this one is done: P may be overwritten, O rescaled
+                if (step > 0) ok = wait(b_pv, step - 1) && ok;
+                if (move) {                     // the same in every thread of the group
+                    float mine = -INFINITY;
+                    scores();
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        const float w = warp_max(x[c]);
+                        if (lane == c) mine = w;
+                    }
+                    float* mx = reinterpret_cast<float*>(s_max + (step & 1u) * N + group * HC);
+                    if (lane < HC) mx[lane * 4 + quarter] = mine;
+                    if (ptx::bar_red_or(1 + group, 128, !ok)) { stop = true; break; }
+                    const float4 w4 = reinterpret_cast<const float4*>(mx)[lane & (HC - 1)];
+                    const float top = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) * scale2;
+                    const float to = fmaxf(my_ref, top);
+                    const float my_a = to > my_ref ? fast_exp2(my_ref - to) : 1.f;
+                    my_ref = to;
+                    unset = __any_sync(~0u, to == -INFINITY);
+                    if (s > 0) ptx::tc_fence_after();
+                    float a[HC];
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        a[c] = __shfl_sync(~0u, my_a, c);
+                        const float r = __shfl_sync(~0u, to, c);
+                        neg[c] = r == -INFINITY ? 0.f : kLift - r;
+                        l[c] *= a[c];
+                    }
+                    if (s > 0) {
+                        float o[HC];
+                        tmem_get<HC>(o_at, o);
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) o[c] *= a[c];
+                        tmem_put<HC>(o_at, o);
+                    }
+                    exponents();
+                }
+                ptx::tc_fence_before();          // the scores were read
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_s_empty + 8 * (step & 1u));
+                // weights: row `prow` of P, columns group * HC ..
+                const uint32_t at = base + L::kP + prow * 128;
+#pragma unroll
+                for (int c0 = 0; c0 < HC; c0 += 8) {
+                    float w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        w[e] = fast_exp2(x[c0 + e]);
+                        w[e + 1] = fast_exp2(x[c0 + e + 1]);
+                        add_pair(l[c0 + e], l[c0 + e + 1], w[e], w[e + 1]);
+                    }
+                    store_chunk(at + ((((group * HC + c0) / 8) ^ (prow & 7)) << 4), pack_half(w[0], w[1]), pack_half(w[2], w[3]),
+                                pack_half(w[4], w[5]), pack_half(w[6], w[7]));
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_p_full);
+                ++step;
+                }
+                if (s > 0 || !pend) continue;
+                // ------------------------------- the rows of the segment before
+                // (its last product was waited for in the step above)
+                pend = false;
+                if (none) ok = wait(b_pv, step - 1) && ok;
+                ok = __all_sync(~0u, ok);
+                const uint32_t pi = si - 1;
+                const Seg& e = const_cast<Seg&>(s_seg[pi % kSegs]);
+                const int e_row = group * HC + (lane & (HC - 1)), e_tok = p.by_group(e.r0 + e_row);
+                const int e_at = (e.q0 + e_tok) * p.Hq + e.h * p.G + (e.r0 + e_row - e_tok * p.G);   // below N * Hq < 2^31
+                const int cols = min(HC, e.rows - group * HC);
+                const int part_slot = e.slot, e_new = e.len - e.n;
+                // (written before the barrier that began this segment)
+                const float4 s4 = s_sum[(pi & 1u) * N + e_row];
+                const float pend_sum = (s4.x + s4.y) + (s4.z + s4.w), e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
+                ptx::tc_fence_after();
+                float o[HC];
+                if (ok) tmem_get<HC>(tmem + lanes + (2 + (pi & 1u)) * N + group * HC, o);
+                else {
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) o[c] = 0.f;
+                }
+                if (s_flags[2]) {
+                    // the NaN of the block's later tokens (this CTA's positions)
+                    for (int pos = max(e_new + 1, e.pos0); pos < e.pos1; ++pos) {
+                        const int pg = p.by_page(pos), page = p.table[(size_t)e.b * p.width + pg];
+                        if (page < 0 || page >= p.pages) continue;
+                        const uint32_t by = p.vs[page * p.scale_stride + ((long long)e.h * p.page_size + (pos - pg * p.page_size)) * (kDim / fp4::kGroup) + dim / fp4::kGroup];
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) {
+                            const int last = e_new + __shfl_sync(~0u, e_tok, c);
+                            if ((by & 0x7fu) == 0x7fu && pos <= last) o[c] = NAN;
+                        }
+                    }
+                }
+                if (part_slot < 0) {
+                    uint16_t* out = static_cast<uint16_t*>(p.out) + dim;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        const float inv = __shfl_sync(~0u, e_inv, c) * p.out_by;
+                        const int to = __shfl_sync(~0u, e_at, c);
+                        if (c < cols) out[(size_t)to * kDim] = (uint16_t)pack_bf16(o[c] * inv, 0.f);
+                    }
+                } else {
+                    float* part = p.part + ((size_t)part_slot * p.row_tile + group * HC) * kDim + dim;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c)
+                        if (c < cols) part[c * kDim] = o[c] * p.out_by;
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_o_empty + 8 * (pi & 1u));
+                if (quarter == 0 && lane < cols) {
+                    if (part_slot >= 0) {
+                        float2* stats = reinterpret_cast<float2*>(part_stats(p));
+                        stats[(size_t)part_slot * p.row_tile + e_row] = make_float2(pend_ref - kLift, pend_sum);
+                    } else if (p.lse) p.lse[e_at] = pend_sum != 0.f ? (pend_ref - kLift) * kLn2 + logf(pend_sum) : -INFINITY;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * (pi % kSegs));
+            }
+            if (stop) { ok = false; break; }
+            if (none) break;
+            // column sums: after the exchanges of 16, 8, .. lanes lane c holds
+            // column c % HC of this warp's positions, then the 4 warps' are added
+            float* sm = reinterpret_cast<float*>(s_sum + (si & 1u) * N + group * HC);
+            {
+#pragma unroll
+                for (int w = HC / 2; w; w >>= 1) {
+                    const bool up = lane & w;
+#pragma unroll
+                    for (int c = 0; c < HC / 2; ++c)
+                        if (c < w) {
+                            const float give = up ? l[c] : l[c + w], keep = up ? l[c + w] : l[c];
+                            l[c] = keep + __shfl_xor_sync(~0u, give, w);
+                        }
+                }
+#pragma unroll
+                for (int w = HC; w < 32; w <<= 1) l[0] += __shfl_xor_sync(~0u, l[0], w);
+            }
+            if (lane < HC) sm[lane * 4 + quarter] = l[0];
+            pend = true;
+            pend_ref = my_ref;
+        }
+        if (!ok && lane == 0) give_up(5);
+    }
+    // requests that own no cache position have no tile: their rows are zero
+    if (warp < kSoftWarps) empty_rows<uint16_t>(p, blockIdx.x, gridDim.x, kSoftWarps * 32);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == R::kMmaWarp) ptx::tmem_dealloc(tmem, L::kTmem);
+}
+
+template <int N>
+cudaError_t launch(const AttnParams& p, cudaStream_t s) {
+    using L = Smem<N>;
+    static_assert(L::kTotal + 1024 <= 232448 && L::kCols <= 512, "shared and tensor memory of a CTA");
+    const cudaError_t e = cudaFuncSetAttribute(attn4_mma_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal + 1024);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn4_mma_kernel<N>, dim3(p.ctas), dim3(Roles<N>::kWarps * 32), L::kTotal + 1024, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s) { return p.row_tile == 32 ? launch<32>(p, s) : launch<64>(p, s); }
+
+}  // namespace dspark

@@ -125,10 +125,14 @@ struct AttnParams {
     uint32_t* status;
 };
 cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s);
-cudaError_t launch_cache_attention4(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_cache_attention4(const AttnParams& p, bool tensor, cudaStream_t s);
 bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can copy
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
-// Over a cache in 4 bits every warp is a worker of its own (AttnParams::ctas of them): query
+// Over a cache in 4 bits, bf16 queries: above 16 rows of a key head of 128 the tensor cores
+// take them, 32 or 64 at a time (cache_attention4_mma.cu).
+inline bool attn4_tensor(int rows, int D) { return D == 128 && rows > 16; }
+cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s);
+// Else every warp is a worker of its own (AttnParams::ctas of them): query
 // rows at a time, and warps of a CTA for groups of 8 rows, as registers allow.
 inline int attn4_row_tile(int rows, int D) { return rows <= 8 ? 8 : rows <= 16 || D > 128 ? 16 : 32; }
 constexpr int attn4_warps(int groups, int D) { return groups == 1 && D <= 128 ? 12 : 8; }
