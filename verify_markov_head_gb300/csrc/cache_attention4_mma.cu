@@ -20,11 +20,13 @@
 // are fp16, 2^(s - ref + 7), as in cache_attention4.cu, whose notes on precision hold
 // here too, except that the rows of a tile share the power of two that q is scaled by.
 //
-// Roles (20 warps, 28 with 64 columns, one CTA per SM):
+// Roles (24 warps, 28 with 64 columns, one CTA per SM):
 //   first 8 or 16    softmax: groups of 4 warps, 16 columns each; thread = position
-//   then eight       keys, values: codes to tensor memory (warp & 3 = its 32 lanes)
+//   then 12 or 8     four keys, the others values: codes to tensor memory (warp & 3 = its 32 lanes)
 //   then two         copies of the keys' and of the values' codes and scales
 //   one              MMA issuer, one more the segments and Q tiles
+#include <cudaTypedefs.h>
+
 #include "attn_rows.cuh"
 #include "fp4.cuh"
 #include "pdl.cuh"
@@ -42,18 +44,19 @@ constexpr int kBadRing = 16;             // steps the copies may be ahead of the
 constexpr float kLift = 7.f;             // log2 of a weight at the reference
 constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
 constexpr long long kDrainCycles = 200000000LL;
-constexpr int kRow = 80;                 // bytes from row to row of codes in shared memory
+constexpr int kRow = 64;                 // bytes of a position's codes, chunks of 16 swizzled as TMA's 64-byte mode does
 constexpr int kCodes = kSteps * kRow;    // of a stage, then the scales
 constexpr int kStageBytes = kCodes + kSteps * (kDim / fp4::kGroup);
-constexpr int kStages = 5;               // of keys, and of values
+constexpr int kStages = 6;               // of keys, and of values
 constexpr int kTiles = 4;                // A tiles in tensor memory: keys 0 and 2, values 1 and 3
 constexpr int kTileCols = kDim / 2;      // columns of one
 
 template <int N>
 struct Roles {
-    static constexpr int kParts = N / 16, kSoftWarps = 4 * kParts;
-    static constexpr int kKeyWarp = kSoftWarps, kValWarp = kSoftWarps + 4, kCopyWarp = kSoftWarps + 8;
-    static constexpr int kMmaWarp = kSoftWarps + 10, kSegWarp = kSoftWarps + 11, kWarps = kSoftWarps + 12;
+    static constexpr int HC = 16;                 // columns of a softmax group
+    static constexpr int kSoftWarps = 4 * (N / HC), kValWarps = N == 32 ? 8 : 4;
+    static constexpr int kKeyWarp = kSoftWarps, kValWarp = kKeyWarp + 4, kCopyWarp = kValWarp + kValWarps;
+    static constexpr int kMmaWarp = kCopyWarp + 2, kSegWarp = kCopyWarp + 3, kWarps = kCopyWarp + 4;
 };
 
 struct Seg {
@@ -70,29 +73,26 @@ struct Smem {
     static constexpr int kCols = 4 * N + kTiles * kTileCols;      // tensor memory: two S, two O, the A tiles
     static constexpr int kTmem = 512;
     static constexpr int kQ = 0;
-    static constexpr int kP = kQ + kQBufs * kQBytes;              // [128][64] fp16, 128-byte rows
-    static constexpr int kRing = kP + kSteps * 128;               // [keys, values][stage]
+    static constexpr int kPBytes = kSteps * 128;
+    static constexpr int kP = kQ + kQBufs * kQBytes;              // two of [128][64] fp16, 128-byte rows
+    static constexpr int kRing = kP + 2 * kPBytes;                // [keys, values][stage]
     static constexpr int kMax = kRing + 2 * kStages * kStageBytes;    // [2][N][4], by the step's parity
     static constexpr int kSum = kMax + 2 * N * 16;                // [2][N][4], by the segment's parity
     static constexpr int kSeg = kSum + 2 * N * 16;
     static constexpr int kBar = (kSeg + kSegs * (int)sizeof(Seg) + 7) / 8 * 8;
-    static constexpr int kBars = 4 * kStages + 2 * kTiles + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 3;
+    static constexpr int kBars = 4 * kStages + 2 * kTiles + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 2 + 2 + 1;
     static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, NaN flag, -
     static constexpr int kExp = kFlags + 16;                      // [kSegs] exponents of the Q tiles
     static constexpr int kLater = kExp + 4 * kSegs;               // [kStages] first of a step's positions that not every row sees
-    static constexpr int kBad = kLater + 4 * kStages;             // [kBadRing][4] positions whose page is out of range
-    static constexpr int kTotal = kBad + 16 * kBadRing;
+    static constexpr int kBad = kLater + 4 * kStages;             // [kBadRing] boxes whose page is out of range
+    static constexpr int kThere = kBad + 4 * kBadRing;            // [kStages] boxes of a step's values that were copied, and its positions before the end
+    static constexpr int kTotal = kThere + 8 * kStages;
 };
 
 __device__ __forceinline__ float warp_max(float x) {     // over the warp, NaN left out
     float y;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// Arrive on an mbarrier once this thread's cp.async so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Nonzero in one lane of the (converged) warp.
@@ -104,6 +104,11 @@ __device__ __forceinline__ uint32_t elect_one() {
 
 // N columns of 32 lanes, waited for.
 template <int C> __device__ __forceinline__ void tmem_get(uint32_t a, float (&v)[C]);
+template <> __device__ __forceinline__ void tmem_get<8>(uint32_t a, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(a) : "memory");
+}
 template <> __device__ __forceinline__ void tmem_get<16>(uint32_t a, float (&v)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  "\n\ttcgen05.wait::ld.sync.aligned;"
@@ -112,6 +117,10 @@ template <> __device__ __forceinline__ void tmem_get<16>(uint32_t a, float (&v)[
                  : "r"(a) : "memory");
 }
 template <int C> __device__ __forceinline__ void tmem_put(uint32_t a, const float (&v)[C]);
+template <> __device__ __forceinline__ void tmem_put<8>(uint32_t a, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;"
+                 ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+}
 template <> __device__ __forceinline__ void tmem_put<16>(uint32_t a, const float (&v)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  "\n\ttcgen05.wait::st.sync.aligned;"
@@ -142,13 +151,22 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 __device__ __forceinline__ void store_chunk(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ void cp_async_8(uint32_t to, const void* from, uint32_t bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+// The box of codes from position `pos` of (page, head) `z`.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m, int pos, int z, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(pos), "r"(z), "r"(bar), "l"(policy)
+        : "memory");
 }
-// 16 lanes x 32 columns of tensor memory, as fragments: thread t holds of every 4 columns
-// column t % 4 of lanes t / 4 and t / 4 + 8.
-__device__ __forceinline__ void tmem_put_16x128b(uint32_t a, const uint32_t (&v)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+// 16 lanes x 8 columns of tensor memory, as fragments: thread t holds columns t % 4 and
+// 4 + t % 4 of lanes t / 4 (v0, v2) and t / 4 + 8 (v1, v3).
+__device__ __forceinline__ void tmem_put_16x128b(uint32_t a, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v0), "r"(v1), "r"(v2), "r"(v3) : "memory");
+}
+// 32 lanes x 16 columns: thread t holds lane t.
+__device__ __forceinline__ void tmem_put_32x32b(uint32_t a, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
                    "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
 }
@@ -158,10 +176,10 @@ constexpr uint32_t idesc_half(int N, bool b_mn_major) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const int bx, const int page_heads) {
     using L = Smem<N>;
     using R = Roles<N>;
-    constexpr int kSoftWarps = R::kSoftWarps, HC = 16;             // columns of a softmax group
+    constexpr int kSoftWarps = R::kSoftWarps, HC = R::HC;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -171,6 +189,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
     volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(gbase + L::kBad);
     volatile int* s_exp = reinterpret_cast<volatile int*>(gbase + L::kExp);
     volatile int* s_later = reinterpret_cast<volatile int*>(gbase + L::kLater);
+    volatile int* s_there = reinterpret_cast<volatile int*>(gbase + L::kThere);
     volatile Seg* s_seg = reinterpret_cast<volatile Seg*>(gbase + L::kSeg);
     volatile uint32_t* abort_flag = s_flags + 1;
     uint32_t bar = base + L::kBar;
@@ -179,19 +198,20 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
     const uint32_t b_full = take(kTiles), b_empty = take(kTiles);                   // A tiles
     const uint32_t b_seg_full = take(kSegs), b_seg_empty = take(kSegs);
     const uint32_t b_q_full = take(L::kQBufs), b_q_empty = take(L::kQBufs), b_s_full = take(2), b_s_empty = take(2);
-    const uint32_t b_o_empty = take(2), b_p_full = take(1), b_pv = take(1), b_end = take(1);
+    const uint32_t b_o_empty = take(2), b_p_full = take(2), b_pv = take(2), b_end = take(1);
 
     if (tid == 0) {
         grid_launch_dependents();       // the join is scheduled now and waits for this grid
-        for (int i = 0; i < 2 * kStages; ++i) { ptx::mbar_init(b_cfull + 8 * i, 33); ptx::mbar_init(b_cempty + 8 * i, 4); }
-        for (int i = 0; i < kTiles; ++i) { ptx::mbar_init(b_full + 8 * i, 4); ptx::mbar_init(b_empty + 8 * i, 1); }
-        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 1 + 2 + 8 + kSoftWarps); }
+        for (int i = 0; i < 2 * kStages; ++i) { ptx::mbar_init(b_cfull + 8 * i, 1); ptx::mbar_init(b_cempty + 8 * i, i < kStages ? 4 : R::kValWarps); }
+        for (int i = 0; i < kTiles; ++i) { ptx::mbar_init(b_full + 8 * i, i & 1 ? R::kValWarps : 4); ptx::mbar_init(b_empty + 8 * i, 1); }
+        for (int i = 0; i < kSegs; ++i) { ptx::mbar_init(b_seg_full + 8 * i, 1); ptx::mbar_init(b_seg_empty + 8 * i, 1 + 2 + 4 + R::kValWarps + kSoftWarps); }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(b_s_full + 8 * i, 1); ptx::mbar_init(b_s_empty + 8 * i, kSoftWarps);
             ptx::mbar_init(b_o_empty + 8 * i, kSoftWarps);
+            ptx::mbar_init(b_p_full + 8 * i, kSoftWarps); ptx::mbar_init(b_pv + 8 * i, 1);
         }
         for (int i = 0; i < L::kQBufs; ++i) { ptx::mbar_init(b_q_full + 8 * i, 1); ptx::mbar_init(b_q_empty + 8 * i, 1); }
-        ptx::mbar_init(b_p_full, kSoftWarps); ptx::mbar_init(b_pv, 1); ptx::mbar_init(b_end, 1);
+        ptx::mbar_init(b_end, 1);
         s_flags[1] = 0u;
         s_flags[2] = 0u;
         ptx::fence_mbar_init();
@@ -288,9 +308,11 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
         if (lane == 0) p.split[cta] = split;
     } else if (warp == R::kCopyWarp || warp == R::kCopyWarp + 1) {
         // --------------------------------------------------------------- copies
-        const int kv = warp - R::kCopyWarp;
-        const uint8_t* codes = static_cast<const uint8_t*>(kv ? p.v : p.k);
+        // lanes 0 .. : a box of bx positions' codes each; lanes 16 .. : their scales
+        const int kv = warp - R::kCopyWarp, mine = lane & 15, nbox = kSteps / bx;
+        const CUtensorMap* map = kv ? &vmap : &kmap;
         const uint8_t* scales = kv ? p.vs : p.ks;
+        const uint64_t pol = p.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
         uint32_t step = 0;
         bool ok = true;
         for (int si = 0; ok; ++si) {
@@ -303,63 +325,46 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
             if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
             const int32_t* row = p.table + (size_t)d.b * p.width;
-            int pages[4];                        // of this lane's positions lane, + 32, + 64, + 96
-            auto look_up = [&](int pos0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = pos0 + 32 * i + lane;
-                    pages[i] = pos < d.pos1 ? __ldg(row + p.by_page(pos)) : -1;
-                }
-            };
-            look_up(d.pos0);
+            auto page_of = [&](int pos) { return mine < nbox && pos < d.pos1 ? __ldg(row + p.by_page(pos)) : -1; };
+            int next = page_of(d.pos0 + mine * bx);
             for (int s = 0; s < d.steps; ++s, ++step) {
-                const int stage = step % kStages, pos0 = d.pos0 + s * kSteps;
-                const uint32_t full = b_cfull + 8 * (kv * kStages + stage);
-                // where this lane's rows lie, in rows of the head's pages
-                int at[4];
-                uint32_t bad[4], there[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = pos0 + 32 * i + lane;
-                    const bool in = pos < d.pos1, have = in && pages[i] >= 0 && pages[i] < p.pages;
-                    at[i] = have ? pos - p.by_page(pos) * p.page_size : 0;
-                    if (!have) pages[i] = 0;
-                    there[i] = __ballot_sync(~0u, have);
-                    bad[i] = __ballot_sync(~0u, in && !have);
-                }
-                if ((bad[0] | bad[1] | bad[2] | bad[3]) && lane == 0) raise_status(p.status, kBadPage);
+                const int stage = step % kStages, pos0 = d.pos0 + s * kSteps, pos = pos0 + mine * bx, page = next;
+                const bool in = mine < nbox && pos < d.pos1, have = in && page >= 0 && page < p.pages;
+                const uint32_t there = __ballot_sync(~0u, have) & 0xffffu, bad = __ballot_sync(~0u, in && !have) & 0xffffu;
+                next = page_of(pos + kSteps);
+                if (bad && lane == 0) raise_status(p.status, kBadPage);
                 if (step >= (uint32_t)kStages) ok = wait_all(b_cempty + 8 * (kv * kStages + stage), step / kStages - 1);
                 if (!ok) { if (lane == 0) give_up(3); break; }
+                const uint32_t full = b_cfull + 8 * (kv * kStages + stage), to = base + L::kRing + (kv * kStages + stage) * kStageBytes;
                 if (lane == 0) {
-                    if (!kv) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s_bad[step % kBadRing * 4 + i] = bad[i];
-                    } else s_later[stage] = d.seen - pos0;
-                    ptx::mbar_arrive(full);
-                }
-                const uint32_t to = base + L::kRing + (kv * kStages + stage) * kStageBytes;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const long long mine = (long long)d.h * p.page_size + at[i];
-                    const long long code_at = pages[i] * p.page_stride + mine * (kDim / 2);
-                    const bool have = there[i] >> lane & 1u;
-                    cp_async_8(to + kCodes + (32 * i + lane) * 8, scales + pages[i] * p.scale_stride + mine * (kDim / fp4::kGroup), have ? 8u : 0u);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = 8 * j + (lane >> 2), c = lane & 3;
-                        const long long o = __shfl_sync(~0u, code_at, r);
-                        ptx::cp_async_16(to + (32 * i + r) * kRow + 16 * c, codes + o + 16 * c, there[i] >> r & 1u ? 16u : 0u);
+                    if (!kv) s_bad[step % kBadRing] = bad;
+                    else {
+                        s_later[stage] = d.seen - pos0;
+                        s_there[2 * stage] = (int)there;
+                        s_there[2 * stage + 1] = d.pos1 - pos0;
                     }
+                    if (there) ptx::mbar_arrive_expect_tx(full, __popc(there) * bx * (kRow + kDim / fp4::kGroup));
+                    else ptx::mbar_arrive(full);
                 }
-                cp_async_arrive(full);           // when this lane's copies have landed
-                look_up(pos0 + kSteps);
+                __syncwarp();
+                if (have) {
+                    const int r = pos - p.by_page(pos) * p.page_size;
+                    if (lane < 16) tma_load_rows(to + mine * bx * kRow, map, r, page * page_heads + d.h, full, pol);
+                    else ptx::bulk_load(to + kCodes + mine * bx * (kDim / fp4::kGroup),
+                                        scales + page * p.scale_stride + ((long long)d.h * p.page_size + r) * (kDim / fp4::kGroup),
+                                        bx * (kDim / fp4::kGroup), full, pol);
+                }
+                __syncwarp();
             }
         }
-        ptx::cp_async_wait_all();                // every copy lands before the CTA leaves
+        // every copy lands before the CTA leaves: the last fill of each stage
+        if (lane == 0)
+            for (uint32_t f = step; f-- > 0 && f + kStages >= step;)
+                ptx::mbar_wait_drain(b_cfull + 8 * (kv * kStages + f % kStages), (f / kStages) & 1u, kDrainCycles);
         __syncwarp();
     } else if (warp >= R::kKeyWarp && warp < R::kCopyWarp) {
         // ------------------------------------------------ codes to tensor memory
-        const int kv = warp >= R::kValWarp, quarter = warp & 3, g = lane >> 2, t = lane & 3;
+        const int kv = warp >= R::kValWarp, quarter = warp & 3, part = kv ? (warp - R::kValWarp) >> 2 : 0, g = lane >> 2, t = lane & 3;
         uint32_t step = 0;
         bool ok = true;
         for (int si = 0; ok; ++si) {
@@ -378,72 +383,65 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 if (!ok) { if (lane == 0) give_up(7); break; }
                 ptx::tc_fence_after();
                 const uint8_t* st = gbase + L::kRing + (kv * kStages + stage) * kStageBytes;
+                // (loops that stay small: twenty warps of six roles share an SM's instruction cache)
                 if (!kv) {
                     // position 32 * quarter + lane: its entries in order
-                    const uint8_t* mine = st + (32 * quarter + lane) * kRow;
-                    const uint2 sc = *reinterpret_cast<const uint2*>(st + kCodes + (32 * quarter + lane) * 8);
+                    const uint4* mine = reinterpret_cast<const uint4*>(st + (32 * quarter + lane) * kRow);
+                    const uint8_t* sc = st + kCodes + (32 * quarter + lane) * 8;
+                    const int turn = lane >> 1 & 3;          // of the chunks
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 w = mine[i ^ turn];
+                        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                        const uint32_t both = fp4::scale_pair(reinterpret_cast<const uint16_t*>(sc)[i]);
+                        const uint32_t by[2] = {__byte_perm(both, both, 0x1010), __byte_perm(both, both, 0x3232)};
+                        uint32_t v[16];
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t v[32];
-                        const uint32_t s4 = hf ? sc.y : sc.x;
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t h[4];
+                            fp4::unpack(words[j], h);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 w = reinterpret_cast<const uint4*>(mine)[2 * hf + i];
-                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-                            const uint32_t both = fp4::scale_pair(i ? s4 >> 16 : s4);
-                            const uint32_t by[2] = {__byte_perm(both, both, 0x1010), __byte_perm(both, both, 0x3232)};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t h[4];
-                                fp4::unpack(words[j], h);
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) v[16 * i + 4 * j + x] = fp4::mul2(h[x], by[j / 2]);
-                            }
+                            for (int x = 0; x < 4; ++x) v[4 * j + x] = fp4::mul2(h[x], by[j / 2]);
                         }
-                        ptx::tmem_st32(at + 32 * hf, v);
+                        tmem_put_32x32b(at + 16 * i, v);
                     }
                 } else {
                     // entries 32 * quarter + 4 g .. + 3 of positions t, t + 4, t + 8, t + 12 of each 16
-                    const uint8_t* mine = st + t * kRow + 16 * quarter + 2 * g;
-                    const uint8_t* sc = st + kCodes + t * 8 + 2 * quarter + (g >> 2);
-                    const int later = s_later[stage];
-                    const bool edge = later < kSteps;
+                    constexpr int kMine = kSteps / 16 * 4 / R::kValWarps;        // sixteens of this warp
+                    // (rows t and t + 8 swap their chunks alike, t + 4 and t + 12 the other way)
+                    const uint8_t* mine = st + (16 * kMine * part + t) * kRow + 2 * g;
+                    const int even_at = 16 * (quarter ^ (t >> 1)), odd_at = 16 * (quarter ^ (t >> 1) ^ 2);
+                    const uint8_t* sc = st + kCodes + (16 * kMine * part + t) * 8 + 2 * quarter + (g >> 2);
+                    const int first = 16 * kMine * part + t, later = s_later[stage], there = s_there[2 * stage], stop = s_there[2 * stage + 1];
+                    const bool edge = later < kSteps || stop < kSteps || there != (1 << kSteps / bx) - 1;
+#pragma unroll 2
+                    for (int k = 0; k < kMine; ++k, mine += 16 * kRow, sc += 16 * 8) {
+                        uint32_t v[4], b[4];
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t lo[16], hi[16];             // lanes 0-15 of the quarter, and 16-31
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int p0 = 16 * (4 * hf + k);
-                            uint32_t v[4], b[4];
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] = *reinterpret_cast<const uint16_t*>(mine + 4 * i * kRow + (i & 1 ? odd_at : even_at));
+                            b[i] = sc[4 * i * 8];
+                        }
+                        if (edge) {
+                            // what no row may use counts as 0, and a NaN among the values of later tokens of the
+                            // block, which must not reach the rows that do not see it (0 * NaN), is left out
+                            // here and added at the segment's end
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                v[i] = *reinterpret_cast<const uint16_t*>(mine + (p0 + 4 * i) * kRow);
-                                b[i] = sc[(p0 + 4 * i) * 8];
+                                const int r = first + 16 * k + 4 * i;
+                                if (r >= stop || !(there >> r / bx & 1)) b[i] = 0u;
+                                else if (r >= later && (b[i] & 0x7fu) == 0x7fu) { b[i] = 0u; s_flags[2] = 1u; }
                             }
-                            if (edge) {
-                                // a NaN among the values of later tokens of the block must not reach the rows
-                                // that do not see it (0 * NaN): it is left out here and added at the segment's end
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (p0 + t + 4 * i >= later && (b[i] & 0x7fu) == 0x7fu) { b[i] = 0u; s_flags[2] = 1u; }
-                            }
-                            // positions t, t + 4 in the lower half of a word, t + 8, t + 12 in the upper
-                            const uint32_t a = v[0] | v[2] << 16, c = v[1] | v[3] << 16;
-                            const uint32_t s0 = fp4::scale_pair(b[0] | b[1] << 8), s1 = fp4::scale_pair(b[2] | b[3] << 8);
-                            uint32_t even[4], odd[4];        // [entry / 2 + 2 * half of the 16 positions]
-                            fp4::unpack((a & 0x0f0f0f0fu) | (c << 4 & 0xf0f0f0f0u), even);
-                            fp4::unpack((a >> 4 & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u), odd);
-                            lo[4 * k] = fp4::mul2(even[0], s0);
-                            lo[4 * k + 1] = fp4::mul2(odd[0], s0);
-                            lo[4 * k + 2] = fp4::mul2(even[2], s1);
-                            lo[4 * k + 3] = fp4::mul2(odd[2], s1);
-                            hi[4 * k] = fp4::mul2(even[1], s0);
-                            hi[4 * k + 1] = fp4::mul2(odd[1], s0);
-                            hi[4 * k + 2] = fp4::mul2(even[3], s1);
-                            hi[4 * k + 3] = fp4::mul2(odd[3], s1);
                         }
-                        tmem_put_16x128b(at + 32 * hf, lo);
-                        tmem_put_16x128b(at + 32 * hf + (16u << 16), hi);
+                        // positions t, t + 4 in the lower half of a word, t + 8, t + 12 in the upper
+                        const uint32_t a = __byte_perm(v[0], v[2], 0x5410), c = __byte_perm(v[1], v[3], 0x5410);
+                        const uint32_t s0 = fp4::scale_pair(b[0] | b[1] << 8), s1 = fp4::scale_pair(b[2] | b[3] << 8);
+                        uint32_t even[4], odd[4];            // [entry / 2 + 2 * half of the 16 positions]
+                        fp4::unpack((a & 0x0f0f0f0fu) | (c << 4 & 0xf0f0f0f0u), even);
+                        fp4::unpack((a >> 4 & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u), odd);
+                        const uint32_t to = at + 8 * (kMine * part + k);
+                        tmem_put_16x128b(to, fp4::mul2(even[0], s0), fp4::mul2(odd[0], s0), fp4::mul2(even[2], s1), fp4::mul2(odd[2], s1));
+                        tmem_put_16x128b(to + (16u << 16), fp4::mul2(even[1], s0), fp4::mul2(odd[1], s0), fp4::mul2(even[3], s1), fp4::mul2(odd[3], s1));
                     }
                 }
                 ptx::tmem_wait_st();
@@ -463,84 +461,57 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
         const uint32_t one = elect_one();
         const uint64_t q_desc = ptx::smem_desc_sw128(base + L::kQ, 16, 1024);
         const uint64_t p_desc = ptx::smem_desc_sw128(base + L::kP, 16, 1024);
-        // Whatever is ready goes first: the O product of the oldest step whose S
-        // product was issued, or the next S product (of the next segment, too), at
-        // most one step ahead, as two S and P fit.  Short segments keep both going.
-        struct Step { uint32_t step, seg; bool first; } old{}, young{};   // S issued, O not: the oldest, and one behind it
-        bool has_old = false, has_young = false, in_seg = false, q_ready = false, done = false, ok = true;
-        uint32_t step = 0, si = 0;
-        int s = 0, steps = 0, idle = 0;
-        long long since = clock64();
-        auto ready = [&](uint32_t b, uint32_t phase) { return __all_sync(~0u, ptx::mbar_test_wait(b, phase & 1u)); };
-        auto landed = [&](uint32_t fill) { return ready(b_full + 8 * (fill % kTiles), fill / kTiles); };
-        while (!(done && !has_old)) {
-            bool moved = false;
-            if (has_old) {                       // O^T (+)= V^T P^T
-                const uint32_t vi = 2 * old.step + 1, ob = old.seg & 1u;
-                if (ready(b_p_full, old.step) && landed(vi) &&
-                    (!old.first || old.seg < 2 || ready(b_o_empty + 8 * ob, old.seg / 2 - 1))) {
-                    ptx::tc_fence_after();
-                    if (one) {
-#pragma unroll
-                        for (int k = 0; k < kSteps / 16; ++k)
-                            ptx::mma_f16_ts(tmem + (2 + ob) * N, tiles + vi % kTiles * kTileCols + 8 * k, p_desc + k * (2048 / 16), id_o,
-                                            old.first && k == 0 ? 0u : 1u);
-                        ptx::mma_commit(b_empty + 8 * (vi % kTiles));
-                        ptx::mma_commit(b_pv);
-                    }
-                    __syncwarp();
-                    old = young;
-                    has_old = has_young;
-                    has_young = false;
-                    moved = true;
-                }
+        // S of a step, then O of the step before
+        uint32_t step = 0, o_seg = 0;
+        bool ok = true, o_first = true;
+        auto product_o = [&](uint32_t of) {      // O^T (+)= V^T P^T of step `of`, of segment o_seg
+            const uint32_t vi = 2 * of + 1, ob = o_seg & 1u;
+            ok = wait_all(b_full + 8 * (vi % kTiles), vi / kTiles) && ok;
+            if (o_first && o_seg >= 2) ok = wait_all(b_o_empty + 8 * ob, o_seg / 2 - 1) && ok;
+            ok = wait_all(b_p_full + 8 * (of & 1u), of / 2) && ok;
+            if (!ok) return;
+            ptx::tc_fence_after();
+            if (one) {
+#pragma unroll 1
+                for (int k = 0; k < kSteps / 16; ++k)
+                    ptx::mma_f16_ts(tmem + (2 + ob) * N, tiles + vi % kTiles * kTileCols + 8 * k, p_desc + (of & 1u) * (L::kPBytes / 16) + k * (2048 / 16),
+                                    id_o, o_first && k == 0 ? 0u : 1u);
+                ptx::mma_commit(b_empty + 8 * (vi % kTiles));
+                ptx::mma_commit(b_pv + 8 * (of & 1u));
             }
-            if (!done && !in_seg && ready(b_seg_full + 8 * (si % kSegs), si / kSegs)) {
-                steps = s_seg[si % kSegs].steps;
+            __syncwarp();
+            o_first = false;
+        };
+        for (uint32_t si = 0; ok; ++si) {
+            ok = wait_all(b_seg_full + 8 * (si % kSegs), si / kSegs);
+            if (!ok) break;
+            const int steps = s_seg[si % kSegs].steps;
+            __syncwarp();
+            if (steps < 0) break;
+            if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * (si % kSegs));
+            const uint32_t qb = si % L::kQBufs;
+            ok = wait_all(b_q_full + 8 * qb, si / L::kQBufs);
+            for (int s = 0; s < steps && ok; ++s, ++step) {
+                const uint32_t ki = 2 * step, sb = step & 1u;
+                ok = wait_all(b_full + 8 * (ki % kTiles), ki / kTiles) && ok;
+                if (step >= 2) ok = wait_all(b_s_empty + 8 * sb, step / 2 - 1) && ok;
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (one) {
+                    const uint64_t qa = q_desc + qb * (L::kQBytes / 16);
+#pragma unroll 1
+                    for (int k = 0; k < kDim / 16; ++k)
+                        ptx::mma_f16_ts(tmem + sb * N, tiles + ki % kTiles * kTileCols + 8 * k, qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, k ? 1u : 0u);
+                    ptx::mma_commit(b_empty + 8 * (ki % kTiles));
+                    ptx::mma_commit(b_s_full + 8 * sb);
+                    if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
+                }
                 __syncwarp();
-                if (steps < 0) done = true;
-                else {
-                    if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * (si % kSegs));
-                    in_seg = true;
-                    q_ready = false;
-                    s = 0;
-                }
-                moved = true;
-            }
-            if (in_seg && !has_young) {          // S^T = K Q^T
-                const uint32_t qb = si % L::kQBufs, ki = 2 * step, sb = step & 1u;
-                if (!q_ready && ready(b_q_full + 8 * qb, si / L::kQBufs)) {
-                    q_ready = true;
-                }
-                if (q_ready && landed(ki) && (step < 2 || ready(b_s_empty + 8 * sb, step / 2 - 1))) {
-                    ptx::tc_fence_after();
-                    if (one) {
-                        const uint64_t qa = q_desc + qb * (L::kQBytes / 16);
-#pragma unroll
-                        for (int k = 0; k < kDim / 16; ++k)
-                            ptx::mma_f16_ts(tmem + sb * N, tiles + ki % kTiles * kTileCols + 8 * k, qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s,
-                                            k ? 1u : 0u);
-                        ptx::mma_commit(b_empty + 8 * (ki % kTiles));
-                        ptx::mma_commit(b_s_full + 8 * sb);
-                        if (s == steps - 1) ptx::mma_commit(b_q_empty + 8 * qb);
-                    }
-                    __syncwarp();
-                    const Step now{step, si, s == 0};
-                    if (has_old) { young = now; has_young = true; }
-                    else { old = now; has_old = true; }
-                    ++step;
-                    if (++s == steps) { in_seg = false; ++si; }
-                    moved = true;
-                }
-            }
-            if (moved) idle = 0;
-            else {
-                if (idle == 0) since = clock64();
-                __nanosleep(20);
-                if ((++idle & 15) == 0 || wl < (1LL << 20))
-                    if (__any_sync(~0u, *abort_flag != 0u || clock64() - since > wl)) { ok = false; break; }
+                if (step > 0) product_o(step - 1);
+                if (s == 0) { o_seg = si; o_first = true; }
             }
         }
+        if (ok && step > 0) product_o(step - 1);
         if (!ok && lane == 0) give_up(4);
         // nothing is in flight in the tensor core when the CTA leaves
         if (one) ptx::mma_commit(b_end);
@@ -554,6 +525,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
         float4* s_max = reinterpret_cast<float4*>(gbase + L::kMax);
         float4* s_sum = reinterpret_cast<float4*>(gbase + L::kSum);
         // the product's step that this position is: of 16, r is (r & 8) + 2 (r & 3) + (r >> 2 & 1)
+        const int my_box = row / bx;
         const int prow = (row & ~7) | (row & 3) << 1 | (row >> 2 & 1);
         // the entry of the head that this lane of O^T holds
         const int dim = (row & ~31) | (row & 7) << 2 | (row >> 4 & 1) << 1 | (row >> 3 & 1);
@@ -588,12 +560,12 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
                 ok = __all_sync(~0u, ok);
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
-                const uint32_t bad = ok ? s_bad[step % kBadRing * 4 + quarter] : 0u;
+                const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
                 // (a segment's first scores follow its Q tile)
                 if (s == 0) scale2 = p.scale * kLog2e * __int_as_float((127 + s_exp[slot]) << 23);
                 // positions beyond the end or in a bad page, and the block's later tokens
                 const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
-                const bool gone = row >= there || (bad >> lane & 1u);
+                const bool gone = row >= there || (bad >> my_box & 1u);
                 float x[HC];
                 // the scores, -inf where the column does not see the position (read
                 // again where a reference moves)
@@ -626,9 +598,11 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 }
                 // (unset is the same in the whole group)
                 const bool move = unset || ptx::bar_red_or(1 + group, 128, high > kLift + kSlack || !ok);
-                // the product before this one is done: P may be overwritten, O rescaled
-                if (step > 0) ok = wait(b_pv, step - 1) && ok;
+                // the product before the last is done: its P may be overwritten
+                if (step > 1) ok = wait(b_pv + 8 * (step & 1u), step / 2 - 1) && ok;
                 if (move) {                     // the same in every thread of the group
+                    // the last one too: O may be rescaled
+                    if (step > 0) ok = wait(b_pv + 8 * ((step - 1) & 1u), (step - 1) / 2) && ok;
                     float mine = -INFINITY;
                     scores();
 #pragma unroll
@@ -667,7 +641,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(b_s_empty + 8 * (step & 1u));
                 // weights: row `prow` of P, columns group * HC ..
-                const uint32_t at = base + L::kP + prow * 128;
+                const uint32_t at = base + L::kP + (step & 1u) * L::kPBytes + prow * 128;
 #pragma unroll
                 for (int c0 = 0; c0 < HC; c0 += 8) {
                     float w[8];
@@ -683,14 +657,16 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(b_p_full);
+                if (lane == 0) ptx::mbar_arrive(b_p_full + 8 * (step & 1u));
                 ++step;
                 }
                 if (s > 0 || !pend) continue;
                 // ------------------------------- the rows of the segment before
-                // (its last product was waited for in the step above)
                 pend = false;
-                if (none) ok = wait(b_pv, step - 1) && ok;
+                {
+                    const uint32_t its = step - (none ? 1u : 2u);          // its last step
+                    ok = wait(b_pv + 8 * (its & 1u), its / 2) && ok;
+                }
                 ok = __all_sync(~0u, ok);
                 const uint32_t pi = si - 1;
                 const Seg& e = const_cast<Seg&>(s_seg[pi % kSegs]);
@@ -784,12 +760,33 @@ template <int N>
 cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     using L = Smem<N>;
     static_assert(L::kTotal + 1024 <= 232448 && L::kCols <= 512, "shared and tensor memory of a CTA");
+    int bx = 128;                                // positions of a box: a power of two that divides a page
+    while (p.page_size % bx) bx >>= 1;
+    const long long per_head = (long long)p.page_size * kRow;
+    const int page_heads = (int)(p.page_stride / per_head);
+    CUtensorMap maps[2];
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encoder());
+    const cuuint64_t dims[3] = {kRow, (cuuint64_t)p.page_size, (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv};
+    const cuuint64_t strides[2] = {kRow, (cuuint64_t)per_head};
+    const cuuint32_t box[3] = {kRow, (cuuint32_t)bx, 1}, es[3] = {1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(i ? p.v : p.k), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(attn4_mma_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal + 1024);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn4_mma_kernel<N>, dim3(p.ctas), dim3(Roles<N>::kWarps * 32), L::kTotal + 1024, s, p);
+    return launch_dependent(attn4_mma_kernel<N>, dim3(p.ctas), dim3(Roles<N>::kWarps * 32), L::kTotal + 1024, s, p, maps[0], maps[1], bx, page_heads);
 }
 
 }  // namespace
+
+bool attn4_tensor(const AttnParams& p, int rows) {
+    // pages a whole number of heads apart, all of them within a tensor map's last dimension, scales that bulk copies reach
+    const long long per_head = (long long)p.page_size * kRow;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.ks) | reinterpret_cast<uintptr_t>(p.vs) | (uintptr_t)p.scale_stride;
+    return attn4_tensor_rows(rows, p.D) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 && p.page_stride / per_head < (1LL << 31) &&
+           p.pages * (p.page_stride / per_head) < (1LL << 31) && at % 16 == 0 && tma_encoder() != nullptr;
+}
 
 cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s) { return p.row_tile == 32 ? launch<32>(p, s) : launch<64>(p, s); }
 

@@ -130,7 +130,8 @@ bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can cop
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
 // Over a cache in 4 bits, bf16 queries: above 16 rows of a key head of 128 the tensor cores
 // take them, 32 or 64 at a time (cache_attention4_mma.cu).
-inline bool attn4_tensor(int rows, int D) { return D == 128 && rows > 16; }
+inline bool attn4_tensor_rows(int rows, int D) { return D == 128 && rows > 16; }
+bool attn4_tensor(const AttnParams& p, int rows);  // and its pages can be copied by TMA
 cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s);
 // Else every warp is a worker of its own (AttnParams::ctas of them): query
 // rows at a time, and warps of a CTA for groups of 8 rows, as registers allow.

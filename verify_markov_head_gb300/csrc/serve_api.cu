@@ -275,7 +275,7 @@ size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_d
     const int all = q_heads / kv_heads * max_new, mma = attn_row_tile(all, true), simt = attn_row_tile(all, false);
     const size_t rows = mma > simt ? mma : simt;
     size_t parts = kMaxAttnCtas * rows, splits = kMaxAttnCtas;
-    if (head_dim % DSPARK_CACHE4_GROUP == 0 && !attn4_tensor(all, head_dim)) {       // and the warps over a cache in 4 bits
+    if (head_dim % DSPARK_CACHE4_GROUP == 0) {       // and the warps over a cache in 4 bits
         const size_t tile = attn4_row_tile(all, head_dim), workers = (size_t)kMaxAttnCtas * attn4_warps((int)tile / 8, head_dim);
         if (workers * tile > parts) parts = workers * tile;
         splits = workers;
@@ -379,7 +379,7 @@ dspark_status dspark_cache_attention4(const void* q, long long q_stride, dspark_
     p.by_page.set((uint32_t)page_size);
     p.by_group.set((uint32_t)p.G);
     const int rows = p.G * max_new;
-    const bool tensor = p.bf16 && attn4_tensor(rows, head_dim);
+    const bool tensor = p.bf16 && attn4_tensor(p, rows);
     p.row_tile = tensor ? (rows <= 32 ? 32 : 64) : p.bf16 ? attn4_row_tile(rows, head_dim) : attn_row_tile(rows, false);
     const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
     if (!p.bf16 && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
