@@ -352,8 +352,11 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const AttnPa
 // so the result does not depend on which CTA ended first.  Latency bounds it:
 // three dependent loads (what CTA c left, the parts' maxima and sums, the parts
 // eight at a time).
-template <typename T>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
+// kWide: heads above 128, two vectors a lane.  Without the second one the registers leave
+// room for four blocks an SM, of which there are many where every warp of the attention
+// leaves parts (a cache in 4 bits, 64 requests of 32 rows: 1216 of them, 23 us with two an SM).
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(256, kWide ? 2 : 4) attn_join_kernel(const AttnParams p) {
     if (threadIdx.x == 0) grid_launch_dependents();
     grid_dependency_wait();
     const int c = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     float l = 0.f, acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    const bool d0 = 4 * lane < p.D, d1 = 4 * lane + 128 < p.D;
+    const bool d0 = 4 * lane < p.D, d1 = kWide && 4 * lane + 128 < p.D;
     for (int i0 = 0; i0 < parts; i0 += 32) {
         // lane i weighs part i0 + i; the parts' rows are then read 8 at a time
         float w = 0.f, s = 0.f;
@@ -382,14 +385,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
         }
         const int n = min(32, parts - i0);
         for (int j0 = 0; j0 < n; j0 += 8) {
-            float4 x[8], y[8];
+            float4 x[8], y[kWide ? 8 : 1];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                x[j] = y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                x[j] = y[kWide ? j : 0] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (j0 + j < n) {
                     const float4* at = reinterpret_cast<const float4*>(p.part + place(i0 + j0 + j) * p.D) + lane;
                     if (d0) x[j] = at[0];
-                    if (d1) y[j] = at[32];
+                    if (d1) y[kWide ? j : 0] = at[32];
                 }
             }
 #pragma unroll
@@ -399,8 +402,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
                 if (wj != 0.f) {
                     acc[0] = fmaf(wj, x[j].x, acc[0]); acc[1] = fmaf(wj, x[j].y, acc[1]);
                     acc[2] = fmaf(wj, x[j].z, acc[2]); acc[3] = fmaf(wj, x[j].w, acc[3]);
-                    acc[4] = fmaf(wj, y[j].x, acc[4]); acc[5] = fmaf(wj, y[j].y, acc[5]);
-                    acc[6] = fmaf(wj, y[j].z, acc[6]); acc[7] = fmaf(wj, y[j].w, acc[7]);
+                    if (kWide) {
+                        const float4 z = y[kWide ? j : 0];
+                        acc[4] = fmaf(wj, z.x, acc[4]); acc[5] = fmaf(wj, z.y, acc[5]);
+                        acc[6] = fmaf(wj, z.z, acc[6]); acc[7] = fmaf(wj, z.w, acc[7]);
+                    }
                 }
             }
         }
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     const int tok = p.by_group(rr), head = w0.z * p.G + rr - tok * p.G;
     const size_t o0 = (size_t)(w0.y + tok) * p.Hq + head;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = 0; hf < (kWide ? 2 : 1); ++hf) {
         const int d = 4 * lane + 128 * hf;
         if (d < p.D)
 #pragma unroll
@@ -432,7 +438,9 @@ cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
-    return launch_dependent(p.bf16 ? attn_join_kernel<uint16_t> : attn_join_kernel<float>, dim3(p.ctas, (p.row_tile + 7) / 8), dim3(256), 0, s, p);
+    auto kernel = p.D > 128 ? (p.bf16 ? attn_join_kernel<uint16_t, true> : attn_join_kernel<float, true>)
+                            : (p.bf16 ? attn_join_kernel<uint16_t, false> : attn_join_kernel<float, false>);
+    return launch_dependent(kernel, dim3(p.ctas, (p.row_tile + 7) / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace

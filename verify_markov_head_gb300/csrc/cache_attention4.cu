@@ -46,7 +46,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kUnit = 32;                // positions of a unit
 constexpr float kLift = 7.f;             // log2 of a weight at the reference
 constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
+constexpr float kUnset = 1e30f;          // in place of kLift - reference before the first score: -inf + kUnset is -inf, any score is above
 
+// x * s + n, and l + w, of two columns in one instruction each.
+__device__ __forceinline__ void fma_pair(float& x0, float& x1, float s0, float s1, float n0, float n1) {
+    asm("{\n\t.reg .b64 x, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tmov.b64 n, {%4, %5};\n\t"
+        "fma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(x0), "+f"(x1) : "f"(s0), "f"(s1), "f"(n0), "f"(n1));
+}
+__device__ __forceinline__ void add_pair(float& l0, float& l1, float w0, float w1) {
+    asm("{\n\t.reg .b64 l, w;\n\tmov.b64 l, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 l, l, w;\n\tmov.b64 {%0, %1}, l;\n\t}"
+        : "+f"(l0), "+f"(l1) : "f"(w0), "f"(w1));
+}
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
         // the queries: rows scaled below 1 by a power of two, in the order in which the keys' entries are read
         uint2* const qs = reinterpret_cast<uint2*>(mine + kStages * L::kStage) + lane;
         uint2 q[L::kQRegs ? kSteps * NT : 1];
-        float by[NT][2], neg[NT][2], sum[NT][2], o[kSteps][NT][4];   // neg: kLift - reference, +inf: none yet
+        float by[NT][2], neg[NT][2], sum[NT][2], o[kSteps][NT][4];   // neg: kLift - reference
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = 8 * nt + g, rr = d.r0 + row, tok = p.by_group(rr);
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             const int e = min(max((int)(top >> 23) - 126, -100), 100);
-            const float down = __int_as_float((127 - e) << 23), up = p.scale * kLog2e * __int_as_float((127 + e) << 23);
+            const float down = __int_as_float((127 - e) << 23), up = fmaxf(p.scale * kLog2e * __int_as_float((127 + e) << 23), 1e-37f);      // (not 0, which -inf would make NaN)
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
                 const uint2 y = make_uint2(pack_half(__uint_as_float(x[j].x << 16) * down, __uint_as_float(x[j].x & 0xffff0000u) * down),
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 by[nt][c] = __shfl_sync(~0u, up, (2 * t + c) * 4);
-                neg[nt][c] = INFINITY;
+                neg[nt][c] = kUnset;
                 sum[nt][c] = 0.f;
             }
         }
@@ -343,12 +353,6 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
             // ----------------------------------------------------- weights
             // in units of log2; positions that a row does not see get -inf
             const bool masked = there != ~0u || pos0 + kUnit > d.seen;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[x][nt][c] *= by[nt][c & 1];
             if (masked) {
                 int last[NT][2];
 #pragma unroll
@@ -365,14 +369,19 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
                             if (!(there >> r & 1u) || pos0 + r > last[nt][c & 1]) s[x][nt][c] = -INFINITY;
                         }
             }
-            // does a score exceed its row's reference by more than the slack?
-            bool grown = false;
+            // does an exponent exceed its row's reference by more than the slack?
+            float high = -INFINITY;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    grown |= fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2])) + neg[nt][c] > kLift + kSlack;
-            if (__any_sync(~0u, grown)) {
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; c += 2) {
+                        float y0 = s[x][nt][c], y1 = s[x][nt][c + 1];
+                        fma_pair(y0, y1, by[nt][0], by[nt][1], neg[nt][0], neg[nt][1]);
+                        high = fmaxf(high, fmaxf(y0, y1));
+                    }
+            if (__any_sync(~0u, high > kLift + kSlack)) {
                 // the references move to the maxima so far
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -381,8 +390,8 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
                         float top = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                        const float to = fminf(neg[nt][c], kLift - top);       // (+inf while nothing is seen)
-                        const float al = neg[nt][c] == INFINITY ? 0.f : fast_exp2(to - neg[nt][c]);
+                        const float to = fminf(neg[nt][c], fmaf(-top, by[nt][c], kLift));       // (+inf while nothing is seen)
+                        const float al = neg[nt][c] == kUnset ? 0.f : fast_exp2(to - neg[nt][c]);
                         if (to != neg[nt][c]) {
                             neg[nt][c] = to;
                             sum[nt][c] *= al;
@@ -398,18 +407,16 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        // (a row that sees nothing yet: -inf + inf)
-                        const float y = s[x][nt][c] + neg[nt][c & 1];
-                        w[c] = fast_exp2(masked && s[x][nt][c] == -INFINITY ? -INFINITY : y);
-                        sum[nt][c & 1] += w[c];
+                    for (int c = 0; c < 4; c += 2) {
+                        float w0 = s[x][nt][c], w1 = s[x][nt][c + 1];
+                        fma_pair(w0, w1, by[nt][0], by[nt][1], neg[nt][0], neg[nt][1]);
+                        w0 = fast_exp2(w0);
+                        w1 = fast_exp2(w1);
+                        add_pair(sum[nt][0], sum[nt][1], w0, w1);
+                        pt[x][nt][c / 2] = transposed(pack_half(w0, w1));
                     }
-                    pt[x][nt][0] = transposed(pack_half(w[0], w[1]));
-                    pt[x][nt][1] = transposed(pack_half(w[2], w[3]));
-                }
             // -------------------------------------------------- O^T += V^T P^T
             const int word0 = g * kValWords;
             bool later = false;

@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
                 const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
                 // (a segment's first scores follow its Q tile)
-                if (s == 0) scale2 = p.scale * kLog2e * __int_as_float((127 + s_exp[slot]) << 23);
+                if (s == 0) scale2 = fmaxf(p.scale * kLog2e * __int_as_float((127 + s_exp[slot]) << 23), 1e-37f);     // (not 0, which -inf would make NaN)
                 // positions beyond the end or in a bad page, and the block's later tokens
                 const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
                 const bool gone = row >= there || (bad >> my_box & 1u);

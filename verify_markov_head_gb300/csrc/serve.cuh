@@ -130,13 +130,19 @@ bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can cop
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
 // Over a cache in 4 bits, bf16 queries: above 16 rows of a key head of 128 the tensor cores
 // take them, 32 or 64 at a time (cache_attention4_mma.cu).
-inline bool attn4_tensor_rows(int rows, int D) { return D == 128 && rows > 16; }
+#ifndef A4TR
+#define A4TR 32
+#endif
+inline bool attn4_tensor_rows(int rows, int D) { return D == 128 && rows > A4TR; }
 bool attn4_tensor(const AttnParams& p, int rows);  // and its pages can be copied by TMA
 cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s);
 // Else every warp is a worker of its own (AttnParams::ctas of them): query
 // rows at a time, and warps of a CTA for groups of 8 rows, as registers allow.
 inline int attn4_row_tile(int rows, int D) { return rows <= 8 ? 8 : rows <= 16 || D > 128 ? 16 : 32; }
-constexpr int attn4_warps(int groups, int D) { return groups == 1 && D <= 128 ? 12 : 8; }
+#ifndef A4WN
+#define A4WN 12
+#endif
+constexpr int attn4_warps(int groups, int D) { return groups == 1 && D <= 128 ? A4WN : 8; }
 cudaError_t launch_attn4_mma(const AttnParams& p, cudaStream_t s);   // bf16 queries, a cache in 4 bits
 // Rows of a row tile where a key-value head has `rows` query rows.
 inline int attn_row_tile(int rows, bool mma) {
