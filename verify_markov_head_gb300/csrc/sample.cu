@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const u64 over = above + sum([&](uint32_t k, uint32_t, u64 w) { return k <= key ? 0ull : w; });
             const u64 at = sum([&](uint32_t k, uint32_t, u64) { return k == key ? 1ull : 0ull; });
             const u64 w = mass ? max(weight.of(value_of(key)), 1ull) : 1ull, needed = (want - over + w - 1ull) / w;
-            uint32_t id = 0x7fffffffu;
+            uint32_t id = value_of(key) == last ? last_id : 0x7fffffffu;      // (where the cut before lies among the same entries, it stays)
             if (needed < at) {
                 id = 0u;                         // the id that has needed - 1 others below it
                 for (int b = 18; b >= 0; --b) {
