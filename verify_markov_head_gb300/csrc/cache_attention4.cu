@@ -25,10 +25,12 @@
 // (AttnSplit), a ring of units of 32 positions that it fills by cp.async some units
 // ahead and into its next segment, and its own maxima, sums and O^T in registers.
 // Nothing waits for another warp.  (Warps that share a segment and join at its end,
-// with one more warp to prepare the next: 236 us for 64 requests of 32 rows, now
-// 184; 225 us for 256 requests of 8 rows, now 168.)
+// with one more warp to prepare the next: 236 us for 64 requests of 2000 positions, 8
+// heads of 32 rows, now 172; 225 us for 256 requests of 8 rows, now 159.)  HBM would take
+// 51 and 93.  Of 8 rows 56 of 100 issue slots are taken, most by conversions; of 32 rows 41,
+// and what is left is latency, since 255 registers a thread leave 8 warps to an SM.
 //
-// Precision: q is scaled by a power of two to below 1 a row and held in fp16, keys and
+// Precision: each row of q is scaled by a power of two to below 1 and held in fp16, keys and
 // values are exact in fp16, products are exact and summed in fp32.  Weights are
 // fp16, 2^(s - ref + 7): the reference of a row moves when a score exceeds it by
 // more than 8, so the largest lies between 2^7 and 2^15, and one of 2^-21 of the
@@ -46,12 +48,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kUnit = 32;                // positions of a unit
 constexpr float kLift = 7.f;             // log2 of a weight at the reference
 constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
-constexpr float kUnset = 1e30f;          // in place of kLift - reference before the first score: -inf + kUnset is -inf, any score is above
+constexpr float kUnset = -3.4e38f;       // a reference before the first score: -inf less it is -inf, and any score is above
 
-// x * s + n, and l + w, of two columns in one instruction each.
-__device__ __forceinline__ void fma_pair(float& x0, float& x1, float s0, float s1, float n0, float n1) {
-    asm("{\n\t.reg .b64 x, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tmov.b64 n, {%4, %5};\n\t"
-        "fma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(x0), "+f"(x1) : "f"(s0), "f"(s1), "f"(n0), "f"(n1));
+// (x - r) * s + n, and l + w, of two columns.  (The difference first: of large scores a
+// product that is rounded by itself and one that is not would differ by whole units.)
+__device__ __forceinline__ void exponent_pair(float& x0, float& x1, float r0, float r1, float s0, float s1, float n) {
+    asm("{\n\t.reg .b64 x, r, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 r, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\tmov.b64 n, {%6, %6};\n\t"
+        "sub.rn.f32x2 x, x, r;\n\tfma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(x0), "+f"(x1) : "f"(r0), "f"(r1), "f"(s0), "f"(s1), "f"(n));
 }
 __device__ __forceinline__ void add_pair(float& l0, float& l1, float w0, float w1) {
     asm("{\n\t.reg .b64 l, w;\n\tmov.b64 l, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 l, l, w;\n\tmov.b64 {%0, %1}, l;\n\t}"
@@ -96,7 +100,7 @@ struct Layout {
     static constexpr int kSteps = DP / 16;                        // of 16 entries
     static constexpr bool kQRegs = NT * kSteps <= 16;             // Q in registers
     static constexpr int kStage = 2 * kUnit * (DP / 2 + DP / 16);    // bytes of a unit, and room for every head size below
-    static constexpr int kStages = DP == 256 ? (NT == 1 ? 3 : 2) : 3;
+    static constexpr int kStages = DP == 256 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3;
     static constexpr int kQ = kQRegs ? 0 : kSteps * NT * 32 * 8;  // bytes of a Q tile
     static constexpr int kWarpBytes = kStages * kStage + kQ;
     static constexpr int kTotal = kWarps * kWarpBytes;
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
         // the queries: rows scaled below 1 by a power of two, in the order in which the keys' entries are read
         uint2* const qs = reinterpret_cast<uint2*>(mine + kStages * L::kStage) + lane;
         uint2 q[L::kQRegs ? kSteps * NT : 1];
-        float by[NT][2], neg[NT][2], sum[NT][2], o[kSteps][NT][4];   // neg: kLift - reference
+        float by[NT][2], ref[NT][2], sum[NT][2], o[kSteps][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = 8 * nt + g, rr = d.r0 + row, tok = p.by_group(rr);
@@ -245,8 +249,9 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
             top = max(top << 16, top & 0xffff0000u);
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
-            const int e = min(max((int)(top >> 23) - 126, -100), 100);
-            const float down = __int_as_float((127 - e) << 23), up = fmaxf(p.scale * kLog2e * __int_as_float((127 + e) << 23), 1e-37f);      // (not 0, which -inf would make NaN)
+            const int e = min(max((int)(top >> 23) - 126, -126), 126);
+            const float down = __int_as_float((127 - e) << 23), 
+                        up = fminf(fmaxf(p.scale * kLog2e * __int_as_float((127 + e) << 23), 1e-37f), 3e38f);      // (neither 0 nor inf, which -inf and 0 would make NaN)
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
                 const uint2 y = make_uint2(pack_half(__uint_as_float(x[j].x << 16) * down, __uint_as_float(x[j].x & 0xffff0000u) * down),
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 by[nt][c] = __shfl_sync(~0u, up, (2 * t + c) * 4);
-                neg[nt][c] = kUnset;
+                ref[nt][c] = kUnset;
                 sum[nt][c] = 0.f;
             }
         }
@@ -372,16 +377,13 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
             // does an exponent exceed its row's reference by more than the slack?
             float high = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; c += 2) {
-                        float y0 = s[x][nt][c], y1 = s[x][nt][c + 1];
-                        fma_pair(y0, y1, by[nt][0], by[nt][1], neg[nt][0], neg[nt][1]);
-                        high = fmaxf(high, fmaxf(y0, y1));
-                    }
-            if (__any_sync(~0u, high > kLift + kSlack)) {
+            for (int nt = 0; nt < NT; ++nt) {
+                float y0 = fmaxf(fmaxf(s[0][nt][0], s[0][nt][2]), fmaxf(s[1][nt][0], s[1][nt][2]));
+                float y1 = fmaxf(fmaxf(s[0][nt][1], s[0][nt][3]), fmaxf(s[1][nt][1], s[1][nt][3]));
+                exponent_pair(y0, y1, ref[nt][0], ref[nt][1], by[nt][0], by[nt][1], 0.f);
+                high = fmaxf(high, fmaxf(y0, y1));
+            }
+            if (__any_sync(~0u, high > kSlack)) {
                 // the references move to the maxima so far
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -390,10 +392,10 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
                         float top = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                        const float to = fminf(neg[nt][c], fmaf(-top, by[nt][c], kLift));       // (+inf while nothing is seen)
-                        const float al = neg[nt][c] == kUnset ? 0.f : fast_exp2(to - neg[nt][c]);
-                        if (to != neg[nt][c]) {
-                            neg[nt][c] = to;
+                        const float to = fmaxf(ref[nt][c], top);
+                        const float al = ref[nt][c] == kUnset ? 0.f : fast_exp2((ref[nt][c] - to) * by[nt][c]);
+                        if (to != ref[nt][c]) {
+                            ref[nt][c] = to;
                             sum[nt][c] *= al;
 #pragma unroll
                             for (int m = 0; m < kSteps; ++m) {
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
 #pragma unroll
                     for (int c = 0; c < 4; c += 2) {
                         float w0 = s[x][nt][c], w1 = s[x][nt][c + 1];
-                        fma_pair(w0, w1, by[nt][0], by[nt][1], neg[nt][0], neg[nt][1]);
+                        exponent_pair(w0, w1, ref[nt][0], ref[nt][1], by[nt][0], by[nt][1], kLift);
                         w0 = fast_exp2(w0);
                         w1 = fast_exp2(w1);
                         add_pair(sum[nt][0], sum[nt][1], w0, w1);
@@ -501,7 +503,8 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
                 if (row >= d.rows) continue;
                 const int rr = d.r0 + row, tok = p.by_group(rr);
                 const bool whole = d.slot < 0;
-                // (relative to the reference less kLift: -neg; of a row that saw nothing -inf)
+                // (weights are relative to the reference less kLift; of a row that saw nothing -inf)
+                const float base = ref[nt][c] == kUnset ? -INFINITY : fmaf(ref[nt][c], by[nt][c], -kLift);
                 const size_t at = whole ? (size_t)(d.q0 + tok) * p.Hq + d.h * p.G + rr - tok * p.G : (size_t)d.slot * p.row_tile + row;
                 const float f = whole ? (l != 0.f ? p.out_by / l : 0.f) : p.out_by;
 #pragma unroll
@@ -526,8 +529,8 @@ __global__ void __launch_bounds__(Layout<NT, DP>::kWarps * 32, 1) attn4_kernel(c
                     }
                 }
                 if (g == 0) {
-                    if (!whole) *reinterpret_cast<float2*>(part_stats(p) + at * 2) = make_float2(-neg[nt][c], l);
-                    else if (p.lse) p.lse[at] = l != 0.f ? logf(l) - neg[nt][c] * kLn2 : -INFINITY;
+                    if (!whole) *reinterpret_cast<float2*>(part_stats(p) + at * 2) = make_float2(base, l);
+                    else if (p.lse) p.lse[at] = l != 0.f ? fmaf(base, kLn2, logf(l)) : -INFINITY;
                 }
             }
     }

@@ -1,28 +1,36 @@
 // cache_attention4_mma.cu -- attention over a paged cache held in 4 bits on the
-// tensor cores: bf16 queries, head size 128, more than 16 query rows a key-value
+// tensor cores: bf16 queries, head size 128, more than 32 query rows a key-value
 // head (formulas: cache_attention.cu; formats: fp4.cuh; fewer rows and other head
 // sizes: cache_attention4.cu).
 //
 // Both products are taken transposed, 128 cache positions at a time:
-//     S^T [128 positions x N] = K [128 x 128] . Q^T       (A: K, B: Q)
-//     O^T [128 entries x N]  += V^T [128 x 128] . P^T     (A: V^T, B: P)
+//     S^T [128 positions x 64] = K [128 x 128] . Q^T       (A: K, B: Q)
+//     O^T [128 entries x 64]  += V^T [128 x 128] . P^T     (A: V^T, B: P)
 // with A in tensor memory.  The codes (18 KB for 128 positions) come to shared memory
-// by cp.async; eight warps turn them into fp16 in registers, exactly, and write
+// by TMA; eight warps turn them into fp16 in registers, exactly, and write
 // them straight into tensor memory, as the rows of A: 64 KB that do not cross shared
 // memory, where the products would read them at 64 bytes a cycle (cache_attention_mma.cu).
 //   keys     a lane of A is a position: a thread takes its 64 bytes of codes and 8
-//            scales; rows of 80 bytes in shared memory keep its reads apart
+//            scales; TMA's 64-byte swizzle keeps the threads' reads apart
 //   values   a lane of A is an entry of the head: a thread takes 4 entries of four
 //            positions at a time, pairs the positions' nibbles (4 operations for 16
 //            entries) and writes fragments of 16 lanes.  Position r of 16 is the
 //            product's step 2r mod 8 + ..: P's rows are written in that order.
+// The products are issued in a fixed order, S of a step and O of the step before, with two
+// buffers of P, so that the softmax of a step runs beside them.
 // The softmax, the segments and the split over CTAs are cache_attention_mma.cu's; weights
 // are fp16, 2^(s - ref + 7), as in cache_attention4.cu, whose notes on precision hold
-// here too, except that the rows of a tile share the power of two that q is scaled by.
+// here too, except that the rows of a tile share the power of two that q is scaled by: to
+// below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of the tile's largest.
 //
-// Roles (24 warps, 28 with 64 columns, one CTA per SM):
-//   first 8 or 16    softmax: groups of 4 warps, 16 columns each; thread = position
-//   then 12 or 8     four keys, the others values: codes to tensor memory (warp & 3 = its 32 lanes)
+// One request of 131072 positions, 8 heads of 8 rows each: 127 us, of them 9 the join (with
+// registers dequantising for mma.sync 169; one buffer of P 145).  HBM would take 22 and the
+// products 15: it is the issue of instructions that bounds it (55 of 100 slots, by 24
+// warps that wait on one another: conversions a third of them, softmax a half).
+//
+// Roles (28 warps, one CTA per SM):
+//   first 16         softmax: groups of 4 warps, 16 columns each; thread = position
+//   then 8           four keys, four values: codes to tensor memory (warp & 3 = its 32 lanes)
 //   then two         copies of the keys' and of the values' codes and scales
 //   one              MMA issuer, one more the segments and Q tiles
 #include <cudaTypedefs.h>
@@ -39,8 +47,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSteps = 128;              // positions per step
 constexpr int kDim = 128;                // head size
+constexpr int N = 64;                    // query rows of a tile: columns of the products
 constexpr int kSegs = 8;                 // segment descriptors in flight
 constexpr int kBadRing = 16;             // steps the copies may be ahead of the softmax, and more
+constexpr int kQTop = 15;                // queries are scaled to below 2^kQTop
 constexpr float kLift = 7.f;             // log2 of a weight at the reference
 constexpr float kSlack = 8.f;            // log2 of the growth of a maximum that is let pass
 constexpr long long kDrainCycles = 200000000LL;
@@ -51,10 +61,9 @@ constexpr int kStages = 6;               // of keys, and of values
 constexpr int kTiles = 4;                // A tiles in tensor memory: keys 0 and 2, values 1 and 3
 constexpr int kTileCols = kDim / 2;      // columns of one
 
-template <int N>
 struct Roles {
     static constexpr int HC = 16;                 // columns of a softmax group
-    static constexpr int kSoftWarps = 4 * (N / HC), kValWarps = N == 32 ? 8 : 4;
+    static constexpr int kSoftWarps = 4 * (N / HC), kValWarps = 4;
     static constexpr int kKeyWarp = kSoftWarps, kValWarp = kKeyWarp + 4, kCopyWarp = kValWarp + kValWarps;
     static constexpr int kMmaWarp = kCopyWarp + 2, kSegWarp = kCopyWarp + 3, kWarps = kCopyWarp + 4;
 };
@@ -67,7 +76,6 @@ struct Seg {
     int slot;                 // -1: the whole segment, else the partial result's slot
 };
 
-template <int N>
 struct Smem {
     static constexpr int kQBytes = N * kDim * 2, kQBufs = 2;
     static constexpr int kCols = 4 * N + kTiles * kTileCols;      // tensor memory: two S, two O, the A tiles
@@ -102,36 +110,27 @@ __device__ __forceinline__ uint32_t elect_one() {
     return r;
 }
 
-// N columns of 32 lanes, waited for.
-template <int C> __device__ __forceinline__ void tmem_get(uint32_t a, float (&v)[C]);
-template <> __device__ __forceinline__ void tmem_get<8>(uint32_t a, float (&v)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-                 : "r"(a) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_get<16>(uint32_t a, float (&v)[16]) {
+// 16 columns of 32 lanes, waited for.
+__device__ __forceinline__ void tmem_get(uint32_t a, float (&v)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  "\n\ttcgen05.wait::ld.sync.aligned;"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
                    "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
                  : "r"(a) : "memory");
 }
-template <int C> __device__ __forceinline__ void tmem_put(uint32_t a, const float (&v)[C]);
-template <> __device__ __forceinline__ void tmem_put<8>(uint32_t a, const float (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;"
-                 ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_put<16>(uint32_t a, const float (&v)[16]) {
+__device__ __forceinline__ void tmem_put(uint32_t a, const float (&v)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  "\n\ttcgen05.wait::st.sync.aligned;"
                  ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
                    "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
 }
 
-// x * s + n, and l + w, of two columns in one instruction each.
-__device__ __forceinline__ void fma_pair(float& x0, float& x1, float s, float n0, float n1) {
-    asm("{\n\t.reg .b64 x, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 n, {%3, %4};\n\t"
-        "fma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(x0), "+f"(x1) : "f"(s), "f"(n0), "f"(n1));
+// (x - r) * s + n, and l + w, of two columns.  (The difference first: of large scores a
+// product that is rounded by itself and one that is not would differ by whole units.)
+__device__ __forceinline__ void exponent_pair(float& x0, float& x1, float r0, float r1, float s, float n) {
+    asm("{\n\t.reg .b64 x, r, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 r, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 n, {%5, %5};\n\t"
+        "sub.rn.f32x2 x, x, r;\n\tfma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(x0), "+f"(x1) : "f"(r0), "f"(r1), "f"(s), "f"(n));
 }
 __device__ __forceinline__ void add_pair(float& l0, float& l1, float w0, float w1) {
     asm("{\n\t.reg .b64 l, w;\n\tmov.b64 l, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 l, l, w;\n\tmov.b64 {%0, %1}, l;\n\t}"
@@ -175,10 +174,9 @@ constexpr uint32_t idesc_half(int N, bool b_mn_major) {
     return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-template <int N>
-__global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const int bx, const int page_heads) {
-    using L = Smem<N>;
-    using R = Roles<N>;
+__global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const int bx, const int page_heads) {
+    using L = Smem;
+    using R = Roles;
     constexpr int kSoftWarps = R::kSoftWarps, HC = R::HC;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
             }
             __syncwarp();
             if (d.steps < 0) break;
-            // the Q tile, scaled by a power of two to below 1, rows beyond the request's as zeros
+            // the Q tile, scaled by a power of two to below 2^kQTop, rows beyond the request's as zeros
             const int qb = si % L::kQBufs;
             if (si >= L::kQBufs) ok = wait_all(b_q_empty + 8 * qb, (si / L::kQBufs) - 1);
             if (!ok) { if (lane == 0) give_up(1); break; }
@@ -288,7 +286,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
             }
             top = __reduce_max_sync(~0u, max(top << 16, top & 0xffff0000u));
-            const int e = min(max((int)(top >> 23) - 126, -100), 100);
+            const int e = min(max((int)(top >> 23) - 126 - kQTop, -126), 126);
             const float down = __int_as_float((127 - e) << 23);
             const uint32_t to = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
 #pragma unroll 8
@@ -364,7 +362,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
         __syncwarp();
     } else if (warp >= R::kKeyWarp && warp < R::kCopyWarp) {
         // ------------------------------------------------ codes to tensor memory
-        const int kv = warp >= R::kValWarp, quarter = warp & 3, part = kv ? (warp - R::kValWarp) >> 2 : 0, g = lane >> 2, t = lane & 3;
+        const int kv = warp >= R::kValWarp, quarter = warp & 3, g = lane >> 2, t = lane & 3;
         uint32_t step = 0;
         bool ok = true;
         for (int si = 0; ok; ++si) {
@@ -407,12 +405,12 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                     }
                 } else {
                     // entries 32 * quarter + 4 g .. + 3 of positions t, t + 4, t + 8, t + 12 of each 16
-                    constexpr int kMine = kSteps / 16 * 4 / R::kValWarps;        // sixteens of this warp
+                    constexpr int kMine = kSteps / 16;                   // sixteens
                     // (rows t and t + 8 swap their chunks alike, t + 4 and t + 12 the other way)
-                    const uint8_t* mine = st + (16 * kMine * part + t) * kRow + 2 * g;
+                    const uint8_t* mine = st + t * kRow + 2 * g;
                     const int even_at = 16 * (quarter ^ (t >> 1)), odd_at = 16 * (quarter ^ (t >> 1) ^ 2);
-                    const uint8_t* sc = st + kCodes + (16 * kMine * part + t) * 8 + 2 * quarter + (g >> 2);
-                    const int first = 16 * kMine * part + t, later = s_later[stage], there = s_there[2 * stage], stop = s_there[2 * stage + 1];
+                    const uint8_t* sc = st + kCodes + t * 8 + 2 * quarter + (g >> 2);
+                    const int later = s_later[stage], there = s_there[2 * stage], stop = s_there[2 * stage + 1];
                     const bool edge = later < kSteps || stop < kSteps || there != (1 << kSteps / bx) - 1;
 #pragma unroll 2
                     for (int k = 0; k < kMine; ++k, mine += 16 * kRow, sc += 16 * 8) {
@@ -428,7 +426,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                             // here and added at the segment's end
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const int r = first + 16 * k + 4 * i;
+                                const int r = t + 16 * k + 4 * i;
                                 if (r >= stop || !(there >> r / bx & 1)) b[i] = 0u;
                                 else if (r >= later && (b[i] & 0x7fu) == 0x7fu) { b[i] = 0u; s_flags[2] = 1u; }
                             }
@@ -439,7 +437,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                         uint32_t even[4], odd[4];            // [entry / 2 + 2 * half of the 16 positions]
                         fp4::unpack((a & 0x0f0f0f0fu) | (c << 4 & 0xf0f0f0f0u), even);
                         fp4::unpack((a >> 4 & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u), odd);
-                        const uint32_t to = at + 8 * (kMine * part + k);
+                        const uint32_t to = at + 8 * k;
                         tmem_put_16x128b(to, fp4::mul2(even[0], s0), fp4::mul2(odd[0], s0), fp4::mul2(even[2], s1), fp4::mul2(odd[2], s1));
                         tmem_put_16x128b(to + (16u << 16), fp4::mul2(even[1], s0), fp4::mul2(odd[1], s0), fp4::mul2(even[3], s1), fp4::mul2(odd[3], s1));
                     }
@@ -535,7 +533,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
         // (its O^T is in the other half of tensor memory), so the tensor core
         // and the producers go on meanwhile.  What is kept of it until then:
         bool pend = false;
-        float pend_ref = 0.f;                                      // lane c: column c's reference
+        float pend_ref = 0.f;                                      // lane c: column c's reference, in units of log2
         for (uint32_t si = 0;; ++si) {
             const int slot = si % kSegs;
             ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
@@ -548,9 +546,9 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
             const int first_new = d.len - d.n;                     // position of the block's first token
             // lane c: the last position that column c of this group sees
             const int my_last = first_new + p.by_group(d.r0 + group * HC + (lane & (HC - 1)));
-            float neg[HC], l[HC], scale2 = 0.f;                    // kLift less the reference, this thread's sum of the weights
+            float ref[HC], l[HC], scale2 = 0.f;                    // the references (of scores before the scale), this thread's sum of the weights
 #pragma unroll
-            for (int c = 0; c < HC; ++c) neg[c] = l[c] = 0.f;
+            for (int c = 0; c < HC; ++c) ref[c] = l[c] = 0.f;
             float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
             bool unset = true;                                     // a column of the group has no reference yet
             bool stop = false;
@@ -562,7 +560,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
                 const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
                 // (a segment's first scores follow its Q tile)
-                if (s == 0) scale2 = fmaxf(p.scale * kLog2e * __int_as_float((127 + s_exp[slot]) << 23), 1e-37f);     // (not 0, which -inf would make NaN)
+                if (s == 0) scale2 = fminf(fmaxf(p.scale * kLog2e * __int_as_float((127 + s_exp[slot]) << 23), 1e-37f), 3e38f);     // (neither 0 nor inf, which -inf and 0 would make NaN)
                 // positions beyond the end or in a bad page, and the block's later tokens
                 const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
                 const bool gone = row >= there || (bad >> my_box & 1u);
@@ -570,7 +568,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 // the scores, -inf where the column does not see the position (read
                 // again where a reference moves)
                 auto scores = [&]() {
-                    if (ok) tmem_get<HC>(s_at, x);
+                    if (ok) tmem_get(s_at, x);
                     else {
 #pragma unroll
                         for (int c = 0; c < HC; ++c) x[c] = 0.f;
@@ -586,7 +584,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 // .. as exponents
                 auto exponents = [&]() {
 #pragma unroll
-                    for (int c = 0; c < HC; c += 2) fma_pair(x[c], x[c + 1], scale2, neg[c], neg[c + 1]);
+                    for (int c = 0; c < HC; c += 2) exponent_pair(x[c], x[c + 1], ref[c], ref[c + 1], scale2, kLift);
                 };
                 ptx::tc_fence_after();
                 float high = -INFINITY;
@@ -614,9 +612,9 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                     if (lane < HC) mx[lane * 4 + quarter] = mine;
                     if (ptx::bar_red_or(1 + group, 128, !ok)) { stop = true; break; }
                     const float4 w4 = reinterpret_cast<const float4*>(mx)[lane & (HC - 1)];
-                    const float top = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) * scale2;
+                    const float top = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w));
                     const float to = fmaxf(my_ref, top);
-                    const float my_a = to > my_ref ? fast_exp2(my_ref - to) : 1.f;
+                    const float my_a = to > my_ref ? fast_exp2((my_ref - to) * scale2) : 1.f;
                     my_ref = to;
                     unset = __any_sync(~0u, to == -INFINITY);
                     if (s > 0) ptx::tc_fence_after();
@@ -625,15 +623,15 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                     for (int c = 0; c < HC; ++c) {
                         a[c] = __shfl_sync(~0u, my_a, c);
                         const float r = __shfl_sync(~0u, to, c);
-                        neg[c] = r == -INFINITY ? 0.f : kLift - r;
+                        ref[c] = r == -INFINITY ? 0.f : r;
                         l[c] *= a[c];
                     }
                     if (s > 0) {
                         float o[HC];
-                        tmem_get<HC>(o_at, o);
+                        tmem_get(o_at, o);
 #pragma unroll
                         for (int c = 0; c < HC; ++c) o[c] *= a[c];
-                        tmem_put<HC>(o_at, o);
+                        tmem_put(o_at, o);
                     }
                     exponents();
                 }
@@ -679,7 +677,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
                 const float pend_sum = (s4.x + s4.y) + (s4.z + s4.w), e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
                 ptx::tc_fence_after();
                 float o[HC];
-                if (ok) tmem_get<HC>(tmem + lanes + (2 + (pi & 1u)) * N + group * HC, o);
+                if (ok) tmem_get(tmem + lanes + (2 + (pi & 1u)) * N + group * HC, o);
                 else {
 #pragma unroll
                     for (int c = 0; c < HC; ++c) o[c] = 0.f;
@@ -744,7 +742,7 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
             }
             if (lane < HC) sm[lane * 4 + quarter] = l[0];
             pend = true;
-            pend_ref = my_ref;
+            pend_ref = my_ref * scale2;
         }
         if (!ok && lane == 0) give_up(5);
     }
@@ -754,28 +752,6 @@ __global__ void __launch_bounds__(Roles<N>::kWarps * 32, 1) attn4_mma_kernel(con
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == R::kMmaWarp) ptx::tmem_dealloc(tmem, L::kTmem);
-}
-
-template <int N>
-cudaError_t launch(const AttnParams& p, cudaStream_t s) {
-    using L = Smem<N>;
-    static_assert(L::kTotal + 1024 <= 232448 && L::kCols <= 512, "shared and tensor memory of a CTA");
-    int bx = 128;                                // positions of a box: a power of two that divides a page
-    while (p.page_size % bx) bx >>= 1;
-    const long long per_head = (long long)p.page_size * kRow;
-    const int page_heads = (int)(p.page_stride / per_head);
-    CUtensorMap maps[2];
-    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encoder());
-    const cuuint64_t dims[3] = {kRow, (cuuint64_t)p.page_size, (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv};
-    const cuuint64_t strides[2] = {kRow, (cuuint64_t)per_head};
-    const cuuint32_t box[3] = {kRow, (cuuint32_t)bx, 1}, es[3] = {1, 1, 1};
-    for (int i = 0; i < 2; ++i)
-        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(i ? p.v : p.k), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(attn4_mma_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal + 1024);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(attn4_mma_kernel<N>, dim3(p.ctas), dim3(Roles<N>::kWarps * 32), L::kTotal + 1024, s, p, maps[0], maps[1], bx, page_heads);
 }
 
 }  // namespace
@@ -788,6 +764,25 @@ bool attn4_tensor(const AttnParams& p, int rows) {
            p.pages * (p.page_stride / per_head) < (1LL << 31) && at % 16 == 0 && tma_encoder() != nullptr;
 }
 
-cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s) { return p.row_tile == 32 ? launch<32>(p, s) : launch<64>(p, s); }
+cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s) {
+    using L = Smem;
+    static_assert(L::kTotal + 1024 <= 232448 && L::kCols <= 512, "shared and tensor memory of a CTA");
+    int bx = kTile;                              // positions of a box: a power of two that divides a page and a tile, where steps begin
+    while (p.page_size % bx) bx >>= 1;
+    const long long per_head = (long long)p.page_size * kRow;
+    const int page_heads = (int)(p.page_stride / per_head);
+    CUtensorMap maps[2];
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encoder());
+    const cuuint64_t dims[3] = {kRow, (cuuint64_t)p.page_size, (cuuint64_t)(p.pages - 1) * page_heads + p.Hkv};
+    const cuuint64_t strides[2] = {kRow, (cuuint64_t)per_head};
+    const cuuint32_t box[3] = {kRow, (cuuint32_t)bx, 1}, es[3] = {1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(i ? p.v : p.k), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(attn4_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal + 1024);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn4_mma_kernel, dim3(p.ctas), dim3(Roles::kWarps * 32), L::kTotal + 1024, s, p, maps[0], maps[1], bx, page_heads);
+}
 
 }  // namespace dspark

@@ -128,21 +128,18 @@ cudaError_t launch_cache_attention(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_cache_attention4(const AttnParams& p, bool tensor, cudaStream_t s);
 bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can copy
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
-// Over a cache in 4 bits, bf16 queries: above 16 rows of a key head of 128 the tensor cores
-// take them, 32 or 64 at a time (cache_attention4_mma.cu).
-#ifndef A4TR
-#define A4TR 32
-#endif
-inline bool attn4_tensor_rows(int rows, int D) { return D == 128 && rows > A4TR; }
+// Over a cache in 4 bits, bf16 queries: above 32 rows of a key head of 128 the tensor cores
+// take them, 64 at a time (cache_attention4_mma.cu).  One request of 131072 positions, 64 rows:
+// 127 us, and 169 where registers dequantise; 64 requests of 32 rows: 195, and 175.
+inline bool attn4_tensor_rows(int rows, int D) { return D == 128 && rows > 32; }
 bool attn4_tensor(const AttnParams& p, int rows);  // and its pages can be copied by TMA
 cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s);
 // Else every warp is a worker of its own (AttnParams::ctas of them): query
-// rows at a time, and warps of a CTA for groups of 8 rows, as registers allow.
+// rows at a time, and warps of a CTA for groups of 8 rows, as registers allow (8 rows a
+// request, 256 requests: 12 warps 159 us, 16 of them with rings of 3 units 156; but one
+// request, whose parts the join reads, 11.0 and 12.3).
 inline int attn4_row_tile(int rows, int D) { return rows <= 8 ? 8 : rows <= 16 || D > 128 ? 16 : 32; }
-#ifndef A4WN
-#define A4WN 12
-#endif
-constexpr int attn4_warps(int groups, int D) { return groups == 1 && D <= 128 ? A4WN : 8; }
+constexpr int attn4_warps(int groups, int D) { return groups == 1 && D <= 128 ? 12 : 8; }
 cudaError_t launch_attn4_mma(const AttnParams& p, cudaStream_t s);   // bf16 queries, a cache in 4 bits
 // Rows of a row tile where a key-value head has `rows` query rows.
 inline int attn_row_tile(int rows, bool mma) {
