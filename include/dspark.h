@@ -100,8 +100,9 @@ dspark_status dspark_workspace_set_wait_limit(void* ws, size_t ws_bytes, uint64_
  * raw status bits are stored there: bit 0 a token out of [0, V), bit 1 a
  * block length out of [0, gamma], bit 2 a bounded wait expired, bit 3 a
  * non-finite score or a temperature that is not positive and finite
- * (dspark_sts_fit), bit 4 a row of logits with no token left
- * (dspark_logits_process), bit 5 a page or slot out of range, a block table
+ * (dspark_sts_fit), or an entry or setting that is no number
+ * (dspark_sample), bit 4 a row of logits with no token left
+ * (dspark_logits_process, dspark_sample), bit 5 a page or slot out of range, a block table
  * too narrow or no free page left (the cache calls), and with bit 2 the bits 8-23 name the wait that gave up
  * (for diagnosis only). */
 dspark_status dspark_sync_status(void* ws, void* stream, uint32_t* bits);
@@ -524,12 +525,12 @@ dspark_status dspark_cache_attention(
  *     code  = the level nearest to x * 2^-exp / scale (0 where the scale is 0)
  * (nearest, ties to the even number; entries beyond 6 scales become 6 scales,
  * infinite ones among them).  A group with a NaN gets a scale that is NaN: it
- * reads as NaN.
+ * reads as NaN.  No slot may appear twice.
  * dspark_cache_read4: the entries of the slots slot_map, in k_t (exact in bf16
  * and fp32 as far as their range goes); a negative slot leaves its row as it
  * was, one beyond the cache too, and sets status bit 5.
- * Limits : head_dim % DSPARK_CACHE4_GROUP == 0, <= DSPARK_MAX_HEAD_DIM; rows at
- *          multiples of 16 bytes, k_cache, v_cache and page_stride of 8, the rest as dspark_cache_append.
+ * Limits : head_dim % DSPARK_CACHE4_GROUP == 0, <= DSPARK_MAX_HEAD_DIM; k, v and their
+ *          strides multiples of 16 bytes, k_cache, v_cache and page_stride of 8.  ws as in dspark_cache_plan.
  */
 #define DSPARK_CACHE4_GROUP 16
 #define DSPARK_CACHE4_MAX_EXP 64
@@ -548,12 +549,16 @@ dspark_status dspark_cache_read4(
  * dspark_cache_attention over a cache held in 4 bits (layout above): the same
  * rows, masks, checks, status bits and workspace.  q and out are fp32 or bf16
  * (q_t).  Keys and values take part as the values they stand for.  In bf16
- * calls a row of q is scaled by a power of two and held in fp16 (entries below
- * 2^-14 of the row's largest to 2^-25 of it), the softmax's weights are rounded
+ * calls q is scaled by powers of two and held in fp16: of head_dim 128 with max_new *
+ * q_heads / kv_heads above 32 in tiles of 64 rows (exact down to 2^-29 of a tile's
+ * largest entry, smaller ones to 2^-40 of it), else row by row (down to 2^-14 of the
+ * row's largest, smaller ones to 2^-25 of it).  The softmax's weights are rounded
  * to fp16 (2^-11 of each, those below 2^-21 of the row's largest to 2^-31 of it);
  * products are exact and sums in fp32.  fp32 calls hold everything in fp32.
- * Limits : as dspark_cache_attention, head_dim % DSPARK_CACHE4_GROUP == 0;
- *          codes at multiples of 16 bytes from page to page, scales of 4.
+ * Limits : as dspark_cache_attention, head_dim % DSPARK_CACHE4_GROUP == 0, scale *
+ *          2^k_exp positive and finite; k_cache, v_cache and page_stride multiples of the largest
+ *          power of two up to 16 that divides a row of head_dim / 2 bytes, k_scale,
+ *          v_scale and scale_stride of the largest that divides one of head_dim / 16.
  */
 dspark_status dspark_cache_attention4(
     const void* q, long long q_stride, dspark_dtype q_t,
@@ -647,17 +652,18 @@ dspark_status dspark_logits_process(
  * and the token is the first id, in ascending order, at which the sum of the
  * weights left exceeds u[n] times their total; logprob = ln of its weight's
  * share.  temperature 0: the row's largest entry (the lowest id), logprob 0.
- * Weights are formed to about 2^-32 of each and summed as integers of 2^-42 of
- * the largest, so the result does not depend on the order of the sums.
+ * Weights are formed to about 2^-31 of each and summed as integers of 2^-42 of
+ * the largest (a smaller one counts 0), so the result does not depend on the order of the sums.
  * Inputs : logits [N][V] (t), row_stride elements between rows; u [N] fp32 in
  *          [0, 1) (taken into that range; NaN as 0); temperature [N] (NULL: 1),
  *          top_k [N] int32, top_p, min_p [N] fp32 (NULL: all).  A
  *          temperature that is negative or not finite counts as 0, a NaN in top_p or min_p as
- *          off, and both set status bit 3.
- * Outputs: tok [N]; logprob [N] or NULL.
+ *          off, and both set status bit 3.  (A temperature above 0 is taken into
+ *          10^-30 .. 10^36.)
+ * Outputs: tok [N]; logprob [N] or NULL.  They overlap no input and not each other.
  * Entries that are NaN or +inf are left out and set status bit 3.  A row of
  * which nothing is left gets token -1 and logprob -inf, and sets bit 4.
- * ws     : dspark_sample_workspace_bytes(N) bytes, 256-byte aligned, cleared once.
+ * ws     : dspark_sample_workspace_bytes(N) bytes, 256-byte aligned, cleared once; it holds the status alone.
  * Limits : 1 <= V <= DSPARK_MAX_SAMPLE_VOCAB; logits and row strides multiples of 16
  *          bytes; 0 <= N <= DSPARK_MAX_SAMPLE_ROWS.
  */

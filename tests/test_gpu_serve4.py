@@ -552,3 +552,220 @@ def test_a_step_in_a_graph_on_another_stream(vm):
     for ws in (eager["ws"], eager["lws"], eager["sws"]):
         assert _status(vm, ws) == 0
     del lse
+
+
+# ------------------------------------------------- attention on the tensor cores
+def test_many_rows_of_128_with_pages_of_any_kind(vm):
+    """More than 32 rows a key head: pages that whole copies take (multiples of 8
+    positions), others, and pages with room between them."""
+    rng = np.random.default_rng(21)
+    D, new, lens = 128, 5, [700, 130, 64, 9, 5]
+    n_new = np.array([5, 2, 4, 1, 3])
+    q_off = np.concatenate([[0], np.cumsum(n_new)])
+    q = torch.from_numpy(rng.standard_normal((int(q_off[-1]) + 2, 22, D))).to(BF16).cuda()
+    for P in (8, 24, 40, 128, 256, 1, 12, 20):
+        pages, table = _case(rng, len(lens), P, lens, D, 2)
+        arrays = _cache(rng, pages, 2, P, D)
+        _poison(arrays, table, lens, P)
+        got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, new)
+        assert status == 0
+        _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), got, lse)
+        # keys' and values' pages in turn, and pages a little further apart than they are long
+        tile_off = np.concatenate([[0], np.cumsum(-(-np.asarray(lens) // 64))])
+        args = (_cu(table), _cu(lens), _cu(q_off), _cu(tile_off))
+        for gap in (0, 64):
+            kv = torch.full((pages, 2 * 2 * P * 64 + gap), 0xFF, dtype=torch.uint8, device="cuda")
+            sc = torch.full((pages, 2 * 2 * P * 8 + gap), 0xFF, dtype=torch.uint8, device="cuda")
+            views = []
+            for i, (store, w) in enumerate(((kv, 64), (kv, 64), (sc, 8), (sc, 8))):
+                at = (i % 2) * 2 * P * w
+                view = store[:, at:at + 2 * P * w].unflatten(1, (2, P, w))
+                view.copy_(torch.from_numpy(arrays[i]))
+                views.append(view)
+            out, l2 = torch.full_like(got, 77.0), torch.full_like(lse, 77.0)
+            ws = vm.CacheWorkspace(len(lens), 22, 2, D, new)
+            vm.dspark_cache_attention4(q, *views, *args, out, ws, max_new=new, lse=l2)
+            assert _status(vm, ws) == 0
+            _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), out, l2)
+
+
+@pytest.mark.parametrize("rows", [33, 64, 65, 136])
+def test_many_rows_leave_out_bad_pages_and_keep_a_nan_to_the_rows_that_see_it(vm, rows):
+    rng = np.random.default_rng(rows)
+    D, P, n = 128, 16, 8 if rows % 8 == 0 else 1
+    Hq = rows // n
+    lens, q_off = [400, 150, 90], np.array([0, n, 2 * n, 3 * n])
+    pages, table = _case(rng, 3, P, lens, D, 1)
+    arrays = _cache(rng, pages, 1, P, D)
+    # among the last positions of the first request, a value group; in the middle of the second, a key's
+    for which, b, pos, group in ((3, 0, 400 - n // 2 - 1, 3), (2, 1, 149, 1), (3, 0, 399, 7)):
+        arrays[which][table[b, pos // P], 0, pos % P, group] = 0x7F
+    q = torch.from_numpy(rng.standard_normal((3 * n, Hq, D))).to(BF16).cuda()
+    q[0, 0] = 0
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, n)
+    assert status == 0
+    _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), got, lse)
+    assert torch.isnan(got[:n, :, 48:64]).any() and not torch.isnan(got[:n, :, :48]).any()
+    table[0, 3], table[0, 20], table[2, 5] = pages, -1, 2 ** 31 - 1
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, n)
+    assert status == BAD_PAGE
+    _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), got, lse)
+    table[2] = -5                                            # a request whose pages are all bad
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, n)
+    assert status == BAD_PAGE and not got[2 * n:].any() and bool((lse[2 * n:] == float("-inf")).all())
+
+
+@pytest.mark.parametrize("lo,hi", [(-8, 0), (0, 28), (-40, 40), (90, 126), (-126, -100)])
+def test_rows_of_very_different_sizes_share_a_tile(vm, lo, hi):
+    """The queries of 64 rows, their sizes 2^lo .. 2^hi: each row against its own bound."""
+    rng = np.random.default_rng(31)
+    P, lens, D, n = 16, [500], 128, 4
+    pages, table = _case(rng, 1, P, lens, D, 1)
+    arrays = _cache(rng, pages, 1, P, D)
+    size = 2.0 ** np.linspace(lo, hi, n * 16).round()
+    q = torch.from_numpy(np.clip(rng.standard_normal((n, 16, D)), -1, 1) * size.reshape(n, 16, 1)).to(BF16).cuda()
+    scale = 2.0 ** min(max(-(lo + hi) // 2, -100), 100)
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, [0, n], n, scale=float(scale))
+    assert status == 0
+    # a tile's queries are exact to 2^-40 of its largest entry (the bound of a row of its own is 2^-25 of the row's)
+    K, V = ref.values(arrays[0], arrays[2], 0), ref.values(arrays[1], arrays[3], 0)
+    want, want_lse, tol, lse_tol = ref.attention(_np(q), K, V, table, lens, [0, n], scale, True)
+    more = scale * 2.0 ** -40 * np.abs(_np(q)).max() * np.abs(K).sum(-1).max()
+    x, ok = _np(got), np.isfinite(want_lse)
+    bound = tol + 2 * more * np.abs(V).max()
+    assert (np.abs(x - want) <= bound)[ok].all(), (np.abs(x - want) / bound)[ok].max()
+
+
+@pytest.mark.parametrize("rows", [8, 64])
+def test_scores_below_any_reference(vm, rows):
+    """Scores of -10^37 everywhere: the weights are those of the differences."""
+    rng = np.random.default_rng(5)
+    P, D, n = 16, 128, 90
+    pages, table = _case(rng, 1, P, [n], D, 1)
+    arrays = _cache(rng, pages, 1, P, D)
+    for a in (arrays[0], arrays[2]):
+        a[:] = 0x22 if a.shape[-1] == 64 else 0x38          # every key entry 1, its scale 1
+    q = torch.full((1, rows, D), -(2.0 ** 122), dtype=BF16, device="cuda")
+    got, lse, status = _attend(vm, rng, q, arrays, table, [n], [0, 1], 1, scale=2.0 ** -7)
+    assert status == 0
+    _check(q, arrays, table, [n], np.array([0, 1]), 2.0 ** -7, got, lse)
+    # every weight is the same: the mean, to a weight's and the result's rounding and 90 sums'
+    V = ref.values(arrays[1], arrays[3], 0)[table[0, np.arange(n) // P], 0, np.arange(n) % P]
+    bound = (ref.EPS16 + ref.EPSH + 100 * 2 * ref.EPS32) * np.abs(V).mean(0)
+    assert (np.abs(_np(got)[0] - V.mean(0)) <= 1.01 * bound).all()
+
+
+def test_expired_waits_are_reported_and_the_workspace_recovers(vm):
+    """With a wait bound of 300 cycles the attention on the tensor cores gives up,
+    reports a timeout and returns; after dspark_workspace_init the same call
+    gives the results of a fresh workspace.  Every wait on the path is bounded."""
+    rng = np.random.default_rng(15)
+    P, lens, D, n = 16, [3000, 700], 128, 8
+    q_off = np.array([0, n, 2 * n])
+    pages, table = _case(rng, 2, P, lens, D, 8)
+    arrays = _cache(rng, pages, 8, P, D)
+    q = torch.from_numpy(rng.standard_normal((2 * n, 64, D))).to(BF16).cuda()
+    ws = vm.CacheWorkspace(2, 64, 8, D, n)
+    out, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, n, ws=ws)
+    assert status == 0
+    vm.dspark_workspace_set_wait_limit(ws.buf, 300)
+    tile_off = np.concatenate([[0], np.cumsum(-(-np.asarray(lens) // 64))])
+    vm.dspark_cache_attention4(q, *(torch.from_numpy(a).cuda() for a in arrays), _cu(table), _cu(lens), _cu(q_off), _cu(tile_off),
+                               torch.empty_like(q), ws, max_new=n)
+    st, bits = vm.dspark_sync_status(ws.buf)
+    assert st == -3 and bits & 4
+    vm.dspark_workspace_init(ws.buf)
+    again, lse2, status = _attend(vm, rng, q, arrays, table, lens, q_off, n, ws=ws)
+    assert status == 0 and torch.equal(again, out) and torch.equal(lse, lse2)
+
+
+# ------------------------------------------------------------ sampling, the rest
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_sampling_where_the_cut_lies_among_more_entries_than_a_list_holds(vm, dtype):
+    """Long rows of few different values, and top-k beyond what is gathered: the
+    last entry kept is found in the slices themselves."""
+    rng = np.random.default_rng(8)
+    V, pad = 60001, 60008
+    x = torch.from_numpy(rng.integers(0, 3, (8, pad)).astype(np.float64)).to(dtype).cuda()[:, :V]
+    x[0] = 2.5
+    x[1] = -0.0
+    u = np.array([0.0, 0.3, 0.5, 0.9, 0.99, 0.25, 0.75, 0.123])
+    k, p = np.array([700, 59999, 20000, 1000, 513, 40000, 60000, 30000]), np.array([0.3, 0.9, 0.5, 0.999, 0.01, 0.7, 0.2, 0.66])
+    for args in ((None, k, None, None), (None, None, p, None), (None, k, p, None), (np.full(8, 0.5), k, p, np.full(8, 0.2))):
+        tok, lp, status = _sample(vm, x, u, *args)
+        assert status == 0
+        _check_rows(x, u, *args, tok, lp)
+
+
+def test_sampling_is_the_same_in_any_batch(vm):
+    """A row's token does not depend on the rows beside it or on how many CTAs take it."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    N, V = 400, 8200
+    x = torch.randn((N, V), generator=g, device="cuda") * 4
+    rng = np.random.default_rng(4)
+    u, k, p = rng.random(N).astype(np.float32), rng.choice([0, 3, 100, 800], N), rng.choice([0.5, 0.95, 1.0], N)
+    tok, lp, _ = _sample(vm, x, u, k=k, p=p)
+    for n in (1, 7, 100):
+        t, l, _ = _sample(vm, x[:n], u[:n], k=k[:n], p=p[:n])
+        assert (t == tok[:n]).all() and (l == lp[:n]).all()
+
+
+def test_sampling_refuses_results_that_overlap(vm):
+    x, f = torch.zeros((4, 64), device="cuda"), torch.zeros(8, device="cuda")
+    tok, ws = torch.zeros(8, dtype=torch.int32, device="cuda"), vm.SampleWorkspace(4)
+    vm.dspark_sample(x, f[:4], tok[:4], ws, logprob=f[4:])
+    for kw in (dict(logprob=f[3:7]), dict(logprob=x[0, :4]), dict(logprob=tok[2:6].view(F32)), dict(top_k=tok[3:7]), dict(temperature=f[4:], logprob=f[4:])):
+        with pytest.raises(vm.DsparkError):
+            vm.dspark_sample(x, f[:4], tok[:4], ws, **kw)
+    assert _status(vm, ws) == 0
+
+
+def test_rope_refuses_outputs_that_overlap(vm):
+    x = torch.randn((6, 8, 64), device="cuda")
+    pos, table = torch.arange(6, dtype=torch.int32, device="cuda"), vm.RopeTable(64)
+    want = torch.empty_like(x)
+    vm.dspark_rope(x, None, pos, table, want)
+    q, k = x[:, :5], x[:, 5:]
+    for qo, ko in ((x[:, 1:6], None), (x[:, :5], x[:, 4:7]), (x[:, 3:], x[:, :3])):
+        with pytest.raises(vm.DsparkError):
+            vm.dspark_rope(q, k if ko is not None else None, pos, table, qo, ko)
+    vm.dspark_rope(q, k, pos, table)                         # slices of the same rows, in place
+    assert torch.equal(x, want)
+
+
+def test_two_streams_at_once(vm):
+    """Two steps' calls on two streams, each with workspaces of its own, give what they give alone."""
+    rng = np.random.default_rng(12)
+    P, D, n, lens = 16, 128, 4, [2000, 300, 40]
+    q_off = n * np.arange(4)
+    pages, table = _case(rng, 3, P, lens, D, 2)
+    ts = [torch.from_numpy(a).cuda() for a in _cache(rng, pages, 2, P, D)]
+    tile_off = np.concatenate([[0], np.cumsum(-(-np.asarray(lens) // 64))])
+    args = (_cu(table), _cu(lens), _cu(q_off), _cu(tile_off))
+    runs = []
+    for i, heads in enumerate((8, 32)):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        q = torch.randn((3 * n, heads, D), generator=g, device="cuda").to(BF16)
+        x = torch.randn((50, 30000), generator=g, device="cuda") * 3
+        runs.append(dict(q=q, x=x, u=torch.rand(50, generator=g, device="cuda"), p=torch.full((50,), 0.9, device="cuda"), ws=vm.CacheWorkspace(3, heads, 2, D, n),
+                         sws=vm.SampleWorkspace(50), s=torch.cuda.Stream()))
+
+    def call(r, stream):
+        out, tok = torch.empty_like(r["q"]), torch.empty(50, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        return out, tok, lambda: (vm.dspark_cache_attention4(r["q"], *ts, *args, out, r["ws"], max_new=n, stream=stream),
+                                  vm.dspark_sample(r["x"], r["u"], tok, r["sws"], top_p=r["p"], stream=stream))
+
+    alone = []
+    for r in runs:
+        out, tok, go = call(r, r["s"])
+        go()
+        torch.cuda.synchronize()
+        alone.append((out, tok))
+    both = [call(r, r["s"]) for r in runs]
+    for _ in range(5):
+        for _, _, go in both:
+            go()
+    torch.cuda.synchronize()
+    for (out, tok, _), (o, t) in zip(both, alone):
+        assert torch.equal(out, o) and torch.equal(tok, t)

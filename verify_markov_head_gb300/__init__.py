@@ -637,6 +637,8 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
         raise ValueError(f"unknown entries of scaling {kind!r}: {sorted(set(s) - set(known[kind]))}")
     if kind in ("yarn", "wavelength") and not s.get("trained", 0) > 0:
         raise ValueError(f"scaling {kind!r} needs the trained length")
+    if kind == "yarn" and not (base > 1 and s.get("fast", 32) > 0 and s.get("slow", 1) > 0):
+        raise ValueError("scaling 'yarn' needs a base above 1 and positive turns")
     if kind == "ntk":
         if r == 2:
             raise ValueError("scaling 'ntk' needs a rotary_dim above 2")
@@ -668,7 +670,7 @@ class RopeTable:
         if len(freq) != int(rotary_dim) // 2:
             raise ValueError("one frequency for each pair")
         self.rotary_dim, self.mult = int(rotary_dim), float(m if mult is None else mult)
-        turns = [int(Fraction(float(x)) / _TURN * 2 ** 64 + Fraction(1, 2)) % 2 ** 64 for x in freq]
+        turns = [math.floor(Fraction(float(x)) / _TURN * 2 ** 64 + Fraction(1, 2)) % 2 ** 64 for x in freq]
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
 
 

@@ -255,6 +255,14 @@ dspark_status dspark_sample(const void* logits, dspark_dtype t, long long row_st
     if (!dev(logits, 16) || !dev(u) || !dev_or_null(temperature) || !dev_or_null(top_k) || !dev_or_null(top_p) ||
         !dev_or_null(min_p) || !dev(tok) || !dev_or_null(logprob) || !dev(ws, 256) || ws_bytes < need)
         return DSPARK_ERR_INVALID;
+    // rows read their inputs while others write their results
+    const long long rows = 4LL * N, all = ((N - 1) * row_stride + V) * bytes_of(t);
+    auto bytes = [](const void* a, long long n) { return Bytes{static_cast<const char*>(a), a ? n : 0}; };
+    const Bytes out[] = {bytes(tok, rows), bytes(logprob, rows)};
+    const Bytes in[] = {bytes(logits, all), bytes(u, rows), bytes(temperature, rows), bytes(top_k, rows), bytes(top_p, rows), bytes(min_p, rows)};
+    for (const Bytes& i : in)
+        if (i.meets(out[0]) || i.meets(out[1])) return DSPARK_ERR_INVALID;
+    if (out[0].meets(out[1])) return DSPARK_ERR_INVALID;
     SampleParams p;
     p.logits = logits; p.row_stride = row_stride; p.bf16 = t == DSPARK_BF16;
     p.N = N; p.V = V;
@@ -380,13 +388,13 @@ dspark_status dspark_cache_attention4(const void* q, long long q_stride, dspark_
     p.by_group.set((uint32_t)p.G);
     const int rows = p.G * max_new;
     const bool tensor = p.bf16 && attn4_tensor(p, rows);
-    p.row_tile = tensor ? (rows <= 32 ? 32 : 64) : p.bf16 ? attn4_row_tile(rows, head_dim) : attn_row_tile(rows, false);
+    p.row_tile = tensor ? 64 : p.bf16 ? attn4_row_tile(rows, head_dim) : attn_row_tile(rows, false);
     const long long tiles = ((long long)width * page_size + kTile - 1) / kTile * B * kv_heads;
     if (!p.bf16 && tiles * ((rows + p.row_tile - 1) / p.row_tile) < 2LL * num_sms()) p.row_tile = 8;
     p.row_tiles = (rows + p.row_tile - 1) / p.row_tile;
     p.ctas = num_sms() < kMaxAttnCtas ? num_sms() : kMaxAttnCtas;      // one resident CTA per SM
     if (p.bf16 && !tensor) p.ctas *= attn4_warps(p.row_tile / 8, head_dim);
-    p.pad = tensor ? 4 : p.bf16 ? 2 : 1;
+    p.pad = tensor ? 4 : 1;
     p.spare = p.bf16;
     p.split = reinterpret_cast<AttnSplitRow*>(static_cast<char*>(ws) + kHead);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead + ws_align256(sizeof(AttnSplitRow) * p.ctas));
