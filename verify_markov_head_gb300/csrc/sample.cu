@@ -39,7 +39,7 @@ constexpr int kCoarse = 3;                       // log2 of the table's steps to
 constexpr float kDeep = 50.f;                    // entries that many powers of 2 below the largest weigh nothing
 constexpr int kFew = 512, kCandidates = 1024;    // top_k that is looked for among candidates, and their most
 constexpr int kListed = 4096;                    // entries of a step that one CTA takes
-constexpr uint32_t kLowest = 0x007fffffu;        // the key of -inf
+constexpr int kDigit = 9;                        // bits of a key that a list is searched by at a time
 constexpr uint32_t kAll = 0xffffffffu;
 
 using u64 = unsigned long long;
@@ -235,6 +235,7 @@ struct Shared {
         struct { float x[kListed]; uint32_t id[kListed]; u64 w[kListed]; } list;
     };
     float tops[kThreads];                        // the threads' maxima
+    uint32_t digit_lo[1 << kDigit], digit_hi[1 << kDigit];
     u64 warp_sum[kWarps], block;
     u64 total, sums[2];                          // read by the other CTAs
     u64 share_above, share_all;
@@ -726,12 +727,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         // The last entry: the largest key at which the sum over the keys from it up
         // reaches what is wanted, and among the entries at it the number of ids that are needed.
         // sum(body): the sum of body(key, id, weight or 1) over the entries, in every thread that is here.
-        auto search = [&](uint32_t key, int bits, auto&& sum) {
-            for (int b = bits - 1; b >= 0; --b) {
-                const uint32_t tried = key | 1u << b;
-                if (above + sum([&](uint32_t k, uint32_t, u64 w) { return k < tried ? 0ull : w; }) >= want) key = tried;
-            }
-            const u64 over = above + sum([&](uint32_t k, uint32_t, u64 w) { return k <= key ? 0ull : w; });
+        // (over: the sum above the key)
+        auto finish = [&](uint32_t key, u64 over, auto&& sum) {
             const u64 at = sum([&](uint32_t k, uint32_t, u64) { return k == key ? 1ull : 0ull; });
             const u64 w = mass ? max(weight.of(value_of(key)), 1ull) : 1ull, needed = (want - over + w - 1ull) / w;
             uint32_t id = value_of(key) == last ? last_id : 0x7fffffffu;      // (where the cut before lies among the same entries, it stays)
@@ -769,7 +766,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 // the digits that all keys share are known
                 const int bits = 32 - __clz(most ^ s.found_bin);
                 const uint32_t known = bits == 32 ? 0u : most >> bits << bits;
-                search(known, bits, [&](auto&& body) {
+                uint32_t key = known;
+                u64 over = above;
+                for (int left = bits; left > 0;) {
+                    static_assert(1 << kDigit == kThreads, "a digit to a thread");
+                    const int d = min(left, kDigit), shift = left - d;
+                    s.digit_lo[tid] = s.digit_hi[tid] = 0u;
+                    __syncthreads();
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (e < rounds && k[e] && (u64)(k[e] ^ key) >> left == 0ull) {
+                            const u64 w = s.list.w[tid + e * kThreads];
+                            const uint32_t at = (k[e] >> shift) & ((1u << d) - 1u), lo = (uint32_t)w, old = atomicAdd(&s.digit_lo[at], lo);
+                            const uint32_t hi = (uint32_t)(w >> 32) + (old > ~lo ? 1u : 0u);
+                            if (hi) atomicAdd(&s.digit_hi[at], hi);
+                        }
+                    __syncthreads();
+                    // the largest digit first
+                    const int mine = kThreads - 1 - tid;
+                    const u64 own = ((u64)s.digit_hi[mine] << 32) + s.digit_lo[mine], scan = warp_scan(own);
+                    if (lane == 31) s.warp_sum[warp] = scan;
+                    __syncthreads();
+                    u64 before = over + scan - own;
+                    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+                    if (before < want && before + own >= want) { s.best = (uint32_t)mine; s.found_above = before; }
+                    __syncthreads();
+                    over = s.found_above;
+                    key |= s.best << shift;
+                    left = shift;
+                }
+                finish(key, over, [&](auto&& body) {
                     u64 sum = 0ull;
 #pragma unroll
                     for (int e = 0; e < kEach; ++e)
@@ -778,11 +804,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 });
             }
         } else {                                 // very many equal entries: over the slices
-            search(0u, 32, [&](auto&& body) {
-                u64 sum = 0ull;
-                each_entry([&](float x, uint32_t id) { sum += body(key_of(x), id, mass ? weight.of(x) : 1ull); });
-                return sum_all(sum);
-            });
+            auto sum = [&](auto&& body) {
+                u64 mine = 0ull;
+                each_entry([&](float x, uint32_t id) { mine += body(key_of(x), id, mass ? weight.of(x) : 1ull); });
+                return sum_all(mine);
+            };
+            uint32_t key = 0u;
+            for (int b = 31; b >= 0; --b) {
+                const uint32_t tried = key | 1u << b;
+                if (above + sum([&](uint32_t k, uint32_t, u64 w) { return k < tried ? 0ull : w; }) >= want) key = tried;
+            }
+            finish(key, above + sum([&](uint32_t k, uint32_t, u64 w) { return k <= key ? 0ull : w; }), sum);
         }
         cluster.sync();
         const float new_x = list->last_x;
