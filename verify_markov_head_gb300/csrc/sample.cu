@@ -239,6 +239,7 @@ struct Shared {
     u64 warp_sum[kWarps], block;
     u64 total, sums[2];                          // read by the other CTAs
     u64 share_above, share_all;
+    u64 warp_kept[kWarps];                       // the weight that is kept of a warp's share
     u64 found_above;
     uint32_t found_bin, found_share;
     float top;
@@ -605,7 +606,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     };
     // Keeps, of what is kept, the entries in descending order (ties: the lower id first)
     // until they reach a wanted amount: `want` of them, or `part` of their weight.
+    bool summed = false;                         // s.warp_kept holds the sums of what is kept
     auto keep = [&](const bool mass, u64 want, float part) {
+        summed = false;
         for (int i = tid; i < kBins / 4; i += kThreads) {
             reinterpret_cast<uint4*>(s.hist.lo)[i] = make_uint4(0u, 0u, 0u, 0u);
             reinterpret_cast<uint4*>(s.hist.hi)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -718,10 +721,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 }
             });
         };
-        each_entry([&](float x, uint32_t id) {
-            const uint32_t at = atomicAdd(&list->gathered, 1u);
-            if (at < kListed) { list->list.x[at] = x; list->list.id[at] = id; }
+        // the entries of the bin to CTA 0, the sums of those above it by warp's share
+        u64 over = 0ull;
+        each_vec(v0 + lane, v1, 32, [&](int v, float (&x)[kVec]) {
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) any |= x[j] >= from;
+            if (!any) return;
+            if (last > -INFINITY)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (!kept(x[j], (uint32_t)(first + v * kVec + j))) x[j] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kVec; j += 2) {
+                u64 w[2];
+                uint32_t k[2];
+                weight(x[j], x[j + 1], w[0], w[1], k[0], k[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t bin = weight.bin(k[e]);
+                    if (bin < found) over += w[e];
+                    if (bin == found && x[j + e] > -INFINITY) {
+                        const uint32_t at = atomicAdd(&list->gathered, 1u);
+                        if (at < kListed) { list->list.x[at] = x[j + e]; list->list.id[at] = (uint32_t)(first + v * kVec + j + e); }
+                    }
+                }
+            }
         });
+        over = warp_add(over);
+        if (lane == 0) s.warp_kept[warp] = over;
         cluster.sync();
         const uint32_t n = list->gathered;
         // The last entry: the largest key at which the sum over the keys from it up
@@ -802,7 +830,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                         if (e < rounds && k[e]) sum += body(k[e], s.list.id[tid + e * kThreads], s.list.w[tid + e * kThreads]);
                     return block_add(sum, s);
                 });
+                __syncthreads();
+                // what is kept of the list, to the warps whose shares hold it
+                const uint32_t last_key = key_of(s.last_x), end_id = s.last_id;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    if (e >= rounds || !k[e]) continue;
+                    const int i = tid + e * kThreads, id = (int)s.list.id[i];
+                    if (k[e] < last_key || (k[e] == last_key && (uint32_t)id > end_id)) continue;
+                    const int r = id / p.slice, at = r * p.slice, all = (min(p.V - at, p.slice) + kVec - 1) / kVec;
+                    atomicAdd(&cluster.map_shared_rank(&s, r)->warp_kept[(id - at) / kVec / ((all + kWarps - 1) / kWarps)],
+                              mass ? s.list.w[i] : weight.of(s.list.x[i]));
+                }
             }
+            summed = true;
         } else {                                 // very many equal entries: over the slices
             auto sum = [&](auto&& body) {
                 u64 mine = 0ull;
@@ -858,12 +899,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 if (w[j] < least_w) w[j] = 0ull;
     };
     u64 mine = 0ull;
-    each_vec(v0 + lane, v1, 32, [&](int v, float (&x)[kVec]) {
-        u64 w[kVec];
-        weigh(v, x, w);
+    if (summed && least_w == 0ull) mine = lane == 0 ? s.warp_kept[warp] : 0ull;
+    else
+        each_vec(v0 + lane, v1, 32, [&](int v, float (&x)[kVec]) {
+            u64 w[kVec];
+            weigh(v, x, w);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) mine += w[j];
-    });
+            for (int j = 0; j < kVec; ++j) mine += w[j];
+        });
     const u64 total = sum_all(mine);
     bool rest;
     const u64 target = part_of(u, total, rest);           // (below the total)
