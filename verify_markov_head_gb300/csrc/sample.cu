@@ -250,6 +250,12 @@ struct Shared {
     uint32_t warp_word[kWarps];
 };
 
+// Adds a weight to a bin of Shared::hist, by its two words and without a branch.
+__device__ __forceinline__ void add_weight(uint32_t bin, u64 w) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 lo, hi, old;\n\tmov.b64 {lo, hi}, %1;\n\tmov.u32 old, 0;\n\tsetp.ne.u64 p, %1, 0;\n\t"
+                 "@p atom.shared.add.u32 old, [%0], lo;\n\tadd.cc.u32 lo, lo, old;\n\taddc.u32 hi, hi, 0;\n\tsetp.ne.u32 p, hi, 0;\n\t"
+                 "@p red.shared.add.u32 [%0 + %2], hi;\n\t}" ::"r"(bin), "l"(w), "n"(4 * kBins) : "memory");
+}
 __device__ __forceinline__ u64 warp_add(u64 x) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
@@ -614,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             reinterpret_cast<uint4*>(s.hist.hi)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         __syncthreads();
+        const uint32_t bins = (uint32_t)__cvta_generic_to_shared(s.hist.lo);
         each_vec(tid, vecs, kThreads, [&](int v, float (&x)[kVec]) {
             if (last > -INFINITY)
 #pragma unroll
@@ -627,10 +634,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     weight(x[j], x[j + 1], w[0], w[1], k[0], k[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (w[e] == 0ull) continue;
-                        const uint32_t bin = weight.bin(k[e]), lo = (uint32_t)w[e], old = atomicAdd(&s.hist.lo[bin], lo);
-                        const uint32_t hi = (uint32_t)(w[e] >> 32) + (old > ~lo ? 1u : 0u);
-                        if (hi) atomicAdd(&s.hist.hi[bin], hi);
+                        add_weight(bins + 4 * weight.bin(k[e]), w[e]);
                     }
                 } else {
                     weight.steps(x[j], x[j + 1], k[0], k[1], m);
