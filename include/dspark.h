@@ -547,19 +547,21 @@ dspark_status dspark_cache_read4(
 
 /*
  * dspark_cache_attention over a cache held in 4 bits (layout above): the same
- * rows, masks, checks, status bits and workspace.  q and out are fp32 or bf16
- * (q_t).  Keys and values take part as the values they stand for.  In bf16
+ * rows, masks, checks and status bits.  q and out are fp32 or bf16 (q_t).  Keys and values take part as the values they stand for.  In bf16
  * calls q is scaled by powers of two and held in fp16: of head_dim 128 with max_new *
  * q_heads / kv_heads above 32 in tiles of 64 rows (exact down to 2^-29 of a tile's
  * largest entry, smaller ones to 2^-40 of it), else row by row (down to 2^-14 of the
  * row's largest, smaller ones to 2^-25 of it).  The softmax's weights are rounded
  * to fp16 (2^-11 of each, those below 2^-21 of the row's largest to 2^-31 of it);
  * products are exact and sums in fp32.  fp32 calls hold everything in fp32.
+ * ws     : dspark_cache4_workspace_bytes(...) bytes, not below dspark_cache_workspace_bytes(...), else as
+ *          in dspark_cache_attention.
  * Limits : as dspark_cache_attention, head_dim % DSPARK_CACHE4_GROUP == 0, scale *
  *          2^k_exp positive and finite; k_cache, v_cache and page_stride multiples of the largest
  *          power of two up to 16 that divides a row of head_dim / 2 bytes, k_scale,
  *          v_scale and scale_stride of the largest that divides one of head_dim / 16.
  */
+size_t dspark_cache4_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new);
 dspark_status dspark_cache_attention4(
     const void* q, long long q_stride, dspark_dtype q_t,
     const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,

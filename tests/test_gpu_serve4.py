@@ -769,3 +769,28 @@ def test_two_streams_at_once(vm):
     torch.cuda.synchronize()
     for (out, tok, _), (o, t) in zip(both, alone):
         assert torch.equal(out, o) and torch.equal(tok, t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group,new", [(1, 1), (8, 1), (3, 3), (2, 8), (4, 8), (8, 8), (16, 8)])
+def test_attention_stays_within_its_workspace(vm, group, new, D, dtype):
+    """Segments split over all workers: what lies behind the workspace is untouched, and a smaller one is refused."""
+    rng = np.random.default_rng(group + new)
+    P, lens, q_off = 16, [5000, 3000], np.array([0, new, new + 1])
+    pages, table = _case(rng, 2, P, lens, D, 2)
+    arrays = _cache(rng, pages, 2, P, D)
+    q = torch.from_numpy(rng.standard_normal((new + 1, 2 * group, D))).to(dtype).cuda()
+    n = vm.dspark_cache4_workspace_bytes(2, 2 * group, 2, D, new)
+    big = torch.full((n + (1 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    ws = vm.CacheWorkspace(2, 2 * group, 2, D, new)
+    assert len(ws.buf4) >= n
+    ws.buf = ws.buf4 = big[:n]
+    vm.dspark_workspace_init(ws.buf)
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, new, ws=ws)
+    assert status == 0 and bool((big[n:] == 0x5a).all())
+    fresh, lse2, _ = _attend(vm, rng, q, arrays, table, lens, q_off, new)
+    assert torch.equal(got, fresh) and torch.equal(lse, lse2)
+    ws.buf4 = big[:n - 256]
+    with pytest.raises(vm.DsparkError):
+        _attend(vm, rng, q, arrays, table, lens, q_off, new, ws=ws)

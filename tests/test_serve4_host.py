@@ -58,7 +58,9 @@ def test_the_workspace_holds_two_tiles_of_rows_a_worker(heads, new):
         tile = 8 if rows <= 8 else 16 if rows <= 16 or D > 128 else 32
         warps = 12 if tile == 8 and D <= 128 else 8
         most = max(warps * tile, 64 if rows > 32 and D == 128 else 0)
-        assert vm.dspark_cache_workspace_bytes(3, 2 * heads, 2, D, new) >= 256 + 152 * warps * 32 + 2 * 152 * most * (D + 2) * 4
+        n = vm.dspark_cache4_workspace_bytes(3, 2 * heads, 2, D, new)
+        assert n >= 256 + 152 * warps * 32 + 2 * 152 * most * (D + 2) * 4 and n >= vm.dspark_cache_workspace_bytes(3, 2 * heads, 2, D, new)
+    assert vm.dspark_cache4_workspace_bytes(3, 2 * heads, 2, 120, new) == 0 and vm.dspark_cache4_workspace_bytes(0, 2 * heads, 2, 128, new) == 0
 
 
 def test_rope_refuses_bad_arguments(host):
@@ -93,7 +95,8 @@ def _i(*s):
 
 
 def _ws():
-    return type("W", (), {"buf": torch.zeros(1 << 20, dtype=torch.uint8)})
+    buf = torch.zeros(1 << 24, dtype=torch.uint8)
+    return type("W", (), {"buf": buf, "buf4": buf})
 
 
 @pytest.mark.parametrize("call", ["append", "read", "attention"])

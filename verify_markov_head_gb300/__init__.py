@@ -26,7 +26,7 @@ __all__ = [
     "dspark_workspace_init", "dspark_workspace_set_wait_limit", "dspark_sync_status", "dspark_draft_markov", "dspark_confidence_sts",
     "dspark_schedule", "dspark_verify", "dspark_draft_markov_target", "target_stream_supported", "dspark_draft_rnn", "dspark_verify_rnn", "dspark_verify_logits", "dspark_rnn_input_table", "rnn_prepare", "dspark_sts_workspace_bytes", "dspark_sts_fit", "dspark_gumbel_stream", "dspark_draft_markov_noalloc", "dspark_noalloc_sync_status", "Workspace", "StepBuffers", "run_step", "run_step_host", "run_step_dp", "GlobalSchedule", "HostPipeline",
     "dspark_cache_plan", "dspark_cache_append", "dspark_cache_workspace_bytes", "dspark_cache_attention", "dspark_logits_workspace_bytes", "dspark_logits_process", "CacheWorkspace", "LogitsWorkspace", "CACHE_TILE",
-    "dspark_cache_append4", "dspark_cache_read4", "dspark_cache_attention4", "Cache4", "CACHE4_GROUP", "dspark_rope", "RopeTable", "rope_frequencies", "dspark_sample_workspace_bytes", "dspark_sample", "SampleWorkspace",
+    "dspark_cache4_workspace_bytes", "dspark_cache_append4", "dspark_cache_read4", "dspark_cache_attention4", "Cache4", "CACHE4_GROUP", "dspark_rope", "RopeTable", "rope_frequencies", "dspark_sample_workspace_bytes", "dspark_sample", "SampleWorkspace",
     "SCHED_OFF", "SCHED_SYNC", "SCHED_ASYNC",
 ]
 
@@ -75,6 +75,8 @@ _lib.dspark_status_string.argtypes = [_i]
 _lib.dspark_status_string.restype = C.c_char_p
 _lib.dspark_workspace_bytes.argtypes = [_i, _i, _i, _i]
 _lib.dspark_workspace_bytes.restype = _sz
+_lib.dspark_cache4_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
+_lib.dspark_cache4_workspace_bytes.restype = _sz
 _lib.dspark_sample_workspace_bytes.argtypes = [_i]
 _lib.dspark_sample_workspace_bytes.restype = _sz
 _lib.dspark_workspace_init.argtypes = [_vp, _sz, _vp]
@@ -489,10 +491,15 @@ class _Scratch(Workspace):
 
 class CacheWorkspace(_Scratch):
     """Workspace of the cache calls for B requests of at most max_new new
-    tokens, q_heads query heads over kv_heads key-value heads of head_dim."""
+    tokens, q_heads query heads over kv_heads key-value heads of head_dim: buf,
+    and buf4, which begins with it, for the attention over 4 bits."""
 
     def __init__(self, B, q_heads, kv_heads, head_dim, max_new, device="cuda", stream=None):
-        super().__init__(dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new), device, stream)
+        sizes = (B, q_heads, kv_heads, head_dim, max_new)
+        plain = dspark_cache_workspace_bytes(*sizes)
+        super().__init__(max(plain, dspark_cache4_workspace_bytes(*sizes)), device, stream)
+        self.buf4 = self.buf
+        self.buf = self.buf4[:plain]
 
 
 class LogitsWorkspace(_Scratch):
@@ -504,6 +511,10 @@ class LogitsWorkspace(_Scratch):
 
 def dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new) -> int:
     return int(_lib.dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new))
+
+
+def dspark_cache4_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new) -> int:
+    return int(_lib.dspark_cache4_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new))
 
 
 def dspark_logits_workspace_bytes(B, R) -> int:
@@ -600,9 +611,9 @@ def dspark_cache_read4(k_cache, v_cache, k_scale, v_scale, slot_map, k, v, *, k_
 def dspark_cache_attention4(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out,
                             ws: Workspace, *, max_new, k_exp=0, v_exp=0, scale=None, lse=None, stream=None):
     """dspark_cache_attention over a Cache4's tensors: q and out [N, q_heads,
-    head_dim] bf16 or fp32, the same plan and workspace (CacheWorkspace)."""
+    head_dim] bf16 or fp32, the same plan and a CacheWorkspace."""
     _check("dspark_cache_attention4", _serve.cache_attention4(
-        q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out, ws.buf, max_new, k_exp, v_exp, scale, lse,
+        q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out, ws.buf4, max_new, k_exp, v_exp, scale, lse,
         stream))
 
 

@@ -282,13 +282,16 @@ size_t dspark_cache_workspace_bytes(int B, int q_heads, int kv_heads, int head_d
     // the larger of the two kernels' tiles (of 9 to 16 rows 32 on CUDA cores, 16 on tensor cores)
     const int all = q_heads / kv_heads * max_new, mma = attn_row_tile(all, true), simt = attn_row_tile(all, false);
     const size_t rows = mma > simt ? mma : simt;
-    size_t parts = kMaxAttnCtas * rows, splits = kMaxAttnCtas;
-    if (head_dim % DSPARK_CACHE4_GROUP == 0) {       // and the warps over a cache in 4 bits
-        const size_t tile = attn4_row_tile(all, head_dim), workers = (size_t)kMaxAttnCtas * attn4_warps((int)tile / 8, head_dim);
-        if (workers * tile > parts) parts = workers * tile;
-        splits = workers;
-    }
-    return kHead + ws_align256(sizeof(AttnSplitRow) * splits) + ws_align256(2 * parts * (head_dim + 2) * sizeof(float));
+    return kHead + ws_align256(sizeof(AttnSplitRow) * kMaxAttnCtas) + ws_align256((size_t)2 * kMaxAttnCtas * rows * (head_dim + 2) * sizeof(float));
+}
+
+size_t dspark_cache4_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, int max_new) {
+    const size_t least = dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new);
+    if (least == 0 || head_dim % DSPARK_CACHE4_GROUP) return 0;
+    // a warp is a worker where registers dequantise; the other kernels' parts are as those of dspark_cache_attention
+    const size_t tile = attn4_row_tile(q_heads / kv_heads * max_new, head_dim), workers = (size_t)kMaxAttnCtas * attn4_warps((int)tile / 8, head_dim);
+    const size_t need = kHead + ws_align256(sizeof(AttnSplitRow) * workers) + ws_align256(2 * workers * tile * (head_dim + 2) * sizeof(float));
+    return need > least ? need : least;
 }
 
 dspark_status dspark_cache_attention(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -373,7 +376,7 @@ dspark_status dspark_cache_attention4(const void* q, long long q_stride, dspark_
         !dev(v_scale, row_align(scale_row)) || !dev(block_table) || !dev(kv_len) || !dev(q_off) || !dev(tile_off) || !dev(out, 16) ||
         !dev_or_null(lse) || !dev(ws, 256))
         return DSPARK_ERR_INVALID;
-    if (ws_bytes < dspark_cache_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new)) return DSPARK_ERR_INVALID;
+    if (ws_bytes < dspark_cache4_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new)) return DSPARK_ERR_INVALID;
     AttnParams p;
     p.q = q; p.q_stride = q_stride; p.k = k_cache; p.v = v_cache; p.page_stride = page_stride;
     p.ks = static_cast<const uint8_t*>(k_scale); p.vs = static_cast<const uint8_t*>(v_scale); p.scale_stride = scale_stride;
