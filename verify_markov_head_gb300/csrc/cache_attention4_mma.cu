@@ -20,8 +20,8 @@
 // buffers of P, so that the softmax of a step runs beside them.
 // The softmax, the segments and the split over CTAs are cache_attention_mma.cu's; weights
 // are fp16, 2^(s - ref + 7), as in cache_attention4.cu, whose notes on precision hold
-// here too, except that the rows of a tile share the power of two that q is scaled by: to
-// below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of the tile's largest.
+// here too, except that 16 rows of a tile share the power of two that q is scaled by: to
+// below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of their largest.
 //
 // One request of 131072 positions, 8 heads of 8 rows each: 127 us, of them 9 the join (with
 // registers dequantising for mma.sync 169; one buffer of P 145).  HBM would take 22 and the
@@ -30,9 +30,9 @@
 //
 // Roles (28 warps, one CTA per SM):
 //   first 16         softmax: groups of 4 warps, 16 columns each; thread = position
-//   then 8           four keys, four values: codes to tensor memory (warp & 3 = its 32 lanes)
+//   then 8           four keys, four values: codes to tensor memory (warp & 3 = its 32 lanes); the keys' also Q
 //   then two         copies of the keys' and of the values' codes and scales
-//   one              MMA issuer, one more the segments and Q tiles
+//   one              MMA issuer, one more the segments
 #include <cudaTypedefs.h>
 
 #include "attn_rows.cuh"
@@ -90,8 +90,8 @@ struct Smem {
     static constexpr int kBar = (kSeg + kSegs * (int)sizeof(Seg) + 7) / 8 * 8;
     static constexpr int kBars = 4 * kStages + 2 * kTiles + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 2 + 2 + 1;
     static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, NaN flag, -
-    static constexpr int kExp = kFlags + 16;                      // [kSegs] exponents of the Q tiles
-    static constexpr int kLater = kExp + 4 * kSegs;               // [kStages] first of a step's positions that not every row sees
+    static constexpr int kExp = kFlags + 16;                      // [kSegs][4] exponents of the Q tiles, 16 rows each
+    static constexpr int kLater = kExp + 16 * kSegs;              // [kStages] first of a step's positions that not every row sees
     static constexpr int kBad = kLater + 4 * kStages;             // [kBadRing] boxes whose page is out of range
     static constexpr int kThere = kBad + 4 * kBadRing;            // [kStages] boxes of a step's values that were copied, and its positions before the end
     static constexpr int kTotal = kThere + 8 * kStages;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             ptx::mbar_init(b_o_empty + 8 * i, kSoftWarps);
             ptx::mbar_init(b_p_full + 8 * i, kSoftWarps); ptx::mbar_init(b_pv + 8 * i, 1);
         }
-        for (int i = 0; i < L::kQBufs; ++i) { ptx::mbar_init(b_q_full + 8 * i, 1); ptx::mbar_init(b_q_empty + 8 * i, 1); }
+        for (int i = 0; i < L::kQBufs; ++i) { ptx::mbar_init(b_q_full + 8 * i, 4); ptx::mbar_init(b_q_empty + 8 * i, 1); }
         ptx::mbar_init(b_end, 1);
         s_flags[1] = 0u;
         s_flags[2] = 0u;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
     };
 
     if (warp == R::kSegWarp) {
-        // ------------------------------------------------ segments and Q tiles
+        // ----------------------------------------------------------- segments
         const AttnSplit sp(p, p.tile_off[p.B], p.tile_off[0]);
         const int cta = blockIdx.x;
         int place = 0, end = 0;
@@ -269,39 +269,6 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             }
             __syncwarp();
             if (d.steps < 0) break;
-            // the Q tile, scaled by a power of two to below 2^kQTop, rows beyond the request's as zeros
-            const int qb = si % L::kQBufs;
-            if (si >= L::kQBufs) ok = wait_all(b_q_empty + 8 * qb, (si / L::kQBufs) - 1);
-            if (!ok) { if (lane == 0) give_up(1); break; }
-            const int c = lane & 15, sub = lane >> 4;              // a 16-byte chunk of rows sub, sub + 2, ..
-            auto chunk_of = [&](int r) {
-                const int rr = d.r0 + r, tok = p.by_group(rr);
-                const uint16_t* src = static_cast<const uint16_t*>(p.q) + (d.q0 + tok) * p.q_stride + (size_t)(d.h * p.G + rr - tok * p.G) * kDim;
-                return r < d.rows ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
-            };
-            uint32_t top = 0u;
-#pragma unroll 8
-            for (int r = sub; r < N; r += 2) {
-                const uint4 x = chunk_of(r);
-                top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-            }
-            top = __reduce_max_sync(~0u, max(top << 16, top & 0xffff0000u));
-            const int e = min(max((int)(top >> 23) - 126 - kQTop, -126), 126);
-            const float down = __int_as_float((127 - e) << 23);
-            const uint32_t to = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
-#pragma unroll 8
-            for (int r = sub; r < N; r += 2) {
-                const uint4 x = chunk_of(r);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = pack_half(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xffff0000u) * down);
-                store_chunk(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-            }
-            if (lane == 0) s_exp[slot] = e;
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
         }
         if (lane == 0) p.split[cta] = split;
     } else if (warp == R::kCopyWarp || warp == R::kCopyWarp + 1) {
@@ -369,11 +336,47 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             const int slot = si % kSegs;
             ok = wait_all(b_seg_full + 8 * slot, si / kSegs);
             if (!ok) { if (lane == 0) give_up(6); break; }
-            const int steps = s_seg[slot].steps;
+            const Seg& sg = const_cast<Seg&>(s_seg[slot]);
+            struct { int h, q0, r0, rows, steps; } d = {sg.h, sg.q0, sg.r0, sg.rows, sg.steps};
             __syncwarp();
-            if (steps < 0) break;
+            if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
-            for (int s = 0; s < steps; ++s, ++step) {
+            if (!kv) {
+                // 16 rows of the Q tile, scaled by a power of two to below 2^kQTop, those beyond the request's
+                // as zeros.  (One warp for the whole tile took 27000 cycles a segment, ahead of the first product)
+                const int c = lane & 15, first = 16 * quarter + (lane >> 4);         // a 16-byte chunk of rows first, first + 2, ..
+                uint4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = d.r0 + min(first + 2 * i, d.rows - 1), tok = p.by_group(rr);
+                    x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (d.q0 + tok) * p.q_stride +
+                                                                (size_t)(d.h * p.G + rr - tok * p.G) * kDim) + c);
+                }
+                uint32_t top = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    top = __vmaxu2(__vmaxu2(top, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu)), __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+                top = __reduce_max_sync(~0u, max(top << 16, top & 0xffff0000u));
+                const int e = min(max((int)(top >> 23) - 126 - kQTop, -126), 126), qb = si % L::kQBufs;
+                if (si >= L::kQBufs) ok = wait_all(b_q_empty + 8 * qb, si / L::kQBufs - 1);
+                if (!ok) { if (lane == 0) give_up(1); break; }
+                const uint32_t to = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = first + 2 * i;
+                    const float by = r < d.rows ? __int_as_float((127 - e) << 23) : 0.f;
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = pack_half(__uint_as_float(w[j] << 16) * by, __uint_as_float(w[j] & 0xffff0000u) * by);
+                    store_chunk(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+                }
+                if (lane == 0) s_exp[4 * slot + quarter] = e;
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
+            }
+            for (int s = 0; s < d.steps; ++s, ++step) {
                 const int stage = step % kStages;
                 const uint32_t fill = 2 * step + kv, tile = fill % kTiles, at = tiles + tile * kTileCols + ((uint32_t)quarter << 21);
                 ok = wait_all(b_cfull + 8 * (kv * kStages + stage), step / kStages);
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
                 const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
                 // (a segment's first scores follow its Q tile)
-                if (s == 0) scale2 = fminf(fmaxf(p.scale * kLog2e * __int_as_float((127 + s_exp[slot]) << 23), 1e-37f), 3e38f);     // (neither 0 nor inf, which -inf and 0 would make NaN)
+                if (s == 0) scale2 = fminf(fmaxf(p.scale * kLog2e * __int_as_float((127 + s_exp[4 * slot + group]) << 23), 1e-37f), 3e38f);     // (neither 0 nor inf, which -inf and 0 would make NaN)
                 // positions beyond the end or in a bad page, and the block's later tokens
                 const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
                 const bool gone = row >= there || (bad >> my_box & 1u);
