@@ -1,7 +1,7 @@
 // cache_attention4_mma.cu -- attention over a paged cache held in 4 bits on the
-// tensor cores: bf16 queries, head size 128, more than 32 query rows a key-value
-// head (formulas: cache_attention.cu; formats: fp4.cuh; fewer rows and other head
-// sizes: cache_attention4.cu).
+// tensor cores: bf16 queries, head size 128, 33 to 64 or more than 96 query rows a
+// key-value head (formulas: cache_attention.cu; formats: fp4.cuh; fewer rows and other
+// head sizes: cache_attention4.cu).
 //
 // Both products are taken transposed, 128 cache positions at a time:
 //     S^T [128 positions x 64] = K [128 x 128] . Q^T       (A: K, B: Q)
@@ -23,10 +23,11 @@
 // here too, except that 16 rows of a tile share the power of two that q is scaled by: to
 // below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of their largest.
 //
-// One request of 131072 positions, 8 heads of 8 rows each: 127 us, of them 9 the join (with
-// registers dequantising for mma.sync 169; one buffer of P 145).  HBM would take 22 and the
-// products 15: it is the issue of instructions that bounds it (55 of 100 slots, by 24
-// warps that wait on one another: conversions a third of them, softmax a half).
+// One request of 131072 positions, 8 heads of 64 rows: 116 us, of them 9 the join (with
+// registers dequantising for mma.sync 169; one buffer of P 145; queries brought by one warp
+// 121).  HBM would take 22 and the products 15: a step's softmax bounds it, 3800 cycles from
+// the scores to the weights for 28 warps that share the issue slots (55 of 100 taken); the
+// warps that convert wait two thirds of the time for a tile to come free.
 //
 // Roles (28 warps, one CTA per SM):
 //   first 16         softmax: groups of 4 warps, 16 columns each; thread = position
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             if (!ok) return;
             ptx::tc_fence_after();
             if (one) {
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < kSteps / 16; ++k)
                     ptx::mma_f16_ts(tmem + (2 + ob) * N, tiles + vi % kTiles * kTileCols + 8 * k, p_desc + (of & 1u) * (L::kPBytes / 16) + k * (2048 / 16),
                                     id_o, o_first && k == 0 ? 0u : 1u);
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                 ptx::tc_fence_after();
                 if (one) {
                     const uint64_t qa = q_desc + qb * (L::kQBytes / 16);
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < kDim / 16; ++k)
                         ptx::mma_f16_ts(tmem + sb * N, tiles + ki % kTiles * kTileCols + 8 * k, qa + (k / 4) * (N * 128 / 16) + (k % 4) * 2, id_s, k ? 1u : 0u);
                     ptx::mma_commit(b_empty + 8 * (ki % kTiles));
