@@ -957,9 +957,12 @@ cudaError_t launch(SampleParams p, cudaStream_t s) {
     // two CTAs to a row, and on an SM: the phases of two rows overlap, and the rows at
     // work fit the L2 for their later passes (512 rows of 151936, settings mixed: 271 us, now 239; one CTA of
     // 1024 threads 276, of 512 322; four of 512 283, eight that keep the row in shared
-    // memory 323).  Up to 16 where SMs would be idle.
+    // memory 323).  Up to 16 while that leaves no more CTAs than run at once, and twice
+    // as many where slices stay long, since rows that are cut take several times as long
+    // as others (64 rows of 151936, settings mixed: two CTAs 104 us, four 61; nothing cut
+    // 46 and 31; 128 rows 109 and 85, 55 and 55; of 32003 entries 48 and 51, 15 and 21).
     int ctas = p.V > 16384 ? 2 : 1;
-    while (ctas < 16 && (long long)p.N * ctas * 2 <= num_sms() && p.V > ctas * 4096) ctas *= 2;
+    while (ctas < 16 && (long long)p.N * ctas * 2 <= (p.V >= ctas * 2 * 24576 ? 4 : 2) * num_sms() && p.V > ctas * 4096) ctas *= 2;
     p.ctas = ctas;
     p.slice = ((p.V + ctas - 1) / ctas + kVec - 1) / kVec * kVec;
     cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
