@@ -553,7 +553,8 @@ dspark_status dspark_cache_read4(
  * largest entry, smaller ones to 2^-40 of it), else row by row (down to 2^-14 of the
  * row's largest, smaller ones to 2^-25 of it).  The softmax's weights are rounded
  * to fp16 (2^-11 of each, those below 2^-21 of the row's largest to 2^-31 of it);
- * products are exact and sums in fp32.  fp32 calls hold everything in fp32.
+ * products are exact and sums in fp32.  fp32 calls hold everything in fp32.  A
+ * NaN among the values reaches the rows that see it with a weight that is not 0 in fp32.
  * ws     : dspark_cache4_workspace_bytes(...) bytes, not below dspark_cache_workspace_bytes(...), else as
  *          in dspark_cache_attention.
  * Limits : as dspark_cache_attention, head_dim % DSPARK_CACHE4_GROUP == 0, scale *
