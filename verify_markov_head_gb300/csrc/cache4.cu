@@ -161,7 +161,6 @@ __device__ __forceinline__ bool place(const Cache4Params& p, int slot, int& page
     return false;
 }
 
-
 // Runs body(Group, token) over the launch's groups and tokens; `lanes` threads to a token.
 template <typename Body>
 __device__ __forceinline__ void each_group(const Cache4Params& p, int lanes, int entry_bytes, Body&& body) {

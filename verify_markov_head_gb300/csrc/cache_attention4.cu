@@ -95,7 +95,6 @@ struct Seg {
 // NT: groups of 8 query rows.  DP: the head size rounded up to 64, 128 or 256.
 template <int NT, int DP>
 struct Layout {
-    static constexpr int kRows = 8 * NT;
     static constexpr int kWarps = attn4_warps(NT, DP);
     static constexpr int kSteps = DP / 16;                        // of 16 entries
     static constexpr bool kQRegs = NT * kSteps <= 16;             // Q in registers

@@ -12,7 +12,6 @@ namespace dspark {
 namespace fp4 {
 
 constexpr int kGroup = 16;               // entries that share a scale
-constexpr float kLargest = 448.f;        // the largest scale
 
 // The 8 codes of a word as 4 fp16 pairs, lower entries first.
 __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&h)[4]) {

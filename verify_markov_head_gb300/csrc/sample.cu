@@ -278,7 +278,6 @@ __device__ __forceinline__ u64 warp_scan(u64 x) {            // inclusive
     return x;
 }
 
-
 // The sum over the CTA, in every thread.
 __device__ __forceinline__ u64 block_add(u64 x, Shared& s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
