@@ -23,7 +23,7 @@
 // here too, except that 16 rows of a tile share the power of two that q is scaled by: to
 // below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of their largest.
 //
-// One request of 131072 positions, 8 heads of 64 rows: 116 us, of them 9 the join (with
+// One request of 131072 positions, 8 heads of 64 rows: 92 us, of them 9 the join (with
 // registers dequantising for mma.sync 169; one buffer of P 145; queries brought by one warp
 // 121).  HBM would take 22 and the products 15: a step's softmax bounds it, 3800 cycles from
 // the scores to the weights for 28 warps that share the issue slots (55 of 100 taken); the
@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                 }
                 // (unset is the same in the whole group)
                 const bool move = unset || ptx::bar_red_or(1 + group, 128, high > kLift + kSlack || !ok);
-                // the product before the last is done: its P may be overwritten
-                if (step > 1) ok = wait(b_pv + 8 * (step & 1u), step / 2 - 1) && ok;
+                // (O of the step before the last is done, and its P may be overwritten: that product was issued
+                // before this step's S, by the same thread, and what a commit signals is all that was issued before it)
                 if (move) {                     // the same in every thread of the group
                     // the last one too: O may be rescaled
                     if (step > 0) ok = wait(b_pv + 8 * ((step - 1) & 1u), (step - 1) / 2) && ok;
