@@ -23,7 +23,7 @@
 // here too, except that 16 rows of a tile share the power of two that q is scaled by: to
 // below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of their largest.
 //
-// One request of 131072 positions, 8 heads of 64 rows: 92 us, of them 9 the join (with
+// One request of 131072 positions, 8 heads of 64 rows: 91 us, of them 9 the join (with
 // registers dequantising for mma.sync 169; one buffer of P 145; queries brought by one warp
 // 121).  HBM would take 22 and the products 15: a step's softmax bounds it, 3800 cycles from
 // the scores to the weights for 28 warps that share the issue slots (55 of 100 taken); the
@@ -90,10 +90,10 @@ struct Smem {
     static constexpr int kSeg = kSum + 2 * N * 16;
     static constexpr int kBar = (kSeg + kSegs * (int)sizeof(Seg) + 7) / 8 * 8;
     static constexpr int kBars = 4 * kStages + 2 * kTiles + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 2 + 2 + 1;
-    static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, NaN flag, -
-    static constexpr int kExp = kFlags + 16;                      // [kSegs][4] exponents of the Q tiles, 16 rows each
+    static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, NaN flag, -, the limit of waits
+    static constexpr int kExp = kFlags + 24;                      // [kSegs][4] exponents of the Q tiles, 16 rows each
     static constexpr int kLater = kExp + 16 * kSegs;              // [kStages] first of a step's positions that not every row sees
-    static constexpr int kBad = kLater + 4 * kStages;             // [kBadRing] boxes whose page is out of range
+    static constexpr int kBad = kLater + 4 * kStages;             // [kBadRing] boxes whose page is out of range, and a bit where not every row sees every position
     static constexpr int kThere = kBad + 4 * kBadRing;            // [kStages] boxes of a step's values that were copied, and its positions before the end
     static constexpr int kTotal = kThere + 8 * kStages;
 };
@@ -109,6 +109,13 @@ __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
+}
+
+// A wait that a test did not end; `flags`: Smem::kFlags.  (Not inlined, and what it reads in
+// shared memory: the roles' loops share the SM's instruction cache, and registers are few.)
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t flags) {
+    const uint8_t* at = static_cast<const uint8_t*>(__cvta_shared_to_generic(flags));
+    return ptx::mbar_wait_strict(bar, parity, reinterpret_cast<const volatile uint32_t*>(at) + 1, *reinterpret_cast<const volatile long long*>(at + 16));
 }
 
 // 16 columns of 32 lanes, waited for.
@@ -224,8 +231,10 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
     ptx::tc_fence_after();
     const uint32_t tmem = s_flags[0], tiles = tmem + 4 * N;
     grid_dependency_wait();             // the set-up above overlaps the launch before this one
-    const long long wl = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
-    auto wait = [&](uint32_t b, uint32_t parity) { return ptx::mbar_wait_strict(b, parity & 1u, abort_flag, wl); };
+    // (every warp writes the limit, the same, for its own waits)
+    if (lane == 0) *reinterpret_cast<volatile long long*>(gbase + L::kFlags + 16) = wait_limit_of(reinterpret_cast<const unsigned long long*>(p.status) + 1);
+    __syncwarp();
+    auto wait = [&](uint32_t b, uint32_t parity) { return ptx::mbar_test_wait(b, parity & 1u) || wait_longer(b, parity & 1u, base + L::kFlags); };
     auto wait_all = [&](uint32_t b, uint32_t parity) { return (bool)__all_sync(~0u, wait(b, parity)); };
     auto give_up = [&](int site) {
         raise_timeout(p.status, site);
@@ -303,7 +312,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                 if (!ok) { if (lane == 0) give_up(3); break; }
                 const uint32_t full = b_cfull + 8 * (kv * kStages + stage), to = base + L::kRing + (kv * kStages + stage) * kStageBytes;
                 if (lane == 0) {
-                    if (!kv) s_bad[step % kBadRing] = bad;
+                    if (!kv) s_bad[step % kBadRing] = bad | (d.seen - pos0 < kSteps || d.pos1 - pos0 < kSteps ? 1u << 16 : 0u);
                     else {
                         s_later[stage] = d.seen - pos0;
                         s_there[2 * stage] = (int)there;
@@ -527,7 +536,6 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
         float4* s_max = reinterpret_cast<float4*>(gbase + L::kMax);
         float4* s_sum = reinterpret_cast<float4*>(gbase + L::kSum);
         // the product's step that this position is: of 16, r is (r & 8) + 2 (r & 3) + (r >> 2 & 1)
-        const int my_box = row / bx;
         const int prow = (row & ~7) | (row & 3) << 1 | (row >> 2 & 1);
         // the entry of the head that this lane of O^T holds
         const int dim = (row & ~31) | (row & 7) << 2 | (row >> 4 & 1) << 1 | (row >> 3 & 1);
@@ -543,31 +551,24 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             ok = wait(b_seg_full + 8 * slot, si / kSegs) && ok;
             if (ptx::bar_red_or(1 + group, 128, !ok)) { ok = false; break; }
             const Seg& sg = const_cast<Seg&>(s_seg[slot]);
-            struct { int n, len, r0, pos0, pos1, steps; } d = {sg.n, sg.len, sg.r0, sg.pos0, sg.pos1, sg.steps};
-            const bool none = d.steps < 0;                         // no more segments
+            const int steps = sg.steps;
+            const bool none = steps < 0;                           // no more segments
             if (none && !pend) break;
             const uint32_t o_at = tmem + lanes + (2 + (si & 1u)) * N + group * HC;
-            const int first_new = d.len - d.n;                     // position of the block's first token
-            // lane c: the last position that column c of this group sees
-            const int my_last = first_new + p.by_group(d.r0 + group * HC + (lane & (HC - 1)));
             float ref[HC], l[HC], scale2 = 0.f;                    // the references (of scores before the scale), this thread's sum of the weights
 #pragma unroll
             for (int c = 0; c < HC; ++c) ref[c] = l[c] = 0.f;
             float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
             bool unset = true;                                     // a column of the group has no reference yet
             bool stop = false;
-            for (int s = 0; s < d.steps || s == 0; ++s) {
+            for (int s = 0; s < steps || s == 0; ++s) {
                 if (!none) {
-                const int pos0 = d.pos0 + s * kSteps, pos = pos0 + row, there = d.pos1 - pos0;
                 ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
                 ok = __all_sync(~0u, ok);
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
-                const uint32_t bad = ok ? s_bad[step % kBadRing] : 0u;
+                const uint32_t marks = ok ? s_bad[step % kBadRing] : 0u;
                 // (a segment's first scores follow its Q tile)
                 if (s == 0) scale2 = fminf(fmaxf(p.scale * kLog2e * __int_as_float((127 + s_exp[4 * slot + group]) << 23), 1e-37f), 3e38f);     // (neither 0 nor inf, which -inf and 0 would make NaN)
-                // positions beyond the end or in a bad page, and the block's later tokens
-                const bool edge = there < kSteps || bad || pos0 + kSteps > first_new + 1;
-                const bool gone = row >= there || (bad >> my_box & 1u);
                 float x[HC];
                 // the scores, -inf where the column does not see the position (read
                 // again where a reference moves)
@@ -577,7 +578,12 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
 #pragma unroll
                         for (int c = 0; c < HC; ++c) x[c] = 0.f;
                     }
-                    if (edge) {
+                    if (marks) {
+                        // positions beyond the end or in a bad page, and the block's later tokens
+                        const int pos = sg.pos0 + s * kSteps + row;
+                        const bool gone = pos >= sg.pos1 || (marks >> (row / bx) & 1u);
+                        // lane c: the last position that column c of this group sees
+                        const int my_last = sg.len - sg.n + p.by_group(sg.r0 + group * HC + (lane & (HC - 1)));
 #pragma unroll
                         for (int c = 0; c < HC; ++c) {
                             const int last = __shfl_sync(~0u, my_last, c);
