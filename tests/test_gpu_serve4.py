@@ -592,7 +592,7 @@ def test_many_rows_of_128_with_pages_of_any_kind(vm):
 @pytest.mark.parametrize("rows", [33, 64, 65, 97, 136])
 def test_many_rows_leave_out_bad_pages_and_keep_a_nan_to_the_rows_that_see_it(vm, rows):
     rng = np.random.default_rng(rows)
-    D, P, n = 128, 16, 8 if rows % 8 == 0 else 1             # (65: in registers, the others on the tensor cores)
+    D, P, n = 128, 16, 8 if rows % 8 == 0 else 1
     Hq = rows // n
     lens, q_off = [400, 150, 90], np.array([0, n, 2 * n, 3 * n])
     pages, table = _case(rng, 3, P, lens, D, 1)

@@ -1,7 +1,7 @@
 // cache_attention4_mma.cu -- attention over a paged cache held in 4 bits on the
-// tensor cores: bf16 queries, head size 128, 33 to 64 or more than 96 query rows a
-// key-value head (formulas: cache_attention.cu; formats: fp4.cuh; fewer rows and other
-// head sizes: cache_attention4.cu).
+// tensor cores: bf16 queries, head size 128, more than 32 query rows a key-value head, or
+// more than 16 of few requests (formulas: cache_attention.cu; formats: fp4.cuh; fewer rows
+// and other head sizes: cache_attention4.cu).
 //
 // Both products are taken transposed, 128 cache positions at a time:
 //     S^T [128 positions x 64] = K [128 x 128] . Q^T       (A: K, B: Q)
@@ -770,7 +770,7 @@ bool attn4_tensor(const AttnParams& p, int rows) {
     // pages a whole number of heads apart, all of them within a tensor map's last dimension, scales that bulk copies reach
     const long long per_head = (long long)p.page_size * kRow;
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.ks) | reinterpret_cast<uintptr_t>(p.vs) | (uintptr_t)p.scale_stride;
-    return attn4_tensor_rows(rows, p.D) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 && p.page_stride / per_head < (1LL << 31) &&
+    return attn4_tensor_rows(rows, p.D, p.B * p.Hkv <= num_sms()) && p.page_size % 8 == 0 && p.page_stride % per_head == 0 && p.page_stride / per_head < (1LL << 31) &&
            p.pages * (p.page_stride / per_head) < (1LL << 31) && at % 16 == 0 && tma_encoder() != nullptr;
 }
 

@@ -129,10 +129,12 @@ cudaError_t launch_cache_attention4(const AttnParams& p, bool tensor, cudaStream
 bool attn_pages_are_boxes(const AttnParams& p);   // bf16 pages that TMA can copy
 cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
 // Over a cache in 4 bits, bf16 queries: above 32 rows of a key head of 128 the tensor cores
-// take them, 64 at a time (cache_attention4_mma.cu), except where three tiles of 32 are less
-// than two of 64.  64 requests of 4096 positions, 8 heads: of 64 rows 238 us, and 290 where
-// registers dequantise; of 80 rows 452, and 416; 64 requests of 1024 to 8192, 32 rows: 195, and 175.
-inline bool attn4_tensor_rows(int rows, int D) { return D == 128 && rows > 32 && (rows + 31) / 32 != 3; }
+// take them, 64 at a time (cache_attention4_mma.cu), and above 16 where there are no more
+// requests and heads than SMs.  4096 positions, 8 heads, and where registers dequantise: 64
+// requests of 64 rows 187 us and 292, of 40 184 and 283, of 80 350 and 418, of 32 181 and
+// 161; one request of 8192 positions, 32 rows 21 and 35, 16 rows 21 and 24 (but eight of
+// 2000, 16 rows 25 and 20); of 32 rows 19 requests 55 and 59, 24 75 and 73.
+inline bool attn4_tensor_rows(int rows, int D, bool few) { return D == 128 && rows > (few ? 16 : 32); }
 bool attn4_tensor(const AttnParams& p, int rows);  // and its pages can be copied by TMA
 cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s);
 // Else every warp is a worker of its own (AttnParams::ctas of them): query
