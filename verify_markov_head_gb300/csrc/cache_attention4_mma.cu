@@ -554,6 +554,8 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             const int steps = sg.steps;
             const bool none = steps < 0;                           // no more segments
             if (none && !pend) break;
+            // no row of the tile in this group's columns: what the products make of them is not read
+            const bool idle = !none && group * HC >= sg.rows;
             const uint32_t o_at = tmem + lanes + (2 + (si & 1u)) * N + group * HC;
             float ref[HC], l[HC], scale2 = 0.f;                    // the references (of scores before the scale), this thread's sum of the weights
 #pragma unroll
@@ -562,7 +564,17 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             bool unset = true;                                     // a column of the group has no reference yet
             bool stop = false;
             for (int s = 0; s < steps || s == 0; ++s) {
-                if (!none) {
+                if (idle) {
+                    ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
+                    ok = __all_sync(~0u, ok);
+                    if (lane == 0) {
+                        if (!ok) give_up(5);                       // (the group leaves where it meets next)
+                        ptx::mbar_arrive(b_s_empty + 8 * (step & 1u));
+                        ptx::mbar_arrive(b_p_full + 8 * (step & 1u));
+                    }
+                    __syncwarp();
+                    ++step;
+                } else if (!none) {
                 ok = wait(b_s_full + 8 * (step & 1u), step / 2) && ok;
                 ok = __all_sync(~0u, ok);
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
@@ -687,12 +699,12 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                 const float pend_sum = (s4.x + s4.y) + (s4.z + s4.w), e_inv = pend_sum != 0.f ? 1.f / pend_sum : 0.f;
                 ptx::tc_fence_after();
                 float o[HC];
-                if (ok) tmem_get(tmem + lanes + (2 + (pi & 1u)) * N + group * HC, o);
+                if (ok && cols > 0) tmem_get(tmem + lanes + (2 + (pi & 1u)) * N + group * HC, o);
                 else {
 #pragma unroll
                     for (int c = 0; c < HC; ++c) o[c] = 0.f;
                 }
-                if (s_flags[2]) {
+                if (s_flags[2] && cols > 0) {
                     // the NaN of the block's later tokens (this CTA's positions)
                     for (int pos = max(e_new + 1, e.pos0); pos < e.pos1; ++pos) {
                         const int pg = p.by_page(pos), page = p.table[(size_t)e.b * p.width + pg];
