@@ -23,11 +23,11 @@
 // here too, except that 16 rows of a tile share the power of two that q is scaled by: to
 // below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of their largest.
 //
-// One request of 131072 positions, 8 heads of 64 rows: 91 us, of them 9 the join (with
-// registers dequantising for mma.sync 169; one buffer of P 145; queries brought by one warp
-// 121).  HBM would take 22 and the products 15: a step's softmax bounds it, 3800 cycles from
-// the scores to the weights for 28 warps that share the issue slots (55 of 100 taken); the
-// warps that convert wait two thirds of the time for a tile to come free.
+// One request of 131072 positions, 8 heads of 64 rows: 89 us, of them 9 the join (with
+// registers dequantising for mma.sync 169; on the way one buffer of P 145, queries brought by
+// one warp 121, one more wait in a step 115).  HBM would take 22 and the products 15: the
+// issue slots bound it, 65 of 100 taken by 28 warps that wait on one another, with 72
+// registers a thread.
 //
 // Roles (28 warps, one CTA per SM):
 //   first 16         softmax: groups of 4 warps, 16 columns each; thread = position

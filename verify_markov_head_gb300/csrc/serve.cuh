@@ -131,9 +131,9 @@ cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
 // Over a cache in 4 bits, bf16 queries: above 32 rows of a key head of 128 the tensor cores
 // take them, 64 at a time (cache_attention4_mma.cu), and above 16 where there are no more
 // requests and heads than SMs.  4096 positions, 8 heads, and where registers dequantise: 64
-// requests of 64 rows 187 us and 292, of 40 184 and 283, of 80 350 and 418, of 32 181 and
-// 161; one request of 8192 positions, 32 rows 21 and 35, 16 rows 21 and 24 (but eight of
-// 2000, 16 rows 25 and 20); of 32 rows 19 requests 55 and 59, 24 75 and 73.
+// requests of 64 rows 185 us and 291, of 40 177 and 282, of 80 331 and 418, of 32 170 and
+// 161; one request of 8192 positions, 32 rows 21 and 35, 16 rows 20 and 24 (but eight of
+// 2000, 16 rows 23 and 20); 16 of 2000, 32 rows 35 and 41.
 inline bool attn4_tensor_rows(int rows, int D, bool few) { return D == 128 && rows > (few ? 16 : 32); }
 bool attn4_tensor(const AttnParams& p, int rows);  // and its pages can be copied by TMA
 cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s);
