@@ -766,17 +766,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         // reaches what is wanted, and among the entries at it the number of ids that are needed.
         // sum(body): the sum of body(key, id, weight or 1) over the entries, in every thread that is here.
         // (over: the sum above the key)
-        auto finish = [&](uint32_t key, u64 over, auto&& sum) {
+        auto finish = [&](uint32_t key, u64 over, auto&& sum, auto&& nth_id) {
             const u64 at = sum([&](uint32_t k, uint32_t, u64) { return k == key ? 1ull : 0ull; });
             const u64 w = mass ? max(weight.of(value_of(key)), 1ull) : 1ull, needed = (want - over + w - 1ull) / w;
             uint32_t id = value_of(key) == last ? last_id : 0x7fffffffu;      // (where the cut before lies among the same entries, it stays)
-            if (needed < at) {
-                id = 0u;                         // the id that has needed - 1 others below it
-                for (int b = 18; b >= 0; --b) {
-                    const uint32_t tried = id | 1u << b;
-                    if (sum([&](uint32_t k, uint32_t i, u64) { return k == key && i < tried ? 1ull : 0ull; }) < needed) id = tried;
-                }
-            }
+            if (needed < at) id = nth_id(needed);        // the id that has needed - 1 others below it
             if (tid == 0) { s.last_x = value_of(key); s.last_id = id; }
         };
         if (n <= kListed) {
@@ -804,41 +798,53 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 // the digits that all keys share are known
                 const int bits = 32 - __clz(most ^ s.found_bin);
                 const uint32_t known = bits == 32 ? 0u : most >> bits << bits;
-                uint32_t key = known;
-                u64 over = above;
-                for (int left = bits; left > 0;) {
-                    static_assert(1 << kDigit == kThreads, "a digit to a thread");
-                    const int d = min(left, kDigit), shift = left - d;
-                    s.digit_lo[tid] = s.digit_hi[tid] = 0u;
-                    __syncthreads();
+                // the largest number at which the amounts of the entries from it up reach `goal` (over: of those above
+                // it), 9 bits at a time; number(e): of the thread's entry e, 0: none; `value` holds the bits above `left`
+                auto by_digits = [&](uint32_t value, int left, u64& over, const u64 goal, auto&& number, auto&& amount) {
+                    while (left > 0) {
+                        static_assert(1 << kDigit == kThreads, "a digit to a thread");
+                        const int d = min(left, kDigit), shift = left - d;
+                        s.digit_lo[tid] = s.digit_hi[tid] = 0u;
+                        __syncthreads();
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e)
-                        if (e < rounds && k[e] && (u64)(k[e] ^ key) >> left == 0ull) {
-                            const u64 w = s.list.w[tid + e * kThreads];
-                            const uint32_t at = (k[e] >> shift) & ((1u << d) - 1u), lo = (uint32_t)w, old = atomicAdd(&s.digit_lo[at], lo);
-                            const uint32_t hi = (uint32_t)(w >> 32) + (old > ~lo ? 1u : 0u);
-                            if (hi) atomicAdd(&s.digit_hi[at], hi);
+                        for (int e = 0; e < kEach; ++e) {
+                            const uint32_t x = e < rounds ? number(e) : 0u;
+                            if (x && (u64)(x ^ value) >> left == 0ull) {
+                                const u64 w = amount(e);
+                                const uint32_t at = (x >> shift) & ((1u << d) - 1u), lo = (uint32_t)w, old = atomicAdd(&s.digit_lo[at], lo);
+                                const uint32_t hi = (uint32_t)(w >> 32) + (old > ~lo ? 1u : 0u);
+                                if (hi) atomicAdd(&s.digit_hi[at], hi);
+                            }
                         }
-                    __syncthreads();
-                    // the largest digit first
-                    const int mine = kThreads - 1 - tid;
-                    const u64 own = ((u64)s.digit_hi[mine] << 32) + s.digit_lo[mine], scan = warp_scan(own);
-                    if (lane == 31) s.warp_sum[warp] = scan;
-                    __syncthreads();
-                    u64 before = over + scan - own;
-                    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-                    if (before < want && before + own >= want) { s.best = (uint32_t)mine; s.found_above = before; }
-                    __syncthreads();
-                    over = s.found_above;
-                    key |= s.best << shift;
-                    left = shift;
-                }
+                        __syncthreads();
+                        // the largest digit first
+                        const int mine = kThreads - 1 - tid;
+                        const u64 own = ((u64)s.digit_hi[mine] << 32) + s.digit_lo[mine], scan = warp_scan(own);
+                        if (lane == 31) s.warp_sum[warp] = scan;
+                        __syncthreads();
+                        u64 before = over + scan - own;
+                        for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+                        if (before < goal && before + own >= goal) { s.best = (uint32_t)mine; s.found_above = before; }
+                        __syncthreads();
+                        over = s.found_above;
+                        value |= s.best << shift;
+                        left = shift;
+                    }
+                    return value;
+                };
+                u64 over = above;
+                const uint32_t key = by_digits(known, bits, over, want, [&](int e) { return k[e]; }, [&](int e) { return s.list.w[tid + e * kThreads]; });
                 finish(key, over, [&](auto&& body) {
                     u64 sum = 0ull;
 #pragma unroll
                     for (int e = 0; e < kEach; ++e)
                         if (e < rounds && k[e]) sum += body(k[e], s.list.id[tid + e * kThreads], s.list.w[tid + e * kThreads]);
                     return block_add(sum, s);
+                }, [&](u64 needed) {
+                    constexpr uint32_t kIds = DSPARK_MAX_SAMPLE_VOCAB - 1;     // (lower ids as larger numbers, above 0)
+                    u64 none = 0ull;
+                    return kIds & ~by_digits(kIds + 1u, 19, none, needed, [&](int e) { return k[e] == key ? kIds + 1u + (kIds ^ s.list.id[tid + e * kThreads]) : 0u; },
+                                             [](int) { return 1ull; });
                 });
                 __syncthreads();
                 // what is kept of the list, to the warps whose shares hold it
@@ -865,7 +871,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 const uint32_t tried = key | 1u << b;
                 if (above + sum([&](uint32_t k, uint32_t, u64 w) { return k < tried ? 0ull : w; }) >= want) key = tried;
             }
-            finish(key, above + sum([&](uint32_t k, uint32_t, u64 w) { return k <= key ? 0ull : w; }), sum);
+            finish(key, above + sum([&](uint32_t k, uint32_t, u64 w) { return k <= key ? 0ull : w; }), sum, [&](u64 needed) {
+                uint32_t id = 0u;
+                for (int b = 18; b >= 0; --b) {
+                    const uint32_t tried = id | 1u << b;
+                    if (sum([&](uint32_t k, uint32_t i, u64) { return k == key && i < tried ? 1ull : 0ull; }) < needed) id = tried;
+                }
+                return id;
+            });
         }
         cluster.sync();
         const float new_x = list->last_x;
