@@ -548,10 +548,9 @@ dspark_status dspark_cache_read4(
 /*
  * dspark_cache_attention over a cache held in 4 bits (layout above): the same
  * rows, masks, checks and status bits.  q and out are fp32 or bf16 (q_t).  Keys and values take part as the values they stand for.  In bf16
- * calls q is scaled by powers of two and held in fp16: of head_dim 128 with more than 16 rows
- * (max_new * q_heads / kv_heads) it may be in groups of 16 rows (exact down to 2^-29 of a group's
- * largest entry, smaller ones to 2^-40 of it), else row by row (down to 2^-14 of the
- * row's largest, smaller ones to 2^-25 of it).  The softmax's weights are rounded
+ * calls each row of q is scaled by a power of two and held in fp16 (exact down to 2^-14 of the
+ * row's largest entry, smaller ones to 2^-25 of it; a row that holds a NaN or an infinity is no number,
+ * the others do not depend on it).  The softmax's weights are rounded
  * to fp16 (2^-11 of each, those below 2^-21 of the row's largest to 2^-31 of it);
  * products are exact and sums in fp32.  fp32 calls hold everything in fp32.  A
  * NaN among the values reaches the rows that see it with a weight that is not 0 in fp32.

@@ -1,0 +1,67 @@
+"""GPU tests of the cache in 4 bits and the sampling at the edges of their types:
+queries that are no numbers, light tokens, cuts that change nothing, flat rows."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _serve4_ref as ref
+from tests import test_gpu_serve4 as s4
+from tests.test_gpu_serve4 import BF16, F32, _attend, _cache, _case, _np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def vm():
+    import verify_markov_head_gb300 as vm
+    return vm
+
+
+def _check(q, arrays, table, lens, q_off, scale, got, lse, k_exp=0, v_exp=0):
+    """test_gpu_serve4's check, and the logarithms are NaN where the definition's are and nowhere else."""
+    s4._check(q, arrays, table, lens, q_off, scale, got, lse, k_exp, v_exp)
+    K, V = ref.values(arrays[0], arrays[2], k_exp), ref.values(arrays[1], arrays[3], v_exp)
+    _, want, _, _ = ref.attention(_np(q), K, V, table, lens, q_off, scale, q.dtype == BF16)
+    a, b = q_off[0], q_off[-1]
+    np.testing.assert_array_equal(np.isnan(_np(lse)[a:b]), np.isnan(want[a:b]))
+
+
+# ----------------------------------------------------------------- attention
+# (rows of a key head, tokens of the block): registers, few requests and many rows on the tensor cores
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,n", [(3, 3), (16, 4), (24, 2), (32, 8), (40, 5), (64, 4), (136, 8)])
+def test_a_query_that_is_no_number_reaches_its_own_row_alone(vm, rows, n, dtype):
+    """NaN and infinities in four rows of a block: every other row keeps its own bound."""
+    rng = np.random.default_rng(rows)
+    P, lens, D = 16, [500, 90], 128
+    G, q_off = rows // n, np.array([0, n, 2 * n])
+    pages, table = _case(rng, 2, P, lens, D, 2)
+    arrays = _cache(rng, pages, 2, P, D)
+    q = torch.from_numpy(rng.standard_normal((2 * n, 2 * G, D))).to(dtype).cuda()
+    clean, clean_lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, n)
+    assert status == 0
+    bad = [(0, 0, float("nan")), (n - 1, G - 1, float("inf")), (n, G, float("-inf")), (2 * n - 1, 2 * G - 1, float("nan"))]
+    for t, h, x in bad:
+        q[t, h, 77] = x
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, n)
+    assert status == 0
+    _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), got, lse)
+    for t, h, _ in bad:
+        assert bool(torch.isnan(got[t, h]).all()) and bool(torch.isnan(lse[t, h]))
+
+
+@pytest.mark.parametrize("lo,hi", [(-60, 0), (0, 60), (-110, -20)])
+@pytest.mark.parametrize("rows,n", [(24, 2), (64, 4), (136, 8)])
+def test_rows_of_a_tile_keep_their_own_precision(vm, rows, n, lo, hi):
+    """Queries of sizes 2^lo .. 2^hi in one block: a row is as exact as by itself."""
+    rng = np.random.default_rng(rows + hi)
+    P, lens, D, G = 16, [300], 128, rows // n
+    pages, table = _case(rng, 1, P, lens, D, 1)
+    arrays = _cache(rng, pages, 1, P, D)
+    size = 2.0 ** rng.permutation(np.linspace(lo, hi, n * G).round())
+    q = torch.from_numpy(np.clip(rng.standard_normal((n, G, D)), -1, 1) * size.reshape(n, G, 1)).to(BF16).cuda()
+    for at in (lo, (lo + hi) // 2, hi):                     # scores of ordinary size from the smallest rows, the middle ones, the largest
+        scale = float(2.0 ** -at)
+        got, lse, status = _attend(vm, rng, q, arrays, table, lens, np.array([0, n]), n, scale=scale)
+        assert status == 0
+        _check(q, arrays, table, lens, np.array([0, n]), scale, got, lse)

@@ -20,8 +20,9 @@
 // buffers of P, so that the softmax of a step runs beside them.
 // The softmax, the segments and the split over CTAs are cache_attention_mma.cu's; weights
 // are fp16, 2^(s - ref + 7), as in cache_attention4.cu, whose notes on precision hold
-// here too, except that 16 rows of a tile share the power of two that q is scaled by: to
-// below 2^15, so that fp16 keeps all of a bf16 entry down to 2^-29 of their largest.
+// here too, except that a row of q is scaled to below 2^15, so that fp16 keeps all of a
+// bf16 entry down to 2^-29 of the row's largest.  (Each row by its own power of two: of one
+// for 16 rows a NaN, an infinity or a large row took the others' entries below fp16's range.)
 //
 // One request of 131072 positions, 8 heads of 64 rows: 89 us, of them 9 the join (with
 // registers dequantising for mma.sync 169; on the way one buffer of P 145, queries brought by
@@ -87,12 +88,12 @@ struct Smem {
     static constexpr int kRing = kP + 2 * kPBytes;                // [keys, values][stage]
     static constexpr int kMax = kRing + 2 * kStages * kStageBytes;    // [2][N][4], by the step's parity
     static constexpr int kSum = kMax + 2 * N * 16;                // [2][N][4], by the segment's parity
-    static constexpr int kSeg = kSum + 2 * N * 16;
+    static constexpr int kScale = kSum + 2 * N * 16;              // [kSegs][N] what the scores of a Q tile's rows are multiplied by
+    static constexpr int kSeg = kScale + kSegs * N * 4;
     static constexpr int kBar = (kSeg + kSegs * (int)sizeof(Seg) + 7) / 8 * 8;
     static constexpr int kBars = 4 * kStages + 2 * kTiles + 2 * kSegs + 2 * kQBufs + 2 + 2 + 2 + 2 + 2 + 1;
     static constexpr int kFlags = kBar + 8 * kBars;               // TMEM address, abort, NaN flag, -, the limit of waits
-    static constexpr int kExp = kFlags + 24;                      // [kSegs][4] exponents of the Q tiles, 16 rows each
-    static constexpr int kLater = kExp + 16 * kSegs;              // [kStages] first of a step's positions that not every row sees
+    static constexpr int kLater = kFlags + 24;                    // [kStages] first of a step's positions that not every row sees
     static constexpr int kBad = kLater + 4 * kStages;             // [kBadRing] boxes whose page is out of range, and a bit where not every row sees every position
     static constexpr int kThere = kBad + 4 * kBadRing;            // [kStages] boxes of a step's values that were copied, and its positions before the end
     static constexpr int kTotal = kThere + 8 * kStages;
@@ -135,10 +136,16 @@ __device__ __forceinline__ void tmem_put(uint32_t a, const float (&v)[16]) {
 
 // (x - r) * s + n, and l + w, of two columns.  (The difference first: of large scores a
 // product that is rounded by itself and one that is not would differ by whole units.)
-__device__ __forceinline__ void exponent_pair(float& x0, float& x1, float r0, float r1, float s, float n) {
-    asm("{\n\t.reg .b64 x, r, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 r, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 n, {%5, %5};\n\t"
+__device__ __forceinline__ void exponent_pair(float& x0, float& x1, float r0, float r1, float s0, float s1, float n) {
+    asm("{\n\t.reg .b64 x, r, s, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 r, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\tmov.b64 n, {%6, %6};\n\t"
         "sub.rn.f32x2 x, x, r;\n\tfma.rn.f32x2 x, x, s, n;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(x0), "+f"(x1) : "f"(r0), "f"(r1), "f"(s), "f"(n));
+        : "+f"(x0), "+f"(x1) : "f"(r0), "f"(r1), "f"(s0), "f"(s1), "f"(n));
+}
+// (volatile: read where it is used, the registers are few)
+__device__ __forceinline__ float4 load_four(uint32_t from) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(from));
+    return v;
 }
 __device__ __forceinline__ void add_pair(float& l0, float& l1, float w0, float w1) {
     asm("{\n\t.reg .b64 l, w;\n\tmov.b64 l, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 l, l, w;\n\tmov.b64 {%0, %1}, l;\n\t}"
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile uint32_t* s_flags = reinterpret_cast<volatile uint32_t*>(gbase + L::kFlags);   // [0] TMEM, [1] abort, [2] NaN
     volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(gbase + L::kBad);
-    volatile int* s_exp = reinterpret_cast<volatile int*>(gbase + L::kExp);
+    volatile float* s_scale = reinterpret_cast<volatile float*>(gbase + L::kScale);
     volatile int* s_later = reinterpret_cast<volatile int*>(gbase + L::kLater);
     volatile int* s_there = reinterpret_cast<volatile int*>(gbase + L::kThere);
     volatile Seg* s_seg = reinterpret_cast<volatile Seg*>(gbase + L::kSeg);
@@ -352,8 +359,8 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             if (d.steps < 0) break;
             if (lane == 0) ptx::mbar_arrive(b_seg_empty + 8 * slot);
             if (!kv) {
-                // 16 rows of the Q tile, scaled by a power of two to below 2^kQTop, those beyond the request's
-                // as zeros.  (One warp for the whole tile took 27000 cycles a segment, ahead of the first product)
+                // 16 rows of the Q tile, each scaled by a power of two to below 2^kQTop, those beyond the
+                // request's as zeros.  (One warp for the whole tile took 27000 cycles a segment, ahead of the first product)
                 const int c = lane & 15, first = 16 * quarter + (lane >> 4);         // a 16-byte chunk of rows first, first + 2, ..
                 uint4 x[8];
 #pragma unroll
@@ -362,26 +369,28 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                     x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (d.q0 + tok) * p.q_stride +
                                                                 (size_t)(d.h * p.G + rr - tok * p.G) * kDim) + c);
                 }
-                uint32_t top = 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    top = __vmaxu2(__vmaxu2(top, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu)), __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-                top = __reduce_max_sync(~0u, max(top << 16, top & 0xffff0000u));
-                const int e = min(max((int)(top >> 23) - 126 - kQTop, -126), 126), qb = si % L::kQBufs;
+                const int qb = si % L::kQBufs;
                 if (si >= L::kQBufs) ok = wait_all(b_q_empty + 8 * qb, si / L::kQBufs - 1);
                 if (!ok) { if (lane == 0) give_up(1); break; }
                 const uint32_t to = base + L::kQ + qb * L::kQBytes + (c / 8) * (N * 128);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = first + 2 * i;
-                    const float by = r < d.rows ? __int_as_float((127 - e) << 23) : 0.f;
                     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    // (magnitudes are ordered as integers; the 16 lanes of a row)
+                    uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                    top = max(top << 16, top & 0xffff0000u);
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+                    const int e = min(max((int)(top >> 23) - 126 - kQTop, -126), 126);
+                    const float by = r < d.rows ? __int_as_float((127 - e) << 23) : 0.f;
                     uint32_t y[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) y[j] = pack_half(__uint_as_float(w[j] << 16) * by, __uint_as_float(w[j] & 0xffff0000u) * by);
                     store_chunk(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+                    // (neither 0 nor inf, which -inf and 0 would make NaN)
+                    if (c == 0) s_scale[N * slot + r] = fminf(fmaxf(p.scale * kLog2e * __int_as_float((127 + e) << 23), 1e-37f), 3e38f);
                 }
-                if (lane == 0) s_exp[4 * slot + quarter] = e;
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(b_q_full + 8 * qb);
@@ -557,7 +566,8 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             // no row of the tile in this group's columns: what the products make of them is not read
             const bool idle = !none && group * HC >= sg.rows;
             const uint32_t o_at = tmem + lanes + (2 + (si & 1u)) * N + group * HC;
-            float ref[HC], l[HC], scale2 = 0.f;                    // the references (of scores before the scale), this thread's sum of the weights
+            float ref[HC], l[HC];                                  // the references (of scores before the scale), this thread's sum of the weights
+            const uint32_t scales = base + L::kScale + 4 * (N * slot + group * HC);      // (a segment's first scores follow its Q tile)
 #pragma unroll
             for (int c = 0; c < HC; ++c) ref[c] = l[c] = 0.f;
             float my_ref = -INFINITY;                              // lane c: column c's reference, -inf before the first score
@@ -579,8 +589,6 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                 ok = __all_sync(~0u, ok);
                 const uint32_t s_at = tmem + lanes + (step & 1u) * N + group * HC;
                 const uint32_t marks = ok ? s_bad[step % kBadRing] : 0u;
-                // (a segment's first scores follow its Q tile)
-                if (s == 0) scale2 = fminf(fmaxf(p.scale * kLog2e * __int_as_float((127 + s_exp[4 * slot + group]) << 23), 1e-37f), 3e38f);     // (neither 0 nor inf, which -inf and 0 would make NaN)
                 float x[HC];
                 // the scores, -inf where the column does not see the position (read
                 // again where a reference moves)
@@ -606,7 +614,11 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                 // .. as exponents
                 auto exponents = [&]() {
 #pragma unroll
-                    for (int c = 0; c < HC; c += 2) exponent_pair(x[c], x[c + 1], ref[c], ref[c + 1], scale2, kLift);
+                    for (int c = 0; c < HC; c += 4) {
+                        const float4 by = load_four(scales + 4 * c);
+                        exponent_pair(x[c], x[c + 1], ref[c], ref[c + 1], by.x, by.y, kLift);
+                        exponent_pair(x[c + 2], x[c + 3], ref[c + 2], ref[c + 3], by.z, by.w, kLift);
+                    }
                 };
                 ptx::tc_fence_after();
                 float high = -INFINITY;
@@ -636,7 +648,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
                     const float4 w4 = reinterpret_cast<const float4*>(mx)[lane & (HC - 1)];
                     const float top = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w));
                     const float to = fmaxf(my_ref, top);
-                    const float my_a = to > my_ref ? fast_exp2((my_ref - to) * scale2) : 1.f;
+                    const float my_a = to > my_ref ? fast_exp2((my_ref - to) * s_scale[N * slot + group * HC + (lane & (HC - 1))]) : 1.f;
                     my_ref = to;
                     unset = __any_sync(~0u, to == -INFINITY);
                     if (s > 0) ptx::tc_fence_after();
@@ -764,7 +776,7 @@ __global__ void __launch_bounds__(Roles::kWarps * 32, 1) attn4_mma_kernel(const 
             }
             if (lane < HC) sm[lane * 4 + quarter] = l[0];
             pend = true;
-            pend_ref = my_ref * scale2;
+            pend_ref = my_ref * s_scale[N * slot + group * HC + (lane & (HC - 1))];
         }
         if (!ok && lane == 0) give_up(5);
     }
