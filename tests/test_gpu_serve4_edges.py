@@ -65,3 +65,25 @@ def test_rows_of_a_tile_keep_their_own_precision(vm, rows, n, lo, hi):
         got, lse, status = _attend(vm, rng, q, arrays, table, lens, np.array([0, n]), n, scale=scale)
         assert status == 0
         _check(q, arrays, table, lens, np.array([0, n]), scale, got, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,Hq,Hkv,D,P,new,lens", [
+    (1, 8, 1, 128, 16, 1, [9000]), (1, 32, 4, 128, 64, 8, [2000]), (1, 24, 1, 128, 16, 1, [3000]), (3, 4, 1, 256, 32, 3, [4000, 0, 33]), (2, 6, 2, 96, 24, 2, [700, 1])])
+def test_a_value_that_is_no_number_leaves_the_logarithm(vm, B, Hq, Hkv, D, P, new, lens, dtype):
+    """NaN groups among the values, over segments that several CTAs share: lse stays a number, out is NaN in that group alone."""
+    rng = np.random.default_rng(D + Hq)
+    q_off = np.concatenate([[0], np.cumsum(np.minimum(new, lens))])
+    pages, table = _case(rng, B, P, lens, D, Hkv)
+    arrays = _cache(rng, pages, Hkv, P, D, spread=0.1)       # (weights of one size: none underflows)
+    for pos in (0, lens[0] // 2, lens[0] - 1):
+        arrays[3][table[0, pos // P], Hkv - 1, pos % P, 1] = 0x7F
+    q = torch.from_numpy(rng.standard_normal((int(q_off[-1]), Hq, D))).to(dtype).cuda()
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, new)
+    assert status == 0 and not bool(torch.isnan(lse).any())
+    _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), got, lse)
+    # and a key that is no number: the whole rows that see it
+    arrays[2][table[0, 5 // P], 0, 5 % P, 2] = 0x7F
+    got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, new)
+    assert status == 0 and bool(torch.isnan(lse[0, :Hq // Hkv]).all())
+    _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), got, lse)
