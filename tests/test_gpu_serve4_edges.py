@@ -87,3 +87,32 @@ def test_a_value_that_is_no_number_leaves_the_logarithm(vm, B, Hq, Hkv, D, P, ne
     got, lse, status = _attend(vm, rng, q, arrays, table, lens, q_off, new)
     assert status == 0 and bool(torch.isnan(lse[0, :Hq // Hkv]).all())
     _check(q, arrays, table, lens, q_off, np.float32(D ** -0.5), got, lse)
+
+
+# ------------------------------------------------------------------ sampling
+def _model_rows(rng, N, V, dtype):
+    """Rows of a model's kind: some candidates stand out, their lead falls with the rank."""
+    x = rng.standard_normal((N, -(-V // 8) * 8)) * 1.5
+    for r in x:
+        r[rng.choice(V, 400, replace=False)] += 9 - rng.uniform(1.2, 1.8) * np.log(np.arange(1, 401))
+    return torch.from_numpy(x).to(dtype).cuda()[:, :V]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [1000, 32003, 151936])
+def test_top_k_beyond_the_entries_that_weigh_something(vm, V, dtype):
+    """Low temperatures: fewer entries than top_k weigh anything, and the cut changes nothing."""
+    rng = np.random.default_rng(V)
+    N = 12
+    x = _model_rows(rng, N, V, dtype)
+    x[0, :] = float("-inf")
+    x[0, V // 2], x[0, V - 1] = 1.0, 1.0                    # fewer entries than top_k at all
+    x[1, 7:] -= 1e4
+    u = rng.random(N).astype(np.float32)
+    for T in (0.02, 0.05, 0.1):
+        for k in (20, 50, 200, 600, 5000):
+            for p, m in ((None, None), (0.9, None), (0.5, 1e-3)):
+                args = (np.full(N, T), np.full(N, k), None if p is None else np.full(N, p), None if m is None else np.full(N, m))
+                tok, lp, status = s4._sample(vm, x, u, *args)
+                assert status == 0
+                s4._check_rows(x, u, *args, tok, lp)

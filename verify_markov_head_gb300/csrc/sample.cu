@@ -44,6 +44,7 @@ constexpr int kUnit = 42;                        // a weight of 1 is 2^kUnit
 constexpr int kFine = 8;                         // log2 of the table's entries
 constexpr int kCoarse = 3;                       // log2 of the table's steps to a bin
 constexpr float kDeep = 50.f;                    // entries that many powers of 2 below the largest weigh nothing
+constexpr uint32_t kNothing = (uint32_t)(kDeep - 1.f) << (kFine - kCoarse);      // the bins from which on entries weigh nothing
 constexpr int kFew = 512, kCandidates = 1024;    // top_k that is looked for among candidates, and their most
 constexpr int kListed = 4096;                    // entries of a step that one CTA takes
 constexpr int kDigit = 9;                        // bits of a key that a list is searched by at a time
@@ -180,7 +181,7 @@ struct Weigher {
     // numbers that no entry of a bin is below, or above: its ends and a little more
     // (the last bins also hold what lies below them)
     __device__ __forceinline__ float least(uint32_t b, const Scale& c) const {
-        if (b >= (uint32_t)(kDeep - 1.f) << (kFine - kCoarse)) return -INFINITY;
+        if (b >= kNothing) return -INFINITY;
         const int at = (int)(top_bin() - (__float_as_uint(kMagic) >> kCoarse) - b) << kCoarse;
         const float x = c.base + ((float)at * (1.f / (1 << kFine)) - 0.01f) / c.c_hi;
         return x - 1e-5f * fabsf(x);
@@ -643,10 +644,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                         add_weight(bins + 4 * weight.bin(k[e]), w[e]);
                     }
                 } else {
+                    // (Entries that weigh nothing are not counted: where the wanted number ends among them,
+                    // keeping all is the same.  At low temperatures nearly all of a row lies there, in one bin.)
                     weight.steps(x[j], x[j + 1], k[0], k[1], m);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (x[j + e] > -INFINITY) atomicAdd(&s.hist.lo[weight.bin(k[e])], 1u);
+                        if (weight.bin(k[e]) < kNothing) atomicAdd(&s.hist.lo[weight.bin(k[e])], 1u);
                 }
             }
         });
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         __syncthreads();
         want = s.share_all;
-        if (want == 0ull) { cluster.sync(); return; }        // all are kept (counts)
+        if (want == 0ull) { cluster.sync(); return; }        // all that weigh something are kept (counts)
         // and the bin, `each` of them to a thread
         {
             const u64* bins = cluster.map_shared_rank(s.hist.merged, s.found_share);
