@@ -654,8 +654,9 @@ dspark_status dspark_logits_process(
  * and the token is the first id, in ascending order, at which the sum of the
  * weights left exceeds u[n] times their total; logprob = ln of its weight's
  * share.  temperature 0: the row's largest entry (the lowest id), logprob 0.
- * Weights are formed to about 2^-31 of each and summed as integers of 2^-42 of
- * the largest (a smaller one counts 0), so the result does not depend on the order of the sums.
+ * Weights are formed to about 2^-31 of each and summed as integers, so the result does not
+ * depend on the order of the sums, whose cut to integers is 2^-31 of a sum at most.  (The integers
+ * count 2^-50 of the largest weight, in flat rows of 2^19 entries 2^-42; a smaller weight counts 0.)
  * Inputs : logits [N][V] (t), row_stride elements between rows; u [N] fp32 in
  *          [0, 1) (taken into that range; NaN as 0); temperature [N] (NULL: 1),
  *          top_k [N] int32, top_p, min_p [N] fp32 (NULL: all).  A

@@ -116,3 +116,28 @@ def test_top_k_beyond_the_entries_that_weigh_something(vm, V, dtype):
                 tok, lp, status = s4._sample(vm, x, u, *args)
                 assert status == 0
                 s4._check_rows(x, u, *args, tok, lp)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [129280, 151936, 1 << 19])
+def test_many_light_entries_count_with_their_whole_weight(vm, V, dtype):
+    """One entry far above all others, which are equal or nearly so: the share that
+    is not its own is the sum of weights of 2^-24 to 2^-47."""
+    rng = np.random.default_rng(V)
+    gaps = np.array([24.3, 30.3, 33.3, 36.5, 38.7, 40.4, 44.6, 47.1])
+    N = len(gaps)
+    x = torch.zeros((N, V + 8 - V % 8), dtype=dtype)[:, :V]
+    x[:, 1::2] = -0.01                                      # (bf16 holds it well enough)
+    x[:, 70001] = torch.from_numpy(gaps * np.log(2)).to(dtype)
+    x, u = x.cuda(), rng.uniform(0.2, 0.8, N).astype(np.float32)
+    one, k = np.ones(N), np.full(N, V - 3)
+    for args in ((None,) * 4, (None, None, one * (1 - 2.0 ** -24), None), (None, k, None, None), (None, None, None, one * 1e-30), (one * 0.9, k, one * (1 - 2.0 ** -23), None)):
+        tok, lp, status = s4._sample(vm, x, u, *args)
+        assert status == 0 and (tok == 70001).all()
+        s4._check_rows(x, u, *args, tok, lp)
+    # rows of few light entries among heavy ones, whose unit is coarser
+    x[:, :1000] = 30.0
+    for args in ((None,) * 4, (None, None, one * 0.999, None), (one * 5, None, one * 0.9, None)):
+        tok, lp, status = s4._sample(vm, x, u, *args)
+        assert status == 0
+        s4._check_rows(x, u, *args, tok, lp)

@@ -22,8 +22,12 @@
 //
 // A token's boundaries are sums over up to 2^19 entries, and a sum that is off by
 // 2^-24 moves the draw across one in a row of some thousand (the boundaries of a
-// flat row are 10^-5 apart).  So weights are integers of 2^-42 of the largest:
-// sums are exact, and the same in any order, atomics among them.  A weight is
+// flat row are 10^-5 apart).  So weights are integers: sums are exact, and the same in
+// any order, atomics among them.  Their unit is 2^-50 of the largest, or what keeps the sum
+// of a row below 2^63: the maxima of 512 groups of entries, each times the n = V / 512 entries of a group,
+// are a sum S that no row's exceeds, and a row's is S / n at least.  So what V entries lose
+// by the cut to integers is V 2^-50 of the largest or V n 2^-60 of the sum, 2^-31 at most.  (With
+// 2^-42 for all rows 130000 light entries lost up to 2^-25 of the sum.)  A weight is
 //     2^(y - ref),  y = x log2(e) / T = k / 256 + r,  |r| <= 2^-9,
 // y by fused multiply-adds with log2(e) / T in two floats, 2^(k mod 256 / 256) from a
 // table of integers, and 2^r - 1 by its series to r^3, as an integer: off by 2^-31 of
@@ -40,10 +44,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048;
-constexpr int kUnit = 42;                        // a weight of 1 is 2^kUnit
+constexpr int kUnit = 50;                        // a weight of 1 is 2^kUnit at most
 constexpr int kFine = 8;                         // log2 of the table's entries
 constexpr int kCoarse = 3;                       // log2 of the table's steps to a bin
-constexpr float kDeep = 50.f;                    // entries that many powers of 2 below the largest weigh nothing
+constexpr float kDeep = 52.f;                    // entries that many powers of 2 below the largest weigh nothing
 constexpr uint32_t kNothing = (uint32_t)(kDeep - 1.f) << (kFine - kCoarse);      // the bins from which on entries weigh nothing
 constexpr int kFew = 512, kCandidates = 1024;    // top_k that is looked for among candidates, and their most
 constexpr int kListed = 4096;                    // entries of a step that one CTA takes
@@ -106,10 +110,12 @@ __device__ __forceinline__ u64 shift_right(u64 x, uint32_t n) {   // (0 from 64 
 // log2(e) / temperature in two floats, and what entries are taken from.
 struct Scale {
     float base, low, c_hi, c_lo;
+    static __device__ __forceinline__ float within(float T) { return fminf(fmaxf(T, 1e-30f), 1e36f); }
+    static __device__ __forceinline__ float per(float T) { return 1.44269502f / within(T); }
     __device__ __forceinline__ Scale(float top, float T) {
         // (Temperatures are taken into 10^-30 .. 10^36: below only the largest entries weigh
         // anything, above -inf would.)
-        T = fminf(fmaxf(T, 1e-30f), 1e36f);
+        T = within(T);
         constexpr float e_hi = 1.44269502f, e_lo = 1.92596303e-8f;
         c_hi = e_hi / T;
         c_lo = (fmaf(-c_hi, T, e_hi) + e_lo) / T;
@@ -132,6 +138,7 @@ struct Weigher {
     u64 base, c_hi, c_lo;                        // (the negative base)
     float low;
     uint32_t ref;                                // the step of the largest entry, rounded down to a power of 2
+    uint32_t down;                               // what a product at ref is shifted by to be a weight
     const uint32_t* powers;
     static constexpr float kMagic = 1.5f * (1 << (23 - kFine));      // a sum's last place is a step
     static constexpr float kRound = 12582912.f;                      // 1.5 * 2^23: a sum's last place is 1
@@ -146,7 +153,8 @@ struct Weigher {
         k1 = __float_as_uint(t);
         return z;
     }
-    __device__ __forceinline__ void set(const Scale& c, float top, const uint32_t* table) {
+    // most: a bound on the sum of the weights, the largest entry's being 1
+    __device__ __forceinline__ void set(const Scale& c, float top, const uint32_t* table, float most) {
         base = two(-c.base, -c.base); c_hi = two(c.c_hi, c.c_hi); c_lo = two(c.c_lo, c.c_lo);
         low = c.low;
         powers = table;
@@ -154,6 +162,9 @@ struct Weigher {
         u64 m;
         steps(top, top, k, same, m);
         ref = k >> kFine;
+        // (a weight is below 2^(unit + 1), the sum below 2^(unit + 1) most)
+        const int log2_most = (int)(__float_as_uint(most) >> 23) - 127;
+        down = ref + 62u - (uint32_t)min(kUnit, 61 - log2_most);
     }
     __device__ __forceinline__ void operator()(float x0, float x1, u64& w0, u64& w1, uint32_t& k0, uint32_t& k1) const {
         u64 m;
@@ -166,8 +177,8 @@ struct Weigher {
         float f0, f1;
         apart(e, f0, f1);
         constexpr uint32_t kOne = 0x80000000u - 0x4b400000u;       // 2^31, less the bits of kRound
-        w0 = shift_right((u64)powers[k0 & ((1 << kFine) - 1)] * (__float_as_uint(f0) + kOne), 62 - kUnit + (ref - (k0 >> kFine)));
-        w1 = shift_right((u64)powers[k1 & ((1 << kFine) - 1)] * (__float_as_uint(f1) + kOne), 62 - kUnit + (ref - (k1 >> kFine)));
+        w0 = shift_right((u64)powers[k0 & ((1 << kFine) - 1)] * (__float_as_uint(f0) + kOne), down - (k0 >> kFine));
+        w1 = shift_right((u64)powers[k1 & ((1 << kFine) - 1)] * (__float_as_uint(f1) + kOne), down - (k1 >> kFine));
     }
     __device__ __forceinline__ u64 of(float x) const {
         u64 w, same;
@@ -243,6 +254,7 @@ struct Shared {
         struct { float x[kListed]; uint32_t id[kListed]; u64 w[kListed]; } list;
     };
     float tops[kThreads];                        // the threads' maxima
+    float warp_top[kWarps], warp_mass[kWarps];   // of warps of groups: the largest entry, and the sum of the groups' weights against it
     uint32_t digit_lo[1 << kDigit], digit_hi[1 << kDigit];
     u64 warp_sum[kWarps], block;
     u64 total, sums[2];                          // read by the other CTAs
@@ -250,7 +262,6 @@ struct Shared {
     u64 warp_kept[kWarps];                       // the weight that is kept of a warp's share
     u64 found_above;
     uint32_t found_bin, found_share;
-    float top;
     uint32_t best;
     uint32_t gathered;                           // candidates, or entries listed, of CTA 0
     float last_x; uint32_t last_id;              // the last entry kept, of CTA 0
@@ -263,6 +274,11 @@ __device__ __forceinline__ void add_weight(uint32_t bin, u64 w) {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 lo, hi, old;\n\tmov.b64 {lo, hi}, %1;\n\tmov.u32 old, 0;\n\tsetp.ne.u64 p, %1, 0;\n\t"
                  "@p atom.shared.add.u32 old, [%0], lo;\n\tadd.cc.u32 lo, lo, old;\n\taddc.u32 hi, hi, 0;\n\tsetp.ne.u32 p, hi, 0;\n\t"
                  "@p red.shared.add.u32 [%0 + %2], hi;\n\t}" ::"r"(bin), "l"(w), "n"(4 * kBins) : "memory");
+}
+__device__ __forceinline__ float warp_add(float x) {         // (the same in every lane)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
 }
 __device__ __forceinline__ u64 warp_add(u64 x) {
 #pragma unroll
@@ -369,23 +385,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         });
     }
     s.tops[tid] = top;
-    const uint32_t warp_top = __reduce_max_sync(~0u, key_of(top));
-    if (lane == 0) s.warp_word[warp] = warp_top;
-    __syncthreads();
-    if (warp == 0) {
-        const uint32_t k = __reduce_max_sync(~0u, lane < kWarps ? s.warp_word[lane] : 0u);
-        if (lane == 0) {
-            s.top = value_of(k);
-            if (dirty) raise_status(p.status, kBadInput);
-        }
-    }
+    if (tid == 0 && dirty) raise_status(p.status, kBadInput);
+    const float T_ = p.temperature ? p.temperature[row] : 1.f;
+    const bool T_ok = T_ >= 0.f && T_ < INFINITY;
     cluster.sync();
-    top = value_of(__reduce_max_sync(~0u, key_of(lane < ctas ? *cluster.map_shared_rank(&s.top, lane) : -INFINITY)));
+    // The largest entry, and the sum over the row's groups (the vectors that thread tid took of every
+    // slice: slices are whole numbers of them, so a group is the same however many CTAs there are)
+    // of the weights of their largest.
+    float mass;
+    {
+        float group = top;
+        for (int r = 0; r < ctas; ++r) group = fmaxf(group, cluster.map_shared_rank(s.tops, r)[tid]);
+        const float c = Scale::per(T_), most = value_of(__reduce_max_sync(~0u, key_of(group)));
+        const float sum = warp_add(group > -INFINITY ? fast_exp2((group - most) * c) : 0.f);
+        if (lane == 0) { s.warp_top[warp] = most; s.warp_mass[warp] = sum; }
+        __syncthreads();
+        const float w = lane < kWarps ? s.warp_top[lane] : -INFINITY;
+        top = value_of(__reduce_max_sync(~0u, key_of(w)));
+        mass = warp_add(w > -INFINITY ? s.warp_mass[lane] * fast_exp2((w - top) * c) : 0.f);
+    }
 
     // a warp's share of the slice, in the order of the ids
     const int share = (vecs + kWarps - 1) / kWarps, v0 = min(vecs, warp * share), v1 = min(vecs, v0 + share);
-    const float T_ = p.temperature ? p.temperature[row] : 1.f;
-    const bool T_ok = T_ >= 0.f && T_ < INFINITY;
     float top_p = p.top_p ? p.top_p[row] : 1.f, min_p = p.min_p ? p.min_p[row] : 0.f;
     int top_k = p.top_k ? p.top_k[row] : 0;
     if (top_k <= 0 || top_k >= p.V) top_k = 0;   // all
@@ -428,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     const Scale scale(top, T_);
     Weigher weight;
-    weight.set(scale, top, s.powers);
+    weight.set(scale, top, s.powers, mass * (float)(((p.V + kVec - 1) / kVec + kThreads - 1) / kThreads * kVec));
     // min_p, of the largest entry's weight
     u64 least_w = 0ull;
     if (min_p > 0.f) {
@@ -979,7 +1000,8 @@ cudaError_t launch(SampleParams p, cudaStream_t s) {
     int ctas = p.V > 16384 ? 2 : 1;
     while (ctas < 16 && (long long)p.N * ctas * 2 <= (p.V >= ctas * 2 * 24576 ? 4 : 2) * num_sms() && p.V > ctas * 4096) ctas *= 2;
     p.ctas = ctas;
-    p.slice = ((p.V + ctas - 1) / ctas + kVec - 1) / kVec * kVec;
+    constexpr int kRound = kVec * kThreads;      // (whole rounds of the threads: a thread takes the same group in every slice)
+    p.slice = ctas == 1 ? (p.V + kVec - 1) / kVec * kVec : ((p.V + ctas - 1) / ctas + kRound - 1) / kRound * kRound;
     cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
     if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
