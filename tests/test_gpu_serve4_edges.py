@@ -141,3 +141,28 @@ def test_many_light_entries_count_with_their_whole_weight(vm, V, dtype):
         tok, lp, status = s4._sample(vm, x, u, *args)
         assert status == 0
         s4._check_rows(x, u, *args, tok, lp)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [600, 5000, 151936])
+@pytest.mark.parametrize("T", [1.0, 0.3])
+def test_the_logarithm_of_a_light_token(vm, V, dtype, T):
+    """u = 0 draws the first id that weighs something, however little."""
+    rng = np.random.default_rng(V)
+    far = np.array([5.0, 12.0, 18.0, 22.0, 25.0, 27.0, 29.0])
+    N = len(far)
+    x = torch.from_numpy(rng.standard_normal((N, -(-V // 8) * 8))).to(dtype)[:, :V]
+    x[:, V // 2] = 8.0
+    x[:, 0] = torch.from_numpy(8.0 - far * T).to(dtype)
+    x, one = x.cuda(), np.ones(N)
+    for k in (None, 500, V - 1):
+        tok, lp, status = s4._sample(vm, x, np.zeros(N), T=one * T, k=None if k is None else np.full(N, k))
+        assert status == 0
+        for i, row in enumerate(_np(x)):
+            w = np.exp((row - row.max()) / float(np.float32(T)))
+            if k is not None:
+                w[np.argsort(-row, kind="stable")[k:]] = 0
+            assert tok[i] == np.flatnonzero(w)[0]
+            want = np.log(w[tok[i]] / w.sum())
+            # a difference, a quotient and a sum rounded to binary32, the logarithm's own, and 2^-29
+            assert abs(lp[i] - want) <= 2.0 ** -29 + 4 * ref.EPS32 * abs(want), (i, tok[i], lp[i], want)

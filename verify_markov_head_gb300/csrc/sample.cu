@@ -262,6 +262,8 @@ struct Shared {
     u64 warp_kept[kWarps];                       // the weight that is kept of a warp's share
     u64 found_above;
     uint32_t found_bin, found_share;
+    u64 top_w;                                   // the largest entry's weight,
+    float top, T;                                // the entry itself, and the temperature
     uint32_t best;
     uint32_t gathered;                           // candidates, or entries listed, of CTA 0
     float last_x; uint32_t last_id;              // the last entry kept, of CTA 0
@@ -450,6 +452,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const Scale scale(top, T_);
     Weigher weight;
     weight.set(scale, top, s.powers, mass * (float)(((p.V + kVec - 1) / kVec + kThreads - 1) / kThreads * kVec));
+    // the logarithm of an entry's share: the largest one's, less the distance to it (a light
+    // entry's own weight is an integer of few digits)
+    if (tid == 0) { s.top_w = weight.of(top); s.top = top; s.T = Scale::within(T_); }      // (barriers lie between)
+    auto log_of = [&](float x, u64 total) { return log_share(s.top_w, total) + (x - s.top) / s.T; };
     // min_p, of the largest entry's weight
     u64 least_w = 0ull;
     if (min_p > 0.f) {
@@ -609,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     const u64 at = s.cand.w[lower[e]];
                     if (at <= target && target < at + w[e]) {
                         p.tok[row] = (int)id[e];
-                        if (p.logprob) p.logprob[row] = log_share(w[e], total);
+                        if (p.logprob) p.logprob[row] = log_of(x[e], total);
                     }
                 }
                 return;
@@ -975,8 +981,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     if (at <= target && target < at + w[j]) {
-                        p.tok[row] = first + (v + lane) * kVec + j;
-                        if (p.logprob) p.logprob[row] = log_share(w[j], total);
+                        const int at_v = (v + lane) * kVec + j;
+                        p.tok[row] = first + at_v;
+                        if (p.logprob) p.logprob[row] = log_of(R::one(src + at_v), total);
                     }
                     at += w[j];
                 }
