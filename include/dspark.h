@@ -529,6 +529,8 @@ dspark_status dspark_cache_attention(
  * dspark_cache_read4: the entries of the slots slot_map, in k_t (exact in bf16
  * and fp32 as far as their range goes); a negative slot leaves its row as it
  * was, one beyond the cache too, and sets status bit 5.
+ * What is written (the caches, or k and v) overlaps no input and no other result;
+ * pages, or tokens, of the same stride may lie in each other's gaps.
  * Limits : head_dim % DSPARK_CACHE4_GROUP == 0, <= DSPARK_MAX_HEAD_DIM; k, v and their
  *          strides multiples of 16 bytes, k_cache, v_cache and page_stride of 8.  ws as in dspark_cache_plan.
  */
@@ -549,11 +551,11 @@ dspark_status dspark_cache_read4(
  * dspark_cache_attention over a cache held in 4 bits (layout above): the same
  * rows, masks, checks and status bits.  q and out are fp32 or bf16 (q_t).  Keys and values take part as the values they stand for.  In bf16
  * calls each row of q is scaled by a power of two and held in fp16 (exact down to 2^-14 of the
- * row's largest entry, smaller ones to 2^-25 of it; a row that holds a NaN or an infinity is no number,
- * the others do not depend on it).  The softmax's weights are rounded
+ * row's largest entry, smaller ones to 2^-25 of it; a NaN or an infinity reaches its own row alone).  The softmax's weights are rounded
  * to fp16 (2^-11 of each, those below 2^-21 of the row's largest to 2^-31 of it);
  * products are exact and sums in fp32.  fp32 calls hold everything in fp32.  A
  * NaN among the values reaches the rows that see it with a weight that is not 0 in fp32.
+ * out and lse overlap no input, not each other and not ws.
  * ws     : dspark_cache4_workspace_bytes(...) bytes, not below dspark_cache_workspace_bytes(...), else as
  *          in dspark_cache_attention.
  * Limits : as dspark_cache_attention, head_dim % DSPARK_CACHE4_GROUP == 0, scale *

@@ -166,3 +166,64 @@ def test_the_logarithm_of_a_light_token(vm, V, dtype, T):
             want = np.log(w[tok[i]] / w.sum())
             # a difference, a quotient and a sum rounded to binary32, the logarithm's own, and 2^-29
             assert abs(lp[i] - want) <= 2.0 ** -29 + 4 * ref.EPS32 * abs(want), (i, tok[i], lp[i], want)
+
+
+# ------------------------------------------------------------------ refusals
+def test_rows_and_caches_that_overlap_are_refused(vm):
+    T, H, D, P, pages = 6, 2, 64, 4, 5
+    slots = s4._cu(np.arange(T))
+    c = vm.Cache4(pages, H, P, D)
+    wide = torch.randn((T, 4, H, D), device="cuda")
+    k, v = wide[:, 0], wide[:, 1]
+
+    def append(k=k, v=v, slots=slots, kc=c.k, vc=c.v, ks=c.k_scale, vs=c.v_scale):
+        vm.dspark_cache_append4(k, v, slots, kc, vc, ks, vs)
+
+    def read(k=wide[:, 2], v=wide[:, 3], slots=slots, kc=c.k, vc=c.v, ks=c.k_scale, vs=c.v_scale):
+        vm.dspark_cache_read4(kc, vc, ks, vs, slots, k, v)
+
+    append()
+    read()
+    assert bool(wide[:, 2].any(2).any(1).all())
+    rows = H * P * D // 2
+    blob = torch.zeros(pages * 4 * rows, dtype=torch.uint8, device="cuda")
+    part = lambda at, w: blob[at:at + pages * H * P * w].view(pages, H, P, w)  # noqa: E731
+    both = torch.zeros((pages, 2, H, P, D // 2), dtype=torch.uint8, device="cuda")
+    append(kc=both[:, 0], vc=both[:, 1])                    # pages in each other's gaps
+    append(kc=part(0, D // 2), vc=part(pages * rows, D // 2))
+    for kw in (dict(kc=c.v), dict(vs=c.k_scale),
+               dict(kc=part(0, D // 2), vc=part(pages * rows - 16, D // 2)), dict(ks=part(0, D // 16), vc=part(0, D // 2)),
+               dict(kc=part(0, D // 2), k=blob[:T * H * D * 4].view(F32).view(T, H, D)), dict(kc=part(0, D // 2), slots=blob[:4 * T].view(torch.int32))):
+        with pytest.raises(vm.DsparkError):
+            append(**kw)
+    out = torch.zeros((T + 1, H, D), device="cuda")
+    for kw in (dict(k=out[1:], v=out[1:]), dict(k=out[1:], v=out[:-1]), dict(k=wide[:, 2], v=wide[:, 2]), dict(kc=part(0, D // 2), v=blob[:T * H * D * 4].view(F32).view(T, H, D)),
+               dict(k=blob[:T * H * D * 4].view(F32).view(T, H, D), slots=blob[64:64 + 4 * T].view(torch.int32))):
+        with pytest.raises(vm.DsparkError):
+            read(**kw)
+    read(v=wide[:, 1])                                      # (what was written may be read over)
+
+
+def test_attention_refuses_results_that_overlap(vm):
+    rng = np.random.default_rng(1)
+    P, lens, D, N = 16, [40, 3], 64, 4
+    pages, table = _case(rng, 2, P, lens, D, 2)
+    ts = [torch.from_numpy(a).cuda() for a in _cache(rng, pages, 2, P, D)]
+    lists = [s4._cu(table), s4._cu(lens), s4._cu([0, 2, 4]), s4._cu([0, 1, 2])]
+    ws = vm.CacheWorkspace(2, 4, 2, D, 2)
+    wide = torch.randn((N + 1, 4, D), device="cuda")
+    q, out, lse = wide[:N], torch.empty((N, 4, D), device="cuda"), torch.empty((N, 4), device="cuda")
+
+    def call(q=q, out=out, lse=lse, ts=ts, lists=lists, ws=ws):
+        vm.dspark_cache_attention4(q, *ts, *lists, out, ws, max_new=2, lse=lse)
+
+    call()
+    big = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    f = lambda at, *s: big[at:at + 4 * int(np.prod(s))].view(F32).view(*s)  # noqa: E731
+    for kw in (dict(out=q), dict(out=wide[1:]), dict(lse=out[0].view(-1)[:16].view(4, 4)), dict(lse=q[1].reshape(-1)[:16].view(4, 4)),
+               dict(out=ws.buf4[256:256 + 4 * N * 4 * D].view(F32).view(N, 4, D)),
+               dict(out=f(0, N, 4, D), ts=[big[:ts[0].numel()].view_as(ts[0])] + ts[1:]), dict(lse=f(0, N, 4), ts=ts[:3] + [big[:ts[3].numel()].view_as(ts[3])]),
+               dict(lse=f(0, N, 4), lists=lists[:2] + [big[16:28].view(torch.int32)] + lists[3:])):
+        with pytest.raises(vm.DsparkError):
+            call(**kw)
+    assert s4._status(vm, ws) == 0

@@ -60,6 +60,16 @@ bool rows_meet(const Bytes& a, long long a_stride, long long a_width, const Byte
     return gap < a_width || gap + b_width > a_stride;
 }
 
+// Rows of `width` bytes, `stride` apart: tokens of a projection, or pages of a cache.
+struct Strided {
+    Bytes all;
+    long long stride, width;
+    Strided(const void* p, long long n, long long stride_, long long width_)
+        : all{static_cast<const char*>(p), p && n > 0 ? (n - 1) * stride_ + width_ : 0}, stride(stride_), width(width_) {}
+    bool meets(const Strided& o) const { return rows_meet(all, stride, width, o.all, o.stride, o.width); }
+    bool meets(const Bytes& o) const { return all.meets(o); }
+};
+
 // Workspaces: the status word in the first 256 bytes, then the regions.
 constexpr size_t kHead = 256;
 
@@ -135,7 +145,7 @@ dspark_status dspark_cache_append(const void* k, const void* v, dspark_dtype kv_
 static bool cache4_params(Cache4Params& p, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
                           long long page_stride, long long scale_stride, int pages, int page_size, int kv_heads, int head_dim,
                           int k_exp, int v_exp, const int32_t* slot_map, int T, const void* k, const void* v, dspark_dtype kv_t,
-                          long long k_stride, long long v_stride, void* ws) {
+                          long long k_stride, long long v_stride, void* ws, bool reads) {
     if (T < 0 || kv_heads < 1 || kv_heads > 4096 || !head_ok(head_dim) || head_dim % DSPARK_CACHE4_GROUP || !pages_ok(pages, page_size) ||
         !exp_ok(k_exp) || !exp_ok(v_exp))
         return false;
@@ -146,6 +156,22 @@ static bool cache4_params(Cache4Params& p, const void* k_cache, const void* v_ca
     if (T > 0 && (!dev(k, 16) || !dev(v, 16) || !dev(slot_map) || !dev(k_cache, 8) || !dev(v_cache, 8) || !dev(k_scale, 1) ||
                   !dev(v_scale, 1) || !dev_or_null(ws, 256)))
         return false;
+    // what is written shares no byte with what is read, nor with another result
+    const Strided tokens[] = {{k, T, k_stride * es, row * es}, {v, T, v_stride * es, row * es}};
+    const Strided cache[] = {{k_cache, pages, page_stride, rows * (head_dim / 2)}, {v_cache, pages, page_stride, rows * (head_dim / 2)},
+                             {k_scale, pages, scale_stride, rows * groups}, {v_scale, pages, scale_stride, rows * groups}};
+    const Bytes slots{reinterpret_cast<const char*>(slot_map), 4LL * T};
+    if (T > 0) {
+        for (const Strided& t : tokens)
+            for (const Strided& c : cache)
+                if (t.meets(c)) return false;
+        if (reads && tokens[0].meets(tokens[1])) return false;
+        for (int i = 0; !reads && i < 4; ++i)
+            for (int j = 0; j < i; ++j)
+                if (cache[i].meets(cache[j])) return false;
+        for (int i = 0; i < (reads ? 2 : 4); ++i)
+            if ((reads ? tokens[i] : cache[i]).meets(slots)) return false;
+    }
     p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride;
     p.bf16 = kv_t == DSPARK_BF16;
     p.slot_map = slot_map; p.T = T;
@@ -167,7 +193,7 @@ dspark_status dspark_cache_append4(const void* k, const void* v, dspark_dtype kv
     if (!dtype_ok(kv_t)) return DSPARK_ERR_UNSUPPORTED;
     Cache4Params p;
     if (!cache4_params(p, k_cache, v_cache, k_scale, v_scale, page_stride, scale_stride, pages, page_size, kv_heads, head_dim,
-                       k_exp, v_exp, slot_map, T, k, v, kv_t, k_stride, v_stride, ws))
+                       k_exp, v_exp, slot_map, T, k, v, kv_t, k_stride, v_stride, ws, false))
         return DSPARK_ERR_INVALID;
     if (T == 0) return DSPARK_OK;
     p.k_by = power(-k_exp);
@@ -183,7 +209,7 @@ dspark_status dspark_cache_read4(const void* k_cache, const void* v_cache, const
     if (!dtype_ok(kv_t)) return DSPARK_ERR_UNSUPPORTED;
     Cache4Params p;
     if (!cache4_params(p, k_cache, v_cache, k_scale, v_scale, page_stride, scale_stride, pages, page_size, kv_heads, head_dim,
-                       k_exp, v_exp, slot_map, T, k, v, kv_t, k_stride, v_stride, ws))
+                       k_exp, v_exp, slot_map, T, k, v, kv_t, k_stride, v_stride, ws, true))
         return DSPARK_ERR_INVALID;
     if (T == 0) return DSPARK_OK;
     p.k_by = power(k_exp);
@@ -376,7 +402,22 @@ dspark_status dspark_cache_attention4(const void* q, long long q_stride, dspark_
         !dev(v_scale, row_align(scale_row)) || !dev(block_table) || !dev(kv_len) || !dev(q_off) || !dev(tile_off) || !dev(out, 16) ||
         !dev_or_null(lse) || !dev(ws, 256))
         return DSPARK_ERR_INVALID;
-    if (ws_bytes < dspark_cache4_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new)) return DSPARK_ERR_INVALID;
+    const size_t need = dspark_cache4_workspace_bytes(B, q_heads, kv_heads, head_dim, max_new);
+    if (ws_bytes < need) return DSPARK_ERR_INVALID;
+    // CTAs write their rows while others read theirs
+    const long long es = bytes_of(q_t), q_row = (long long)q_heads * head_dim * es;
+    const Strided in[] = {{q, N, q_stride * es, q_row}, {k_cache, pages, page_stride, rows_a_page * code_row}, {v_cache, pages, page_stride, rows_a_page * code_row},
+                          {k_scale, pages, scale_stride, rows_a_page * scale_row}, {v_scale, pages, scale_stride, rows_a_page * scale_row}};
+    auto bytes = [](const void* a, long long n) { return Bytes{static_cast<const char*>(a), a ? n : 0}; };
+    const Bytes lists[] = {bytes(block_table, 4LL * B * width), bytes(kv_len, 4LL * B), bytes(q_off, 4LL * (B + 1)), bytes(tile_off, 4LL * (B + 1)), bytes(ws, (long long)need)};
+    const Bytes results[] = {bytes(out, N * q_row), bytes(lse, 4LL * N * q_heads)};
+    if (results[0].meets(results[1])) return DSPARK_ERR_INVALID;
+    for (const Bytes& r : results) {
+        for (const Strided& i : in)
+            if (i.meets(r)) return DSPARK_ERR_INVALID;
+        for (const Bytes& i : lists)
+            if (i.meets(r)) return DSPARK_ERR_INVALID;
+    }
     AttnParams p;
     p.q = q; p.q_stride = q_stride; p.k = k_cache; p.v = v_cache; p.page_stride = page_stride;
     p.ks = static_cast<const uint8_t*>(k_scale); p.vs = static_cast<const uint8_t*>(v_scale); p.scale_stride = scale_stride;
