@@ -93,7 +93,7 @@ class Decoder:
         self.mask = word[:, None].expand(B, gamma + 1, W).contiguous()
         self.mask_draft = word[:, None].expand(B, gamma, W).contiguous()
         self.buf = vm.StepBuffers(B, gamma, m.V, r, device)
-        self.cache_ws = vm.CacheWorkspace(B, m.q_heads, m.kv_heads, D, gamma + 1, device)
+        self.cache_ws = vm.CacheWorkspace(B, m.q_heads, m.kv_heads, D, gamma + 1, device, four_bits=False)
         self.target_ws, self.draft_ws = vm.LogitsWorkspace(B, gamma + 1, device), vm.LogitsWorkspace(B, gamma, device)
         self.target = torch.empty((B, gamma + 1, m.V), device=device)
         self.U = torch.empty((B, gamma, m.V), device=device)

@@ -227,3 +227,23 @@ def test_attention_refuses_results_that_overlap(vm):
         with pytest.raises(vm.DsparkError):
             call(**kw)
     assert s4._status(vm, ws) == 0
+
+
+def test_a_workspace_without_room_for_four_bits_is_the_smaller_one(vm):
+    sizes = (3, 8, 2, 128, 8)
+    ws, both = vm.CacheWorkspace(*sizes, four_bits=False), vm.CacheWorkspace(*sizes)
+    n, n4 = vm.dspark_cache_workspace_bytes(*sizes), vm.dspark_cache4_workspace_bytes(*sizes)
+    assert len(ws.buf) == len(both.buf) == n < n4 == len(both.buf4) and ws.buf4 is None and len(ws.tensor) < n + 512
+    B, P, lens = 3, 16, np.array([100, 40, 8])
+    rng = np.random.default_rng(2)
+    pages, table = _case(rng, B, P, lens, 128, 2)
+    k, v = (torch.from_numpy(rng.standard_normal((pages, 2, P, 128))).to(BF16).cuda() for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((24, 8, 128))).to(BF16).cuda()
+    lists = [s4._cu(table), s4._cu(lens), s4._cu([0, 8, 16, 24]), s4._cu([0, 2, 3, 4])]
+    outs = [torch.empty_like(q) for _ in range(2)]
+    for w, out in zip((ws, both), outs):
+        vm.dspark_cache_attention(q, k, v, *lists, out, w, max_new=8)
+        assert s4._status(vm, w) == 0
+    assert torch.equal(*outs)
+    with pytest.raises(ValueError):
+        vm.dspark_cache_attention4(q, *vm.Cache4(pages, 2, P, 128).tensors, *lists, outs[0], ws, max_new=8)

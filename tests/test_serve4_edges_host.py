@@ -1,0 +1,13 @@
+"""Host-side checks of the cache in 4 bits and the rotary positions that need no GPU."""
+import pytest
+import torch
+
+import verify_markov_head_gb300 as vm
+
+
+def test_attention_over_four_bits_names_a_workspace_without_room_for_it():
+    c, x = vm.Cache4(2, 1, 16, 64, device="cpu"), torch.zeros((1, 1, 64))
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    ws = type("W", (), {"buf": torch.zeros(1 << 20, dtype=torch.uint8), "buf4": None})()
+    with pytest.raises(ValueError, match="four_bits"):
+        vm.dspark_cache_attention4(x, *c.tensors, i(1, 2), i(1), i(2), i(2), x.clone(), ws, max_new=1, stream=0)

@@ -492,14 +492,16 @@ class _Scratch(Workspace):
 class CacheWorkspace(_Scratch):
     """Workspace of the cache calls for B requests of at most max_new new
     tokens, q_heads query heads over kv_heads key-value heads of head_dim: buf,
-    and buf4, which begins with it, for the attention over 4 bits."""
+    and buf4, which begins with it, for the attention over 4 bits.  That one takes
+    up to eight times the room (64 requests of 32 rows a key head 43 MB for 5): four_bits
+    False leaves it out (buf4 is None)."""
 
-    def __init__(self, B, q_heads, kv_heads, head_dim, max_new, device="cuda", stream=None):
+    def __init__(self, B, q_heads, kv_heads, head_dim, max_new, device="cuda", stream=None, *, four_bits=True):
         sizes = (B, q_heads, kv_heads, head_dim, max_new)
         plain = dspark_cache_workspace_bytes(*sizes)
-        super().__init__(max(plain, dspark_cache4_workspace_bytes(*sizes)), device, stream)
-        self.buf4 = self.buf
-        self.buf = self.buf4[:plain]
+        super().__init__(max(plain, dspark_cache4_workspace_bytes(*sizes)) if four_bits else plain, device, stream)
+        self.buf4 = self.buf if four_bits else None
+        self.buf = self.buf[:plain]
 
 
 class LogitsWorkspace(_Scratch):
@@ -611,7 +613,9 @@ def dspark_cache_read4(k_cache, v_cache, k_scale, v_scale, slot_map, k, v, *, k_
 def dspark_cache_attention4(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out,
                             ws: Workspace, *, max_new, k_exp=0, v_exp=0, scale=None, lse=None, stream=None):
     """dspark_cache_attention over a Cache4's tensors: q and out [N, q_heads,
-    head_dim] bf16 or fp32, the same plan and a CacheWorkspace."""
+    head_dim] bf16 or fp32, the same plan and a CacheWorkspace (four_bits)."""
+    if ws.buf4 is None:
+        raise ValueError("a CacheWorkspace with four_bits=False has no room for the attention over 4 bits")
     _check("dspark_cache_attention4", _serve.cache_attention4(
         q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_off, tile_off, out, ws.buf4, max_new, k_exp, v_exp, scale, lse,
         stream))
