@@ -11,3 +11,12 @@ def test_attention_over_four_bits_names_a_workspace_without_room_for_it():
     ws = type("W", (), {"buf": torch.zeros(1 << 20, dtype=torch.uint8), "buf4": None})()
     with pytest.raises(ValueError, match="four_bits"):
         vm.dspark_cache_attention4(x, *c.tensors, i(1, 2), i(1), i(2), i(2), x.clone(), ws, max_new=1, stream=0)
+
+
+def test_a_factor_without_a_kind_is_refused():
+    for bad in (dict(factor=8.0), dict(kind=None, factor=0.5)):
+        with pytest.raises(ValueError, match="kind"):
+            vm.rope_frequencies(64, 10000.0, bad)
+        with pytest.raises(ValueError, match="kind"):
+            vm.RopeTable(64, scaling=bad, device="cpu")
+    assert vm.rope_frequencies(64, 10000.0, {}) == vm.rope_frequencies(64) == vm.rope_frequencies(64, scaling=dict(kind=None))

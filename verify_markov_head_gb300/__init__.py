@@ -645,6 +645,8 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
     kind, f = s.pop("kind", None), float(s.pop("factor", 1.0))
     if not f > 0 or not math.isfinite(f):
         raise ValueError("factor must be positive and finite")
+    if kind is None and f != 1.0:
+        raise ValueError("a scaling's factor needs its kind")
     known = {None: (), "linear": (), "ntk": (), "yarn": ("trained", "fast", "slow", "mult"), "wavelength": ("trained", "low", "high")}
     if kind not in known:
         raise ValueError(f"unknown scaling {kind!r}")
