@@ -20,3 +20,9 @@ def test_a_factor_without_a_kind_is_refused():
         with pytest.raises(ValueError, match="kind"):
             vm.RopeTable(64, scaling=bad, device="cpu")
     assert vm.rope_frequencies(64, 10000.0, {}) == vm.rope_frequencies(64) == vm.rope_frequencies(64, scaling=dict(kind=None))
+
+
+def test_an_order_of_pairs_that_is_no_truth_value_is_refused():
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        vm.dspark_rope(torch.zeros((1, 1, 64)), None, torch.zeros(1, dtype=torch.int32), vm.RopeTable(64, device="cpu"), interleaved=torch.zeros(2),
+                     stream=type("Stream", (), {"cuda_stream": 256})())   # (not used: the tensors are not on the device)

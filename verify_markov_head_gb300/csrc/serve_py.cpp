@@ -330,6 +330,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
             heads = extent(k.size(1)); kp = k.data_ptr(); kop = ko.data_ptr();
         }
         const int tokens = extent(T), hq = extent(q.size(1)), dim = extent(D), rotary = integer(a[4]), interleaved = PyObject_IsTrue(a[8]);
+        if (interleaved < 0) throw PyRaised{};
         const float mult = number(a[5]);
         const auto* positions = static_cast<const int32_t*>(typed(a[2], "positions", at::kInt, T));
         const auto* turns = static_cast<const uint64_t*>(typed(a[3], "turns", at::kLong, rotary / 2));
