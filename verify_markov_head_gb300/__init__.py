@@ -594,7 +594,7 @@ class Cache4:
 
 def dspark_cache_append4(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, k_exp=0, v_exp=0, ws: Workspace = None,
                          stream=None):
-    """Quantise keys and values k, v [T, kv_heads, head_dim] (any token stride)
+    """Quantise keys and values k, v [T, kv_heads, head_dim] (any token stride of whole 16 bytes)
     to 4 bits and write them to the slots slot_map [T] int32 of a Cache4's
     tensors; negative slots are skipped."""
     _check("dspark_cache_append4", _serve.cache_append4(
@@ -604,7 +604,7 @@ def dspark_cache_append4(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, 
 def dspark_cache_read4(k_cache, v_cache, k_scale, v_scale, slot_map, k, v, *, k_exp=0, v_exp=0, ws: Workspace = None,
                        stream=None):
     """Read the slots slot_map [T] int32 of a Cache4's tensors into k, v
-    [T, kv_heads, head_dim] (any token stride); rows of negative slots are left
+    [T, kv_heads, head_dim] (any token stride of whole 16 bytes); rows of negative slots are left
     as they were."""
     _check("dspark_cache_read4", _serve.cache_read4(
         k_cache, v_cache, k_scale, v_scale, slot_map, k, v, k_exp, v_exp, None if ws is None else ws.buf, stream))
@@ -698,7 +698,7 @@ _TURN = Fraction(7964883625991394727376702227904, 2 ** 100)
 def dspark_rope(q, k, positions, table: RopeTable, q_out=None, k_out=None, *, interleaved=False, stream=None):
     """Turn the first table.rotary_dim entries of every head of q [T, q_heads,
     head_dim] and k [T, kv_heads, head_dim] (or None) by the tokens' positions
-    [T] int32, into q_out and k_out (None: in place; any token stride).  Pairs
+    [T] int32, into q_out and k_out (None: in place; any token stride of whole 16 bytes).  Pairs
     are (2 i, 2 i + 1) if interleaved, (i, i + rotary_dim / 2) otherwise; rows
     of negative positions are left as they were."""
     if q_out is None:
@@ -714,10 +714,12 @@ def dspark_sample_workspace_bytes(N) -> int:
 
 def dspark_sample(logits, u, tok, ws: Workspace, *, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
                   stream=None):
-    """Draw a token of each row of logits [N, V] (any row stride) from the
+    """Draw a token of each row of logits [N, V] from the
     random numbers u [N] fp32 in [0, 1): tok [N] int32, logprob [N] fp32 or None
     (of the token among what is left).  temperature, top_p, min_p [N] fp32 and
-    top_k [N] int32, or None; temperature 0 takes the largest entry."""
+    top_k [N] int32, or None; temperature 0 takes the largest entry.  Rows begin at
+    multiples of 16 bytes: of a vocabulary that is not one of 4 fp32 or 8 bf16
+    entries, logits are a slice of padded rows."""
     _check("dspark_sample", _serve.sample(logits, u, tok, ws.buf, temperature, top_k, top_p, min_p, logprob, stream))
 
 

@@ -11,7 +11,9 @@
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // theorem 1), three operations an entry.  It cannot fall on a border that y / scale
 // is not on: neighbours of (border * scale), a number of 7 bits, are 2^-23 of it
-// away or more, the quotient's rounding moves it by 2^-24 at most.
+// away or more, the quotient's rounding moves it by 2^-24 at most.  (That is what fp32
+// entries need; a bf16 entry's quotient is on a border or 2^-8 of it away, and would do with
+// two operations.  Both types share these three.)
 //
 // The work on a group bounds both as much as HBM does: of 32768 tokens of 4 KB the
 // append takes 38 us and the read 30, 172 MB each (4.5 and 5.7 TB/s).  On the way, both

@@ -7,18 +7,20 @@
 //            which the k-th largest lies is a bound that k entries reach; the entries that
 //            reach it, hardly more than k, go to one CTA, which ranks, cuts and draws.
 //   many     top-k beyond, and top-p: a histogram of counts, or of weights, over such
-//            steps, the step in which the wanted count or sum is reached, and its entries (a
-//            hundredth of the row) to one CTA, which finds the last one kept, 9 bits at a
-//            time.  No sort.
+//            steps, the step in which the wanted count or sum is reached, and its entries (of a
+//            model's row a hundredth, up to 4096) to one CTA, which finds the last one kept, 9
+//            bits at a time.  No sort.  A step of more entries (rows of few different values,
+//            and flat ones: of 151936 normal entries of deviation 0.3 a step holds up to 4500) is
+//            searched over the slices, a bit of the key and then of the id to a pass.
 //   the draw sums of the weights left, by warp and CTA in the order of the ids (formed on
 //            the way to the list, where there is one), and a walk through the one warp's
 //            share that holds u times the total.
 //
-// 512 rows of 151936 fp32 entries, 311 MB that HBM reads in 46 us: the largest entry 86 us,
-// nothing cut 180, top-k 50 104, top-k 200 131, top-k 2000 281, top-p 0.9 391; one row 7 to 30.
-// Issue of instructions bounds it once weights are formed: 20 an entry, 35 with the
-// histogram, whose additions take a fourth of the time of a row with top-p, as the list's
-// search on one CTA does.
+// 512 rows of 151936 fp32 entries, 311 MB that HBM reads in 46 us: the largest entry 88 us,
+// nothing cut 170, top-k 50 106, top-k 200 134, top-k 2000 290, top-p 0.9 378; one row 7 to
+// 30, of 34 to 53 passes over its slices 144 to 177 (64 rows 500 to 650).  No unit bounds it: 1.5 to 1.9 of 4
+// instructions a cycle are issued (20 an entry where weights are formed, 35 with the histogram), and warps
+// wait at the barriers between a row's phases first, which the other row on an SM covers in part.
 //
 // A token's boundaries are sums over up to 2^19 entries, and a sum that is off by
 // 2^-24 moves the draw across one in a row of some thousand (the boundaries of a
@@ -890,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 }
             }
             summed = true;
-        } else {                                 // very many equal entries: over the slices
+        } else {                                 // many equal entries, or a flat row: over the slices
             auto sum = [&](auto&& body) {
                 u64 mine = 0ull;
                 each_entry([&](float x, uint32_t id) { mine += body(key_of(x), id, mass ? weight.of(x) : 1ull); });
@@ -998,12 +1000,12 @@ template <typename T>
 cudaError_t launch(SampleParams p, cudaStream_t s) {
     constexpr int kVec = Row<T>::kVec;
     // two CTAs to a row, and on an SM: the phases of two rows overlap, and the rows at
-    // work fit the L2 for their later passes (512 rows of 151936, settings mixed: 271 us, now 239; one CTA of
-    // 1024 threads 276, of 512 322; four of 512 283, eight that keep the row in shared
-    // memory 323).  Up to 16 while that leaves no more CTAs than run at once, and twice
+    // work fit the L2 for their later passes (512 rows of 151936, settings mixed: 240 us; one CTA 299,
+    // four 244, eight that keep the row in shared memory, at an earlier stage, 323 for 265).  Up to 16
+    // while that leaves no more CTAs than run at once, and twice
     // as many where slices stay long, since rows that are cut take several times as long
-    // as others (64 rows of 151936, settings mixed: two CTAs 104 us, four 61; nothing cut
-    // 46 and 31; 128 rows 109 and 85, 55 and 55; of 32003 entries 48 and 51, 15 and 21).
+    // as others (64 rows of 151936, settings mixed: two CTAs 92 us, four 62; nothing cut
+    // 44 and 31; 128 rows 98 and 77, 52 and 53).
     int ctas = p.V > 16384 ? 2 : 1;
     while (ctas < 16 && (long long)p.N * ctas * 2 <= (p.V >= ctas * 2 * 24576 ? 4 : 2) * num_sms() && p.V > ctas * 4096) ctas *= 2;
     p.ctas = ctas;

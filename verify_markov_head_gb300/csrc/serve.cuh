@@ -131,9 +131,11 @@ cudaError_t launch_attn_mma(const AttnParams& p, cudaStream_t s);
 // Over a cache in 4 bits, bf16 queries: above 32 rows of a key head of 128 the tensor cores
 // take them, 64 at a time (cache_attention4_mma.cu), and above 16 where there are no more
 // requests and heads than SMs.  4096 positions, 8 heads, and where registers dequantise: 64
-// requests of 64 rows 185 us and 291, of 40 177 and 282, of 80 331 and 418, of 32 170 and
-// 161; one request of 8192 positions, 32 rows 21 and 35, 16 rows 20 and 24 (but eight of
-// 2000, 16 rows 23 and 20); 16 of 2000, 32 rows 35 and 41.
+// requests of 64 rows 189 us and 290, of 40 179 and 282, of 80 334 and 417, of 32 170 and
+// 160; one request of 8192 positions, 32 rows 20 and 35, 16 rows 19 and 23 (but eight of
+// 2000, 16 rows 23 and 19); 16 of 2000, 32 rows 35 and 41.  Short contexts are slower so, and the
+// lengths are not known here: 17 positions, 96 requests of 64 rows 41 and 27, of 80 74 and 27
+// (of 317 positions, 64 requests, 45 and 60, 83 and 79).
 inline bool attn4_tensor_rows(int rows, int D, bool few) { return D == 128 && rows > (few ? 16 : 32); }
 bool attn4_tensor(const AttnParams& p, int rows);  // and its pages can be copied by TMA
 cudaError_t launch_attn4_tensor(const AttnParams& p, cudaStream_t s);
