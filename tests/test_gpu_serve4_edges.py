@@ -247,3 +247,18 @@ def test_a_workspace_without_room_for_four_bits_is_the_smaller_one(vm):
     assert torch.equal(*outs)
     with pytest.raises(ValueError):
         vm.dspark_cache_attention4(q, *vm.Cache4(pages, 2, P, 128).tensors, *lists, outs[0], ws, max_new=8)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_flat_rows_of_many_different_entries(vm, dtype):
+    """A step of weights holds more entries than a list, few of them equal (bf16: some)."""
+    rng = np.random.default_rng(17)
+    N, V = 5, 151936
+    x = torch.from_numpy(rng.standard_normal((N, V)) * np.array([0.3, 0.3, 1.5, 1.5, 0.01])[:, None]).to(dtype).cuda()
+    u = rng.random(N).astype(np.float32)
+    T = np.array([1.0, 2.0, 5.0, 10.0, 1.0])
+    for k, p in ((None, 0.5), (None, 0.03), (50000, None), (70000, 0.6), (V - 2, 0.999)):
+        args = (T, None if k is None else np.full(N, k), None if p is None else np.full(N, p), None)
+        tok, lp, status = s4._sample(vm, x, u, *args)
+        assert status == 0
+        s4._check_rows(x, u, *args, tok, lp)
