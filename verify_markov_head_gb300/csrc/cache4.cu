@@ -16,7 +16,7 @@
 // two operations.  Both types share these three.)
 //
 // The work on a group bounds both as much as HBM does: of 32768 tokens of 4 KB the
-// append takes 38 us and the read 30, 172 MB each (4.5 and 5.7 TB/s).  On the way, both
+// append takes 33 us and the read 33, 172 MB each (5.2 TB/s), of fp32 rows 50 and 52 (306 MB, 6.0 TB/s).  On the way, both
 // together: a division of 64 bits and two loads of 16 bytes a group 78 us, a block to
 // two tokens and no more 91 (the places of a group are formed anew), 8 blocks an
 // SM with one operation an entry 70, with two entries 68, 6 blocks 67.

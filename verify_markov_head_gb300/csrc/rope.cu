@@ -10,7 +10,8 @@
 //
 // Bytes bound it: a token's rows are read and written once.  32768 tokens of 40
 // heads of 128, 671 MB: 102 us (6.6 TB/s; with sines in shared memory, a block to 4
-// tokens and two barriers each, 139), 512 tokens 3.9 (4.6 without sharing the sines).
+// tokens and two barriers each, 139), 512 tokens 3.9 (4.6 without sharing the sines); in fp32, 1342 MB,
+// 230 us in halves and 248 in neighbours (5.8 and 5.4 TB/s, some registers spilled).
 #include <cuda_bf16.h>
 
 #include "pdl.cuh"
