@@ -170,7 +170,7 @@ def test_the_logarithm_of_a_light_token(vm, V, dtype, T):
 
 # ------------------------------------------------------------------ refusals
 def test_rows_and_caches_that_overlap_are_refused(vm):
-    T, H, D, P, pages = 6, 2, 64, 4, 5
+    T, H, D, P, pages = 5, 2, 64, 4, 5
     slots = s4._cu(np.arange(T))
     c = vm.Cache4(pages, H, P, D)
     wide = torch.randn((T, 4, H, D), device="cuda")
@@ -262,3 +262,24 @@ def test_flat_rows_of_many_different_entries(vm, dtype):
         tok, lp, status = s4._sample(vm, x, u, *args)
         assert status == 0
         s4._check_rows(x, u, *args, tok, lp)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [20001, 70003, 151936])
+def test_a_long_row_is_the_same_however_many_ctas_take_it(vm, V, dtype):
+    """One row is taken by up to 16 CTAs, many by two or one each: tokens and logarithms, bit by bit."""
+    rng = np.random.default_rng(V)
+    N = 160
+    x = torch.empty((N, -(-V // 8) * 8), dtype=dtype, device="cuda")[:, :V]
+    x.copy_(torch.randn((N, V), generator=torch.Generator(device="cuda").manual_seed(V), device="cuda") * 2)
+    x[::3] *= 0.1                                           # flat rows, whose unit is coarser
+    x[1::3, V // 3] = 40.0                                  # and rows of one entry far above the others
+    u, T = rng.random(N).astype(np.float32), rng.choice([0.05, 0.7, 1.0, 4.0], N)
+    k, p, m = rng.choice([0, 3, 300, 2000, V - 5], N), rng.choice([0.5, 0.95, 1.0], N), rng.choice([0.0, 0.01], N)
+    for args in ((None,) * 4, (T, None, None, None), (T, k, None, m), (T, None, p, None), (T, k, p, m)):
+        tok, lp, status = s4._sample(vm, x, u, *args)
+        assert status == 0
+        for a, b in ((0, 1), (1, 2), (2, 3), (5, 12), (10, 60)):
+            part = [None if v is None else v[a:b] for v in args]
+            t, l, _ = s4._sample(vm, x[a:b], u[a:b], *part)
+            assert (t == tok[a:b]).all() and (l == lp[a:b]).all()

@@ -25,10 +25,10 @@
 // for 16 rows a NaN, an infinity or a large row took the others' entries below fp16's range.)
 //
 // One request of 131072 positions, 8 heads of 64 rows: 91 us, of them 9 the join (with
-// registers dequantising for mma.sync 153; one scale to 16 rows of queries 89; on the way one buffer of P 145, queries brought by
-// one warp 121, one more wait in a step 115).  HBM would take 22 and the products 15: the
-// issue slots bound it, 65 of 100 taken by 28 warps that wait on one another, with 72
-// registers a thread.
+// registers dequantising for mma.sync 153; with one scale to 16 rows of queries 89; on the
+// way one buffer of P 145, queries brought by one warp 121, one more wait in a step 115).
+// HBM would take 22 and the products 15: the issue slots bind it, 65 of 100 taken by 28 warps
+// that wait on one another, with 72 registers a thread (160 bytes spilled).
 //
 // Roles (28 warps, one CTA per SM):
 //   first 16         softmax: groups of 4 warps, 16 columns each; thread = position
